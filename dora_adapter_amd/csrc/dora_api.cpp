@@ -4,7 +4,8 @@
 // launch plan (tile shape and split-K per product), the workspace carve-up
 // and the launch sequences of the factored norm, the compose, the forward
 // and the norm-detached backward.  Every step of the computation runs in
-// the HIP kernels of gemm_bf16.hip, gemm_f32.hip and elementwise.hip.
+// the HIP kernels of gemm_bf16.hip, gemm_f32.hip, elementwise.hip, rows8.hip
+// and gemm_i8.hip.
 #include <stdio.h>
 #include <stdarg.h>
 #include <stdlib.h>
@@ -390,7 +391,7 @@ struct BwdPlan {
     size_t bytes;
 };
 
-BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype)
+BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype, bool y8 = false)
 {
     const bool bf = dtype == DORA_BF16;
     BwdPlan b;
@@ -409,10 +410,10 @@ BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dty
     // dh/dm inside the dB product: bf16, the pipelined layout, tokens to
     // stream, and no tile configuration other than the one that implements
     // it requested (a test restricting the planners to another one runs the
-    // separate pass)
+    // separate pass; y in 8 bits has a pass of its own)
     const int forced = forced_tile_cfg();
     b.fused_dhdm = false;
-    if (bf && dbs.dma_ok && T > 0)
+    if (bf && dbs.dma_ok && T > 0 && !y8)
         for (int c = 0; c < gemm_bf16_num_cfgs() && !b.fused_dhdm; ++c)
             if (gemm_bf16_cfg(c).dhdm_ok && (forced < 0 || forced == c)) {
                 b.dB = plan_gemm(bf, dbs, d_out * r, c);
@@ -448,11 +449,12 @@ struct ThruPlan {
     size_t bytes;
 };
 
-ThruPlan plan_through_norm(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype)
+ThruPlan plan_through_norm(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype,
+                           bool y8 = false)
 {
     const bool bf = dtype == DORA_BF16;
     ThruPlan p;
-    p.b = plan_backward(T, d_in, d_out, r, dtype);
+    p.b = plan_backward(T, d_in, d_out, r, dtype, y8);
     p.g = plan_gemm(bf, nt_shape(r, r, d_in), r * r);
     p.da = plan_gemm(bf, GemmShape{r, d_in, {T, d_out}, 2, 2,
                                    dma_mn_operand(T, r) && dma_mn_operand(T, d_in) &&
@@ -660,6 +662,172 @@ int run_dhdm_dB(const BwdPlan &b, const void *dy, const void *y, const float *m,
     a.out_f32 = f32;
     a.alpha = alpha;
     DORA_LAUNCH(launch_gemm_bf16_dhdm(a, b.dB.cfg, st), "dh, dm and dB");
+    return DORA_OK;
+}
+
+// y held as 8-bit rows.
+struct Rows8 {
+    const int8_t *q;
+    const float *scale;
+    int group;
+};
+
+// The separate dh/dm pass, from y or from its 8-bit rows.
+int run_dhdm(bool bf16, const void *dy, const void *y, const Rows8 *y8, const float *m,
+             const float *n, int64_t T, int64_t d_out, int64_t sweep, void *dh, float *dmpart,
+             hipStream_t st)
+{
+    if (y8)
+        DORA_LAUNCH(launch_dh_dm_rows8(bf16, dy, y8->q, y8->scale, y8->group, m, n, T, d_out, sweep,
+                                       dh, dmpart, st),
+                    "dh/dm from 8 bits");
+    else
+        DORA_LAUNCH(launch_dh_dm_partial(bf16, dy, y, m, n, T, d_out, sweep, dh, dmpart, st),
+                    "dh/dm");
+    return DORA_OK;
+}
+
+// dora_backward after its checks (y8 set: y is not read).
+int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W, const void *A,
+                  const void *B, const float *m, const float *n, float s, const void *P,
+                  const void *y, const Rows8 *y8, int64_t T, int64_t d_in, int64_t d_out, int64_t r,
+                  int dtype, void *dx, void *dA, void *dB, float *dm, void *ws, void *stream)
+{
+    const bool bf = dtype == DORA_BF16;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char *w = static_cast<char *>(ws);
+    void *dh = w + p.o_dh;
+    float *dmpart = reinterpret_cast<float *>(w + p.o_dmpart);
+    void *Q = w + p.o_Q;
+
+    // 1. dh = g dy and dm partial sums (one pass over dy and y), then dm;
+    //    with the fused plan the same pass also forms dB = s dh^T P.
+    if (p.fused_dhdm) {
+        float *part = reinterpret_cast<float *>(w + p.o_dBpart);
+        const bool split = p.dB.splits > 1;
+        DORA_CHECK(run_dhdm_dB(p, dy, y, m, n, P, T, d_out, r, dh, dmpart, split ? part : dB,
+                               split ? 1 : 0, split ? 1.0f : s, st));
+        if (split)
+            DORA_LAUNCH(launch_splitk_reduce(bf, part, p.dB.splits, d_out, r, s, dB, st), "dB");
+    } else {
+        DORA_CHECK(run_dhdm(bf, dy, y, y8, m, n, T, d_out, p.sweep, dh, dmpart, st));
+    }
+    DORA_LAUNCH(launch_dm_finish(dmpart, p.nchunks, m, d_out, dm, st), "dm finish");
+    // 2. Q = s dh B  (A K-major, B MN-major).
+    DORA_CHECK(run_store(bf, p.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
+                         reinterpret_cast<float *>(w + p.o_Qpart), st, "Q = s dh B"));
+    // 3. dx = [dh | Q] [W ; A]  (K-concatenated segments, B MN-major).
+    {
+        GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
+        g.seg[1] = GemmSeg{Q, r, A, d_in, r};
+        g.nseg = 2;
+        DORA_CHECK(run_store(bf, p.dx, g, 1, dx, d_in, 1.0f,
+                             reinterpret_cast<float *>(w + p.o_dxpart), st, "dx"));
+    }
+    // 4. dB = s dh^T P  (both MN-major, K = T), unless formed in step 1.
+    if (!p.fused_dhdm)
+        DORA_CHECK(run_store(bf, p.dB, seg1(d_out, r, dh, d_out, P, r, T), 2, dB, r, s,
+                             reinterpret_cast<float *>(w + p.o_dBpart), st, "dB"));
+    // 5. dA = Q^T x  (both MN-major, K = T).
+    DORA_CHECK(run_store(bf, p.dA, seg1(r, d_in, Q, r, x, d_in, T), 2, dA, d_in, 1.0f,
+                         reinterpret_cast<float *>(w + p.o_dApart), st, "dA"));
+    return DORA_OK;
+}
+
+// dora_backward_through_norm after its checks (y8 set: y is not read).
+int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const void *W,
+                      const void *A, const void *B, const float *m, const float *n, float s,
+                      const void *P, const void *y, const Rows8 *y8, const float *U, int64_t T,
+                      int64_t d_in, int64_t d_out, int64_t r, int dtype, void *dx, void *dA,
+                      void *dB, float *dm, void *ws, void *stream)
+{
+    const bool bf = dtype == DORA_BF16;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char *w = static_cast<char *>(ws);
+    const BwdPlan &b = p.b;
+    void *dh = w + b.o_dh;
+    float *dmpart = reinterpret_cast<float *>(w + b.o_dmpart);
+    void *Q = w + b.o_Q;
+    float *cs = reinterpret_cast<float *>(w + p.o_cs);
+    void *cB = w + p.o_cB;
+    float *aslots = reinterpret_cast<float *>(w + p.o_aslots);
+    float *bslots = reinterpret_cast<float *>(w + p.o_bslots);
+    float *yslots = reinterpret_cast<float *>(w + p.o_yslots);
+    const size_t gsz = bf ? static_cast<size_t>(r) * r * 2 : 0;  // lo half of a hi/lo pair
+
+    // 1-3. As with n held constant: dh = g dy and dm (with the fused plan the
+    //      same pass also puts s dh^T P into dB's fp32 slots), Q = s dh B,
+    //      dx = [dh | Q] [W ; A].
+    if (b.fused_dhdm)
+        DORA_CHECK(run_dhdm_dB(b, dy, y, m, n, P, T, d_out, r, dh, dmpart, bslots, 1, s, st));
+    else
+        DORA_CHECK(run_dhdm(bf, dy, y, y8, m, n, T, d_out, b.sweep, dh, dmpart, st));
+    DORA_LAUNCH(launch_dm_finish(dmpart, b.nchunks, m, d_out, dm, st), "dm finish");
+    DORA_CHECK(run_store(bf, b.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
+                         reinterpret_cast<float *>(w + b.o_Qpart), st, "Q = s dh B"));
+    {
+        GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
+        g.seg[1] = GemmSeg{Q, r, A, d_in, r};
+        g.nseg = 2;
+        DORA_CHECK(run_store(bf, b.dx, g, 1, dx, d_in, 1.0f,
+                             reinterpret_cast<float *>(w + b.o_dxpart), st, "dx"));
+    }
+    // 4. The norm's row coefficient cs = -s m dm / n^2 and cB = cs (.) B.
+    DORA_LAUNCH(launch_norm_grad_coef(bf, m, dm, n, s, B, d_out, r, cs, cB, st), "norm grad coef");
+    // 5. dA = [Q^T | cB^T] [x ; W] + s (cB^T B) A.
+    {
+        GemmArgs g = seg1(r, d_in, cB, r, W, d_in, d_out);
+        if (T > 0) {
+            g.seg[1] = g.seg[0];
+            g.seg[0] = GemmSeg{Q, r, x, d_in, T};
+            g.nseg = 2;
+        }
+        DORA_CHECK(run_slots(bf, p.da, g, 2, aslots, 1.0f, st, "dA: Q^T x + cB^T W"));
+        float *gspart = reinterpret_cast<float *>(w + p.o_gspart);
+        char *gs = w + p.o_gsfin;
+        DORA_CHECK(run_slots(bf, p.gs, seg1(r, r, cB, r, B, r, d_out), 2, gspart, 1.0f, st,
+                             "dA: cB^T B"));
+        DORA_LAUNCH(launch_gram_finalize(bf, gspart, p.gs.splits, r, gs, st), "dA: cB^T B sum");
+        GemmArgs z = seg1(r, d_in, gs, r, A, d_in, r);
+        if (bf) {
+            z.seg[1] = GemmSeg{gs + gsz, r, A, d_in, r};
+            z.nseg = 2;
+        }
+        DORA_CHECK(run_slots(bf, p.z, z, 1, aslots + static_cast<size_t>(p.da.splits) * r * d_in,
+                             s, st, "dA: s (cB^T B) A"));
+        DORA_LAUNCH(launch_combine_rows(bf, aslots, p.da.splits,
+                                        aslots + static_cast<size_t>(p.da.splits) * r * d_in,
+                                        p.z.splits, nullptr, r, d_in, dA, st),
+                    "dA combine");
+    }
+    // 6. dB = s dh^T P + cs (.) V A^T,  V A^T = W A^T + s B G,  G = A A^T.
+    {
+        if (!b.fused_dhdm)
+            DORA_CHECK(run_slots(bf, b.dB, seg1(d_out, r, dh, d_out, P, r, T), 2, bslots, s, st,
+                                 "dB: s dh^T P"));
+        // V A^T = W A^T + s B G: the norm's own product when the caller kept it
+        // (U), else formed here
+        if (!U) {
+            float *gpart = reinterpret_cast<float *>(w + p.o_gpart);
+            char *G = w + p.o_gfin;
+            DORA_CHECK(run_slots(bf, p.g, seg1(r, r, A, d_in, A, d_in, d_in), 0, gpart, 1.0f,
+                                 st, "dB: A A^T"));
+            DORA_LAUNCH(launch_gram_finalize(bf, gpart, p.g.splits, r, G, st), "dB: A A^T sum");
+            DORA_CHECK(run_slots(bf, p.y1, seg1(d_out, r, W, d_in, A, d_in, d_in), 0, yslots,
+                                 1.0f, st, "dB: W A^T"));
+            GemmArgs g = seg1(d_out, r, B, r, G, r, r);
+            if (bf) {
+                g.seg[1] = GemmSeg{B, r, G + gsz, r, r};
+                g.nseg = 2;
+            }
+            DORA_CHECK(run_slots(bf, p.y2, g, 1,
+                                 yslots + static_cast<size_t>(p.y1.splits) * d_out * r, s, st,
+                                 "dB: s B G"));
+        }
+        DORA_LAUNCH(launch_combine_rows(bf, bslots, p.nb, yslots, U ? 0 : p.ny, cs, d_out, r, dB,
+                                        st, U),
+                    "dB combine");
+    }
     return DORA_OK;
 }
 
@@ -1349,6 +1517,7 @@ const char *dora_strerror(int status)
     case DORA_E_WORKSPACE: return "workspace missing or too small";
     case DORA_E_ALIAS: return "buffers overlap";
     case DORA_E_HIP: return "HIP error";
+    case DORA_E_VALUE: return "scalar argument out of range";
     default: return "unknown status";
     }
 }
@@ -1473,7 +1642,6 @@ int dora_backward(const void *dy, const void *x, const void *W, const void *A, c
                            {dm, "dm", true}}));
     const BwdPlan p = plan_backward(T, d_in, d_out, r, dtype);
     DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
-    const bool bf = dtype == DORA_BF16;
     const size_t e = esize(dtype);
     DORA_CHECK(check_disjoint(
         {{{dx, T * d_in * e}, "dx"}, {{dA, r * d_in * e}, "dA"}, {{dB, d_out * r * e}, "dB"},
@@ -1482,45 +1650,8 @@ int dora_backward(const void *dy, const void *x, const void *W, const void *A, c
          {{A, r * d_in * e}, "A"}, {{B, d_out * r * e}, "B"}, {{m, d_out * sizeof(float)}, "m"},
          {{n, d_out * sizeof(float)}, "n"}, {{P, T * r * e}, "P"}, {{y, T * d_out * e}, "y"}}));
 
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    char *w = static_cast<char *>(ws);
-    void *dh = w + p.o_dh;
-    float *dmpart = reinterpret_cast<float *>(w + p.o_dmpart);
-    void *Q = w + p.o_Q;
-
-    // 1. dh = g dy and dm partial sums (one pass over dy and y), then dm;
-    //    with the fused plan the same pass also forms dB = s dh^T P.
-    if (p.fused_dhdm) {
-        float *part = reinterpret_cast<float *>(w + p.o_dBpart);
-        const bool split = p.dB.splits > 1;
-        DORA_CHECK(run_dhdm_dB(p, dy, y, m, n, P, T, d_out, r, dh, dmpart, split ? part : dB,
-                               split ? 1 : 0, split ? 1.0f : s, st));
-        if (split)
-            DORA_LAUNCH(launch_splitk_reduce(bf, part, p.dB.splits, d_out, r, s, dB, st), "dB");
-    } else {
-        DORA_LAUNCH(launch_dh_dm_partial(bf, dy, y, m, n, T, d_out, p.sweep, dh, dmpart, st),
-                    "dh/dm");
-    }
-    DORA_LAUNCH(launch_dm_finish(dmpart, p.nchunks, m, d_out, dm, st), "dm finish");
-    // 2. Q = s dh B  (A K-major, B MN-major).
-    DORA_CHECK(run_store(bf, p.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
-                         reinterpret_cast<float *>(w + p.o_Qpart), st, "Q = s dh B"));
-    // 3. dx = [dh | Q] [W ; A]  (K-concatenated segments, B MN-major).
-    {
-        GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
-        g.seg[1] = GemmSeg{Q, r, A, d_in, r};
-        g.nseg = 2;
-        DORA_CHECK(run_store(bf, p.dx, g, 1, dx, d_in, 1.0f,
-                             reinterpret_cast<float *>(w + p.o_dxpart), st, "dx"));
-    }
-    // 4. dB = s dh^T P  (both MN-major, K = T), unless formed in step 1.
-    if (!p.fused_dhdm)
-        DORA_CHECK(run_store(bf, p.dB, seg1(d_out, r, dh, d_out, P, r, T), 2, dB, r, s,
-                             reinterpret_cast<float *>(w + p.o_dBpart), st, "dB"));
-    // 5. dA = Q^T x  (both MN-major, K = T).
-    DORA_CHECK(run_store(bf, p.dA, seg1(r, d_in, Q, r, x, d_in, T), 2, dA, d_in, 1.0f,
-                         reinterpret_cast<float *>(w + p.o_dApart), st, "dA"));
-    return DORA_OK;
+    return backward_impl(p, dy, x, W, A, B, m, n, s, P, y, nullptr, T, d_in, d_out, r, dtype, dx, dA,
+                         dB, dm, ws, stream);
 }
 
 size_t dora_backward_through_norm_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
@@ -1548,7 +1679,6 @@ int dora_backward_through_norm(const void *dy, const void *x, const void *W, con
                            {dm, "dm", true}, {U, "U", false}}));
     const ThruPlan p = plan_through_norm(T, d_in, d_out, r, dtype);
     DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
-    const bool bf = dtype == DORA_BF16;
     const size_t e = esize(dtype);
     DORA_CHECK(check_disjoint(
         {{{dx, T * d_in * e}, "dx"}, {{dA, r * d_in * e}, "dA"}, {{dB, d_out * r * e}, "dB"},
@@ -1558,94 +1688,8 @@ int dora_backward_through_norm(const void *dy, const void *x, const void *W, con
          {{n, d_out * sizeof(float)}, "n"}, {{P, T * r * e}, "P"}, {{y, T * d_out * e}, "y"},
          {{U, d_out * r * sizeof(float)}, "U"}}));
 
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    char *w = static_cast<char *>(ws);
-    const BwdPlan &b = p.b;
-    void *dh = w + b.o_dh;
-    float *dmpart = reinterpret_cast<float *>(w + b.o_dmpart);
-    void *Q = w + b.o_Q;
-    float *cs = reinterpret_cast<float *>(w + p.o_cs);
-    void *cB = w + p.o_cB;
-    float *aslots = reinterpret_cast<float *>(w + p.o_aslots);
-    float *bslots = reinterpret_cast<float *>(w + p.o_bslots);
-    float *yslots = reinterpret_cast<float *>(w + p.o_yslots);
-    const size_t gsz = bf ? static_cast<size_t>(r) * r * 2 : 0;  // lo half of a hi/lo pair
-
-    // 1-3. As with n held constant: dh = g dy and dm (with the fused plan the
-    //      same pass also puts s dh^T P into dB's fp32 slots), Q = s dh B,
-    //      dx = [dh | Q] [W ; A].
-    if (b.fused_dhdm)
-        DORA_CHECK(run_dhdm_dB(b, dy, y, m, n, P, T, d_out, r, dh, dmpart, bslots, 1, s, st));
-    else
-        DORA_LAUNCH(launch_dh_dm_partial(bf, dy, y, m, n, T, d_out, b.sweep, dh, dmpart, st),
-                    "dh/dm");
-    DORA_LAUNCH(launch_dm_finish(dmpart, b.nchunks, m, d_out, dm, st), "dm finish");
-    DORA_CHECK(run_store(bf, b.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
-                         reinterpret_cast<float *>(w + b.o_Qpart), st, "Q = s dh B"));
-    {
-        GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
-        g.seg[1] = GemmSeg{Q, r, A, d_in, r};
-        g.nseg = 2;
-        DORA_CHECK(run_store(bf, b.dx, g, 1, dx, d_in, 1.0f,
-                             reinterpret_cast<float *>(w + b.o_dxpart), st, "dx"));
-    }
-    // 4. The norm's row coefficient cs = -s m dm / n^2 and cB = cs (.) B.
-    DORA_LAUNCH(launch_norm_grad_coef(bf, m, dm, n, s, B, d_out, r, cs, cB, st), "norm grad coef");
-    // 5. dA = [Q^T | cB^T] [x ; W] + s (cB^T B) A.
-    {
-        GemmArgs g = seg1(r, d_in, cB, r, W, d_in, d_out);
-        if (T > 0) {
-            g.seg[1] = g.seg[0];
-            g.seg[0] = GemmSeg{Q, r, x, d_in, T};
-            g.nseg = 2;
-        }
-        DORA_CHECK(run_slots(bf, p.da, g, 2, aslots, 1.0f, st, "dA: Q^T x + cB^T W"));
-        float *gspart = reinterpret_cast<float *>(w + p.o_gspart);
-        char *gs = w + p.o_gsfin;
-        DORA_CHECK(run_slots(bf, p.gs, seg1(r, r, cB, r, B, r, d_out), 2, gspart, 1.0f, st,
-                             "dA: cB^T B"));
-        DORA_LAUNCH(launch_gram_finalize(bf, gspart, p.gs.splits, r, gs, st), "dA: cB^T B sum");
-        GemmArgs z = seg1(r, d_in, gs, r, A, d_in, r);
-        if (bf) {
-            z.seg[1] = GemmSeg{gs + gsz, r, A, d_in, r};
-            z.nseg = 2;
-        }
-        DORA_CHECK(run_slots(bf, p.z, z, 1, aslots + static_cast<size_t>(p.da.splits) * r * d_in,
-                             s, st, "dA: s (cB^T B) A"));
-        DORA_LAUNCH(launch_combine_rows(bf, aslots, p.da.splits,
-                                        aslots + static_cast<size_t>(p.da.splits) * r * d_in,
-                                        p.z.splits, nullptr, r, d_in, dA, st),
-                    "dA combine");
-    }
-    // 6. dB = s dh^T P + cs (.) V A^T,  V A^T = W A^T + s B G,  G = A A^T.
-    {
-        if (!b.fused_dhdm)
-            DORA_CHECK(run_slots(bf, b.dB, seg1(d_out, r, dh, d_out, P, r, T), 2, bslots, s, st,
-                                 "dB: s dh^T P"));
-        // V A^T = W A^T + s B G: the norm's own product when the caller kept it
-        // (U), else formed here
-        if (!U) {
-            float *gpart = reinterpret_cast<float *>(w + p.o_gpart);
-            char *G = w + p.o_gfin;
-            DORA_CHECK(run_slots(bf, p.g, seg1(r, r, A, d_in, A, d_in, d_in), 0, gpart, 1.0f,
-                                 st, "dB: A A^T"));
-            DORA_LAUNCH(launch_gram_finalize(bf, gpart, p.g.splits, r, G, st), "dB: A A^T sum");
-            DORA_CHECK(run_slots(bf, p.y1, seg1(d_out, r, W, d_in, A, d_in, d_in), 0, yslots,
-                                 1.0f, st, "dB: W A^T"));
-            GemmArgs g = seg1(d_out, r, B, r, G, r, r);
-            if (bf) {
-                g.seg[1] = GemmSeg{B, r, G + gsz, r, r};
-                g.nseg = 2;
-            }
-            DORA_CHECK(run_slots(bf, p.y2, g, 1,
-                                 yslots + static_cast<size_t>(p.y1.splits) * d_out * r, s, st,
-                                 "dB: s B G"));
-        }
-        DORA_LAUNCH(launch_combine_rows(bf, bslots, p.nb, yslots, U ? 0 : p.ny, cs, d_out, r, dB,
-                                        st, U),
-                    "dB combine");
-    }
-    return DORA_OK;
+    return through_norm_impl(p, dy, x, W, A, B, m, n, s, P, y, nullptr, U, T, d_in, d_out, r, dtype,
+                             dx, dA, dB, dm, ws, stream);
 }
 
 size_t dora_factored_norm_grouped_workspace(const dora_module *mods, int count, int dtype)
@@ -1847,6 +1891,276 @@ int dora_linear(const void *x, const void *W, int64_t T, int64_t d_in, int64_t d
     return run_store(dtype == DORA_BF16, p.g, seg1(T, d_out, x, d_in, W, d_in, d_in), 0, y, d_out,
                      1.0f, static_cast<float *>(ws), static_cast<hipStream_t>(stream),
                      "linear x W^T");
+}
+
+// ------------------------------------------------ 8-bit rows and their users
+namespace {
+
+// 0, or a power of two from 32 to 512
+int check_group(int64_t group)
+{
+    if (group != 0 && (group < 32 || group > 512 || (group & (group - 1)) != 0))
+        return fail(DORA_E_SHAPE, "group %lld is neither 0 nor a power of two from 32 to 512",
+                    (long long)group);
+    return DORA_OK;
+}
+
+int check_rows(int64_t rows, int64_t d)
+{
+    if (rows < 0 || rows > kMaxDim || d < 1 || d > kMaxDim)
+        return fail(DORA_E_SHAPE, "need 0 <= rows < 2^31 and 1 <= width < 2^31 (got %lld, %lld)",
+                    (long long)rows, (long long)d);
+    return DORA_OK;
+}
+
+size_t scale_bytes(int64_t rows, int64_t d, int64_t group)
+{
+    return static_cast<size_t>(rows) * (group ? (d + group - 1) / group : 1) * sizeof(float);
+}
+
+// int32 sums of int8 products: 128 * 128 * 131071 < 2^31
+constexpr int64_t kMaxI8Width = 131071;
+
+int check_i8_width(int64_t d_in)
+{
+    if (d_in > kMaxI8Width)
+        return fail(DORA_E_SHAPE, "d_in=%lld above %lld, where int32 sums could overflow",
+                    (long long)d_in, (long long)kMaxI8Width);
+    return DORA_OK;
+}
+
+}  // namespace
+
+int dora_rmsnorm(const void *x, const void *residual, const void *w, float eps, int64_t T,
+                 int64_t d, int dtype, int64_t group, void *y, void *h, float *rstd, void *q,
+                 float *scale, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(T, d));
+    DORA_CHECK(check_group(group));
+    if (!(eps >= 0.f) || eps > 3.4e38f)
+        return fail(DORA_E_VALUE, "eps must be finite and not negative");
+    const bool has_t = T > 0;
+    if (has_t && !y && !q)
+        return fail(DORA_E_NULL, "y and q are both NULL");
+    DORA_CHECK(check_ptrs({{x, "x", has_t}, {residual, "residual", false}, {w, "w", true},
+                           {y, "y", false}, {h, "h", false}, {rstd, "rstd", false},
+                           {q, "q", false}, {scale, "scale", has_t && q != nullptr}}));
+    const size_t e = esize(dtype), rows = static_cast<size_t>(T) * d * e;
+    const Range rx{x, rows}, rr{residual, rows}, rw{w, d * e};
+    // h in place of x or the residual, y in place of x: the same element,
+    // read before it is written by the same thread
+    if (h && h != x && overlap({h, rows}, rx))
+        return fail(DORA_E_ALIAS, "h partially overlaps x");
+    if (h && h != residual && overlap({h, rows}, rr))
+        return fail(DORA_E_ALIAS, "h partially overlaps residual");
+    if (y && y != x && overlap({y, rows}, rx))
+        return fail(DORA_E_ALIAS, "y partially overlaps x");
+    const size_t sb = q ? scale_bytes(T, d, group) : 0;
+    const Range rq{q, static_cast<size_t>(T) * d};
+    DORA_CHECK(check_disjoint({{{y, rows}, "y"}, {{h, rows}, "h"}, {{rstd, T * sizeof(float)}, "rstd"},
+                               {rq, "q"}, {{scale, sb}, "scale"}},
+                              {{rw, "w"}}));
+    DORA_CHECK(check_disjoint({{{y, rows}, "y"}}, {{rr, "residual"}}));
+    DORA_CHECK(check_disjoint({{{rstd, T * sizeof(float)}, "rstd"}, {rq, "q"}, {{scale, sb}, "scale"}},
+                              {{rx, "x"}, {rr, "residual"}}));
+    NormArgs a{x, residual, w, eps, static_cast<int>(group), T, d, y, h, rstd,
+               static_cast<int8_t *>(q), scale};
+    DORA_LAUNCH(launch_rmsnorm(dtype == DORA_BF16, a, static_cast<hipStream_t>(stream)), "rmsnorm");
+    return DORA_OK;
+}
+
+size_t dora_rmsnorm_backward_workspace(int64_t T, int64_t d, int dtype)
+{
+    if (check_dtype(dtype) || check_rows(T, d))
+        return 0;
+    return align_up(static_cast<size_t>(rmsnorm_parts(T, d)) * d * sizeof(float));
+}
+
+int dora_rmsnorm_backward(const void *dy, const void *h, const void *w, const float *rstd,
+                          const void *dres, int64_t T, int64_t d, int dtype, void *dx, float *dw,
+                          void *ws, size_t ws_bytes, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(T, d));
+    const bool has_t = T > 0;
+    DORA_CHECK(check_ptrs({{dy, "dy", has_t}, {h, "h", has_t}, {w, "w", true},
+                           {rstd, "rstd", has_t}, {dres, "dres", false}, {dx, "dx", has_t},
+                           {dw, "dw", false}}));
+    const size_t need = dw ? dora_rmsnorm_backward_workspace(T, d, dtype) : 0;
+    DORA_CHECK(check_ws(ws, ws_bytes, need));
+    const size_t e = esize(dtype), rows = static_cast<size_t>(T) * d * e;
+    if (dx && dx != dres && overlap({dx, rows}, {dres, rows}))
+        return fail(DORA_E_ALIAS, "dx partially overlaps dres");
+    DORA_CHECK(check_disjoint(
+        {{{dx, rows}, "dx"}, {{dw, d * sizeof(float)}, "dw"}, {{ws, need}, "workspace"}},
+        {{{dy, rows}, "dy"}, {{h, rows}, "h"}, {{w, d * e}, "w"},
+         {{rstd, T * sizeof(float)}, "rstd"}}));
+    DORA_CHECK(check_disjoint({{{dw, d * sizeof(float)}, "dw"}, {{ws, need}, "workspace"}},
+                              {{{dres, rows}, "dres"}}));
+    NormGradArgs a{dy, h, w, dres, rstd, T, d, dx, static_cast<float *>(ws), rmsnorm_parts(T, d)};
+    DORA_LAUNCH(launch_rmsnorm_grad(dtype == DORA_BF16, a, dw, static_cast<hipStream_t>(stream)),
+                "rmsnorm backward");
+    return DORA_OK;
+}
+
+int dora_quantize_rows(const void *x, int64_t rows, int64_t d, int dtype, int64_t group, void *q,
+                       float *scale, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(rows, d));
+    DORA_CHECK(check_group(group));
+    const bool some = rows > 0;
+    DORA_CHECK(check_ptrs({{x, "x", some}, {q, "q", some}, {scale, "scale", some}}));
+    DORA_CHECK(check_disjoint({{{q, static_cast<size_t>(rows) * d}, "q"},
+                               {{scale, scale_bytes(rows, d, group)}, "scale"}},
+                              {{{x, rows * d * esize(dtype)}, "x"}}));
+    DORA_LAUNCH(launch_quantize_rows(dtype == DORA_BF16, x, rows, d, static_cast<int>(group),
+                                     static_cast<int8_t *>(q), scale,
+                                     static_cast<hipStream_t>(stream)),
+                "quantize rows");
+    return DORA_OK;
+}
+
+int dora_dequantize_rows(const void *q, const float *scale, int64_t rows, int64_t d, int dtype,
+                         int64_t group, void *out, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(rows, d));
+    DORA_CHECK(check_group(group));
+    const bool some = rows > 0;
+    DORA_CHECK(check_ptrs({{q, "q", some}, {scale, "scale", some}, {out, "out", some}}));
+    DORA_CHECK(check_disjoint({{{out, rows * d * esize(dtype)}, "out"}},
+                              {{{q, static_cast<size_t>(rows) * d}, "q"},
+                               {{scale, scale_bytes(rows, d, group)}, "scale"}}));
+    DORA_LAUNCH(launch_dequantize_rows(dtype == DORA_BF16, static_cast<const int8_t *>(q), scale,
+                                       rows, d, static_cast<int>(group), out,
+                                       static_cast<hipStream_t>(stream)),
+                "dequantize rows");
+    return DORA_OK;
+}
+
+size_t dora_linear_quantized_workspace(int64_t T, int64_t d_in, int64_t d_out, int dtype)
+{
+    if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, 8) || check_i8_width(d_in))
+        return 0;
+    return align_up(plan_gemm_i8(T, d_out, d_in).part_bytes);
+}
+
+int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const float *wscale,
+                          int64_t T, int64_t d_in, int64_t d_out, int dtype, void *y, void *ws,
+                          size_t ws_bytes, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_dims(dtype, T, d_in, d_out, 8));
+    DORA_CHECK(check_i8_width(d_in));
+    const bool has_t = T > 0;
+    DORA_CHECK(check_ptrs({{xq, "xq", has_t}, {xs, "xs", has_t}, {wq, "wq", true},
+                           {wscale, "wscale", true}, {y, "y", has_t}}));
+    const I8Plan p = plan_gemm_i8(T, d_out, d_in);
+    const size_t need = align_up(p.part_bytes);
+    DORA_CHECK(check_ws(ws, ws_bytes, need));
+    DORA_CHECK(check_disjoint(
+        {{{y, T * d_out * esize(dtype)}, "y"}, {{ws, need}, "workspace"}},
+        {{{xq, static_cast<size_t>(T) * d_in}, "xq"}, {{xs, T * sizeof(float)}, "xs"},
+         {{wq, static_cast<size_t>(d_out) * d_in}, "wq"}, {{wscale, d_out * sizeof(float)}, "wscale"}}));
+    I8GemmArgs g{};
+    g.x = static_cast<const int8_t *>(xq);
+    g.w = static_cast<const int8_t *>(wq);
+    g.xs = xs;
+    g.ws = wscale;
+    g.y = y;
+    g.M = T;
+    g.N = d_out;
+    g.K = d_in;
+    DORA_LAUNCH(launch_gemm_i8(dtype == DORA_BF16, g, p, ws, static_cast<hipStream_t>(stream)),
+                "linear xq wq^T");
+    return DORA_OK;
+}
+
+// The backward from 8-bit checkpoints: x restored into the workspace (the
+// product that reads it takes matrices of the element type), y read in 8 bits
+// by the dh/dm pass.
+namespace {
+struct CkptPlan {
+    BwdPlan b;
+    ThruPlan t;
+    size_t o_x, o_bwd, bytes;
+};
+
+CkptPlan plan_checkpoint(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype,
+                         int through_norm)
+{
+    CkptPlan p;
+    Carve cv;
+    p.o_x = cv.take(static_cast<size_t>(T) * d_in * esize(dtype));
+    p.o_bwd = cv.off;
+    if (through_norm)
+        p.t = plan_through_norm(T, d_in, d_out, r, dtype, true);
+    else
+        p.b = plan_backward(T, d_in, d_out, r, dtype, true);
+    cv.take(through_norm ? p.t.bytes : p.b.bytes);
+    p.bytes = cv.off;
+    return p;
+}
+}  // namespace
+
+size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
+                                          int dtype, int through_norm)
+{
+    if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, r))
+        return 0;
+    return plan_checkpoint(T, d_in, d_out, r, dtype, through_norm).bytes;
+}
+
+int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, const void *W,
+                             const void *A, const void *B, const float *m, const float *n, float s,
+                             const void *P, const void *yq, const float *ys, int64_t group,
+                             const float *U, int through_norm, int64_t T, int64_t d_in,
+                             int64_t d_out, int64_t r, int dtype, void *dx, void *dA, void *dB,
+                             float *dm, void *ws, size_t ws_bytes, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_dims(dtype, T, d_in, d_out, r));
+    DORA_CHECK(check_group(group));
+    if (U && !through_norm)
+        return fail(DORA_E_VALUE, "U is used by the backward through the norm only");
+    const bool has_t = T > 0;
+    DORA_CHECK(check_ptrs({{dy, "dy", has_t}, {xq, "xq", has_t}, {xs, "xs", has_t}, {W, "W", true},
+                           {A, "A", true}, {B, "B", true}, {m, "m", true}, {n, "n", true},
+                           {P, "P", has_t}, {yq, "yq", has_t}, {ys, "ys", has_t},
+                           {dx, "dx", has_t}, {dA, "dA", true}, {dB, "dB", true},
+                           {dm, "dm", true}, {U, "U", false}}));
+    const CkptPlan p = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm);
+    DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
+    const size_t e = esize(dtype);
+    DORA_CHECK(check_disjoint(
+        {{{dx, T * d_in * e}, "dx"}, {{dA, r * d_in * e}, "dA"}, {{dB, d_out * r * e}, "dB"},
+         {{dm, d_out * sizeof(float)}, "dm"}, {{ws, p.bytes}, "workspace"}},
+        {{{dy, T * d_out * e}, "dy"}, {{xq, static_cast<size_t>(T) * d_in}, "xq"},
+         {{xs, scale_bytes(T, d_in, group)}, "xs"}, {{W, d_out * d_in * e}, "W"},
+         {{A, r * d_in * e}, "A"}, {{B, d_out * r * e}, "B"}, {{m, d_out * sizeof(float)}, "m"},
+         {{n, d_out * sizeof(float)}, "n"}, {{P, T * r * e}, "P"},
+         {{yq, static_cast<size_t>(T) * d_out}, "yq"}, {{ys, scale_bytes(T, d_out, group)}, "ys"},
+         {{U, d_out * r * sizeof(float)}, "U"}}));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool bf = dtype == DORA_BF16;
+    char *w = static_cast<char *>(ws);
+    DORA_LAUNCH(launch_dequantize_rows(bf, static_cast<const int8_t *>(xq), xs, T, d_in,
+                                       static_cast<int>(group), w + p.o_x, st),
+                "restore x");
+    const Rows8 y8{static_cast<const int8_t *>(yq), ys, static_cast<int>(group)};
+    if (through_norm)
+        return through_norm_impl(p.t, dy, w + p.o_x, W, A, B, m, n, s, P, nullptr, &y8, U, T, d_in,
+                                 d_out, r, dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
+    return backward_impl(p.b, dy, w + p.o_x, W, A, B, m, n, s, P, nullptr, &y8, T, d_in, d_out, r,
+                         dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
 }
 
 }  // extern "C"

@@ -231,6 +231,58 @@ hipError_t launch_norm_finish_grouped(const ItemGroup<NormFinishItem> &g, hipStr
 hipError_t launch_copy_f32(const float *src, float *dst, int64_t n, hipStream_t st);
 hipError_t launch_fill_f32(float *dst, float v, int64_t n, hipStream_t st);
 
+// The row kernels around a module (rows8.hip).  `group`: 0 (one scale a row)
+// or a power of two from 32 to 512 (one scale for that many columns; the
+// scales are then [T, ceil(d / group)]).
+struct NormArgs {
+    const void *x, *res, *w;  // res may be null
+    float eps;
+    int group;
+    int64_t T, d;
+    void *y, *h;   // each may be null
+    float *rstd;   // may be null
+    int8_t *q;     // may be null; with it, scale
+    float *scale;
+};
+hipError_t launch_rmsnorm(int bf16, const NormArgs &a, hipStream_t st);
+struct NormGradArgs {
+    const void *dy, *h, *w, *dres;  // dres may be null
+    const float *rstd;
+    int64_t T, d;
+    void *dx;
+    float *dw_part;  // [parts, d] partial sums of dw
+    int parts;
+};
+// Partial sums of dw the gradient keeps (its workspace is parts * d floats).
+int rmsnorm_parts(int64_t T, int64_t d);
+// dw null: not formed.
+hipError_t launch_rmsnorm_grad(int bf16, const NormGradArgs &a, float *dw, hipStream_t st);
+hipError_t launch_quantize_rows(int bf16, const void *x, int64_t rows, int64_t d, int group,
+                                int8_t *q, float *scale, hipStream_t st);
+hipError_t launch_dequantize_rows(int bf16, const int8_t *q, const float *scale, int64_t rows,
+                                  int64_t d, int group, void *out, hipStream_t st);
+// launch_dh_dm_partial with y held as 8-bit rows (dm sums of dy (q scale)).
+hipError_t launch_dh_dm_rows8(int bf16, const void *dy, const int8_t *yq, const float *ys,
+                              int group, const float *m, const float *n, int64_t T, int64_t d_out,
+                              int64_t sweep, void *dh, float *dm_part, hipStream_t st);
+
+// y[m, n] = xs[m] ws[n] sum_k x[m, k] w[n, k], int8 operands (gemm_i8.hip).
+struct I8GemmArgs {
+    const int8_t *x, *w;
+    const float *xs, *ws;
+    void *y;
+    int *part;  // split products: int32 partial sums [splits, M, N], else null
+    int64_t M, N, K;
+    int64_t k_per_split;
+};
+struct I8Plan {
+    int splits;
+    int64_t k_per_split;
+    size_t part_bytes;
+};
+I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hipStream_t st);
+
 // The thread-local message dora_last_error() returns (dora_api.cpp): set it
 // and return `status`, or clear it.
 int set_error(int status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));

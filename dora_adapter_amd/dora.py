@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(HERE, "libdora.so")
 
 DORA_F32, DORA_BF16 = 0, 1
 STATUS = {0: "DORA_OK", 1: "DORA_E_NULL", 2: "DORA_E_SHAPE", 3: "DORA_E_DTYPE",
-          4: "DORA_E_ALIGN", 5: "DORA_E_WORKSPACE", 6: "DORA_E_ALIAS", 7: "DORA_E_HIP"}
+          4: "DORA_E_ALIGN", 5: "DORA_E_WORKSPACE", 6: "DORA_E_ALIAS", 7: "DORA_E_HIP",
+          8: "DORA_E_VALUE"}
 
 # Every symbol include/dora.h declares.
 EXPORTS = ("dora_strerror", "dora_last_error", "dora_norm_workspace", "dora_forward_workspace",
@@ -24,7 +25,11 @@ EXPORTS = ("dora_strerror", "dora_last_error", "dora_norm_workspace", "dora_forw
            "dora_backward", "dora_linear_workspace", "dora_linear", "dora_merge_workspace",
            "dora_merge", "dora_backward_through_norm_workspace", "dora_backward_through_norm",
            "dora_factored_norm_grouped_workspace", "dora_factored_norm_grouped",
-           "dora_forward_grouped_workspace", "dora_forward_grouped", "dora_forward_noalloc")
+           "dora_forward_grouped_workspace", "dora_forward_grouped", "dora_forward_noalloc",
+           "dora_rmsnorm", "dora_rmsnorm_backward_workspace", "dora_rmsnorm_backward",
+           "dora_quantize_rows", "dora_dequantize_rows", "dora_linear_quantized_workspace",
+           "dora_linear_quantized", "dora_backward_checkpoint_workspace",
+           "dora_backward_checkpoint")
 
 _lib = None
 
@@ -97,6 +102,25 @@ def lib():
         L.dora_merge_workspace.argtypes = [i64, i64, i64, c_int]
         L.dora_merge.restype = c_int
         L.dora_merge.argtypes = [p, p, p, p, f, i64, i64, i64, c_int, p, p, p, sz, p]
+        L.dora_rmsnorm.restype = c_int
+        L.dora_rmsnorm.argtypes = [p, p, p, f, i64, i64, c_int, i64, p, p, p, p, p, p]
+        L.dora_rmsnorm_backward_workspace.restype = sz
+        L.dora_rmsnorm_backward_workspace.argtypes = [i64, i64, c_int]
+        L.dora_rmsnorm_backward.restype = c_int
+        L.dora_rmsnorm_backward.argtypes = [p, p, p, p, p, i64, i64, c_int, p, p, p, sz, p]
+        L.dora_quantize_rows.restype = c_int
+        L.dora_quantize_rows.argtypes = [p, i64, i64, c_int, i64, p, p, p]
+        L.dora_dequantize_rows.restype = c_int
+        L.dora_dequantize_rows.argtypes = [p, p, i64, i64, c_int, i64, p, p]
+        L.dora_linear_quantized_workspace.restype = sz
+        L.dora_linear_quantized_workspace.argtypes = [i64, i64, i64, c_int]
+        L.dora_linear_quantized.restype = c_int
+        L.dora_linear_quantized.argtypes = [p, p, p, p, i64, i64, i64, c_int, p, p, sz, p]
+        L.dora_backward_checkpoint_workspace.restype = sz
+        L.dora_backward_checkpoint_workspace.argtypes = [i64, i64, i64, i64, c_int, c_int]
+        L.dora_backward_checkpoint.restype = c_int
+        L.dora_backward_checkpoint.argtypes = [p, p, p, p, p, p, p, p, f, p, p, p, i64, p, c_int,
+                                               i64, i64, i64, i64, c_int, p, p, p, p, p, sz, p]
         _lib = L
     return _lib
 
@@ -362,3 +386,215 @@ def dora_forward_grouped(x, mods, n_in=None, want_P=True, ws=None, ys=None, ns=N
     _check(lib().dora_forward_grouped(_ptr(x), T, d_in, arr, len(mods), dt, vp(py), vp(pn),
                                       vp(pP), vp(pnin), _ptr(ws), ws.numel(), _stream(dev)))
     return ys, ns, Ps
+
+
+# ------------------------------------------------ 8-bit rows and their users
+# The calls below check what they are given: every tensor on one device,
+# contiguous, of the type and shape the call documents (ValueError, TypeError
+# otherwise), and they launch with that device current.
+
+def _need(name, t, dev, dtype, *shape):
+    """Refuse a tensor that is not what the library would read."""
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t
+
+
+def _rows(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has {t.dim()} dimensions, not 2")
+    return t.shape
+
+
+def _groups(d, group):
+    """Scales of a row of d values (one, or one for each `group` columns)."""
+    if group == 0:
+        return 1
+    if group not in (32, 64, 128, 256, 512):
+        raise ValueError(f"group {group} is neither 0 nor a power of two from 32 to 512")
+    return -(-d // group)
+
+
+def _need_ws(ws, dev):
+    if ws is not None:
+        if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+            raise ValueError(f"ws is not a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def _launch(dev, call, *args):
+    """The call on the current stream of `dev`, with `dev` current."""
+    if torch.cuda.current_device() == dev.index:
+        _check(call(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(*args, _stream(dev)))
+
+
+def dora_rmsnorm(x, w, eps=1e-6, residual=None, want_y=True, want_h=None, want_rstd=False,
+                 quantize=False, group=0, out=None):
+    """h = x + residual (rounded to the element type) and y = w h / sqrt(mean(h^2) + eps) by
+    rows of x [T, d].  Returns a dict of what was asked for: "y", "h" (want_h; by default with
+    a residual), "rstd" (fp32 [T], for the backward), and with quantize "q" (int8 [T, d]) and
+    "scale" (fp32 [T, groups]: one group, or one for each `group` columns) standing for y.
+    out: a dict of preallocated outputs; then those are what is asked for.  out["h"] may be x
+    or residual, out["y"] may be x."""
+    dev = _dev(x)
+    T, d = _rows("x", x)
+    dt = _dt(x)
+    n = _groups(d, group)
+    _need("x", x, dev, x.dtype, T, d)
+    _need("w", w, dev, x.dtype, d)
+    if residual is not None:
+        _need("residual", residual, dev, x.dtype, T, d)
+    kinds = {"y": (x.dtype, T, d), "h": (x.dtype, T, d), "rstd": (torch.float32, T),
+             "q": (torch.int8, T, d), "scale": (torch.float32, T, n)}
+    if out is None:
+        want = {"y": want_y, "h": residual is not None if want_h is None else want_h,
+                "rstd": want_rstd, "q": quantize, "scale": quantize}
+        out = {k: torch.empty(*v[1:], dtype=v[0], device=dev) for k, v in kinds.items()
+               if want[k]}
+    else:
+        for k, t in out.items():
+            if k not in kinds:
+                raise ValueError(f"out has no place for {k!r}")
+            _need(k, t, dev, *kinds[k])
+        if ("q" in out) != ("scale" in out):
+            raise ValueError("q and scale come together")
+    if "y" not in out and "q" not in out:
+        raise ValueError("neither y nor its 8-bit form is asked for")
+    _launch(dev, lib().dora_rmsnorm, _ptr(x), _ptr(residual), _ptr(w), float(eps), T, d, dt, group,
+            _ptr(out.get("y")), _ptr(out.get("h")), _ptr(out.get("rstd")), _ptr(out.get("q")),
+            _ptr(out.get("scale")))
+    return out
+
+
+def dora_rmsnorm_backward_workspace(T, d, dtype):
+    return lib().dora_rmsnorm_backward_workspace(T, d, dtype)
+
+
+def dora_rmsnorm_backward(dy, h, w, rstd, dres=None, ws=None, out=None):
+    """Gradients of dora_rmsnorm from the h and rstd it returned: dict(dx, dw), dx [T, d] the
+    gradient of x (and of the residual), dw fp32 [d].  dres: the gradient that reaches h along
+    the residual stream, added to dx (out["dx"] may be dres)."""
+    dev = _dev(dy)
+    T, d = _rows("dy", dy)
+    dt = _dt(dy)
+    _need("dy", dy, dev, dy.dtype, T, d)
+    _need("h", h, dev, dy.dtype, T, d)
+    _need("w", w, dev, dy.dtype, d)
+    _need("rstd", rstd, dev, torch.float32, T)
+    if dres is not None:
+        _need("dres", dres, dev, dy.dtype, T, d)
+    if out is None:
+        out = {"dx": torch.empty_like(dy), "dw": torch.empty(d, dtype=torch.float32, device=dev)}
+    else:
+        _need("dx", out["dx"], dev, dy.dtype, T, d)
+        _need("dw", out["dw"], dev, torch.float32, d)
+    if _need_ws(ws, dev) is None:
+        ws = _ws(dora_rmsnorm_backward_workspace(T, d, dt), dev)
+    _launch(dev, lib().dora_rmsnorm_backward, _ptr(dy), _ptr(h), _ptr(w), _ptr(rstd), _ptr(dres),
+            T, d, dt, _ptr(out["dx"]), _ptr(out["dw"]), _ptr(ws), ws.numel())
+    return out
+
+
+def dora_quantize_rows(x, group=0, q=None, scale=None):
+    """Rows of x [T, d] as int8 values and fp32 scales [T, groups]: q = rint(x / scale), scale =
+    max|x| / 127 over the row (group 0) or over each `group` columns.  Returns (q, scale)."""
+    dev = _dev(x)
+    T, d = _rows("x", x)
+    dt = _dt(x)
+    n = _groups(d, group)
+    _need("x", x, dev, x.dtype, T, d)
+    q = torch.empty(T, d, dtype=torch.int8, device=dev) if q is None \
+        else _need("q", q, dev, torch.int8, T, d)
+    scale = torch.empty(T, n, dtype=torch.float32, device=dev) if scale is None \
+        else _need("scale", scale, dev, torch.float32, T, n)
+    _launch(dev, lib().dora_quantize_rows, _ptr(x), T, d, dt, group, _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def dora_dequantize_rows(q, scale, group=0, dtype=torch.bfloat16, out=None):
+    """The values int8 rows stand for, q scale, in `dtype` (or in out's)."""
+    dev = _dev(q)
+    T, d = _rows("q", q)
+    _need("q", q, dev, torch.int8, T, d)
+    _need("scale", scale, dev, torch.float32, T, _groups(d, group))
+    out = torch.empty(T, d, dtype=dtype, device=dev) if out is None \
+        else _need("out", out, dev, out.dtype, T, d)
+    _launch(dev, lib().dora_dequantize_rows, _ptr(q), _ptr(scale), T, d, _dt(out), group,
+            _ptr(out))
+    return out
+
+
+def dora_linear_quantized_workspace(T, d_in, d_out, dtype):
+    return lib().dora_linear_quantized_workspace(T, d_in, d_out, dtype)
+
+
+def dora_linear_quantized(xq, xs, wq, wscale, dtype=torch.bfloat16, y=None, ws=None):
+    """y = (xs xq) (wscale wq)^T: the linear layer of a merged weight in int8, one scale per
+    token (xs [T, 1]) and one per output channel (wscale [d_out, 1]), as dora_rmsnorm and
+    dora_quantize_rows give them with group 0.  int32 sums; y [T, d_out] in `dtype` (or y's)."""
+    dev = _dev(xq)
+    T, d_in = _rows("xq", xq)
+    d_out = _rows("wq", wq)[0]
+    _need("xq", xq, dev, torch.int8, T, d_in)
+    _need("wq", wq, dev, torch.int8, d_out, d_in)
+    _need("xs", xs, dev, torch.float32, T, 1)
+    _need("wscale", wscale, dev, torch.float32, d_out, 1)
+    y = torch.empty(T, d_out, dtype=dtype, device=dev) if y is None \
+        else _need("y", y, dev, y.dtype, T, d_out)
+    dt = _dt(y)
+    if _need_ws(ws, dev) is None:
+        need = dora_linear_quantized_workspace(T, d_in, d_out, dt)
+        ws = _ws(need, dev) if need > 0 else None
+    _launch(dev, lib().dora_linear_quantized, _ptr(xq), _ptr(xs), _ptr(wq), _ptr(wscale), T, d_in,
+            d_out, dt, _ptr(y), _ptr(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+def dora_backward_checkpoint_workspace(T, d_in, d_out, r, dtype, through_norm=False):
+    return lib().dora_backward_checkpoint_workspace(T, d_in, d_out, r, dtype, int(through_norm))
+
+
+def dora_backward_checkpoint(dy, xq, xs, W, A, B, m, n, s, P, yq, ys, group=0, through_norm=False,
+                             U=None, ws=None, out=None):
+    """dora_backward (or, with through_norm, dora_backward_through_norm) from x and y kept in 8
+    bits by dora_quantize_rows (or dora_rmsnorm) with this `group`; returns
+    dict(dx, dA, dB, dm)."""
+    dev = _dev(dy)
+    T, d_out = _rows("dy", dy)
+    r, d_in = _rows("A", A)
+    dt = _dt(dy)
+    f32 = torch.float32
+    for name, t, kind, shape in (
+            ("dy", dy, dy.dtype, (T, d_out)), ("xq", xq, torch.int8, (T, d_in)),
+            ("xs", xs, f32, (T, _groups(d_in, group))), ("W", W, dy.dtype, (d_out, d_in)),
+            ("A", A, dy.dtype, (r, d_in)), ("B", B, dy.dtype, (d_out, r)), ("m", m, f32, (d_out,)),
+            ("n", n, f32, (d_out,)), ("P", P, dy.dtype, (T, r)),
+            ("yq", yq, torch.int8, (T, d_out)), ("ys", ys, f32, (T, _groups(d_out, group)))):
+        _need(name, t, dev, kind, *shape)
+    if U is not None:
+        if not through_norm:
+            raise ValueError("U is used by the backward through the norm only")
+        _need("U", U, dev, f32, d_out, r)
+    kinds = {"dx": (dy.dtype, T, d_in), "dA": (dy.dtype, r, d_in), "dB": (dy.dtype, d_out, r),
+             "dm": (f32, d_out)}
+    if out is None:
+        out = {k: torch.empty(*v[1:], dtype=v[0], device=dev) for k, v in kinds.items()}
+    else:
+        for k, v in kinds.items():
+            _need(k, out[k], dev, *v)
+    if _need_ws(ws, dev) is None:
+        ws = _ws(dora_backward_checkpoint_workspace(T, d_in, d_out, r, dt, through_norm), dev)
+    _launch(dev, lib().dora_backward_checkpoint, _ptr(dy), _ptr(xq), _ptr(xs), _ptr(W), _ptr(A),
+            _ptr(B), _ptr(m), _ptr(n), float(s), _ptr(P), _ptr(yq), _ptr(ys), group, _ptr(U),
+            int(through_norm), T, d_in, d_out, r, dt, _ptr(out["dx"]), _ptr(out["dA"]),
+            _ptr(out["dB"]), _ptr(out["dm"]), _ptr(ws), ws.numel())
+    return out

@@ -70,7 +70,8 @@ typedef enum {
     DORA_E_ALIGN = 4,     /* a pointer is not 16-byte aligned                */
     DORA_E_WORKSPACE = 5, /* ws is NULL or ws_bytes is below the query       */
     DORA_E_ALIAS = 6,     /* two buffers overlap where that is not allowed   */
-    DORA_E_HIP = 7        /* a HIP launch or runtime call failed             */
+    DORA_E_HIP = 7,       /* a HIP launch or runtime call failed             */
+    DORA_E_VALUE = 8      /* a scalar argument is out of range               */
 } dora_status;
 
 typedef enum {
@@ -323,6 +324,97 @@ int dora_forward_noalloc(const void *x, const void *W, const void *A, const void
                          const float *m, float s, int64_t T, int64_t d_in, int64_t d_out,
                          int64_t r, int dtype, void *y, float *n_out, void *P_out,
                          const float *n_in, float *U_out, void *stream);
+
+/*
+ * 8-bit rows.  A matrix [rows, d] is held as int8 values q [rows, d] with fp32
+ * scales: one a row (group = 0, scale [rows, 1]) or one for each `group`
+ * consecutive columns (group a power of two from 32 to 512, scale
+ * [rows, ceil(d / group)]; the last group of a row may be short).  Within a
+ * group with values v_j
+ *     scale = max_j |v_j| / 127          (0 for a group of zeros)
+ *     q_j   = rint(v_j / scale)          ties to even, decided exactly
+ * and q_j stands for q_j scale.  The scale is kept between 2^-126 and the
+ * largest one for which 127 scale is finite.  A group that holds an infinity
+ * or a NaN gets a NaN scale: it stands for NaN throughout.
+ * Rows of int8 need no alignment of their own (any d); the buffers do.
+ *
+ * dora_rmsnorm - the root-mean-square norm in front of an adapted projection,
+ * with the residual's addition:
+ *     h    = x + residual   summed in fp32, rounded to `dtype` (x without one)
+ *     rstd = 1 / sqrt(mean_j h_j^2 + eps)          of the rounded h, in fp32
+ *     y    = w (.) h rstd   in fp32, rounded once to `dtype` (y), and / or
+ *            held as 8-bit rows (q, scale) taken from the unrounded y
+ *   x, residual (nullable) [T, d], w [d] in `dtype`; eps finite, >= 0.
+ *   y [T, d], h [T, d] in `dtype`, rstd [T] fp32, q [T, d] int8 with scale
+ *   [T, groups] fp32: each NULL to skip, but y or q is required and q needs
+ *   scale.  h may be x or residual itself, y may be x itself; no other
+ *   overlap.
+ *   q with group = 0 is dora_linear_quantized's xq; any group serves
+ *   dora_backward_checkpoint.
+ *
+ * dora_rmsnorm_backward - its gradient, from the h and rstd it returned:
+ *     dx   = dres + rstd (w (.) dy) - h rstd^3 / d * sum_j w_j dy_j h_j
+ *     dw_j = sum_t dy_tj h_tj rstd_t
+ *   dx is the gradient of x and, with a residual, of the residual too.  dres
+ *   [T, d] (nullable) is the gradient that reaches h along the residual
+ *   stream; dx may be dres itself.  dy, h, dres, dx [T, d], w [d] in `dtype`,
+ *   rstd [T], dw [d] fp32 (dw NULL to skip; ws may then be NULL).  T = 0
+ *   gives dw = 0.
+ */
+int dora_rmsnorm(const void *x, const void *residual, const void *w, float eps, int64_t T,
+                 int64_t d, int dtype, int64_t group, void *y, void *h, float *rstd, void *q,
+                 float *scale, void *stream);
+size_t dora_rmsnorm_backward_workspace(int64_t T, int64_t d, int dtype);
+int dora_rmsnorm_backward(const void *dy, const void *h, const void *w, const float *rstd,
+                          const void *dres, int64_t T, int64_t d, int dtype, void *dx, float *dw,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * dora_quantize_rows / dora_dequantize_rows - a matrix [rows, d] of `dtype` to
+ * 8-bit rows and back (see above).  With group = 0 and x = the merged weight
+ * of dora_merge, q and scale are dora_linear_quantized's wq and wscale.
+ * Restored values are q scale in fp32, rounded once to `dtype`, which need not
+ * be the type the rows came from.
+ */
+int dora_quantize_rows(const void *x, int64_t rows, int64_t d, int dtype, int64_t group, void *q,
+                       float *scale, void *stream);
+int dora_dequantize_rows(const void *q, const float *scale, int64_t rows, int64_t d, int dtype,
+                         int64_t group, void *out, void *stream);
+
+/*
+ * dora_linear_quantized - dora_linear in 8-bit integers, for a merged weight
+ * held as 8-bit rows: one scale per token and one per output channel,
+ *     y[t, i] = xs[t] wscale[i] sum_k xq[t, k] wq[i, k]
+ * with exact int32 sums, scaled in fp32 and rounded once to `dtype` (the type
+ * of y).  xq [T, d_in], wq [d_out, d_in] int8, xs [T], wscale [d_out] fp32.
+ * d_in <= 131071 (beyond, int32 sums could overflow).  y must not overlap any
+ * input.  ws: dora_linear_quantized_workspace(T, d_in, d_out, dtype) bytes
+ * (0: ws may be NULL).
+ */
+size_t dora_linear_quantized_workspace(int64_t T, int64_t d_in, int64_t d_out, int dtype);
+int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const float *wscale,
+                          int64_t T, int64_t d_in, int64_t d_out, int dtype, void *y, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/*
+ * dora_backward_checkpoint - dora_backward (through_norm = 0) or
+ * dora_backward_through_norm (otherwise) with the forward's x and y kept
+ * between the passes as 8-bit rows, half the bytes of bf16: xq [T, d_in] with
+ * xs and yq [T, d_out] with ys, both of this `group`.  The gradients are those
+ * of the restored x = xq xs and y = yq ys; x is rounded to `dtype` where a
+ * matrix product reads it, y enters dm in fp32.  All other arguments, layouts,
+ * aliasing rules and the T = 0 case are those of the two calls.
+ * ws: dora_backward_checkpoint_workspace(...) bytes, which hold x restored for
+ * the duration of the call.
+ */
+size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
+                                          int dtype, int through_norm);
+int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, const void *W,
+                             const void *A, const void *B, const float *m, const float *n, float s,
+                             const void *P, const void *yq, const float *ys, int64_t group,
+                             const float *U, int through_norm, int64_t T, int64_t d_in,
+                             int64_t d_out, int64_t r, int dtype, void *dx, void *dA, void *dB,
+                             float *dm, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,204 @@
+"""GPU: the module's backward from x and y kept in 8 bits, against the plain
+form in 64 bits on the restored values.
+
+Tolerances: dm is an fp32 sum of T products: (T + 8) 2^-24 sum_t |dy y| / |m|.
+The others follow the rules of the unquantized backward (gpu_util: 1e-5 or
+2e-2 of max(|ref|, rms)), or the bound of the operands stored in bf16 where a
+few tokens cancel; x restored to bf16 adds 2^-8 |Q|^T |x| to dA's."""
+import numpy as np
+import pytest
+import torch
+
+import rows8_ref as R
+from dora_adapter_amd import dora as D
+from dora_adapter_amd import synth
+from gpu_util import check_close, np64, reduction_bound_bf16, say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def module(T, d_in, d_out, r, dt, s, seed):
+    name = "bf16" if dt == BF else "f32"
+    mod = synth.custom(d_out, d_in, r, T, name, s=s, seed=seed, with_dy=True)
+    t = {k: mod[k].to(DEV) for k in ("x", "W", "A", "B", "m", "dy")}
+    return mod, t
+
+
+def check(mod, t, group, through, keep_U, n, P, y, U):
+    s, dt = mod["s"], mod["dtype"]
+    T, d_in = mod["x"].shape
+    d_out = mod["W"].shape[0]
+    xq, xs = D.dora_quantize_rows(t["x"], group=group)
+    yq, ys = D.dora_quantize_rows(y, group=group)
+    g = D.dora_backward_checkpoint(t["dy"], xq, xs, t["W"], t["A"], t["B"], t["m"], n, s, P, yq, ys,
+                                   group=group, through_norm=through, U=U if keep_U else None)
+    torch.cuda.synchronize()
+    xr = xq.cpu().double() * R.spread(xs.cpu(), d_in, group)
+    yr = yq.cpu().double() * R.spread(ys.cpu(), d_out, group)
+    ref = R.backward(mod["dy"], xr, mod["W"], mod["A"], mod["B"], mod["m"], n.cpu(), s, P.cpu(), yr,
+                     through)
+    each = (mod["dy"].double() * yr).abs().sum(0) / mod["m"].double().abs()
+    off = (g["dm"].cpu().double() - ref["dm"]).abs()
+    assert (off <= (T + 8) * 2.0 ** -24 * each + 1e-30).all(), "dm"
+    bounds = {}
+    if dt == BF:
+        bA, bB = reduction_bound_bf16(mod["dy"], xr, mod["W"], mod["A"], mod["B"], mod["m"],
+                                      n.cpu(), ref["dm"], s, through)
+        Q = s * (mod["dy"].double() * (mod["m"] / n.cpu()).double()) @ mod["B"].double()
+        bA = bA + 2.0 ** -8 * np64(Q.abs().T @ xr.abs())
+        bounds = {"dA": bA + 2.0 ** -8 * np.abs(np64(ref["dA"])),
+                  "dB": bB + 2.0 ** -8 * np.abs(np64(ref["dB"]))}
+    for k in ("dx", "dA", "dB"):
+        check_close(g[k], ref[k], dt, k, bound=bounds.get(k), cos=T > 8)
+    return g, xq, xs, yq, ys
+
+
+SIZES = [(1, 64, 48, 8), (5, 100, 37, 3), (16, 128, 64, 8), (40, 264, 136, 24), (33, 1027, 411, 37),
+         (130, 520, 776, 64), (257, 1032, 512, 96), (1000, 72, 2056, 16)]
+
+
+@pytest.mark.parametrize("through", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,d_in,d_out,r", SIZES)
+def test_backward_checkpoint_matches_plain_form(T, d_in, d_out, r, dt, through):
+    mod, t = module(T, d_in, d_out, r, dt, 1.5, T + r)
+    U = torch.empty(d_out, r, device=DEV)
+    say("forward", T, d_in, d_out, r, dt)
+    y, n, P = D.dora_forward(t["x"], t["W"], t["A"], t["B"], t["m"], mod["s"], U_out=U)
+    for group, keep_U in ((0, False), (128, through), (32, False)):
+        say("backward from 8 bits", T, d_in, d_out, r, dt, through, group)
+        check(mod, t, group, through, keep_U, n, P, y, U)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_products_are_those_of_the_unquantized_backward(dt):
+    """On x and y that are what their 8-bit rows stand for, dx and dA are the
+    unquantized backward's, bit for bit (the same products on the same
+    operands)."""
+    mod, t = module(160, 256, 192, 16, dt, 1.0, 3)
+    y, n, P = D.dora_forward(t["x"], t["W"], t["A"], t["B"], t["m"], 1.0)
+    xq, xs = D.dora_quantize_rows(t["x"], group=64)
+    yq, ys = D.dora_quantize_rows(y, group=64)
+    say("backward from 8 bits against the backward", dt)
+    a = D.dora_backward_checkpoint(t["dy"], xq, xs, t["W"], t["A"], t["B"], t["m"], n, 1.0, P, yq,
+                                   ys, group=64)
+    x1 = D.dora_dequantize_rows(xq, xs, group=64, dtype=dt)
+    y1 = D.dora_dequantize_rows(yq, ys, group=64, dtype=dt)
+    b = D.dora_backward(t["dy"], x1, t["W"], t["A"], t["B"], t["m"], n, 1.0, P, y1)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dA"], b["dA"])
+
+
+@pytest.mark.parametrize("through", [False, True])
+def test_no_tokens(through):
+    mod, t = module(4, 64, 48, 8, BF, 1.0, 1)
+    n = torch.ones(48, device=DEV)
+    e8 = lambda d: torch.empty(0, d, dtype=torch.int8, device=DEV)  # noqa: E731
+    sc = torch.empty(0, 1, device=DEV)
+    say("backward from 8 bits, T=0", through)
+    g = D.dora_backward_checkpoint(t["dy"][:0], e8(64), sc, t["W"], t["A"], t["B"], t["m"], n, 1.0,
+                                   torch.empty(0, 8, dtype=BF, device=DEV), e8(48), sc,
+                                   through_norm=through)
+    torch.cuda.synchronize()
+    assert all((g[k] == 0).all() for k in ("dA", "dB", "dm")) and g["dx"].shape == (0, 64)
+
+
+def test_refuses_what_it_cannot_read():
+    mod, t = module(16, 64, 48, 8, BF, 1.0, 1)
+    y, n, P = D.dora_forward(t["x"], t["W"], t["A"], t["B"], t["m"], 1.0)
+    xq, xs = D.dora_quantize_rows(t["x"])
+    yq, ys = D.dora_quantize_rows(y)
+
+    def call(xq=xq, xs=xs, P=P, ys=ys, group=0, **kw):
+        return D.dora_backward_checkpoint(t["dy"], xq, xs, t["W"], t["A"], t["B"], t["m"], n, 1.0,
+                                          P, yq, ys, group=group, **kw)
+
+    for kw in ({"xs": xs[:, 0]}, {"group": 32}, {"P": P[:8]}, {"xq": xq.T}, {"ys": ys[:3]},
+               {"U": torch.empty(48, 8, device=DEV)}):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(TypeError):
+        call(xq=t["x"])
+
+
+def chain(t, res, w, dy, dres, s, group):
+    """One training step of norm and module with 8-bit checkpoints."""
+    f = D.dora_rmsnorm(t["x"], w, residual=res, want_rstd=True, quantize=True, group=group)
+    y, n, P = D.dora_forward(f["y"], t["W"], t["A"], t["B"], t["m"], s)
+    yq, ys = D.dora_quantize_rows(y, group=group)
+    g = D.dora_backward_checkpoint(dy, f["q"], f["scale"], t["W"], t["A"], t["B"], t["m"], n, s, P,
+                                   yq, ys, group=group)
+    b = D.dora_rmsnorm_backward(g["dx"], f["h"], w, f["rstd"], dres=dres)
+    return {"y": y, "q": f["q"], "scale": f["scale"], "n": n, "P": P, "yq": yq, "ys": ys, **g,
+            "dh": b["dx"], "dw": b["dw"], "h": f["h"], "rstd": f["rstd"]}
+
+
+def test_norm_module_and_checkpoints_together():
+    T, d_in, d_out, r, s, group = 96, 264, 200, 16, 2.0, 128
+    mod, t = module(T, d_in, d_out, r, BF, s, 9)
+    g = torch.Generator().manual_seed(5)
+    res, dres = (torch.randn(T, d_in, generator=g).bfloat16() for _ in range(2))
+    w = (1 + 0.1 * torch.randn(d_in, generator=g)).bfloat16()
+    say("norm, module, 8-bit checkpoints, backward of both")
+    o = chain(t, res.to(DEV), w.to(DEV), t["dy"], dres.to(DEV), s, group)
+    h = R.norm_h(mod["x"], res)
+    assert torch.equal(o["h"].cpu(), h)
+    xr = o["q"].cpu().double() * R.spread(o["scale"].cpu(), d_in, group)
+    yr = o["yq"].cpu().double() * R.spread(o["ys"].cpu(), d_out, group)
+    ref = R.backward(mod["dy"], xr, mod["W"], mod["A"], mod["B"], mod["m"], o["n"].cpu(), s,
+                     o["P"].cpu(), yr, False)
+    for k in ("dx", "dA", "dB"):
+        check_close(o[k], ref[k], BF, k)
+    dh, dw, _, _ = R.norm_grad(o["dx"].cpu(), h, w, o["rstd"].cpu(), dres)
+    check_close(o["dh"], dh, BF, "dh")
+    check_close(o["dw"], dw, F32, "dw", cos=False)
+
+
+def test_captured_steps_replay_and_a_second_stream():
+    """The whole step captured into a graph, replayed on other inputs with
+    eager work between the replays; and the same step on a stream of its own."""
+    T, d_in, d_out, r, s, group = 80, 136, 264, 16, 1.0, 32
+    mod, t = module(T, d_in, d_out, r, BF, s, 2)
+    gen = torch.Generator(DEV).manual_seed(3)
+
+    def rnd(*sh):
+        return torch.randn(*sh, generator=gen, device=DEV).bfloat16()
+
+    res, dres, w = rnd(T, d_in), rnd(T, d_in), 1 + rnd(d_in) / 8
+    wq, ws = D.dora_quantize_rows(t["W"])
+
+    def step():
+        o = chain(t, res, w, t["dy"], dres, s, group)
+        e = D.dora_rmsnorm(t["x"], w, residual=res, want_y=False, quantize=True)
+        o["served"] = D.dora_linear_quantized(e["q"], e["scale"], wq, ws)
+        one = {k: e[k][:1] for k in ("q", "scale")}
+        o["token"] = D.dora_linear_quantized(one["q"], one["scale"], wq, ws)
+        return o
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    say("step on a second stream")
+    with torch.cuda.stream(side):
+        eager = step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    say("capture")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for k in range(4):
+        if k:
+            t["x"].copy_(rnd(T, d_in))
+            t["dy"].copy_(rnd(T, d_out))
+            res.copy_(rnd(T, d_in))
+        say("replay", k)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {key: v.clone() for key, v in kept.items()}
+        now = step()
+        torch.cuda.synchronize()
+        for key in now:
+            assert torch.equal(got[key], now[key]), (k, key)
+            if k == 0:
+                assert torch.equal(eager[key], now[key]), key

@@ -1,0 +1,135 @@
+"""GPU: the int8 linear layer against exact integer sums.
+
+The sums are exact, so y differs from the 64-bit value by the conversion of
+the sum (2^-24), the product of the scales (2^-24), their product (2^-24) and
+the output's rounding (half a step): all relative to y itself."""
+import pytest
+import torch
+
+import rows8_ref as R
+from dora_adapter_amd import dora as D
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def operands(seed, T, d_in, d_out, lo=-127):
+    g = torch.Generator().manual_seed(seed)
+    xq = torch.randint(lo, 128, (T, d_in), generator=g, dtype=torch.int8)
+    wq = torch.randint(lo, 128, (d_out, d_in), generator=g, dtype=torch.int8)
+    xs = torch.rand(T, 1, generator=g) * 0.1 + 0.01
+    ws = torch.rand(d_out, 1, generator=g) * 0.01 + 0.001
+    return xq, xs, wq, ws
+
+
+def check(ops, dt, what):
+    y = D.dora_linear_quantized(*[t.to(DEV) for t in ops], dtype=dt).cpu()
+    assert y.dtype == dt and y.shape == (ops[0].shape[0], ops[2].shape[0])
+    ref = R.linear(*ops)
+    lim = ref.abs() * (3.1 * 2.0 ** -24 + torch.finfo(dt).eps / 2)
+    off = (y.double() - ref).abs()
+    assert (off <= lim).all(), f"{what}: {int((off > lim).sum())} of {off.numel()} off"
+
+
+SIZES = [(1, 1, 1), (1, 8, 8), (1, 16, 3), (2, 17, 9), (3, 64, 130), (5, 1029, 257), (7, 63, 64),
+         (8, 4096, 512), (15, 100, 33), (16, 128, 129), (17, 2048, 256), (31, 144, 1000),
+         (33, 65, 127), (48, 4096, 520), (64, 512, 2051), (65, 1040, 264), (100, 192, 1024),
+         (128, 8192, 384), (129, 80, 136), (255, 1024, 512), (300, 4099, 260), (513, 256, 1032),
+         (777, 1029, 411), (1024, 2064, 768)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,d_in,d_out", SIZES)
+def test_linear_quantized_matches_exact_sums(T, d_in, d_out, dt):
+    say("int8 linear", T, d_in, d_out, dt)
+    check(operands(T + d_in, T, d_in, d_out), dt, f"{T} x {d_in} x {d_out}")
+
+
+@pytest.mark.parametrize("T", [1, 20, 200])
+def test_largest_sums_fit_32_bits(T):
+    d_in = 131071
+    say("int8 linear, all -128", T, d_in)
+    xq = torch.full((T, d_in), -128, dtype=torch.int8)
+    wq = torch.full((24, d_in), -128, dtype=torch.int8)
+    wq[1] = 127
+    check((xq, torch.ones(T, 1), wq, torch.ones(24, 1)), F32, "largest sums")
+
+
+def test_zero_and_nan_scales():
+    xq, xs, wq, ws = operands(4, 9, 256, 40)
+    xs[2] = 0
+    xs[5] = float("nan")
+    ws[7] = 0
+    say("int8 linear, zero and NaN scales")
+    y = D.dora_linear_quantized(*[t.to(DEV) for t in (xq, xs, wq, ws)]).cpu()
+    assert (y[2] == 0).all() and torch.isnan(y[5]).all()
+    keep = [0, 1, 3, 4, 6, 7, 8]
+    assert (y[keep][:, 7] == 0).all() and torch.isfinite(y[keep]).all()
+
+
+def test_empty_tokens_and_rows_behind_the_last():
+    xq, xs, wq, ws = [t.to(DEV) for t in operands(5, 12, 320, 72)]
+    say("int8 linear T=0")
+    assert D.dora_linear_quantized(xq[:0], xs[:0], wq, ws).shape == (0, 72)
+    for T in (1, 5):
+        y = torch.full((12, 72), 3.0, dtype=BF, device=DEV)
+        say("int8 linear, rows of a larger buffer", T)
+        D.dora_linear_quantized(xq[:T], xs[:T], wq, ws, y=y[:T])
+        assert (y[T:] == 3).all() and not (y[:T] == 3).all()
+
+
+def test_results_do_not_depend_on_the_batch():
+    """Integer sums are exact: a token's row is the same alone and in a batch."""
+    xq, xs, wq, ws = [t.to(DEV) for t in operands(6, 300, 1040, 264)]
+    say("int8 linear, batch invariance")
+    full = D.dora_linear_quantized(xq, xs, wq, ws)
+    for lo, hi in ((0, 1), (7, 9), (10, 50), (100, 240)):
+        assert torch.equal(D.dora_linear_quantized(xq[lo:hi].clone(), xs[lo:hi].clone(),
+                                                   wq, ws), full[lo:hi])
+
+
+def test_linear_quantized_refuses_what_it_cannot_read():
+    xq, xs, wq, ws = [t.to(DEV) for t in operands(7, 4, 64, 32)]
+    for call in (lambda: D.dora_linear_quantized(xq, xs, wq[:, :32], ws),
+                 lambda: D.dora_linear_quantized(xq, xs[:3], wq, ws),
+                 lambda: D.dora_linear_quantized(xq, xs, wq, ws[:, 0]),
+                 lambda: D.dora_linear_quantized(xq, xs, wq.T.contiguous().T, ws),
+                 lambda: D.dora_linear_quantized(xq, xs, wq, ws,
+                                                 ws=torch.empty(4, device=DEV))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: D.dora_linear_quantized(xq.float(), xs, wq, ws),
+                 lambda: D.dora_linear_quantized(xq, xs, wq, ws, dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_merged_weight_in_8_bits_behind_the_norm():
+    """Serving: the residual's addition and norm to 8 bits, then the merged
+    weight's layer, as they are used together."""
+    from dora_adapter_amd import synth
+    mod = synth.custom(520, 1032, 24, 70, "bf16", s=2.0, seed=4)
+    t = {k: mod[k].to(DEV) for k in ("x", "W", "A", "B", "m")}
+    res = torch.randn(70, 1032, generator=torch.Generator().manual_seed(1)).bfloat16()
+    w = (1 + 0.1 * torch.randn(1032, generator=torch.Generator().manual_seed(2))).bfloat16()
+    say("merge, quantize, norm to 8 bits, linear")
+    merged = D.dora_merge(t["W"], t["A"], t["B"], t["m"], mod["s"])
+    wq, ws = D.dora_quantize_rows(merged)
+    rq, rs = R.quantize(merged.cpu(), 0)
+    assert torch.equal(wq.cpu(), rq) and torch.equal(ws.cpu(), rs)
+    o = D.dora_rmsnorm(t["x"], w.to(DEV), residual=res.to(DEV), want_y=False, quantize=True)
+    y = D.dora_linear_quantized(o["q"], o["scale"], wq, ws).cpu()
+    ref = R.linear(o["q"].cpu(), o["scale"].cpu(), rq, rs)
+    lim = ref.abs() * (3.1 * 2.0 ** -24 + 2.0 ** -8)
+    assert ((y.double() - ref).abs() <= lim).all()
+    # and near the unquantized layer: each operand is within half a step of its
+    # group, s / 2 a value, independent of the other's: a sum of d_in products
+    # is off by at most sum (s_x / 2 |w| + s_w / 2 |v|) + its product term
+    v, _ = R.norm(R.norm_h(mod["x"], res), w, 1e-6)
+    full = v @ merged.cpu().double().T
+    sx, sw = o["scale"].cpu().double(), ws.cpu().double()
+    bound = (sx / 2 * merged.cpu().double().abs().sum(1)[None]
+             + v.abs().sum(1, keepdim=True) * sw.T / 2 + 1032 * sx * sw.T / 4)
+    assert ((ref - full).abs() <= 1.01 * bound).all()
