@@ -50,7 +50,7 @@ __device__ __forceinline__ void norm_y(const Raw8<T> &h, const T *w, int cnt, fl
                                        float (&y)[8])
 {
     Raw8<T> wr;
-    wr.load(w, cnt);
+    wr.template load<true>(w, cnt);
     float hv[8], wv[8];
     h.get(hv);
     wr.get(wv);
@@ -68,6 +68,42 @@ __device__ __forceinline__ unsigned int top8(const float (&v)[8])
         t = t > b ? t : b;
     }
     return t;
+}
+
+// The 8-bit form of row t, held as VPT vectors a thread (zeros past its end).
+template <int VPT>
+__device__ __forceinline__ void quantize_held(const float (&v)[VPT][8], int d, int group, int64_t t,
+                                              int8_t *q, float *scale, unsigned int *redu)
+{
+    const int threads = static_cast<int>(blockDim.x);
+    unsigned int top[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        top[i] = top8(v[i]);
+    float s = 0.f, inv = 0.f;
+    const int lanes = group / 8;
+    const int groups = group ? (d + group - 1) / group : 1;
+    if (group == 0) {
+        unsigned int all = top[0];
+#pragma unroll
+        for (int i = 1; i < VPT; ++i)
+            all = all > top[i] ? all : top[i];
+        s = scale_of(block_max(all, redu, threads >> 6));
+        inv = inverse_scale(s);
+        if (threadIdx.x == 0)
+            scale[t] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int k = static_cast<int>(threadIdx.x) + i * threads;
+        if (group != 0) {
+            s = scale_of(lanes_max(top[i], lanes));
+            inv = inverse_scale(s);
+            if (k % lanes == 0 && k / lanes < groups)
+                scale[t * groups + k / lanes] = s;
+        }
+        quantize8(v[i], s, inv).store(q + t * d + k * 8, count8(d, k * 8));
+    }
 }
 
 // Rows of any width: every pass reads the row again.  A thread meets the same
@@ -94,7 +130,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_kernel(NormArgs a)
             for (int q = 0; q < 8; ++q)
                 ss = __fmaf_rn(f[q], f[q], ss);
         }
-        ss = block_sum<ROW_WAVES>(ss, red);
+        ss = block_sum(ss, red, ROW_WAVES);
         const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
         if (a.rstd != nullptr && threadIdx.x == 0)
             a.rstd[t] = rstd;
@@ -109,7 +145,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_kernel(NormArgs a)
                 const unsigned int b = top8(y);
                 top = top > b ? top : b;
             }
-            s = scale_of(block_max<ROW_WAVES>(top, redu));
+            s = scale_of(block_max(top, redu, ROW_WAVES));
             if (threadIdx.x == 0)
                 a.scale[t] = s;
         }
@@ -137,6 +173,67 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_kernel(NormArgs a)
     }
 }
 
+// Rows that fit a workgroup's registers: thread i holds the vectors i, i +
+// threads, ... (VPT of them), so x, the residual and w are read once (w before
+// the first reduction, whose wait covers it) and everything is written once.
+// h goes out as soon as it is formed.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) rmsnorm_held_kernel(NormArgs a)
+{
+    __shared__ float red[16];
+    __shared__ unsigned int redu[16];
+    const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
+    const int d = static_cast<int>(a.d);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * a.d;
+    float y[VPT][8];
+    Raw8<T> w[VPT];
+    {
+        Raw8<T> h[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = (static_cast<int>(threadIdx.x) + i * threads) * 8;
+            h[i] = load_h<T>(a, row + j, count8(d, j));
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = (static_cast<int>(threadIdx.x) + i * threads) * 8;
+            w[i].template load<true>(static_cast<const T *>(a.w) + j, count8(d, j));
+            if (a.h != nullptr)
+                h[i].store(static_cast<T *>(a.h) + row + j, count8(d, j));
+            h[i].get(y[i]);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            ss = __fmaf_rn(y[i][q], y[i][q], ss);
+    ss = block_sum(ss, red, waves);
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(d) + a.eps);
+    if (a.rstd != nullptr && threadIdx.x == 0)
+        a.rstd[blockIdx.x] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float wv[8];
+        w[i].get(wv);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            y[i][q] = y[i][q] * rstd * wv[q];
+    }
+    if (a.y != nullptr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = (static_cast<int>(threadIdx.x) + i * threads) * 8;
+            Raw8<T> o;
+            o.set(y[i]);
+            o.store(static_cast<T *>(a.y) + row + j, count8(d, j));
+        }
+    }
+    if (a.q != nullptr)
+        quantize_held<VPT>(y, d, a.group, blockIdx.x, a.q, a.scale, redu);
+}
+
 // The gradient with respect to h:
 //   dx = dres + rstd (w dy) - h rstd^3 / d * sum_j w_j dy_j h_j
 // (dres: the gradient that reaches h along the residual stream).  dx may be
@@ -155,7 +252,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
             Raw8<T> hr, gr, wr;
             hr.load(static_cast<const T *>(a.h) + row + v * 8, cnt);
             gr.load(static_cast<const T *>(a.dy) + row + v * 8, cnt);
-            wr.load(w + v * 8, cnt);
+            wr.template load<true>(w + v * 8, cnt);
             float h[8], g[8], wv[8];
             hr.get(h);
             gr.get(g);
@@ -164,7 +261,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
             for (int q = 0; q < 8; ++q)
                 dot = __fmaf_rn(wv[q] * g[q], h[q], dot);
         }
-        dot = block_sum<ROW_WAVES>(dot, red);
+        dot = block_sum(dot, red, ROW_WAVES);
         const float rstd = a.rstd[t];
         const float c = -(dot / static_cast<float>(a.d)) * rstd * rstd * rstd;
         for (int64_t v = threadIdx.x; v < vecs; v += ROW_THREADS) {
@@ -172,7 +269,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
             Raw8<T> hr, gr, wr, rr;
             hr.load(static_cast<const T *>(a.h) + row + v * 8, cnt);
             gr.load(static_cast<const T *>(a.dy) + row + v * 8, cnt);
-            wr.load(w + v * 8, cnt);
+            wr.template load<true>(w + v * 8, cnt);
             float h[8], g[8], wv[8], o[8];
             hr.get(h);
             gr.get(g);
@@ -222,17 +319,136 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dw_kernel(NormGradArgs a)
         a.dw_part[static_cast<int64_t>(blockIdx.y) * a.d + j + q] = acc[q];
 }
 
-__global__ void __launch_bounds__(ROW_THREADS) sum_parts_kernel(const float *__restrict__ part,
-                                                                int parts, int64_t d,
-                                                                float *__restrict__ out)
+// dx and dw in one pass over dy, h and dres, for rows that fit a workgroup's
+// registers: workgroup b takes rows b, b + parts, ...; a thread keeps its
+// columns' w and running dw.  PRE: the next row's loads go out before this
+// row's reduction, and cover it.
+template <typename T, int VPT, bool PRE>
+__global__ void __launch_bounds__(1024) rmsnorm_grad_held_kernel(NormGradArgs a)
 {
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * ROW_THREADS + threadIdx.x;
-    if (j >= d)
-        return;
+    __shared__ float red[2][16];
+    const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
+    const int d = static_cast<int>(a.d);
+    const float inv_d = 1.f / static_cast<float>(d);
+    const bool with_res = a.dres != nullptr;
+    auto col = [&](int i) { return (static_cast<int>(threadIdx.x) + i * threads) * 8; };
+    Raw8<T> w[VPT];
+    float dw[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        w[i].template load<true>(static_cast<const T *>(a.w) + col(i), count8(d, col(i)));
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            dw[i][q] = 0.f;
+    }
+    struct Row {
+        Raw8<T> h[VPT], g[VPT], r[VPT];
+        float rstd;
+    };
+    auto fetch = [&](Row &o, int64_t t) {
+        const int64_t at = t * a.d;
+        o.rstd = a.rstd[t];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int cnt = count8(d, col(i));
+            o.h[i].load(static_cast<const T *>(a.h) + at + col(i), cnt);
+            o.g[i].load(static_cast<const T *>(a.dy) + at + col(i), cnt);
+            if (with_res)
+                o.r[i].load(static_cast<const T *>(a.dres) + at + col(i), cnt);
+        }
+    };
+    Row cur, nxt;
+    int64_t t = blockIdx.x;
+    if (t < a.T)
+        fetch(cur, t);
+    for (int par = 0; t < a.T; par ^= 1) {
+        const int64_t tn = t + gridDim.x;
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float h[8], g[8], wv[8];
+            cur.h[i].get(h);
+            cur.g[i].get(g);
+            w[i].get(wv);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                dot = __fmaf_rn(wv[q] * g[q], h[q], dot);
+        }
+        if (PRE && tn < a.T)
+            fetch(nxt, tn);
+        dot = wave_sum(dot);
+        if (waves > 1) {
+            // one barrier a row: the next row writes the other half of `red`
+            if ((threadIdx.x & 63) == 0)
+                red[par][threadIdx.x >> 6] = dot;
+            __syncthreads();
+            dot = red[par][0];
+            for (int k = 1; k < waves; ++k)
+                dot += red[par][k];
+        }
+        const float c = -(dot * inv_d) * cur.rstd * cur.rstd * cur.rstd;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float h[8], g[8], wv[8], o[8];
+            cur.h[i].get(h);
+            cur.g[i].get(g);
+            w[i].get(wv);
+            if (with_res) {
+                cur.r[i].get(o);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    o[q] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                o[q] += __fmaf_rn(c, h[q], cur.rstd * (wv[q] * g[q]));
+                dw[i][q] = __fmaf_rn(g[q], h[q] * cur.rstd, dw[i][q]);
+            }
+            Raw8<T> out;
+            out.set(o);
+            out.store(static_cast<T *>(a.dx) + t * a.d + col(i), count8(d, col(i)));
+        }
+        t = tn;
+        if (PRE)
+            cur = nxt;
+        else if (t < a.T)
+            fetch(cur, t);
+    }
+    if (a.dw_part != nullptr) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int cnt = count8(d, col(i));
+            float *p = a.dw_part + static_cast<int64_t>(blockIdx.x) * a.d + col(i);
+            for (int q = 0; q < cnt; ++q)
+                p[q] = dw[i][q];
+        }
+    }
+}
+
+// Sums of `parts` rows: 64 columns a workgroup, its 16 waves taking every 16th
+// row each, then the 16 sums in order.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict__ part, int parts,
+                                                         int64_t d, float *__restrict__ out)
+{
+    __shared__ float sums[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + lane;
     float acc = 0.f;
-    for (int p = 0; p < parts; ++p)
-        acc += part[static_cast<int64_t>(p) * d + j];
-    out[j] = acc;
+    if (j < d) {
+#pragma unroll 8
+        for (int p = wave; p < parts; p += 16)
+            acc += part[static_cast<int64_t>(p) * d + j];
+    }
+    sums[wave][lane] = acc;
+    __syncthreads();
+    if (wave == 0 && j < d) {
+        acc = sums[0][lane];
+#pragma unroll
+        for (int k = 1; k < 16; ++k)
+            acc += sums[k][lane];
+        out[j] = acc;
+    }
 }
 
 template <typename T>
@@ -256,7 +472,7 @@ __global__ void __launch_bounds__(ROW_THREADS) quantize_kernel(const T *x, int64
                 const unsigned int b = top8(f);
                 top = top > b ? top : b;
             }
-            s = scale_of(block_max<ROW_WAVES>(top, redu));
+            s = scale_of(block_max(top, redu, ROW_WAVES));
             if (threadIdx.x == 0)
                 scale[t] = s;
         }
@@ -274,6 +490,26 @@ __global__ void __launch_bounds__(ROW_THREADS) quantize_kernel(const T *x, int64
             quantize8(f, s, inverse_scale(s)).store(q + row + v * 8, cnt);
         }
     }
+}
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024)
+    quantize_held_kernel(const T *x, int64_t width, int group, int8_t *q, float *scale)
+{
+    __shared__ unsigned int redu[16];
+    const int d = static_cast<int>(width);
+    const T *row = x + static_cast<int64_t>(blockIdx.x) * width;
+    Raw8<T> r[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int j = static_cast<int>(threadIdx.x + i * blockDim.x) * 8;
+        r[i].load(row + j, count8(d, j));
+    }
+    float v[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        r[i].get(v[i]);
+    quantize_held<VPT>(v, d, group, blockIdx.x, q, scale, redu);
 }
 
 template <typename T>
@@ -350,52 +586,130 @@ unsigned row_groups(int64_t rows)
     return static_cast<unsigned>(rows < MAX_ROW_GROUPS ? rows : MAX_ROW_GROUPS);
 }
 
+// Rows held in registers: vectors a thread and threads a row.  Fewer rows than
+// two a CU: as many threads as the row has vectors, so that one row's latency
+// is short; more rows: four vectors a thread.  vpt = 0: the row is too long.
+struct RowShape {
+    int vpt, threads;
+};
+RowShape held_shape(int64_t T, int64_t d)
+{
+    const int64_t vecs = (d + 7) / 8;
+    if (vecs > 4096 || T > 0x7fffffff)
+        return {0, 0};
+    int vpt = T <= 512 ? 1 : 4;
+    while (vecs > 1024 * static_cast<int64_t>(vpt))
+        vpt *= 2;
+    const int64_t threads = ((vecs + vpt - 1) / vpt + 63) / 64 * 64;
+    return {vpt, static_cast<int>(threads)};
+}
+
+template <typename T>
+void rmsnorm_launch(const NormArgs &a, hipStream_t st)
+{
+    const RowShape s = held_shape(a.T, a.d);
+    const dim3 grid(static_cast<unsigned>(a.T)), block(static_cast<unsigned>(s.threads));
+    if (s.vpt == 1)
+        hipLaunchKernelGGL((rmsnorm_held_kernel<T, 1>), grid, block, 0, st, a);
+    else if (s.vpt == 2)
+        hipLaunchKernelGGL((rmsnorm_held_kernel<T, 2>), grid, block, 0, st, a);
+    else if (s.vpt == 4)
+        hipLaunchKernelGGL((rmsnorm_held_kernel<T, 4>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((rmsnorm_kernel<T>), dim3(row_groups(a.T)), dim3(ROW_THREADS), 0, st, a);
+}
+
+template <typename T>
+void quantize_launch(const T *x, int64_t rows, int64_t d, int group, int8_t *q, float *scale,
+                     hipStream_t st)
+{
+    const RowShape s = held_shape(rows, d);
+    const dim3 grid(static_cast<unsigned>(rows)), block(static_cast<unsigned>(s.threads));
+    if (s.vpt == 1)
+        hipLaunchKernelGGL((quantize_held_kernel<T, 1>), grid, block, 0, st, x, d, group, q,
+                           scale);
+    else if (s.vpt == 2)
+        hipLaunchKernelGGL((quantize_held_kernel<T, 2>), grid, block, 0, st, x, d, group, q,
+                           scale);
+    else if (s.vpt == 4)
+        hipLaunchKernelGGL((quantize_held_kernel<T, 4>), grid, block, 0, st, x, d, group, q,
+                           scale);
+    else
+        hipLaunchKernelGGL((quantize_kernel<T>), dim3(row_groups(rows)), dim3(ROW_THREADS), 0, st, x,
+                           rows, d, group, q, scale);
+}
+
 }  // namespace
 
 int rmsnorm_parts(int64_t T, int64_t d)
 {
-    // about 2048 workgroups over column blocks and row shares, 16 rows each
-    // at least
-    const int64_t blocks = ((d + 7) / 8 + ROW_THREADS - 1) / ROW_THREADS;
-    int64_t p = 2048 / blocks;
-    p = p < (T + 15) / 16 ? p : (T + 15) / 16;
-    return static_cast<int>(p < 1 ? 1 : (p > 512 ? 512 : p));
+    // a workgroup a CU as soon as there are rows for them, then 16 rows a
+    // workgroup, up to the workgroups that fit the CUs at once (rows too long
+    // for the registers: column blocks times row shares)
+    const int64_t vecs = (d + 7) / 8;
+    const int64_t waves = vecs <= 4096 ? (vecs + 127) / 128 : 4;
+    const int64_t fit = 256 * (16 / (waves < 16 ? waves : 16));
+    int64_t p = T / 16 > 256 ? T / 16 : 256;
+    p = p < fit ? p : fit;
+    p = p < T ? p : T;
+    return static_cast<int>(p < 1 ? 1 : p);
 }
 
 hipError_t launch_rmsnorm(int bf16, const NormArgs &a, hipStream_t st)
 {
     if (a.T == 0)
         return hipSuccess;
-    const dim3 grid(row_groups(a.T)), block(ROW_THREADS);
     if (bf16)
-        hipLaunchKernelGGL((rmsnorm_kernel<uint16_t>), grid, block, 0, st, a);
+        rmsnorm_launch<uint16_t>(a, st);
     else
-        hipLaunchKernelGGL((rmsnorm_kernel<float>), grid, block, 0, st, a);
+        rmsnorm_launch<float>(a, st);
     return hipGetLastError();
 }
 
+namespace {
+template <typename T>
+void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
+{
+    constexpr bool WIDE = sizeof(T) == 4;
+    const int64_t vecs = (a.d + 7) / 8;
+    const unsigned parts = static_cast<unsigned>(a.parts);
+    float *const part = a.dw_part;
+    // one part is the sum itself
+    a.dw_part = dw == nullptr ? nullptr : (parts == 1 ? dw : part);
+    if (a.T > 0 && vecs <= (WIDE ? 2048 : 4096)) {
+        // the fewest vectors a thread that 1024 threads allow, two at least
+        // where the registers take two rows of them (bf16)
+        const int vpt = vecs <= 64 ? 1 : (WIDE && vecs <= 1024 ? 1 : (vecs <= 2048 ? 2 : 4));
+        const dim3 grid(parts), block(static_cast<unsigned>(((vecs + vpt - 1) / vpt + 63) / 64 * 64));
+        if (vpt == 1)
+            hipLaunchKernelGGL((rmsnorm_grad_held_kernel<T, 1, true>), grid, block, 0, st, a);
+        else if (vpt == 2)
+            hipLaunchKernelGGL((rmsnorm_grad_held_kernel<T, 2, !WIDE>), grid, block, 0, st, a);
+        else if constexpr (!WIDE)
+            hipLaunchKernelGGL((rmsnorm_grad_held_kernel<T, 4, false>), grid, block, 0, st, a);
+    } else {
+        const dim3 block(ROW_THREADS);
+        if (a.T > 0)
+            hipLaunchKernelGGL((rmsnorm_dx_kernel<T>), dim3(row_groups(a.T)), block, 0, st, a);
+        // (T = 0: the partial sums are zeros)
+        if (dw != nullptr)
+            hipLaunchKernelGGL((rmsnorm_dw_kernel<T>),
+                               dim3(static_cast<unsigned>((vecs + ROW_THREADS - 1) / ROW_THREADS),
+                                    parts),
+                               block, 0, st, a);
+    }
+    if (dw != nullptr && parts > 1)
+        hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64)), dim3(1024),
+                           0, st, part, a.parts, a.d, dw);
+}
+}  // namespace
+
 hipError_t launch_rmsnorm_grad(int bf16, const NormGradArgs &a, float *dw, hipStream_t st)
 {
-    const dim3 block(ROW_THREADS);
-    const unsigned cols = static_cast<unsigned>(((a.d + 7) / 8 + ROW_THREADS - 1) / ROW_THREADS);
-    if (a.T > 0) {
-        const dim3 rows(row_groups(a.T));
-        if (bf16)
-            hipLaunchKernelGGL((rmsnorm_dx_kernel<uint16_t>), rows, block, 0, st, a);
-        else
-            hipLaunchKernelGGL((rmsnorm_dx_kernel<float>), rows, block, 0, st, a);
-    }
-    if (dw != nullptr) {
-        // (T = 0: the partial sums are zeros)
-        const dim3 grid(cols, static_cast<unsigned>(a.parts));
-        if (bf16)
-            hipLaunchKernelGGL((rmsnorm_dw_kernel<uint16_t>), grid, block, 0, st, a);
-        else
-            hipLaunchKernelGGL((rmsnorm_dw_kernel<float>), grid, block, 0, st, a);
-        hipLaunchKernelGGL(sum_parts_kernel,
-                           dim3(static_cast<unsigned>((a.d + ROW_THREADS - 1) / ROW_THREADS)), block,
-                           0, st, a.dw_part, a.parts, a.d, dw);
-    }
+    if (bf16)
+        rmsnorm_grad_launch<uint16_t>(a, dw, st);
+    else
+        rmsnorm_grad_launch<float>(a, dw, st);
     return hipGetLastError();
 }
 
@@ -404,13 +718,10 @@ hipError_t launch_quantize_rows(int bf16, const void *x, int64_t rows, int64_t d
 {
     if (rows == 0)
         return hipSuccess;
-    const dim3 grid(row_groups(rows)), block(ROW_THREADS);
     if (bf16)
-        hipLaunchKernelGGL((quantize_kernel<uint16_t>), grid, block, 0, st,
-                           static_cast<const uint16_t *>(x), rows, d, group, q, scale);
+        quantize_launch(static_cast<const uint16_t *>(x), rows, d, group, q, scale, st);
     else
-        hipLaunchKernelGGL((quantize_kernel<float>), grid, block, 0, st,
-                           static_cast<const float *>(x), rows, d, group, q, scale);
+        quantize_launch(static_cast<const float *>(x), rows, d, group, q, scale, st);
     return hipGetLastError();
 }
 

@@ -25,10 +25,13 @@ struct Raw8;
 template <>
 struct Raw8<uint16_t> {
     unsigned int w[4];
+    // KEEP: the data is read again soon (by the other rows), leave it in the caches
+    template <bool KEEP = false>
     __device__ __forceinline__ void load(const uint16_t *p, int cnt)
     {
         if (cnt >= 8) {
-            const u32x4_a2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2_t *>(p));
+            const u32x4_a2_t *u = reinterpret_cast<const u32x4_a2_t *>(p);
+            const u32x4_a2_t v = KEEP ? *u : __builtin_nontemporal_load(u);
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         } else {
 #pragma unroll
@@ -71,12 +74,13 @@ struct Raw8<uint16_t> {
 template <>
 struct Raw8<float> {
     unsigned int w[8];
+    template <bool KEEP = false>
     __device__ __forceinline__ void load(const float *p, int cnt)
     {
         if (cnt >= 8) {
-            const u32x4_a4_t a = __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4_t *>(p));
-            const u32x4_a4_t b =
-                __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4_t *>(p + 4));
+            const u32x4_a4_t *u = reinterpret_cast<const u32x4_a4_t *>(p);
+            const u32x4_a4_t a = KEEP ? u[0] : __builtin_nontemporal_load(u);
+            const u32x4_a4_t b = KEEP ? u[1] : __builtin_nontemporal_load(u + 1);
             w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
             w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         } else {
@@ -173,36 +177,50 @@ __device__ __forceinline__ float scale_of(unsigned int top)
 // 1 / s, and 0 where nothing is to be scaled (s = 0 or NaN: q = 0).
 __device__ __forceinline__ float inverse_scale(float s) { return s > 0.f ? 1.f / s : 0.f; }
 
-// rint(v / s), ties to even, exactly: v inv is off by less than 2e-5 (|v / s|
-// <= 127, two roundings of 2^-24), so only quotients within that of a tie
-// need the remainder v - q s, which one fma forms without rounding.
-__device__ __forceinline__ int quantize1(float v, float s, float inv)
+// rint(v / s), ties to even, for a quotient v inv near a tie: the remainder
+// v - q s of the nearest integer q, which one fma forms without rounding,
+// decides (both v and q s are multiples of the smaller one's last place, and
+// the difference is about s / 2).
+__device__ __forceinline__ float quantize_near_tie(float v, float s, float q)
 {
-    const float t = v * inv;
-    float q = rintf(t);
-    if (fabsf(t - q) > 0.4999f) {
-        const float rem2 = 2.f * __fmaf_rn(-q, s, v);
-        const bool odd = (static_cast<int>(q) & 1) != 0;
-        if (rem2 > s || (rem2 == s && odd))
-            q += 1.f;
-        else if (-rem2 > s || (-rem2 == s && odd))
-            q -= 1.f;
-    }
-    // a scale capped from above leaves |v / s| a hair over 127
-    return static_cast<int>(fminf(fmaxf(q, -127.f), 127.f));
+    const float rem2 = 2.f * __fmaf_rn(-q, s, v);
+    const bool odd = (static_cast<int>(q) & 1) != 0;
+    if (rem2 > s || (rem2 == s && odd))
+        return q + 1.f;
+    if (-rem2 > s || (-rem2 == s && odd))
+        return q - 1.f;
+    return q;
 }
 
+// Eight quotients rint(v / s).  Adding 1.5 * 2^23 rounds v inv to an integer
+// whose two's complement byte is the sum's lowest.  inv is 1 / s to 2^-24, so v
+// inv is off by at most 127 * 2^-24 < 8e-6 (|v / s| <= 127 but for a capped
+// scale, a hair over): only what lies within 1e-5 of a tie takes the exact
+// path, about one vector of 64 lanes in a hundred.
 __device__ __forceinline__ Raw8i quantize8(const float (&v)[8], float s, float inv)
 {
-    Raw8i r;
-    r.w[0] = r.w[1] = 0u;
+    constexpr float MAGIC = 12582912.f;
+    float f[8], worst = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-        r.w[q >> 2] |= (static_cast<unsigned int>(quantize1(v[q], s, inv)) & 0xffu) << (8 * (q & 3));
-    // (an infinity times an inverse of 0 is a NaN, not 0)
-    const unsigned int some = s > 0.f ? 0xffffffffu : 0u;
-    r.w[0] &= some;
-    r.w[1] &= some;
+    for (int q = 0; q < 8; ++q) {
+        f[q] = __fmaf_rn(v[q], inv, MAGIC);
+        worst = fmaxf(worst, fabsf(__fmaf_rn(v[q], inv, MAGIC - f[q])));
+    }
+    if (worst > 0.49999f) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            f[q] = quantize_near_tie(v[q], s, f[q] - MAGIC) + MAGIC;
+    }
+    Raw8i r;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const unsigned int lo = __builtin_amdgcn_perm(
+            __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k]), 0x0c0c0400u);
+        const unsigned int hi = __builtin_amdgcn_perm(
+            __float_as_uint(f[4 * k + 3]), __float_as_uint(f[4 * k + 2]), 0x04000c0cu);
+        // (a NaN or zero scale: all zeros)
+        r.w[k] = s > 0.f ? lo | hi : 0u;
+    }
     return r;
 }
 
@@ -226,34 +244,34 @@ __device__ __forceinline__ unsigned int lanes_max(unsigned int v, int lanes)
     return v;
 }
 
-// Over a workgroup of NW waves; `red` holds NW values and is free again after
-// the call's second barrier.
-template <int NW>
-__device__ __forceinline__ float block_sum(float v, float *red)
+// Over a workgroup of `waves` waves in a fixed order; `red` holds one value a
+// wave (and may be used again by the next call: its writes follow a barrier).
+__device__ __forceinline__ float block_sum(float v, float *red, int waves)
 {
     v = wave_sum(v);
+    if (waves == 1)
+        return v;
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = red[0];
-#pragma unroll
-    for (int k = 1; k < NW; ++k)
+    for (int k = 1; k < waves; ++k)
         s += red[k];
     return s;
 }
 
-template <int NW>
-__device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *red)
+__device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *red, int waves)
 {
     v = lanes_max(v, 64);
+    if (waves == 1)
+        return v;
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
     unsigned int s = red[0];
-#pragma unroll
-    for (int k = 1; k < NW; ++k)
+    for (int k = 1; k < waves; ++k)
         s = s > red[k] ? s : red[k];
     return s;
 }
