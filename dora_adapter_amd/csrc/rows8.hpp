@@ -7,6 +7,8 @@
 #include "dora_internal.hpp"
 #include "epilogue.hpp"
 
+#include <type_traits>
+
 namespace dora {
 
 // 16 bytes at any element boundary: rows of an odd width start anywhere, and
@@ -115,6 +117,16 @@ struct Raw8<float> {
             w[q] = __float_as_uint(v[q]);
     }
 };
+
+// The same vector, its values to be formed again from here on: what was unpacked
+// from it earlier is then not kept in registers for the next use.
+template <typename T>
+__device__ __forceinline__ void forget(Raw8<T> &r)
+{
+#pragma unroll
+    for (unsigned int &w : r.w)
+        __asm__ volatile("" : "+v"(w));
+}
 
 // Eight int8 values.
 struct Raw8i {
@@ -234,14 +246,37 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// The largest over aligned runs of `lanes` lanes (a power of two up to 64).
-__device__ __forceinline__ unsigned int lanes_max(unsigned int v, int lanes)
+// The largest over aligned runs of `lanes` lanes (a power of two up to 64, the
+// same for the whole wave), for N values at once: the exchanges of one step
+// are independent of each other, and a step's distance is a constant.
+template <int N>
+__device__ __forceinline__ void lanes_max(unsigned int (&v)[N], int lanes)
 {
-    for (int d = lanes >> 1; d > 0; d >>= 1) {
-        const unsigned int o = __shfl_xor(v, d);
-        v = v > o ? v : o;
-    }
-    return v;
+    auto step = [&](auto dist) {
+        constexpr int D = decltype(dist)::value;
+        if (lanes > D) {
+            unsigned int o[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                o[i] = __shfl_xor(v[i], D);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] = v[i] > o[i] ? v[i] : o[i];
+        }
+    };
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 4>{});
+    step(std::integral_constant<int, 8>{});
+    step(std::integral_constant<int, 16>{});
+    step(std::integral_constant<int, 32>{});
+}
+
+__device__ __forceinline__ unsigned int lane_max(unsigned int v, int lanes)
+{
+    unsigned int a[1] = {v};
+    lanes_max(a, lanes);
+    return a[0];
 }
 
 // Over a workgroup of `waves` waves in a fixed order; `red` holds one value a
@@ -263,7 +298,7 @@ __device__ __forceinline__ float block_sum(float v, float *red, int waves)
 
 __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *red, int waves)
 {
-    v = lanes_max(v, 64);
+    v = lane_max(v, 64);
     if (waves == 1)
         return v;
     __syncthreads();
