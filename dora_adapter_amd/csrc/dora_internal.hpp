@@ -273,15 +273,20 @@ struct I8GemmArgs {
     void *y;
     int *part;  // split products: int32 partial sums [splits, M, N], else null
     int64_t M, N, K;
-    int64_t k_per_split;
+    int64_t k_per_split;  // bytes of K a split, whole stages of the kernel
+    int splits;
 };
 struct I8Plan {
+    int cfg;  // tile configuration of the pipelined kernel, or -1: the general one
     int splits;
     int64_t k_per_split;
     size_t part_bytes;
 };
-I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K);
+I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16);
 hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hipStream_t st);
+// The pipelined kernel (gemm_i8_dma.hip): K % 16 == 0, whole 16-byte chunks of
+// y's rows, operands and output under 2 GiB.
+hipError_t launch_gemm_i8_dma(int bf16, const I8GemmArgs &g, int cfg, hipStream_t st);
 
 // The thread-local message dora_last_error() returns (dora_api.cpp): set it
 // and return `status`, or clear it.

@@ -173,18 +173,68 @@ __global__ void __launch_bounds__(GTHREADS) i8_finish_kernel(I8GemmArgs g, int s
 
 }  // namespace
 
-I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K)
+namespace {
+
+constexpr int64_t I8_STAGE_K = 128;                  // bytes of K a stage of the pipelined kernel
+constexpr int64_t I8_MAX_BYTES = (1LL << 31) - 8192;  // 32-bit buffer offsets
+struct I8Tile {
+    int bm, bn, resident;  // workgroups a CU
+    double rate;           // relative rate of a full tile
+};
+constexpr I8Tile I8_TILES[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16)
 {
-    I8Plan p;
-    const int64_t tiles = ((M + GB - 1) / GB) * ((N + GB - 1) / GB);
-    const int64_t steps = (K + GK - 1) / GK;
-    // split K until two workgroups a CU are reached, eight steps a split at least
-    int64_t z = tiles > 0 ? 512 / tiles : 1;
-    z = z < steps / 8 ? z : steps / 8;
-    z = z < 1 ? 1 : (z > 32 ? 32 : z);
-    const int64_t per = (steps + z - 1) / z;
-    p.splits = static_cast<int>((steps + per - 1) / per);
-    p.k_per_split = per * GK;
+    I8Plan p{-1, 1, 0, 0};
+    const int64_t elt = bf16 ? 2 : 4;
+    if (K % 16 == 0 && N % (16 / elt) == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES &&
+        M * N * 4 < I8_MAX_BYTES) {
+        // Time of a configuration: rounds of resident workgroups, each its
+        // products at the rate a full GPU sustains plus a fill and an epilogue;
+        // a split writes and reads int32 partial sums and launches once more.
+        const int64_t stages = ceil_div(K, I8_STAGE_K);
+        double best = -1.0;
+        for (int c = 0; c < 2; ++c) {
+            const I8Tile &t = I8_TILES[c];
+            const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+            for (int64_t z = 1; z <= 16 && (z == 1 || stages / z >= 4); ++z) {
+                const int64_t sps = ceil_div(stages, z);
+                const int64_t used = ceil_div(stages, sps);
+                if (used != z || (z > 1 && z * M * N * 4 >= I8_MAX_BYTES))
+                    continue;
+                const int64_t slots = 256 * t.resident;
+                const int64_t rounds = ceil_div(tiles * z, slots);
+                const int64_t busy = tiles * z < slots ? ceil_div(tiles * z, 256) : t.resident;
+                double s = static_cast<double>(rounds) *
+                           (2.0 * t.bm * t.bn * sps * I8_STAGE_K * static_cast<double>(busy) /
+                                (9.0e12 * t.rate) +
+                            4e-6);
+                if (z > 1)
+                    s += 8.0 * z * M * N / 4.0e12 + 5e-6;
+                if (best < 0 || s < best) {
+                    best = s;
+                    p.cfg = c;
+                    p.splits = static_cast<int>(z);
+                    p.k_per_split = sps * I8_STAGE_K;
+                }
+            }
+        }
+    } else {
+        const int64_t tiles = ceil_div(M, GB) * ceil_div(N, GB);
+        const int64_t steps = ceil_div(K, GK);
+        // split K until two workgroups a CU are reached, eight steps a split at
+        // least
+        int64_t z = tiles > 0 ? 512 / tiles : 1;
+        z = z < steps / 8 ? z : steps / 8;
+        z = z < 1 ? 1 : (z > 32 ? 32 : z);
+        const int64_t per = ceil_div(steps, z);
+        p.splits = static_cast<int>(ceil_div(steps, per));
+        p.k_per_split = per * GK;
+    }
     p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * M * N * 4 : 0;
     return p;
 }
@@ -195,24 +245,31 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
         return hipSuccess;
     g.part = p.splits > 1 ? static_cast<int *>(ws) : nullptr;
     g.k_per_split = p.k_per_split;
-    const int64_t tiles = ((g.M + GB - 1) / GB) * ((g.N + GB - 1) / GB);
-    if (tiles > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
-    if (bf16)
-        hipLaunchKernelGGL((gemm_i8_general_kernel<uint16_t>), grid, dim3(GTHREADS), 0, st, g);
-    else
-        hipLaunchKernelGGL((gemm_i8_general_kernel<float>), grid, dim3(GTHREADS), 0, st, g);
-    if (p.splits > 1) {
-        int64_t blocks = (g.M * g.N + GTHREADS - 1) / GTHREADS;
-        blocks = blocks < 8192 ? blocks : 8192;
+    g.splits = p.splits;
+    hipError_t e = hipSuccess;
+    if (p.cfg >= 0) {
+        e = launch_gemm_i8_dma(bf16, g, p.cfg, st);
+    } else {
+        const int64_t tiles = ceil_div(g.M, GB) * ceil_div(g.N, GB);
+        if (tiles > 0x7fffffff)
+            return hipErrorInvalidConfiguration;
+        const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
         if (bf16)
-            hipLaunchKernelGGL((i8_finish_kernel<uint16_t>), dim3(static_cast<unsigned>(blocks)),
-                               dim3(GTHREADS), 0, st, g, p.splits);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<uint16_t>), grid, dim3(GTHREADS), 0, st, g);
         else
-            hipLaunchKernelGGL((i8_finish_kernel<float>), dim3(static_cast<unsigned>(blocks)),
-                               dim3(GTHREADS), 0, st, g, p.splits);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<float>), grid, dim3(GTHREADS), 0, st, g);
+        e = hipGetLastError();
     }
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    int64_t blocks = ceil_div(g.M * g.N, GTHREADS);
+    blocks = blocks < 8192 ? blocks : 8192;
+    if (bf16)
+        hipLaunchKernelGGL((i8_finish_kernel<uint16_t>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(GTHREADS), 0, st, g, p.splits);
+    else
+        hipLaunchKernelGGL((i8_finish_kernel<float>), dim3(static_cast<unsigned>(blocks)),
+                           dim3(GTHREADS), 0, st, g, p.splits);
     return hipGetLastError();
 }
 
