@@ -277,7 +277,8 @@ struct I8GemmArgs {
     int splits;
 };
 struct I8Plan {
-    int cfg;  // tile configuration of the pipelined kernel, or -1: the general one
+    int cfg;  // tile configuration of the pipelined kernel, or one of these:
+    static constexpr int GENERAL = -1, ROWS = -2;
     int splits;
     int64_t k_per_split;
     size_t part_bytes;
@@ -287,6 +288,9 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
 // The pipelined kernel (gemm_i8_dma.hip): K % 16 == 0, whole 16-byte chunks of
 // y's rows, operands and output under 2 GiB.
 hipError_t launch_gemm_i8_dma(int bf16, const I8GemmArgs &g, int cfg, hipStream_t st);
+// A few tokens (gemm_i8_rows.hip): M <= 64, K % 16 == 0, operands under 2 GiB.
+constexpr int I8_ROWS_MOST = 64;
+hipError_t launch_gemm_i8_rows(int bf16, const I8GemmArgs &g, hipStream_t st);
 
 // The thread-local message dora_last_error() returns (dora_api.cpp): set it
 // and return `status`, or clear it.

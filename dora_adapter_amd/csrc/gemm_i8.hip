@@ -189,9 +189,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16)
 {
-    I8Plan p{-1, 1, 0, 0};
+    I8Plan p{I8Plan::GENERAL, 1, 0, 0};
     const int64_t elt = bf16 ? 2 : 4;
-    if (K % 16 == 0 && N % (16 / elt) == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES &&
+    if (M <= I8_ROWS_MOST && K % 16 == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES) {
+        p.cfg = I8Plan::ROWS;
+    } else if (K % 16 == 0 && N % (16 / elt) == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES &&
         M * N * 4 < I8_MAX_BYTES) {
         // Time of a configuration: rounds of resident workgroups, each its
         // products at the rate a full GPU sustains plus a fill and an epilogue;
@@ -247,7 +249,9 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
     g.k_per_split = p.k_per_split;
     g.splits = p.splits;
     hipError_t e = hipSuccess;
-    if (p.cfg >= 0) {
+    if (p.cfg == I8Plan::ROWS) {
+        e = launch_gemm_i8_rows(bf16, g, st);
+    } else if (p.cfg != I8Plan::GENERAL) {
         e = launch_gemm_i8_dma(bf16, g, p.cfg, st);
     } else {
         const int64_t tiles = ceil_div(g.M, GB) * ceil_div(g.N, GB);
