@@ -2048,7 +2048,7 @@ size_t dora_linear_quantized_workspace(int64_t T, int64_t d_in, int64_t d_out, i
 {
     if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, 8) || check_i8_width(d_in))
         return 0;
-    return align_up(plan_gemm_i8(T, d_out, d_in, dtype == DORA_BF16).part_bytes);
+    return align_up(plan_gemm_i8(T, d_out, d_in).part_bytes);
 }
 
 int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const float *wscale,
@@ -2062,7 +2062,7 @@ int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const
     const bool has_t = T > 0;
     DORA_CHECK(check_ptrs({{xq, "xq", has_t}, {xs, "xs", has_t}, {wq, "wq", true},
                            {wscale, "wscale", true}, {y, "y", has_t}}));
-    const I8Plan p = plan_gemm_i8(T, d_out, d_in, dtype == DORA_BF16);
+    const I8Plan p = plan_gemm_i8(T, d_out, d_in);
     const size_t need = align_up(p.part_bytes);
     DORA_CHECK(check_ws(ws, ws_bytes, need));
     DORA_CHECK(check_disjoint(

@@ -283,13 +283,13 @@ struct I8Plan {
     int64_t k_per_split;
     size_t part_bytes;
 };
-I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16);
+I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hipStream_t st);
-// The pipelined kernel (gemm_i8_dma.hip): K % 16 == 0, whole 16-byte chunks of
-// y's rows, operands and output under 2 GiB.
+// The pipelined kernel (gemm_i8_dma.hip): K % 16 == 0, operands and output
+// under 2 GiB.
 hipError_t launch_gemm_i8_dma(int bf16, const I8GemmArgs &g, int cfg, hipStream_t st);
-// A few tokens (gemm_i8_rows.hip): M <= 64, K % 16 == 0, operands under 2 GiB.
-constexpr int I8_ROWS_MOST = 64;
+// A few tokens (gemm_i8_rows.hip): K % 16 == 0, operands under 2 GiB.
+bool gemm_i8_rows_ok(int64_t M, int64_t N);
 hipError_t launch_gemm_i8_rows(int bf16, const I8GemmArgs &g, hipStream_t st);
 
 // The thread-local message dora_last_error() returns (dora_api.cpp): set it

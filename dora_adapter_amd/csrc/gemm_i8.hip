@@ -10,8 +10,9 @@
 // consecutive columns 4 (l >> 4) + 0..3.
 //
 // The general kernel: any width and alignment, operands staged through
-// registers.  128 x 128 tiles of four waves (64 x 64 each), 64 bytes of K a
-// step; the next step's loads are in flight during this one's products.
+// registers.  128 x 128 or 64 x 64 tiles of four waves, 128 bytes of K a step
+// in two LDS buffers; the next step's loads are in flight during this one's
+// products.
 #include "dora_internal.hpp"
 #include "rows8.hpp"
 
@@ -20,9 +21,8 @@ namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int GB = 128;           // tile rows and columns
-constexpr int GK = 64;            // bytes of K a step
-constexpr int GPITCH = GK + 16;   // LDS row: 8 rows of a 16-byte read phase on distinct banks
+constexpr int GK = 128;          // bytes of K a step
+constexpr int GPITCH = GK + 16;  // LDS row: 8 rows of a 16-byte read phase on distinct banks
 constexpr int GTHREADS = 256;
 
 // 16 bytes of a row from byte k on, zeros past the width K.
@@ -66,78 +66,96 @@ __device__ __forceinline__ void store_scaled(const I8GemmArgs &g, int64_t m, int
         }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(GTHREADS) gemm_i8_general_kernel(I8GemmArgs g)
+// B x B tiles (128 or 64) of four waves.
+template <int B, typename T>
+__global__ void __launch_bounds__(GTHREADS, 2) gemm_i8_general_kernel(I8GemmArgs g)
 {
-    __shared__ __align__(16) unsigned char As[GB * GPITCH];
-    __shared__ __align__(16) unsigned char Bs[GB * GPITCH];
+    constexpr int TM = B / 32, PER = B / 32;  // blocks of a wave; rows a thread loads
+    __shared__ __align__(16) unsigned char lds[2][2][B * GPITCH];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const int64_t num_n = (g.N + GB - 1) / GB;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / num_n) * GB;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x % num_n) * GB;
-    const int64_t k_end_all = (g.K + GK - 1) / GK * GK;
+    const int wm = (wave >> 1) * (B / 2), wn = (wave & 1) * (B / 2);
+    const int64_t num_n = (g.N + B - 1) / B;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x / num_n) * B;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x % num_n) * B;
     const int64_t kb = static_cast<int64_t>(blockIdx.y) * g.k_per_split;
-    const int64_t ke = kb + g.k_per_split < k_end_all ? kb + g.k_per_split : k_end_all;
+    const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
 
-    // thread: chunk tid & 3 of rows tid >> 2 and 64 + (tid >> 2) of either
-    // operand (rows past the end: the last one, never stored)
-    const int lr = tid >> 2, lc = (tid & 3) * 16;
-    const int8_t *ap[2], *bp[2];
+    // thread: chunk tid & 7 of rows (tid >> 3) + 32 i of either operand (rows
+    // past the end: the last one, never stored)
+    const int lr = tid >> 3, lc = (tid & 7) * 16;
+    const int8_t *ap[PER], *bp[PER];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t m = m0 + lr + 64 * i, n = n0 + lr + 64 * i;
+    for (int i = 0; i < PER; ++i) {
+        const int64_t m = m0 + lr + 32 * i, n = n0 + lr + 32 * i;
         ap[i] = g.x + (m < g.M ? m : g.M - 1) * g.K;
         bp[i] = g.w + (n < g.N ? n : g.N - 1) * g.K;
     }
-    i32x4_t ra[2], rb[2];
+    i32x4_t ra[PER], rb[PER];
+    // (whole steps without a branch a load)
     auto fetch = [&](int64_t k) {
+        if (k + GK <= g.K) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ra[i] = load_k16(ap[i], k + lc, g.K);
-            rb[i] = load_k16(bp[i], k + lc, g.K);
+            for (int i = 0; i < PER; ++i) {
+                ra[i] = __builtin_bit_cast(
+                    i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(ap[i] + k + lc));
+                rb[i] = __builtin_bit_cast(
+                    i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(bp[i] + k + lc));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                ra[i] = load_k16(ap[i], k + lc, g.K);
+                rb[i] = load_k16(bp[i], k + lc, g.K);
+            }
         }
     };
-    i32x4_t acc[4][4];
+    i32x4_t acc[TM][TM];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < TM; ++j)
             acc[i][j] = i32x4_t{0, 0, 0, 0};
     if (kb < ke)
         fetch(kb);
-    for (int64_t k = kb; k < ke; k += GK) {
-        __syncthreads();
+    int at = 0;
+    // one barrier a step: a wave past it is done with the other buffer's
+    // fragments, which the next step overwrites
+    for (int64_t k = kb; k < ke; k += GK, at ^= 1) {
+        unsigned char *const As = lds[at][0], *const Bs = lds[at][1];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<i32x4_t *>(As + (lr + 64 * i) * GPITCH + lc) = ra[i];
-            *reinterpret_cast<i32x4_t *>(Bs + (lr + 64 * i) * GPITCH + lc) = rb[i];
+        for (int i = 0; i < PER; ++i) {
+            *reinterpret_cast<i32x4_t *>(As + (lr + 32 * i) * GPITCH + lc) = ra[i];
+            *reinterpret_cast<i32x4_t *>(Bs + (lr + 32 * i) * GPITCH + lc) = rb[i];
         }
         __syncthreads();
         if (k + GK < ke)
             fetch(k + GK);
-        i32x4_t fa[4], fb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 16 * i + (lane & 15), c = (lane >> 4) * 16;
-            fa[i] = *reinterpret_cast<const i32x4_t *>(As + (wm + r) * GPITCH + c);
-            fb[i] = *reinterpret_cast<const i32x4_t *>(Bs + (wn + r) * GPITCH + c);
+        for (int h = 0; h < GK / 64; ++h) {
+            i32x4_t fa[TM], fb[TM];
+            const int c = h * 64 + (lane >> 4) * 16;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int r = 16 * i + (lane & 15);
+                fa[i] = *reinterpret_cast<const i32x4_t *>(As + (wm + r) * GPITCH + c);
+                fb[i] = *reinterpret_cast<const i32x4_t *>(Bs + (wn + r) * GPITCH + c);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[i][j] =
+                        __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] =
-                    __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < TM; ++i) {
         const int64_t m = m0 + wm + 16 * i + (lane & 15);
         if (m >= g.M)
             continue;
         const float sx = g.xs[m];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < TM; ++j) {
             const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
             const int c[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
             if (g.part == nullptr) {
@@ -177,48 +195,61 @@ namespace {
 
 constexpr int64_t I8_STAGE_K = 128;                  // bytes of K a stage of the pipelined kernel
 constexpr int64_t I8_MAX_BYTES = (1LL << 31) - 8192;  // 32-bit buffer offsets
+
+// The pipelined kernel's tiles: microseconds a stage takes an item with one
+// and with all of its workgroups resident on a CU, and microseconds an item
+// takes beside its stages (epilogue, drain).  Fitted to measurements between
+// 128 and 8192 tokens, 512 and 8192 wide, 4096 and 28672 channels; for
+// instance (us, tile and slots in LDS): 128 tokens, 4096 -> 14336: 128 x 64 of
+// four 20, 128 x 128 of four 25, of two 33, 64 x 64 24, 256 x 256 54; 512 tokens,
+// 8192 -> 8192: 128 x 128 of four 43, 128 x 64 58, 128 x 128 of two 60; 2048
+// tokens, 4096 -> 4096: 128 x 128 of two 36, of four 42, 256 x 256 51.
 struct I8Tile {
-    int bm, bn, resident;  // workgroups a CU
-    double rate;           // relative rate of a full tile
+    int bm, bn, resident;
+    double stage_one, stage_all, item;
 };
-constexpr I8Tile I8_TILES[] = {{256, 256, 1, 1.0}, {128, 128, 2, 0.8}};
+constexpr I8Tile I8_TILES[] = {{256, 256, 1, 1.5, 1.5, 8.0},
+                               {128, 128, 2, 0.7, 0.95, 2.5},
+                               {128, 128, 1, 0.56, 0.56, 1.5},
+                               {128, 64, 1, 0.43, 0.43, 1.0},
+                               {64, 64, 2, 0.34, 0.5, 1.0}};
+constexpr int I8_NUM_TILES = sizeof(I8_TILES) / sizeof(I8_TILES[0]);
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The general kernel's tile: 64 x 64 where 128 x 128 ones are fewer than two a CU.
+int64_t general_tile(int64_t M, int64_t N)
+{
+    return ceil_div(M, 128) * ceil_div(N, 128) < 512 ? 64 : 128;
+}
+
 }  // namespace
 
-I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16)
+I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K)
 {
     I8Plan p{I8Plan::GENERAL, 1, 0, 0};
-    const int64_t elt = bf16 ? 2 : 4;
-    if (M <= I8_ROWS_MOST && K % 16 == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES) {
+    const bool dma = K % 16 == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES;
+    if (dma && gemm_i8_rows_ok(M, N)) {
         p.cfg = I8Plan::ROWS;
-    } else if (K % 16 == 0 && N % (16 / elt) == 0 && M * K < I8_MAX_BYTES && N * K < I8_MAX_BYTES &&
-        M * N * 4 < I8_MAX_BYTES) {
-        // Time of a configuration: rounds of resident workgroups, each its
-        // products at the rate a full GPU sustains plus a fill and an epilogue;
-        // a split writes and reads int32 partial sums and launches once more.
+    } else if (dma && M * N * 4 < I8_MAX_BYTES) {
+        // rounds of resident workgroups, each its items' stages; a split writes
+        // and reads int32 partial sums and launches once more
         const int64_t stages = ceil_div(K, I8_STAGE_K);
         double best = -1.0;
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < I8_NUM_TILES; ++c) {
             const I8Tile &t = I8_TILES[c];
             const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
             for (int64_t z = 1; z <= 16 && (z == 1 || stages / z >= 4); ++z) {
                 const int64_t sps = ceil_div(stages, z);
-                const int64_t used = ceil_div(stages, sps);
-                if (used != z || (z > 1 && z * M * N * 4 >= I8_MAX_BYTES))
+                if (ceil_div(stages, sps) != z || z * M * N * 4 >= I8_MAX_BYTES)
                     continue;
-                const int64_t slots = 256 * t.resident;
-                const int64_t rounds = ceil_div(tiles * z, slots);
-                const int64_t busy = tiles * z < slots ? ceil_div(tiles * z, 256) : t.resident;
-                double s = static_cast<double>(rounds) *
-                           (2.0 * t.bm * t.bn * sps * I8_STAGE_K * static_cast<double>(busy) /
-                                (9.0e12 * t.rate) +
-                            4e-6);
+                const int64_t rounds = ceil_div(tiles * z, 256 * t.resident);
+                const double stage = tiles * z <= 256 ? t.stage_one : t.stage_all;
+                double us = 5.0 + static_cast<double>(rounds) * (sps * stage + t.item);
                 if (z > 1)
-                    s += 8.0 * z * M * N / 4.0e12 + 5e-6;
-                if (best < 0 || s < best) {
-                    best = s;
+                    us += 8.0 * z * M * N / 4.0e6 + 5.0;
+                if (best < 0 || us < best) {
+                    best = us;
                     p.cfg = c;
                     p.splits = static_cast<int>(z);
                     p.k_per_split = sps * I8_STAGE_K;
@@ -226,12 +257,12 @@ I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K, int bf16)
             }
         }
     } else {
-        const int64_t tiles = ceil_div(M, GB) * ceil_div(N, GB);
-        const int64_t steps = ceil_div(K, GK);
-        // split K until two workgroups a CU are reached, eight steps a split at
+        // split K until two workgroups a CU are reached, four steps a split at
         // least
+        const int64_t b = general_tile(M, N), tiles = ceil_div(M, b) * ceil_div(N, b);
+        const int64_t steps = ceil_div(K, GK);
         int64_t z = tiles > 0 ? 512 / tiles : 1;
-        z = z < steps / 8 ? z : steps / 8;
+        z = z < steps / 4 ? z : steps / 4;
         z = z < 1 ? 1 : (z > 32 ? 32 : z);
         const int64_t per = ceil_div(steps, z);
         p.splits = static_cast<int>(ceil_div(steps, per));
@@ -254,14 +285,18 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
     } else if (p.cfg != I8Plan::GENERAL) {
         e = launch_gemm_i8_dma(bf16, g, p.cfg, st);
     } else {
-        const int64_t tiles = ceil_div(g.M, GB) * ceil_div(g.N, GB);
+        const int64_t b = general_tile(g.M, g.N), tiles = ceil_div(g.M, b) * ceil_div(g.N, b);
         if (tiles > 0x7fffffff)
             return hipErrorInvalidConfiguration;
         const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
-        if (bf16)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<uint16_t>), grid, dim3(GTHREADS), 0, st, g);
+        if (bf16 && b == 64)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, uint16_t>), grid, dim3(GTHREADS), 0, st, g);
+        else if (bf16)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, uint16_t>), grid, dim3(GTHREADS), 0, st, g);
+        else if (b == 64)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, float>), grid, dim3(GTHREADS), 0, st, g);
         else
-            hipLaunchKernelGGL((gemm_i8_general_kernel<float>), grid, dim3(GTHREADS), 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, float>), grid, dim3(GTHREADS), 0, st, g);
         e = hipGetLastError();
     }
     if (e != hipSuccess || p.splits == 1)

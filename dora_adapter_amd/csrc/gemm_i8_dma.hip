@@ -1,5 +1,5 @@
 // gemm_i8_dma.hip - the pipelined int8 product (gfx950): y = xq wq^T scaled by
-// token and output channel, for widths of whole 16-byte chunks.
+// token and output channel, for widths d_in of whole 16-byte chunks.
 //
 // v_mfma_i32_16x16x64_i8 takes 16 bytes of a row per lane like the bf16
 // 16 x 16 x 32 form, so an int8 matrix of width K is loaded and laid out in
@@ -9,7 +9,7 @@
 //
 // A workgroup walks its share of the work items (an output tile, or one K
 // range of it) as one unbroken stream of stages: while the products of stage
-// S run, stage S + 2 loads, whichever item it belongs to, so that the pipeline
+// S run, stage S + SLOTS loads, whichever item it belongs to, so that the pipeline
 // does not drain between items.  Item order: XCD x owns a contiguous run of
 // items, its workgroups take them in turn.
 //
@@ -32,8 +32,7 @@ struct FragsI8 {
 // Output kinds: the element types of y, or int32 partial sums.
 constexpr int OUT_BF16 = 0, OUT_F32 = 1, OUT_PART = 2;
 
-constexpr int I8_STAGE_ROWS = 32;                       // rows of a wave's staging area
-constexpr int I8_STAGE_BYTES = I8_STAGE_ROWS * 128;     // 64 bf16 or 32 fp32 / int32 columns
+constexpr int I8_STAGE_ROWS = 32;  // rows of a wave's staging area, 128 bytes each at most
 
 // Fragment read number O of half `h`: A fragments, then B.
 template <int TM, int TN, int WTM, int WTN, int O>
@@ -48,8 +47,9 @@ __device__ __forceinline__ void read_one_i8(FragsI8<TM, TN> &f, const unsigned c
             __builtin_bit_cast(i32x4_t, read_frag16(Bs, wn * WTN + (O - TM) * 16, h, lane));
 }
 
-// PERCU: workgroups resident on a CU (the register budget).
-template <int BM, int BN, int WM, int WN, int PERCU, int OUT>
+// SLOTS: stages held in LDS (a power of two); PERCU: workgroups resident on a CU
+// (the register budget).
+template <int BM, int BN, int WM, int WN, int SLOTS, int PERCU, int OUT>
 __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
     gemm_i8_dma_kernel(I8GemmArgs g)
 {
@@ -62,14 +62,18 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
     constexpr int WTM = BM / WM, WTN = BN / WN;
     constexpr int TM = WTM / 16, TN = WTN / 16;
     constexpr int ELT = OUT == OUT_BF16 ? 2 : 4;
-    constexpr int SLAB = 128 / ELT;  // columns of a staging pass
+    constexpr int SLAB = WTN < 128 / ELT ? WTN : 128 / ELT;  // columns of a staging pass
+    constexpr int SROW = SLAB * ELT;                         // bytes of a staging row
+    constexpr int SCH = SROW / 16;                           // its 16-byte chunks
+    constexpr int STAGE = I8_STAGE_ROWS * SROW;
     static_assert(WTM % I8_STAGE_ROWS == 0 && WTN % SLAB == 0, "whole staging passes");
     static_assert(DA::PER + DB::PER == C::LPS, "load count");
     // scales of the wave's rows and columns: in LDS where the accumulators leave
     // no registers for them
     constexpr bool LDS_SCALES = TM * TN > 32 && OUT != OUT_PART;
-    constexpr int WAVE_BYTES = I8_STAGE_BYTES + (LDS_SCALES ? (WTM + WTN) * 4 : 0);
-    constexpr int SMEM = C::OPS + NW * WAVE_BYTES;
+    constexpr int WAVE_BYTES = STAGE + (LDS_SCALES ? (WTM + WTN) * 4 : 0);
+    constexpr int OPS = SLOTS * C::STAGE_BYTES;
+    constexpr int SMEM = OPS + NW * WAVE_BYTES;
     static_assert(SMEM * PERCU <= 160 * 1024, "LDS");
     __shared__ __align__(1024) unsigned char smem[SMEM];
 
@@ -140,8 +144,8 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
     };
     plan();
 
-    auto slot = [&](int S) { return smem + (S & 1) * C::STAGE_BYTES; };
-    unsigned char *const stg = smem + C::OPS + wave * WAVE_BYTES;
+    auto slot = [&](int S) { return smem + (S & (SLOTS - 1)) * C::STAGE_BYTES; };
+    unsigned char *const stg = smem + OPS + wave * WAVE_BYTES;
 
     constexpr int GA = DA::PER / G, NG = C::LPS / G;
     struct Group {
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
 
     // One half stage: the products of `cur`, the fragment reads of the next
     // half into `nxt` (READS), and in half 1 the loads of the cursor's stage
-    // into the slot of running stage S + 2.
+    // into this stage's slot, for running stage S + SLOTS.
     auto half = [&](ACC &acc, auto h_c, int S, FR &cur, FR &nxt, auto reads_c) {
         constexpr int H = decltype(h_c)::value;
         constexpr bool READS = decltype(reads_c)::value;
@@ -191,9 +195,9 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
         constexpr int NOPS = (READS ? NRD : 0) + NLH;
         wait_lgkm0();
         if constexpr (H == 1) {
-            // stage S + 1 has landed, and every wave is done with this slot's
-            // fragments
-            wait_vmcnt<0>();
+            // stage S + 1 has landed (the loads of SLOTS - 2 stages may still be
+            // under way), and every wave is done with this slot's fragments
+            wait_vmcnt<(SLOTS - 2) * C::LPS>();
             stage_barrier();
         }
         const unsigned char *An = slot(H == 0 ? S : S + 1);
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                 constexpr int rd = o - (o * NLH + NOPS - 1) / NOPS;
                 if constexpr (li >= 0) {
                     if constexpr (li % G == 0)
-                        grp = dma_prep(S + 2, li / G);
+                        grp = dma_prep(S + SLOTS, li / G);
                     issue(grp, std::integral_constant<int, li % G>{});
                 } else if constexpr (READS) {
                     read_one_i8<TM, TN, WTM, WTN, rd>(nxt, An, Bn, 1 - H, wm, wn, lane);
@@ -228,15 +232,18 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
         0x00020000);
 
     // Accumulator block (i, j): lane l holds row 16 i + (l & 15), columns
-    // 16 j + 4 (l >> 4) + 0..3 of the wave's tile.  Staging rows are 128
-    // bytes; 16-byte chunk c of row r sits at c ^ swz(r).
+    // 16 j + 4 (l >> 4) + 0..3 of the wave's tile.  16-byte chunk c of staging
+    // row r sits at c ^ swz(r) (of as many bits as a row has chunks).
+    auto chunk = [](int r, int c) { return (c ^ (swz(r) & (SCH - 1))) << 4; };
     auto epilogue = [&](ACC &acc, const Item &it) {
         const int64_t m0 = static_cast<int64_t>(it.tm) * BM + wm * WTM;
         const int64_t n0 = static_cast<int64_t>(it.tn) * BN + wn * WTN;
         const int q4 = lane >> 4;
+        // rows of y in whole 16-byte chunks; else element by element
+        const bool whole = g.N % (16 / ELT) == 0;
         float4 swr[LDS_SCALES ? 1 : TN];
         float sxr[LDS_SCALES ? 1 : TM];
-        float *const lsx = reinterpret_cast<float *>(stg + I8_STAGE_BYTES), *const lsw = lsx + WTM;
+        float *const lsx = reinterpret_cast<float *>(stg + STAGE), *const lsw = lsx + WTM;
         if constexpr (LDS_SCALES) {
 #pragma unroll
             for (int b = 0; b < WTM; b += 64) {
@@ -251,10 +258,14 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
         } else if constexpr (OUT != OUT_PART) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                // (N is a multiple of 4 here: whole quads)
-                const int64_t n = n0 + 16 * j + 4 * q4;
-                swr[j] = n < g.N ? *reinterpret_cast<const float4 *>(g.ws + n)
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                const int64_t n = n0 + 16 * j + 4 * q4, last = g.N - 1;
+                if (whole)
+                    swr[j] = n < g.N ? *reinterpret_cast<const float4 *>(g.ws + n)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                else
+                    swr[j] = make_float4(g.ws[n < last ? n : last], g.ws[n + 1 < last ? n + 1 : last],
+                                         g.ws[n + 2 < last ? n + 2 : last],
+                                         g.ws[n + 3 < last ? n + 3 : last]);
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                         const i32x4_t c = acc[i][j];
                         if constexpr (OUT == OUT_PART) {
                             *reinterpret_cast<i32x4_t *>(
-                                stg + rr * 128 + (((4 * jj + q4) ^ swz(rr)) << 4)) = c;
+                                stg + rr * SROW + chunk(rr, 4 * jj + q4)) = c;
                         } else {
                             const float sx = scale_x(i);
                             const float4 sw = scale_w(j);
@@ -298,27 +309,40 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                                                          static_cast<float>(c[3]) * (sx * sw.w));
                             if constexpr (OUT == OUT_F32)
                                 *reinterpret_cast<float4 *>(
-                                    stg + rr * 128 + (((4 * jj + q4) ^ swz(rr)) << 4)) = v;
+                                    stg + rr * SROW + chunk(rr, 4 * jj + q4)) = v;
                             else
                                 *reinterpret_cast<uint2 *>(
-                                    stg + rr * 128 + (((2 * jj + (q4 >> 1)) ^ swz(rr)) << 4) +
+                                    stg + rr * SROW + chunk(rr, 2 * jj + (q4 >> 1)) +
                                     8 * (q4 & 1)) =
                                     make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                         }
                     }
                 }
 #pragma unroll
-                for (int ps = 0; ps < 4; ++ps) {
-                    const int rr = ps * 8 + (lane >> 3), c = lane & 7;
+                for (int ps = 0; ps < STAGE / 1024; ++ps) {
+                    const int rr = ps * (64 / SCH) + lane / SCH, c = lane % SCH;
                     const i32x4_t v =
-                        *reinterpret_cast<const i32x4_t *>(stg + rr * 128 + ((c ^ swz(rr)) << 4));
+                        *reinterpret_cast<const i32x4_t *>(stg + rr * SROW + chunk(rr, c));
                     const int64_t m = m0 + i2 * 32 + rr;
                     const int64_t n = n0 + hf * SLAB + c * (16 / ELT);
                     const int64_t at =
                         ((OUT == OUT_PART ? static_cast<int64_t>(it.z) * g.M : 0) + m) * g.N + n;
-                    const uint32_t off =
-                        m < g.M && n < g.N ? static_cast<uint32_t>(at * ELT) : OOB_OFFSET;
-                    __builtin_amdgcn_raw_buffer_store_b128(v, out_rs, off, 0, 0);
+                    if (whole) {
+                        const uint32_t off =
+                            m < g.M && n < g.N ? static_cast<uint32_t>(at * ELT) : OOB_OFFSET;
+                        __builtin_amdgcn_raw_buffer_store_b128(v, out_rs, off, 0, 0);
+                    } else if (m < g.M) {
+                        using E = std::conditional_t<ELT == 2, uint16_t, int>;
+                        E *const out = reinterpret_cast<E *>(OUT == OUT_PART
+                                                                 ? static_cast<void *>(g.part)
+                                                                 : g.y) + at;
+#pragma unroll
+                        for (int e = 0; e < 16 / ELT; ++e)
+                            if (n + e < g.N)
+                                out[e] = static_cast<E>(
+                                    ELT == 2 ? static_cast<unsigned int>(v[e / 2]) >> (16 * (e & 1))
+                                             : static_cast<unsigned int>(v[e & 3]));
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -326,9 +350,9 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
     };
 
     FR fa, fb;
-    // prologue: running stages 0 and 1
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    // prologue: running stages 0 .. SLOTS - 1
+#pragma unroll 1
+    for (int p = 0; p < SLOTS; ++p) {
 #pragma unroll
         for (int d = 0; d < NG; ++d) {
             const Group grp = dma_prep(p, d);
@@ -336,7 +360,7 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
         }
         advance();
     }
-    wait_vmcnt<C::LPS>();
+    wait_vmcnt<(SLOTS - 1) * C::LPS>();
     stage_barrier();
     static_for<NRD>([&](auto oc) {
         read_one_i8<TM, TN, WTM, WTN, decltype(oc)::value>(fa, slot(0), slot(0) + C::A_BYTES, 0, wm,
@@ -374,20 +398,20 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
     wait_vmcnt<0>();  // the last loads (of nothing) have deposited their zeros
 }
 
-template <int BM, int BN, int WM, int WN, int PERCU>
+template <int BM, int BN, int WM, int WN, int SLOTS, int PERCU>
 hipError_t launch_i8(int bf16, const I8GemmArgs &g, hipStream_t st)
 {
     const int64_t items = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN) * g.splits;
     const int64_t per = std::min<int64_t>(cus_per_xcd() * PERCU, (items + 7) / 8);
     const dim3 grid(static_cast<unsigned>(8 * per)), block(WM * WN * 64);
     if (g.part != nullptr)
-        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, PERCU, OUT_PART>), grid, block, 0, st,
+        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, SLOTS, PERCU, OUT_PART>), grid, block, 0, st,
                            g);
     else if (bf16)
-        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, PERCU, OUT_BF16>), grid, block, 0, st,
+        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, SLOTS, PERCU, OUT_BF16>), grid, block, 0, st,
                            g);
     else
-        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, PERCU, OUT_F32>), grid, block, 0, st,
+        hipLaunchKernelGGL((gemm_i8_dma_kernel<BM, BN, WM, WN, SLOTS, PERCU, OUT_F32>), grid, block, 0, st,
                            g);
     return hipGetLastError();
 }
@@ -396,11 +420,17 @@ hipError_t launch_i8(int bf16, const I8GemmArgs &g, hipStream_t st)
 
 hipError_t launch_gemm_i8_dma(int bf16, const I8GemmArgs &g, int cfg, hipStream_t st)
 {
-    switch (cfg) {
+    switch (cfg) {  // in the order of I8_TILES
     case 0:
-        return dma::launch_i8<256, 256, 2, 2, 1>(bf16, g, st);
+        return dma::launch_i8<256, 256, 2, 2, 2, 1>(bf16, g, st);
     case 1:
-        return dma::launch_i8<128, 128, 2, 2, 2>(bf16, g, st);
+        return dma::launch_i8<128, 128, 2, 2, 2, 2>(bf16, g, st);
+    case 2:
+        return dma::launch_i8<128, 128, 2, 2, 4, 1>(bf16, g, st);
+    case 3:
+        return dma::launch_i8<128, 64, 2, 2, 4, 1>(bf16, g, st);
+    case 4:
+        return dma::launch_i8<64, 64, 2, 2, 4, 2>(bf16, g, st);
     default:
         return hipErrorInvalidValue;
     }

@@ -1,6 +1,6 @@
 // gemm_i8_rows.hip - the int8 product for a few tokens (gfx950): y = xq wq^T
-// scaled by token and output channel, up to 64 tokens, widths of whole 16-byte
-// chunks.
+// scaled by token and output channel, up to 64 tokens, widths d_in of whole
+// 16-byte chunks.
 //
 // Bound by reading wq once.  A workgroup takes BN output channels; its four
 // waves split K, wave w taking the 128-byte stages w, w + 4, ... (so the
@@ -165,27 +165,34 @@ hipError_t launch_rows(int bf16, const I8GemmArgs &g, hipStream_t st)
 
 }  // namespace dma
 
-// Channels a workgroup and ring slots, by tokens and channels.  More channels
-// read the tokens' rows less often; fewer make more workgroups.  Measured (us,
-// d_in -> d_out):
-//   up to 16 tokens   two workgroups a CU either way: 16 channels (8192 -> 28672:
-//                     42 at one token, 46 at 16; 32 channels 54, 57), but 32 where
-//                     they make one round of the CUs and 16 make two (4096 ->
-//                     14336: 14 against 17)
-//   up to 32          64 channels (8192 -> 28672: 51, with 32 60; 8192 -> 8192: 19,
-//                     21), 16 for few channels (14336 -> 4096: 16, 64 channels 28)
-//   up to 64          64 channels (8192 -> 28672: 56, with 32 78), 16 for few
-//                     (14336 -> 4096: 24, 64 channels 38)
-// The pipelined kernel takes 65 us at 8192 -> 28672 for any of these.
+// Which products run here, and how many channels a workgroup takes and slots a
+// ring has.  More channels read the tokens' rows less often; fewer make more
+// workgroups.  Measured (us, d_in -> d_out):
+//   up to 16 tokens   16 channels, two workgroups a CU (8192 -> 28672: 42 at one
+//                     token, 46 at 16; 32 channels 54, 57; the pipelined kernel
+//                     51), but 32 where they make one round of the CUs and 16 make
+//                     two (4096 -> 14336: 14 against 17)
+//   up to 32          64 channels (8192 -> 28672: 51, 32 channels 60; 8192 -> 8192:
+//                     19, 21), 16 where that is one round (14336 -> 4096: 16, 64
+//                     channels 28)
+//   up to 64          while one round of the CUs takes them: 16 channels up to 4096
+//                     (14336 -> 4096: 24, 32 channels 28), 32 up to 8192 (8192 ->
+//                     8192: 23, 64 channels 25); beyond, the pipelined kernel is as
+//                     fast (4096 -> 14336: 16, 64 channels here 17; 8192 -> 28672: 51,
+//                     56)
+bool gemm_i8_rows_ok(int64_t M, int64_t N) { return M <= 32 || (M <= 64 && N <= 8192); }
+
 hipError_t launch_gemm_i8_rows(int bf16, const I8GemmArgs &g, hipStream_t st)
 {
-    const bool few = g.N < 8192;
+    if (!gemm_i8_rows_ok(g.M, g.N))
+        return hipErrorInvalidValue;
+    const bool few = g.N <= 4096;
     if (g.M <= 16)
         return g.N > 8192 && g.N <= 16384 ? dma::launch_rows<1, 32, 3>(bf16, g, st)
                                           : dma::launch_rows<1, 16, 4>(bf16, g, st);
     if (g.M <= 32)
         return few ? dma::launch_rows<2, 16, 4>(bf16, g, st) : dma::launch_rows<2, 64, 3>(bf16, g, st);
-    return few ? dma::launch_rows<4, 16, 3>(bf16, g, st) : dma::launch_rows<4, 64, 2>(bf16, g, st);
+    return few ? dma::launch_rows<4, 16, 3>(bf16, g, st) : dma::launch_rows<4, 32, 2>(bf16, g, st);
 }
 
 }  // namespace dora
