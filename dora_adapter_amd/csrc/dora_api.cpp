@@ -421,7 +421,7 @@ BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dty
             }
     if (!b.fused_dhdm)
         b.dB = plan_gemm(bf, dbs, d_out * r);
-    b.sweep = T > 0 ? dm_sweep_rows(T, d_out) : 0;
+    b.sweep = T > 0 ? (y8 ? dm_rows8_sweep(T, d_out) : dm_sweep_rows(T, d_out)) : 0;
     b.nchunks = b.fused_dhdm ? b.dB.splits : static_cast<int>(b.sweep);
     const size_t e = esize(dtype);
     b.o_dh = cv.take(static_cast<size_t>(T) * d_out * e);
@@ -687,6 +687,16 @@ int run_dhdm(bool bf16, const void *dy, const void *y, const Rows8 *y8, const fl
     return DORA_OK;
 }
 
+int finish_dm(const Rows8 *y8, const float *dmpart, int nchunks, const float *m, int64_t d_out,
+              float *dm, hipStream_t st)
+{
+    if (y8)
+        DORA_LAUNCH(launch_sum_parts(dmpart, nchunks, d_out, m, dm, st), "dm finish");
+    else
+        DORA_LAUNCH(launch_dm_finish(dmpart, nchunks, m, d_out, dm, st), "dm finish");
+    return DORA_OK;
+}
+
 // dora_backward after its checks (y8 set: y is not read).
 int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W, const void *A,
                   const void *B, const float *m, const float *n, float s, const void *P,
@@ -712,7 +722,7 @@ int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W
     } else {
         DORA_CHECK(run_dhdm(bf, dy, y, y8, m, n, T, d_out, p.sweep, dh, dmpart, st));
     }
-    DORA_LAUNCH(launch_dm_finish(dmpart, p.nchunks, m, d_out, dm, st), "dm finish");
+    DORA_CHECK(finish_dm(y8, dmpart, p.nchunks, m, d_out, dm, st));
     // 2. Q = s dh B  (A K-major, B MN-major).
     DORA_CHECK(run_store(bf, p.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
                          reinterpret_cast<float *>(w + p.o_Qpart), st, "Q = s dh B"));
@@ -762,7 +772,7 @@ int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const vo
         DORA_CHECK(run_dhdm_dB(b, dy, y, m, n, P, T, d_out, r, dh, dmpart, bslots, 1, s, st));
     else
         DORA_CHECK(run_dhdm(bf, dy, y, y8, m, n, T, d_out, b.sweep, dh, dmpart, st));
-    DORA_LAUNCH(launch_dm_finish(dmpart, b.nchunks, m, d_out, dm, st), "dm finish");
+    DORA_CHECK(finish_dm(y8, dmpart, b.nchunks, m, d_out, dm, st));
     DORA_CHECK(run_store(bf, b.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
                          reinterpret_cast<float *>(w + b.o_Qpart), st, "Q = s dh B"));
     {

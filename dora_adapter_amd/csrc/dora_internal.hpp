@@ -266,6 +266,11 @@ hipError_t launch_dh_dm_rows8(int bf16, const void *dy, const int8_t *yq, const 
                               int group, const float *m, const float *n, int64_t T, int64_t d_out,
                               int64_t sweep, void *dh, float *dm_part, hipStream_t st);
 
+// Its rows per sweep, and sums of its partial sums: out = sum_p part[p] / over.
+int64_t dm_rows8_sweep(int64_t T, int64_t d_out);
+hipError_t launch_sum_parts(const float *part, int parts, int64_t d, const float *over, float *out,
+                            hipStream_t st);
+
 // y[m, n] = xs[m] ws[n] sum_k x[m, k] w[n, k], int8 operands (gemm_i8.hip).
 struct I8GemmArgs {
     const int8_t *x, *w;

@@ -480,10 +480,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_held_kernel(NormGradArgs a)
     }
 }
 
-// Sums of `parts` rows: 64 columns a workgroup, its 16 waves taking every 16th
-// row each, then the 16 sums in order.
+// Sums of `parts` rows, each divided by its column's `over` (or 1): 64 columns a
+// workgroup, its 16 waves taking every 16th row each, then the 16 sums in order.
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict__ part, int parts,
-                                                         int64_t d, float *__restrict__ out)
+                                                         int64_t d, const float *__restrict__ over,
+                                                         float *__restrict__ out)
 {
     __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
 #pragma unroll
         for (int k = 1; k < 16; ++k)
             acc += sums[k][lane];
-        out[j] = acc;
+        out[j] = over != nullptr ? acc / over[j] : acc;
     }
 }
 
@@ -775,7 +776,7 @@ void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
     }
     if (dw != nullptr && parts > 1)
         hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64)), dim3(1024),
-                           0, st, part, a.parts, a.d, dw);
+                           0, st, part, a.parts, a.d, static_cast<const float *>(nullptr), dw);
 }
 }  // namespace
 
@@ -834,6 +835,22 @@ hipError_t launch_dh_dm_rows8(int bf16, const void *dy, const int8_t *yq, const 
         hipLaunchKernelGGL((dh_dm_rows8_kernel<float>), grid, dim3(ROW_THREADS), 0, st,
                            static_cast<const float *>(dy), yq, ys, group, m, n, T, d_out, sweep,
                            static_cast<float *>(dh), dm_part);
+    return hipGetLastError();
+}
+
+int64_t dm_rows8_sweep(int64_t T, int64_t d_out)
+{
+    // as the pass over a stored y, but at least two rows a thread: one leaves
+    // more bytes of partial sums than the pass reads
+    const int64_t r = dm_sweep_rows(T, d_out), most = (T + 1) / 2;
+    return r < most ? r : most;
+}
+
+hipError_t launch_sum_parts(const float *part, int parts, int64_t d, const float *over, float *out,
+                            hipStream_t st)
+{
+    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((d + 63) / 64)), dim3(1024), 0, st,
+                       part, parts, d, over, out);
     return hipGetLastError();
 }
 
