@@ -1985,7 +1985,7 @@ size_t dora_rmsnorm_backward_workspace(int64_t T, int64_t d, int dtype)
 {
     if (check_dtype(dtype) || check_rows(T, d))
         return 0;
-    return align_up(static_cast<size_t>(rmsnorm_parts(T, d)) * d * sizeof(float));
+    return align_up(static_cast<size_t>(rmsnorm_parts(T, d, dtype == DORA_BF16)) * d * sizeof(float));
 }
 
 int dora_rmsnorm_backward(const void *dy, const void *h, const void *w, const float *rstd,
@@ -2010,7 +2010,8 @@ int dora_rmsnorm_backward(const void *dy, const void *h, const void *w, const fl
          {{rstd, T * sizeof(float)}, "rstd"}}));
     DORA_CHECK(check_disjoint({{{dw, d * sizeof(float)}, "dw"}, {{ws, need}, "workspace"}},
                               {{{dres, rows}, "dres"}}));
-    NormGradArgs a{dy, h, w, dres, rstd, T, d, dx, static_cast<float *>(ws), rmsnorm_parts(T, d)};
+    NormGradArgs a{dy, h, w, dres, rstd, T, d, dx, static_cast<float *>(ws),
+                   rmsnorm_parts(T, d, dtype == DORA_BF16)};
     DORA_LAUNCH(launch_rmsnorm_grad(dtype == DORA_BF16, a, dw, static_cast<hipStream_t>(stream)),
                 "rmsnorm backward");
     return DORA_OK;

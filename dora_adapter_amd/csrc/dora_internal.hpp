@@ -254,7 +254,7 @@ struct NormGradArgs {
     int parts;
 };
 // Partial sums of dw the gradient keeps (its workspace is parts * d floats).
-int rmsnorm_parts(int64_t T, int64_t d);
+int rmsnorm_parts(int64_t T, int64_t d, int bf16);
 // dw null: not formed.
 hipError_t launch_rmsnorm_grad(int bf16, const NormGradArgs &a, float *dw, hipStream_t st);
 hipError_t launch_quantize_rows(int bf16, const void *x, int64_t rows, int64_t d, int group,

@@ -488,21 +488,25 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
 {
     __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-    float acc = 0.f;
-    if (j < d) {
+    for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 64; j0 < d;
+         j0 += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t j = j0 + lane;
+        float acc = 0.f;
+        if (j < d) {
 #pragma unroll 8
-        for (int p = wave; p < parts; p += 16)
-            acc += part[static_cast<int64_t>(p) * d + j];
-    }
-    sums[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0 && j < d) {
-        acc = sums[0][lane];
+            for (int p = wave; p < parts; p += 16)
+                acc += part[static_cast<int64_t>(p) * d + j];
+        }
+        __syncthreads();  // the last columns' sums have been read
+        sums[wave][lane] = acc;
+        __syncthreads();
+        if (wave == 0 && j < d) {
+            acc = sums[0][lane];
 #pragma unroll
-        for (int k = 1; k < 16; ++k)
-            acc += sums[k][lane];
-        out[j] = over != nullptr ? acc / over[j] : acc;
+            for (int k = 1; k < 16; ++k)
+                acc += sums[k][lane];
+            out[j] = over != nullptr ? acc / over[j] : acc;
+        }
     }
 }
 
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(1024)
                        scale, redu);
 }
 
-// Row blockIdx.x + k gridDim.x, vectors of blockIdx.y's share.
+// Rows blockIdx.x + k gridDim.x, shares (8192 columns) blockIdx.y + k gridDim.y.
 template <typename T>
 __global__ void __launch_bounds__(ROW_THREADS) dequantize_kernel(const int8_t *q,
                                                                  const float *scale, int64_t rows,
@@ -575,9 +579,11 @@ __global__ void __launch_bounds__(ROW_THREADS) dequantize_kernel(const int8_t *q
     constexpr int VPT = 4;
     const int64_t groups = group ? (d + group - 1) / group : 1;
     const int shift = group ? 31 - __clz(group) : 63;
-    const int64_t j0 =
-        (static_cast<int64_t>(blockIdx.y) * ROW_THREADS * VPT + threadIdx.x) * 8;
+    constexpr int SHARE = ROW_THREADS * VPT * 8;
+    for (int64_t c = blockIdx.y * static_cast<int64_t>(SHARE); c < d;
+         c += gridDim.y * static_cast<int64_t>(SHARE))
     for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
+        const int64_t j0 = c + threadIdx.x * 8;
         Raw8i r[VPT];
         float s[VPT];
 #pragma unroll
@@ -650,22 +656,26 @@ unsigned row_groups(int64_t rows)
     return static_cast<unsigned>(rows < MAX_ROW_GROUPS ? rows : MAX_ROW_GROUPS);
 }
 
+// A launch holds fewer than 2^32 threads.
+bool launchable(int64_t groups, int64_t threads) { return groups < (int64_t(1) << 32) / threads; }
+
 // Rows held in registers: vectors a thread and threads a row.  Up to two rows a
 // CU: as many threads as the row has vectors, so that one row's latency is
-// short; more rows: `most` vectors a thread.  vpt = 0: the row is too long.
+// short; more rows: `most` vectors a thread.  vpt = 0: the row is too long, or
+// the rows too many for one launch of a workgroup each.
 struct RowShape {
     int vpt, threads;
 };
 RowShape held_shape(int64_t T, int64_t d, int most)
 {
     const int64_t vecs = (d + 7) / 8;
-    if (vecs > 4096 || T > 0x7fffffff)
+    if (vecs > 4096)
         return {0, 0};
     int vpt = T <= 512 ? 1 : most;
     while (vecs > 1024 * static_cast<int64_t>(vpt))
         vpt *= 2;
     const int64_t threads = ((vecs + vpt - 1) / vpt + 63) / 64 * 64;
-    return {vpt, static_cast<int>(threads)};
+    return {launchable(T, threads) ? vpt : 0, static_cast<int>(threads)};
 }
 
 template <typename T>
@@ -692,17 +702,17 @@ void quantize_launch(const T *x, int64_t rows, int64_t d, int group, int8_t *q, 
     // four vectors a thread: 35 us at 8192 x 8192, against 58 (one) and 40 (two)
     RowShape s = held_shape(rows, d, 4);
     int64_t shares = 1;
-    if (group != 0 && rows <= 0x7fffffff && d <= (int64_t(1) << 30)) {
+    if (group != 0 && d <= (int64_t(1) << 30)) {
         // no reduction over the row: 8192 columns a workgroup (2048 with few rows)
         const int64_t vecs = (d + 7) / 8;
         s.vpt = rows <= 512 ? 1 : 4;
         s.threads = static_cast<int>(vecs < 256 * s.vpt ? ((vecs + s.vpt - 1) / s.vpt + 63) / 64 * 64
                                                        : 256);
         shares = (vecs + s.vpt * s.threads - 1) / (s.vpt * s.threads);
-        if (shares > 65535)
+        if (shares > 65535 || !launchable(rows * shares, s.threads))
             s.vpt = 0;
     }
-    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(shares)),
+    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(s.vpt ? shares : 1)),
         block(static_cast<unsigned>(s.threads));
     if (s.vpt == 1)
         hipLaunchKernelGGL((quantize_held_kernel<T, 1>), grid, block, 0, st, x, d, group, q, scale);
@@ -716,17 +726,29 @@ void quantize_launch(const T *x, int64_t rows, int64_t d, int group, int8_t *q, 
 }
 }  // namespace
 
-int rmsnorm_parts(int64_t T, int64_t d)
+namespace {
+// Rows whose gradient is formed in one pass, held in a workgroup's registers.
+bool grad_held(int64_t d, bool wide) { return (d + 7) / 8 <= (wide ? 2048 : 4096); }
+}  // namespace
+
+int rmsnorm_parts(int64_t T, int64_t d, int bf16)
 {
-    // a workgroup a CU as soon as there are rows for them, then 16 rows a
-    // workgroup, up to the workgroups that fit the CUs at once (rows too long
-    // for the registers: column blocks times row shares)
     const int64_t vecs = (d + 7) / 8;
-    const int64_t waves = vecs <= 4096 ? (vecs + 127) / 128 : 4;
-    const int64_t fit = 256 * (16 / (waves < 16 ? waves : 16));
-    int64_t p = T / 16 > 256 ? T / 16 : 256;
-    p = p < fit ? p : fit;
-    p = p < T ? p : T;
+    int64_t p;
+    if (grad_held(d, !bf16)) {
+        // a workgroup a CU as soon as there are rows for them, then 16 rows a
+        // workgroup, up to the workgroups that fit the CUs at once
+        const int64_t waves = (vecs + 127) / 128;
+        const int64_t fit = 256 * (16 / (waves < 16 ? waves : 16));
+        p = T / 16 > 256 ? T / 16 : 256;
+        p = p < fit ? p : fit;
+        p = p < T ? p : T;
+    } else {
+        // about 2048 workgroups over column blocks and row shares, 16 rows each
+        // at least
+        p = 2048 / ((vecs + ROW_THREADS - 1) / ROW_THREADS);
+        p = p < (T + 15) / 16 ? p : (T + 15) / 16;
+    }
     return static_cast<int>(p < 1 ? 1 : p);
 }
 
@@ -741,6 +763,16 @@ hipError_t launch_rmsnorm(int bf16, const NormArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
+hipError_t launch_sum_parts(const float *part, int parts, int64_t d, const float *over, float *out,
+                            hipStream_t st)
+{
+    const int64_t blocks = (d + 63) / 64;
+    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
+                       dim3(1024), 0, st, part, parts, d, over, out);
+    return hipGetLastError();
+}
+
+
 namespace {
 template <typename T>
 void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
@@ -751,7 +783,7 @@ void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
     float *const part = a.dw_part;
     // one part is the sum itself
     a.dw_part = dw == nullptr ? nullptr : (parts == 1 ? dw : part);
-    if (a.T > 0 && vecs <= (WIDE ? 2048 : 4096)) {
+    if (a.T > 0 && grad_held(a.d, WIDE)) {
         // the fewest vectors a thread that 1024 threads allow, two at least
         // where the registers take two rows of them (bf16)
         const int vpt = vecs <= 64 ? 1 : (WIDE && vecs <= 1024 ? 1 : (vecs <= 2048 ? 2 : 4));
@@ -775,8 +807,7 @@ void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
                                block, 0, st, a);
     }
     if (dw != nullptr && parts > 1)
-        hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((a.d + 63) / 64)), dim3(1024),
-                           0, st, part, a.parts, a.d, static_cast<const float *>(nullptr), dw);
+        launch_sum_parts(part, a.parts, a.d, nullptr, dw, st);
 }
 }  // namespace
 
@@ -806,10 +837,13 @@ hipError_t launch_dequantize_rows(int bf16, const int8_t *q, const float *scale,
 {
     if (rows == 0)
         return hipSuccess;
-    const int64_t shares = (d + ROW_THREADS * 32 - 1) / (ROW_THREADS * 32);
-    if (shares > 65535)
-        return hipErrorInvalidConfiguration;
-    const dim3 grid(row_groups(rows), static_cast<unsigned>(shares)), block(ROW_THREADS);
+    int64_t shares = (d + ROW_THREADS * 32 - 1) / (ROW_THREADS * 32);
+    shares = shares < 4096 ? shares : 4096;
+    // (2^23 workgroups at most)
+    const int64_t groups = (int64_t(1) << 23) / shares;
+    const dim3 grid(static_cast<unsigned>(rows < groups ? rows : groups),
+                    static_cast<unsigned>(shares)),
+        block(ROW_THREADS);
     if (bf16)
         hipLaunchKernelGGL((dequantize_kernel<uint16_t>), grid, block, 0, st, q, scale, rows, d,
                            group, static_cast<uint16_t *>(out));
@@ -844,14 +878,6 @@ int64_t dm_rows8_sweep(int64_t T, int64_t d_out)
     // more bytes of partial sums than the pass reads
     const int64_t r = dm_sweep_rows(T, d_out), most = (T + 1) / 2;
     return r < most ? r : most;
-}
-
-hipError_t launch_sum_parts(const float *part, int parts, int64_t d, const float *over, float *out,
-                            hipStream_t st)
-{
-    hipLaunchKernelGGL(sum_parts_kernel, dim3(static_cast<unsigned>((d + 63) / 64)), dim3(1024), 0, st,
-                       part, parts, d, over, out);
-    return hipGetLastError();
 }
 
 }  // namespace dora

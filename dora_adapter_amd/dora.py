@@ -471,17 +471,24 @@ def dora_rmsnorm(x, w, eps=1e-6, residual=None, want_y=True, want_h=None, want_r
     _need("w", w, dev, x.dtype, d)
     if residual is not None:
         _need("residual", residual, dev, x.dtype, T, d)
-    kinds = _norm_outputs(x.dtype, T, d, n)
     if out is None:
+        kinds = _norm_outputs(x.dtype, T, d, n)
         want = {"y": want_y, "h": residual is not None if want_h is None else want_h,
                 "rstd": want_rstd, "q": quantize, "scale": quantize}
         out = {k: torch.empty(*v[1:], dtype=v[0], device=dev) for k, v in kinds.items()
                if want[k]}
     else:
         for k, t in out.items():
-            if k not in kinds:
+            if k == "y" or k == "h":
+                _need(k, t, dev, x.dtype, T, d)
+            elif k == "q":
+                _need(k, t, dev, torch.int8, T, d)
+            elif k == "scale":
+                _need(k, t, dev, torch.float32, T, n)
+            elif k == "rstd":
+                _need(k, t, dev, torch.float32, T)
+            else:
                 raise ValueError(f"out has no place for {k!r}")
-            _need(k, t, dev, *kinds[k])
         if ("q" in out) != ("scale" in out):
             raise ValueError("q and scale come together")
     if "y" not in out and "q" not in out:

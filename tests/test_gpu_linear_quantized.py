@@ -133,3 +133,29 @@ def test_merged_weight_in_8_bits_behind_the_norm():
     bound = (sx / 2 * merged.cpu().double().abs().sum(1)[None]
              + v.abs().sum(1, keepdim=True) * sw.T / 2 + 1032 * sx * sw.T / 4)
     assert ((ref - full).abs() <= 1.01 * bound).all()
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(3, 32768, 65600), (70, 32768, 65600)])
+def test_operands_past_2_gib(T, d_in, d_out):
+    say("int8 linear", T, d_in, d_out)
+    g = torch.Generator(DEV).manual_seed(3)
+    wq = torch.randint(-127, 128, (d_out, d_in), generator=g, device=DEV, dtype=torch.int8)
+    xq = torch.randint(-127, 128, (T, d_in), generator=g, device=DEV, dtype=torch.int8)
+    xs = torch.rand(T, 1, generator=g, device=DEV)
+    ws = torch.rand(d_out, 1, generator=g, device=DEV)
+    y = D.dora_linear_quantized(xq, xs, wq, ws, dtype=F32)
+    at = torch.tensor([0, 1, 40000, 65535, 65536, d_out - 1], device=DEV)
+    ref = R.linear(xq.cpu(), xs.cpu(), wq[at].cpu(), ws[at].cpu())
+    off = (y[:, at].cpu().double() - ref).abs()
+    assert (off <= ref.abs() * 4.1 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,d_in,d_out", [
+    (20, 512, 4100), (20, 512, 9000), (40, 512, 4090), (40, 256, 8200), (60, 256, 8192),
+    (128, 256, 14336), (200, 16, 16), (512, 512, 4097), (700, 128, 8200), (2048, 128, 4096),
+    (2049, 272, 8199), (96, 8192, 64), (130, 16400, 72)])
+def test_every_tile_choice(T, d_in, d_out, dt):
+    """Sizes on both sides of the rules that choose a kernel and its tile."""
+    say("int8 linear", T, d_in, d_out, dt)
+    check(operands(T * 3 + d_out, T, d_in, d_out, lo=-128), dt, f"{T} x {d_in} x {d_out}")

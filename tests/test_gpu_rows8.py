@@ -318,3 +318,81 @@ def test_rows_calls_refuse_what_they_cannot_read():
         D.dora_rmsnorm(x, w, eps=-1.0)
     with pytest.raises(D.DoraError):
         D.dora_rmsnorm(x, w, out={"y": x, "h": x})
+
+
+# ------------------------------------------------------------ the largest sizes
+def test_more_rows_than_one_launch_holds():
+    """70 million rows of 4: a workgroup a row would be more threads than a
+    launch takes."""
+    T, d = 70_000_000, 4
+    g = torch.Generator(DEV).manual_seed(1)
+    x = torch.randn(T, d, generator=g, device=DEV, dtype=BF)
+    say("quantize", T, d)
+    q, s = D.dora_quantize_rows(x)
+    at = torch.tensor([0, 1, 2 ** 20 - 1, 2 ** 20, 67_108_863, 67_108_864, T - 2, T - 1])
+    rq, rs = R.quantize(x[at.to(DEV)].cpu(), 0)
+    assert torch.equal(q[at.to(DEV)].cpu(), rq) and torch.equal(s[at.to(DEV)].cpu(), rs)
+    say("dequantize", T, d)
+    v = D.dora_dequantize_rows(q, s)
+    assert torch.equal(v[at.to(DEV)].cpu(), (rq.float() * rs).to(BF))
+    del q, s, v
+    w = torch.ones(d, device=DEV, dtype=BF)
+    say("rmsnorm", T, d)
+    o = D.dora_rmsnorm(x, w, 1e-5)
+    ref, _ = R.norm(x[at.to(DEV)].cpu(), w.cpu(), 1e-5)
+    within(o["y"][at.to(DEV)], ref, ref.abs() * (2.0 ** -8 + 100 * U), "y")
+
+
+def test_offsets_past_32_bits():
+    T, d = 1_050_000, 2056   # 2.16e9 elements
+    g = torch.Generator(DEV).manual_seed(2)
+    x = torch.randn(T, d, generator=g, device=DEV, dtype=BF)
+    at = torch.tensor([0, T // 2, 1_044_494, 1_044_495, T - 1])
+    for group in (0, 128):
+        say("quantize", T, d, group)
+        q, s = D.dora_quantize_rows(x, group=group)
+        rq, rs = R.quantize(x[at.to(DEV)].cpu(), group)
+        assert torch.equal(q[at.to(DEV)].cpu(), rq) and torch.equal(s[at.to(DEV)].cpu(), rs)
+        say("dequantize", T, d, group)
+        v = D.dora_dequantize_rows(q, s, group=group)
+        assert torch.equal(v[at.to(DEV)].cpu(), (rq.float() * R.spread(rs, d, group).float()).to(BF))
+        del q, s, v
+    w = (1 + torch.randn(d, generator=g, device=DEV) / 8).to(BF)
+    say("rmsnorm and its gradient", T, d)
+    f = D.dora_rmsnorm(x, w, 1e-5, want_rstd=True)
+    o = D.dora_rmsnorm_backward(f["y"], x, w, f["rstd"])
+    xs, ys = x[at.to(DEV)].cpu(), f["y"][at.to(DEV)].cpu()
+    ref, _ = R.norm(xs, w.cpu(), 1e-5)
+    within(ys, ref, ref.abs() * (2.0 ** -8 + (d / 64 + 64) * U), "y")
+    rs = f["rstd"][at.to(DEV)].cpu()
+    dx, _, dot, _ = R.norm_grad(ys, xs, w.cpu(), rs, None)
+    r = rs.double()[:, None]
+    bound = (dx.abs() * 2.0 ** -8 + 8 * U * (w.cpu().double() * ys.double()).abs() * r
+             + xs.double().abs() * r ** 3 / d * dot * ((d / 64 + 64) * U + 8 * U))
+    within(o["dx"][at.to(DEV)], dx, bound * (1 + 1e-6), "dx")
+    # dw of one column in 64 bits: at most T / 1 terms summed by parts of T / parts
+    col = (f["y"][:, 5].double() * x[:, 5].double() * f["rstd"].double())
+    assert abs(float(o["dw"][5]) - float(col.sum())) <= (T / 256 + 300) * U * float(col.abs().sum())
+
+
+def test_long_rows():
+    for T, d in ((1, 3_000_001), (3, 600_000)):
+        x, res, w, dy, dres = draw(d, T, d, BF)
+        gx, gres, gw, gdy, gdres = up(x, res, w, dy, dres)
+        say("rmsnorm", T, d)
+        f = D.dora_rmsnorm(gx, gw, 1e-5, residual=gres, want_rstd=True, quantize=True, group=256)
+        h = R.norm_h(x, res)
+        y, _ = R.norm(h, w, 1e-5)
+        E = (d / 64 + 70) * U
+        within(f["y"], y, y.abs() * (E + 2.0 ** -8), "y")
+        s = R.spread(f["scale"].cpu(), d, 256)
+        within(f["q"].cpu().double() * s, y, s / 2 + y.abs() * E, "q scale")
+        say("rmsnorm backward", T, d)
+        o = D.dora_rmsnorm_backward(gdy, f["h"], gw, f["rstd"], dres=gdres)
+        dx, dw, dot, each = R.norm_grad(dy, h, w, f["rstd"].cpu(), dres)
+        within(o["dw"], dw, (T + 8) * U * each, "dw")
+        r = f["rstd"].cpu().double()[:, None]
+        bound = (dx.abs() * 2.0 ** -8
+                 + 8 * U * ((w.double() * dy.double()).abs() * r + dres.double().abs())
+                 + h.double().abs() * r ** 3 / d * dot * E)
+        within(o["dx"], dx, bound * (1 + 1e-6), "dx")
