@@ -10,9 +10,9 @@
 // consecutive columns 4 (l >> 4) + 0..3.
 //
 // The general kernel: any width and alignment, operands staged through
-// registers.  128 x 128 or 64 x 64 tiles of four waves, 128 bytes of K a step
-// in two LDS buffers; the next step's loads are in flight during this one's
-// products.
+// registers.  256 x 256 (eight waves), 128 x 128 or 64 x 64 (four) tiles, 128 bytes of K
+// a step in two LDS buffers; the next step's loads are in flight during this
+// one's products.
 #include "dora_internal.hpp"
 #include "rows8.hpp"
 
@@ -25,28 +25,18 @@ constexpr int GK = 128;          // bytes of K a step
 constexpr int GPITCH = GK + 16;  // LDS row: 8 rows of a 16-byte read phase on distinct banks
 constexpr int GTHREADS = 256;
 
-// 16 bytes of a row from byte k on, zeros past the width K.
-__device__ __forceinline__ i32x4_t load_k16(const int8_t *row, int64_t k, int64_t K)
+// 16 bytes at p, those at or past `left` (their row's end) read as zero.
+__device__ __forceinline__ i32x4_t load_k16(const int8_t *p, int64_t left)
 {
-    i32x4_t v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        const u32x4_a1_t u = *reinterpret_cast<const u32x4_a1_t *>(row + k);
-        v[0] = static_cast<int>(u.x);
-        v[1] = static_cast<int>(u.y);
-        v[2] = static_cast<int>(u.z);
-        v[3] = static_cast<int>(u.w);
-    } else if (k < K) {
-        unsigned int w[4] = {0u, 0u, 0u, 0u};
+    if (left >= 16)
+        return __builtin_bit_cast(i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(p));
+    unsigned int w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int b = 0; b < 15; ++b)
-            if (k + b < K)
-                w[b >> 2] |= static_cast<unsigned int>(static_cast<uint8_t>(row[k + b]))
-                             << (8 * (b & 3));
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = static_cast<int>(w[q]);
-    }
-    return v;
+    for (int b = 0; b < 15; ++b)
+        if (b < left)
+            w[b >> 2] |= static_cast<unsigned int>(static_cast<uint8_t>(p[b])) << (8 * (b & 3));
+    return i32x4_t{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]),
+                   static_cast<int>(w[3])};
 }
 
 // Four consecutive outputs of row m from column n on.
@@ -66,29 +56,30 @@ __device__ __forceinline__ void store_scaled(const I8GemmArgs &g, int64_t m, int
         }
 }
 
-// B x B tiles (128 or 64) of four waves.
-template <int B, typename T>
-__global__ void __launch_bounds__(GTHREADS, 2) gemm_i8_general_kernel(I8GemmArgs g)
+// B x B tiles of 2 x WN waves (B / 2 rows x B / WN columns each).
+template <int B, int WN, typename T>
+__global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs g)
 {
-    constexpr int TM = B / 32, PER = B / 32;  // blocks of a wave; rows a thread loads
+    constexpr int NT = 128 * WN, ROWS = NT / 8;  // threads; rows they load at a time
+    constexpr int WTN = B / WN, TM = B / 32, TN = WTN / 16, PER = B / ROWS;
     __shared__ __align__(16) unsigned char lds[2][2][B * GPITCH];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * (B / 2), wn = (wave & 1) * (B / 2);
-    const int64_t num_n = (g.N + B - 1) / B;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x / num_n) * B;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x % num_n) * B;
+    const int wm = (wave / WN) * (B / 2), wn = (wave % WN) * WTN;
+    int tm, tn;
+    tile_coords(g.M, g.N, B, B, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * B, n0 = static_cast<int64_t>(tn) * B;
     const int64_t kb = static_cast<int64_t>(blockIdx.y) * g.k_per_split;
     const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
 
-    // thread: chunk tid & 7 of rows (tid >> 3) + 32 i of either operand (rows
+    // thread: chunk tid & 7 of rows (tid >> 3) + ROWS i of either operand (rows
     // past the end: the last one, never stored)
     const int lr = tid >> 3, lc = (tid & 7) * 16;
     const int8_t *ap[PER], *bp[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int64_t m = m0 + lr + 32 * i, n = n0 + lr + 32 * i;
-        ap[i] = g.x + (m < g.M ? m : g.M - 1) * g.K;
-        bp[i] = g.w + (n < g.N ? n : g.N - 1) * g.K;
+        const int64_t m = m0 + lr + ROWS * i, n = n0 + lr + ROWS * i;
+        ap[i] = g.x + (m < g.M ? m : g.M - 1) * g.K + lc;
+        bp[i] = g.w + (n < g.N ? n : g.N - 1) * g.K + lc;
     }
     i32x4_t ra[PER], rb[PER];
     // (whole steps without a branch a load)
@@ -96,24 +87,24 @@ __global__ void __launch_bounds__(GTHREADS, 2) gemm_i8_general_kernel(I8GemmArgs
         if (k + GK <= g.K) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                ra[i] = __builtin_bit_cast(
-                    i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(ap[i] + k + lc));
-                rb[i] = __builtin_bit_cast(
-                    i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(bp[i] + k + lc));
+                ra[i] = __builtin_bit_cast(i32x4_t,
+                                           *reinterpret_cast<const u32x4_a1_t *>(ap[i] + k));
+                rb[i] = __builtin_bit_cast(i32x4_t,
+                                           *reinterpret_cast<const u32x4_a1_t *>(bp[i] + k));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                ra[i] = load_k16(ap[i], k + lc, g.K);
-                rb[i] = load_k16(bp[i], k + lc, g.K);
+                ra[i] = load_k16(ap[i] + k, g.K - k - lc);
+                rb[i] = load_k16(bp[i] + k, g.K - k - lc);
             }
         }
     };
-    i32x4_t acc[TM][TM];
+    i32x4_t acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
+        for (int j = 0; j < TN; ++j)
             acc[i][j] = i32x4_t{0, 0, 0, 0};
     if (kb < ke)
         fetch(kb);
@@ -124,26 +115,28 @@ __global__ void __launch_bounds__(GTHREADS, 2) gemm_i8_general_kernel(I8GemmArgs
         unsigned char *const As = lds[at][0], *const Bs = lds[at][1];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            *reinterpret_cast<i32x4_t *>(As + (lr + 32 * i) * GPITCH + lc) = ra[i];
-            *reinterpret_cast<i32x4_t *>(Bs + (lr + 32 * i) * GPITCH + lc) = rb[i];
+            *reinterpret_cast<i32x4_t *>(As + (lr + ROWS * i) * GPITCH + lc) = ra[i];
+            *reinterpret_cast<i32x4_t *>(Bs + (lr + ROWS * i) * GPITCH + lc) = rb[i];
         }
         __syncthreads();
         if (k + GK < ke)
             fetch(k + GK);
 #pragma unroll
         for (int h = 0; h < GK / 64; ++h) {
-            i32x4_t fa[TM], fb[TM];
+            i32x4_t fa[TM], fb[TN];
             const int c = h * 64 + (lane >> 4) * 16;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int r = 16 * i + (lane & 15);
-                fa[i] = *reinterpret_cast<const i32x4_t *>(As + (wm + r) * GPITCH + c);
-                fb[i] = *reinterpret_cast<const i32x4_t *>(Bs + (wn + r) * GPITCH + c);
-            }
+            for (int i = 0; i < TM; ++i)
+                fa[i] = *reinterpret_cast<const i32x4_t *>(
+                    As + (wm + 16 * i + (lane & 15)) * GPITCH + c);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                fb[j] = *reinterpret_cast<const i32x4_t *>(
+                    Bs + (wn + 16 * j + (lane & 15)) * GPITCH + c);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TM; ++j)
+                for (int j = 0; j < TN; ++j)
                     acc[i][j] =
                         __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
         }
@@ -155,7 +148,7 @@ __global__ void __launch_bounds__(GTHREADS, 2) gemm_i8_general_kernel(I8GemmArgs
             continue;
         const float sx = g.xs[m];
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
+        for (int j = 0; j < TN; ++j) {
             const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
             const int c[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
             if (g.part == nullptr) {
@@ -217,10 +210,14 @@ constexpr int I8_NUM_TILES = sizeof(I8_TILES) / sizeof(I8_TILES[0]);
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The general kernel's tile: 64 x 64 where 128 x 128 ones are fewer than two a CU.
+// The general kernel's tile: 256 x 256 where there is one for every CU (its steps
+// have the products to cover their loads: 8192 tokens, 8190 -> 28672 2.8 ms, 128 x
+// 128 3.8), 64 x 64 where there is no 128 x 128 one for every CU.
 int64_t general_tile(int64_t M, int64_t N)
 {
-    return ceil_div(M, 128) * ceil_div(N, 128) < 512 ? 64 : 128;
+    if (ceil_div(M, 256) * ceil_div(N, 256) >= 256)
+        return 256;
+    return ceil_div(M, 128) * ceil_div(N, 128) < 256 ? 64 : 128;
 }
 
 }  // namespace
@@ -261,7 +258,7 @@ I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K)
         // least
         const int64_t b = general_tile(M, N), tiles = ceil_div(M, b) * ceil_div(N, b);
         const int64_t steps = ceil_div(K, GK);
-        int64_t z = tiles > 0 ? 512 / tiles : 1;
+        int64_t z = b < 256 && tiles > 0 ? 512 / tiles : 1;
         z = z < steps / 4 ? z : steps / 4;
         z = z < 1 ? 1 : (z > 32 ? 32 : z);
         const int64_t per = ceil_div(steps, z);
@@ -289,14 +286,19 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
         if (tiles > 0x7fffffff)
             return hipErrorInvalidConfiguration;
         const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
-        if (bf16 && b == 64)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<64, uint16_t>), grid, dim3(GTHREADS), 0, st, g);
+        const dim3 block(b == 256 ? 512 : 256);
+        if (b == 256 && bf16)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, uint16_t>), grid, block, 0, st, g);
+        else if (b == 256)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, float>), grid, block, 0, st, g);
+        else if (b == 128 && bf16)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, uint16_t>), grid, block, 0, st, g);
+        else if (b == 128)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, float>), grid, block, 0, st, g);
         else if (bf16)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<128, uint16_t>), grid, dim3(GTHREADS), 0, st, g);
-        else if (b == 64)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<64, float>), grid, dim3(GTHREADS), 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, uint16_t>), grid, block, 0, st, g);
         else
-            hipLaunchKernelGGL((gemm_i8_general_kernel<128, float>), grid, dim3(GTHREADS), 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, float>), grid, block, 0, st, g);
         e = hipGetLastError();
     }
     if (e != hipSuccess || p.splits == 1)
