@@ -47,47 +47,41 @@ struct OpRegs {
     static constexpr int PER = KMAJ ? (R * 8) / NT : ((R + NT - 1) / NT) * 8;
 };
 
-// Eight consecutive bf16 values from element `at` of the matrix at `p`, those at
-// or past `live` (their row's end) read as zero, for rows of a ragged width,
-// which start at any element: one 16-byte load at whatever element.  Where the
-// row ends inside the eight: SHIFT, the load ends with the row instead and is
-// shifted into place (what it also reads lies before, in the same matrix; for
-// MN-major operands, which end a row in every step), only a first row narrower
-// than eight going element by element; else element by element (K-major
-// operands, which do so in their last step: 23 against 39 us on a 1411 x 37
-// product of width 1027).
+// Eight consecutive bf16 values p[0 .. 8) with those at or past `live` (their
+// row's end) read as zero, for rows of a ragged width, which start at any
+// element: one 16-byte load at whatever element, or, where the row ends inside
+// the eight, element by element.
 typedef unsigned int u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
-template <bool SHIFT>
-__device__ __forceinline__ uint4 load8_masked(const uint16_t *__restrict__ p, int64_t at,
-                                              int64_t live)
+__device__ __forceinline__ uint4 load8_any(const uint16_t *__restrict__ p)
 {
-    const int cut = live < 8 ? 8 - static_cast<int>(live) : 0;
-    if (SHIFT ? at >= cut : cut == 0) {
-        // (SHIFT: one load for whole and cut chunks alike)
-        const u32x4_any_t v =
-            *reinterpret_cast<const u32x4_any_t *>(p + (SHIFT ? at - cut : at));
-        if (!SHIFT || cut == 0)
-            return make_uint4(v.x, v.y, v.z, v.w);
-        uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32;
-        uint64_t hi = v.z | static_cast<uint64_t>(v.w) << 32;
-        if (cut >= 4) {
-            lo = hi >> (16 * (cut - 4));
-            hi = 0;
-        } else {
-            lo = lo >> (16 * cut) | hi << (64 - 16 * cut);
-            hi >>= 16 * cut;
-        }
-        return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                          static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
-    }
+    const u32x4_any_t v = *reinterpret_cast<const u32x4_any_t *>(p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint4 load8_masked(const uint16_t *__restrict__ p, int64_t live)
+{
+    if (live >= 8)
+        return load8_any(p);
     uint32_t w[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = 2 * q < live ? p[at + 2 * q] : 0u;
-        const uint32_t hi = 2 * q + 1 < live ? p[at + 2 * q + 1] : 0u;
+        const uint32_t lo = 2 * q < live ? p[2 * q] : 0u;
+        const uint32_t hi = 2 * q + 1 < live ? p[2 * q + 1] : 0u;
         w[q] = lo | (hi << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A ragged MN-major operand ends its rows inside a chunk.  That chunk is taken
+// from the row's last eight values instead (rows of at least eight): the first
+// column, from the tile's, of the eight that chunk mb holds.  Those columns are
+// written to LDS twice, with the same values; columns past the row's end keep
+// the zeros they start with.  (Loading the rest of a row element by element
+// instead holds up every load behind it: dA, 37 x 1027 over 509 tokens and 1411
+// rows of W, 93 us so, 34 this way; dx at 4096 x 8191 x 4097 1.17 ms and 0.87.)
+__device__ __forceinline__ int mn_first(int64_t MN, int64_t mn0, int mb)
+{
+    const int64_t c = mn0 + mb * 8;
+    return static_cast<int>((MN >= 8 && c + 8 > MN ? MN - 8 : c) - mn0);
 }
 
 // RG (ragged): any K, M, N and leading dimension; rows start at any element
@@ -106,7 +100,7 @@ __device__ __forceinline__ void load_operand(uint4 (&v)[NV], const uint16_t *__r
             const int idx = tid + i * NT;
             const int row = idx >> 3, c = idx & 7;
             const int64_t mn = mn0 + row, k = k0 + c * 8;
-            v[i] = mn < MN && k < K ? load8_masked<false>(p, mn * ld + k, K - k)
+            v[i] = mn < MN && k < K ? load8_masked(p + mn * ld + k, K - k)
                                     : make_uint4(0, 0, 0, 0);
         }
     } else if constexpr (RG) {
@@ -114,12 +108,18 @@ __device__ __forceinline__ void load_operand(uint4 (&v)[NV], const uint16_t *__r
         for (int b = 0; b < OpRegs<KMAJ, R, NT>::PER / 8; ++b) {
             const int idx = tid + b * NT;
             const int kb = idx / (R / 8), mb = idx % (R / 8);
-            const int64_t mn = mn0 + mb * 8;
+            const int64_t mn = mn0 + mb * 8, kk = k0 + kb * 8;
+            const int64_t rows = idx < R && mn < MN ? K - kk : 0;  // K values there
+            if (MN >= 8) {
+                const uint16_t *q = p + kk * ld + mn0 + mn_first(MN, mn0, mb);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t k = k0 + kb * 8 + j;
-                v[b * 8 + j] = idx < R && mn < MN && k < K ? load8_masked<true>(p, k * ld + mn, MN - mn)
-                                                           : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < 8; ++j, q += ld)
+                    v[b * 8 + j] = j < rows ? load8_any(q) : make_uint4(0, 0, 0, 0);
+            } else {
+                const uint16_t *q = p + kk * ld + mn;
+#pragma unroll
+                for (int j = 0; j < 8; ++j, q += ld)
+                    v[b * 8 + j] = j < rows ? load8_masked(q, MN - mn) : make_uint4(0, 0, 0, 0);
             }
         }
     } else if constexpr (KMAJ) {
@@ -168,9 +168,11 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int w)
     return w == 0 ? v.x : (w == 1 ? v.y : (w == 2 ? v.z : v.w));
 }
 
-// Write one operand tile into LDS as R rows of eight swizzled 16-byte chunks.
-template <bool KMAJ, int R, int NT, int NV>
-__device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4 (&v)[NV], int tid)
+// Write one operand tile into LDS as R rows of eight swizzled 16-byte chunks
+// (MN, mn0: of a ragged MN-major operand).
+template <bool KMAJ, int R, int NT, bool RG, int NV>
+__device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4 (&v)[NV], int64_t MN,
+                                              int64_t mn0, int tid)
 {
     static_assert(NV == OpRegs<KMAJ, R, NT>::PER, "register count");
     if constexpr (KMAJ) {
@@ -187,8 +189,11 @@ __device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4
             if (idx >= R)
                 continue;
             const int kb = idx / (R / 8), mb = idx % (R / 8);
+            if (RG && mn0 + mb * 8 >= MN)
+                continue;
+            const int first = RG ? mn_first(MN, mn0, mb) : mb * 8;
             // v[b*8 + j] holds k = kb*8 + j, mn = mb*8 .. mb*8+7 (two per word).
-            // Output q holds mn = mb*8 + q, k = kb*8 .. kb*8+7.
+            // Output q holds mn = mb*8 + q, k = kb*8 .. kb*8+7 (RG: first + q).
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const int w = q >> 1;
@@ -204,8 +209,14 @@ __device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4
                     o.z = hi_halves(word(v[b * 8 + 4], w), word(v[b * 8 + 5], w));
                     o.w = hi_halves(word(v[b * 8 + 6], w), word(v[b * 8 + 7], w));
                 }
-                const int row = mb * 8 + q;
-                S[row * 8 + (kb ^ (row & 7))] = o;
+                // (rows of whole chunks at constant distances)
+                if (!RG || first == mb * 8) {
+                    const int row = mb * 8 + q;
+                    S[row * 8 + (kb ^ (row & 7))] = o;
+                } else if (first + q >= 0) {
+                    const int row = first + q;
+                    S[row * 8 + (kb ^ (row & 7))] = o;
+                }
             }
         }
     }
@@ -288,8 +299,8 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
                 }
             }
         }
-        store_operand<AK, BM, NT>(As + buf * BM * 8, ra, tid);
-        store_operand<BKM, BN, NT>(Bs + buf * BN * 8, rb, tid);
+        store_operand<AK, BM, NT, RG>(As + buf * BM * 8, ra, g.M, m0, tid);
+        store_operand<BKM, BN, NT, RG>(Bs + buf * BN * 8, rb, g.N, n0, tid);
     };
     auto compute = [&](int buf) {
         const uint4 *Ab = As + buf * BM * 8;
@@ -317,6 +328,12 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
         }
     };
 
+    if constexpr (RG && (!AK || !BKM)) {
+        // columns past a ragged row's end are never written
+        for (int i = tid; i < 2 * (BM + BN) * 8; i += NT)
+            As[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     if (s_begin < s_end) {
         load_step(s_begin);
         store_step(0);
