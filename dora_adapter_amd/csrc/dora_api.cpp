@@ -111,8 +111,8 @@ bool dma_mn_operand(int64_t K, int64_t ld)
 
 // Whether a bf16 product has an operand of ragged width: a K-major operand
 // ([rows][K], ld = K) whose K is not a multiple of 8, or an MN-major one
-// ([K][M or N], ld = M or N) whose M or N is not.  Only the element-masked
-// configuration takes those.
+// ([K][M or N], ld = M or N) whose M or N is not.  Only the
+// configuration for rows of any width takes those.
 bool shape_ragged(const GemmShape &sh)
 {
     const bool ak = sh.layout < 2, bk = sh.layout == 0;
@@ -141,13 +141,15 @@ int forced_tile_cfg()
 }
 
 // Choose the tile configuration and the split-K count by a small time
-// model: (256-CU waves) x (one workgroup's MFMA or VALU time), plus, for a
+// model: (256-CU waves) x (one workgroup's MFMA time), plus, for a
 // split, writing and re-reading `part_per_split` fp32 values per split and
 // one extra launch.  A split keeps at least 512 K values (128 for row-dot
 // products, whose partials are one value per row and tile column) and its
 // partials under 1 GiB.
 GPlan plan_gemm(bool bf16, const GemmShape &sh, int64_t part_per_split, int only = -1)
 {
+    // (fp32: the rate the plans were made with on the vector ALUs; the split
+    // counts, and so the order of fp32 sums, follow from it)
     const double cu_flops = bf16 ? 4.0e12 : 157.3e12 / kCUs * 0.5;
     const double hbm = 5.0e12;
     GPlan best;

@@ -162,14 +162,14 @@ struct TileCfg {
     bool store_ok;    // EPI_STORE supported (else EPI_ROWDOT only)
     bool rowsq_ok;    // row sums of squares of A supported
     bool direct_rowdot;  // EPI_ROWDOT formed from the accumulators (no LDS staging)
-    bool ragged_ok;      // also takes operands of any width (element-masked loads)
+    bool ragged_ok;      // also takes operands of any width (rows at any element)
     bool dhdm_ok;        // has the dh/dm-producing variant (launch_gemm_bf16_dhdm)
 };
 int gemm_bf16_num_cfgs();
 TileCfg gemm_bf16_cfg(int cfg);
 constexpr int GEMM_BK = 64;      // bf16 K step of the general kernel
 constexpr int GEMM_DMA_BK = 64;  // bf16 K stage of the direct-to-LDS kernel
-constexpr int GEMM_F32_BM = 64;  // fp32 VALU tile
+constexpr int GEMM_F32_BM = 64;  // fp32 tile
 constexpr int GEMM_F32_BN = 64;
 constexpr int GEMM_F32_BK = 16;
 

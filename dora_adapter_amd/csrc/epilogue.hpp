@@ -1,4 +1,4 @@
-// epilogue.hpp - GEMM epilogues shared by the bf16 MFMA and fp32 VALU GEMMs.
+// epilogue.hpp - GEMM epilogues shared by the bf16 and fp32 MFMA GEMMs.
 //
 // After the K loop a workgroup stages R rows of its fp32 accumulator tile in
 // LDS (Cs, row stride CST floats) and calls epilogue_rows, which either

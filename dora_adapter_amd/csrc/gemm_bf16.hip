@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
 // rate they reach as one wave of tiles on the rank-r products (x A^T,
 // dh^T P, Q^T x at the training shape).
 // The 128 x 128 register-staged configuration also exists with
-// element-masked loads (ragged_ok), for operands of any width.
+// loads at any element (ragged_ok), for operands of any width.
 constexpr TileCfg kCfgs[] = {
     {256, 256, GEMM_BK, false, 0.76f, true, true, false, false, false},
     {256, 128, GEMM_BK, false, 0.68f, true, true, false, false, false},
@@ -452,7 +452,7 @@ hipError_t launch_cfg(const GemmArgs &a, int layout, bool rowsq, hipStream_t st)
     }
 }
 
-// Whether a product needs the element-masked loads: a leading dimension or
+// Whether a product needs the loads at any element: a leading dimension or
 // base address that leaves rows unaligned to 16 bytes, a K-major operand
 // whose K is not a multiple of 8, or an MN-major one whose M (or N) is not.
 bool ragged_args(const GemmArgs &a, int layout)
@@ -489,7 +489,7 @@ hipError_t launch_gemm_bf16(const GemmArgs &a, int layout, int cfg, bool rowsq, 
         (rowsq && !kCfgs[cfg].rowsq_ok))
         return hipErrorInvalidValue;
     if (ragged_args(a, layout)) {
-        // only the element-masked configuration takes unaligned operands
+        // only the any-width configuration takes unaligned operands
         if (!kCfgs[cfg].ragged_ok)
             return hipErrorInvalidValue;
         return launch_cfg<128, 128, true>(a, layout, rowsq, st);

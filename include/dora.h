@@ -22,7 +22,8 @@
  * Conventions shared by every call:
  *   - Every matrix is dense, row-major and contiguous.  Matrix data (x, W,
  *     A, B, dy, y, P, base, lora, dx, dA, dB) has one element type given by
- *     the dora_dtype argument.  m, n, dm and the optional norm terms are
+ *     the dora_dtype argument (the 8-bit rows further down: int8 with fp32
+ *     scales).  m, n, dm and the optional norm terms are
  *     always fp32.  s is an fp32 scalar passed by value.
  *   - Every pointer is device memory owned by the caller (e.g. torch
  *     tensors).  The library never allocates device memory and keeps no
@@ -37,7 +38,7 @@
  *   - Every pointer must be 16-byte aligned.  Sizes need not be multiples
  *     of anything: T >= 0, and d_in, d_out, r >= 1 (all < 2^31).  Tails are
  *     masked in the kernels; a bf16 width that leaves rows unaligned to 16
- *     bytes (not a multiple of 8) runs on element-masked loads, slower than
+ *     bytes (not a multiple of 8) runs on register-staged tiles, slower than
  *     the pipelined path but with the same arithmetic.
  *   - Results are bitwise deterministic for identical inputs: there are no
  *     floating-point atomics and every reduction runs in a fixed order.
