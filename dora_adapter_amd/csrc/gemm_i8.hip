@@ -14,6 +14,7 @@
 // a step in two LDS buffers; the next step's loads are in flight during this
 // one's products.
 #include "dora_internal.hpp"
+#include "gemm_bf16_dma.hpp"
 #include "rows8.hpp"
 
 namespace dora {
@@ -25,11 +26,29 @@ constexpr int GK = 128;          // bytes of K a step
 constexpr int GPITCH = GK + 16;  // LDS row: 8 rows of a 16-byte read phase on distinct banks
 constexpr int GTHREADS = 256;
 
-// 16 bytes at p, those at or past `left` (their row's end) read as zero.
-__device__ __forceinline__ i32x4_t load_k16(const int8_t *p, int64_t left)
+// What is left of 16 bytes that were loaded `back` bytes early and of which
+// `left` belong to the row (the rest zeros): the row's last chunk.
+__device__ __forceinline__ i32x4_t row_end16(i32x4_t v, int back, int64_t left)
 {
-    if (left >= 16)
-        return __builtin_bit_cast(i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(p));
+    uint64_t lo = static_cast<uint32_t>(v[0]) | static_cast<uint64_t>(static_cast<uint32_t>(v[1])) << 32;
+    uint64_t hi = static_cast<uint32_t>(v[2]) | static_cast<uint64_t>(static_cast<uint32_t>(v[3])) << 32;
+    if (back >= 8) {
+        lo = hi >> (8 * (back - 8));
+        hi = 0;
+    } else if (back > 0) {
+        lo = lo >> (8 * back) | hi << (64 - 8 * back);
+        hi >>= 8 * back;
+    }
+    const int n = left < 0 ? 0 : (left < 16 ? static_cast<int>(left) : 16);
+    lo = n >= 8 ? lo : lo & ((1ull << (8 * n)) - 1);
+    hi = n >= 16 ? hi : (n > 8 ? hi & ((1ull << (8 * (n - 8))) - 1) : 0);
+    return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi),
+                   static_cast<int>(hi >> 32)};
+}
+
+// The first `left` bytes at p, one by one (operands of fewer than 16 bytes).
+__device__ __forceinline__ i32x4_t load_bytes(const int8_t *p, int64_t left)
+{
     unsigned int w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int b = 0; b < 15; ++b)
@@ -56,8 +75,9 @@ __device__ __forceinline__ void store_scaled(const I8GemmArgs &g, int64_t m, int
         }
 }
 
-// B x B tiles of 2 x WN waves (B / 2 rows x B / WN columns each).
-template <int B, int WN, typename T>
+// B x B tiles of 2 x WN waves (B / 2 rows x B / WN columns each); AHEAD: steps
+// whose loads are in flight in registers; TINY: an operand of fewer than 16 bytes.
+template <int B, int WN, int AHEAD, bool TINY, typename T>
 __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs g)
 {
     constexpr int NT = 128 * WN, ROWS = NT / 8;  // threads; rows they load at a time
@@ -72,32 +92,53 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
     const int64_t ke = kb + g.k_per_split < g.K ? kb + g.k_per_split : g.K;
 
     // thread: chunk tid & 7 of rows (tid >> 3) + ROWS i of either operand (rows
-    // past the end: the last one, never stored)
+    // past the end: the last one, never stored), as offsets of their first byte
     const int lr = tid >> 3, lc = (tid & 7) * 16;
-    const int8_t *ap[PER], *bp[PER];
+    int64_t ao[PER], bo[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int64_t m = m0 + lr + ROWS * i, n = n0 + lr + ROWS * i;
-        ap[i] = g.x + (m < g.M ? m : g.M - 1) * g.K + lc;
-        bp[i] = g.w + (n < g.N ? n : g.N - 1) * g.K + lc;
+        ao[i] = (m < g.M ? m : g.M - 1) * g.K + lc;
+        bo[i] = (n < g.N ? n : g.N - 1) * g.K + lc;
     }
-    i32x4_t ra[PER], rb[PER];
-    // (whole steps without a branch a load)
-    auto fetch = [&](int64_t k) {
-        if (k + GK <= g.K) {
+    struct Regs {
+        i32x4_t a[PER], b[PER];
+    } regs[AHEAD];
+    // The loads of K values k .. k + GK - 1: whole chunks, without a branch or a
+    // wait among them.  Where the row ends they run into the next one, and at the
+    // operand's end they start early; the last step's are put right when they
+    // go to LDS (row_end16).
+    const int64_t alim = g.M * g.K - 16, blim = g.N * g.K - 16;
+    auto load16 = [](const int8_t *p) {
+        return __builtin_bit_cast(i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(p));
+    };
+    auto fetch = [&](Regs &r, int64_t k) {
+        if constexpr (TINY) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                ra[i] = __builtin_bit_cast(i32x4_t,
-                                           *reinterpret_cast<const u32x4_a1_t *>(ap[i] + k));
-                rb[i] = __builtin_bit_cast(i32x4_t,
-                                           *reinterpret_cast<const u32x4_a1_t *>(bp[i] + k));
+                r.a[i] = load_bytes(g.x + ao[i] + k, g.K - k - lc);
+                r.b[i] = load_bytes(g.w + bo[i] + k, g.K - k - lc);
+            }
+        } else if (k + GK <= g.K) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                r.a[i] = load16(g.x + ao[i] + k);
+                r.b[i] = load16(g.w + bo[i] + k);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                ra[i] = load_k16(ap[i] + k, g.K - k - lc);
-                rb[i] = load_k16(bp[i] + k, g.K - k - lc);
+                r.a[i] = load16(g.x + (ao[i] + k < alim ? ao[i] + k : alim));
+                r.b[i] = load16(g.w + (bo[i] + k < blim ? bo[i] + k : blim));
             }
+        }
+    };
+    auto row_ends = [&](Regs &r, int64_t k) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t ab = ao[i] + k - alim, bb = bo[i] + k - blim, left = g.K - k - lc;
+            r.a[i] = row_end16(r.a[i], ab > 0 && left > 0 ? static_cast<int>(ab) : 0, left);
+            r.b[i] = row_end16(r.b[i], bb > 0 && left > 0 ? static_cast<int>(bb) : 0, left);
         }
     };
     i32x4_t acc[TM][TN];
@@ -106,21 +147,27 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             acc[i][j] = i32x4_t{0, 0, 0, 0};
-    if (kb < ke)
-        fetch(kb);
     int at = 0;
-    // one barrier a step: a wave past it is done with the other buffer's
-    // fragments, which the next step overwrites
-    for (int64_t k = kb; k < ke; k += GK, at ^= 1) {
+    const int64_t steps = kb < ke ? (ke - kb + GK - 1) / GK : 0;
+    auto k_of = [&](int64_t s) { return kb + (s < steps ? s : steps - 1) * GK; };
+    // step s from the registers r, which then take step s + AHEAD (past the end
+    // the last one again: the loads in flight are always the same number, which
+    // the waits before their use count on).  One barrier a step: a wave past it
+    // is done with the other buffer's fragments, which the next step overwrites.
+    auto step = [&](Regs &r, int64_t s) {
+        if (!TINY && k_of(s) + GK > g.K)
+            row_ends(r, k_of(s));
         unsigned char *const As = lds[at][0], *const Bs = lds[at][1];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            *reinterpret_cast<i32x4_t *>(As + (lr + ROWS * i) * GPITCH + lc) = ra[i];
-            *reinterpret_cast<i32x4_t *>(Bs + (lr + ROWS * i) * GPITCH + lc) = rb[i];
+            *reinterpret_cast<i32x4_t *>(As + (lr + ROWS * i) * GPITCH + lc) = r.a[i];
+            *reinterpret_cast<i32x4_t *>(Bs + (lr + ROWS * i) * GPITCH + lc) = r.b[i];
         }
-        __syncthreads();
-        if (k + GK < ke)
-            fetch(k + GK);
+        // (a bare barrier behind this wave's LDS writes: __syncthreads would wait
+        // for the loads in flight as well)
+        dma::wait_lgkm0();
+        dma::stage_barrier();
+        fetch(r, k_of(s + AHEAD));
 #pragma unroll
         for (int h = 0; h < GK / 64; ++h) {
             i32x4_t fa[TM], fb[TN];
@@ -140,6 +187,22 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
                     acc[i][j] =
                         __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
         }
+        at ^= 1;
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+            fetch(regs[p], k_of(p));
+        int64_t s = 0;
+        for (; s + AHEAD <= steps; s += AHEAD) {
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p)
+                step(regs[p], s + p);
+        }
+#pragma unroll
+        for (int p = 0; p < AHEAD - 1; ++p)
+            if (s + p < steps)
+                step(regs[p], s + p);
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -211,10 +274,12 @@ constexpr int I8_NUM_TILES = sizeof(I8_TILES) / sizeof(I8_TILES[0]);
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The general kernel's tile: 256 x 256 where there is one for every CU (its steps
-// have the products to cover their loads: 8192 tokens, 8190 -> 28672 2.8 ms, 128 x
+// have the products to cover their loads: 8192 tokens, 8190 -> 28672 2.9 ms, 128 x
 // 128 3.8), 64 x 64 where there is no 128 x 128 one for every CU.
-int64_t general_tile(int64_t M, int64_t N)
+int64_t general_tile(int64_t M, int64_t N, int64_t K)
 {
+    if (M * K < 16 || N * K < 16)
+        return 64;
     if (ceil_div(M, 256) * ceil_div(N, 256) >= 256)
         return 256;
     return ceil_div(M, 128) * ceil_div(N, 128) < 256 ? 64 : 128;
@@ -256,7 +321,7 @@ I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K)
     } else {
         // split K until two workgroups a CU are reached, four steps a split at
         // least
-        const int64_t b = general_tile(M, N), tiles = ceil_div(M, b) * ceil_div(N, b);
+        const int64_t b = general_tile(M, N, K), tiles = ceil_div(M, b) * ceil_div(N, b);
         const int64_t steps = ceil_div(K, GK);
         int64_t z = b < 256 && tiles > 0 ? 512 / tiles : 1;
         z = z < steps / 4 ? z : steps / 4;
@@ -282,23 +347,30 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
     } else if (p.cfg != I8Plan::GENERAL) {
         e = launch_gemm_i8_dma(bf16, g, p.cfg, st);
     } else {
-        const int64_t b = general_tile(g.M, g.N), tiles = ceil_div(g.M, b) * ceil_div(g.N, b);
+        const int64_t b = general_tile(g.M, g.N, g.K), tiles = ceil_div(g.M, b) * ceil_div(g.N, b);
         if (tiles > 0x7fffffff)
             return hipErrorInvalidConfiguration;
         const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
         const dim3 block(b == 256 ? 512 : 256);
-        if (b == 256 && bf16)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, uint16_t>), grid, block, 0, st, g);
+        if (b == 64 && (g.M * g.K < 16 || g.N * g.K < 16)) {
+            if (bf16)
+                hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, 1, true, uint16_t>), grid, block, 0,
+                                   st, g);
+            else
+                hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, 1, true, float>), grid, block, 0, st,
+                                   g);
+        } else if (b == 256 && bf16)
+            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, 1, false, uint16_t>), grid, block, 0, st, g);
         else if (b == 256)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, float>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<256, 4, 1, false, float>), grid, block, 0, st, g);
         else if (b == 128 && bf16)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, uint16_t>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, 2, false, uint16_t>), grid, block, 0, st, g);
         else if (b == 128)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, float>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<128, 2, 2, false, float>), grid, block, 0, st, g);
         else if (bf16)
-            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, uint16_t>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, 3, false, uint16_t>), grid, block, 0, st, g);
         else
-            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, float>), grid, block, 0, st, g);
+            hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, 3, false, float>), grid, block, 0, st, g);
         e = hipGetLastError();
     }
     if (e != hipSuccess || p.splits == 1)
