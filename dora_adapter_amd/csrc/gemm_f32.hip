@@ -13,15 +13,16 @@
 //
 // 64 x 64 tiles of four waves (32 x 32 each), K in granules of 16 (the unit of
 // the splits; each segment's last one is filled with zeros), two granules a
-// step, double-buffered in LDS with the next step's loads in flight.  A
+// step, double-buffered in LDS, the next two steps' loads in flight.  A
 // K-major operand lies in LDS as rows of K with the even K values of every
 // eight before the odd ones, so that one 16-byte read gives a lane (the lower
 // 32 lanes hold even K, the upper odd) its operand of four MFMAs; an MN-major
 // one lies as it comes, [K][64], read four bytes at a time.  x W^T at 4096 x 4096 x
-// 4096: 1.66 ms (83 TFLOP/s), against 2.34 on the vector ALUs; 1024 x 2048 x 4096:
-// 0.25 against 0.40; 512 x 8192 x 384: 0.10 against 0.23.
+// 4096: 1.48 ms (93 TFLOP/s), against 2.34 on the vector ALUs; 1024 x 2048 x 4096:
+// 0.22 against 0.40; 512 x 8192 x 384: 0.08 against 0.23.
 #include "dora_internal.hpp"
 #include "epilogue.hpp"
+#include "gemm_bf16_dma.hpp"
 
 namespace dora {
 namespace {
@@ -29,6 +30,7 @@ namespace {
 constexpr int BM = GEMM_F32_BM, BN = GEMM_F32_BN, BK = GEMM_F32_BK, NT = 256;
 static_assert(BM == 64 && BN == 64 && BK == 16, "thread and wave layout");
 constexpr int STEP = 2;                  // granules a step
+constexpr int AHEAD = 2;                 // steps whose loads are in flight
 constexpr int KPITCH = STEP * BK + 4;    // floats of a K-major LDS row
 constexpr int MPITCH = 64 + 4;           // floats of an MN-major LDS row
 
@@ -51,6 +53,17 @@ __device__ __forceinline__ float4 load4(const float *__restrict__ p, int64_t ld,
         return make_float4(v.x, v.y, v.z, v.w);
     }
     return make_float4(left > 0 ? q[0] : 0.f, left > 1 ? q[1] : 0.f, left > 2 ? q[2] : 0.f, 0.f);
+}
+
+// The same for a granule that lies wholly inside the operand: no branch.
+template <bool KMAJ>
+__device__ __forceinline__ float4 load4_whole(const float *__restrict__ p, int64_t ld, int64_t mn0,
+                                              int64_t k0, int tid)
+{
+    const float *q = KMAJ ? p + (mn0 + (tid >> 2)) * ld + k0 + (tid & 3) * 4
+                          : p + (k0 + (tid >> 4)) * ld + mn0 + (tid & 15) * 4;
+    const f32x4_a4_t v = *reinterpret_cast<const f32x4_a4_t *>(q);
+    return make_float4(v.x, v.y, v.z, v.w);
 }
 
 // Where K value k (of a step) of a K-major row lies: evens, then odds of every 8.
@@ -114,35 +127,43 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
         acc[i] = 0.f;
     float sq = 0.f;
 
-    float4 ra[STEP], rb[STEP];
-    auto fetch = [&](int64_t s) {
+    struct Regs {
+        float4 a[STEP], b[STEP];
+    } regs[AHEAD];
+    const bool inside = m0 + BM <= g.M && n0 + BN <= g.N;
+    // the loads of step s (granules past the split's end: its last one again, so
+    // that every step has the same number of loads in flight)
+    auto fetch = [&](Regs &r, int64_t s) {
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
-            if (s + j >= s_end)
-                break;
-            const bool first = s + j < st1;
+            const int64_t gr = s + j < s_end ? s + j : s_end - 1;
+            const bool first = gr < st1;
             const GemmSeg &sg = first ? g.seg[0] : g.seg[1];
-            const int64_t k0 = (first ? s + j : s + j - st1) * BK;
-            ra[j] = load4<AK>(static_cast<const float *>(sg.a), sg.lda, g.M, sg.K, m0, k0, tid);
-            rb[j] = load4<BKM>(static_cast<const float *>(sg.b), sg.ldb, g.N, sg.K, n0, k0, tid);
+            const int64_t k0 = (first ? gr : gr - st1) * BK;
+            const float *pa = static_cast<const float *>(sg.a);
+            const float *pb = static_cast<const float *>(sg.b);
+            if (inside && k0 + BK <= sg.K) {
+                r.a[j] = load4_whole<AK>(pa, sg.lda, m0, k0, tid);
+                r.b[j] = load4_whole<BKM>(pb, sg.ldb, n0, k0, tid);
+            } else {
+                r.a[j] = load4<AK>(pa, sg.lda, g.M, sg.K, m0, k0, tid);
+                r.b[j] = load4<BKM>(pb, sg.ldb, g.N, sg.K, n0, k0, tid);
+            }
         }
     };
-    if (s_begin < s_end)
-        fetch(s_begin);
     int at = 0;
-    // one barrier a step: a wave past it is done with the other buffer
-    for (int64_t s = s_begin; s < s_end; s += STEP, at ^= 1) {
+    // One barrier a step (a wave past it is done with the other buffer), bare:
+    // __syncthreads would wait for the loads in flight as well.
+    auto step = [&](Regs &r, int64_t s) {
         float *const As = lds + at * (AF + BF), *const Bs = As + AF;
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
-            if (s + j >= s_end)
-                break;
-            store4<AK>(As, ra[j], j, tid);
-            store4<BKM>(Bs, rb[j], j, tid);
+            store4<AK>(As, r.a[j], j, tid);
+            store4<BKM>(Bs, r.b[j], j, tid);
         }
-        __syncthreads();
-        if (s + STEP < s_end)
-            fetch(s + STEP);
+        dma::wait_lgkm0();
+        dma::stage_barrier();
+        fetch(r, s + AHEAD * STEP);
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
             if (s + j >= s_end)
@@ -164,6 +185,18 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
                     }
                 }
             }
+        }
+        at ^= 1;
+    };
+    if (s_begin < s_end) {
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+            fetch(regs[p], s_begin + p * STEP);
+        for (int64_t s = s_begin; s < s_end; s += AHEAD * STEP) {
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p)
+                if (s + p * STEP < s_end)
+                    step(regs[p], s + p * STEP);
         }
     }
 
