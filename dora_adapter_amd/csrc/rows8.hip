@@ -581,27 +581,28 @@ __global__ void __launch_bounds__(ROW_THREADS) dequantize_kernel(const int8_t *q
     const int shift = group ? 31 - __clz(group) : 63;
     constexpr int SHARE = ROW_THREADS * VPT * 8;
     for (int64_t c = blockIdx.y * static_cast<int64_t>(SHARE); c < d;
-         c += gridDim.y * static_cast<int64_t>(SHARE))
-    for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
-        const int64_t j0 = c + threadIdx.x * 8;
-        Raw8i r[VPT];
-        float s[VPT];
+         c += gridDim.y * static_cast<int64_t>(SHARE)) {
+        for (int64_t t = blockIdx.x; t < rows; t += gridDim.x) {
+            const int64_t j0 = c + threadIdx.x * 8;
+            Raw8i r[VPT];
+            float s[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t j = j0 + i * (ROW_THREADS * 8);
-            r[i].load(q + t * d + j, count8(d, j));
-            s[i] = j < d ? scale[t * groups + (j >> shift)] : 0.f;
-        }
+            for (int i = 0; i < VPT; ++i) {
+                const int64_t j = j0 + i * (ROW_THREADS * 8);
+                r[i].load(q + t * d + j, count8(d, j));
+                s[i] = j < d ? scale[t * groups + (j >> shift)] : 0.f;
+            }
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int64_t j = j0 + i * (ROW_THREADS * 8);
-            float f[8];
+            for (int i = 0; i < VPT; ++i) {
+                const int64_t j = j0 + i * (ROW_THREADS * 8);
+                float f[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = r[i].value(k) * s[i];
-            Raw8<T> o;
-            o.set(f);
-            o.store(out + t * d + j, count8(d, j));
+                for (int k = 0; k < 8; ++k)
+                    f[k] = r[i].value(k) * s[i];
+                Raw8<T> o;
+                o.set(f);
+                o.store(out + t * d + j, count8(d, j));
+            }
         }
     }
 }
@@ -724,9 +725,7 @@ void quantize_launch(const T *x, int64_t rows, int64_t d, int group, int8_t *q, 
         hipLaunchKernelGGL((quantize_kernel<T>), dim3(row_groups(rows)), dim3(ROW_THREADS), 0, st, x,
                            rows, d, group, q, scale);
 }
-}  // namespace
 
-namespace {
 // Rows whose gradient is formed in one pass, held in a workgroup's registers.
 bool grad_held(int64_t d, bool wide) { return (d + 7) / 8 <= (wide ? 2048 : 4096); }
 }  // namespace
@@ -772,10 +771,9 @@ hipError_t launch_sum_parts(const float *part, int parts, int64_t d, const float
     return hipGetLastError();
 }
 
-
 namespace {
 template <typename T>
-void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
+hipError_t rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
 {
     constexpr bool WIDE = sizeof(T) == 4;
     const int64_t vecs = (a.d + 7) / 8;
@@ -797,8 +795,12 @@ void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
                                block.x * 4 * 32, st, a);
     } else {
         const dim3 block(ROW_THREADS);
-        if (a.T > 0)
+        if (a.T > 0) {
             hipLaunchKernelGGL((rmsnorm_dx_kernel<T>), dim3(row_groups(a.T)), block, 0, st, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess)
+                return e;
+        }
         // (T = 0: the partial sums are zeros)
         if (dw != nullptr)
             hipLaunchKernelGGL((rmsnorm_dw_kernel<T>),
@@ -806,18 +808,16 @@ void rmsnorm_grad_launch(NormGradArgs a, float *dw, hipStream_t st)
                                     parts),
                                block, 0, st, a);
     }
-    if (dw != nullptr && parts > 1)
-        launch_sum_parts(part, a.parts, a.d, nullptr, dw, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || dw == nullptr || parts == 1)
+        return e;
+    return launch_sum_parts(part, a.parts, a.d, nullptr, dw, st);
 }
 }  // namespace
 
 hipError_t launch_rmsnorm_grad(int bf16, const NormGradArgs &a, float *dw, hipStream_t st)
 {
-    if (bf16)
-        rmsnorm_grad_launch<uint16_t>(a, dw, st);
-    else
-        rmsnorm_grad_launch<float>(a, dw, st);
-    return hipGetLastError();
+    return bf16 ? rmsnorm_grad_launch<uint16_t>(a, dw, st) : rmsnorm_grad_launch<float>(a, dw, st);
 }
 
 hipError_t launch_quantize_rows(int bf16, const void *x, int64_t rows, int64_t d, int group,
