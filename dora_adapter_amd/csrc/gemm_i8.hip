@@ -67,7 +67,7 @@ __device__ __forceinline__ void store_scaled(const I8GemmArgs &g, int64_t m, int
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (n + e < g.N) {
-            const float v = static_cast<float>(c[e]) * (sx * g.ws[n + e]);
+            const float v = i8_scaled(c[e], sx, i8_ws(g.ws[n + e]));
             if constexpr (sizeof(T) == 2)
                 out[e] = f32_to_bf16(v);
             else
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
         const int64_t m = m0 + wm + 16 * i + (lane & 15);
         if (m >= g.M)
             continue;
-        const float sx = g.xs[m];
+        const float sx = i8_xs(g.xs[m]);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(GTHREADS) i8_finish_kernel(I8GemmArgs g, int s
         int c = 0;
         for (int z = 0; z < splits; ++z)
             c += g.part[static_cast<int64_t>(z) * MN + e];
-        const float v = static_cast<float>(c) * (g.xs[e / g.N] * g.ws[e % g.N]);
+        const float v = i8_scaled(c, i8_xs(g.xs[e / g.N]), i8_ws(g.ws[e % g.N]));
         if constexpr (sizeof(T) == 2)
             static_cast<T *>(g.y)[e] = f32_to_bf16(v);
         else
@@ -348,10 +348,10 @@ hipError_t launch_gemm_i8(int bf16, I8GemmArgs g, const I8Plan &p, void *ws, hip
         e = launch_gemm_i8_dma(bf16, g, p.cfg, st);
     } else {
         const int64_t b = general_tile(g.M, g.N, g.K), tiles = ceil_div(g.M, b) * ceil_div(g.N, b);
-        if (tiles > 0x7fffffff)
-            return hipErrorInvalidConfiguration;
         const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.splits));
         const dim3 block(b == 256 ? 512 : 256);
+        if (tiles >= (int64_t(1) << 32) / block.x)  // a launch holds fewer than 2^32 threads
+            return hipErrorInvalidConfiguration;
         if (b == 64 && (g.M * g.K < 16 || g.N * g.K < 16)) {
             if (bf16)
                 hipLaunchKernelGGL((gemm_i8_general_kernel<64, 2, 1, true, uint16_t>), grid, block, 0,

@@ -15,9 +15,10 @@
 //
 // The sums are exact in int32, so a product may be split over K into any
 // number of ranges without changing its bits.  Epilogue, per wave: sums times
-// (token scale times channel scale) in fp32, rounded once, through the wave's
+// token scale times channel scale in fp32, rounded once, through the wave's
 // own LDS rows into 16-byte stores of whole 128-byte lines.
 #include "gemm_dma_launch.hpp"
+#include "rows8.hpp"
 
 namespace dora {
 namespace dma {
@@ -248,12 +249,12 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
 #pragma unroll
             for (int b = 0; b < WTM; b += 64) {
                 const int64_t m = m0 + b + lane;
-                lsx[b + lane] = g.xs[m < g.M ? m : g.M - 1];
+                lsx[b + lane] = i8_xs(g.xs[m < g.M ? m : g.M - 1]);
             }
 #pragma unroll
             for (int b = 0; b < WTN; b += 64) {
                 const int64_t n = n0 + b + lane;
-                lsw[b + lane] = g.ws[n < g.N ? n : g.N - 1];
+                lsw[b + lane] = i8_ws(g.ws[n < g.N ? n : g.N - 1]);
             }
         } else if constexpr (OUT != OUT_PART) {
 #pragma unroll
@@ -266,11 +267,12 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                     swr[j] = make_float4(g.ws[n < last ? n : last], g.ws[n + 1 < last ? n + 1 : last],
                                          g.ws[n + 2 < last ? n + 2 : last],
                                          g.ws[n + 3 < last ? n + 3 : last]);
+                swr[j] = make_float4(i8_ws(swr[j].x), i8_ws(swr[j].y), i8_ws(swr[j].z), i8_ws(swr[j].w));
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int64_t m = m0 + 16 * i + (lane & 15);
-                sxr[i] = g.xs[m < g.M ? m : g.M - 1];
+                sxr[i] = i8_xs(g.xs[m < g.M ? m : g.M - 1]);
             }
         }
         auto scale_x = [&](int i) {
@@ -303,10 +305,8 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                         } else {
                             const float sx = scale_x(i);
                             const float4 sw = scale_w(j);
-                            const float4 v = make_float4(static_cast<float>(c[0]) * (sx * sw.x),
-                                                         static_cast<float>(c[1]) * (sx * sw.y),
-                                                         static_cast<float>(c[2]) * (sx * sw.z),
-                                                         static_cast<float>(c[3]) * (sx * sw.w));
+                            const float4 v = make_float4(i8_scaled(c[0], sx, sw.x), i8_scaled(c[1], sx, sw.y),
+                                                         i8_scaled(c[2], sx, sw.z), i8_scaled(c[3], sx, sw.w));
                             if constexpr (OUT == OUT_F32)
                                 *reinterpret_cast<float4 *>(
                                     stg + rr * SROW + chunk(rr, 4 * jj + q4)) = v;

@@ -311,4 +311,15 @@ __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *
     return s;
 }
 
+// y = c xs wscale for an int32 sum c, as (c i8_xs(xs)) i8_ws(wscale).  The scales'
+// own product would leave the range where c times it does not (1e-30 and 1e-12
+// in front of 1e7, or 1e30 and 1e9 in front of a sum of 0); with xs at 2^-24 and
+// wscale at 2^24 (exact) neither step does for 2^-102 <= xs, wscale < 2^104.
+__device__ __forceinline__ float i8_xs(float xs) { return xs * 0x1p-24f; }
+__device__ __forceinline__ float i8_ws(float ws) { return ws * 0x1p24f; }
+__device__ __forceinline__ float i8_scaled(int c, float xs, float ws)
+{
+    return static_cast<float>(c) * xs * ws;
+}
+
 }  // namespace dora

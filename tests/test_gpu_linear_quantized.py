@@ -1,8 +1,8 @@
 """GPU: the int8 linear layer against exact integer sums.
 
 The sums are exact, so y differs from the 64-bit value by the conversion of
-the sum (2^-24), the product of the scales (2^-24), their product (2^-24) and
-the output's rounding (half a step): all relative to y itself."""
+the sum (2^-24), its products with the two scales (2^-24 each) and the output's
+rounding (half a step): all relative to y itself."""
 import pytest
 import torch
 
@@ -67,6 +67,25 @@ def test_zero_and_nan_scales():
     assert (y[2] == 0).all() and torch.isnan(y[5]).all()
     keep = [0, 1, 3, 4, 6, 7, 8]
     assert (y[keep][:, 7] == 0).all() and torch.isfinite(y[keep]).all()
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(3, 512, 40), (40, 513, 37), (100, 512, 9000), (600, 1024, 1032)])
+def test_scales_far_apart(T, d_in, d_out):
+    # the scales' own product leaves fp32's range, the result does not
+    for fx, fw in ((1e-28, 1e-9), (1e-12, 1e-24), (1e24, 1e-30), (1e-28, 1e30)):
+        xq, xs, wq, ws = operands(9, T, d_in, d_out)
+        xq[0] = 0
+        say("int8 linear, scales far apart", T, d_in, d_out, fx, fw)
+        ref = R.linear(xq, xs * fx, wq, ws * fw)
+        big = (ref.abs() > 1e-37) | (ref == 0)
+        y = D.dora_linear_quantized(*[t.to(DEV) for t in (xq, xs * fx, wq, ws * fw)], dtype=F32).cpu()
+        lim = ref.abs() * (3.1 * 2.0 ** -24 + 2.0 ** -24)
+        assert big.double().mean() > 0.5 and ((y.double() - ref).abs() <= lim)[big].all()
+    say("int8 linear, large scales, a row of zeros")
+    xq, xs, wq, ws = operands(10, T, d_in, d_out)
+    xq[0] = 0
+    y = D.dora_linear_quantized(*[t.to(DEV) for t in (xq, xs * 1e36, wq, ws * 1e30)], dtype=F32)
+    assert (y[0] == 0).all()
 
 
 def test_empty_tokens_and_rows_behind_the_last():
@@ -159,3 +178,31 @@ def test_every_tile_choice(T, d_in, d_out, dt):
     """Sizes on both sides of the rules that choose a kernel and its tile."""
     say("int8 linear", T, d_in, d_out, dt)
     check(operands(T * 3 + d_out, T, d_in, d_out, lo=-128), dt, f"{T} x {d_in} x {d_out}")
+
+
+def test_two_streams_at_once():
+    """Calls with split sums and workspaces of their own, in flight together."""
+    one, two = [[t.to(DEV) for t in operands(s, *size)] for s, size in
+                ((11, (150, 8192, 512)), (12, (70, 4099, 300)))]
+    x = torch.randn(700, 1000, generator=torch.Generator().manual_seed(13)).to(DEV)
+    w = x[0].clone()
+    n = D.dora_rmsnorm(x, w, 1e-6, residual=x, want_rstd=True)
+    say("int8 linear and norm gradient, two streams")
+    want = [D.dora_linear_quantized(*one), D.dora_linear_quantized(*two),
+            D.dora_rmsnorm_backward(x, n["h"], w, n["rstd"])]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        with torch.cuda.stream(a):
+            got.append((0, D.dora_linear_quantized(*one)))
+            got.append((2, D.dora_rmsnorm_backward(x, n["h"], w, n["rstd"])))
+        with torch.cuda.stream(b):
+            got.append((1, D.dora_linear_quantized(*two)))
+            got.append((2, D.dora_rmsnorm_backward(x, n["h"], w, n["rstd"])))
+    torch.cuda.synchronize()
+    for i, y in got:
+        if i == 2:
+            assert torch.equal(y["dx"], want[2]["dx"]) and torch.equal(y["dw"], want[2]["dw"])
+        else:
+            assert torch.equal(y, want[i])
