@@ -18,7 +18,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 # (source, extra defines, object name): the pipelined GEMM's tile
 # configurations are one source compiled once per configuration, so that they
 # build in parallel.
-SOURCES = [("gemm_bf16.hip", (), "gemm_bf16"), ("gemm_f32.hip", (), "gemm_f32"),
+SOURCES = [("gemm_bf16.hip", (), "gemm_bf16"), ("gemm_bf16_any.hip", (), "gemm_bf16_any"),
+           ("gemm_f32.hip", (), "gemm_f32"),
            ("elementwise.hip", (), "elementwise"), ("dora_api.cpp", (), "dora_api"),
            ("noalloc.hip", (), "noalloc"),
            ("rows8.hip", (), "rows8"), ("gemm_i8.hip", (), "gemm_i8"),

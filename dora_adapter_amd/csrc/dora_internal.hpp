@@ -139,6 +139,8 @@ static_assert(sizeof(GemmGroup) <= 4096, "a group must fit the kernel argument s
 // (C = A B); 2 = A MN-major, B MN-major (C = A^T B).  `cfg` picks the tile
 // shape (see gemm_configs in the .hip file).
 hipError_t launch_gemm_bf16(const GemmArgs &a, int layout, int cfg, bool rowsq, hipStream_t st);
+// The same for operands of any width and alignment (gemm_bf16_any.hip).
+hipError_t launch_gemm_bf16_any(const GemmArgs &a, int layout, bool rowsq, hipStream_t st);
 hipError_t launch_gemm_f32(const GemmArgs &a, int layout, bool rowsq, hipStream_t st);
 // The backward's dB = alpha dh^T P with dh = g (.) dy and the dm sums formed
 // in the same pass (both operands MN-major, one segment: a.seg[0].a = dy,

@@ -47,82 +47,16 @@ struct OpRegs {
     static constexpr int PER = KMAJ ? (R * 8) / NT : ((R + NT - 1) / NT) * 8;
 };
 
-// Eight consecutive bf16 values p[0 .. 8) with those at or past `live` (their
-// row's end) read as zero, for rows of a ragged width, which start at any
-// element: one 16-byte load at whatever element, or, where the row ends inside
-// the eight, element by element.
-typedef unsigned int u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ uint4 load8_any(const uint16_t *__restrict__ p)
-{
-    const u32x4_any_t v = *reinterpret_cast<const u32x4_any_t *>(p);
-    return make_uint4(v.x, v.y, v.z, v.w);
-}
-__device__ __forceinline__ uint4 load8_masked(const uint16_t *__restrict__ p, int64_t live)
-{
-    if (live >= 8)
-        return load8_any(p);
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t lo = 2 * q < live ? p[2 * q] : 0u;
-        const uint32_t hi = 2 * q + 1 < live ? p[2 * q + 1] : 0u;
-        w[q] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// A ragged MN-major operand ends its rows inside a chunk.  That chunk is taken
-// from the row's last eight values instead (rows of at least eight): the first
-// column, from the tile's, of the eight that chunk mb holds.  Those columns are
-// written to LDS twice, with the same values; columns past the row's end keep
-// the zeros they start with.  (Loading the rest of a row element by element
-// instead holds up every load behind it: dA, 37 x 1027 over 509 tokens and 1411
-// rows of W, 93 us so, 34 this way; dx at 4096 x 8191 x 4097 1.17 ms and 0.87.)
-__device__ __forceinline__ int mn_first(int64_t MN, int64_t mn0, int mb)
-{
-    const int64_t c = mn0 + mb * 8;
-    return static_cast<int>((MN >= 8 && c + 8 > MN ? MN - 8 : c) - mn0);
-}
-
-// RG (ragged): any K, M, N and leading dimension; rows start at any element
-// and the chunks they end in are masked.  Otherwise K-major operands need K and ld
-// multiples of 8, MN-major ones M (or N) and ld multiples of 8, so that
-// every 16-byte chunk is aligned and wholly in or wholly out.
-template <bool KMAJ, int R, int NT, bool RG, int NV>
+// K-major operands need K and ld multiples of 8, MN-major ones M (or N) and ld
+// multiples of 8, so that every 16-byte chunk is aligned and wholly in or wholly
+// out (others: gemm_bf16_any.hip).
+template <bool KMAJ, int R, int NT, int NV>
 __device__ __forceinline__ void load_operand(uint4 (&v)[NV], const uint16_t *__restrict__ p,
                                              int64_t ld, int64_t MN, int64_t K, int64_t mn0,
                                              int64_t k0, int tid)
 {
     static_assert(NV == OpRegs<KMAJ, R, NT>::PER, "register count");
-    if constexpr (RG && KMAJ) {
-#pragma unroll
-        for (int i = 0; i < OpRegs<KMAJ, R, NT>::PER; ++i) {
-            const int idx = tid + i * NT;
-            const int row = idx >> 3, c = idx & 7;
-            const int64_t mn = mn0 + row, k = k0 + c * 8;
-            v[i] = mn < MN && k < K ? load8_masked(p + mn * ld + k, K - k)
-                                    : make_uint4(0, 0, 0, 0);
-        }
-    } else if constexpr (RG) {
-#pragma unroll
-        for (int b = 0; b < OpRegs<KMAJ, R, NT>::PER / 8; ++b) {
-            const int idx = tid + b * NT;
-            const int kb = idx / (R / 8), mb = idx % (R / 8);
-            const int64_t mn = mn0 + mb * 8, kk = k0 + kb * 8;
-            const int64_t rows = idx < R && mn < MN ? K - kk : 0;  // K values there
-            if (MN >= 8) {
-                const uint16_t *q = p + kk * ld + mn0 + mn_first(MN, mn0, mb);
-#pragma unroll
-                for (int j = 0; j < 8; ++j, q += ld)
-                    v[b * 8 + j] = j < rows ? load8_any(q) : make_uint4(0, 0, 0, 0);
-            } else {
-                const uint16_t *q = p + kk * ld + mn;
-#pragma unroll
-                for (int j = 0; j < 8; ++j, q += ld)
-                    v[b * 8 + j] = j < rows ? load8_masked(q, MN - mn) : make_uint4(0, 0, 0, 0);
-            }
-        }
-    } else if constexpr (KMAJ) {
+    if constexpr (KMAJ) {
         static_assert((R * 8) % NT == 0, "K-major tile must split evenly");
 #pragma unroll
         for (int i = 0; i < OpRegs<KMAJ, R, NT>::PER; ++i) {
@@ -168,11 +102,9 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int w)
     return w == 0 ? v.x : (w == 1 ? v.y : (w == 2 ? v.z : v.w));
 }
 
-// Write one operand tile into LDS as R rows of eight swizzled 16-byte chunks
-// (MN, mn0: of a ragged MN-major operand).
-template <bool KMAJ, int R, int NT, bool RG, int NV>
-__device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4 (&v)[NV], int64_t MN,
-                                              int64_t mn0, int tid)
+// Write one operand tile into LDS as R rows of eight swizzled 16-byte chunks.
+template <bool KMAJ, int R, int NT, int NV>
+__device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4 (&v)[NV], int tid)
 {
     static_assert(NV == OpRegs<KMAJ, R, NT>::PER, "register count");
     if constexpr (KMAJ) {
@@ -189,11 +121,8 @@ __device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4
             if (idx >= R)
                 continue;
             const int kb = idx / (R / 8), mb = idx % (R / 8);
-            if (RG && mn0 + mb * 8 >= MN)
-                continue;
-            const int first = RG ? mn_first(MN, mn0, mb) : mb * 8;
             // v[b*8 + j] holds k = kb*8 + j, mn = mb*8 .. mb*8+7 (two per word).
-            // Output q holds mn = mb*8 + q, k = kb*8 .. kb*8+7 (RG: first + q).
+            // Output q holds mn = mb*8 + q, k = kb*8 .. kb*8+7.
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const int w = q >> 1;
@@ -209,14 +138,8 @@ __device__ __forceinline__ void store_operand(uint4 *__restrict__ S, const uint4
                     o.z = hi_halves(word(v[b * 8 + 4], w), word(v[b * 8 + 5], w));
                     o.w = hi_halves(word(v[b * 8 + 6], w), word(v[b * 8 + 7], w));
                 }
-                // (rows of whole chunks at constant distances)
-                if (!RG || first == mb * 8) {
-                    const int row = mb * 8 + q;
-                    S[row * 8 + (kb ^ (row & 7))] = o;
-                } else if (first + q >= 0) {
-                    const int row = first + q;
-                    S[row * 8 + (kb ^ (row & 7))] = o;
-                }
+                const int row = mb * 8 + q;
+                S[row * 8 + (kb ^ (row & 7))] = o;
             }
         }
     }
@@ -231,7 +154,7 @@ struct Smem {
     static constexpr int BYTES = OPS > EPI ? OPS : EPI;
 };
 
-template <int BM, int BN, int WM, int WN, bool AK, bool BKM, bool ROWSQ, bool RG>
+template <int BM, int BN, int WM, int WN, bool AK, bool BKM, bool ROWSQ>
 __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
 {
     using SM = Smem<BM, BN, WM, WN>;
@@ -280,10 +203,10 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
         const bool first = s < st1;
         const GemmSeg &sg = first ? g.seg[0] : g.seg[1];
         const int64_t k0 = (first ? s : s - st1) * BK;
-        load_operand<AK, BM, NT, RG>(ra, static_cast<const uint16_t *>(sg.a), sg.lda, g.M, sg.K,
-                                     m0, k0, tid);
-        load_operand<BKM, BN, NT, RG>(rb, static_cast<const uint16_t *>(sg.b), sg.ldb, g.N, sg.K,
-                                      n0, k0, tid);
+        load_operand<AK, BM, NT>(ra, static_cast<const uint16_t *>(sg.a), sg.lda, g.M, sg.K, m0,
+                                 k0, tid);
+        load_operand<BKM, BN, NT>(rb, static_cast<const uint16_t *>(sg.b), sg.ldb, g.N, sg.K, n0,
+                                  k0, tid);
     };
     auto store_step = [&](int buf) {
         if constexpr (ROWSQ) {
@@ -299,8 +222,8 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
                 }
             }
         }
-        store_operand<AK, BM, NT, RG>(As + buf * BM * 8, ra, g.M, m0, tid);
-        store_operand<BKM, BN, NT, RG>(Bs + buf * BN * 8, rb, g.N, n0, tid);
+        store_operand<AK, BM, NT>(As + buf * BM * 8, ra, tid);
+        store_operand<BKM, BN, NT>(Bs + buf * BN * 8, rb, tid);
     };
     auto compute = [&](int buf) {
         const uint4 *Ab = As + buf * BM * 8;
@@ -328,12 +251,6 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
         }
     };
 
-    if constexpr (RG && (!AK || !BKM)) {
-        // columns past a ragged row's end are never written
-        for (int i = tid; i < 2 * (BM + BN) * 8; i += NT)
-            As[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
     if (s_begin < s_end) {
         load_step(s_begin);
         store_step(0);
@@ -393,8 +310,8 @@ __global__ void __launch_bounds__(WM *WN * 64) gemm_bf16_kernel(GemmArgs g)
 // for the square ones, and, for 128 x 128 and the rank-wide tiles, the
 // rate they reach as one wave of tiles on the rank-r products (x A^T,
 // dh^T P, Q^T x at the training shape).
-// The 128 x 128 register-staged configuration also exists with
-// loads at any element (ragged_ok), for operands of any width.
+// The 128 x 128 register-staged configuration also stands for the kernel that
+// loads at any element (ragged_ok; gemm_bf16_any.hip).
 constexpr TileCfg kCfgs[] = {
     {256, 256, GEMM_BK, false, 0.76f, true, true, false, false, false},
     {256, 128, GEMM_BK, false, 0.68f, true, true, false, false, false},
@@ -424,29 +341,28 @@ constexpr TileCfg kCfgs[] = {
 
 namespace {
 
-template <int BM, int BN, bool AK, bool BKM, bool RS, bool RG>
+template <int BM, int BN, bool AK, bool BKM, bool RS>
 hipError_t launch_one(const GemmArgs &a, hipStream_t st)
 {
     const int64_t tiles = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
     if (tiles == 0 || a.splits == 0)
         return hipSuccess;
     dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.splits));
-    hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, 2, 2, AK, BKM, RS, RG>), grid, dim3(256), 0, st,
-                       a);
+    hipLaunchKernelGGL((gemm_bf16_kernel<BM, BN, 2, 2, AK, BKM, RS>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
-template <int BM, int BN, bool RG = false>
+template <int BM, int BN>
 hipError_t launch_cfg(const GemmArgs &a, int layout, bool rowsq, hipStream_t st)
 {
     switch (layout) {
     case 0:
-        return rowsq ? launch_one<BM, BN, true, true, true, RG>(a, st)
-                     : launch_one<BM, BN, true, true, false, RG>(a, st);
+        return rowsq ? launch_one<BM, BN, true, true, true>(a, st)
+                     : launch_one<BM, BN, true, true, false>(a, st);
     case 1:
-        return launch_one<BM, BN, true, false, false, RG>(a, st);
+        return launch_one<BM, BN, true, false, false>(a, st);
     case 2:
-        return launch_one<BM, BN, false, false, false, RG>(a, st);
+        return launch_one<BM, BN, false, false, false>(a, st);
     default:
         return hipErrorInvalidValue;
     }
@@ -492,7 +408,7 @@ hipError_t launch_gemm_bf16(const GemmArgs &a, int layout, int cfg, bool rowsq, 
         // only the any-width configuration takes unaligned operands
         if (!kCfgs[cfg].ragged_ok)
             return hipErrorInvalidValue;
-        return launch_cfg<128, 128, true>(a, layout, rowsq, st);
+        return launch_gemm_bf16_any(a, layout, rowsq, st);
     }
     switch (cfg) {
     case 0:

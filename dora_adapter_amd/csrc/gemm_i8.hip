@@ -15,6 +15,7 @@
 // one's products.
 #include "dora_internal.hpp"
 #include "gemm_bf16_dma.hpp"
+#include "ragged.hpp"
 #include "rows8.hpp"
 
 namespace dora {
@@ -25,26 +26,6 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 constexpr int GK = 128;          // bytes of K a step
 constexpr int GPITCH = GK + 16;  // LDS row: 8 rows of a 16-byte read phase on distinct banks
 constexpr int GTHREADS = 256;
-
-// What is left of 16 bytes that were loaded `back` bytes early and of which
-// `left` belong to the row (the rest zeros): the row's last chunk.
-__device__ __forceinline__ i32x4_t row_end16(i32x4_t v, int back, int64_t left)
-{
-    uint64_t lo = static_cast<uint32_t>(v[0]) | static_cast<uint64_t>(static_cast<uint32_t>(v[1])) << 32;
-    uint64_t hi = static_cast<uint32_t>(v[2]) | static_cast<uint64_t>(static_cast<uint32_t>(v[3])) << 32;
-    if (back >= 8) {
-        lo = hi >> (8 * (back - 8));
-        hi = 0;
-    } else if (back > 0) {
-        lo = lo >> (8 * back) | hi << (64 - 8 * back);
-        hi >>= 8 * back;
-    }
-    const int n = left < 0 ? 0 : (left < 16 ? static_cast<int>(left) : 16);
-    lo = n >= 8 ? lo : lo & ((1ull << (8 * n)) - 1);
-    hi = n >= 16 ? hi : (n > 8 ? hi & ((1ull << (8 * (n - 8))) - 1) : 0);
-    return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi),
-                   static_cast<int>(hi >> 32)};
-}
 
 // The first `left` bytes at p, one by one (operands of fewer than 16 bytes).
 __device__ __forceinline__ i32x4_t load_bytes(const int8_t *p, int64_t left)
@@ -110,7 +91,10 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
     // go to LDS (row_end16).
     const int64_t alim = g.M * g.K - 16, blim = g.N * g.K - 16;
     auto load16 = [](const int8_t *p) {
-        return __builtin_bit_cast(i32x4_t, *reinterpret_cast<const u32x4_a1_t *>(p));
+        return __builtin_bit_cast(i32x4_t, load16_any(p));
+    };
+    auto ended = [](i32x4_t v, int back, int64_t left) {
+        return __builtin_bit_cast(i32x4_t, row_end16(__builtin_bit_cast(uint4, v), back, left));
     };
     auto fetch = [&](Regs &r, int64_t k) {
         if constexpr (TINY) {
@@ -137,8 +121,8 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int64_t ab = ao[i] + k - alim, bb = bo[i] + k - blim, left = g.K - k - lc;
-            r.a[i] = row_end16(r.a[i], ab > 0 && left > 0 ? static_cast<int>(ab) : 0, left);
-            r.b[i] = row_end16(r.b[i], bb > 0 && left > 0 ? static_cast<int>(bb) : 0, left);
+            r.a[i] = ended(r.a[i], ab > 0 && left > 0 ? static_cast<int>(ab) : 0, left);
+            r.b[i] = ended(r.b[i], bb > 0 && left > 0 ? static_cast<int>(bb) : 0, left);
         }
     };
     i32x4_t acc[TM][TN];

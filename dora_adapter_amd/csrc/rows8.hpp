@@ -17,7 +17,6 @@ namespace dora {
 typedef unsigned int u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned int u32x4_a4_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef unsigned int u32x2_a1_t __attribute__((ext_vector_type(2), aligned(1)));
-typedef unsigned int u32x4_a1_t __attribute__((ext_vector_type(4), aligned(1)));
 
 // Eight consecutive elements, as they are stored.  load() takes the first
 // `cnt` of them (the rest read as zero), store() writes the first `cnt`.
