@@ -3,22 +3,25 @@
 // epilogues as gemm_bf16.hip's kernel, with 128 x 128 or 64 x 64 tiles.
 //
 // Operands are staged through registers by 16-byte loads at whatever element.
-// A load that runs past its row's end takes in the next row's values; the last K
-// step's are put right on the way into LDS, so that no load waits for another.
+// A load that runs past its row's end takes in the next row's values, and at the
+// matrix's end it starts early; the last K steps' are put right on the way into
+// LDS, so that there is no branch and no wait among the loads.
 //   K-major: a thread holds chunk tid & 7 of rows (tid >> 3) + 32 i (rows past
 //     the end: the last one, never stored);
 //   MN-major: KR = B / 32 consecutive K rows of eight columns, written to LDS as
-//     2 KR bytes of each of the eight rows there.  The chunk in which the rows
-//     end is taken from their last eight values instead (matrices of at least
-//     eight columns): those columns are written twice, with the same values, and
-//     columns past the end keep the zeros they start with.
+//     2 KR bytes of each of the eight rows there.  The chunk in which rows of at
+//     least eight columns end is taken from their last eight instead: those
+//     columns are written twice, with the same values.  Columns past the end
+//     are never stored.
 // LDS rows hold 64 K values as eight 16-byte chunks, chunk c of row r at
 // c ^ (r & 7) ^ (r / 8 & 7): fragment reads, and the writes of one chunk column
 // by threads eight rows apart, meet distinct banks.
 //
-// These products are small, so a step's time is its loads' round trip: AHEAD
-// steps' loads are in flight, and 64 x 64 tiles serve where there are few 128 x
-// 128 ones.
+// Most of these products are small, and a step's time is its loads' round trip:
+// 64 x 64 tiles, with AHEAD = 2 steps' loads in flight, serve where there are few
+// 128 x 128 ones (whose accumulators leave registers for one step's).  The nine
+// products of a backward through the norm, 509 tokens, 1027 -> 1411, r 37, call
+// included: 148 us, with one step ahead 170, three 155, 128 x 128 tiles alone 245.
 #include "dora_internal.hpp"
 #include "epilogue.hpp"
 #include "gemm_bf16_dma.hpp"
@@ -33,8 +36,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int BK = GEMM_BK, NT = 256;
 static_assert(BK == 64, "eight chunks a row");
 
-// Eight values p[0 .. 8), those at or past `live` zero, one by one (matrices of
-// fewer than eight values, rows of fewer than eight columns).
+// Eight values p[0 .. 8), those at or past `live` zero, one by one (products with
+// a matrix of fewer than eight values).
 __device__ __forceinline__ uint4 load8_masked(const uint16_t *p, int64_t live)
 {
     uint32_t w[4];
@@ -55,7 +58,7 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int w)
 __device__ __forceinline__ int place(int row, int c) { return row * 8 + (c ^ ((row ^ (row >> 3)) & 7)); }
 
 // One operand's share of a step: B rows (of M or N) x 64 K values, rows from mn0.
-template <bool KMAJ, int B>
+template <bool KMAJ, int B, bool TINY>
 struct Operand {
     static constexpr int PER = B / 32;  // chunks a thread
     static constexpr int CB = B / 8;    // column chunks of an MN-major tile
@@ -67,67 +70,63 @@ struct Operand {
         return static_cast<int>((MN >= 8 && c + 8 > MN ? MN - 8 : c) - mn0);
     }
 
-    static __device__ __forceinline__ void load(uint4 (&v)[PER], const uint16_t *p, int64_t ld,
-                                                int64_t MN, int64_t K, int64_t mn0, int64_t k0,
-                                                int tid)
+    // the matrix's last eight values
+    static __device__ __forceinline__ int64_t last(int64_t ld, int64_t MN, int64_t K)
+    {
+        return KMAJ ? (MN - 1) * ld + K - 8 : (K - 1) * ld + MN - 8;
+    }
+
+    // where chunk i of a step starts, from the step's first K value on: its row
+    // (K-major), its K value and its first column (MN-major)
+    static __device__ __forceinline__ int64_t start(int64_t ld, int64_t MN, int64_t mn0, int tid,
+                                                    int i)
     {
         if constexpr (KMAJ) {
-            const int64_t k = k0 + (tid & 7) * 8, last = (MN - 1) * ld + K - 8;
-            if (k0 + BK <= K) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int64_t mn = mn0 + (tid >> 3) + 32 * i;
-                    v[i] = load16_any(p + (mn < MN ? mn : MN - 1) * ld + k);
-                }
-            } else if (last >= 0) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int64_t mn = mn0 + (tid >> 3) + 32 * i;
-                    const int64_t at = (mn < MN ? mn : MN - 1) * ld + k;
-                    v[i] = load16_any(p + (at < last ? at : last));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int64_t mn = mn0 + (tid >> 3) + 32 * i;
-                    v[i] = mn < MN ? load8_masked(p + mn * ld + k, K - k) : make_uint4(0, 0, 0, 0);
-                }
-            }
+            const int64_t mn = mn0 + (tid >> 3) + 32 * i;
+            return (mn < MN ? mn : MN - 1) * ld + (tid & 7) * 8;
         } else {
             const int mb = tid % CB;
-            const int64_t k = k0 + tid / CB * PER;
-            const int64_t c = mn0 + mb * 8 < MN ? mn0 + first(MN, mn0, mb) : 0;
-            if (MN >= 8) {
+            return (tid / CB * PER + i) * ld + (mn0 + mb * 8 < MN ? mn0 + first(MN, mn0, mb) : 0);
+        }
+    }
+    int64_t from[PER];  // those of the segment that is being loaded
+    __device__ __forceinline__ void init(int64_t ld, int64_t MN, int64_t mn0, int tid)
+    {
 #pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    v[j] = load16_any(p + (k + j < K ? k + j : K - 1) * ld + c);
+        for (int i = 0; i < PER; ++i)
+            from[i] = start(ld, MN, mn0, tid, i);
+    }
+
+    __device__ __forceinline__ void load(uint4 (&v)[PER], const uint16_t *p, int64_t ld, int64_t MN,
+                                         int64_t K, int64_t mn0, int64_t k0, int tid) const
+    {
+        const int64_t end = last(ld, MN, K), step = KMAJ ? k0 : k0 * ld;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int64_t at = from[i] + step;
+            if constexpr (TINY) {
+                const int64_t k = k0 + (KMAJ ? (tid & 7) * 8 : tid / CB * PER + i);
+                const int64_t c = mn0 + tid % CB * 8;
+                v[i] = k < K ? load8_masked(p + at, KMAJ ? K - k : (c < MN ? MN - mn0 - first(MN, mn0, tid % CB) : 0))
+                             : make_uint4(0, 0, 0, 0);
             } else {
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    v[j] = load8_masked(p + (k + j < K ? k + j : K - 1) * ld + c, MN - c);
+                v[i] = load16_any(p + (at < end ? at : end));
             }
         }
     }
 
-    // The values past the K range's end, zeroed (the last step's).
-    static __device__ __forceinline__ void end(uint4 (&v)[PER], int64_t ld, int64_t MN, int64_t K,
-                                               int64_t mn0, int64_t k0, int tid)
+    // What of the loads near the K range's end belongs there (`tail`).
+    static constexpr int TAIL = KMAJ ? 0 : 8;  // MN-major rows of fewer than eight columns
+    static __device__ __forceinline__ void tail(uint4 (&v)[PER], int64_t ld, int64_t MN, int64_t K,
+                                                int64_t mn0, int64_t k0, int tid)
     {
-        if constexpr (KMAJ) {
-            const int64_t k = k0 + (tid & 7) * 8, last = (MN - 1) * ld + K - 8, left = K - k;
+        const int64_t end = last(ld, MN, K);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int64_t mn = mn0 + (tid >> 3) + 32 * i;
-                const int64_t back = (mn < MN ? mn : MN - 1) * ld + k - last;
-                v[i] = row_end16(v[i], last >= 0 && back > 0 && left > 0 ? static_cast<int>(2 * back) : 0,
-                                 2 * left);
-            }
-        } else {
-            const int64_t k = k0 + tid / CB * PER;
-#pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (k + j >= K)
-                    v[j] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < PER; ++i) {
+            const int64_t k = k0 + (KMAJ ? (tid & 7) * 8 : tid / CB * PER + i), left = K - k;
+            const int64_t back = start(ld, MN, mn0, tid, i) + (KMAJ ? k0 : k0 * ld) - end;
+            v[i] = row_end16(v[i], !TINY && back > 0 && left > 0 ? static_cast<int>(2 * back) : 0,
+                             KMAJ ? 2 * left : (left > 0 ? 16 : 0));
         }
     }
 
@@ -165,14 +164,15 @@ struct Operand {
     }
 };
 
-template <int B, int AHEAD, bool AK, bool BKM, bool ROWSQ>
+// TINY: a matrix of fewer than eight values
+template <int B, int AHEAD, bool TINY, bool AK, bool BKM, bool ROWSQ>
 __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
 {
     constexpr int WT = B / 2, TT = WT / 16, PER = B / 32;
     constexpr int CST = B + 4;  // floats of an epilogue row
     constexpr int OPS = 2 * 2 * B * BK * 2, EPI = WT * CST * 4;
-    using OA = Operand<AK, B>;
-    using OB = Operand<BKM, B>;
+    using OA = Operand<AK, B, TINY>;
+    using OB = Operand<BKM, B, TINY>;
     static_assert(!ROWSQ || AK, "row sums of squares need a K-major A");
     __shared__ __align__(16) unsigned char smem[OPS > EPI ? OPS : EPI];
     uint4 *const lds = reinterpret_cast<uint4 *>(smem);  // [2][A, B][B * 8]
@@ -207,13 +207,21 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
     } regs[AHEAD];
     // the loads of step s (past the split's end its last one again: the loads in
     // flight are always the same number)
+    OA oa;
+    OB ob;
+    int64_t seg_end = -1;  // the loads' segment ends here
     auto load = [&](Regs &r, int64_t s) {
         s = s < s_end ? s : s_end - 1;
         const bool one = s < st1;
         const GemmSeg &sg = one ? g.seg[0] : g.seg[1];
+        if (s >= seg_end) {
+            seg_end = one ? st1 : st_total;
+            oa.init(sg.lda, g.M, m0, tid);
+            ob.init(sg.ldb, g.N, n0, tid);
+        }
         const int64_t k0 = (one ? s : s - st1) * BK;
-        OA::load(r.a, static_cast<const uint16_t *>(sg.a), sg.lda, g.M, sg.K, m0, k0, tid);
-        OB::load(r.b, static_cast<const uint16_t *>(sg.b), sg.ldb, g.N, sg.K, n0, k0, tid);
+        oa.load(r.a, static_cast<const uint16_t *>(sg.a), sg.lda, g.M, sg.K, m0, k0, tid);
+        ob.load(r.b, static_cast<const uint16_t *>(sg.b), sg.ldb, g.N, sg.K, n0, k0, tid);
     };
     int at = 0;
     // One barrier a step (a wave past it is done with the other buffer), bare:
@@ -222,10 +230,10 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
         const bool one = s < st1;
         const GemmSeg &sg = one ? g.seg[0] : g.seg[1];
         const int64_t k0 = (one ? s : s - st1) * BK;
-        if (k0 + BK > sg.K) {
-            OA::end(r.a, sg.lda, g.M, sg.K, m0, k0, tid);
-            OB::end(r.b, sg.ldb, g.N, sg.K, n0, k0, tid);
-        }
+        if (k0 + BK + OA::TAIL > sg.K)
+            OA::tail(r.a, sg.lda, g.M, sg.K, m0, k0, tid);
+        if (k0 + BK + OB::TAIL > sg.K)
+            OB::tail(r.b, sg.ldb, g.N, sg.K, n0, k0, tid);
         if constexpr (ROWSQ) {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -262,12 +270,6 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
         }
         at ^= 1;
     };
-    if constexpr (!AK || !BKM) {
-        // columns past an MN-major matrix's end are never written
-        for (int i = tid; i < 2 * 2 * B * 8; i += NT)
-            lds[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
     if (s_begin < s_end) {
 #pragma unroll
         for (int p = 0; p < AHEAD; ++p)
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
     }
 }
 
-template <int B, int AHEAD>
+template <int B, int AHEAD, bool TINY = false>
 hipError_t launch_any(const GemmArgs &a, int layout, bool rowsq, hipStream_t st)
 {
     const int64_t tiles = ((a.M + B - 1) / B) * ((a.N + B - 1) / B);
@@ -328,26 +330,43 @@ hipError_t launch_any(const GemmArgs &a, int layout, bool rowsq, hipStream_t st)
         return hipSuccess;
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(a.splits)), block(NT);
     if (layout == 0 && rowsq)
-        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, true, true, true>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, TINY, true, true, true>), grid, block, 0, st, a);
     else if (layout == 0)
-        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, true, true, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, TINY, true, true, false>), grid, block, 0, st, a);
     else if (layout == 1)
-        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, true, false, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, TINY, true, false, false>), grid, block, 0, st, a);
     else if (layout == 2)
-        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, false, false, false>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((gemm_bf16_any_kernel<B, AHEAD, TINY, false, false, false>), grid, block, 0, st, a);
     else
         return hipErrorInvalidValue;
     return hipGetLastError();
+}
+
+// Whether a matrix holds fewer than the eight values of one load.
+bool tiny(const GemmArgs &a, int layout)
+{
+    for (int q = 0; q < a.nseg; ++q) {
+        const GemmSeg &sg = a.seg[q];
+        if (sg.K > 0 && ((layout < 2 ? (a.M - 1) * sg.lda + sg.K : (sg.K - 1) * sg.lda + a.M) < 8 ||
+                         (layout == 0 ? (a.N - 1) * sg.ldb + sg.K : (sg.K - 1) * sg.ldb + a.N) < 8))
+            return true;
+    }
+    return false;
 }
 
 }  // namespace
 
 // The planner counts 128 x 128 tiles, whose columns also number the row-dot
 // partial sums; stored products take 64 x 64 ones, with the same bits, where
-// those are too few for the CUs.
+// those are fewer than the CUs (x W^T, 1027 -> 1411 at 509 tokens, 48 tiles of
+// 128 x 128: 18 us, by those 26; 4097 -> 4096 at 2048, 512 of them: 178 us, by
+// those 103).
 hipError_t launch_gemm_bf16_any(const GemmArgs &a, int layout, bool rowsq, hipStream_t st)
 {
     const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128) * a.splits;
+    if (tiny(a, layout))
+        return a.mode == EPI_ROWDOT ? launch_any<128, 1, true>(a, layout, rowsq, st)
+                                    : launch_any<64, 1, true>(a, layout, rowsq, st);
     if (a.mode != EPI_ROWDOT && tiles < 256)
         return launch_any<64, 2>(a, layout, rowsq, st);
     return launch_any<128, 1>(a, layout, rowsq, st);

@@ -202,3 +202,32 @@ def test_captured_steps_replay_and_a_second_stream():
             assert torch.equal(got[key], now[key]), (k, key)
             if k == 0:
                 assert torch.equal(eager[key], now[key]), key
+
+
+# sizes at which operands end inside a load, or hold less than one
+ANY = [(1, 1, 1, 1), (2, 3, 2, 1), (1, 1, 9, 2), (5, 1, 3, 7), (1, 9, 1, 9), (7, 4, 65, 3), (65, 67, 3, 2),
+       (3, 65, 127, 5), (63, 5, 200, 1), (70, 7, 129, 3), (129, 8, 8, 7), (130, 200, 5, 6),
+       (257, 71, 66, 13), (300, 255, 250, 31)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,d_in,d_out,r", ANY)
+def test_products_of_any_width_are_exact_on_integers(T, d_in, d_out, r, dt):
+    # values -1, 0, 1 and g = s = 1: |Q| <= d_out <= 256 is exact in bf16, every
+    # sum is exact in fp32, so each gradient is the exact one rounded once
+    g = torch.Generator().manual_seed(T + d_in)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g).double()
+    dy, W, A, B, P = ints(T, d_out), ints(d_out, d_in), ints(r, d_in), ints(d_out, r), ints(T, r)
+    x, y = ints(T, d_in), ints(T, d_out)
+    one = torch.ones(d_out, device=DEV)
+    dev = lambda t: t.to(dt).to(DEV)
+    i8 = lambda t: (t.to(torch.int8).to(DEV), torch.ones(T, 1, device=DEV))
+    say("integers", T, d_in, d_out, r, dt)
+    got = D.dora_backward_checkpoint(dev(dy), *i8(x), dev(W), dev(A), dev(B), one, one, 1.0, dev(P),
+                                     *i8(y))
+    Q = dy @ B
+    want = {"dx": dy @ W + Q @ A, "dA": Q.T @ x, "dB": dy.T @ P, "dm": (dy * y).sum(0)}
+    for k, v in want.items():
+        assert torch.equal(got[k].cpu(), v.to(got[k].dtype)), k
+    xd, Wd = dev(x), dev(W)
+    assert torch.equal(D.dora_linear(xd, Wd).cpu(), (x @ W.T).to(dt))
