@@ -735,11 +735,14 @@ int rmsnorm_parts(int64_t T, int64_t d, int bf16)
     const int64_t vecs = (d + 7) / 8;
     int64_t p;
     if (grad_held(d, !bf16)) {
-        // a workgroup a CU as soon as there are rows for them, then 16 rows a
-        // workgroup, up to the workgroups that fit the CUs at once
-        const int64_t waves = (vecs + 127) / 128;
-        const int64_t fit = 256 * (16 / (waves < 16 ? waves : 16));
-        p = T / 16 > 256 ? T / 16 : 256;
+        // a workgroup a CU as soon as there are rows for them, and where rows are
+        // short, up to four, of eight rows at least.  us with 256, 512, 768, 1024
+        // workgroups: 8192 x 8192 94, 101, 105, 110; 16384 x 4096 92, 94, 101, 104;
+        // 8192 x 2048 45, 33, 34, 36; 32768 x 1024 131, 78, 58, 53; 2048 x 2048 17,
+        // 17, 18, 20
+        const int64_t lanes = bf16 ? 128 : 64, waves = (vecs + lanes - 1) / lanes;
+        const int64_t fit = 256 * (waves > 4 ? 1 : waves > 2 ? 2 : waves > 1 ? 3 : 4);
+        p = T / 8 > 256 ? T / 8 : 256;
         p = p < fit ? p : fit;
         p = p < T ? p : T;
     } else {
