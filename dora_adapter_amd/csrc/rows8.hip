@@ -735,15 +735,16 @@ int rmsnorm_parts(int64_t T, int64_t d, int bf16)
     const int64_t vecs = (d + 7) / 8;
     int64_t p;
     if (grad_held(d, !bf16)) {
-        // a workgroup a CU as soon as there are rows for them, and where rows are
-        // short, up to four, of eight rows at least.  us with 256, 512, 768, 1024
-        // workgroups: 8192 x 8192 94, 101, 105, 110; 16384 x 4096 92, 94, 101, 104;
-        // 8192 x 2048 45, 33, 34, 36; 32768 x 1024 131, 78, 58, 53; 2048 x 2048 17,
-        // 17, 18, 20
-        const int64_t lanes = bf16 ? 128 : 64, waves = (vecs + lanes - 1) / lanes;
-        const int64_t fit = 256 * (waves > 4 ? 1 : waves > 2 ? 2 : waves > 1 ? 3 : 4);
-        p = T / 8 > 256 ? T / 8 : 256;
-        p = p < fit ? p : fit;
+        // a workgroup a CU as soon as there are rows for them, and the shorter the
+        // rows the more, of eight rows at least (four of up to 1024 columns).  us
+        // with 256, 512, 1024, 2048 workgroups (bf16): 8192 x 8192 94, 101, 110, 128;
+        // 16384 x 4096 92, 94, 104, 108; 8192 x 2048 45, 33, 36, 44; 32768 x 1024 131,
+        // 78, 53, 58; 32768 x 512 91, 54, 38, 35 (4096: 43); 65536 x 128 381, 229, 128,
+        // 77 (4096: 55); 4096 x 768 41, 27, 21, 24
+        const int most = vecs > 512 ? 1 : vecs > 128 ? 2 : vecs > 64 ? 4 : vecs > 32 ? 8 : 16;
+        const int64_t share = vecs > 128 ? T / 8 : T / 4;
+        p = share > 256 ? share : 256;
+        p = p < 256 * most ? p : 256 * most;
         p = p < T ? p : T;
     } else {
         // about 2048 workgroups over column blocks and row shares, 16 rows each
