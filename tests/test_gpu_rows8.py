@@ -152,7 +152,8 @@ def test_rows_behind_the_last_are_left_alone():
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
-@pytest.mark.parametrize("T,d", SHAPES + [(300, 136), (1000, 65), (70, 4096), (517, 2047)])
+@pytest.mark.parametrize("T,d", SHAPES + [(300, 136), (1000, 65), (70, 4096), (517, 2047),
+                                           (9000, 40), (4100, 256), (2100, 1000)])
 def test_rmsnorm_backward_matches_formula(T, d, dt):
     for with_dres in (True, False):
         say("rmsnorm backward", T, d, dt, with_dres)
