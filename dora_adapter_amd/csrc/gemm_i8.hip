@@ -42,13 +42,13 @@ __device__ __forceinline__ i32x4_t load_bytes(const int8_t *p, int64_t left)
 // Four consecutive outputs of row m from column n on.
 template <typename T>
 __device__ __forceinline__ void store_scaled(const I8GemmArgs &g, int64_t m, int64_t n,
-                                             const int (&c)[4], float sx)
+                                             const int (&c)[4], I8Scale sx)
 {
     T *out = static_cast<T *>(g.y) + m * g.N + n;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (n + e < g.N) {
-            const float v = i8_scaled(c[e], sx, i8_ws(g.ws[n + e]));
+            const float v = i8_scaled(c[e], sx, g.ws[n + e]);
             if constexpr (sizeof(T) == 2)
                 out[e] = f32_to_bf16(v);
             else
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(128 * WN, 2) gemm_i8_general_kernel(I8GemmArgs
         const int64_t m = m0 + wm + 16 * i + (lane & 15);
         if (m >= g.M)
             continue;
-        const float sx = i8_xs(g.xs[m]);
+        const I8Scale sx = i8_xs(g.xs[m]);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(GTHREADS) i8_finish_kernel(I8GemmArgs g, int s
         int c = 0;
         for (int z = 0; z < splits; ++z)
             c += g.part[static_cast<int64_t>(z) * MN + e];
-        const float v = i8_scaled(c, i8_xs(g.xs[e / g.N]), i8_ws(g.ws[e % g.N]));
+        const float v = i8_scaled(c, i8_xs(g.xs[e / g.N]), g.ws[e % g.N]);
         if constexpr (sizeof(T) == 2)
             static_cast<T *>(g.y)[e] = f32_to_bf16(v);
         else

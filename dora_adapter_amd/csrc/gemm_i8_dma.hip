@@ -249,12 +249,12 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
 #pragma unroll
             for (int b = 0; b < WTM; b += 64) {
                 const int64_t m = m0 + b + lane;
-                lsx[b + lane] = i8_xs(g.xs[m < g.M ? m : g.M - 1]);
+                lsx[b + lane] = g.xs[m < g.M ? m : g.M - 1];
             }
 #pragma unroll
             for (int b = 0; b < WTN; b += 64) {
                 const int64_t n = n0 + b + lane;
-                lsw[b + lane] = i8_ws(g.ws[n < g.N ? n : g.N - 1]);
+                lsw[b + lane] = g.ws[n < g.N ? n : g.N - 1];
             }
         } else if constexpr (OUT != OUT_PART) {
 #pragma unroll
@@ -267,19 +267,18 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                     swr[j] = make_float4(g.ws[n < last ? n : last], g.ws[n + 1 < last ? n + 1 : last],
                                          g.ws[n + 2 < last ? n + 2 : last],
                                          g.ws[n + 3 < last ? n + 3 : last]);
-                swr[j] = make_float4(i8_ws(swr[j].x), i8_ws(swr[j].y), i8_ws(swr[j].z), i8_ws(swr[j].w));
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int64_t m = m0 + 16 * i + (lane & 15);
-                sxr[i] = i8_xs(g.xs[m < g.M ? m : g.M - 1]);
+                sxr[i] = g.xs[m < g.M ? m : g.M - 1];
             }
         }
         auto scale_x = [&](int i) {
             if constexpr (LDS_SCALES)
-                return lsx[16 * i + (lane & 15)];
+                return i8_xs(lsx[16 * i + (lane & 15)]);
             else
-                return sxr[i];
+                return i8_xs(sxr[i]);
         };
         auto scale_w = [&](int j) {
             if constexpr (LDS_SCALES)
@@ -295,6 +294,9 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                 for (int ii = 0; ii < 2; ++ii) {
                     const int i = 2 * i2 + ii;
                     const int rr = 16 * ii + (lane & 15);
+                    I8Scale sx;
+                    if constexpr (OUT != OUT_PART)
+                        sx = scale_x(i);
 #pragma unroll
                     for (int jj = 0; jj < SLAB / 16; ++jj) {
                         const int j = hf * (SLAB / 16) + jj;
@@ -303,7 +305,6 @@ __global__ void __launch_bounds__(WM *WN * 64, WM *WN *PERCU / 4)
                             *reinterpret_cast<i32x4_t *>(
                                 stg + rr * SROW + chunk(rr, 4 * jj + q4)) = c;
                         } else {
-                            const float sx = scale_x(i);
                             const float4 sw = scale_w(j);
                             const float4 v = make_float4(i8_scaled(c[0], sx, sw.x), i8_scaled(c[1], sx, sw.y),
                                                          i8_scaled(c[2], sx, sw.z), i8_scaled(c[3], sx, sw.w));

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(ROWS_WAVES * 64) gemm_i8_rows_kernel(I8GemmArg
 #pragma unroll
         for (int w = 0; w < ROWS_WAVES; ++w)
             c += sums[(w * 16 * TM + m) * PITCH + n];
-        const float v = i8_scaled(c, i8_xs(g.xs[m]), i8_ws(g.ws[n0 + n]));
+        const float v = i8_scaled(c, i8_xs(g.xs[m]), g.ws[n0 + n]);
         T *out = static_cast<T *>(g.y) + m * g.N + n0 + n;
         if constexpr (sizeof(T) == 2)
             *out = f32_to_bf16(v);

@@ -310,15 +310,24 @@ __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *
     return s;
 }
 
-// y = c xs wscale for an int32 sum c, as (c i8_xs(xs)) i8_ws(wscale).  The scales'
-// own product would leave the range where c times it does not (1e-30 and 1e-12
-// in front of 1e7, or 1e30 and 1e9 in front of a sum of 0); with xs at 2^-24 and
-// wscale at 2^24 (exact) neither step does for 2^-102 <= xs, wscale < 2^104.
-__device__ __forceinline__ float i8_xs(float xs) { return xs * 0x1p-24f; }
-__device__ __forceinline__ float i8_ws(float ws) { return ws * 0x1p24f; }
-__device__ __forceinline__ float i8_scaled(int c, float xs, float ws)
+// y = c xs wscale for an int32 sum c, as (c xs) wscale: c xs leaves fp32's range only
+// where xs is so large that c xs wscale need not (2^97 and 2^-97 in front of 1e9), and
+// loses no bit below 2^-126, where it is a multiple of 2^-149 like xs.  (The scales' own
+// product would leave it far sooner.)  A token scale from 2^96 on is taken 2^64 smaller,
+// which the result gets back: c xs wscale is then between 2^-117 and what overflows
+// in any case, so that every finite scale gives a y that is right to its own rounding.
+// Costs one product an output (by 1, for all but such tokens).
+struct I8Scale {
+    float by, after;
+};
+__device__ __forceinline__ I8Scale i8_xs(float xs)
 {
-    return static_cast<float>(c) * xs * ws;
+    const bool big = fabsf(xs) >= 0x1p96f;
+    return {big ? xs * 0x1p-64f : xs, big ? 0x1p64f : 1.f};
+}
+__device__ __forceinline__ float i8_scaled(int c, I8Scale xs, float ws)
+{
+    return static_cast<float>(c) * xs.by * ws * xs.after;
 }
 
 }  // namespace dora

@@ -386,8 +386,10 @@ int dora_dequantize_rows(const void *q, const float *scale, int64_t rows, int64_
  * dora_linear_quantized - dora_linear in 8-bit integers, for a merged weight
  * held as 8-bit rows: one scale per token and one per output channel,
  *     y[t, i] = xs[t] wscale[i] sum_k xq[t, k] wq[i, k]
- * with exact int32 sums, scaled in fp32 (no intermediate leaves its range for
- * 2^-102 <= xs and wscale < 2^104) and rounded once to `dtype` (the type of y).  xq [T, d_in], wq [d_out, d_in] int8, xs [T], wscale [d_out] fp32.
+ * with exact int32 sums, scaled in fp32 (the scales may be any fp32 numbers: no
+ * intermediate leaves the range where y does not) and rounded once to `dtype`
+ * (the type of y).  xq [T, d_in], wq [d_out, d_in] int8, xs [T], wscale [d_out]
+ * fp32.
  * d_in <= 131071 (beyond, int32 sums could overflow).  y must not overlap any
  * input.  ws: dora_linear_quantized_workspace(T, d_in, d_out, dtype) bytes
  * (0: ws may be NULL).
