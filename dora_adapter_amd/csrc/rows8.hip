@@ -115,6 +115,23 @@ __device__ __forceinline__ void quantize_held(F &&value, int k0, int d, int grou
     }
 }
 
+// 1 / sqrt(ss / d + eps) of a row whose squares sum to ss (the same in every thread).
+// The squares leave fp32's range long before h and rstd do (overflow from 2^64 on,
+// lost bits below 2^-50 where eps is as small): such a row's are summed again, of
+// k h with a power of two k that puts them inside (every |h| < 2^128, d < 2^31: k h to
+// 2^48; the mean below 2^-100: k h to 2^56, denormal h from 2^-59 on), and the root
+// gets it back.  rstd is a number for rows whose root mean square lies from 2^-127 to
+// the largest value (denormal from 2^126 on).
+template <typename F>
+__device__ __forceinline__ float rstd_of(float ss, float d, float eps, F &&sum_squares_of)
+{
+    const float ms = ss / d + eps;
+    if (ms >= 0x1p-100f && ms < __builtin_inff())
+        return 1.f / sqrtf(ms);
+    const float k = ms > 1.f ? 0x1p-80f : 0x1p90f;
+    return k / sqrtf(sum_squares_of(k) / d + eps * k * k);
+}
+
 // Rows of any width: every pass reads the row again.  A thread meets the same
 // columns in each pass and writes them only in the last, so that h may be x
 // or the residual, and y may be x.
@@ -129,18 +146,20 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_kernel(NormArgs a)
     const int64_t vecs = ((a.d + 7) / 8 + 63) / 64 * 64;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * a.d;
-        float ss = 0.f;
-        for (int64_t v = threadIdx.x; v < vecs; v += ROW_THREADS) {
-            const int cnt = count8(a.d, v * 8);
-            const Raw8<T> h = load_h<T>(a, row + v * 8, cnt);
-            float f[8];
-            h.get(f);
+        auto sum_squares = [&](float k) {
+            float ss = 0.f;
+            for (int64_t v = threadIdx.x; v < vecs; v += ROW_THREADS) {
+                const int cnt = count8(a.d, v * 8);
+                const Raw8<T> h = load_h<T>(a, row + v * 8, cnt);
+                float f[8];
+                h.get(f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                ss = __fmaf_rn(f[q], f[q], ss);
-        }
-        ss = block_sum(ss, red, ROW_WAVES);
-        const float rstd = 1.f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+                for (int q = 0; q < 8; ++q)
+                    ss = __fmaf_rn(k * f[q], k * f[q], ss);
+            }
+            return block_sum(ss, red, ROW_WAVES);
+        };
+        const float rstd = rstd_of(sum_squares(1.f), static_cast<float>(a.d), a.eps, sum_squares);
         if (a.rstd != nullptr && threadIdx.x == 0)
             a.rstd[t] = rstd;
         float s = 0.f;
@@ -214,7 +233,18 @@ __global__ void __launch_bounds__(1024) rmsnorm_held_kernel(NormArgs a)
             ss = __fmaf_rn(f[q], f[q], ss);
     }
     ss = block_sum(ss, red, waves);
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(d) + a.eps);
+    const float rstd = rstd_of(ss, static_cast<float>(d), a.eps, [&](float k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float f[8];
+            h[i].get(f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                sum = __fmaf_rn(k * f[q], k * f[q], sum);
+        }
+        return block_sum(sum, red, waves);
+    });
     if (a.rstd != nullptr && threadIdx.x == 0)
         a.rstd[blockIdx.x] = rstd;
     auto value = [&](int i, float (&y)[8]) {

@@ -345,7 +345,8 @@ int dora_forward_noalloc(const void *x, const void *W, const void *A, const void
  *     rstd = 1 / sqrt(mean_j h_j^2 + eps)          of the rounded h, in fp32
  *     y    = w (.) h rstd   in fp32, rounded once to `dtype` (y), and / or
  *            held as 8-bit rows (q, scale) taken from the unrounded y
- *   x, residual (nullable) [T, d], w [d] in `dtype`; eps finite, >= 0.
+ *   x, residual (nullable) [T, d], w [d] in `dtype`; eps finite, >= 0.  Rows of
+ *   any magnitude: squares that leave fp32's range are summed scaled.
  *   y [T, d], h [T, d] in `dtype`, rstd [T] fp32, q [T, d] int8 with scale
  *   [T, groups] fp32: each NULL to skip, but y or q is required and q needs
  *   scale.  h may be x or residual itself, y may be x itself; no other
