@@ -271,9 +271,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_held_kernel(NormArgs a)
 }
 
 // The gradient with respect to h:
-//   dx = dres + rstd (w dy) - h rstd^3 / d * sum_j w_j dy_j h_j
+//   dx = dres + rstd (w dy - hat * mean_j(w_j dy_j hat_j)),  hat = h rstd
 // (dres: the gradient that reaches h along the residual stream).  dx may be
-// dres.
+// dres.  Every h meets rstd first: hat is of the order of one, where sums of
+// w dy h, and rstd^3, leave fp32's range for rows of 2^-43 or 2^43 already.
 template <typename T>
 __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
 {
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
     const int64_t vecs = (a.d + 7) / 8;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * a.d;
+        const float rstd = a.rstd[t];
         float dot = 0.f;
         for (int64_t v = threadIdx.x; v < vecs; v += ROW_THREADS) {
             const int cnt = count8(a.d, v * 8);
@@ -295,11 +297,9 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
             wr.get(wv);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                dot = __fmaf_rn(wv[q] * g[q], h[q], dot);
+                dot = __fmaf_rn(wv[q] * g[q], h[q] * rstd, dot);
         }
-        dot = block_sum(dot, red, ROW_WAVES);
-        const float rstd = a.rstd[t];
-        const float c = -(dot / static_cast<float>(a.d)) * rstd * rstd * rstd;
+        const float mean = block_sum(dot, red, ROW_WAVES) / static_cast<float>(a.d);
         for (int64_t v = threadIdx.x; v < vecs; v += ROW_THREADS) {
             const int cnt = count8(a.d, v * 8);
             Raw8<T> hr, gr, wr, rr;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(ROW_THREADS) rmsnorm_dx_kernel(NormGradArgs a)
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                o[q] += __fmaf_rn(c, h[q], rstd * (wv[q] * g[q]));
+                o[q] += rstd * __fmaf_rn(-mean, h[q] * rstd, wv[q] * g[q]);
             rr.set(o);
             rr.store(static_cast<T *>(a.dx) + row + v * 8, cnt);
         }
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_held_kernel(NormGradArgs a)
             w[i].get(wv);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                dot = __fmaf_rn(wv[q] * g[q], h[q], dot);
+                dot = __fmaf_rn(wv[q] * g[q], h[q] * cur.rstd, dot);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (PRE && tn < a.T)
@@ -440,13 +440,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_held_kernel(NormGradArgs a)
             for (int k = 1; k < waves; ++k)
                 dot += red[par][k];
         }
-        const float c = -(dot * inv_d) * cur.rstd * cur.rstd * cur.rstd;
+        const float mean = dot * inv_d;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if constexpr (LDW) {
-                forget(cur.h[i]);
-                forget(cur.g[i]);
-            }
+            // (what the dot product made of them would not leave the registers else)
+            forget(cur.h[i]);
+            forget(cur.g[i]);
             float h[8], g[8], wv[8], o[8];
             cur.h[i].get(h);
             cur.g[i].get(g);
@@ -460,7 +459,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_held_kernel(NormGradArgs a)
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                o[q] += __fmaf_rn(c, h[q], cur.rstd * (wv[q] * g[q]));
+                o[q] += cur.rstd * __fmaf_rn(-mean, h[q] * cur.rstd, wv[q] * g[q]);
             if constexpr (LDW) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {

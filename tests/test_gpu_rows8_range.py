@@ -61,6 +61,35 @@ def test_rmsnorm_of_small_and_large_rows(T, d, dt):
         within(o["q"].cpu().double() * s, y, s / 2 + y.abs() * Ey + 2.0 ** -126, f"q scale, 2^{e}")
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,d", SHAPES)
+def test_rmsnorm_gradient_of_small_and_large_rows(T, d, dt):
+    """dx and dw from h of 2^e and dy of 2^f: sums whose terms leave fp32's range
+    before they meet rstd, coefficients that leave it before they meet h."""
+    for e, f in ((-100, 0), (-65, 0), (-65, 40), (-65, -100), (0, 100), (64, 60), (100, 60), (100, 0),
+                 (40, -100), (-40, 80)):
+        h, w, dy, dres, scale = rows(T, d, e, dt, T + d)
+        dy = (dy * 2.0 ** f).to(dt)
+        rstd = R.norm(h, w, 0.0)[1].float()
+        # the stream's gradient, of dx's own magnitude
+        dres = (dres * 2.0 ** f / scale).to(dt)
+        for res in (None, dres):
+            say("rmsnorm backward", T, d, dt, "h of 2^%d, dy of 2^%d" % (e, f), res is not None)
+            o = D.dora_rmsnorm_backward(*[t.to(DEV) for t in (dy, h, w, rstd)],
+                                        dres=None if res is None else res.to(DEV))
+            dx, dw, dot, each = R.norm_grad(dy, h, w, rstd, res)
+            r = rstd.double()[:, None]
+            terms = (w.double() * dy.double()).abs() * r
+            if res is not None:
+                terms = terms + res.double().abs()
+            bound = (dx.abs() * half(dt) + 8 * U * terms
+                     + h.double().abs() * r ** 3 / d * dot * ((d / 64 + 64) * U + 8 * U))
+            tiny = 2.0 ** -133 if dt == BF else 2.0 ** -148
+            # (a term's own denormal step meets rstd: of rows of 2^e, 2^-e of it)
+            within(o["dx"], dx, bound * (1 + 1e-6) + tiny + 2.0 ** -148 * r, f"dx, 2^{e}, 2^{f}")
+            within(o["dw"], dw, (T + 8) * U * each + T * 2.0 ** -148, f"dw, 2^{e}, 2^{f}")
+
+
 def test_zero_rows_and_infinities_as_before():
     x = torch.zeros(4, 300)
     x[1, 5] = float("inf")
