@@ -24,6 +24,8 @@
 #include "epilogue.hpp"
 #include "gemm_bf16_dma.hpp"
 
+#include <type_traits>
+
 namespace dora {
 namespace {
 
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
         float4 a[STEP], b[STEP];
     } regs[AHEAD];
     const bool inside = m0 + BM <= g.M && n0 + BN <= g.N;
-    // the loads of step s (a granule past the split's end: its last one again, so
+    // the loads of step s (granules past the split's end: its last one again, so
     // that every step has the same number of loads in flight; none in a lone step)
     auto fetch = [&](Regs &r, int64_t s) {
 #pragma unroll
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
     int at = 0;
     // One barrier a step (a wave past it is done with the other buffer), bare:
     // __syncthreads would wait for the loads in flight as well.
-    auto step = [&](Regs &r, int64_t s, bool more) {
+    auto step = [&](Regs &r, int64_t s, auto more) {
         float *const As = lds + at * (AF + BF), *const Bs = As + AF;
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
         }
         dma::wait_lgkm0();
         dma::stage_barrier();
-        if (more)
+        if constexpr (decltype(more)::value)
             fetch(r, s + AHEAD * STEP);
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
@@ -191,24 +193,28 @@ __global__ void __launch_bounds__(NT) gemm_f32_kernel(GemmArgs g)
         }
         at ^= 1;
     };
-    const int64_t steps = s_begin < s_end ? (s_end - s_begin + STEP - 1) / STEP : 0;
-    auto at_step = [&](int64_t i) { return s_begin + i * STEP; };
-#pragma unroll
-    for (int p = 0; p < AHEAD; ++p)
-        if (p < steps)
-            fetch(regs[p], at_step(p));
-    int64_t i = 0;
-    for (; i + 2 * AHEAD <= steps; i += AHEAD) {
+    if (s_begin + AHEAD * STEP < s_end) {
 #pragma unroll
         for (int p = 0; p < AHEAD; ++p)
-            step(regs[p], at_step(i + p), true);
-    }
-    // the last steps load nothing that is not used (the epilogue's barrier would
-    // wait for it, which a product of one or two steps feels)
+            fetch(regs[p], s_begin + p * STEP);
+        for (int64_t s = s_begin; s < s_end; s += AHEAD * STEP) {
 #pragma unroll
-    for (int p = 0; p < 2 * AHEAD - 1; ++p)
-        if (i + p < steps)
-            step(regs[p % AHEAD], at_step(i + p), i + p + AHEAD < steps);
+            for (int p = 0; p < AHEAD; ++p)
+                if (s + p * STEP < s_end)
+                    step(regs[p], s + p * STEP, std::true_type{});
+        }
+    } else {
+        // few steps: no loads but theirs (the epilogue's barrier would wait for more:
+        // a norm of 16 x 16, r 2, 21 us with them, 15 without)
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+            if (s_begin + p * STEP < s_end)
+                fetch(regs[p], s_begin + p * STEP);
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p)
+            if (s_begin + p * STEP < s_end)
+                step(regs[p], s_begin + p * STEP, std::false_type{});
+    }
 
     if constexpr (ROWSQ) {
         if (g.rowsq != nullptr && tn == 0 && tid < BM && m0 + tid < g.M)
