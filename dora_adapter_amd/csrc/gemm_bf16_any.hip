@@ -27,6 +27,8 @@
 #include "gemm_bf16_dma.hpp"
 #include "ragged.hpp"
 
+#include <type_traits>
+
 namespace dora {
 namespace {
 
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
     int at = 0;
     // One barrier a step (a wave past it is done with the other buffer), bare:
     // __syncthreads would wait for the loads in flight as well.
-    auto step = [&](Regs &r, int64_t s) {
+    auto step = [&](Regs &r, int64_t s, auto more) {
         const bool one = s < st1;
         const GemmSeg &sg = one ? g.seg[0] : g.seg[1];
         const int64_t k0 = (one ? s : s - st1) * BK;
@@ -250,7 +252,8 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
         OB::store(Bs, r.b, g.N, n0, tid);
         dma::wait_lgkm0();
         dma::stage_barrier();
-        load(r, s + AHEAD);
+        if constexpr (decltype(more)::value)
+            load(r, s + AHEAD);
 #pragma unroll
         for (int h = 0; h < BK / 32; ++h) {
             const int c = h * 4 + (lane >> 4);
@@ -270,7 +273,11 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
         }
         at ^= 1;
     };
-    if (s_begin < s_end) {
+    if (s_begin + 1 == s_end) {
+        // (no load but this step's: the epilogue's barrier would wait for more)
+        load(regs[0], s_begin);
+        step(regs[0], s_begin, std::false_type{});
+    } else if (s_begin < s_end) {
 #pragma unroll
         for (int p = 0; p < AHEAD; ++p)
             load(regs[p], s_begin + p);
@@ -278,12 +285,12 @@ __global__ void __launch_bounds__(NT, 2) gemm_bf16_any_kernel(GemmArgs g)
         for (; s + AHEAD <= s_end; s += AHEAD) {
 #pragma unroll
             for (int p = 0; p < AHEAD; ++p)
-                step(regs[p], s + p);
+                step(regs[p], s + p, std::true_type{});
         }
 #pragma unroll
         for (int p = 0; p < AHEAD - 1; ++p)
             if (s + p < s_end)
-                step(regs[p], s + p);
+                step(regs[p], s + p, std::true_type{});
     }
 
     if constexpr (ROWSQ) {
