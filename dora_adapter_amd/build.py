@@ -22,7 +22,8 @@ SOURCES = [("gemm_bf16.hip", (), "gemm_bf16"), ("gemm_bf16_any.hip", (), "gemm_b
            ("gemm_f32.hip", (), "gemm_f32"),
            ("elementwise.hip", (), "elementwise"), ("dora_api.cpp", (), "dora_api"),
            ("noalloc.hip", (), "noalloc"),
-           ("rows8.hip", (), "rows8"), ("gemm_i8.hip", (), "gemm_i8"),
+           ("rows8.hip", (), "rows8"), ("gemm_rows8.hip", (), "gemm_rows8"),
+           ("gemm_i8.hip", (), "gemm_i8"),
            ("gemm_i8_dma.hip", (), "gemm_i8_dma"), ("gemm_i8_rows.hip", (), "gemm_i8_rows")] + \
           [("gemm_dma_cfg.hip", (f"-DDORA_DMA_CFG={k}",), f"gemm_dma_cfg{k}") for k in range(8)]
 # Measurement helper for bench.py (not part of the DoRA library): the HBM

@@ -389,11 +389,15 @@ struct BwdPlan {
     bool fused_dhdm;
     int64_t sweep;  // rows per sweep of the dh/dm pass
     int nchunks;    // dm partial sums per column
-    size_t o_dh, o_dmpart, o_Q, o_Qpart, o_dxpart, o_dBpart, o_dApart;
+    // dA from x's int8 rows: Q kept in fp32 too, dA always in slots (dA unused)
+    bool x8;
+    Rows8Plan dA8;
+    size_t o_dh, o_dmpart, o_Q, o_Qpart, o_Qf, o_dxpart, o_dBpart, o_dApart;
     size_t bytes;
 };
 
-BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype, bool y8 = false)
+BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype, bool y8 = false,
+                      bool x8 = false)
 {
     const bool bf = dtype == DORA_BF16;
     BwdPlan b;
@@ -429,10 +433,14 @@ BwdPlan plan_backward(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dty
     b.o_dh = cv.take(static_cast<size_t>(T) * d_out * e);
     b.o_dmpart = cv.take(static_cast<size_t>(std::max(b.nchunks, 1)) * d_out * 4);
     b.o_Q = cv.take(static_cast<size_t>(T) * r * e);
-    b.o_Qpart = cv.take(b.q.splits > 1 ? static_cast<size_t>(b.q.splits) * T * r * 4 : 0);
+    b.x8 = x8;
+    b.dA8 = x8 ? plan_rows8(T, r, d_in) : Rows8Plan{};
+    b.o_Qpart = cv.take(b.q.splits > 1 || x8 ? static_cast<size_t>(b.q.splits) * T * r * 4 : 0);
+    b.o_Qf = cv.take(static_cast<size_t>(T) * b.dA8.ldq * 4);
     b.o_dxpart = cv.take(b.dx.splits > 1 ? static_cast<size_t>(b.dx.splits) * T * d_in * 4 : 0);
     b.o_dBpart = cv.take(b.dB.splits > 1 ? static_cast<size_t>(b.dB.splits) * d_out * r * 4 : 0);
-    b.o_dApart = cv.take(b.dA.splits > 1 ? static_cast<size_t>(b.dA.splits) * r * d_in * 4 : 0);
+    const int dA_slots = x8 ? b.dA8.splits : (b.dA.splits > 1 ? b.dA.splits : 0);
+    b.o_dApart = cv.take(static_cast<size_t>(dA_slots) * r * d_in * 4);
     b.bytes = cv.off;
     return b;
 }
@@ -452,15 +460,18 @@ struct ThruPlan {
 };
 
 ThruPlan plan_through_norm(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype,
-                           bool y8 = false)
+                           bool y8 = false, bool x8 = false)
 {
     const bool bf = dtype == DORA_BF16;
     ThruPlan p;
-    p.b = plan_backward(T, d_in, d_out, r, dtype, y8);
+    p.b = plan_backward(T, d_in, d_out, r, dtype, y8, x8);
     p.g = plan_gemm(bf, nt_shape(r, r, d_in), r * r);
-    p.da = plan_gemm(bf, GemmShape{r, d_in, {T, d_out}, 2, 2,
-                                   dma_mn_operand(T, r) && dma_mn_operand(T, d_in) &&
-                                       dma_mn_operand(d_out, r) && dma_mn_operand(d_out, d_in)},
+    // (x in 8 bits: cB^T W alone)
+    const bool w_ok = dma_mn_operand(d_out, r) && dma_mn_operand(d_out, d_in);
+    p.da = plan_gemm(bf,
+                     x8 ? GemmShape{r, d_in, {d_out, 0}, 1, 2, w_ok}
+                        : GemmShape{r, d_in, {T, d_out}, 2, 2,
+                                    dma_mn_operand(T, r) && dma_mn_operand(T, d_in) && w_ok},
                      r * d_in);
     p.gs = plan_gemm(bf, GemmShape{r, r, {d_out, 0}, 1, 2, dma_mn_operand(d_out, r)}, r * r);
     p.z = plan_gemm(bf, GemmShape{r, d_in, {r, r}, bf ? 2 : 1, 1,
@@ -470,7 +481,7 @@ ThruPlan plan_through_norm(int64_t T, int64_t d_in, int64_t d_out, int64_t r, in
     p.y2 = plan_gemm(bf, GemmShape{d_out, r, {r, r}, bf ? 2 : 1, 1,
                                    dma_operand(d_out, r) && dma_mn_operand(r, r)},
                      d_out * r);
-    p.na = p.da.splits + p.z.splits;
+    p.na = p.b.dA8.splits + p.da.splits + p.z.splits;
     p.nb = p.b.dB.splits;
     p.ny = p.y1.splits + p.y2.splits;
     Carve cv;
@@ -667,12 +678,38 @@ int run_dhdm_dB(const BwdPlan &b, const void *dy, const void *y, const float *m,
     return DORA_OK;
 }
 
-// y held as 8-bit rows.
+// x or y held as 8-bit rows.
 struct Rows8 {
     const int8_t *q;
     const float *scale;
     int group;
 };
+
+// Q = s dh B in bf16 (and in fp32 where dA is formed from x's int8 rows).
+int run_Q(const BwdPlan &p, bool bf, const void *dh, const void *B, float s, int64_t T, int64_t d_out,
+          int64_t r, char *w, hipStream_t st)
+{
+    void *Q = w + p.o_Q;
+    float *part = reinterpret_cast<float *>(w + p.o_Qpart);
+    const GemmArgs g = seg1(T, r, dh, d_out, B, r, d_out);
+    if (!p.x8)
+        return run_store(bf, p.q, g, 1, Q, r, s, part, st, "Q = s dh B");
+    DORA_CHECK(run_slots(bf, p.q, g, 1, part, 1.0f, st, "Q = s dh B"));
+    DORA_LAUNCH(launch_q_rows8(part, p.q.splits, T, r, p.dA8.ldq, s, Q,
+                               reinterpret_cast<float *>(w + p.o_Qf), st),
+                "Q in both types");
+    return DORA_OK;
+}
+
+// The fp32 slots of Q^T x from x's int8 rows.
+int run_dA8(const BwdPlan &p, const Rows8 &x8, int64_t T, int64_t d_in, int64_t r, char *w,
+            float *slots, hipStream_t st)
+{
+    const Rows8Args g{reinterpret_cast<const float *>(w + p.o_Qf), p.dA8.ldq, x8.q, x8.scale,
+                      x8.group, T, r, d_in, p.dA8.t_per_split, slots};
+    DORA_LAUNCH(launch_gemm_rows8(g, p.dA8.splits, st), "dA from 8 bits");
+    return DORA_OK;
+}
 
 // The separate dh/dm pass, from y or from its 8-bit rows.
 int run_dhdm(bool bf16, const void *dy, const void *y, const Rows8 *y8, const float *m,
@@ -699,11 +736,12 @@ int finish_dm(const Rows8 *y8, const float *dmpart, int nchunks, const float *m,
     return DORA_OK;
 }
 
-// dora_backward after its checks (y8 set: y is not read).
-int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W, const void *A,
-                  const void *B, const float *m, const float *n, float s, const void *P,
-                  const void *y, const Rows8 *y8, int64_t T, int64_t d_in, int64_t d_out, int64_t r,
-                  int dtype, void *dx, void *dA, void *dB, float *dm, void *ws, void *stream)
+// dora_backward after its checks (y8 set: y is not read; p.x8: x8 in x's place).
+int backward_impl(const BwdPlan &p, const void *dy, const void *x, const Rows8 *x8, const void *W,
+                  const void *A, const void *B, const float *m, const float *n, float s,
+                  const void *P, const void *y, const Rows8 *y8, int64_t T, int64_t d_in,
+                  int64_t d_out, int64_t r, int dtype, void *dx, void *dA, void *dB, float *dm,
+                  void *ws, void *stream)
 {
     const bool bf = dtype == DORA_BF16;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -726,8 +764,7 @@ int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W
     }
     DORA_CHECK(finish_dm(y8, dmpart, p.nchunks, m, d_out, dm, st));
     // 2. Q = s dh B  (A K-major, B MN-major).
-    DORA_CHECK(run_store(bf, p.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
-                         reinterpret_cast<float *>(w + p.o_Qpart), st, "Q = s dh B"));
+    DORA_CHECK(run_Q(p, bf, dh, B, s, T, d_out, r, w, st));
     // 3. dx = [dh | Q] [W ; A]  (K-concatenated segments, B MN-major).
     {
         GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
@@ -741,14 +778,21 @@ int backward_impl(const BwdPlan &p, const void *dy, const void *x, const void *W
         DORA_CHECK(run_store(bf, p.dB, seg1(d_out, r, dh, d_out, P, r, T), 2, dB, r, s,
                              reinterpret_cast<float *>(w + p.o_dBpart), st, "dB"));
     // 5. dA = Q^T x  (both MN-major, K = T).
+    if (p.x8) {
+        float *part = reinterpret_cast<float *>(w + p.o_dApart);
+        DORA_CHECK(run_dA8(p, *x8, T, d_in, r, w, part, st));
+        DORA_LAUNCH(launch_splitk_reduce(bf, part, p.dA8.splits, r, d_in, 1.0f, dA, st), "dA");
+        return DORA_OK;
+    }
     DORA_CHECK(run_store(bf, p.dA, seg1(r, d_in, Q, r, x, d_in, T), 2, dA, d_in, 1.0f,
                          reinterpret_cast<float *>(w + p.o_dApart), st, "dA"));
     return DORA_OK;
 }
 
-// dora_backward_through_norm after its checks (y8 set: y is not read).
-int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const void *W,
-                      const void *A, const void *B, const float *m, const float *n, float s,
+// dora_backward_through_norm after its checks (y8 set: y is not read; p.b.x8: x8 in x's
+// place).
+int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const Rows8 *x8,
+                      const void *W, const void *A, const void *B, const float *m, const float *n, float s,
                       const void *P, const void *y, const Rows8 *y8, const float *U, int64_t T,
                       int64_t d_in, int64_t d_out, int64_t r, int dtype, void *dx, void *dA,
                       void *dB, float *dm, void *ws, void *stream)
@@ -775,8 +819,7 @@ int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const vo
     else
         DORA_CHECK(run_dhdm(bf, dy, y, y8, m, n, T, d_out, b.sweep, dh, dmpart, st));
     DORA_CHECK(finish_dm(y8, dmpart, b.nchunks, m, d_out, dm, st));
-    DORA_CHECK(run_store(bf, b.q, seg1(T, r, dh, d_out, B, r, d_out), 1, Q, r, s,
-                         reinterpret_cast<float *>(w + b.o_Qpart), st, "Q = s dh B"));
+    DORA_CHECK(run_Q(b, bf, dh, B, s, T, d_out, r, w, st));
     {
         GemmArgs g = seg1(T, d_in, dh, d_out, W, d_in, d_out);
         g.seg[1] = GemmSeg{Q, r, A, d_in, r};
@@ -786,15 +829,20 @@ int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const vo
     }
     // 4. The norm's row coefficient cs = -s m dm / n^2 and cB = cs (.) B.
     DORA_LAUNCH(launch_norm_grad_coef(bf, m, dm, n, s, B, d_out, r, cs, cB, st), "norm grad coef");
-    // 5. dA = [Q^T | cB^T] [x ; W] + s (cB^T B) A.
+    // 5. dA = [Q^T | cB^T] [x ; W] + s (cB^T B) A  (x in 8 bits: Q^T x in slots of its own).
     {
+        const int nx = b.dA8.splits;  // slots of Q^T x, then of the rest
+        float *wslots = aslots + static_cast<size_t>(nx) * r * d_in;
+        float *zslots = wslots + static_cast<size_t>(p.da.splits) * r * d_in;
         GemmArgs g = seg1(r, d_in, cB, r, W, d_in, d_out);
-        if (T > 0) {
+        if (b.x8) {
+            DORA_CHECK(run_dA8(b, *x8, T, d_in, r, w, aslots, st));
+        } else if (T > 0) {
             g.seg[1] = g.seg[0];
             g.seg[0] = GemmSeg{Q, r, x, d_in, T};
             g.nseg = 2;
         }
-        DORA_CHECK(run_slots(bf, p.da, g, 2, aslots, 1.0f, st, "dA: Q^T x + cB^T W"));
+        DORA_CHECK(run_slots(bf, p.da, g, 2, wslots, 1.0f, st, "dA: Q^T x + cB^T W"));
         float *gspart = reinterpret_cast<float *>(w + p.o_gspart);
         char *gs = w + p.o_gsfin;
         DORA_CHECK(run_slots(bf, p.gs, seg1(r, r, cB, r, B, r, d_out), 2, gspart, 1.0f, st,
@@ -805,11 +853,9 @@ int through_norm_impl(const ThruPlan &p, const void *dy, const void *x, const vo
             z.seg[1] = GemmSeg{gs + gsz, r, A, d_in, r};
             z.nseg = 2;
         }
-        DORA_CHECK(run_slots(bf, p.z, z, 1, aslots + static_cast<size_t>(p.da.splits) * r * d_in,
-                             s, st, "dA: s (cB^T B) A"));
-        DORA_LAUNCH(launch_combine_rows(bf, aslots, p.da.splits,
-                                        aslots + static_cast<size_t>(p.da.splits) * r * d_in,
-                                        p.z.splits, nullptr, r, d_in, dA, st),
+        DORA_CHECK(run_slots(bf, p.z, z, 1, zslots, s, st, "dA: s (cB^T B) A"));
+        DORA_LAUNCH(launch_combine_rows(bf, aslots, nx + p.da.splits, zslots, p.z.splits, nullptr, r,
+                                        d_in, dA, st),
                     "dA combine");
     }
     // 6. dB = s dh^T P + cs (.) V A^T,  V A^T = W A^T + s B G,  G = A A^T.
@@ -1662,7 +1708,7 @@ int dora_backward(const void *dy, const void *x, const void *W, const void *A, c
          {{A, r * d_in * e}, "A"}, {{B, d_out * r * e}, "B"}, {{m, d_out * sizeof(float)}, "m"},
          {{n, d_out * sizeof(float)}, "n"}, {{P, T * r * e}, "P"}, {{y, T * d_out * e}, "y"}}));
 
-    return backward_impl(p, dy, x, W, A, B, m, n, s, P, y, nullptr, T, d_in, d_out, r, dtype, dx, dA,
+    return backward_impl(p, dy, x, nullptr, W, A, B, m, n, s, P, y, nullptr, T, d_in, d_out, r, dtype, dx, dA,
                          dB, dm, ws, stream);
 }
 
@@ -1700,7 +1746,7 @@ int dora_backward_through_norm(const void *dy, const void *x, const void *W, con
          {{n, d_out * sizeof(float)}, "n"}, {{P, T * r * e}, "P"}, {{y, T * d_out * e}, "y"},
          {{U, d_out * r * sizeof(float)}, "U"}}));
 
-    return through_norm_impl(p, dy, x, W, A, B, m, n, s, P, y, nullptr, U, T, d_in, d_out, r, dtype,
+    return through_norm_impl(p, dy, x, nullptr, W, A, B, m, n, s, P, y, nullptr, U, T, d_in, d_out, r, dtype,
                              dx, dA, dB, dm, ws, stream);
 }
 
@@ -2096,31 +2142,38 @@ int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const
     return DORA_OK;
 }
 
-// The backward from 8-bit checkpoints: x restored into the workspace (the
-// product that reads it takes matrices of the element type), y read in 8 bits
-// by the dh/dm pass.
+// The backward from 8-bit checkpoints: y is read in 8 bits by the dh/dm pass, and so is
+// x by a bf16 module's dA product where a tile's columns share a scale.  Otherwise x
+// is restored into the workspace, rounded to the element type, and dA is what
+// dora_backward makes of that x, bit for bit (bf16: 0.0032 of its norm off, 0.0023
+// where x is read in 8 bits).
 namespace {
 struct CkptPlan {
+    bool x8;
     BwdPlan b;
     ThruPlan t;
     size_t o_x, o_bwd, bytes;
 };
 
 CkptPlan plan_checkpoint(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype,
-                         int through_norm)
+                         int through_norm, bool x8)
 {
     CkptPlan p;
     Carve cv;
-    p.o_x = cv.take(static_cast<size_t>(T) * d_in * esize(dtype));
+    p.x8 = x8;
+    p.o_x = cv.take(x8 ? 0 : static_cast<size_t>(T) * d_in * esize(dtype));
     p.o_bwd = cv.off;
     if (through_norm)
-        p.t = plan_through_norm(T, d_in, d_out, r, dtype, true);
+        p.t = plan_through_norm(T, d_in, d_out, r, dtype, true, x8);
     else
-        p.b = plan_backward(T, d_in, d_out, r, dtype, true);
+        p.b = plan_backward(T, d_in, d_out, r, dtype, true, x8);
     cv.take(through_norm ? p.t.bytes : p.b.bytes);
     p.bytes = cv.off;
     return p;
 }
+
+// Whether dA reads x's rows in 8 bits: bf16 modules, one scale for a tile's columns.
+bool reads_x8(int dtype, int64_t group) { return dtype == DORA_BF16 && group % ROWS8_TILE == 0; }
 }  // namespace
 
 size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
@@ -2128,7 +2181,11 @@ size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out
 {
     if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, r))
         return 0;
-    return plan_checkpoint(T, d_in, d_out, r, dtype, through_norm).bytes;
+    // of any group
+    size_t need = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, false).bytes;
+    if (reads_x8(dtype, 0))
+        need = std::max(need, plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, true).bytes);
+    return need;
 }
 
 int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, const void *W,
@@ -2150,12 +2207,13 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
                            {P, "P", has_t}, {yq, "yq", has_t}, {ys, "ys", has_t},
                            {dx, "dx", has_t}, {dA, "dA", true}, {dB, "dB", true},
                            {dm, "dm", true}, {U, "U", false}}));
-    const CkptPlan p = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm);
-    DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
+    const CkptPlan p = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, reads_x8(dtype, group));
+    const size_t need = dora_backward_checkpoint_workspace(T, d_in, d_out, r, dtype, through_norm);
+    DORA_CHECK(check_ws(ws, ws_bytes, need));
     const size_t e = esize(dtype);
     DORA_CHECK(check_disjoint(
         {{{dx, T * d_in * e}, "dx"}, {{dA, r * d_in * e}, "dA"}, {{dB, d_out * r * e}, "dB"},
-         {{dm, d_out * sizeof(float)}, "dm"}, {{ws, p.bytes}, "workspace"}},
+         {{dm, d_out * sizeof(float)}, "dm"}, {{ws, need}, "workspace"}},
         {{{dy, T * d_out * e}, "dy"}, {{xq, static_cast<size_t>(T) * d_in}, "xq"},
          {{xs, scale_bytes(T, d_in, group)}, "xs"}, {{W, d_out * d_in * e}, "W"},
          {{A, r * d_in * e}, "A"}, {{B, d_out * r * e}, "B"}, {{m, d_out * sizeof(float)}, "m"},
@@ -2165,14 +2223,15 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool bf = dtype == DORA_BF16;
     char *w = static_cast<char *>(ws);
-    DORA_LAUNCH(launch_dequantize_rows(bf, static_cast<const int8_t *>(xq), xs, T, d_in,
-                                       static_cast<int>(group), w + p.o_x, st),
-                "restore x");
+    const Rows8 x8{static_cast<const int8_t *>(xq), xs, static_cast<int>(group)};
     const Rows8 y8{static_cast<const int8_t *>(yq), ys, static_cast<int>(group)};
+    if (!p.x8)
+        DORA_LAUNCH(launch_dequantize_rows(bf, x8.q, xs, T, d_in, x8.group, w + p.o_x, st),
+                    "restore x");
     if (through_norm)
-        return through_norm_impl(p.t, dy, w + p.o_x, W, A, B, m, n, s, P, nullptr, &y8, U, T, d_in,
+        return through_norm_impl(p.t, dy, w + p.o_x, &x8, W, A, B, m, n, s, P, nullptr, &y8, U, T, d_in,
                                  d_out, r, dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
-    return backward_impl(p.b, dy, w + p.o_x, W, A, B, m, n, s, P, nullptr, &y8, T, d_in, d_out, r,
+    return backward_impl(p.b, dy, w + p.o_x, &x8, W, A, B, m, n, s, P, nullptr, &y8, T, d_in, d_out, r,
                          dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
 }
 

@@ -405,11 +405,13 @@ int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const
  * dora_backward_through_norm (otherwise) with the forward's x and y kept
  * between the passes as 8-bit rows, half the bytes of bf16: xq [T, d_in] with
  * xs and yq [T, d_out] with ys, both of this `group`.  The gradients are those
- * of the restored x = xq xs and y = yq ys; x is rounded to `dtype` where a
- * matrix product reads it, y enters dm in fp32.  All other arguments, layouts,
- * aliasing rules and the T = 0 case are those of the two calls.
- * ws: dora_backward_checkpoint_workspace(...) bytes, which hold x restored for
- * the duration of the call.
+ * of the restored x = xq xs and y = yq ys; y enters dm in fp32.  x enters dA in
+ * bf16 modules with group 0, 128, 256 or 512 unrounded, beside a Q = s dh B kept
+ * to 16 bits (dA is then rounded once, behind dh); with group 32 or 64, and in
+ * fp32 modules, x is rounded to `dtype` and dA is what the two calls make of it.
+ * All other arguments, layouts, aliasing rules and the T = 0 case are those of
+ * the two calls.
+ * ws: dora_backward_checkpoint_workspace(...) bytes, enough for any group.
  */
 size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
                                           int dtype, int through_norm);
