@@ -4,8 +4,9 @@
 // launch plan (tile shape and split-K per product), the workspace carve-up
 // and the launch sequences of the factored norm, the compose, the forward
 // and the norm-detached backward.  Every step of the computation runs in
-// the HIP kernels of gemm_bf16.hip, gemm_f32.hip, elementwise.hip, rows8.hip
-// and gemm_i8.hip.
+// the HIP kernels: products in gemm_bf16.hip, gemm_bf16_any.hip, gemm_dma_cfg.hip and
+// gemm_f32.hip, of int8 operands in gemm_i8.hip, gemm_i8_dma.hip, gemm_i8_rows.hip and
+// gemm_rows8.hip, the rest in elementwise.hip and rows8.hip.
 #include <stdio.h>
 #include <stdarg.h>
 #include <stdlib.h>
@@ -17,6 +18,7 @@
 
 #include "../../include/dora.h"
 #include "dora_internal.hpp"
+#include "gemm_rows8.hpp"
 
 namespace dora {
 namespace {

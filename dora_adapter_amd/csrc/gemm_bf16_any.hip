@@ -20,8 +20,8 @@
 // Most of these products are small, and a step's time is its loads' round trip:
 // 64 x 64 tiles, with AHEAD = 2 steps' loads in flight, serve where there are few
 // 128 x 128 ones (whose accumulators leave registers for one step's).  The nine
-// products of a backward through the norm, 509 tokens, 1027 -> 1411, r 37, call
-// included: 148 us, with one step ahead 170, three 155, 128 x 128 tiles alone 245.
+// products of a backward through the norm from a bf16 x, 509 tokens, 1027 -> 1411, r 37,
+// call included: 148 us, with one step ahead 170, three 155, 128 x 128 tiles alone 245.
 #include "dora_internal.hpp"
 #include "epilogue.hpp"
 #include "gemm_bf16_dma.hpp"

@@ -278,6 +278,8 @@ I8Plan plan_gemm_i8(int64_t M, int64_t N, int64_t K)
     if (dma && gemm_i8_rows_ok(M, N)) {
         p.cfg = I8Plan::ROWS;
     } else if (dma && M * N * 4 < I8_MAX_BYTES) {
+        // (four bytes an output whichever its type: a y of 1 to 2 GiB in bf16 takes the
+        // general kernel, at half the rate)
         // rounds of resident workgroups, each its items' stages; a split writes
         // and reads int32 partial sums and launches once more
         const int64_t stages = ceil_div(K, I8_STAGE_K);

@@ -18,8 +18,8 @@
 // pair's products), bound by the conversions on the way to LDS (vector ALUs busy 0.58
 // of the time, matrix cores 0.24), against 80 from an x and a Q in bf16 and 35 for
 // restoring that x: 1.3% of that backward, for 0.7 of dA's error.
-#include "dora_internal.hpp"
 #include "gemm_bf16_dma.hpp"
+#include "gemm_rows8.hpp"
 #include "rows8.hpp"
 
 namespace dora {
