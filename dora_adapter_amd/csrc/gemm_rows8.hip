@@ -1,8 +1,9 @@
 // gemm_rows8.hip - dA = Q^T x of a bf16 module's backward from x's int8 rows
 // (gfx950), with nothing rounded to bf16 on the way:
-//   dA[i, j] = sum_t (Q[t, i] xs[t, g(j)]) xq[t, j]
-// An int8 value is exact in bf16; the token's scale goes to Q, which is still in
-// fp32, and the product to a pair of bf16 (16 bits of it).  Restoring x and storing Q
+//   dA[i, j] = sum_t (Q[t, i] m) (2^e xq[t, j]),  xs[t, g(j)] = m 2^e
+// An int8 value times a power of two is exact in bf16; what the token's scale has beside
+// that, 1 to 2, goes to Q, which is still in fp32, and the product to a pair of bf16 (16
+// bits of it).  Either operand keeps its own range.  Restoring x and storing Q
 // in bf16 first, as the backward from a bf16 x does, rounds both: dA is then 0.0032
 // of its norm off against 0.0023 here, where 0.0017 is its own last rounding
 // and the rest dh's.
@@ -11,13 +12,14 @@
 // whole tiles of 128 columns.
 //
 // 64 x 128 tiles of four waves (32 x 64 each), 64 tokens a step in two LDS buffers, the
-// next step's loads in flight (two steps': 305 us where one takes 198).  Both operands
+// next step's loads in flight (two steps' took half as long again).  Both operands
 // come MN-major; a thread writes two tokens of eight columns of Q, or four of x, as
 // K-consecutive pairs.  K is split over workgroups; the fp32 sums go to slots that the
-// caller adds in order.  r 384, 8192 tokens, 8192 columns: 198 us (520 TFLOP/s of the
-// pair's products), bound by the conversions on the way to LDS (vector ALUs busy 0.58
-// of the time, matrix cores 0.24), against 80 from an x and a Q in bf16 and 35 for
-// restoring that x: 1.3% of that backward, for 0.7 of dA's error.
+// caller adds in order.  r 384, 8192 tokens, 8192 columns: 204 us (505 TFLOP/s of the
+// pair's products), bound by the conversions on the way to LDS (vector ALUs busy 0.6
+// of the time, matrix cores a quarter), against 80 from an x and a Q in bf16 and 35
+// for restoring that x: 2% of that backward, for 0.7 of dA's error.  r 37, 509 tokens,
+// 1027 columns: 7 us.
 #include "gemm_bf16_dma.hpp"
 #include "gemm_rows8.hpp"
 #include "rows8.hpp"
@@ -47,6 +49,16 @@ __device__ __forceinline__ float rest_of(float v, float hi)
     return __builtin_amdgcn_fmed3f(v - hi, -0x1p121f, 0x1p121f);
 }
 
+// A scale as a number from 1 to 2 (0, NaN and infinities: itself) times a power of two.
+__device__ __forceinline__ float mantissa(float s)
+{
+    return 2.f * __builtin_amdgcn_frexp_mantf(s);
+}
+__device__ __forceinline__ float power(float s)
+{
+    return __builtin_amdgcn_ldexpf(0.5f, __builtin_amdgcn_frexp_expf(s));
+}
+
 __global__ void __launch_bounds__(NT, 2) gemm_rows8_kernel(Rows8Args g)
 {
     __shared__ __align__(16) uint4 lds[2][2 * BM * 8 + BN * 8];  // Q's pair, x
@@ -62,15 +74,43 @@ __global__ void __launch_bounds__(NT, 2) gemm_rows8_kernel(Rows8Args g)
 
     // thread: columns 8 am .. of tokens AROWS ak .. of Q, 8 bm .. of BROWS bk .. of x
     const int am = tid & 7, ak = tid >> 3, bm = tid & 15, bk = tid >> 4;
-    const int cnt = g.d - n0 - bm * 8 < 8 ? static_cast<int>(g.d - n0 - bm * 8) : 8;
-    const bool inside = n0 + BN <= g.d;
+    // columns past the end: a row's last eight, shifted into place (past all of them: any)
+    const bool inside = n0 + BN <= g.d, tiny = g.d < 8;
+    const int64_t col = n0 + bm * 8, from = col + 8 <= g.d || tiny ? col : g.d - 8;
+    const int shift = 8 * static_cast<int>(col - from < 7 ? col - from : 7);
     struct Regs {
         float4 q[AROWS][2];
-        float s[AROWS];
+        float s[AROWS], sx[BROWS];
         Raw8i x[BROWS];
     } regs;
-    // (tokens past the end: the last one, taken as zeros of Q)
+    // offsets of the thread's rows from a step's first
+    int64_t qo[AROWS], xo[BROWS];
+#pragma unroll
+    for (int i = 0; i < AROWS; ++i)
+        qo[i] = (ak * AROWS + i) * g.ldq + m0 + am * 8;
+#pragma unroll
+    for (int i = 0; i < BROWS; ++i)
+        xo[i] = (bk * BROWS + i) * g.d + from;
     auto load = [&](int64_t k0) {
+        if (!tiny && k0 + BK <= g.T) {
+            const float *const q0 = g.q + k0 * g.ldq, *const s0 = xs + k0 * groups;
+            const int8_t *const x0 = g.xq + k0 * g.d;
+#pragma unroll
+            for (int i = 0; i < AROWS; ++i) {
+                regs.q[i][0] = reinterpret_cast<const float4 *>(q0 + qo[i])[0];
+                regs.q[i][1] = reinterpret_cast<const float4 *>(q0 + qo[i])[1];
+                regs.s[i] = s0[(ak * AROWS + i) * groups];
+            }
+#pragma unroll
+            for (int i = 0; i < BROWS; ++i) {
+                const u32x2_a1_t v = *reinterpret_cast<const u32x2_a1_t *>(x0 + xo[i]);
+                regs.x[i].w[0] = v.x;
+                regs.x[i].w[1] = v.y;
+                regs.sx[i] = s0[(bk * BROWS + i) * groups];
+            }
+            return;
+        }
+        // (tokens past the end: the last one, whose Q is then taken as zeros)
 #pragma unroll
         for (int i = 0; i < AROWS; ++i) {
             const int64_t k = k0 + ak * AROWS + i, t = k < g.T ? k : g.T - 1;
@@ -82,14 +122,15 @@ __global__ void __launch_bounds__(NT, 2) gemm_rows8_kernel(Rows8Args g)
 #pragma unroll
         for (int i = 0; i < BROWS; ++i) {
             const int64_t k = k0 + bk * BROWS + i, t = k < g.T ? k : g.T - 1;
-            const int8_t *x = g.xq + t * g.d + n0 + bm * 8;
-            if (inside) {
+            const int8_t *x = g.xq + t * g.d + from;
+            if (tiny) {
+                regs.x[i].load(x, static_cast<int>(g.d - col));
+            } else {
                 const u32x2_a1_t v = *reinterpret_cast<const u32x2_a1_t *>(x);
                 regs.x[i].w[0] = v.x;
                 regs.x[i].w[1] = v.y;
-            } else {
-                regs.x[i].load(x, cnt);
             }
+            regs.sx[i] = xs[t * groups];
         }
     };
     f32x4_t acc[2][4];
@@ -107,12 +148,27 @@ __global__ void __launch_bounds__(NT, 2) gemm_rows8_kernel(Rows8Args g)
         float v[AROWS][8];
 #pragma unroll
         for (int i = 0; i < AROWS; ++i) {
-            const bool live = k0 + ak * AROWS + i < g.T;
+            const float m = mantissa(regs.s[i]);
             const float q[8] = {regs.q[i][0].x, regs.q[i][0].y, regs.q[i][0].z, regs.q[i][0].w,
                                 regs.q[i][1].x, regs.q[i][1].y, regs.q[i][1].z, regs.q[i][1].w};
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                v[i][c] = live ? q[c] * regs.s[i] : 0.f;
+                v[i][c] = q[c] * m;
+        }
+        if (k0 + BK > g.T) {
+#pragma unroll
+            for (int i = 0; i < AROWS; ++i)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    v[i][c] = k0 + ak * AROWS + i < g.T ? v[i][c] : 0.f;
+        }
+        if (!inside && !tiny) {
+#pragma unroll
+            for (int i = 0; i < BROWS; ++i) {
+                const uint64_t x = (static_cast<uint64_t>(regs.x[i].w[1]) << 32 | regs.x[i].w[0]) >> shift;
+                regs.x[i].w[0] = static_cast<unsigned int>(x);
+                regs.x[i].w[1] = static_cast<unsigned int>(x >> 32);
+            }
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -123,10 +179,15 @@ __global__ void __launch_bounds__(NT, 2) gemm_rows8_kernel(Rows8Args g)
             reinterpret_cast<uint32_t *>(Hi + to)[ak % 4] = hi;
             reinterpret_cast<uint32_t *>(Lo + to)[ak % 4] = lo;
         }
+        float p2[BROWS];
+#pragma unroll
+        for (int i = 0; i < BROWS; ++i)
+            p2[i] = power(regs.sx[i]);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const uint2 x = make_uint2(pack_bf16x2(regs.x[0].value(c), regs.x[1].value(c)),
-                                       pack_bf16x2(regs.x[2].value(c), regs.x[3].value(c)));
+            const uint2 x = make_uint2(
+                pack_bf16x2(regs.x[0].value(c) * p2[0], regs.x[1].value(c) * p2[1]),
+                pack_bf16x2(regs.x[2].value(c) * p2[2], regs.x[3].value(c) * p2[3]));
             reinterpret_cast<uint2 *>(X + place(bm * 8 + c, bk / 2))[bk % 2] = x;
         }
         // (one barrier a step, bare: a wave past it is done with the other buffer, and

@@ -106,6 +106,17 @@ def test_scales_of_any_size_zeros_and_nan(through):
     assert torch.isfinite(got[:, :128]).all() and torch.isfinite(got[:, 256:]).all()
 
 
+@pytest.mark.parametrize("ex,eq", [(-118, 100), (-126, 60), (110, -110), (90, -100), (-60, -40), (-120, 118)])
+def test_rows_and_gradients_far_from_one(ex, eq):
+    """Scales and Q of which one is far below and the other far above one, or whose
+    product is near the smallest normal number: dA is right to its own rounding."""
+    ops = operands(300, 260, 48, 20, 128, 8)
+    ops[5] = (ops[5] / ops[5].max() * 2.0 ** ex).clamp_min(2.0 ** -126)
+    ops[0] = (ops[0].float() * 2.0 ** eq).to(BF)
+    say("dA from 8 bits, scales of 2^%d, dy of 2^%d" % (ex, eq))
+    check(ops, 1.0, 128, False, call(ops, 1.0, 128, False))
+
+
 def test_an_infinite_gradient_stays_one():
     ops = operands(70, 136, 16, 8, 0, 6)
     ops[0][3] = 3.0e38  # Q of token 3 overflows
