@@ -139,3 +139,75 @@ def test_one_workspace_for_every_group():
             assert torch.equal(a[k], b[k]), (group, k)
         if group % 128 == 0:
             check(ops, 1.0, group, False, a)
+
+
+@pytest.mark.parametrize("through", [False, True])
+def test_captured_replayed_and_on_a_second_stream(through):
+    """Replays on other inputs, with eager work between them, give the eager bits; so
+    does a call on a stream of its own beside one on another."""
+    T, d_in, d_out, r, group = 190, 270, 200, 40, 128
+    dev = [t.to(DEV) for t in operands(T, d_in, d_out, r, group, 11)]
+    dy, W, A, B, xq, xs, yq, ys = dev
+    gen = torch.Generator(DEV).manual_seed(12)
+    m = torch.rand(d_out, generator=gen, device=DEV) + 0.5
+    n = torch.rand(d_out, generator=gen, device=DEV) + 0.5
+    P = torch.randn(T, r, generator=gen, device=DEV).to(BF)
+    yq.copy_(torch.randint(-127, 128, (T, d_out), generator=gen, device=DEV, dtype=torch.int8))
+
+    def step():
+        return D.dora_backward_checkpoint(dy, xq, xs, W, A, B, m, n, 1.25, P, yq, ys, group=group,
+                                          through_norm=through)
+
+    say("dA from 8 bits, two streams", through)
+    eager = step()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for st in (a, b):
+            with torch.cuda.stream(st):
+                got.append(step())
+    torch.cuda.synchronize()
+    for o in got:
+        assert all(torch.equal(o[k], eager[k]) for k in eager)
+    say("dA from 8 bits, capture", through)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for k in range(4):
+        if k:
+            dy.copy_(torch.randn(T, d_out, generator=gen, device=DEV))
+            xq.copy_(torch.randint(-127, 128, (T, d_in), generator=gen, device=DEV, dtype=torch.int8))
+            xs.copy_(torch.rand(xs.shape, generator=gen, device=DEV))
+        say("replay", k)
+        graph.replay()
+        torch.cuda.synchronize()
+        copy = {key: v.clone() for key, v in kept.items()}
+        now = step()
+        torch.cuda.synchronize()
+        for key in now:
+            assert torch.equal(copy[key], now[key]), (k, key)
+
+
+def test_offsets_past_32_bits():
+    """2.2e9 int8 values of x; whole numbers, so that every sum is exact."""
+    T, d_in, d_out, r = 66_001, 32_776, 8, 3
+    g = torch.Generator(DEV).manual_seed(1)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g, device=DEV).to(BF)  # noqa: E731
+    dy, W, A, B, P = ints(T, d_out), ints(d_out, d_in), ints(r, d_in), ints(d_out, r), ints(T, r)
+    xq = torch.randint(-127, 128, (T, d_in), generator=g, device=DEV, dtype=torch.int8)
+    for group in (0, 128):
+        one = torch.ones(d_out, device=DEV)
+        xs = torch.ones(T, 1 if group == 0 else -(-d_in // group), device=DEV)
+        yq, ys = torch.zeros(T, d_out, dtype=torch.int8, device=DEV), torch.ones(T, 1, device=DEV)
+        say("dA from 8 bits, past 32 bits", group)
+        got = D.dora_backward_checkpoint(dy, xq, xs, W, A, B, one, one, 1.0, P, yq, ys, group=group)
+        Q = dy.cpu().double() @ B.cpu().double()
+        at = torch.tensor([0, 1, 127, 128, 16_000, d_in - 9, d_in - 8, d_in - 1])
+        want = Q.T @ xq[:, at.to(DEV)].cpu().double()
+        assert want.abs().max() < 2 ** 23
+        assert torch.equal(got["dA"][:, at.to(DEV)].cpu(), want.to(BF)), group
+        rows = torch.tensor([0, 40_000, 65_535, 65_536, T - 1])
+        full = dy[rows.to(DEV)].cpu().double() @ W.cpu().double() + Q[rows] @ A.cpu().double()
+        assert torch.equal(got["dx"][rows.to(DEV)].cpu(), full.to(BF))
+        del got
