@@ -2176,6 +2176,18 @@ CkptPlan plan_checkpoint(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int 
 
 // Whether dA reads x's rows in 8 bits: bf16 modules, one scale for a tile's columns.
 bool reads_x8(int dtype, int64_t group) { return dtype == DORA_BF16 && group % ROWS8_TILE == 0; }
+
+// The plan for this group; `need` is the workspace of any group.
+CkptPlan plan_checkpoint_group(int64_t T, int64_t d_in, int64_t d_out, int64_t r, int dtype,
+                               int through_norm, int64_t group, size_t &need)
+{
+    const bool x8 = reads_x8(dtype, group);
+    const CkptPlan p = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, x8);
+    need = p.bytes;
+    if (dtype == DORA_BF16)
+        need = std::max(need, plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, !x8).bytes);
+    return p;
+}
 }  // namespace
 
 size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out, int64_t r,
@@ -2183,10 +2195,8 @@ size_t dora_backward_checkpoint_workspace(int64_t T, int64_t d_in, int64_t d_out
 {
     if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, r))
         return 0;
-    // of any group
-    size_t need = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, false).bytes;
-    if (reads_x8(dtype, 0))
-        need = std::max(need, plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, true).bytes);
+    size_t need;
+    plan_checkpoint_group(T, d_in, d_out, r, dtype, through_norm, 0, need);
     return need;
 }
 
@@ -2209,8 +2219,8 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
                            {P, "P", has_t}, {yq, "yq", has_t}, {ys, "ys", has_t},
                            {dx, "dx", has_t}, {dA, "dA", true}, {dB, "dB", true},
                            {dm, "dm", true}, {U, "U", false}}));
-    const CkptPlan p = plan_checkpoint(T, d_in, d_out, r, dtype, through_norm, reads_x8(dtype, group));
-    const size_t need = dora_backward_checkpoint_workspace(T, d_in, d_out, r, dtype, through_norm);
+    size_t need;
+    const CkptPlan p = plan_checkpoint_group(T, d_in, d_out, r, dtype, through_norm, group, need);
     DORA_CHECK(check_ws(ws, ws_bytes, need));
     const size_t e = esize(dtype);
     DORA_CHECK(check_disjoint(
