@@ -2147,7 +2147,7 @@ int dora_linear_quantized(const void *xq, const float *xs, const void *wq, const
 // The backward from 8-bit checkpoints: y is read in 8 bits by the dh/dm pass, and so is
 // x by a bf16 module's dA product where a tile's columns share a scale.  Otherwise x
 // is restored into the workspace, rounded to the element type, and dA is what
-// dora_backward makes of that x, bit for bit (bf16: 0.0032 of its norm off, 0.0023
+// dora_backward makes of that x, bit for bit (bf16: 0.0032 of its norm off, 0.0024
 // where x is read in 8 bits).
 namespace {
 struct CkptPlan {

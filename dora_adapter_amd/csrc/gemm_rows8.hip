@@ -5,7 +5,7 @@
 // that, 1 to 2, goes to Q, which is still in fp32, and the product to a pair of bf16 (16
 // bits of it).  Either operand keeps its own range.  Restoring x and storing Q
 // in bf16 first, as the backward from a bf16 x does, rounds both: dA is then 0.0032
-// of its norm off against 0.0023 here, where 0.0017 is its own last rounding
+// of its norm off against 0.0024 here, where 0.0017 is its own last rounding
 // and the rest dh's.
 //
 // The scale has to be one for all columns of a tile: one scale a row, or groups of
