@@ -352,15 +352,15 @@ def _own(st):
     if op == "weight4":
         rows, d, g = c["rows"], c["d"], c["group"]
         n = -(-d // g)
-        codes, scale = D.dora_quantize_rows4(
+        codes, scale = D.dora_quantize_fourbit(
             st["W"], group=g, codes=empty("codes", rows, n * g // 2, dtype=torch.uint8),
             scale=empty("scale", rows, n, dtype=torch.bfloat16))
-        values = D.dora_dequantize_rows4(codes, scale, d, group=g, out=empty("values", rows, d))
+        values = D.dora_dequantize_fourbit(codes, scale, d, group=g, out=empty("values", rows, d))
         return {"values": values, "scale": scale}
     if op == "linear4":
         T, d_in, d_out = c["T"], c["d_in"], c["d_out"]
-        need = D.dora_linear_rows4_workspace(T, d_in, d_out, lib_dt)
-        return D.dora_linear_rows4(st["x"], st["codes"], st["scale"], group=c["group"],
+        need = D.dora_linear_fourbit_workspace(T, d_in, d_out, lib_dt)
+        return D.dora_linear_fourbit(st["x"], st["codes"], st["scale"], group=c["group"],
                                    y=empty("y", T, d_out), ws=space(need))
     if not c["step"]:
         rows, cols = c["rows"], c["cols"]
