@@ -1,0 +1,42 @@
+// around.hpp - the operators that stand around a module, as dora_api.cpp plans and launches
+// them: the norms on both sides of a residual addition (block_norm.hip), 4-bit weights
+// (fourbit.hip, gemm_fourbit.hip) and orthogonalised updates (newton_schulz.hip).
+#pragma once
+
+#include "dora_internal.hpp"
+
+namespace dora {
+
+// ------------------------------------------------------------ block_norm.hip
+// Row t of x uses row t / gate_rows of the gate (gate_rows 0: no gate).
+struct BlockNormArgs {
+    const void *x, *res, *w_post, *gate, *w_pre;  // w_post, gate may be null
+    float res_scale, branch_scale, eps;
+    int64_t T, d, gate_rows;
+    void *h, *y;
+    float *rstd_post, *rstd_pre;  // each may be null
+};
+hipError_t launch_block_norm(int bf16, const BlockNormArgs &a, hipStream_t st);
+
+// How the rows are dealt to the gradient's workgroups, and what it keeps in its workspace.
+struct BlockNormPlan {
+    bool held;         // rows held in a workgroup's registers, one pass
+    int64_t chunk;     // consecutive rows a workgroup
+    int parts;         // of them
+    bool direct;       // a gate row's rows all lie in one chunk: its sum is final there
+    int64_t slots;     // partial sums of gate rows otherwise
+    size_t o_pre, o_post, o_gate, o_mean, bytes;
+};
+BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows, int bf16);
+struct BlockNormGradArgs {
+    const void *dy, *dh, *x, *h, *w_pre, *w_post, *gate;  // dh, w_post, gate may be null
+    const float *rstd_pre, *rstd_post;
+    float res_scale, branch_scale;
+    int64_t T, d, gate_rows;
+    void *dx, *dres, *dgate;   // dgate may be null
+    float *dw_pre, *dw_post;   // each may be null
+};
+hipError_t launch_block_norm_grad(int bf16, const BlockNormGradArgs &a, const BlockNormPlan &p,
+                                  void *ws, hipStream_t st);
+
+}  // namespace dora

@@ -1,0 +1,823 @@
+// block_norm.hip - the norms on both sides of a residual addition (gfx950):
+//
+//   u = w_post (.) x / rms(x)              the block's output normed (or x itself)
+//   h = a residual + b gate (.) u          rounded to the element type, as it is stored
+//   y = w_pre (.) h / rms(h)               normed for the block behind it
+//
+// and the gradients, with hat(v) = v / rms(v) and m1, m2 means over a row's columns:
+//
+//   dh        = dh_in + (w_pre dy - m1 hat(h)) / rms(h),   m1 = mean(w_pre dy hat(h))
+//   dresidual = a dh,  db = b dh,  dgate = sum db u,  du = gate db
+//   dx        = (w_post du - m2 hat(x)) / rms(x),          m2 = mean(w_post du hat(x))
+//   dw_pre    = sum dy hat(h),  dw_post = sum du hat(x)
+//
+// Both are bound by memory traffic: two matrices in and two out forward, four in and two out
+// backward, each once.  A workgroup takes whole rows, a thread eight consecutive columns at a
+// time (16 bytes of bf16).
+#include "around.hpp"
+#include "rows8.hpp"
+
+namespace dora {
+namespace {
+
+constexpr int LOOP_THREADS = 256;
+constexpr int LOOP_WAVES = LOOP_THREADS / 64;
+
+// gate row of row t (no gate, or one for all rows: 0)
+__device__ __forceinline__ int64_t gate_row(int64_t t, int64_t gate_rows, int64_t T)
+{
+    return gate_rows == 1 ? t : (gate_rows == 0 || gate_rows >= T ? 0 : t / gate_rows);
+}
+
+// h of eight columns from x, the residual, and what x is scaled by (b / rms(x), or b)
+template <typename T>
+__device__ __forceinline__ Raw8<T> block_h(const BlockNormArgs &a, const Raw8<T> &x,
+                                           const Raw8<T> &res, const Raw8<T> &w, const Raw8<T> &gate,
+                                           float rstd)
+{
+    float u[8], r[8];
+    x.get(u);
+    res.get(r);
+    if (a.w_post != nullptr) {
+        float v[8];
+        w.get(v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            u[q] = u[q] * rstd * v[q];
+    }
+    if (a.gate != nullptr) {
+        float v[8];
+        gate.get(v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            u[q] *= v[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        u[q] = __fmaf_rn(a.branch_scale, u[q], a.res_scale * r[q]);
+    Raw8<T> h;
+    h.set(u);
+    return h;
+}
+
+template <typename T>
+__device__ __forceinline__ float squares8(const Raw8<T> &v, float k, float acc)
+{
+    float f[8];
+    v.get(f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        acc = __fmaf_rn(k * f[q], k * f[q], acc);
+    return acc;
+}
+
+// Rows that fit a workgroup's registers, VPT vectors a thread: everything is read before the
+// first reduction, whose wait covers it, and written once.  h may be the residual, y may be x.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
+{
+    __shared__ float red[16];
+    const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
+    const int d = static_cast<int>(a.d);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * a.d;
+    const T *const gate = static_cast<const T *>(a.gate) + gate_row(blockIdx.x, a.gate_rows, a.T) * a.d;
+    auto col = [&](int i) { return (static_cast<int>(threadIdx.x) + i * threads) * 8; };
+    Raw8<T> x[VPT], h[VPT], w1[VPT], g[VPT], w2[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        x[i].load(static_cast<const T *>(a.x) + row + col(i), count8(d, col(i)));
+        h[i].load(static_cast<const T *>(a.res) + row + col(i), count8(d, col(i)));
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (a.w_post != nullptr)
+            w1[i].template load<true>(static_cast<const T *>(a.w_post) + col(i), count8(d, col(i)));
+        if (a.gate != nullptr)
+            g[i].template load<true>(gate + col(i), count8(d, col(i)));
+        w2[i].template load<true>(static_cast<const T *>(a.w_pre) + col(i), count8(d, col(i)));
+    }
+    float r1 = 1.f;
+    if (a.w_post != nullptr) {
+        auto sum = [&](float k) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                ss = squares8(x[i], k, ss);
+            return block_sum(ss, red, waves);
+        };
+        r1 = rstd_of(sum(1.f), static_cast<float>(d), a.eps, sum);
+        if (a.rstd_post != nullptr && threadIdx.x == 0)
+            a.rstd_post[blockIdx.x] = r1;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        h[i] = block_h(a, x[i], h[i], w1[i], g[i], r1);
+        h[i].store(static_cast<T *>(a.h) + row + col(i), count8(d, col(i)));
+    }
+    auto sum = [&](float k) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            ss = squares8(h[i], k, ss);
+        return block_sum(ss, red, waves);
+    };
+    const float r2 = rstd_of(sum(1.f), static_cast<float>(d), a.eps, sum);
+    if (a.rstd_pre != nullptr && threadIdx.x == 0)
+        a.rstd_pre[blockIdx.x] = r2;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        float f[8], w[8];
+        h[i].get(f);
+        w2[i].get(w);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            f[q] = f[q] * r2 * w[q];
+        Raw8<T> o;
+        o.set(f);
+        o.store(static_cast<T *>(a.y) + row + col(i), count8(d, col(i)));
+    }
+}
+
+// Rows of any width: every pass reads the row again, the same columns by the same thread.
+template <typename T>
+__global__ void __launch_bounds__(LOOP_THREADS) block_norm_kernel(BlockNormArgs a)
+{
+    __shared__ float red[LOOP_WAVES];
+    const int64_t vecs = (a.d + 7) / 8;
+    const float d = static_cast<float>(a.d);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int64_t row = t * a.d, grow = gate_row(t, a.gate_rows, a.T) * a.d;
+        auto squares = [&](const void *m) {
+            return [&, m](float k) {
+                float ss = 0.f;
+                for (int64_t v = threadIdx.x; v < vecs; v += LOOP_THREADS) {
+                    Raw8<T> r;
+                    r.load(static_cast<const T *>(m) + row + v * 8, count8(a.d, v * 8));
+                    ss = squares8(r, k, ss);
+                }
+                return block_sum(ss, red, LOOP_WAVES);
+            };
+        };
+        float r1 = 1.f;
+        if (a.w_post != nullptr) {
+            const auto sum = squares(a.x);
+            r1 = rstd_of(sum(1.f), d, a.eps, sum);
+            if (a.rstd_post != nullptr && threadIdx.x == 0)
+                a.rstd_post[t] = r1;
+        }
+        float ss = 0.f;
+        for (int64_t v = threadIdx.x; v < vecs; v += LOOP_THREADS) {
+            const int cnt = count8(a.d, v * 8);
+            Raw8<T> x, r, w1, g;
+            x.load(static_cast<const T *>(a.x) + row + v * 8, cnt);
+            r.load(static_cast<const T *>(a.res) + row + v * 8, cnt);
+            if (a.w_post != nullptr)
+                w1.template load<true>(static_cast<const T *>(a.w_post) + v * 8, cnt);
+            if (a.gate != nullptr)
+                g.template load<true>(static_cast<const T *>(a.gate) + grow + v * 8, cnt);
+            r = block_h(a, x, r, w1, g, r1);
+            r.store(static_cast<T *>(a.h) + row + v * 8, cnt);
+            ss = squares8(r, 1.f, ss);
+        }
+        // (a thread reads back only what it wrote)
+        const float r2 = rstd_of(block_sum(ss, red, LOOP_WAVES), d, a.eps, squares(a.h));
+        if (a.rstd_pre != nullptr && threadIdx.x == 0)
+            a.rstd_pre[t] = r2;
+        for (int64_t v = threadIdx.x; v < vecs; v += LOOP_THREADS) {
+            const int cnt = count8(a.d, v * 8);
+            Raw8<T> h, w2;
+            h.load(static_cast<const T *>(a.h) + row + v * 8, cnt);
+            w2.template load<true>(static_cast<const T *>(a.w_pre) + v * 8, cnt);
+            float f[8], w[8];
+            h.get(f);
+            w2.get(w);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                f[q] = f[q] * r2 * w[q];
+            h.set(f);
+            h.store(static_cast<T *>(a.y) + row + v * 8, cnt);
+        }
+    }
+}
+
+// --------------------------------------------------------------- the gradients
+// A row's eight columns as the gradient reads them, and its vectors of weights.
+template <typename T>
+struct GradVec {
+    Raw8<T> dy, dh, x, h;
+};
+template <typename T>
+struct GradWeights {
+    Raw8<T> pre, post, gate;
+};
+// The row's three sums, from which m1 and m2 follow in one reduction: with
+// k = b gate w_post hat(x), m2 is the mean of k dh, and dh is linear in m1:
+//   s1 = sum w_pre dy hat(h),  sa = sum k (dh_in + w_pre dy / rms(h)),
+//   sb = sum k hat(h) / rms(h),   m1 = s1 / d,  m2 = (sa - m1 sb) / d
+struct GradSums {
+    float s1, sa, sb;
+};
+
+template <bool POST, bool GATE, typename T>
+__device__ __forceinline__ void grad_sums(GradSums &s, const GradVec<T> &v, const GradWeights<T> &w,
+                                          bool with_dh, float r1, float r2, float b)
+{
+    float dy[8], h[8], wp[8];
+    v.dy.get(dy);
+    v.h.get(h);
+    w.pre.get(wp);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        h[q] *= r2;
+        dy[q] *= wp[q];
+        s.s1 = __fmaf_rn(dy[q], h[q], s.s1);
+    }
+    if constexpr (POST) {
+        float x[8], k[8], dh[8];
+        v.x.get(x);
+        w.post.get(k);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            k[q] *= x[q] * r1;
+        if constexpr (GATE) {
+            float g[8];
+            w.gate.get(g);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                k[q] *= g[q];
+        }
+        if (with_dh) {
+            v.dh.get(dh);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                dh[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            k[q] *= b;
+            s.sa = __fmaf_rn(k[q], __fmaf_rn(r2, dy[q], dh[q]), s.sa);
+            s.sb = __fmaf_rn(k[q], r2 * h[q], s.sb);
+        }
+    }
+}
+
+// What is left of eight columns once m1 and m2 are known: dx and dresidual, and
+// the terms of the three column sums.
+template <bool POST, bool GATE, typename T>
+__device__ __forceinline__ void grad_apply(const GradVec<T> &v, const GradWeights<T> &w, bool with_dh,
+                                           float r1, float r2, float a, float b, float m1, float m2,
+                                           Raw8<T> &dx, Raw8<T> &dres, float (&dw2)[8],
+                                           float (&dw1)[8], float (&dg)[8])
+{
+    float dy[8], h[8], o[8], f[8];
+    v.dy.get(dy);
+    v.h.get(h);
+    w.pre.get(f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        o[q] = 0.f;
+    if (with_dh)
+        v.dh.get(o);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        h[q] *= r2;
+        dw2[q] = __fmaf_rn(dy[q], h[q], dw2[q]);
+        o[q] += r2 * __fmaf_rn(-m1, h[q], f[q] * dy[q]);
+        f[q] = a * o[q];
+        o[q] *= b;
+    }
+    dres.set(f);
+    if constexpr (POST || GATE) {
+        float x[8];
+        v.x.get(x);
+        if constexpr (POST)
+            w.post.get(f);
+        float g[8];
+        if constexpr (GATE)
+            w.gate.get(g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float xh = POST ? x[q] * r1 : x[q];
+            if constexpr (GATE) {
+                dg[q] = __fmaf_rn(o[q], POST ? xh * f[q] : xh, dg[q]);
+                o[q] *= g[q];
+            }
+            if constexpr (POST) {
+                dw1[q] = __fmaf_rn(o[q], xh, dw1[q]);
+                o[q] = r1 * __fmaf_rn(-m2, xh, o[q] * f[q]);
+            }
+        }
+    }
+    dx.set(o);
+}
+
+struct GradOut {  // partial sums (or, where there is one part, the sums)
+    float *pre, *post, *gate;
+    float *mean;  // rows of any width: m1 and m2 of each row
+    int64_t chunk;
+    int direct;
+};
+
+// One pass over rows that fit a workgroup's registers: workgroup b takes rows
+// [b chunk, (b + 1) chunk); a thread keeps its columns' weights and sums.  GATE: 0 none,
+// 1 rows share gate rows (its sum goes out where the gate row changes: rounded, or to slot b +
+// gate row of the partial sums, which no other pair has, both indices growing along the
+// rows), 2 a gate row of its own each.
+template <typename T, int VPT, bool POST, int GATE, bool PRE, int THREADS>
+__global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNormGradArgs a, GradOut out)
+{
+    __shared__ float red[2][3][16];
+    const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
+    const int d = static_cast<int>(a.d);
+    const bool with_dh = a.dh != nullptr;
+    auto col = [&](int i) { return (static_cast<int>(threadIdx.x) + i * threads) * 8; };
+    auto at = [&](const void *m, int64_t row, int i) { return static_cast<const T *>(m) + row * a.d + col(i); };
+    GradWeights<T> w[VPT];
+    float dw2[VPT][8], dw1[VPT][8], dg[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int cnt = count8(d, col(i));
+        w[i].pre.template load<true>(at(a.w_pre, 0, i), cnt);
+        if constexpr (POST)
+            w[i].post.template load<true>(at(a.w_post, 0, i), cnt);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            dw2[i][q] = dw1[i][q] = dg[i][q] = 0.f;
+    }
+    struct Row {
+        GradVec<T> v[VPT];
+        Raw8<T> gate[VPT];
+        float r1, r2;
+    };
+    auto fetch = [&](Row &o, int64_t t) {
+        o.r2 = a.rstd_pre[t];
+        if constexpr (POST)
+            o.r1 = a.rstd_post[t];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int cnt = count8(d, col(i));
+            o.v[i].dy.load(at(a.dy, t, i), cnt);
+            o.v[i].h.load(at(a.h, t, i), cnt);
+            if constexpr (POST || GATE != 0)
+                o.v[i].x.load(at(a.x, t, i), cnt);
+            if (with_dh)
+                o.v[i].dh.load(at(a.dh, t, i), cnt);
+            if constexpr (GATE == 2)
+                o.gate[i].load(at(a.gate, t, i), cnt);
+        }
+    };
+    int64_t t = static_cast<int64_t>(blockIdx.x) * out.chunk;
+    const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
+    int64_t grow = 0, gend = 0;  // GATE 1: the gate row held, and the row behind its last
+    auto gate_out = [&]() {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int cnt = count8(d, col(i));
+            if (out.direct) {
+                Raw8<T> o;
+                o.set(dg[i]);
+                o.store(static_cast<T *>(a.dgate) + grow * a.d + col(i), cnt);
+            } else {
+                float *p = out.gate + (blockIdx.x + grow) * a.d + col(i);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q < cnt)
+                        p[q] = dg[i][q];
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                dg[i][q] = 0.f;
+        }
+    };
+    Row cur, nxt;
+    if (t < end)
+        fetch(cur, t);
+    for (int par = 0; t < end; par ^= 1) {
+        if constexpr (GATE == 1) {
+            if (t >= gend) {
+                if (gend != 0 && a.dgate != nullptr)
+                    gate_out();
+                grow = gate_row(t, a.gate_rows, a.T);
+                gend = (grow + 1) * a.gate_rows;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    w[i].gate.template load<true>(at(a.gate, grow, i), count8(d, col(i)));
+            }
+        }
+        GradSums s{0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if constexpr (GATE == 2)
+                w[i].gate = cur.gate[i];
+            grad_sums<POST, GATE != 0>(s, cur.v[i], w[i], with_dh, cur.r1, cur.r2, a.branch_scale);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (PRE && t + 1 < end)
+            fetch(nxt, t + 1);
+        s.s1 = wave_sum(s.s1);
+        if constexpr (POST) {
+            s.sa = wave_sum(s.sa);
+            s.sb = wave_sum(s.sb);
+        }
+        if (waves > 1) {
+            // one barrier a row: the next row writes the other half of `red`
+            if ((threadIdx.x & 63) == 0) {
+                red[par][0][threadIdx.x >> 6] = s.s1;
+                if constexpr (POST) {
+                    red[par][1][threadIdx.x >> 6] = s.sa;
+                    red[par][2][threadIdx.x >> 6] = s.sb;
+                }
+            }
+            __syncthreads();
+            s = GradSums{red[par][0][0], red[par][1][0], red[par][2][0]};
+            for (int k = 1; k < waves; ++k) {
+                s.s1 += red[par][0][k];
+                if constexpr (POST) {
+                    s.sa += red[par][1][k];
+                    s.sb += red[par][2][k];
+                }
+            }
+        }
+        const float m1 = s.s1 / static_cast<float>(d);
+        const float m2 = POST ? __fmaf_rn(-m1, s.sb, s.sa) / static_cast<float>(d) : 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            // (what the sums made of them would not leave the registers else)
+            forget(cur.v[i].dy);
+            forget(cur.v[i].h);
+            if constexpr (POST)
+                forget(cur.v[i].x);
+            Raw8<T> dx, dres;
+            grad_apply<POST, GATE != 0>(cur.v[i], w[i], with_dh, cur.r1, cur.r2, a.res_scale,
+                                        a.branch_scale, m1, m2, dx, dres, dw2[i], dw1[i], dg[i]);
+            const int cnt = count8(d, col(i));
+            dx.store(static_cast<T *>(a.dx) + t * a.d + col(i), cnt);
+            dres.store(static_cast<T *>(a.dres) + t * a.d + col(i), cnt);
+            if constexpr (GATE == 2) {
+                if (a.dgate != nullptr) {
+                    Raw8<T> o;
+                    o.set(dg[i]);
+                    o.store(static_cast<T *>(a.dgate) + t * a.d + col(i), cnt);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    dg[i][q] = 0.f;
+            }
+            // one vector at a time (left free, the scheduler unpacks them all)
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        ++t;
+        if (PRE)
+            cur = nxt;
+        else if (t < end)
+            fetch(cur, t);
+    }
+    if constexpr (GATE == 1)
+        if (gend != 0 && a.dgate != nullptr)
+            gate_out();
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int cnt = count8(d, col(i));
+        const int64_t o = blockIdx.x * a.d + col(i);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < cnt) {
+                if (out.pre != nullptr)
+                    out.pre[o + q] = dw2[i][q];
+                if (POST && out.post != nullptr)
+                    out.post[o + q] = dw1[i][q];
+            }
+    }
+}
+
+// Rows of any width, first pass: m1 and m2 of every row.
+template <typename T, bool POST, bool GATE>
+__global__ void __launch_bounds__(LOOP_THREADS) block_norm_mean_kernel(BlockNormGradArgs a, float *mean)
+{
+    __shared__ float red[LOOP_WAVES];
+    const int64_t vecs = (a.d + 7) / 8;
+    const float d = static_cast<float>(a.d);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int64_t row = t * a.d, grow = gate_row(t, a.gate_rows, a.T) * a.d;
+        GradSums s{0.f, 0.f, 0.f};
+        const float r2 = a.rstd_pre[t], r1 = POST ? a.rstd_post[t] : 1.f;
+        for (int64_t i = threadIdx.x; i < vecs; i += LOOP_THREADS) {
+            const int cnt = count8(a.d, i * 8);
+            GradVec<T> v;
+            GradWeights<T> w;
+            v.dy.load(static_cast<const T *>(a.dy) + row + i * 8, cnt);
+            v.h.load(static_cast<const T *>(a.h) + row + i * 8, cnt);
+            w.pre.template load<true>(static_cast<const T *>(a.w_pre) + i * 8, cnt);
+            if constexpr (POST) {
+                v.x.load(static_cast<const T *>(a.x) + row + i * 8, cnt);
+                if (a.dh != nullptr)
+                    v.dh.load(static_cast<const T *>(a.dh) + row + i * 8, cnt);
+                w.post.template load<true>(static_cast<const T *>(a.w_post) + i * 8, cnt);
+                if constexpr (GATE)
+                    w.gate.template load<true>(static_cast<const T *>(a.gate) + grow + i * 8, cnt);
+            }
+            grad_sums<POST, GATE>(s, v, w, a.dh != nullptr, r1, r2, a.branch_scale);
+        }
+        const float m1 = block_sum(s.s1, red, LOOP_WAVES) / d;
+        float m2 = 0.f;
+        if constexpr (POST) {
+            s.sa = block_sum(s.sa, red, LOOP_WAVES);
+            s.sb = block_sum(s.sb, red, LOOP_WAVES);
+            m2 = __fmaf_rn(-m1, s.sb, s.sa) / d;
+        }
+        if (threadIdx.x == 0) {
+            mean[2 * t] = m1;
+            mean[2 * t + 1] = m2;
+        }
+    }
+}
+
+// Second pass: workgroup (i, b) walks rows [b chunk, (b + 1) chunk) of its 2048 columns.
+template <typename T, bool POST, int GATE>
+__global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNormGradArgs a, GradOut out)
+{
+    const int64_t j = (static_cast<int64_t>(blockIdx.x) * LOOP_THREADS + threadIdx.x) * 8;
+    if (j >= a.d)
+        return;
+    const int cnt = count8(a.d, j);
+    GradWeights<T> w;
+    w.pre.template load<true>(static_cast<const T *>(a.w_pre) + j, cnt);
+    if constexpr (POST)
+        w.post.template load<true>(static_cast<const T *>(a.w_post) + j, cnt);
+    float dw2[8], dw1[8], dg[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        dw2[q] = dw1[q] = dg[q] = 0.f;
+    int64_t t = static_cast<int64_t>(blockIdx.y) * out.chunk;
+    const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
+    int64_t grow = 0, gend = 0;
+    auto gate_out = [&]() {
+        if (out.direct) {
+            Raw8<T> o;
+            o.set(dg);
+            o.store(static_cast<T *>(a.dgate) + grow * a.d + j, cnt);
+        } else {
+            for (int q = 0; q < cnt; ++q)
+                out.gate[(blockIdx.y + grow) * a.d + j + q] = dg[q];
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            dg[q] = 0.f;
+    };
+    for (; t < end; ++t) {
+        if constexpr (GATE != 0) {
+            if (GATE == 2 || t >= gend) {
+                if (GATE == 1 && gend != 0 && a.dgate != nullptr)
+                    gate_out();
+                grow = gate_row(t, a.gate_rows, a.T);
+                gend = (grow + 1) * a.gate_rows;
+                w.gate.template load<GATE == 1>(static_cast<const T *>(a.gate) + grow * a.d + j, cnt);
+            }
+        }
+        const int64_t at = t * a.d + j;
+        GradVec<T> v;
+        v.dy.load(static_cast<const T *>(a.dy) + at, cnt);
+        v.h.load(static_cast<const T *>(a.h) + at, cnt);
+        if constexpr (POST || GATE != 0)
+            v.x.load(static_cast<const T *>(a.x) + at, cnt);
+        if (a.dh != nullptr)
+            v.dh.load(static_cast<const T *>(a.dh) + at, cnt);
+        Raw8<T> dx, dres;
+        grad_apply<POST, GATE != 0>(v, w, a.dh != nullptr, POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t],
+                                    a.res_scale, a.branch_scale, out.mean[2 * t], out.mean[2 * t + 1],
+                                    dx, dres, dw2, dw1, dg);
+        dx.store(static_cast<T *>(a.dx) + at, cnt);
+        dres.store(static_cast<T *>(a.dres) + at, cnt);
+        if constexpr (GATE == 2) {
+            if (a.dgate != nullptr) {
+                Raw8<T> o;
+                o.set(dg);
+                o.store(static_cast<T *>(a.dgate) + at, cnt);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                dg[q] = 0.f;
+        }
+    }
+    if constexpr (GATE == 1)
+        if (gend != 0 && a.dgate != nullptr)
+            gate_out();
+    const int64_t o = static_cast<int64_t>(blockIdx.y) * a.d + j;
+    for (int q = 0; q < cnt; ++q) {
+        if (out.pre != nullptr)
+            out.pre[o + q] = dw2[q];
+        if (POST && out.post != nullptr)
+            out.post[o + q] = dw1[q];
+    }
+}
+
+// The partial sums in order: blockIdx.y 0 dw_pre, 1 dw_post, 2 + g gate row g; 64 columns a
+// workgroup, whose 16 waves take every 16th part each.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+    block_norm_finish_kernel(GradOut part, int parts, int64_t Tn, int64_t d, int64_t gate_rows,
+                             float *dw_pre, float *dw_post, T *dgate)
+{
+    __shared__ float sums[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t g = static_cast<int64_t>(blockIdx.y) - 2;
+    const float *from = blockIdx.y == 0 ? part.pre : part.post;
+    int64_t count = parts;
+    if (g >= 0) {
+        if (dgate == nullptr)
+            return;
+        const int64_t first = g * gate_rows;
+        const int64_t last = (first + gate_rows < Tn ? first + gate_rows : Tn) - 1;
+        from = part.gate + (first / part.chunk + g) * d;
+        count = Tn == 0 ? 0 : last / part.chunk - first / part.chunk + 1;
+    } else if ((blockIdx.y == 0 ? dw_pre : dw_post) == nullptr) {
+        return;
+    }
+    for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 64; j0 < d;
+         j0 += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t j = j0 + lane;
+        float acc = 0.f;
+        if (j < d) {
+#pragma unroll 8
+            for (int64_t p = wave; p < count; p += 16)
+                acc += from[p * d + j];
+        }
+        __syncthreads();  // the last columns' sums have been read
+        sums[wave][lane] = acc;
+        __syncthreads();
+        if (wave == 0 && j < d) {
+            acc = sums[0][lane];
+#pragma unroll
+            for (int k = 1; k < 16; ++k)
+                acc += sums[k][lane];
+            if (g >= 0) {
+                if constexpr (sizeof(T) == 2)
+                    dgate[g * d + j] = f32_to_bf16(acc);
+                else
+                    dgate[g * d + j] = acc;
+            } else {
+                (blockIdx.y == 0 ? dw_pre : dw_post)[j] = acc;
+            }
+        }
+    }
+}
+
+constexpr int64_t MAX_ROW_GROUPS = 1 << 20;  // workgroups of a row launch
+
+template <typename T>
+hipError_t forward(const BlockNormArgs &a, hipStream_t st)
+{
+    const int64_t vecs = (a.d + 7) / 8;
+    int vpt = a.T <= 512 ? 1 : 2;
+    while (vecs > 1024 * static_cast<int64_t>(vpt) && vpt < 4)
+        vpt *= 2;
+    const int64_t threads = ((vecs + vpt - 1) / vpt + 63) / 64 * 64;
+    const dim3 grid(static_cast<unsigned>(a.T)), block(static_cast<unsigned>(threads));
+    // (a launch holds fewer than 2^32 threads)
+    if (vecs > 1024 * static_cast<int64_t>(vpt) || a.T >= (int64_t(1) << 32) / threads)
+        hipLaunchKernelGGL((block_norm_kernel<T>),
+                           dim3(static_cast<unsigned>(a.T < MAX_ROW_GROUPS ? a.T : MAX_ROW_GROUPS)),
+                           dim3(LOOP_THREADS), 0, st, a);
+    else if (vpt == 1)
+        hipLaunchKernelGGL((block_norm_held_kernel<T, 1>), grid, block, 0, st, a);
+    else if (vpt == 2)
+        hipLaunchKernelGGL((block_norm_held_kernel<T, 2>), grid, block, 0, st, a);
+    else
+        hipLaunchKernelGGL((block_norm_held_kernel<T, 4>), grid, block, 0, st, a);
+    return hipGetLastError();
+}
+
+// Columns whose rows are held in registers: eight of 1024 threads each, or, in bf16, sixteen.
+bool grad_held(int64_t d, bool bf16) { return d <= (bf16 ? 16384 : 8192); }
+
+template <typename T, bool POST, int GATE>
+hipError_t backward(const BlockNormGradArgs &a, const BlockNormPlan &p, const GradOut &out, hipStream_t st)
+{
+    const int64_t vecs = (a.d + 7) / 8;
+    if (p.held) {
+        constexpr bool BF = sizeof(T) == 2;
+        const int vpt = BF && vecs > 512 ? 2 : 1;
+        const dim3 grid(static_cast<unsigned>(p.parts)),
+            block(static_cast<unsigned>(((vecs + vpt - 1) / vpt + 63) / 64 * 64));
+        if (vecs <= 512)
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 1, POST, GATE, true, 512>), grid, block,
+                               0, st, a, out);
+        else if constexpr (!BF)
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 1, POST, GATE, false, 1024>), grid,
+                               block, 0, st, a, out);
+        else if (vecs <= 1024)
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 2, POST, GATE, true, 512>), grid, block,
+                               0, st, a, out);
+        else
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 2, POST, GATE, false, 1024>), grid,
+                               block, 0, st, a, out);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((block_norm_mean_kernel<T, POST, GATE != 0>),
+                       dim3(static_cast<unsigned>(a.T < MAX_ROW_GROUPS ? a.T : MAX_ROW_GROUPS)),
+                       dim3(LOOP_THREADS), 0, st, a, out.mean);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((block_norm_grad_kernel<T, POST, GATE>),
+                       dim3(static_cast<unsigned>((vecs + LOOP_THREADS - 1) / LOOP_THREADS),
+                            static_cast<unsigned>(p.parts)),
+                       dim3(LOOP_THREADS), 0, st, a, out);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t backward_any(const BlockNormGradArgs &a, const BlockNormPlan &p, char *ws, hipStream_t st)
+{
+    const bool one = p.parts <= 1;  // one part is the sum itself
+    auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+    const GradOut out{a.dw_pre == nullptr ? nullptr : (one ? a.dw_pre : at(p.o_pre)),
+                      a.dw_post == nullptr ? nullptr : (one ? a.dw_post : at(p.o_post)),
+                      at(p.o_gate), at(p.o_mean), p.chunk, p.direct};
+    const int gate = a.gate == nullptr ? 0 : (a.gate_rows == 1 ? 2 : 1);
+    hipError_t e = hipSuccess;
+    if (a.T == 0)
+        ;  // (no partial sums: the finish writes zeros)
+    else if (a.w_post != nullptr)
+        e = gate == 0   ? backward<T, true, 0>(a, p, out, st)
+            : gate == 1 ? backward<T, true, 1>(a, p, out, st)
+                        : backward<T, true, 2>(a, p, out, st);
+    else
+        e = gate == 0   ? backward<T, false, 0>(a, p, out, st)
+            : gate == 1 ? backward<T, false, 1>(a, p, out, st)
+                        : backward<T, false, 2>(a, p, out, st);
+    const bool slots = a.dgate != nullptr && (a.T == 0 || (gate == 1 && !p.direct));
+    const bool sums = (!one || a.T == 0) && (a.dw_pre != nullptr || a.dw_post != nullptr);
+    if (e != hipSuccess || (!slots && !sums))
+        return e;
+    const int64_t blocks = (a.d + 63) / 64, rows = !slots ? 0 : a.T == 0 ? 1 : (a.T + a.gate_rows - 1) / a.gate_rows;
+    hipLaunchKernelGGL((block_norm_finish_kernel<T>),
+                       dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536),
+                            static_cast<unsigned>(2 + rows)),
+                       dim3(1024), 0, st, out, p.parts, a.T, a.d, a.gate_rows,
+                       sums ? a.dw_pre : nullptr, sums ? a.dw_post : nullptr,
+                       slots ? static_cast<T *>(a.dgate) : nullptr);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(int bf16, const BlockNormArgs &a, hipStream_t st)
+{
+    if (a.T == 0)
+        return hipSuccess;
+    return bf16 ? forward<uint16_t>(a, st) : forward<float>(a, st);
+}
+
+BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows, int bf16)
+{
+    BlockNormPlan p;
+    p.held = grad_held(d, bf16 != 0);
+    const int64_t vecs = (d + 7) / 8;
+    int64_t parts;
+    if (p.held) {
+        // a workgroup a CU, and the shorter the rows the more of them
+        const int most = vecs > 512 ? 1 : vecs > 128 ? 2 : vecs > 64 ? 4 : vecs > 32 ? 8 : 16;
+        const int64_t share = vecs > 128 ? T / 8 : T / 4;
+        parts = share > 256 ? share : 256;
+        parts = parts < 256 * most ? parts : 256 * most;
+        parts = parts < T ? parts : T;
+    } else {
+        // about 2048 workgroups over column blocks and chunks, 16 rows each at least
+        parts = 2048 / ((vecs + LOOP_THREADS - 1) / LOOP_THREADS);
+        parts = parts < (T + 15) / 16 ? parts : (T + 15) / 16;
+    }
+    parts = parts < 1 ? 1 : parts;
+    p.chunk = (T + parts - 1) / parts;
+    p.chunk = p.chunk < 1 ? 1 : p.chunk;
+    // Whole gate rows in a chunk, where that makes it longer by a quarter at most, leave no
+    // partial sums; else the slots are at most five a workgroup.
+    p.direct = gate_rows > 1 && (gate_rows >= T ? p.chunk >= T : 4 * gate_rows <= p.chunk);
+    if (p.direct && gate_rows < T)
+        p.chunk = (p.chunk + gate_rows - 1) / gate_rows * gate_rows;
+    p.parts = static_cast<int>((T + p.chunk - 1) / p.chunk);
+    p.slots = gate_rows > 1 && !p.direct && T > 0 ? p.parts + (T + gate_rows - 1) / gate_rows : 0;
+    auto take = [off = size_t(0)](size_t bytes) mutable {
+        const size_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    const size_t row = static_cast<size_t>(d) * sizeof(float);
+    const size_t sums = p.parts > 1 ? p.parts * row : 0;
+    p.o_pre = take(sums);
+    p.o_post = take(sums);
+    p.o_gate = take(p.slots * row);
+    p.o_mean = take(p.held ? 0 : static_cast<size_t>(T) * 2 * sizeof(float));
+    p.bytes = take(0);
+    return p;
+}
+
+hipError_t launch_block_norm_grad(int bf16, const BlockNormGradArgs &a, const BlockNormPlan &p,
+                                  void *ws, hipStream_t st)
+{
+    char *const w = static_cast<char *>(ws);
+    return bf16 ? backward_any<uint16_t>(a, p, w, st) : backward_any<float>(a, p, w, st);
+}
+
+}  // namespace dora

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/dora.h"
+#include "around.hpp"
 #include "dora_internal.hpp"
 #include "gemm_rows8.hpp"
 
@@ -2245,6 +2246,127 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
                                  d_out, r, dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
     return backward_impl(p.b, dy, w + p.o_x, &x8, W, A, B, m, n, s, P, nullptr, &y8, T, d_in, d_out, r,
                          dtype, dx, dA, dB, dm, w + p.o_bwd, stream);
+}
+
+namespace {
+
+int check_scalars(std::initializer_list<std::pair<float, const char *>> vs)
+{
+    for (const auto &v : vs)
+        if (!(v.first >= -3.4028235e38f && v.first <= 3.4028235e38f))
+            return fail(DORA_E_VALUE, "%s is not finite", v.second);
+    return DORA_OK;
+}
+
+int check_gate(const void *gate, int64_t gate_rows)
+{
+    if (gate && (gate_rows < 1 || gate_rows > kMaxDim))
+        return fail(DORA_E_SHAPE, "gate_rows=%lld out of range [1, 2^31)", (long long)gate_rows);
+    return DORA_OK;
+}
+
+// Bytes of a gate (or its gradient): a row for each gate_rows tokens, one at least.
+size_t gate_bytes(int64_t T, int64_t d, int64_t gate_rows, size_t e)
+{
+    const int64_t rows = T == 0 ? 1 : (T + gate_rows - 1) / gate_rows;
+    return static_cast<size_t>(rows) * d * e;
+}
+
+}  // namespace
+
+int dora_block_norm(const void *x, const void *residual, const void *w_post, const void *gate,
+                    int64_t gate_rows, const void *w_pre, float residual_scale, float branch_scale,
+                    float eps, int64_t T, int64_t d, int dtype, void *h, void *y, float *rstd_post,
+                    float *rstd_pre, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(T, d));
+    DORA_CHECK(check_gate(gate, gate_rows));
+    if (!(eps >= 0.f) || eps > 3.4e38f)
+        return fail(DORA_E_VALUE, "eps must be finite and not negative");
+    DORA_CHECK(check_scalars({{residual_scale, "residual_scale"}, {branch_scale, "branch_scale"}}));
+    const bool has_t = T > 0;
+    DORA_CHECK(check_ptrs({{x, "x", has_t}, {residual, "residual", has_t}, {w_post, "w_post", false},
+                           {gate, "gate", false}, {w_pre, "w_pre", true}, {h, "h", has_t},
+                           {y, "y", has_t}, {rstd_post, "rstd_post", false},
+                           {rstd_pre, "rstd_pre", false}}));
+    if (rstd_post && !w_post)
+        return fail(DORA_E_VALUE, "rstd_post is asked for without w_post");
+    const size_t e = esize(dtype), rows = static_cast<size_t>(T) * d * e, r = T * sizeof(float);
+    const Range rx{x, rows}, rr{residual, rows};
+    // h in place of the residual, y in place of x: the same element, read before it is
+    // written by the same thread
+    if (h && h != residual && overlap({h, rows}, rr))
+        return fail(DORA_E_ALIAS, "h partially overlaps residual");
+    if (y && y != x && overlap({y, rows}, rx))
+        return fail(DORA_E_ALIAS, "y partially overlaps x");
+    DORA_CHECK(check_disjoint({{{h, rows}, "h"}, {{y, rows}, "y"}, {{rstd_post, r}, "rstd_post"},
+                               {{rstd_pre, r}, "rstd_pre"}},
+                              {{{w_post, d * e}, "w_post"}, {{w_pre, d * e}, "w_pre"},
+                               {{gate, gate ? gate_bytes(T, d, gate_rows, e) : 0}, "gate"}}));
+    DORA_CHECK(check_disjoint({{{h, rows}, "h"}}, {{rx, "x"}}));
+    DORA_CHECK(check_disjoint({{{y, rows}, "y"}}, {{rr, "residual"}}));
+    DORA_CHECK(check_disjoint({{{rstd_post, r}, "rstd_post"}, {{rstd_pre, r}, "rstd_pre"}},
+                              {{rx, "x"}, {rr, "residual"}}));
+    const BlockNormArgs a{x, residual, w_post, gate, w_pre, residual_scale, branch_scale, eps, T, d,
+                          gate ? gate_rows : 0, h, y, rstd_post, rstd_pre};
+    DORA_LAUNCH(launch_block_norm(dtype == DORA_BF16, a, static_cast<hipStream_t>(stream)),
+                "block norm");
+    return DORA_OK;
+}
+
+size_t dora_block_norm_backward_workspace(int64_t T, int64_t d, int64_t gate_rows, int dtype)
+{
+    if (check_dtype(dtype) || check_rows(T, d) || gate_rows < 0 || gate_rows > kMaxDim)
+        return 0;
+    return plan_block_norm_grad(T, d, gate_rows, dtype == DORA_BF16).bytes;
+}
+
+int dora_block_norm_backward(const void *dy, const void *dh, const void *x, const void *h,
+                             const void *w_post, const void *gate, int64_t gate_rows,
+                             const void *w_pre, const float *rstd_post, const float *rstd_pre,
+                             float residual_scale, float branch_scale, int64_t T, int64_t d,
+                             int dtype, void *dx, void *dresidual, void *dgate, float *dw_post,
+                             float *dw_pre, void *ws, size_t ws_bytes, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(T, d));
+    DORA_CHECK(check_gate(gate, gate_rows));
+    DORA_CHECK(check_scalars({{residual_scale, "residual_scale"}, {branch_scale, "branch_scale"}}));
+    const bool has_t = T > 0;
+    DORA_CHECK(check_ptrs({{dy, "dy", has_t}, {dh, "dh", false}, {x, "x", has_t}, {h, "h", has_t},
+                           {w_post, "w_post", false}, {gate, "gate", false}, {w_pre, "w_pre", true},
+                           {rstd_post, "rstd_post", has_t && w_post}, {rstd_pre, "rstd_pre", has_t},
+                           {dx, "dx", has_t}, {dresidual, "dresidual", has_t},
+                           {dgate, "dgate", false}, {dw_post, "dw_post", false},
+                           {dw_pre, "dw_pre", false}}));
+    if (dw_post && !w_post)
+        return fail(DORA_E_VALUE, "dw_post is asked for without w_post");
+    if (dgate && !gate)
+        return fail(DORA_E_VALUE, "dgate is asked for without gate");
+    const BlockNormPlan p = plan_block_norm_grad(T, d, gate ? gate_rows : 0, dtype == DORA_BF16);
+    DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
+    const size_t e = esize(dtype), rows = static_cast<size_t>(T) * d * e, r = T * sizeof(float);
+    const size_t gb = gate ? gate_bytes(T, d, gate_rows, e) : 0, v = d * sizeof(float);
+    if (dresidual && dresidual != dh && overlap({dresidual, rows}, {dh, rows}))
+        return fail(DORA_E_ALIAS, "dresidual partially overlaps dh");
+    DORA_CHECK(check_disjoint(
+        {{{dx, rows}, "dx"}, {{dresidual, rows}, "dresidual"}, {{dgate, gb}, "dgate"},
+         {{dw_post, v}, "dw_post"}, {{dw_pre, v}, "dw_pre"}, {{ws, p.bytes}, "workspace"}},
+        {{{dy, rows}, "dy"}, {{x, rows}, "x"}, {{h, rows}, "h"}, {{w_post, d * e}, "w_post"},
+         {{gate, gb}, "gate"}, {{w_pre, d * e}, "w_pre"}, {{rstd_post, w_post ? r : 0}, "rstd_post"},
+         {{rstd_pre, r}, "rstd_pre"}}));
+    DORA_CHECK(check_disjoint({{{dx, rows}, "dx"}, {{dgate, gb}, "dgate"}, {{dw_post, v}, "dw_post"},
+                               {{dw_pre, v}, "dw_pre"}, {{ws, p.bytes}, "workspace"}},
+                              {{{dh, rows}, "dh"}}));
+    const BlockNormGradArgs a{dy, dh, x, h, w_pre, w_post, gate, rstd_pre, rstd_post, residual_scale,
+                              branch_scale, T, d, gate ? gate_rows : 0, dx, dresidual, dgate,
+                              dw_pre, dw_post};
+    DORA_LAUNCH(launch_block_norm_grad(dtype == DORA_BF16, a, p, ws, static_cast<hipStream_t>(stream)),
+                "block norm backward");
+    return DORA_OK;
 }
 
 }  // extern "C"

@@ -17,11 +17,6 @@ constexpr int ROW_THREADS = 256;
 constexpr int ROW_WAVES = ROW_THREADS / 64;
 constexpr int64_t MAX_ROW_GROUPS = 1 << 20;  // workgroups of a row launch
 
-__device__ __forceinline__ int count8(int64_t d, int64_t j)
-{
-    return d - j < 8 ? static_cast<int>(d - j > 0 ? d - j : 0) : 8;
-}
-
 // h of eight columns: x + residual summed in fp32 and rounded to the element
 // type, because that is what the residual stream keeps and what the backward
 // pass reads (the norm is then a function of the stored h).
@@ -113,23 +108,6 @@ __device__ __forceinline__ void quantize_held(F &&value, int k0, int d, int grou
         value(i, v);
         quantize8(v, s, inv).store(q + t * d + k * 8, count8(d, k * 8));
     }
-}
-
-// 1 / sqrt(ss / d + eps) of a row whose squares sum to ss (the same in every thread).
-// The squares leave fp32's range long before h and rstd do (overflow from 2^64 on,
-// lost bits below 2^-50 where eps is as small): such a row's are summed again, of
-// k h with a power of two k that puts them inside (every |h| < 2^128, d < 2^31: k h to
-// 2^48; the mean below 2^-100: k h to 2^56, denormal h from 2^-59 on), and the root
-// gets it back.  rstd is a number for rows whose root mean square lies from 2^-127 to
-// the largest value (denormal from 2^126 on).
-template <typename F>
-__device__ __forceinline__ float rstd_of(float ss, float d, float eps, F &&sum_squares_of)
-{
-    const float ms = ss / d + eps;
-    if (ms >= 0x1p-100f && ms < __builtin_inff())
-        return 1.f / sqrtf(ms);
-    const float k = ms > 1.f ? 0x1p-80f : 0x1p90f;
-    return k / sqrtf(sum_squares_of(k) / d + eps * k * k);
 }
 
 // Rows of any width: every pass reads the row again.  A thread meets the same

@@ -117,6 +117,12 @@ struct Raw8<float> {
     }
 };
 
+// Elements from j to the row's end, eight at most.
+__device__ __forceinline__ int count8(int64_t d, int64_t j)
+{
+    return d - j < 8 ? static_cast<int>(d - j > 0 ? d - j : 0) : 8;
+}
+
 // The same vector, its values to be formed again from here on: what was unpacked
 // from it earlier is then not kept in registers for the next use.
 template <typename T>
@@ -308,6 +314,23 @@ __device__ __forceinline__ unsigned int block_max(unsigned int v, unsigned int *
     for (int k = 1; k < waves; ++k)
         s = s > red[k] ? s : red[k];
     return s;
+}
+
+// 1 / sqrt(ss / d + eps) of a row whose squares sum to ss (the same in every thread).
+// The squares leave fp32's range long before h and rstd do (overflow from 2^64 on,
+// lost bits below 2^-50 where eps is as small): such a row's are summed again, of
+// k h with a power of two k that puts them inside (every |h| < 2^128, d < 2^31: k h to
+// 2^48; the mean below 2^-100: k h to 2^56, denormal h from 2^-59 on), and the root
+// gets it back.  rstd is a number for rows whose root mean square lies from 2^-127 to
+// the largest value (denormal from 2^126 on).
+template <typename F>
+__device__ __forceinline__ float rstd_of(float ss, float d, float eps, F &&sum_squares_of)
+{
+    const float ms = ss / d + eps;
+    if (ms >= 0x1p-100f && ms < __builtin_inff())
+        return 1.f / sqrtf(ms);
+    const float k = ms > 1.f ? 0x1p-80f : 0x1p90f;
+    return k / sqrtf(sum_squares_of(k) / d + eps * k * k);
 }
 
 // y = c xs wscale for an int32 sum c, as (c xs) wscale: c xs leaves fp32's range only

@@ -29,7 +29,8 @@ EXPORTS = ("dora_strerror", "dora_last_error", "dora_norm_workspace", "dora_forw
            "dora_rmsnorm", "dora_rmsnorm_backward_workspace", "dora_rmsnorm_backward",
            "dora_quantize_rows", "dora_dequantize_rows", "dora_linear_quantized_workspace",
            "dora_linear_quantized", "dora_backward_checkpoint_workspace",
-           "dora_backward_checkpoint")
+           "dora_backward_checkpoint", "dora_block_norm", "dora_block_norm_backward_workspace",
+           "dora_block_norm_backward")
 
 _lib = None
 
@@ -121,6 +122,13 @@ def lib():
         L.dora_backward_checkpoint.restype = c_int
         L.dora_backward_checkpoint.argtypes = [p, p, p, p, p, p, p, p, f, p, p, p, i64, p, c_int,
                                                i64, i64, i64, i64, c_int, p, p, p, p, p, sz, p]
+        L.dora_block_norm.restype = c_int
+        L.dora_block_norm.argtypes = [p, p, p, p, i64, p, f, f, f, i64, i64, c_int, p, p, p, p, p]
+        L.dora_block_norm_backward_workspace.restype = sz
+        L.dora_block_norm_backward_workspace.argtypes = [i64, i64, i64, c_int]
+        L.dora_block_norm_backward.restype = c_int
+        L.dora_block_norm_backward.argtypes = [p, p, p, p, p, p, i64, p, p, p, f, f, i64, i64,
+                                               c_int, p, p, p, p, p, p, sz, p]
         _lib = L
     return _lib
 
@@ -621,4 +629,111 @@ def dora_backward_checkpoint(dy, xq, xs, W, A, B, m, n, s, P, yq, ys, group=0, t
             _at(B), _at(m), _at(n), float(s), _at(P), _at(yq), _at(ys), group, _at(U),
             int(through_norm), T, d_in, d_out, r, dt, _at(out["dx"]), _at(out["dA"]),
             _at(out["dB"]), _at(out["dm"]), _at(ws), ws.numel())
+    return out
+
+
+# ------------------------------------------- norms on both sides of a residual
+def _gate_rows(gate, T, d):
+    """Tokens that share a row of the gate (0 without one): gate [d] or [G, d], G dividing T."""
+    if gate is None:
+        return 0
+    if gate.dim() == 1:
+        return max(T, 1)
+    G = gate.shape[0]
+    if T == 0 and G == 1:
+        return 1
+    if gate.dim() != 2 or G < 1 or T < G or T % G:
+        raise ValueError(f"gate of shape {tuple(gate.shape)} for {T} tokens: [d], or [G, d] with "
+                         "G dividing them")
+    return T // G
+
+
+def _block_inputs(x, w_pre, w_post, gate):
+    dev = _dev(x)
+    T, d = _rows("x", x)
+    rows = _gate_rows(gate, T, d)
+    _need("x", x, dev, x.dtype, T, d)
+    _need("w_pre", w_pre, dev, x.dtype, d)
+    if w_post is not None:
+        _need("w_post", w_post, dev, x.dtype, d)
+    if gate is not None:
+        _need("gate", gate, dev, x.dtype, *gate.shape[:-1], d)
+    return dev, T, d, _dt(x), rows
+
+
+def dora_block_norm(x, residual, w_pre, w_post=None, gate=None, residual_scale=1.0,
+                    branch_scale=1.0, eps=1e-6, want_rstd=False, out=None):
+    """The norms on both sides of a residual addition: u = w_post x / rms(x) (x without w_post),
+    h = residual_scale residual + branch_scale gate u (rounded to the element type), y = w_pre h /
+    rms(h).  gate: [d], or [G, d] for sequences of T / G tokens each (G = T: one a token).  Returns
+    a dict of "h", "y" and, with want_rstd, "rstd_pre" and (with w_post) "rstd_post" (fp32 [T], for
+    the backward).  out: a dict of preallocated outputs, h and y at least; then those are what is
+    asked for.  out["h"] may be residual, out["y"] may be x."""
+    dev, T, d, dt, rows = _block_inputs(x, w_pre, w_post, gate)
+    _need("residual", residual, dev, x.dtype, T, d)
+    if out is None:
+        out = {"h": torch.empty_like(x), "y": torch.empty_like(x)}
+        if want_rstd:
+            out["rstd_pre"] = torch.empty(T, dtype=torch.float32, device=dev)
+            if w_post is not None:
+                out["rstd_post"] = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        if "h" not in out or "y" not in out:
+            raise ValueError("out needs h and y")
+        for k, t in out.items():
+            if k in ("h", "y"):
+                _need(k, t, dev, x.dtype, T, d)
+            elif k in ("rstd_pre", "rstd_post"):
+                _need(k, t, dev, torch.float32, T)
+            else:
+                raise ValueError(f"out has no place for {k!r}")
+    _launch(dev, lib().dora_block_norm, _at(x), _at(residual), _at(w_post), _at(gate), rows,
+            _at(w_pre), float(residual_scale), float(branch_scale), float(eps), T, d, dt,
+            _at(out["h"]), _at(out["y"]), _at(out.get("rstd_post")), _at(out.get("rstd_pre")))
+    return out
+
+
+def dora_block_norm_backward_workspace(T, d, gate_rows, dtype):
+    return lib().dora_block_norm_backward_workspace(T, d, gate_rows, dtype)
+
+
+def dora_block_norm_backward(dy, x, h, w_pre, rstd_pre, w_post=None, rstd_post=None, gate=None,
+                             dh=None, residual_scale=1.0, branch_scale=1.0, ws=None, out=None):
+    """Gradients of dora_block_norm from its x, h and factors.  dh: the gradient that reaches h
+    along the residual stream.  Returns dict(dx, dresidual, dw_pre) with "dw_post" and "dgate"
+    where there is a w_post and a gate; dw are fp32, dgate has the gate's shape and type.  out: a
+    dict of preallocated outputs, dx and dresidual at least (out["dresidual"] may be dh)."""
+    dev, T, d, dt, rows = _block_inputs(x, w_pre, w_post, gate)
+    f32 = torch.float32
+    _need("dy", dy, dev, x.dtype, T, d)
+    _need("h", h, dev, x.dtype, T, d)
+    _need("rstd_pre", rstd_pre, dev, f32, T)
+    if w_post is not None:
+        if rstd_post is None:
+            raise ValueError("w_post comes with rstd_post")
+        _need("rstd_post", rstd_post, dev, f32, T)
+    if dh is not None:
+        _need("dh", dh, dev, x.dtype, T, d)
+    kinds = {"dx": (x.dtype, T, d), "dresidual": (x.dtype, T, d), "dw_pre": (f32, d)}
+    if w_post is not None:
+        kinds["dw_post"] = (f32, d)
+    if gate is not None:
+        kinds["dgate"] = (x.dtype, *gate.shape)
+    if out is None:
+        out = {k: torch.empty(*v[1:], dtype=v[0], device=dev) for k, v in kinds.items()}
+    else:
+        if "dx" not in out or "dresidual" not in out:
+            raise ValueError("out needs dx and dresidual")
+        for k, t in out.items():
+            if k not in kinds:
+                raise ValueError(f"out has no place for {k!r}")
+            _need(k, t, dev, *kinds[k])
+    if _need_ws(ws, dev) is None:
+        need = dora_block_norm_backward_workspace(T, d, rows, dt)
+        ws = _ws(need, dev) if need > 0 else None
+    _launch(dev, lib().dora_block_norm_backward, _at(dy), _at(dh), _at(x), _at(h), _at(w_post),
+            _at(gate), rows, _at(w_pre), _at(rstd_post) if w_post is not None else None,
+            _at(rstd_pre), float(residual_scale), float(branch_scale), T, d, dt, _at(out["dx"]),
+            _at(out["dresidual"]), _at(out.get("dgate")), _at(out.get("dw_post")),
+            _at(out.get("dw_pre")), _at(ws), 0 if ws is None else ws.numel())
     return out

@@ -422,6 +422,51 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
                              int64_t d_out, int64_t r, int dtype, void *dx, void *dA, void *dB,
                              float *dm, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * dora_block_norm - the norms on both sides of a residual addition, behind one
+ * block and in front of the next (dora_rmsnorm is the one in front alone):
+ *     u = w_post (.) x / sqrt(mean_j x_j^2 + eps)        (u = x without w_post)
+ *     h = residual_scale residual + branch_scale gate (.) u
+ *                                formed in fp32, rounded to `dtype`
+ *     y = w_pre (.) h / sqrt(mean_j h_j^2 + eps)         of the rounded h
+ *   x (the block's output), residual [T, d], w_post (nullable), w_pre [d],
+ *   h, y [T, d] in `dtype`.  gate (nullable, then 1): [ceil(T / gate_rows), d] in
+ *   `dtype` (one row with T = 0), token t uses row t / gate_rows: gate_rows = T is
+ *   a gate a channel, 1 a gate a token and channel, and the length of sequences of
+ *   one length a gate vector for each.  rstd_post, rstd_pre [T] fp32 (each NULL to
+ *   skip): the two factors 1 / sqrt(...), for the backward.  eps finite, >= 0; rows
+ *   of any magnitude.  h may be residual itself, y may be x itself; no other
+ *   overlap.
+ *
+ * dora_block_norm_backward - its gradients, from the x, h and factors of the
+ * forward; dy is the gradient of y, dh (nullable) the one that reaches h along the
+ * residual stream:
+ *     Dh        = dh + rstd_pre (w_pre dy - hath mean_j(w_pre dy hath)),
+ *                                                     hath = h rstd_pre
+ *     dresidual = residual_scale Dh
+ *     du        = branch_scale gate (.) Dh
+ *     dx        = rstd_post (w_post du - hatx mean_j(w_post du hatx)),
+ *                                    hatx = x rstd_post   (du without w_post)
+ *     dgate     = sum branch_scale Dh (.) u   over the tokens of a gate row
+ *     dw_post   = sum_t du hatx,  dw_pre = sum_t dy hath
+ *   dx, dresidual [T, d], dgate (shaped as gate) in `dtype`; dw_post, dw_pre [d]
+ *   fp32; the last three NULL to skip.  Dh and du stay in fp32 throughout.
+ *   dresidual may be dh itself.  T = 0 gives zeros.
+ *   ws: dora_block_norm_backward_workspace(T, d, gate_rows, dtype) bytes, with
+ *   gate_rows = 0 for no gate (0 bytes: ws may be NULL).
+ */
+int dora_block_norm(const void *x, const void *residual, const void *w_post, const void *gate,
+                    int64_t gate_rows, const void *w_pre, float residual_scale, float branch_scale,
+                    float eps, int64_t T, int64_t d, int dtype, void *h, void *y, float *rstd_post,
+                    float *rstd_pre, void *stream);
+size_t dora_block_norm_backward_workspace(int64_t T, int64_t d, int64_t gate_rows, int dtype);
+int dora_block_norm_backward(const void *dy, const void *dh, const void *x, const void *h,
+                             const void *w_post, const void *gate, int64_t gate_rows,
+                             const void *w_pre, const float *rstd_post, const float *rstd_pre,
+                             float residual_scale, float branch_scale, int64_t T, int64_t d,
+                             int dtype, void *dx, void *dresidual, void *dgate, float *dw_post,
+                             float *dw_pre, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

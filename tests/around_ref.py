@@ -1,0 +1,88 @@
+"""Plain fp64 forms of the operators around a module, for their tests (CPU tensors).
+
+Written from the formulas: the norms on both sides of a residual addition and
+their gradients.  Each comes with what its error bound needs."""
+import torch
+
+U = 2.0 ** -24
+
+
+def half(dt):
+    """Half a step of a type, relative: the most one rounding is off by."""
+    return torch.finfo(dt).eps / 2
+
+
+def sum_error(d):
+    """A row's sum of d terms in fp32 by partial sums of at most d / 64 + 64 terms."""
+    return (d / 64 + 64) * U
+
+
+def _gate(gate, T, d):
+    if gate is None:
+        return torch.ones(1, 1, dtype=torch.float64)
+    g = gate.double().reshape(-1, d)
+    return g.repeat_interleave(max(T // g.shape[0], 1), dim=0)[:T]
+
+
+def rms_factor(v, eps):
+    v = v.double()
+    return ((v * v).mean(dim=1) + eps).rsqrt()
+
+
+def block_h(x, res, w_post, gate, a, b, eps):
+    """(h unrounded, its bound for an fp32 evaluation rounded to x's type)."""
+    T, d = x.shape
+    u = x.double()
+    E = 0.0
+    if w_post is not None:
+        u = u * rms_factor(x, eps)[:, None] * w_post.double()
+        E = sum_error(d) + 5 * U
+    branch = b * _gate(gate, T, d) * u
+    h = a * res.double() + branch
+    bound = branch.abs() * (E + 4 * U) + (a * res.double()).abs() * 3 * U
+    return h, bound + (h.abs() + bound) * half(x.dtype)
+
+
+def block_grad(dy, dh, x, h, w_pre, r2, w_post, r1, gate, a, b):
+    """{name: (gradient, bound)} from the stored h and the kept factors r1, r2."""
+    T, d = x.shape
+    dt = x.dtype
+    dy, x, h, w2, r2 = dy.double(), x.double(), h.double(), w_pre.double(), r2.double()[:, None]
+    dh = torch.zeros_like(dy) if dh is None else dh.double()
+    E = sum_error(d) + 8 * U
+    hath = h * r2
+    wdy = w2 * dy
+    m1 = (wdy * hath).mean(1, keepdim=True)
+    e1 = E * (wdy * hath).abs().mean(1, keepdim=True)
+    Dh = dh + r2 * (wdy - m1 * hath)
+    eD = 8 * U * (dh.abs() + r2 * (wdy.abs() + (m1 * hath).abs())) + r2 * hath.abs() * e1
+    each = dy * hath
+    out = {"dresidual": (a * Dh, abs(a) * eD + (a * Dh).abs() * (half(dt) + 2 * U)),
+           "dw_pre": (each.sum(0), (T + 8) * U * each.abs().sum(0))}
+    G = _gate(gate, T, d)
+    w1 = torch.ones(d, dtype=torch.float64) if w_post is None else w_post.double()
+    f1 = torch.ones(T, 1, dtype=torch.float64) if w_post is None else r1.double()[:, None]
+    hatx = x * f1
+    if gate is not None:
+        n = gate.numel() // d
+        each, err = b * Dh * hatx * w1, abs(b) * eD * (hatx * w1).abs()
+        fold = lambda t: t.reshape(n, -1, d).sum(1).reshape(gate.shape)  # noqa: E731
+        g = fold(each)
+        e = fold(err) + (T // max(n, 1) + 10) * U * fold(each.abs())
+        out["dgate"] = (g, e + (g.abs() + e) * half(dt))
+    du = b * G * Dh
+    edu = (b * G).abs() * eD + 4 * U * du.abs()
+    if w_post is None:
+        out["dx"] = (du, edu + (du.abs() + edu) * half(dt))
+        return out
+    each = du * hatx
+    out["dw_post"] = (each.sum(0), (edu * hatx.abs()).sum(0) + (T + 8) * U * each.abs().sum(0))
+    k = (b * G * w1 * hatx).abs()
+    A = (k * (dh.abs() + r2 * wdy.abs())).mean(1, keepdim=True)
+    B = (k * r2 * hath.abs()).mean(1, keepdim=True)
+    m2 = (w1 * du * hatx).mean(1, keepdim=True)
+    e2 = E * (A + m1.abs() * B) + B * e1
+    dx = f1 * (w1 * du - m2 * hatx)
+    e = f1 * (w1.abs() * edu + 8 * U * ((w1 * du).abs() + (m2 * hatx).abs()) + hatx.abs() * e2)
+    out["dx"] = (dx, e + (dx.abs() + e) * half(dt))
+    return out

@@ -1,0 +1,109 @@
+"""CPU: the calls around a module refuse bad arguments on the host (fake
+pointers, nothing is launched), size their workspaces, and the plain forms
+that their GPU tests compare with agree with differentiation."""
+import ctypes
+
+import pytest
+import torch
+
+import around_ref as R
+from dora_adapter_amd import dora as D
+
+E_NULL, E_SHAPE, E_DTYPE, E_ALIGN, E_WS, E_ALIAS, E_VALUE = 1, 2, 3, 4, 5, 6, 8
+F32, BF16 = 0, 1
+FAKE = 1 << 40
+AT = [FAKE + (k << 33) for k in range(24)]
+
+
+def _p(addr):
+    return ctypes.c_void_p(addr)
+
+
+def block(x=AT[0], res=AT[1], w1=AT[2], gate=AT[3], rows=4, w2=AT[4], a=1.0, b=1.0, eps=1e-6, T=16,
+          d=64, dt=BF16, h=AT[5], y=AT[6], r1=AT[7], r2=AT[8]):
+    return D.lib().dora_block_norm(_p(x), _p(res), _p(w1), _p(gate), rows, _p(w2), a, b, eps, T, d,
+                                   dt, _p(h), _p(y), _p(r1), _p(r2), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"x": 0}, E_NULL), ({"res": 0}, E_NULL), ({"w2": 0}, E_NULL), ({"h": 0}, E_NULL),
+    ({"y": 0}, E_NULL), ({"dt": 2}, E_DTYPE), ({"T": -1}, E_SHAPE), ({"d": 0}, E_SHAPE),
+    ({"T": 1 << 31}, E_SHAPE), ({"rows": 0}, E_SHAPE), ({"rows": -3}, E_SHAPE),
+    ({"rows": 1 << 31}, E_SHAPE), ({"eps": -1e-6}, E_VALUE), ({"eps": float("nan")}, E_VALUE),
+    ({"eps": float("inf")}, E_VALUE), ({"a": float("nan")}, E_VALUE), ({"b": float("inf")}, E_VALUE),
+    ({"w1": 0}, E_VALUE),                     # rstd_post without it
+    ({"x": AT[0] + 8}, E_ALIGN), ({"gate": AT[3] + 2}, E_ALIGN), ({"r2": AT[8] + 4}, E_ALIGN),
+    ({"h": AT[1] + 16}, E_ALIAS), ({"h": AT[0]}, E_ALIAS), ({"y": AT[0] + 64}, E_ALIAS),
+    ({"y": AT[1]}, E_ALIAS), ({"y": AT[5]}, E_ALIAS), ({"y": AT[2]}, E_ALIAS),
+    ({"h": AT[3] + 3 * 128}, E_ALIAS),        # the last of four gate rows
+    ({"r1": AT[0]}, E_ALIAS), ({"r1": AT[8]}, E_ALIAS), ({"r2": AT[4] + 64}, E_ALIAS),
+])
+def test_block_norm_refuses(kw, code):
+    assert block(**kw) == code
+    assert D.lib().dora_last_error()
+
+
+def block_bwd(dy=AT[0], dh=AT[1], x=AT[2], h=AT[3], w1=AT[4], gate=AT[5], rows=4, w2=AT[6], r1=AT[7],
+              r2=AT[8], a=1.0, b=1.0, T=16, d=64, dt=BF16, dx=AT[9], dres=AT[10], dgate=AT[11],
+              dw1=AT[12], dw2=AT[13], ws=AT[14], ws_bytes=1 << 24):
+    return D.lib().dora_block_norm_backward(
+        _p(dy), _p(dh), _p(x), _p(h), _p(w1), _p(gate), rows, _p(w2), _p(r1), _p(r2), a, b, T, d, dt,
+        _p(dx), _p(dres), _p(dgate), _p(dw1), _p(dw2), _p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"dy": 0}, E_NULL), ({"x": 0}, E_NULL), ({"h": 0}, E_NULL), ({"w2": 0}, E_NULL),
+    ({"r1": 0}, E_NULL), ({"r2": 0}, E_NULL), ({"dx": 0}, E_NULL), ({"dres": 0}, E_NULL),
+    ({"dt": 7}, E_DTYPE), ({"d": -4}, E_SHAPE), ({"rows": 0}, E_SHAPE),
+    ({"a": float("inf")}, E_VALUE), ({"w1": 0}, E_VALUE), ({"gate": 0}, E_VALUE),
+    ({"ws": 0}, E_WS), ({"ws_bytes": 64}, E_WS), ({"ws": AT[14] + 8}, E_ALIGN),
+    ({"dw2": AT[13] + 4}, E_ALIGN), ({"dx": AT[0]}, E_ALIAS), ({"dx": AT[1]}, E_ALIAS),
+    ({"dx": AT[2]}, E_ALIAS), ({"dres": AT[1] + 16}, E_ALIAS), ({"dres": AT[3]}, E_ALIAS),
+    ({"dres": AT[9] + 512}, E_ALIAS), ({"dgate": AT[5]}, E_ALIAS), ({"dgate": AT[9]}, E_ALIAS),
+    ({"dw1": AT[13]}, E_ALIAS), ({"dw1": AT[4]}, E_ALIAS), ({"ws": AT[2]}, E_ALIAS),
+    ({"ws": AT[1]}, E_ALIAS), ({"ws": AT[12]}, E_ALIAS),
+])
+def test_block_norm_backward_refuses(kw, code):
+    assert block_bwd(**kw) == code
+    assert D.lib().dora_last_error()
+
+
+def test_block_norm_workspaces():
+    q = D.dora_block_norm_backward_workspace
+    assert q(-1, 64, 0, BF16) == 0 and q(4, 0, 0, BF16) == 0 and q(4, 64, -1, BF16) == 0
+    assert q(4, 64, 0, 9) == 0
+    # sums of a few rows a workgroup: never more than the matrix in fp32, about
+    for T, d in ((8192, 8192), (65536, 128), (4096, 28672), (100000, 40000)):
+        for rows in (0, 1, 2, 47, 1000, T):
+            for dt in (F32, BF16):
+                assert q(T, d, rows, dt) <= 2 * T * d * 4 + (1 << 20), (T, d, rows, dt)
+    assert q((1 << 31) - 1, (1 << 31) - 1, 3, BF16) > 0
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [None, (20,), (6, 20), (2, 20)])
+def test_plain_block_gradients_are_those_of_differentiation(post, gate):
+    g = torch.Generator().manual_seed(3)
+    T, d, eps, a, b = 6, 20, 1e-3, 0.75, 1.5
+
+    def leaf(*s):
+        return torch.randn(*s, generator=g, dtype=torch.float64, requires_grad=True)
+
+    x, res, w1, w2 = leaf(T, d), leaf(T, d), leaf(d), leaf(d)
+    gt = None if gate is None else leaf(*gate)
+    dy, dh = torch.randn(T, d, generator=g).double(), torch.randn(T, d, generator=g).double()
+    h, _ = R.block_h(x, res, w1 if post else None, gt, a, b, eps)
+    r2 = R.rms_factor(h, eps)
+    y = h * r2[:, None] * w2
+    ((y * dy).sum() + (h * dh).sum()).backward()
+    r1 = R.rms_factor(x, eps)
+    with torch.no_grad():
+        ref = R.block_grad(dy, dh, x, h, w2, r2, w1 if post else None, r1, gt, a, b)
+    leaves = {"dx": x, "dresidual": res, "dw_pre": w2}
+    if post:
+        leaves["dw_post"] = w1
+    if gate is not None:
+        leaves["dgate"] = gt
+    assert set(ref) == set(leaves)
+    for k, t in leaves.items():
+        assert torch.allclose(ref[k][0], t.grad, rtol=1e-10, atol=1e-12), k
