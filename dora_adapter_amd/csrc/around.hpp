@@ -27,7 +27,7 @@ struct BlockNormPlan {
     int64_t slots;     // partial sums of gate rows otherwise
     size_t o_pre, o_post, o_gate, o_mean, bytes;
 };
-BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows, int bf16);
+BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows);
 struct BlockNormGradArgs {
     const void *dy, *dh, *x, *h, *w_pre, *w_post, *gate;  // dh, w_post, gate may be null
     const float *rstd_pre, *rstd_post;

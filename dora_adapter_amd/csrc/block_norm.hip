@@ -201,115 +201,170 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_kernel(BlockNormArgs 
 }
 
 // --------------------------------------------------------------- the gradients
-// A row's eight columns as the gradient reads them, and its vectors of weights.
+// A row's eight columns as the gradient reads them.
 template <typename T>
 struct GradVec {
-    Raw8<T> dy, dh, x, h;
+    Raw8<T> dy, dh, x, h, gate;  // gate: where every row has its own
 };
+// A thread's columns: w_pre, and what scales Dh: c = b w_post gate (the gate where rows share
+// it, w_post and gate 1 where there are none).
 template <typename T>
 struct GradWeights {
-    Raw8<T> pre, post, gate;
+    Raw8<T> pre;
+    float c[8];
 };
+// What the sums need of the scalars.
+struct GradScalars {
+    float r1, r2;
+    bool with_dh;
+};
+
+// GATE: 0 none, 1 rows share gate rows, 2 a gate row of its own each.
+template <bool POST, int GATE, typename T>
+__device__ __forceinline__ GradWeights<T> grad_weights(const BlockNormGradArgs &a, int64_t grow,
+                                                       int64_t j, int cnt)
+{
+    GradWeights<T> w;
+    w.pre.template load<true>(static_cast<const T *>(a.w_pre) + j, cnt);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        w.c[q] = a.branch_scale;
+    auto times = [&](const T *m) {
+        Raw8<T> r;
+        r.template load<true>(m + j, cnt);
+        float f[8];
+        r.get(f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            w.c[q] *= f[q];
+    };
+    if constexpr (POST)
+        times(static_cast<const T *>(a.w_post));
+    if constexpr (GATE == 1)
+        times(static_cast<const T *>(a.gate) + grow * a.d);
+    return w;
+}
+
+template <bool POST, int GATE, typename T>
+__device__ __forceinline__ void grad_load(GradVec<T> &v, const BlockNormGradArgs &a, int64_t at, int cnt)
+{
+    v.dy.load(static_cast<const T *>(a.dy) + at, cnt);
+    v.h.load(static_cast<const T *>(a.h) + at, cnt);
+    if constexpr (POST || GATE != 0)
+        v.x.load(static_cast<const T *>(a.x) + at, cnt);
+    if (a.dh != nullptr)
+        v.dh.load(static_cast<const T *>(a.dh) + at, cnt);
+    if constexpr (GATE == 2)
+        v.gate.load(static_cast<const T *>(a.gate) + at, cnt);
+}
+
+// Dh before m1 is known: dh_in + w_pre dy / rms(h); and hat(h).
+template <typename T>
+__device__ __forceinline__ void grad_front(const GradVec<T> &v, const GradWeights<T> &w,
+                                           const GradScalars &k, float (&dy)[8], float (&hh)[8],
+                                           float (&e)[8], float &s1)
+{
+    float wp[8];
+    v.dy.get(dy);
+    v.h.get(hh);
+    w.pre.get(wp);
+    if (k.with_dh) {
+        v.dh.get(e);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            e[q] = 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        hh[q] *= k.r2;
+        const float wdy = dy[q] * wp[q];
+        s1 = __fmaf_rn(wdy, hh[q], s1);
+        e[q] = __fmaf_rn(k.r2, wdy, e[q]);
+    }
+}
+
 // The row's three sums, from which m1 and m2 follow in one reduction: with
-// k = b gate w_post hat(x), m2 is the mean of k dh, and dh is linear in m1:
-//   s1 = sum w_pre dy hat(h),  sa = sum k (dh_in + w_pre dy / rms(h)),
-//   sb = sum k hat(h) / rms(h),   m1 = s1 / d,  m2 = (sa - m1 sb) / d
+// k = c gate hat(x), m2 is the mean of k Dh, and Dh is linear in m1:
+//   s1 = sum w_pre dy hat(h),  sa = sum k (dh_in + w_pre dy / rms(h)),  sb = sum k hat(h),
+//   m1 = s1 / d,  m2 = (sa - m1 sb / rms(h)) / d
 struct GradSums {
     float s1, sa, sb;
 };
 
-template <bool POST, bool GATE, typename T>
+template <bool POST, int GATE, typename T>
 __device__ __forceinline__ void grad_sums(GradSums &s, const GradVec<T> &v, const GradWeights<T> &w,
-                                          bool with_dh, float r1, float r2, float b)
+                                          const GradScalars &sc)
 {
-    float dy[8], h[8], wp[8];
-    v.dy.get(dy);
-    v.h.get(h);
-    w.pre.get(wp);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        h[q] *= r2;
-        dy[q] *= wp[q];
-        s.s1 = __fmaf_rn(dy[q], h[q], s.s1);
-    }
+    float dy[8], hh[8], e[8];
+    grad_front(v, w, sc, dy, hh, e, s.s1);
     if constexpr (POST) {
-        float x[8], k[8], dh[8];
-        v.x.get(x);
-        w.post.get(k);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            k[q] *= x[q] * r1;
-        if constexpr (GATE) {
-            float g[8];
-            w.gate.get(g);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                k[q] *= g[q];
-        }
-        if (with_dh) {
-            v.dh.get(dh);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                dh[q] = 0.f;
-        }
+        float k[8], g[8];
+        v.x.get(k);
+        if constexpr (GATE == 2)
+            v.gate.get(g);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            k[q] *= b;
-            s.sa = __fmaf_rn(k[q], __fmaf_rn(r2, dy[q], dh[q]), s.sa);
-            s.sb = __fmaf_rn(k[q], r2 * h[q], s.sb);
+            k[q] *= sc.r1;
+            k[q] *= GATE == 2 ? w.c[q] * g[q] : w.c[q];
+            s.sa = __fmaf_rn(k[q], e[q], s.sa);
+            s.sb = __fmaf_rn(k[q], hh[q], s.sb);
         }
     }
 }
 
-// What is left of eight columns once m1 and m2 are known: dx and dresidual, and
-// the terms of the three column sums.
-template <bool POST, bool GATE, typename T>
-__device__ __forceinline__ void grad_apply(const GradVec<T> &v, const GradWeights<T> &w, bool with_dh,
-                                           float r1, float r2, float a, float b, float m1, float m2,
-                                           Raw8<T> &dx, Raw8<T> &dres, float (&dw2)[8],
-                                           float (&dw1)[8], float (&dg)[8])
+// What is left of eight columns once m1 and m2 are known: dx and dresidual, dw_pre's terms,
+// and z = sum Dh hat(x), from which the gradients of the gate and of w_post both follow while
+// rows share the gate: dgate = b w_post z, dw_post = b gate z.  With a gate row for
+// each row (GATE 2), z = sum gate Dh hat(x) and dgate is the row's own.
+template <bool POST, int GATE, typename T>
+__device__ __forceinline__ void grad_apply(const GradVec<T> &v, const GradWeights<T> &w,
+                                           const GradScalars &sc, float a, float m1, float m2,
+                                           Raw8<T> &dx, Raw8<T> &dres, Raw8<T> &dgate,
+                                           float (&dw2)[8], float (&z)[8])
 {
-    float dy[8], h[8], o[8], f[8];
-    v.dy.get(dy);
-    v.h.get(h);
-    w.pre.get(f);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        o[q] = 0.f;
-    if (with_dh)
-        v.dh.get(o);
+    float dy[8], hh[8], o[8], f[8], unused = 0.f;
+    grad_front(v, w, sc, dy, hh, o, unused);
+    const float back = -sc.r2 * m1;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        h[q] *= r2;
-        dw2[q] = __fmaf_rn(dy[q], h[q], dw2[q]);
-        o[q] += r2 * __fmaf_rn(-m1, h[q], f[q] * dy[q]);
+        dw2[q] = __fmaf_rn(dy[q], hh[q], dw2[q]);
+        o[q] = __fmaf_rn(back, hh[q], o[q]);
         f[q] = a * o[q];
-        o[q] *= b;
     }
     dres.set(f);
-    if constexpr (POST || GATE) {
-        float x[8];
+    float x[8], g[8];
+    if constexpr (POST || GATE != 0)
         v.x.get(x);
-        if constexpr (POST)
-            w.post.get(f);
-        float g[8];
-        if constexpr (GATE)
-            w.gate.get(g);
+    if constexpr (GATE == 2)
+        v.gate.get(g);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float xh = POST ? x[q] * r1 : x[q];
-            if constexpr (GATE) {
-                dg[q] = __fmaf_rn(o[q], POST ? xh * f[q] : xh, dg[q]);
+    for (int q = 0; q < 8; ++q) {
+        if constexpr (POST || GATE != 0) {
+            if constexpr (POST)
+                x[q] *= sc.r1;
+            if constexpr (GATE == 2) {
+                const float t = o[q] * x[q];
+                z[q] = __fmaf_rn(g[q], t, z[q]);
+                f[q] = w.c[q] * t;
                 o[q] *= g[q];
-            }
-            if constexpr (POST) {
-                dw1[q] = __fmaf_rn(o[q], xh, dw1[q]);
-                o[q] = r1 * __fmaf_rn(-m2, xh, o[q] * f[q]);
+            } else {
+                z[q] = __fmaf_rn(o[q], x[q], z[q]);
             }
         }
+        o[q] *= w.c[q];
+        if constexpr (POST)
+            o[q] = sc.r1 * __fmaf_rn(-m2, x[q], o[q]);
     }
+    if constexpr (GATE == 2)
+        dgate.set(f);
     dx.set(o);
+}
+
+// m2 from the row's sums
+__device__ __forceinline__ float grad_m2(const GradSums &s, float m1, float r2, float d)
+{
+    return __fmaf_rn(-m1 * r2, s.sb, s.sa) / d;
 }
 
 struct GradOut {  // partial sums (or, where there is one part, the sums)
@@ -319,102 +374,103 @@ struct GradOut {  // partial sums (or, where there is one part, the sums)
     int direct;
 };
 
-// One pass over rows that fit a workgroup's registers: workgroup b takes rows
-// [b chunk, (b + 1) chunk); a thread keeps its columns' weights and sums.  GATE: 0 none,
-// 1 rows share gate rows (its sum goes out where the gate row changes: rounded, or to slot b +
-// gate row of the partial sums, which no other pair has, both indices growing along the
-// rows), 2 a gate row of its own each.
-template <typename T, int VPT, bool POST, int GATE, bool PRE, int THREADS>
-__global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNormGradArgs a, GradOut out)
+// The end of a run of rows that share gate row `grow`, in workgroup `part`: the gate's gradient
+// goes out (rounded, or to slot part + grow of the partial sums, which no other pair has, both
+// indices growing along the rows), f becomes dw_post's share of z, and z is cleared.
+template <bool POST, typename T>
+__device__ __forceinline__ void grad_gate_end(const BlockNormGradArgs &a, const GradOut &out,
+                                              int64_t part, int64_t grow, int64_t j, int cnt,
+                                              float (&z)[8], float (&f)[8])
 {
-    __shared__ float red[2][3][16];
-    const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
-    const int d = static_cast<int>(a.d);
-    const bool with_dh = a.dh != nullptr;
-    auto col = [&](int i) { return (static_cast<int>(threadIdx.x) + i * threads) * 8; };
-    auto at = [&](const void *m, int64_t row, int i) { return static_cast<const T *>(m) + row * a.d + col(i); };
-    GradWeights<T> w[VPT];
-    float dw2[VPT][8], dw1[VPT][8], dg[VPT][8];
+    Raw8<T> r;
+    float g[8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int cnt = count8(d, col(i));
-        w[i].pre.template load<true>(at(a.w_pre, 0, i), cnt);
-        if constexpr (POST)
-            w[i].post.template load<true>(at(a.w_post, 0, i), cnt);
+    for (int q = 0; q < 8; ++q)
+        g[q] = a.branch_scale * z[q];
+    if constexpr (POST) {
+        r.template load<true>(static_cast<const T *>(a.gate) + grow * a.d + j, cnt);
+        r.get(f);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            dw2[i][q] = dw1[i][q] = dg[i][q] = 0.f;
-    }
-    struct Row {
-        GradVec<T> v[VPT];
-        Raw8<T> gate[VPT];
-        float r1, r2;
-    };
-    auto fetch = [&](Row &o, int64_t t) {
-        o.r2 = a.rstd_pre[t];
-        if constexpr (POST)
-            o.r1 = a.rstd_post[t];
+            f[q] *= g[q];
+        r.template load<true>(static_cast<const T *>(a.w_post) + j, cnt);
+        float w[8];
+        r.get(w);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int cnt = count8(d, col(i));
-            o.v[i].dy.load(at(a.dy, t, i), cnt);
-            o.v[i].h.load(at(a.h, t, i), cnt);
-            if constexpr (POST || GATE != 0)
-                o.v[i].x.load(at(a.x, t, i), cnt);
-            if (with_dh)
-                o.v[i].dh.load(at(a.dh, t, i), cnt);
-            if constexpr (GATE == 2)
-                o.gate[i].load(at(a.gate, t, i), cnt);
+        for (int q = 0; q < 8; ++q)
+            g[q] *= w[q];
+    }
+    if (a.dgate != nullptr) {
+        if (out.direct) {
+            r.set(g);
+            r.store(static_cast<T *>(a.dgate) + grow * a.d + j, cnt);
+        } else {
+            float *p = out.gate + (part + grow) * a.d + j;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < cnt)
+                    p[q] = g[q];
         }
-    };
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        z[q] = 0.f;
+}
+
+// One pass over rows that fit a workgroup's registers: workgroup b takes rows
+// [b chunk, (b + 1) chunk); a thread keeps its eight columns' weights and sums.
+template <typename T, bool POST, int GATE, int THREADS>
+__global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNormGradArgs a, GradOut out)
+{
+    constexpr bool FOLD = POST && GATE == 1;  // dw_post is gathered where gate rows end
+    __shared__ float red[2][3][16];
+    __shared__ float4 fold[2][FOLD ? THREADS : 1];
+    const int waves = static_cast<int>(blockDim.x) >> 6;
+    const float d = static_cast<float>(a.d);
+    const int64_t j = threadIdx.x * 8;
+    const int cnt = count8(a.d, j);
+    GradWeights<T> w;
+    float dw2[8], z[8];
+    if constexpr (GATE != 1)
+        w = grad_weights<POST, GATE, T>(a, 0, j, cnt);
+    if constexpr (FOLD)
+        fold[0][threadIdx.x] = fold[1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        dw2[q] = z[q] = 0.f;
     int64_t t = static_cast<int64_t>(blockIdx.x) * out.chunk;
     const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
     int64_t grow = 0, gend = 0;  // GATE 1: the gate row held, and the row behind its last
-    auto gate_out = [&]() {
+    auto gate_end = [&]() {
+        float f[8];
+        grad_gate_end<POST, T>(a, out, blockIdx.x, grow, j, cnt, z, f);
+        if constexpr (FOLD) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int cnt = count8(d, col(i));
-            if (out.direct) {
-                Raw8<T> o;
-                o.set(dg[i]);
-                o.store(static_cast<T *>(a.dgate) + grow * a.d + col(i), cnt);
-            } else {
-                float *p = out.gate + (blockIdx.x + grow) * a.d + col(i);
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (q < cnt)
-                        p[q] = dg[i][q];
+            for (int k = 0; k < 2; ++k) {
+                float4 p = fold[k][threadIdx.x];
+                p.x += f[4 * k];
+                p.y += f[4 * k + 1];
+                p.z += f[4 * k + 2];
+                p.w += f[4 * k + 3];
+                fold[k][threadIdx.x] = p;
             }
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                dg[i][q] = 0.f;
         }
     };
-    Row cur, nxt;
-    if (t < end)
-        fetch(cur, t);
-    for (int par = 0; t < end; par ^= 1) {
+    for (int par = 0; t < end; ++t, par ^= 1) {
+        GradVec<T> v;
+        grad_load<POST, GATE>(v, a, t * a.d + j, cnt);
+        const GradScalars sc{POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t], a.dh != nullptr};
         if constexpr (GATE == 1) {
             if (t >= gend) {
-                if (gend != 0 && a.dgate != nullptr)
-                    gate_out();
+                if (gend != 0)
+                    gate_end();
                 grow = gate_row(t, a.gate_rows, a.T);
                 gend = (grow + 1) * a.gate_rows;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-                    w[i].gate.template load<true>(at(a.gate, grow, i), count8(d, col(i)));
+                w = grad_weights<POST, GATE, T>(a, grow, j, cnt);
             }
         }
         GradSums s{0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if constexpr (GATE == 2)
-                w[i].gate = cur.gate[i];
-            grad_sums<POST, GATE != 0>(s, cur.v[i], w[i], with_dh, cur.r1, cur.r2, a.branch_scale);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (PRE && t + 1 < end)
-            fetch(nxt, t + 1);
+        grad_sums<POST, GATE>(s, v, w, sc);
         s.s1 = wave_sum(s.s1);
         if constexpr (POST) {
             s.sa = wave_sum(s.sa);
@@ -430,7 +486,11 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
                 }
             }
             __syncthreads();
-            s = GradSums{red[par][0][0], red[par][1][0], red[par][2][0]};
+            s.s1 = red[par][0][0];
+            if constexpr (POST) {
+                s.sa = red[par][1][0];
+                s.sb = red[par][2][0];
+            }
             for (int k = 1; k < waves; ++k) {
                 s.s1 += red[par][0][k];
                 if constexpr (POST) {
@@ -439,92 +499,68 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
                 }
             }
         }
-        const float m1 = s.s1 / static_cast<float>(d);
-        const float m2 = POST ? __fmaf_rn(-m1, s.sb, s.sa) / static_cast<float>(d) : 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            // (what the sums made of them would not leave the registers else)
-            forget(cur.v[i].dy);
-            forget(cur.v[i].h);
-            if constexpr (POST)
-                forget(cur.v[i].x);
-            Raw8<T> dx, dres;
-            grad_apply<POST, GATE != 0>(cur.v[i], w[i], with_dh, cur.r1, cur.r2, a.res_scale,
-                                        a.branch_scale, m1, m2, dx, dres, dw2[i], dw1[i], dg[i]);
-            const int cnt = count8(d, col(i));
-            dx.store(static_cast<T *>(a.dx) + t * a.d + col(i), cnt);
-            dres.store(static_cast<T *>(a.dres) + t * a.d + col(i), cnt);
-            if constexpr (GATE == 2) {
-                if (a.dgate != nullptr) {
-                    Raw8<T> o;
-                    o.set(dg[i]);
-                    o.store(static_cast<T *>(a.dgate) + t * a.d + col(i), cnt);
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    dg[i][q] = 0.f;
-            }
-            // one vector at a time (left free, the scheduler unpacks them all)
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        ++t;
-        if (PRE)
-            cur = nxt;
-        else if (t < end)
-            fetch(cur, t);
+        const float m1 = s.s1 / d;
+        const float m2 = POST ? grad_m2(s, m1, sc.r2, d) : 0.f;
+        // (what the sums made of them would not leave the registers else)
+        forget(v.dy);
+        forget(v.h);
+        if constexpr (POST)
+            forget(v.x);
+        Raw8<T> dx, dres, dgate;
+        grad_apply<POST, GATE>(v, w, sc, a.res_scale, m1, m2, dx, dres, dgate, dw2, z);
+        dx.store(static_cast<T *>(a.dx) + t * a.d + j, cnt);
+        dres.store(static_cast<T *>(a.dres) + t * a.d + j, cnt);
+        if (GATE == 2 && a.dgate != nullptr)
+            dgate.store(static_cast<T *>(a.dgate) + t * a.d + j, cnt);
     }
-    if constexpr (GATE == 1)
-        if (gend != 0 && a.dgate != nullptr)
-            gate_out();
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int cnt = count8(d, col(i));
-        const int64_t o = blockIdx.x * a.d + col(i);
+    if (GATE == 1 && gend != 0)
+        gate_end();
+    const int64_t o = blockIdx.x * a.d + j;
+    float f[8];
+    if constexpr (FOLD) {
+        const float4 u = fold[0][threadIdx.x], v = fold[1][threadIdx.x];
+        const float all[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (q < cnt) {
-                if (out.pre != nullptr)
-                    out.pre[o + q] = dw2[i][q];
-                if (POST && out.post != nullptr)
-                    out.post[o + q] = dw1[i][q];
-            }
+            f[q] = all[q];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            f[q] = a.branch_scale * z[q];
     }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < cnt) {
+            if (out.pre != nullptr)
+                out.pre[o + q] = dw2[q];
+            if (POST && out.post != nullptr)
+                out.post[o + q] = f[q];
+        }
 }
 
 // Rows of any width, first pass: m1 and m2 of every row.
-template <typename T, bool POST, bool GATE>
+template <typename T, bool POST, int GATE>
 __global__ void __launch_bounds__(LOOP_THREADS) block_norm_mean_kernel(BlockNormGradArgs a, float *mean)
 {
     __shared__ float red[LOOP_WAVES];
     const int64_t vecs = (a.d + 7) / 8;
     const float d = static_cast<float>(a.d);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const int64_t row = t * a.d, grow = gate_row(t, a.gate_rows, a.T) * a.d;
+        const int64_t grow = GATE == 1 ? gate_row(t, a.gate_rows, a.T) : 0;
         GradSums s{0.f, 0.f, 0.f};
-        const float r2 = a.rstd_pre[t], r1 = POST ? a.rstd_post[t] : 1.f;
+        const GradScalars sc{POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t], a.dh != nullptr};
         for (int64_t i = threadIdx.x; i < vecs; i += LOOP_THREADS) {
             const int cnt = count8(a.d, i * 8);
             GradVec<T> v;
-            GradWeights<T> w;
-            v.dy.load(static_cast<const T *>(a.dy) + row + i * 8, cnt);
-            v.h.load(static_cast<const T *>(a.h) + row + i * 8, cnt);
-            w.pre.template load<true>(static_cast<const T *>(a.w_pre) + i * 8, cnt);
-            if constexpr (POST) {
-                v.x.load(static_cast<const T *>(a.x) + row + i * 8, cnt);
-                if (a.dh != nullptr)
-                    v.dh.load(static_cast<const T *>(a.dh) + row + i * 8, cnt);
-                w.post.template load<true>(static_cast<const T *>(a.w_post) + i * 8, cnt);
-                if constexpr (GATE)
-                    w.gate.template load<true>(static_cast<const T *>(a.gate) + grow + i * 8, cnt);
-            }
-            grad_sums<POST, GATE>(s, v, w, a.dh != nullptr, r1, r2, a.branch_scale);
+            grad_load<POST, POST ? GATE : 0>(v, a, t * a.d + i * 8, cnt);
+            grad_sums<POST, GATE>(s, v, grad_weights<POST, GATE, T>(a, grow, i * 8, cnt), sc);
         }
         const float m1 = block_sum(s.s1, red, LOOP_WAVES) / d;
         float m2 = 0.f;
         if constexpr (POST) {
             s.sa = block_sum(s.sa, red, LOOP_WAVES);
             s.sb = block_sum(s.sb, red, LOOP_WAVES);
-            m2 = __fmaf_rn(-m1, s.sb, s.sa) / d;
+            m2 = grad_m2(s, m1, sc.r2, d);
         }
         if (threadIdx.x == 0) {
             mean[2 * t] = m1;
@@ -542,67 +578,52 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
         return;
     const int cnt = count8(a.d, j);
     GradWeights<T> w;
-    w.pre.template load<true>(static_cast<const T *>(a.w_pre) + j, cnt);
-    if constexpr (POST)
-        w.post.template load<true>(static_cast<const T *>(a.w_post) + j, cnt);
-    float dw2[8], dw1[8], dg[8];
+    if constexpr (GATE != 1)
+        w = grad_weights<POST, GATE, T>(a, 0, j, cnt);
+    float dw2[8], z[8], dw1[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-        dw2[q] = dw1[q] = dg[q] = 0.f;
+        dw2[q] = z[q] = dw1[q] = 0.f;
     int64_t t = static_cast<int64_t>(blockIdx.y) * out.chunk;
     const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
     int64_t grow = 0, gend = 0;
-    auto gate_out = [&]() {
-        if (out.direct) {
-            Raw8<T> o;
-            o.set(dg);
-            o.store(static_cast<T *>(a.dgate) + grow * a.d + j, cnt);
-        } else {
-            for (int q = 0; q < cnt; ++q)
-                out.gate[(blockIdx.y + grow) * a.d + j + q] = dg[q];
-        }
+    auto gate_end = [&]() {
+        float f[8];
+        grad_gate_end<POST, T>(a, out, blockIdx.y, grow, j, cnt, z, f);
+        if constexpr (POST) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            dg[q] = 0.f;
+            for (int q = 0; q < 8; ++q)
+                dw1[q] += f[q];
+        }
     };
     for (; t < end; ++t) {
-        if constexpr (GATE != 0) {
-            if (GATE == 2 || t >= gend) {
-                if (GATE == 1 && gend != 0 && a.dgate != nullptr)
-                    gate_out();
-                grow = gate_row(t, a.gate_rows, a.T);
-                gend = (grow + 1) * a.gate_rows;
-                w.gate.template load<GATE == 1>(static_cast<const T *>(a.gate) + grow * a.d + j, cnt);
-            }
+        if (GATE == 1 && t >= gend) {
+            if (gend != 0)
+                gate_end();
+            grow = gate_row(t, a.gate_rows, a.T);
+            gend = (grow + 1) * a.gate_rows;
+            w = grad_weights<POST, GATE, T>(a, grow, j, cnt);
         }
         const int64_t at = t * a.d + j;
         GradVec<T> v;
-        v.dy.load(static_cast<const T *>(a.dy) + at, cnt);
-        v.h.load(static_cast<const T *>(a.h) + at, cnt);
-        if constexpr (POST || GATE != 0)
-            v.x.load(static_cast<const T *>(a.x) + at, cnt);
-        if (a.dh != nullptr)
-            v.dh.load(static_cast<const T *>(a.dh) + at, cnt);
-        Raw8<T> dx, dres;
-        grad_apply<POST, GATE != 0>(v, w, a.dh != nullptr, POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t],
-                                    a.res_scale, a.branch_scale, out.mean[2 * t], out.mean[2 * t + 1],
-                                    dx, dres, dw2, dw1, dg);
+        grad_load<POST, GATE>(v, a, at, cnt);
+        const GradScalars sc{POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t], a.dh != nullptr};
+        Raw8<T> dx, dres, dgate;
+        grad_apply<POST, GATE>(v, w, sc, a.res_scale, out.mean[2 * t], out.mean[2 * t + 1], dx, dres,
+                               dgate, dw2, z);
         dx.store(static_cast<T *>(a.dx) + at, cnt);
         dres.store(static_cast<T *>(a.dres) + at, cnt);
-        if constexpr (GATE == 2) {
-            if (a.dgate != nullptr) {
-                Raw8<T> o;
-                o.set(dg);
-                o.store(static_cast<T *>(a.dgate) + at, cnt);
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                dg[q] = 0.f;
-        }
+        if (GATE == 2 && a.dgate != nullptr)
+            dgate.store(static_cast<T *>(a.dgate) + at, cnt);
     }
-    if constexpr (GATE == 1)
-        if (gend != 0 && a.dgate != nullptr)
-            gate_out();
+    if (GATE == 1) {
+        if (gend != 0)
+            gate_end();
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            dw1[q] = a.branch_scale * z[q];
+    }
     const int64_t o = static_cast<int64_t>(blockIdx.y) * a.d + j;
     for (int q = 0; q < cnt; ++q) {
         if (out.pre != nullptr)
@@ -688,33 +709,25 @@ hipError_t forward(const BlockNormArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Columns whose rows are held in registers: eight of 1024 threads each, or, in bf16, sixteen.
-bool grad_held(int64_t d, bool bf16) { return d <= (bf16 ? 16384 : 8192); }
+// Rows held in registers: eight columns of each of 1024 threads.
+bool grad_held(int64_t d) { return d <= 8192; }
 
 template <typename T, bool POST, int GATE>
 hipError_t backward(const BlockNormGradArgs &a, const BlockNormPlan &p, const GradOut &out, hipStream_t st)
 {
     const int64_t vecs = (a.d + 7) / 8;
     if (p.held) {
-        constexpr bool BF = sizeof(T) == 2;
-        const int vpt = BF && vecs > 512 ? 2 : 1;
         const dim3 grid(static_cast<unsigned>(p.parts)),
-            block(static_cast<unsigned>(((vecs + vpt - 1) / vpt + 63) / 64 * 64));
+            block(static_cast<unsigned>((vecs + 63) / 64 * 64));
         if (vecs <= 512)
-            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 1, POST, GATE, true, 512>), grid, block,
-                               0, st, a, out);
-        else if constexpr (!BF)
-            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 1, POST, GATE, false, 1024>), grid,
-                               block, 0, st, a, out);
-        else if (vecs <= 1024)
-            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 2, POST, GATE, true, 512>), grid, block,
-                               0, st, a, out);
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, POST, GATE, 512>), grid, block, 0, st, a,
+                               out);
         else
-            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, 2, POST, GATE, false, 1024>), grid,
-                               block, 0, st, a, out);
+            hipLaunchKernelGGL((block_norm_grad_held_kernel<T, POST, GATE, 1024>), grid, block, 0, st,
+                               a, out);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((block_norm_mean_kernel<T, POST, GATE != 0>),
+    hipLaunchKernelGGL((block_norm_mean_kernel<T, POST, GATE>),
                        dim3(static_cast<unsigned>(a.T < MAX_ROW_GROUPS ? a.T : MAX_ROW_GROUPS)),
                        dim3(LOOP_THREADS), 0, st, a, out.mean);
     const hipError_t e = hipGetLastError();
@@ -770,16 +783,16 @@ hipError_t launch_block_norm(int bf16, const BlockNormArgs &a, hipStream_t st)
     return bf16 ? forward<uint16_t>(a, st) : forward<float>(a, st);
 }
 
-BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows, int bf16)
+BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows)
 {
     BlockNormPlan p;
-    p.held = grad_held(d, bf16 != 0);
+    p.held = grad_held(d);
     const int64_t vecs = (d + 7) / 8;
     int64_t parts;
     if (p.held) {
         // a workgroup a CU, and the shorter the rows the more of them
-        const int most = vecs > 512 ? 1 : vecs > 128 ? 2 : vecs > 64 ? 4 : vecs > 32 ? 8 : 16;
-        const int64_t share = vecs > 128 ? T / 8 : T / 4;
+        const int most = vecs > 512 ? 1 : vecs > 128 ? 2 : vecs > 64 ? 4 : 8;
+        const int64_t share = T / 4;
         parts = share > 256 ? share : 256;
         parts = parts < 256 * most ? parts : 256 * most;
         parts = parts < T ? parts : T;

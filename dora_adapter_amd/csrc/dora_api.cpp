@@ -2320,7 +2320,7 @@ size_t dora_block_norm_backward_workspace(int64_t T, int64_t d, int64_t gate_row
 {
     if (check_dtype(dtype) || check_rows(T, d) || gate_rows < 0 || gate_rows > kMaxDim)
         return 0;
-    return plan_block_norm_grad(T, d, gate_rows, dtype == DORA_BF16).bytes;
+    return plan_block_norm_grad(T, d, gate_rows).bytes;
 }
 
 int dora_block_norm_backward(const void *dy, const void *dh, const void *x, const void *h,
@@ -2346,7 +2346,7 @@ int dora_block_norm_backward(const void *dy, const void *dh, const void *x, cons
         return fail(DORA_E_VALUE, "dw_post is asked for without w_post");
     if (dgate && !gate)
         return fail(DORA_E_VALUE, "dgate is asked for without gate");
-    const BlockNormPlan p = plan_block_norm_grad(T, d, gate ? gate_rows : 0, dtype == DORA_BF16);
+    const BlockNormPlan p = plan_block_norm_grad(T, d, gate ? gate_rows : 0);
     DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
     const size_t e = esize(dtype), rows = static_cast<size_t>(T) * d * e, r = T * sizeof(float);
     const size_t gb = gate ? gate_bytes(T, d, gate_rows, e) : 0, v = d * sizeof(float);
