@@ -23,6 +23,51 @@ namespace {
 constexpr int LOOP_THREADS = 256;
 constexpr int LOOP_WAVES = LOOP_THREADS / 64;
 
+// Sums over aligned runs of 16 lanes, and over the wave, in a fixed order (every lane gets the
+// result): lane exchanges of the vector ALU, a few cycles each, where the ones through LDS take
+// about a hundred (the forward at 8192 x 8192 in bf16: 101 -> 95 us).
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v)
+{
+    return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row16_sum(float v)
+{
+    v = add_dpp<0xb1>(v);    // lanes 1 apart (quad_perm 1 0 3 2)
+    v = add_dpp<0x4e>(v);    // 2 apart (quad_perm 2 3 0 1)
+    v = add_dpp<0x141>(v);   // the other quad of eight (row_half_mirror)
+    return add_dpp<0x140>(v);  // the other eight (row_mirror)
+}
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    v = row16_sum(v);
+    auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// N sums over a workgroup of up to 16 waves with one barrier; red [N][16] may be written again
+// behind a further one.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float (*red)[16], int waves)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = lanes_sum(v[i]);
+    if (waves == 1)
+        return;
+    const int lane = threadIdx.x & 63;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            red[i][threadIdx.x >> 6] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = row16_sum((lane & 15) < waves ? red[i][lane & 15] : 0.f);
+}
+
 // gate row of row t (no gate, or one for all rows: 0)
 __device__ __forceinline__ int64_t gate_row(int64_t t, int64_t gate_rows, int64_t T)
 {
@@ -71,12 +116,31 @@ __device__ __forceinline__ float squares8(const Raw8<T> &v, float k, float acc)
     return acc;
 }
 
+// 1 / rms of a row held as VPT vectors a thread; red [2][16], its first row written once.
+template <typename T, int VPT>
+__device__ __forceinline__ float row_rstd(const Raw8<T> (&v)[VPT], const BlockNormArgs &a,
+                                          float (*red)[16], int waves)
+{
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        ss[0] = squares8(v[i], 1.f, ss[0]);
+    group_sums(ss, red, waves);
+    return rstd_of(ss[0], static_cast<float>(a.d), a.eps, [&](float k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            sum = squares8(v[i], k, sum);
+        return block_sum(sum, red[1], waves);
+    });
+}
+
 // Rows that fit a workgroup's registers, VPT vectors a thread: everything is read before the
 // first reduction, whose wait covers it, and written once.  h may be the residual, y may be x.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
 {
-    __shared__ float red[16];
+    __shared__ float red[3][16];
     const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
     const int d = static_cast<int>(a.d);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * a.d;
@@ -98,14 +162,7 @@ __global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
     }
     float r1 = 1.f;
     if (a.w_post != nullptr) {
-        auto sum = [&](float k) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                ss = squares8(x[i], k, ss);
-            return block_sum(ss, red, waves);
-        };
-        r1 = rstd_of(sum(1.f), static_cast<float>(d), a.eps, sum);
+        r1 = row_rstd(x, a, red, waves);
         if (a.rstd_post != nullptr && threadIdx.x == 0)
             a.rstd_post[blockIdx.x] = r1;
     }
@@ -114,14 +171,7 @@ __global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
         h[i] = block_h(a, x[i], h[i], w1[i], g[i], r1);
         h[i].store(static_cast<T *>(a.h) + row + col(i), count8(d, col(i)));
     }
-    auto sum = [&](float k) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            ss = squares8(h[i], k, ss);
-        return block_sum(ss, red, waves);
-    };
-    const float r2 = rstd_of(sum(1.f), static_cast<float>(d), a.eps, sum);
+    const float r2 = row_rstd(h, a, red + 1, waves);
     if (a.rstd_pre != nullptr && threadIdx.x == 0)
         a.rstd_pre[blockIdx.x] = r2;
 #pragma unroll
@@ -219,6 +269,15 @@ struct GradScalars {
     bool with_dh;
 };
 
+// Column j of a row that starts at `base`: a scalar base and a 32-bit offset (rows of under
+// 2^30 columns).
+template <typename P>
+__device__ __forceinline__ P *in_row(P *base, unsigned int j)
+{
+    using B = std::conditional_t<std::is_const_v<P>, const char, char>;
+    return reinterpret_cast<P *>(reinterpret_cast<B *>(base) + j * static_cast<unsigned int>(sizeof(P)));
+}
+
 // GATE: 0 none, 1 rows share gate rows, 2 a gate row of its own each.
 template <bool POST, int GATE, typename T>
 __device__ __forceinline__ GradWeights<T> grad_weights(const BlockNormGradArgs &a, int64_t grow,
@@ -246,16 +305,17 @@ __device__ __forceinline__ GradWeights<T> grad_weights(const BlockNormGradArgs &
 }
 
 template <bool POST, int GATE, typename T>
-__device__ __forceinline__ void grad_load(GradVec<T> &v, const BlockNormGradArgs &a, int64_t at, int cnt)
+__device__ __forceinline__ void grad_load(GradVec<T> &v, const BlockNormGradArgs &a, int64_t row,
+                                          unsigned int j, int cnt)
 {
-    v.dy.load(static_cast<const T *>(a.dy) + at, cnt);
-    v.h.load(static_cast<const T *>(a.h) + at, cnt);
+    v.dy.load(in_row(static_cast<const T *>(a.dy) + row, j), cnt);
+    v.h.load(in_row(static_cast<const T *>(a.h) + row, j), cnt);
     if constexpr (POST || GATE != 0)
-        v.x.load(static_cast<const T *>(a.x) + at, cnt);
+        v.x.load(in_row(static_cast<const T *>(a.x) + row, j), cnt);
     if (a.dh != nullptr)
-        v.dh.load(static_cast<const T *>(a.dh) + at, cnt);
+        v.dh.load(in_row(static_cast<const T *>(a.dh) + row, j), cnt);
     if constexpr (GATE == 2)
-        v.gate.load(static_cast<const T *>(a.gate) + at, cnt);
+        v.gate.load(in_row(static_cast<const T *>(a.gate) + row, j), cnt);
 }
 
 // Dh before m1 is known: dh_in + w_pre dy / rms(h); and hat(h).
@@ -362,16 +422,26 @@ __device__ __forceinline__ void grad_apply(const GradVec<T> &v, const GradWeight
 }
 
 // m2 from the row's sums
-__device__ __forceinline__ float grad_m2(const GradSums &s, float m1, float r2, float d)
+__device__ __forceinline__ float grad_m2(const GradSums &s, float m1, float r2, float inv_d)
 {
-    return __fmaf_rn(-m1 * r2, s.sb, s.sa) / d;
+    return __fmaf_rn(-m1 * r2, s.sb, s.sa) * inv_d;
 }
 
 struct GradOut {  // partial sums (or, where there is one part, the sums)
     float *pre, *post, *gate;
     float *mean;  // rows of any width: m1 and m2 of each row
-    int64_t chunk;
+    int64_t chunk;  // rows a workgroup
     int direct;
+    // 0: workgroup b's rows are b chunk and on; else b, b + stride, ..., so that the rows in
+    // work at one time lie next to each other (chunks start a power of two apart, and their
+    // lines in the same memory channels: 16384 x 4096 in bf16 171 -> 158 us)
+    int64_t stride;
+    __device__ __forceinline__ int64_t first(int64_t b) const { return stride ? b : b * chunk; }
+    __device__ __forceinline__ int64_t end(int64_t b, int64_t T) const
+    {
+        return !stride && (b + 1) * chunk < T ? (b + 1) * chunk : T;
+    }
+    __device__ __forceinline__ int64_t step() const { return stride ? stride : 1; }
 };
 
 // The end of a run of rows that share gate row `grow`, in workgroup `part`: the gate's gradient
@@ -417,8 +487,7 @@ __device__ __forceinline__ void grad_gate_end(const BlockNormGradArgs &a, const 
         z[q] = 0.f;
 }
 
-// One pass over rows that fit a workgroup's registers: workgroup b takes rows
-// [b chunk, (b + 1) chunk); a thread keeps its eight columns' weights and sums.
+// One pass over rows that fit a workgroup's registers; a thread keeps its eight columns' weights and sums.
 template <typename T, bool POST, int GATE, int THREADS>
 __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNormGradArgs a, GradOut out)
 {
@@ -426,8 +495,8 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
     __shared__ float red[2][3][16];
     __shared__ float4 fold[2][FOLD ? THREADS : 1];
     const int waves = static_cast<int>(blockDim.x) >> 6;
-    const float d = static_cast<float>(a.d);
-    const int64_t j = threadIdx.x * 8;
+    const float inv_d = 1.f / static_cast<float>(a.d);
+    const unsigned int j = threadIdx.x * 8;
     const int cnt = count8(a.d, j);
     GradWeights<T> w;
     float dw2[8], z[8];
@@ -438,8 +507,8 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         dw2[q] = z[q] = 0.f;
-    int64_t t = static_cast<int64_t>(blockIdx.x) * out.chunk;
-    const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
+    int64_t t = out.first(blockIdx.x);
+    const int64_t end = out.end(blockIdx.x, a.T), step = out.step();
     int64_t grow = 0, gend = 0;  // GATE 1: the gate row held, and the row behind its last
     auto gate_end = [&]() {
         float f[8];
@@ -456,9 +525,9 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
             }
         }
     };
-    for (int par = 0; t < end; ++t, par ^= 1) {
+    for (int par = 0; t < end; t += step, par ^= 1) {
         GradVec<T> v;
-        grad_load<POST, GATE>(v, a, t * a.d + j, cnt);
+        grad_load<POST, GATE>(v, a, t * a.d, j, cnt);
         const GradScalars sc{POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t], a.dh != nullptr};
         if constexpr (GATE == 1) {
             if (t >= gend) {
@@ -471,36 +540,18 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
         }
         GradSums s{0.f, 0.f, 0.f};
         grad_sums<POST, GATE>(s, v, w, sc);
-        s.s1 = wave_sum(s.s1);
+        // one barrier a row: the next row writes the other half of `red`
         if constexpr (POST) {
-            s.sa = wave_sum(s.sa);
-            s.sb = wave_sum(s.sb);
+            float all[3] = {s.s1, s.sa, s.sb};
+            group_sums(all, red[par], waves);
+            s = GradSums{all[0], all[1], all[2]};
+        } else {
+            float all[1] = {s.s1};
+            group_sums(all, red[par], waves);
+            s.s1 = all[0];
         }
-        if (waves > 1) {
-            // one barrier a row: the next row writes the other half of `red`
-            if ((threadIdx.x & 63) == 0) {
-                red[par][0][threadIdx.x >> 6] = s.s1;
-                if constexpr (POST) {
-                    red[par][1][threadIdx.x >> 6] = s.sa;
-                    red[par][2][threadIdx.x >> 6] = s.sb;
-                }
-            }
-            __syncthreads();
-            s.s1 = red[par][0][0];
-            if constexpr (POST) {
-                s.sa = red[par][1][0];
-                s.sb = red[par][2][0];
-            }
-            for (int k = 1; k < waves; ++k) {
-                s.s1 += red[par][0][k];
-                if constexpr (POST) {
-                    s.sa += red[par][1][k];
-                    s.sb += red[par][2][k];
-                }
-            }
-        }
-        const float m1 = s.s1 / d;
-        const float m2 = POST ? grad_m2(s, m1, sc.r2, d) : 0.f;
+        const float m1 = s.s1 * inv_d;
+        const float m2 = POST ? grad_m2(s, m1, sc.r2, inv_d) : 0.f;
         // (what the sums made of them would not leave the registers else)
         forget(v.dy);
         forget(v.h);
@@ -508,10 +559,10 @@ __global__ void __launch_bounds__(THREADS) block_norm_grad_held_kernel(BlockNorm
             forget(v.x);
         Raw8<T> dx, dres, dgate;
         grad_apply<POST, GATE>(v, w, sc, a.res_scale, m1, m2, dx, dres, dgate, dw2, z);
-        dx.store(static_cast<T *>(a.dx) + t * a.d + j, cnt);
-        dres.store(static_cast<T *>(a.dres) + t * a.d + j, cnt);
+        dx.store(in_row(static_cast<T *>(a.dx) + t * a.d, j), cnt);
+        dres.store(in_row(static_cast<T *>(a.dres) + t * a.d, j), cnt);
         if (GATE == 2 && a.dgate != nullptr)
-            dgate.store(static_cast<T *>(a.dgate) + t * a.d + j, cnt);
+            dgate.store(in_row(static_cast<T *>(a.dgate) + t * a.d, j), cnt);
     }
     if (GATE == 1 && gend != 0)
         gate_end();
@@ -544,7 +595,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_mean_kernel(BlockNorm
 {
     __shared__ float red[LOOP_WAVES];
     const int64_t vecs = (a.d + 7) / 8;
-    const float d = static_cast<float>(a.d);
+    const float inv_d = 1.f / static_cast<float>(a.d);
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t grow = GATE == 1 ? gate_row(t, a.gate_rows, a.T) : 0;
         GradSums s{0.f, 0.f, 0.f};
@@ -552,15 +603,15 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_mean_kernel(BlockNorm
         for (int64_t i = threadIdx.x; i < vecs; i += LOOP_THREADS) {
             const int cnt = count8(a.d, i * 8);
             GradVec<T> v;
-            grad_load<POST, POST ? GATE : 0>(v, a, t * a.d + i * 8, cnt);
+            grad_load<POST, POST ? GATE : 0>(v, a, t * a.d + i * 8, 0u, cnt);
             grad_sums<POST, GATE>(s, v, grad_weights<POST, GATE, T>(a, grow, i * 8, cnt), sc);
         }
-        const float m1 = block_sum(s.s1, red, LOOP_WAVES) / d;
+        const float m1 = block_sum(s.s1, red, LOOP_WAVES) * inv_d;
         float m2 = 0.f;
         if constexpr (POST) {
             s.sa = block_sum(s.sa, red, LOOP_WAVES);
             s.sb = block_sum(s.sb, red, LOOP_WAVES);
-            m2 = grad_m2(s, m1, sc.r2, d);
+            m2 = grad_m2(s, m1, sc.r2, inv_d);
         }
         if (threadIdx.x == 0) {
             mean[2 * t] = m1;
@@ -569,7 +620,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_mean_kernel(BlockNorm
     }
 }
 
-// Second pass: workgroup (i, b) walks rows [b chunk, (b + 1) chunk) of its 2048 columns.
+// Second pass: workgroup (i, b) walks its rows at 2048 columns.
 template <typename T, bool POST, int GATE>
 __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNormGradArgs a, GradOut out)
 {
@@ -584,8 +635,8 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         dw2[q] = z[q] = dw1[q] = 0.f;
-    int64_t t = static_cast<int64_t>(blockIdx.y) * out.chunk;
-    const int64_t end = t + out.chunk < a.T ? t + out.chunk : a.T;
+    int64_t t = out.first(blockIdx.y);
+    const int64_t end = out.end(blockIdx.y, a.T), step = out.step();
     int64_t grow = 0, gend = 0;
     auto gate_end = [&]() {
         float f[8];
@@ -596,7 +647,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
                 dw1[q] += f[q];
         }
     };
-    for (; t < end; ++t) {
+    for (; t < end; t += step) {
         if (GATE == 1 && t >= gend) {
             if (gend != 0)
                 gate_end();
@@ -606,7 +657,7 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
         }
         const int64_t at = t * a.d + j;
         GradVec<T> v;
-        grad_load<POST, GATE>(v, a, at, cnt);
+        grad_load<POST, GATE>(v, a, at, 0u, cnt);
         const GradScalars sc{POST ? a.rstd_post[t] : 1.f, a.rstd_pre[t], a.dh != nullptr};
         Raw8<T> dx, dres, dgate;
         grad_apply<POST, GATE>(v, w, sc, a.res_scale, out.mean[2 * t], out.mean[2 * t + 1], dx, dres,
@@ -633,8 +684,9 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
     }
 }
 
-// The partial sums in order: blockIdx.y 0 dw_pre, 1 dw_post, 2 + g gate row g; 64 columns a
-// workgroup, whose 16 waves take every 16th part each.
+// The partial sums in order: blockIdx.y 0 dw_pre, 1 dw_post, then the gate rows, one at a time or,
+// where they have few slots (a slot at least a chunk of rows, see the plan), 16 of them, a wave
+// each; 64 columns a workgroup, whose 16 waves take every 16th part each.
 template <typename T>
 __global__ void __launch_bounds__(1024)
     block_norm_finish_kernel(GradOut part, int parts, int64_t Tn, int64_t d, int64_t gate_rows,
@@ -642,11 +694,13 @@ __global__ void __launch_bounds__(1024)
 {
     __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t g = static_cast<int64_t>(blockIdx.y) - 2;
+    const bool few = gate_rows <= 16 * part.chunk && gate_rows < Tn;
+    const int64_t g = blockIdx.y < 2 ? -1 : few ? (blockIdx.y - 2ll) * 16 + wave : blockIdx.y - 2ll;
+    const bool alone = few && g >= 0;  // the wave sums by itself
     const float *from = blockIdx.y == 0 ? part.pre : part.post;
     int64_t count = parts;
     if (g >= 0) {
-        if (dgate == nullptr)
+        if (dgate == nullptr || (alone && g * gate_rows >= Tn))
             return;
         const int64_t first = g * gate_rows;
         const int64_t last = (first + gate_rows < Tn ? first + gate_rows : Tn) - 1;
@@ -661,17 +715,19 @@ __global__ void __launch_bounds__(1024)
         float acc = 0.f;
         if (j < d) {
 #pragma unroll 8
-            for (int64_t p = wave; p < count; p += 16)
+            for (int64_t p = alone ? 0 : wave; p < count; p += alone ? 1 : 16)
                 acc += from[p * d + j];
         }
-        __syncthreads();  // the last columns' sums have been read
-        sums[wave][lane] = acc;
-        __syncthreads();
-        if (wave == 0 && j < d) {
+        if (!alone) {
+            __syncthreads();  // the last columns' sums have been read
+            sums[wave][lane] = acc;
+            __syncthreads();
             acc = sums[0][lane];
 #pragma unroll
             for (int k = 1; k < 16; ++k)
                 acc += sums[k][lane];
+        }
+        if ((alone || wave == 0) && j < d) {
             if (g >= 0) {
                 if constexpr (sizeof(T) == 2)
                     dgate[g * d + j] = f32_to_bf16(acc);
@@ -747,7 +803,8 @@ hipError_t backward_any(const BlockNormGradArgs &a, const BlockNormPlan &p, char
     auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
     const GradOut out{a.dw_pre == nullptr ? nullptr : (one ? a.dw_pre : at(p.o_pre)),
                       a.dw_post == nullptr ? nullptr : (one ? a.dw_post : at(p.o_post)),
-                      at(p.o_gate), at(p.o_mean), p.chunk, p.direct};
+                      at(p.o_gate), at(p.o_mean), p.chunk, p.direct,
+                      a.gate_rows > 1 && a.gate_rows < a.T ? 0 : p.parts};
     const int gate = a.gate == nullptr ? 0 : (a.gate_rows == 1 ? 2 : 1);
     hipError_t e = hipSuccess;
     if (a.T == 0)
@@ -765,9 +822,10 @@ hipError_t backward_any(const BlockNormGradArgs &a, const BlockNormPlan &p, char
     if (e != hipSuccess || (!slots && !sums))
         return e;
     const int64_t blocks = (a.d + 63) / 64, rows = !slots ? 0 : a.T == 0 ? 1 : (a.T + a.gate_rows - 1) / a.gate_rows;
+    const bool few = a.gate_rows <= 16 * p.chunk && a.gate_rows < a.T;
     hipLaunchKernelGGL((block_norm_finish_kernel<T>),
                        dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536),
-                            static_cast<unsigned>(2 + rows)),
+                            static_cast<unsigned>(2 + (few ? (rows + 15) / 16 : rows))),
                        dim3(1024), 0, st, out, p.parts, a.T, a.d, a.gate_rows,
                        sums ? a.dw_pre : nullptr, sums ? a.dw_post : nullptr,
                        slots ? static_cast<T *>(a.dgate) : nullptr);
