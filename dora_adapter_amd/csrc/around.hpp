@@ -39,4 +39,23 @@ struct BlockNormGradArgs {
 hipError_t launch_block_norm_grad(int bf16, const BlockNormGradArgs &a, const BlockNormPlan &p,
                                   void *ws, hipStream_t st);
 
+// --------------------------------------------------- fourbit.hip, gemm_fourbit.hip
+// 4-bit rows: e2m1 codes two a byte, rows of whole groups (`groups` of them), bf16 scales.
+hipError_t launch_quantize_fourbit(int bf16, const void *x, int64_t rows, int64_t d, int group,
+                                   uint8_t *codes, uint16_t *scale, hipStream_t st);
+// ldo: elements between rows of `out`.
+hipError_t launch_dequantize_fourbit(int bf16, const uint8_t *codes, const uint16_t *scale,
+                                     int64_t rows, int64_t d, int group, void *out, int64_t ldo,
+                                     hipStream_t st);
+struct FourbitArgs {
+    const void *x;  // [T, d_in]
+    const uint8_t *codes;
+    const uint16_t *scale;
+    void *y;  // [T, d_out]
+    int64_t T, d_in, d_out;
+    int64_t groups;
+    int group;
+};
+hipError_t launch_linear_fourbit(int bf16, const FourbitArgs &a, hipStream_t st);
+
 }  // namespace dora

@@ -2369,4 +2369,149 @@ int dora_block_norm_backward(const void *dy, const void *dh, const void *x, cons
     return DORA_OK;
 }
 
+// ------------------------------------------------------------- 4-bit weights
+namespace {
+
+int check_fourbit_group(int64_t group)
+{
+    if (group < 32 || group > 512 || (group & (group - 1)) != 0)
+        return fail(DORA_E_SHAPE, "group %lld is not a power of two from 32 to 512", (long long)group);
+    return DORA_OK;
+}
+
+// Bytes of the codes and of the scales of a matrix.
+size_t fourbit_codes(int64_t rows, int64_t d, int64_t group)
+{
+    return static_cast<size_t>(rows) * ((d + group - 1) / group) * (group / 2);
+}
+size_t fourbit_scales(int64_t rows, int64_t d, int64_t group)
+{
+    return static_cast<size_t>(rows) * ((d + group - 1) / group) * 2;
+}
+
+// The products of more tokens: the weight's rows in `dtype`, a panel of them at a time (128 MiB
+// at most, or 256 rows), through the linear layer's own product.
+struct FourbitPlan {
+    bool rows;          // few tokens: straight from the codes
+    int64_t panel = 0;  // rows of the weight at a time
+    GPlan g, last;
+    size_t o_part = 0, bytes = 0;
+};
+constexpr int64_t kFourbitTokens = 64;
+constexpr int64_t kFourbitPanel = int64_t(128) << 20;
+
+FourbitPlan plan_fourbit(int64_t T, int64_t d_in, int64_t d_out, int dtype)
+{
+    FourbitPlan p;
+    p.rows = T <= kFourbitTokens;
+    if (p.rows)
+        return p;
+    const bool bf = dtype == DORA_BF16;
+    const int64_t row = d_in * static_cast<int64_t>(esize(dtype));
+    const int64_t most = std::max<int64_t>(kFourbitPanel / row / 256 * 256, 256);
+    const int64_t count = (d_out + most - 1) / most;
+    p.panel = count == 1 ? d_out : ((d_out + count - 1) / count + 255) / 256 * 256;
+    const int64_t part = count == 1 ? T * d_out : kNoSplit;
+    p.g = plan_gemm(bf, nt_shape(T, p.panel, d_in), part);
+    p.last = p.g;
+    if (d_out % p.panel)
+        p.last = plan_gemm(bf, nt_shape(T, d_out % p.panel, d_in), part);
+    Carve cv;
+    cv.take(static_cast<size_t>(p.panel) * row);
+    p.o_part = cv.take(p.g.splits > 1 ? static_cast<size_t>(p.g.splits) * T * d_out * 4 : 0);
+    p.bytes = cv.off;
+    return p;
+}
+
+}  // namespace
+
+int dora_quantize_fourbit(const void *x, int64_t rows, int64_t d, int dtype, int64_t group,
+                          void *codes, void *scale, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(rows, d));
+    DORA_CHECK(check_fourbit_group(group));
+    const bool any = rows > 0;
+    DORA_CHECK(check_ptrs({{x, "x", any}, {codes, "codes", any}, {scale, "scale", any}}));
+    DORA_CHECK(check_disjoint({{{codes, fourbit_codes(rows, d, group)}, "codes"},
+                               {{scale, fourbit_scales(rows, d, group)}, "scale"}},
+                              {{{x, static_cast<size_t>(rows) * d * esize(dtype)}, "x"}}));
+    DORA_LAUNCH(launch_quantize_fourbit(dtype == DORA_BF16, x, rows, d, static_cast<int>(group),
+                                        static_cast<uint8_t *>(codes), static_cast<uint16_t *>(scale),
+                                        static_cast<hipStream_t>(stream)),
+                "quantize to 4 bits");
+    return DORA_OK;
+}
+
+int dora_dequantize_fourbit(const void *codes, const void *scale, int64_t rows, int64_t d, int dtype,
+                            int64_t group, void *out, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_rows(rows, d));
+    DORA_CHECK(check_fourbit_group(group));
+    const bool any = rows > 0;
+    DORA_CHECK(check_ptrs({{codes, "codes", any}, {scale, "scale", any}, {out, "out", any}}));
+    DORA_CHECK(check_disjoint({{{out, static_cast<size_t>(rows) * d * esize(dtype)}, "out"}},
+                              {{{codes, fourbit_codes(rows, d, group)}, "codes"},
+                               {{scale, fourbit_scales(rows, d, group)}, "scale"}}));
+    DORA_LAUNCH(launch_dequantize_fourbit(dtype == DORA_BF16, static_cast<const uint8_t *>(codes),
+                                          static_cast<const uint16_t *>(scale), rows, d,
+                                          static_cast<int>(group), out, d,
+                                          static_cast<hipStream_t>(stream)),
+                "restore from 4 bits");
+    return DORA_OK;
+}
+
+size_t dora_linear_fourbit_workspace(int64_t T, int64_t d_in, int64_t d_out, int dtype)
+{
+    if (check_dtype(dtype) || check_dims(dtype, T, d_in, d_out, 8))
+        return 0;
+    return plan_fourbit(T, d_in, d_out, dtype).bytes;
+}
+
+int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int64_t group,
+                        int64_t T, int64_t d_in, int64_t d_out, int dtype, void *y, void *ws,
+                        size_t ws_bytes, void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_dims(dtype, T, d_in, d_out, 8));
+    DORA_CHECK(check_fourbit_group(group));
+    const bool any = T > 0;
+    DORA_CHECK(check_ptrs({{x, "x", any}, {codes, "codes", true}, {scale, "scale", true},
+                           {y, "y", any}}));
+    const FourbitPlan p = plan_fourbit(T, d_in, d_out, dtype);
+    DORA_CHECK(check_ws(ws, ws_bytes, p.bytes));
+    const size_t e = esize(dtype);
+    DORA_CHECK(check_disjoint({{{y, T * d_out * e}, "y"}, {{ws, p.bytes}, "workspace"}},
+                              {{{x, T * d_in * e}, "x"},
+                               {{codes, fourbit_codes(d_out, d_in, group)}, "codes"},
+                               {{scale, fourbit_scales(d_out, d_in, group)}, "scale"}}));
+    if (T == 0)
+        return DORA_OK;
+    const bool bf = dtype == DORA_BF16;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const uint8_t *c = static_cast<const uint8_t *>(codes);
+    const uint16_t *s = static_cast<const uint16_t *>(scale);
+    const int64_t groups = (d_in + group - 1) / group;
+    if (p.rows) {
+        const FourbitArgs a{x, c, s, y, T, d_in, d_out, groups, static_cast<int>(group)};
+        DORA_LAUNCH(launch_linear_fourbit(bf, a, st), "linear from 4 bits");
+        return DORA_OK;
+    }
+    for (int64_t n0 = 0; n0 < d_out; n0 += p.panel) {
+        const int64_t n = std::min(p.panel, d_out - n0);
+        DORA_LAUNCH(launch_dequantize_fourbit(bf, c + n0 * groups * (group / 2), s + n0 * groups, n,
+                                              d_in, static_cast<int>(group), ws, d_in, st),
+                    "restore from 4 bits");
+        DORA_CHECK(run_store(bf, n == p.panel ? p.g : p.last, seg1(T, n, x, d_in, ws, d_in, d_in), 0,
+                             static_cast<char *>(y) + n0 * e, d_out, 1.0f,
+                             reinterpret_cast<float *>(static_cast<char *>(ws) + p.o_part), st,
+                             "linear x W^T"));
+    }
+    return DORA_OK;
+}
+
 }  // extern "C"

@@ -30,7 +30,8 @@ EXPORTS = ("dora_strerror", "dora_last_error", "dora_norm_workspace", "dora_forw
            "dora_quantize_rows", "dora_dequantize_rows", "dora_linear_quantized_workspace",
            "dora_linear_quantized", "dora_backward_checkpoint_workspace",
            "dora_backward_checkpoint", "dora_block_norm", "dora_block_norm_backward_workspace",
-           "dora_block_norm_backward")
+           "dora_block_norm_backward", "dora_quantize_fourbit", "dora_dequantize_fourbit",
+           "dora_linear_fourbit_workspace", "dora_linear_fourbit")
 
 _lib = None
 
@@ -129,6 +130,14 @@ def lib():
         L.dora_block_norm_backward.restype = c_int
         L.dora_block_norm_backward.argtypes = [p, p, p, p, p, p, i64, p, p, p, f, f, i64, i64,
                                                c_int, p, p, p, p, p, p, sz, p]
+        L.dora_quantize_fourbit.restype = c_int
+        L.dora_quantize_fourbit.argtypes = [p, i64, i64, c_int, i64, p, p, p]
+        L.dora_dequantize_fourbit.restype = c_int
+        L.dora_dequantize_fourbit.argtypes = [p, p, i64, i64, c_int, i64, p, p]
+        L.dora_linear_fourbit_workspace.restype = sz
+        L.dora_linear_fourbit_workspace.argtypes = [i64, i64, i64, c_int]
+        L.dora_linear_fourbit.restype = c_int
+        L.dora_linear_fourbit.argtypes = [p, p, p, i64, i64, i64, i64, c_int, p, p, sz, p]
         _lib = L
     return _lib
 
@@ -737,3 +746,66 @@ def dora_block_norm_backward(dy, x, h, w_pre, rstd_pre, w_post=None, rstd_post=N
             _at(out["dresidual"]), _at(out.get("dgate")), _at(out.get("dw_post")),
             _at(out.get("dw_pre")), _at(ws), 0 if ws is None else ws.numel())
     return out
+
+
+# ------------------------------------------------------------- 4-bit weights
+def _fourbit_groups(d, group):
+    if group not in (32, 64, 128, 256, 512):
+        raise ValueError(f"group {group} is not a power of two from 32 to 512")
+    return -(-d // group)
+
+
+def dora_quantize_fourbit(x, group=128, codes=None, scale=None):
+    """Rows of x [T, d] as e2m1 codes (uint8 [T, groups * group / 2], two a byte) and bf16 scales
+    [T, groups], one for each `group` columns: max|x| / 6 at six significant bits, so that every
+    restored value is a bf16 number.  Returns (codes, scale)."""
+    dev = _dev(x)
+    T, d = _rows("x", x)
+    dt = _dt(x)
+    n = _fourbit_groups(d, group)
+    _need("x", x, dev, x.dtype, T, d)
+    codes = torch.empty(T, n * group // 2, dtype=torch.uint8, device=dev) if codes is None \
+        else _need("codes", codes, dev, torch.uint8, T, n * group // 2)
+    scale = torch.empty(T, n, dtype=torch.bfloat16, device=dev) if scale is None \
+        else _need("scale", scale, dev, torch.bfloat16, T, n)
+    _launch(dev, lib().dora_quantize_fourbit, _at(x), T, d, dt, group, _at(codes), _at(scale))
+    return codes, scale
+
+
+def dora_dequantize_fourbit(codes, scale, d, group=128, dtype=torch.bfloat16, out=None):
+    """The values [T, d] that 4-bit rows stand for, in `dtype` (or in out's)."""
+    dev = _dev(codes)
+    T = _rows("codes", codes)[0]
+    n = _fourbit_groups(d, group)
+    _need("codes", codes, dev, torch.uint8, T, n * group // 2)
+    _need("scale", scale, dev, torch.bfloat16, T, n)
+    out = torch.empty(T, d, dtype=dtype, device=dev) if out is None \
+        else _need("out", out, dev, out.dtype, T, d)
+    _launch(dev, lib().dora_dequantize_fourbit, _at(codes), _at(scale), T, d, _dt(out), group,
+            _at(out))
+    return out
+
+
+def dora_linear_fourbit_workspace(T, d_in, d_out, dtype):
+    return lib().dora_linear_fourbit_workspace(T, d_in, d_out, dtype)
+
+
+def dora_linear_fourbit(x, codes, scale, group=128, y=None, ws=None):
+    """y = x W^T for a weight W [d_out, d_in] held as dora_quantize_fourbit gives it (codes, scale,
+    with this group); x [T, d_in], y [T, d_out] in x's type."""
+    dev = _dev(x)
+    T, d_in = _rows("x", x)
+    d_out = _rows("codes", codes)[0]
+    dt = _dt(x)
+    n = _fourbit_groups(d_in, group)
+    _need("x", x, dev, x.dtype, T, d_in)
+    _need("codes", codes, dev, torch.uint8, d_out, n * group // 2)
+    _need("scale", scale, dev, torch.bfloat16, d_out, n)
+    y = torch.empty(T, d_out, dtype=x.dtype, device=dev) if y is None \
+        else _need("y", y, dev, x.dtype, T, d_out)
+    if _need_ws(ws, dev) is None:
+        need = dora_linear_fourbit_workspace(T, d_in, d_out, dt)
+        ws = _ws(need, dev) if need > 0 else None
+    _launch(dev, lib().dora_linear_fourbit, _at(x), _at(codes), _at(scale), group, T, d_in, d_out,
+            dt, _at(y), _at(ws), 0 if ws is None else ws.numel())
+    return y

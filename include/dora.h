@@ -467,6 +467,47 @@ int dora_block_norm_backward(const void *dy, const void *dh, const void *x, cons
                              int dtype, void *dx, void *dresidual, void *dgate, float *dw_post,
                              float *dw_pre, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * 4-bit rows.  A matrix [rows, d] is held as e2m1 codes (sign, two bits of
+ * exponent, one of fraction: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with
+ * one bf16 scale for each `group` consecutive columns (a power of two from 32 to
+ * 512): codes [rows, groups group / 2] bytes with groups = ceil(d / group), two
+ * codes a byte, the even column in the low half, rows of whole groups (what lies
+ * past column d is written as zeros and not read as part of the matrix); scale
+ * [rows, groups] bf16.  A code stands for its value times its group's scale.
+ *
+ * dora_quantize_fourbit - rows of `dtype` to this form:
+ *     scale = max_j |v_j| / 6 rounded to six significant bits (ties to even)
+ *     code  = v_j / scale rounded to the nearest e2m1 value (ties to the even
+ *             code, above 6 to 6), decided exactly
+ *   With six bits of scale every restored value is a bf16 number: nothing is lost
+ *   behind the codes.  A group of zeros has scale 0; the scale is kept between
+ *   2^-125 and 1.3125 2^125; a group that holds an infinity or a NaN gets a NaN
+ *   scale: it stands for NaN throughout.
+ * dora_dequantize_fourbit - code times scale in fp32, rounded once to `dtype`
+ *   (exact for the scales above).
+ *
+ * dora_linear_fourbit - dora_linear for a weight held this way (codes and scale of
+ * dora_quantize_fourbit on the merged weight of dora_merge, with group), y = x W^T
+ * with fp32 sums, rounded once.  x [T, d_in], y [T, d_out] in `dtype`.
+ *   Up to 64 tokens read the codes as they are: products with the codes' values,
+ *   each group's fp32 sum times its scale (fp32 tokens of 2^-100 and less in
+ *   magnitude may lose bits there, and the sums of six times a group's tokens must
+ *   stay finite).  More tokens restore the weight into the workspace, some of its
+ *   rows at a time, rounded once to `dtype`: exact for scales of six bits.
+ *   y must not overlap any input.  ws: dora_linear_fourbit_workspace(T, d_in, d_out,
+ *   dtype) bytes: none up to 64 tokens (ws may be NULL); beyond, 128 MiB or 256 rows
+ *   of the weight at most, and split-K partials of y where the product needs them.
+ */
+int dora_quantize_fourbit(const void *x, int64_t rows, int64_t d, int dtype, int64_t group,
+                          void *codes, void *scale, void *stream);
+int dora_dequantize_fourbit(const void *codes, const void *scale, int64_t rows, int64_t d, int dtype,
+                            int64_t group, void *out, void *stream);
+size_t dora_linear_fourbit_workspace(int64_t T, int64_t d_in, int64_t d_out, int dtype);
+int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int64_t group,
+                        int64_t T, int64_t d_in, int64_t d_out, int dtype, void *y, void *ws,
+                        size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -86,3 +86,41 @@ def block_grad(dy, dh, x, h, w_pre, r2, w_post, r1, gate, a, b):
     e = f1 * (w1.abs() * edu + 8 * U * ((w1 * du).abs() + (m2 * hatx).abs()) + hatx.abs() * e2)
     out["dx"] = (dx, e + (dx.abs() + e) * half(dt))
     return out
+
+
+# -------------------------------------------------------------- 4-bit rows
+E2M1 = torch.tensor([0.0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+
+
+def fourbit(v, group):
+    """(values the codes stand for without their scale, scales) of the rows of v, in 64 bits:
+    the nearest e2m1 values, ties to the even code; the scale max / 6 at six bits."""
+    v = v.double()
+    T, d = v.shape
+    n = -(-d // group)
+    p = torch.zeros(T, n * group, dtype=torch.float64)
+    p[:, :d] = v
+    p = p.view(T, n, group)
+    bad = ~torch.isfinite(p).all(dim=2)
+    top = torch.where(bad[:, :, None], torch.zeros_like(p), p).abs().amax(dim=2)
+    m, e = torch.frexp(top / 6)
+    s = torch.ldexp(torch.round(m * 64) / 64, e).clamp(2.0 ** -125, 1.3125 * 2.0 ** 125)
+    s = torch.where(top > 0, s, torch.zeros_like(s))
+    t = p.abs() / torch.where(s > 0, s, torch.ones_like(s))[:, :, None]
+    near = (t[..., None] - E2M1).abs()
+    # the least distance, and of two the even code
+    order = near + torch.tensor([0.0, 1e-15] * 4, dtype=torch.float64)
+    code = order.argmin(dim=-1)
+    values = torch.sign(p) * E2M1[code]
+    s = torch.where(bad, torch.full_like(s, float("nan")), s)
+    return values.view(T, n * group)[:, :d], s
+
+
+def unpack(codes):
+    """The values of packed codes, scale apart."""
+    c = torch.stack([codes & 15, codes >> 4], dim=2).view(codes.shape[0], -1).long()
+    return E2M1[c & 7] * torch.where(c >= 8, -1.0, 1.0).double()
+
+
+def restored(codes, scale, d, group):
+    return (unpack(codes) * scale.double().repeat_interleave(group, dim=1))[:, :d]

@@ -107,3 +107,86 @@ def test_plain_block_gradients_are_those_of_differentiation(post, gate):
     assert set(ref) == set(leaves)
     for k, t in leaves.items():
         assert torch.allclose(ref[k][0], t.grad, rtol=1e-10, atol=1e-12), k
+
+
+def quant4(x=AT[0], rows=16, d=64, dt=BF16, group=32, codes=AT[1], scale=AT[2]):
+    return D.lib().dora_quantize_fourbit(_p(x), rows, d, dt, group, _p(codes), _p(scale), None)
+
+
+def dequant4(codes=AT[0], scale=AT[1], rows=16, d=64, dt=BF16, group=32, out=AT[2]):
+    return D.lib().dora_dequantize_fourbit(_p(codes), _p(scale), rows, d, dt, group, _p(out), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"codes": 0}, E_NULL), ({"scale": 0}, E_NULL), ({"rows": -1}, E_SHAPE), ({"d": 0}, E_SHAPE),
+    ({"group": 0}, E_SHAPE), ({"group": 16}, E_SHAPE), ({"group": 96}, E_SHAPE),
+    ({"group": 1024}, E_SHAPE), ({"group": -32}, E_SHAPE), ({"dt": 3}, E_DTYPE),
+    ({"codes": AT[1] + 8}, E_ALIGN), ({"scale": AT[0] + 512}, E_ALIAS), ({"codes": AT[0]}, E_ALIAS),
+])
+def test_fourbit_rows_refuse(kw, code):
+    if kw.get("codes") == AT[0]:  # (its own default in the second call)
+        assert quant4(**kw) == code
+        return
+    assert quant4(**kw) == code
+    back = {k: v for k, v in kw.items() if k != "scale" or v == 0}
+    if "codes" in back and back["codes"]:
+        back["codes"] = AT[0] + 8
+    if back:
+        assert dequant4(**back) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"out": 0}, E_NULL), ({"out": AT[0] + 16}, E_ALIAS), ({"out": AT[1]}, E_ALIAS),
+    ({"out": AT[2] + 4}, E_ALIGN),
+])
+def test_fourbit_restore_refuses(kw, code):
+    assert dequant4(**kw) == code
+
+
+def test_fourbit_extents_count_in_the_overlap_check():
+    # 16 rows of 65 columns: three groups, 48 bytes of codes and 6 of scales a row
+    assert quant4(d=65, scale=AT[1] + 15 * 48) == E_ALIAS
+    assert dequant4(d=65, out=AT[1] + 80) == E_ALIAS
+
+
+def linear4(x=AT[0], codes=AT[1], scale=AT[2], group=32, T=4, d_in=64, d_out=32, dt=BF16, y=AT[3],
+            ws=AT[4], ws_bytes=1 << 28):
+    return D.lib().dora_linear_fourbit(_p(x), _p(codes), _p(scale), group, T, d_in, d_out, dt, _p(y),
+                                       _p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"x": 0}, E_NULL), ({"codes": 0}, E_NULL), ({"scale": 0}, E_NULL), ({"y": 0}, E_NULL),
+    ({"T": -1}, E_SHAPE), ({"d_in": 0}, E_SHAPE), ({"d_out": 0}, E_SHAPE), ({"group": 48}, E_SHAPE),
+    ({"dt": 4}, E_DTYPE), ({"x": AT[0] + 2}, E_ALIGN), ({"codes": AT[1] + 1}, E_ALIGN),
+    ({"T": 65, "ws": 0}, E_WS), ({"T": 65, "ws_bytes": 100}, E_WS), ({"y": AT[0]}, E_ALIAS),
+    ({"y": AT[1] + 16}, E_ALIAS), ({"y": AT[2]}, E_ALIAS), ({"T": 65, "ws": AT[1]}, E_ALIAS),
+    ({"T": 65, "ws": AT[3]}, E_ALIAS),
+])
+def test_linear_fourbit_refuses(kw, code):
+    assert linear4(**kw) == code
+    assert D.lib().dora_last_error()
+
+
+def test_linear_fourbit_workspace_holds_no_dense_weight():
+    q = D.dora_linear_fourbit_workspace
+    for T in (0, 1, 64):
+        assert q(T, 8192, 28672, BF16) == 0
+    assert q(-1, 8, 8, BF16) == 0 and q(100, 0, 8, BF16) == 0 and q(100, 8, 8, 5) == 0
+    for dt, e in ((BF16, 2), (F32, 4)):
+        for d_in, d_out in ((8192, 28672), (28672, 8192), (1 << 17, 1 << 14), (100, 1 << 20)):
+            part = 32 * 65 * d_out * 4
+            assert 0 < q(65, d_in, d_out, dt) <= max(128 << 20, 256 * d_in * e) + part + 512
+
+
+def test_plain_fourbit_is_the_nearest_value():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(40, 96, generator=g).double()
+    values, s = R.fourbit(x, 32)
+    v = (values * s.repeat_interleave(32, dim=1))
+    each = R.E2M1 * s.repeat_interleave(32, dim=1)[..., None]
+    both = torch.cat([each, -each], dim=-1)
+    best = (x[..., None] - both).abs().amin(dim=-1)
+    assert torch.equal((x - v).abs(), best)
+    assert torch.equal(s.to(torch.bfloat16).double(), s)
+    assert torch.equal(v.to(torch.bfloat16).double(), v)
