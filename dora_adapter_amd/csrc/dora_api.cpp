@@ -2397,13 +2397,14 @@ struct FourbitPlan {
     GPlan g, last;
     size_t o_part = 0, bytes = 0;
 };
-constexpr int64_t kFourbitTokens = 64;
+constexpr int64_t kFourbitTokens = 256;
 constexpr int64_t kFourbitPanel = int64_t(128) << 20;
 
 FourbitPlan plan_fourbit(int64_t T, int64_t d_in, int64_t d_out, int dtype)
 {
     FourbitPlan p;
-    p.rows = T <= kFourbitTokens;
+    // (the kernels of few tokens address 256 channels of the codes with 31 bits)
+    p.rows = T <= kFourbitTokens && d_in < (int64_t(1) << 23);
     if (p.rows)
         return p;
     const bool bf = dtype == DORA_BF16;

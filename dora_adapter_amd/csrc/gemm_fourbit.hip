@@ -1,14 +1,14 @@
 // gemm_fourbit.hip - y = x W^T for a few tokens and a weight held as 4-bit rows (gfx950).
 //
-// Bound by reading the codes once (half a byte a weight).  A workgroup takes 16 NT output
-// channels and up to 16 TM tokens; its waves split K, wave w taking the lines (256 columns, the
-// 128 bytes of codes that one cache line holds) w, w + W, ...  A lane loads 16 bytes of its
-// channel's codes at a time, D lines ahead, straight into registers; exchanges between the lane
-// groups turn four such registers into four MFMA operands of 32 consecutive columns each, and
-// one conversion instruction makes two bf16 weights of two codes.  The weights enter the
-// products as the codes' own values, exact in bf16, and the fp32 sums over a group's columns
-// meet its scale, so that nothing is rounded before the sums.  fp32 tokens enter as three bf16
-// numbers each, which hold all 24 bits.  The waves' sums meet in LDS, in order.
+// Bound by reading the codes once (half a byte a weight), as whole cache lines: a line is 256
+// columns, the 128 bytes of codes that one cache line holds.  A wave loads eight rows of a line
+// an instruction into registers (16 rows of half a line are 64-byte requests: 30 us against 24.5
+// for one token over 28672 channels of 8192), turns them in LDS, and exchanges between the
+// lane groups make four MFMA operands of 32 consecutive columns each of four registers; one
+// conversion instruction makes two bf16 weights of two codes.  The weights enter the products as
+// the codes' own values, exact in bf16, and the fp32 sums over a group's columns meet its
+// scale, so that nothing is rounded before the sums.  fp32 tokens enter as three bf16 numbers
+// each, which hold all 24 bits.  The sums of waves that split K meet in LDS, in order.
 #include "around.hpp"
 #include "fourbit.hpp"
 
@@ -87,18 +87,19 @@ __device__ __forceinline__ void split8(const Raw8<T> &v, unsigned int (&w)[plane
 template <int PER>
 struct LineScales {
     unsigned int w[(PER + 1) / 2];
-    __device__ __forceinline__ void load(const uint16_t *p)
+    // (rows of an odd number of scales start at any 2 bytes)
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t v, int s)
     {
         if constexpr (PER == 8) {
-            const u32x4_a2_t v = *reinterpret_cast<const u32x4_a2_t *>(p);
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            const auto q = __builtin_amdgcn_raw_buffer_load_b128(r, v, s, 0);
+            w[0] = q[0]; w[1] = q[1]; w[2] = q[2]; w[3] = q[3];
         } else if constexpr (PER == 4) {
-            const u32x2_a2_t v = *reinterpret_cast<const u32x2_a2_t *>(p);
-            w[0] = v.x; w[1] = v.y;
+            const auto q = __builtin_amdgcn_raw_buffer_load_b64(r, v, s, 0);
+            w[0] = q[0]; w[1] = q[1];
         } else if constexpr (PER == 2) {
-            w[0] = *reinterpret_cast<const u32_a2_t *>(p);
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, v, s, 0);
         } else {
-            w[0] = *p;
+            w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, v, s, 0);
         }
     }
     // the first `cnt` of them
@@ -119,249 +120,474 @@ struct LineScales {
 
 template <int NT, int PER>
 struct Line {
-    unsigned int c[NT][2][4];
+    u32x4_t c[NT][2];
     LineScales<PER> s[NT];
 };
 
-// XLDS: the tokens' rows lie whole in LDS (dynamic: planes x T x pitch elements); else every
-// lane reads its own operands from memory, half a line ahead of their use.
-template <typename T, int TM, int NT, int PER, bool XLDS, int W, int D>
-__global__ void __launch_bounds__(W * 64) linear_fourbit_kernel(FourbitArgs a)
+// A descriptor of `bytes` bytes (under 2^31) from `p`, in scalar registers.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *p, int64_t bytes)
 {
-    constexpr int P = planes<T>, HALF = STEPS / 2;
-    constexpr int PITCH = 16 * NT + 4;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ __align__(16) float sums[W][16 * TM][PITCH];
-    const int lane = static_cast<int>(threadIdx.x) & 63, nl = lane & 15, kq = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NT);
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * (16 * TM);
-    const int64_t lines = a.d_in / LINE;
-    const int64_t code_pitch = a.groups * (a.group / 2);
-    const int line_groups_shift = PER > 1 ? 0 : 31 - __clz(a.group / LINE);  // lines a group, its log
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void *>((static_cast<uint64_t>(hi) << 32) | lo), static_cast<short>(0),
+        __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
+}
+constexpr int AUX_NT = 2;  // non-temporal
 
-    const uint8_t *code_row[NT];
-    const uint16_t *scale_row[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int64_t n = n0 + 16 * i + nl < a.d_out ? n0 + 16 * i + nl : a.d_out - 1;
-        code_row[i] = a.codes + n * code_pitch + 16 * kq;
-        scale_row[i] = a.scale + n * a.groups;
-    }
-    auto load = [&](Line<NT, PER> &l, int64_t line) {
+// 16-byte chunk c of row r of a tile in LDS lies at c ^ swizzle(r): neither 8 rows written whole
+// nor 16 rows read at one chunk meet on a bank.
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+
+// A wave's reader of the codes of tiles of 16 NT channels.
+template <int NT, int PER>
+struct Codes {
+    const FourbitArgs &a;
+    unsigned char *turned;  // the wave's LDS, NT x 2 KiB
+    int lane, nl, kq, lrow, lchunk, per_shift;
+    int64_t whole, pitch;  // lines that lie inside the row; bytes of a row
+    uint32_t code_off[NT][2], scale_off[NT];
+
+    __device__ __forceinline__ Codes(const FourbitArgs &args, unsigned char *lds, int l)
+        : a(args), turned(lds), lane(l), nl(l & 15), kq(l >> 4), lrow(l >> 3), lchunk(l & 7),
+          per_shift(PER > 1 ? 0 : 31 - __clz(args.group / LINE)), whole(args.d_in / LINE),
+          pitch(args.groups * (args.group / 2))
+    {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4_t v = __builtin_nontemporal_load(
-                    reinterpret_cast<const u32x4_t *>(code_row[i] + line * (LINE / 2) + 64 * h));
-                l.c[i][h][0] = v.x; l.c[i][h][1] = v.y; l.c[i][h][2] = v.z; l.c[i][h][3] = v.w;
-            }
-            l.s[i].load(scale_row[i] + (PER > 1 ? line * PER : line >> line_groups_shift));
+            for (int u = 0; u < 2; ++u)
+                code_off[i][u] =
+                    (16 * i + 8 * u + lrow) * static_cast<uint32_t>(pitch) + 16 * lchunk;
+            scale_off[i] = (16 * i + nl) * static_cast<uint32_t>(a.groups) * 2;
         }
-    };
-    // the line that the row ends in: nothing past the row's codes and scales
-    auto load_tail = [&](Line<NT, PER> &l) {
+    }
+    __device__ __forceinline__ int64_t row_of(int64_t n) const { return n < a.d_out ? n : a.d_out - 1; }
+
+    // Line `line` of tile `tile`: eight rows of whole cache lines an instruction, lane l the
+    // l & 7th 16 bytes of rows l >> 3 and 8 + (l >> 3).  Through descriptors of the tile's
+    // rows: channels past the last one read zeros, and everything does unless `any`, with no
+    // branch: around a branch the compiler cannot count the loads in flight, and waits for all
+    // of them at each use.
+    __device__ __forceinline__ void load(Line<NT, PER> &l, int64_t tile, int64_t line, bool any) const
+    {
+        const int64_t n0 = tile * (16 * NT), left = a.d_out - n0 < 16 * NT ? a.d_out - n0 : 16 * NT;
+        const auto rc = rows_rsrc(a.codes + n0 * pitch, any ? left * pitch : 0);
+        const auto rs = rows_rsrc(a.scale + n0 * a.groups, any ? left * a.groups * 2 : 0);
+        const int co = static_cast<int>(line * (LINE / 2));
+        const int so = static_cast<int>(PER > 1 ? line * PER : line >> per_shift) * 2;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4_t v = {0u, 0u, 0u, 0u};
-                if (lines * (LINE / 2) + 64 * h + 16 * kq < code_pitch)
-                    v = *reinterpret_cast<const u32x4_t *>(code_row[i] + lines * (LINE / 2) + 64 * h);
-                l.c[i][h][0] = v.x; l.c[i][h][1] = v.y; l.c[i][h][2] = v.z; l.c[i][h][3] = v.w;
+            for (int u = 0; u < 2; ++u)
+                l.c[i][u] = __builtin_bit_cast(
+                    u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rc, code_off[i][u], co, AUX_NT));
+            l.s[i].load(rs, scale_off[i], so);
+        }
+    }
+    // the line that the row ends in, nothing past its end
+    __device__ __forceinline__ void load_tail(Line<NT, PER> &l, int64_t tile) const
+    {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int64_t n0 = (tile * NT + i) * 16, at = whole * (LINE / 2) + 16 * lchunk;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                l.c[i][u] = u32x4_t{0u, 0u, 0u, 0u};
+                if (at < pitch)
+                    l.c[i][u] = *reinterpret_cast<const u32x4_t *>(
+                        a.codes + row_of(n0 + 8 * u + lrow) * pitch + at);
             }
+            const uint16_t *s = a.scale + row_of(n0 + nl) * a.groups;
             if constexpr (PER > 1)
-                l.s[i].load_some(scale_row[i] + lines * PER, a.groups - lines * PER);
+                l.s[i].load_some(s + whole * PER, a.groups - whole * PER);
             else
-                l.s[i].load(scale_row[i] + (lines >> line_groups_shift));
+                l.s[i].load_some(s + (whole >> per_shift), 1);
         }
-    };
-
-    Line<NT, PER> ring[D];
-    const int64_t mine = lines > wave ? (lines - wave + W - 1) / W : 0;
+    }
+    // a line into the wave's LDS, and the four operand registers of its half h from there
+    __device__ __forceinline__ void turn(const Line<NT, PER> &l) const
+    {
 #pragma unroll
-    for (int k = 0; k < D; ++k)
-        if (k < mine)
-            load(ring[k], wave + static_cast<int64_t>(k) * W);
-
-    // the tokens
-    const int64_t xpitch = (a.d_in + LINE - 1) / LINE * LINE + 8;  // in LDS
-    const int tokens = static_cast<int>(a.T - t0 < 16 * TM ? a.T - t0 : 16 * TM);
-    if constexpr (XLDS) {
-        const int64_t vecs = xpitch / 8;
-        for (int t = 0; t < tokens; ++t)
-            for (int64_t v = threadIdx.x; v < vecs; v += W * 64) {
-                Raw8<T> r;
-                r.template load<true>(static_cast<const T *>(a.x) + (t0 + t) * a.d_in + v * 8,
-                                      count8(a.d_in, v * 8));
-                unsigned int w[P][4];
-                split8(r, w);
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<u32x4_t *>(smem + ((p * tokens + t) * xpitch + v * 8) * 2) =
-                        u32x4_t{w[p][0], w[p][1], w[p][2], w[p][3]};
+            for (int u = 0; u < 2; ++u) {
+                const int r = 8 * u + lrow;
+                *reinterpret_cast<u32x4_t *>(turned + i * 2048 + r * 128 + 16 * (lchunk ^ swizzle(r))) =
+                    l.c[i][u];
             }
-        __syncthreads();
     }
-    const T *x_row[TM];
-    const unsigned char *x_lds[TM];
+    __device__ __forceinline__ void half(unsigned int (&c)[NT][4], int h) const
+    {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int t = 16 * i + nl < tokens ? 16 * i + nl : tokens - 1;
-        x_row[i] = static_cast<const T *>(a.x) + (t0 + t) * a.d_in + 8 * kq;
-        x_lds[i] = smem + (t * xpitch + 8 * kq) * 2;
+        for (int i = 0; i < NT; ++i) {
+            const u32x4_t v = *reinterpret_cast<const u32x4_t *>(
+                turned + i * 2048 + nl * 128 + 16 * ((4 * h + kq) ^ swizzle(nl)));
+            c[i][0] = v.x; c[i][1] = v.y; c[i][2] = v.z; c[i][3] = v.w;
+            exchange4(c[i]);
+        }
     }
+};
 
+// A wave's sums: of the group under way, and of those whose scale has been met.
+template <int TM, int NT>
+struct Sums {
     f32x4_t acc[TM][NT], part[TM][NT];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            acc[i][j] = part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    struct Half {
-        Raw8<T> x[HALF][TM];
-    };
-    auto fetch = [&](Half &o, int64_t line, int h, bool tail) {
-        if constexpr (!XLDS) {
+            for (int j = 0; j < NT; ++j)
+                acc[i][j] = part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    // step `step` of a line: the products of 32 columns, and the scale where a group ends
+    template <int PER, int P>
+    __device__ __forceinline__ void step(const bf16x8_t (&x)[TM][P], const unsigned int (&c)[NT][4],
+                                         const Line<NT, PER> &l, int step)
+    {
 #pragma unroll
-            for (int s = 0; s < HALF; ++s)
+        for (int j = 0; j < NT; ++j) {
+            const bf16x8_t w = weights8(c[j][step % 4]);
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const int64_t k = line * LINE + (h * HALF + s) * 32;
-                    o.x[s][i].template load<true>(x_row[i] + k, tail ? count8(a.d_in, k + 8 * kq) : 8);
-                }
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int p = P - 1; p >= 0; --p)  // the smallest parts first
+                    part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i][p], w, part[i][j], 0, 0, 0);
         }
-    };
-    // half a line: the codes of register quad c, scales from the line's
-    auto products = [&](Line<NT, PER> &l, const Half &x, int64_t line, int h) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            exchange4(l.c[j][h]);
-#pragma unroll
-        for (int s = 0; s < HALF; ++s) {
-            bf16x8_t xs[TM][P];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                if constexpr (XLDS) {
-                    const int64_t at = (line * LINE + (h * HALF + s) * 32) * 2;
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        xs[i][p] = __builtin_bit_cast(
-                            bf16x8_t, *reinterpret_cast<const u32x4_t *>(
-                                          x_lds[i] + p * tokens * xpitch * 2 + at));
-                } else {
-                    unsigned int w[P][4];
-                    split8(x.x[s][i], w);
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        xs[i][p] = __builtin_bit_cast(bf16x8_t,
-                                                      u32x4_t{w[p][0], w[p][1], w[p][2], w[p][3]});
-                }
-            }
+        constexpr int EVERY = STEPS / PER;
+        if ((step + 1) % EVERY == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const bf16x8_t w = weights8(l.c[j][h][s]);
+                const float by = l.s[j].get(step / EVERY);
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int p = P - 1; p >= 0; --p)  // the smallest parts first
-                        part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[i][p], w, part[i][j],
-                                                                             0, 0, 0);
+                    for (int q = 0; q < 4; ++q) {
+                        acc[i][j][q] = __fmaf_rn(by, part[i][j][q], acc[i][j][q]);
+                        part[i][j][q] = 0.f;
+                    }
             }
-            // the end of a group (or of the line): its sums meet its scale
-            constexpr int EVERY = STEPS / PER;
-            const int step = h * HALF + s;
-            if ((step + 1) % EVERY == 0) {
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void put(T *p, float v)
+{
+    if constexpr (sizeof(T) == 2)
+        *p = f32_to_bf16(v);
+    else
+        *p = v;
+}
+
+// Up to FEW tokens (a block of them, blockIdx.y), whose rows lie whole in LDS (dynamic: planes x
+// tokens x pitch elements).  The W waves split K; a workgroup walks the tiles blockIdx.x,
+// blockIdx.x + gridDim.x, ... of 16 channels and keeps its waves' loads going across them, so
+// that the workgroups at work read rows that lie close to each other (one workgroup a CU over
+// 28672 channels of 8192: 24.5 us, two 28, a workgroup a tile 38).
+constexpr int FEW = 4;
+template <typename T, int PER, int W>
+__global__ void __launch_bounds__(W * 64) linear_fourbit_kernel(FourbitArgs a)
+{
+    constexpr int P = planes<T>, PITCH = 20;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ __align__(16) float sums[2][W][FEW][PITCH];  // (two buffers: one barrier a tile)
+    __shared__ __align__(16) unsigned char turned[W][2048];
+    const int lane = static_cast<int>(threadIdx.x) & 63, nl = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * FEW;
+    const int tokens = static_cast<int>(a.T - t0 < FEW ? a.T - t0 : FEW);
+    const Codes<1, PER> codes(a, turned[wave], lane);
+    const int64_t whole = codes.whole, lines = (a.d_in + LINE - 1) / LINE;
+    const int64_t rounds = whole > 0 ? (whole + W - 1) / W : 1;
+    const int64_t tiles = (a.d_out + 15) / 16;
+
+    // the wave's whole lines in order, over all its tiles: where the next load stands
+    Line<1, PER> ring;
+    int64_t ltile = blockIdx.x, lround = 0;
+    auto load_next = [&]() {
+        const int64_t line = wave + lround * W;
+        codes.load(ring, ltile < tiles ? ltile : 0, line, ltile < tiles && line < whole);
+        if (++lround == rounds) {
+            lround = 0;
+            ltile += gridDim.x;
+        }
+    };
+    load_next();
+
+    const int64_t xpitch = lines * LINE + 8, vecs = xpitch / 8;
+    for (int t = 0; t < tokens; ++t)
+        for (int64_t v = threadIdx.x; v < vecs; v += W * 64) {
+            Raw8<T> r;
+            r.template load<true>(static_cast<const T *>(a.x) + (t0 + t) * a.d_in + v * 8,
+                                  count8(a.d_in, v * 8));
+            unsigned int w[P][4];
+            split8(r, w);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float by = l.s[j].get(step / EVERY);
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<u32x4_t *>(smem + ((p * tokens + t) * xpitch + v * 8) * 2) =
+                    u32x4_t{w[p][0], w[p][1], w[p][2], w[p][3]};
+        }
+    __syncthreads();
+    const unsigned char *const x = smem + ((nl < tokens ? nl : tokens - 1) * xpitch + 8 * kq) * 2;
+
+    Sums<1, 1> sum;
+    sum.clear();
+    auto products = [&](const Line<1, PER> &l, int64_t line) {
+        codes.turn(l);
 #pragma unroll
-                    for (int i = 0; i < TM; ++i)
+        for (int h = 0; h < 2; ++h) {
+            unsigned int c[1][4];
+            codes.half(c, h);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            acc[i][j][q] = __fmaf_rn(by, part[i][j][q], acc[i][j][q]);
-                            part[i][j][q] = 0.f;
-                        }
-                }
+            for (int s = 4 * h; s < 4 * h + 4; ++s) {
+                bf16x8_t xs[1][P];
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    xs[0][p] = __builtin_bit_cast(
+                        bf16x8_t, *reinterpret_cast<const u32x4_t *>(
+                                      x + (p * tokens * xpitch + line * LINE + s * 32) * 2));
+                sum.step(xs, c, l, s);
             }
         }
     };
-
-    Half xa, xb;
-    if (mine > 0)
-        fetch(xa, wave, 0, false);
-    for (int64_t k0 = 0; k0 < mine; k0 += D) {
+    // the end of a tile: the waves' sums, in order (the tokens are rows 0 to 3, lanes 0 to 15)
+    int buf = 0;
+    auto finish = [&](int64_t tile) {
+        if (kq == 0)
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int64_t k = k0 + d;
-            if (k < mine) {
-                const int64_t line = wave + k * W;
-                fetch(xb, line, 1, false);
-                products(ring[d], xa, line, 0);
-                if (k + 1 < mine)
-                    fetch(xa, line + W, 0, false);
-                products(ring[d], xb, line, 1);
-                if (k + D < mine)
-                    load(ring[d], line + static_cast<int64_t>(D) * W);
+            for (int q = 0; q < FEW; ++q)
+                sums[buf][wave][q][nl] = sum.acc[0][0][q];
+        sum.clear();
+        __syncthreads();
+        const int e = static_cast<int>(threadIdx.x), m = e / 16, n = e % 16;
+        if (m < tokens && tile * 16 + n < a.d_out) {
+            float v = sums[buf][0][m][n];
+#pragma unroll
+            for (int w = 1; w < W; ++w)
+                v += sums[buf][w][m][n];
+            put(static_cast<T *>(a.y) + (t0 + m) * a.d_out + tile * 16 + n, v);
+        }
+        buf ^= 1;
+    };
+    for (int64_t tile = blockIdx.x, round = 0; tile < tiles;) {
+        const int64_t line = wave + round * W;
+        if (line < whole)
+            products(ring, line);
+        load_next();
+        if (++round == rounds) {
+            if (whole < lines && whole % W == wave) {
+                Line<1, PER> l;
+                codes.load_tail(l, tile);
+                products(l, whole);
             }
+            finish(tile);
+            round = 0;
+            tile += gridDim.x;
         }
     }
-    if (lines * LINE < a.d_in && lines % W == wave) {
-        Line<NT, PER> l;
-        load_tail(l);
-        fetch(xa, lines, 0, true);
-        products(l, xa, lines, 0);
-        fetch(xb, lines, 1, true);
-        products(l, xb, lines, 1);
-    }
+}
 
+// More tokens: CW waves a K group take 16 NT channels each and share the tokens' line, which lies
+// in LDS, the next one on its way; KG such groups split K.  (d_in of a line at least.)
+template <typename T, int TM, int NT, int PER, int CW, int KG, int D>
+__global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(FourbitArgs a)
+{
+    constexpr int P = planes<T>;
+    constexpr int ROW = LINE * 2;                    // bytes of a token's line
+    constexpr int XBYTES = P * 16 * TM * ROW;        // a line of the tokens
+    constexpr int LOADS = 16 * TM * (LINE / 8) / (CW * 64);  // vectors of eight a thread
+    static_assert(LOADS * CW * 64 == 16 * TM * (LINE / 8), "whole vectors a thread");
+    constexpr int PITCH = CW * 16 * NT + 4;
+    static_assert(KG * 16 * TM * PITCH * 4 <= 2 * KG * XBYTES, "the sums lie where the tokens lay");
+    __shared__ __align__(16) unsigned char xs[KG][2][XBYTES];
+    __shared__ __align__(16) unsigned char turned[KG * CW][NT * 2048];
+    const int lane = static_cast<int>(threadIdx.x) & 63, nl = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int cw = wave % CW, kg = wave / CW, tid = static_cast<int>(threadIdx.x) % (CW * 64);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * (16 * TM);
+    const int tokens = static_cast<int>(a.T - t0 < 16 * TM ? a.T - t0 : 16 * TM);
+    const Codes<NT, PER> codes(a, turned[wave], lane);
+    const int64_t whole = codes.whole, lines = (a.d_in + LINE - 1) / LINE;
+    const int64_t rounds = (lines + KG - 1) / KG;
+    const int64_t tile = static_cast<int64_t>(blockIdx.x) * CW + cw;
+    const bool mine = tile * (16 * NT) < a.d_out;
+
+    Line<NT, PER> ring[D];
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+        codes.load(ring[k], mine ? tile : 0, kg + k * KG, mine && kg + k * KG < whole);
+
+    // the tokens' line: thread i takes chunks i, i + threads, ... (32 a token)
+    struct Tokens {
+        Raw8<T> v[LOADS];
+    };
+    auto fetch = [&](Tokens &x, int64_t line, auto WHOLE) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int v = tid + i * CW * 64, r = v / 32;
+            const int64_t k = line * LINE + 8 * (v % 32);
+            const T *p = static_cast<const T *>(a.x) + (t0 + (r < tokens ? r : tokens - 1)) * a.d_in;
+            x.v[i].template load<true>(p + k, WHOLE() ? 8 : count8(a.d_in, k));
+        }
+    };
+    using Yes = std::true_type;
+    // (the next whole line, or the last one again, with no branch; the row's end apart)
+    auto fetch_next = [&](Tokens &x, int64_t line) {
+        fetch(x, line < whole ? line : whole - 1, Yes());
+        if (line == whole && whole < lines)
+            fetch(x, line, std::false_type());
+    };
+    auto keep = [&](const Tokens &x, int buf) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int v = tid + i * CW * 64, r = v / 32, c = v % 32;
+            unsigned int w[P][4];
+            split8(x.v[i], w);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<u32x4_t *>(&xs[kg][buf][(p * 16 * TM + r) * ROW +
+                                                          16 * (c ^ swizzle(r))]) =
+                    u32x4_t{w[p][0], w[p][1], w[p][2], w[p][3]};
+        }
+    };
+    Sums<TM, NT> sum;
+    sum.clear();
+    auto products = [&](const Line<NT, PER> &l, int buf) {
+        codes.turn(l);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            unsigned int c[NT][4];
+            codes.half(c, h);
+#pragma unroll
+            for (int s = 4 * h; s < 4 * h + 4; ++s) {
+                bf16x8_t x[TM][P];
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        x[i][p] = __builtin_bit_cast(
+                            bf16x8_t, *reinterpret_cast<const u32x4_t *>(
+                                          &xs[kg][buf][(p * 16 * TM + 16 * i + nl) * ROW +
+                                                       16 * ((4 * s + kq) ^ swizzle(nl))]));
+                sum.step(x, c, l, s);
+            }
+        }
+    };
+    // Two lines of the tokens are on their way: loads return in order, so that a wait for them is
+    // one for all codes loaded before them too.
+    Tokens x[2];
+    fetch_next(x[0], kg);
+    fetch_next(x[1], kg + KG);
+    keep(x[0], 0);
+    __syncthreads();
+    for (int64_t r0 = 0; r0 < rounds; r0 += 2) {
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const int64_t line = kg + (r0 + d) * KG;
+            fetch_next(x[d], line + 2 * KG);
+            if (line < whole) {
+                products(ring[d % D], d);
+            } else if (line < lines && mine) {
+                Line<NT, PER> l;
+                codes.load_tail(l, tile);
+                products(l, d);
+            }
+            const int64_t ahead = line + static_cast<int64_t>(D) * KG;
+            codes.load(ring[d % D], mine ? tile : 0, ahead, mine && ahead < whole);
+            keep(x[d ^ 1], d ^ 1);
+            __syncthreads();
+        }
+    }
+    float *const sums = reinterpret_cast<float *>(&xs[0][0][0]);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                sums[wave][16 * i + 4 * kq + q][16 * j + nl] = acc[i][j][q];
+                sums[(kg * 16 * TM + 16 * i + 4 * kq + q) * PITCH + 16 * (cw * NT + j) + nl] =
+                    sum.acc[i][j][q];
     __syncthreads();
-    for (int e = static_cast<int>(threadIdx.x); e < tokens * 16 * NT; e += W * 64) {
-        const int m = e / (16 * NT), n = e % (16 * NT);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (CW * 16 * NT);
+    for (int e = static_cast<int>(threadIdx.x); e < tokens * CW * 16 * NT; e += CW * KG * 64) {
+        const int m = e / (CW * 16 * NT), n = e % (CW * 16 * NT);
         if (n0 + n >= a.d_out)
             continue;
-        float v = sums[0][m][n];
+        float v = sums[m * PITCH + n];
 #pragma unroll
-        for (int w = 1; w < W; ++w)
-            v += sums[w][m][n];
-        T *out = static_cast<T *>(a.y) + (t0 + m) * a.d_out + n0 + n;
-        if constexpr (sizeof(T) == 2)
-            *out = f32_to_bf16(v);
-        else
-            *out = v;
+        for (int g = 1; g < KG; ++g)
+            v += sums[(g * 16 * TM + m) * PITCH + n];
+        put(static_cast<T *>(a.y) + (t0 + m) * a.d_out + n0 + n, v);
     }
 }
 
-template <typename T, int TM, int NT, int PER, bool XLDS, int W, int D>
-hipError_t launch(const FourbitArgs &a, hipStream_t st)
+constexpr int FEW_WAVES = 16;
+template <typename T>
+size_t few_lds(const FourbitArgs &a)
 {
     const int64_t xpitch = (a.d_in + LINE - 1) / LINE * LINE + 8;
-    const size_t lds = XLDS ? static_cast<size_t>(planes<T> * a.T * xpitch * 2) : 0;
-    const dim3 grid(static_cast<unsigned>((a.d_out + 16 * NT - 1) / (16 * NT)),
-                    static_cast<unsigned>((a.T + 16 * TM - 1) / (16 * TM)));
-    hipLaunchKernelGGL((linear_fourbit_kernel<T, TM, NT, PER, XLDS, W, D>), grid, dim3(W * 64), lds, st,
-                       a);
-    return hipGetLastError();
+    return static_cast<size_t>(planes<T> * (a.T < FEW ? a.T : FEW) * xpitch * 2);
 }
 
 template <typename T, int PER>
+hipError_t launch_few(const FourbitArgs &a, hipStream_t st)
+{
+    // (with 43 KiB of the waves' sums and lines)
+    if (few_lds<T>(a) > 64 * 1024)
+        return hipErrorInvalidValue;
+    const int64_t tiles = (a.d_out + 15) / 16, rounds = (tiles + 255) / 256;
+    const dim3 grid(static_cast<unsigned>((tiles + rounds - 1) / rounds),
+                    static_cast<unsigned>((a.T + FEW - 1) / FEW));
+    hipLaunchKernelGGL((linear_fourbit_kernel<T, PER, FEW_WAVES>), grid, dim3(FEW_WAVES * 64),
+                       few_lds<T>(a), st, a);
+    return hipGetLastError();
+}
+
+template <typename T, int TM, int NT, int PER, int CW, int KG, int D>
+hipError_t launch_shared(const FourbitArgs &a, hipStream_t st)
+{
+    constexpr size_t LDS = 2 * KG * planes<T> * 16 * TM * LINE * 2 + KG * CW * NT * 2048;
+    static_assert(LDS <= 160 * 1024, "LDS");
+    const dim3 grid(static_cast<unsigned>((a.d_out + CW * 16 * NT - 1) / (CW * 16 * NT)),
+                    static_cast<unsigned>((a.T + 16 * TM - 1) / (16 * TM)));
+    hipLaunchKernelGGL((linear_fourbit_shared_kernel<T, TM, NT, PER, CW, KG, D>), grid,
+                       dim3(CW * KG * 64), 0, st, a);
+    return hipGetLastError();
+}
+
+// Up to four tokens whose rows fit in LDS, and rows of less than a line, take the first kernel.
+// The other one's tile is the widest that makes 192 workgroups (us at 14336 channels of 4096, 24
+// tokens: 64 channels 14, 128 19, 32 20; at 8192 of 8192: 32 channels 18, 64 23, 128 34); 33 to
+// 64 tokens over many channels share a read of the codes (28672 of 8192: 59, two blocks of 32
+// tokens 74).
+template <typename T, int PER>
 hipError_t launch_per(const FourbitArgs &a, hipStream_t st)
 {
-    const int64_t xpitch = (a.d_in + LINE - 1) / LINE * LINE + 8;
-    if (planes<T> * a.T * xpitch * 2 <= 64 * 1024 && a.T <= 4)
-        return launch<T, 1, 2, PER, true, 4, 3>(a, st);
-    if (a.T <= 16)
-        return launch<T, 1, 4, PER, false, 4, 2>(a, st);
-    return launch<T, 2, 2, PER, false, 4, 2>(a, st);
+    if (a.d_in < LINE || (a.T <= FEW && few_lds<T>(a) <= 64 * 1024))
+        return launch_few<T, PER>(a, st);
+    auto fills = [&](int channels, int tokens) {
+        return (a.d_out + channels - 1) / channels * ((a.T + tokens - 1) / tokens) >= 192;
+    };
+    if constexpr (sizeof(T) == 4) {
+        // (three planes of the tokens: 16 of them at a time)
+        if (fills(64, 16))
+            return launch_shared<T, 1, 1, PER, 4, 2, 2>(a, st);
+        return launch_shared<T, 1, 1, PER, 2, 2, 2>(a, st);
+    } else {
+        if (a.T <= 16)
+            return fills(64, 16) ? launch_shared<T, 1, 1, PER, 4, 2, 2>(a, st)
+                                 : launch_shared<T, 1, 1, PER, 2, 4, 1>(a, st);
+        if (a.T > 32 && fills(128, 64))
+            return launch_shared<T, 4, 1, PER, 8, 1, 1>(a, st);
+        if (fills(128, 32))
+            return launch_shared<T, 2, 2, PER, 4, 2, 2>(a, st);
+        if (fills(64, 32))
+            return launch_shared<T, 2, 1, PER, 4, 2, 1>(a, st);
+        return launch_shared<T, 2, 1, PER, 2, 4, 1>(a, st);
+    }
 }
 
 template <typename T>

@@ -490,13 +490,13 @@ int dora_block_norm_backward(const void *dy, const void *dh, const void *x, cons
  * dora_linear_fourbit - dora_linear for a weight held this way (codes and scale of
  * dora_quantize_fourbit on the merged weight of dora_merge, with group), y = x W^T
  * with fp32 sums, rounded once.  x [T, d_in], y [T, d_out] in `dtype`.
- *   Up to 64 tokens read the codes as they are: products with the codes' values,
+ *   Up to 256 tokens read the codes as they are: products with the codes' values,
  *   each group's fp32 sum times its scale (fp32 tokens of 2^-100 and less in
  *   magnitude may lose bits there, and the sums of six times a group's tokens must
- *   stay finite).  More tokens restore the weight into the workspace, some of its
+ *   stay finite).  More tokens (or 2^23 columns) restore the weight into the workspace, some of its
  *   rows at a time, rounded once to `dtype`: exact for scales of six bits.
  *   y must not overlap any input.  ws: dora_linear_fourbit_workspace(T, d_in, d_out,
- *   dtype) bytes: none up to 64 tokens (ws may be NULL); beyond, 128 MiB or 256 rows
+ *   dtype) bytes: none up to 256 tokens (ws may be NULL); beyond, 128 MiB or 256 rows
  *   of the weight at most, and split-K partials of y where the product needs them.
  */
 int dora_quantize_fourbit(const void *x, int64_t rows, int64_t d, int dtype, int64_t group,

@@ -159,9 +159,9 @@ def linear4(x=AT[0], codes=AT[1], scale=AT[2], group=32, T=4, d_in=64, d_out=32,
     ({"x": 0}, E_NULL), ({"codes": 0}, E_NULL), ({"scale": 0}, E_NULL), ({"y": 0}, E_NULL),
     ({"T": -1}, E_SHAPE), ({"d_in": 0}, E_SHAPE), ({"d_out": 0}, E_SHAPE), ({"group": 48}, E_SHAPE),
     ({"dt": 4}, E_DTYPE), ({"x": AT[0] + 2}, E_ALIGN), ({"codes": AT[1] + 1}, E_ALIGN),
-    ({"T": 65, "ws": 0}, E_WS), ({"T": 65, "ws_bytes": 100}, E_WS), ({"y": AT[0]}, E_ALIAS),
-    ({"y": AT[1] + 16}, E_ALIAS), ({"y": AT[2]}, E_ALIAS), ({"T": 65, "ws": AT[1]}, E_ALIAS),
-    ({"T": 65, "ws": AT[3]}, E_ALIAS),
+    ({"T": 257, "ws": 0}, E_WS), ({"T": 257, "ws_bytes": 100}, E_WS), ({"y": AT[0]}, E_ALIAS),
+    ({"y": AT[1] + 16}, E_ALIAS), ({"y": AT[2]}, E_ALIAS), ({"T": 257, "ws": AT[1]}, E_ALIAS),
+    ({"T": 257, "ws": AT[3]}, E_ALIAS),
 ])
 def test_linear_fourbit_refuses(kw, code):
     assert linear4(**kw) == code
@@ -170,13 +170,13 @@ def test_linear_fourbit_refuses(kw, code):
 
 def test_linear_fourbit_workspace_holds_no_dense_weight():
     q = D.dora_linear_fourbit_workspace
-    for T in (0, 1, 64):
+    for T in (0, 1, 256):
         assert q(T, 8192, 28672, BF16) == 0
-    assert q(-1, 8, 8, BF16) == 0 and q(100, 0, 8, BF16) == 0 and q(100, 8, 8, 5) == 0
+    assert q(-1, 8, 8, BF16) == 0 and q(300, 0, 8, BF16) == 0 and q(300, 8, 8, 5) == 0
     for dt, e in ((BF16, 2), (F32, 4)):
         for d_in, d_out in ((8192, 28672), (28672, 8192), (1 << 17, 1 << 14), (100, 1 << 20)):
-            part = 32 * 65 * d_out * 4
-            assert 0 < q(65, d_in, d_out, dt) <= max(128 << 20, 256 * d_in * e) + part + 512
+            part = 32 * 257 * d_out * 4
+            assert 0 < q(257, d_in, d_out, dt) <= max(128 << 20, 256 * d_in * e) + part + 512
 
 
 def test_plain_fourbit_is_the_nearest_value():

@@ -3,7 +3,7 @@ plain forms in 64 bits.
 
 Rows: the same values and scales, exactly (the rounding is decided exactly, and
 a scale of six bits times a code of two is a bf16 number).
-The linear layer (u = 2^-24): up to 64 tokens exact products and fp32 sums in
+The linear layer (u = 2^-24): up to 256 tokens exact products and fp32 sums in
 any order, d_in terms, each group's sum times its scale: (d_in + 8) u sum |x w|
 at most (no order of d_in additions is off by more), and the output's rounding,
 2^-8 |y| for bf16 and 2^-24 |y| for fp32; more tokens the same bound, the
@@ -136,7 +136,7 @@ def check_linear(T, d_in, d_out, dt, group, bits=6, x=None):
         x = x.to(dt)
     y = D.dora_linear_fourbit(x.to(DEV), codes, scale, group=group)
     W = R.restored(codes.cpu(), scale.cpu(), d_in, group)
-    rounded = W if T <= 64 else W.to(dt).double()
+    rounded = W if T <= 256 else W.to(dt).double()
     ref = x.double() @ rounded.T
     bound = (d_in + 8) * U * (x.double().abs() @ W.abs().T) + ref.abs() * half(dt)
     off = (y.cpu().double() - ref).abs()
@@ -165,18 +165,29 @@ def test_linear_sizes(d_in, d_out, dt):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("T,d_in,d_out,group", [
-    (65, 1029, 515, 32), (100, 256, 1024, 64), (129, 100, 70, 128), (300, 2048, 512, 128),
-    (70, 513, 9, 512)])
+    (65, 1029, 515, 32), (100, 256, 1024, 64), (129, 100, 70, 128), (256, 300, 40, 64),
+    (257, 1029, 515, 32), (300, 2048, 512, 128), (270, 513, 9, 512), (400, 31, 70, 32)])
 def test_linear_more_tokens(T, d_in, d_out, group, dt):
     check_linear(T, d_in, d_out, dt, group)
     check_linear(T, d_in, d_out, dt, group, bits=8)
+
+
+@pytest.mark.parametrize("dt,T,d_out", [
+    (BF, 4, 30000), (BF, 16, 12400), (BF, 16, 4000), (BF, 40, 24700), (BF, 64, 12300), (BF, 20, 24600),
+    (BF, 20, 12300), (BF, 20, 4000), (BF, 200, 6200), (F32, 16, 12400), (F32, 30, 4000),
+    (F32, 4, 4200)])
+def test_linear_every_kernel(dt, T, d_out):
+    """Enough channels that each tile rule is met from both sides, tiles cut off at the end, and
+    workgroups that walk several tiles."""
+    for d_in, group in ((512, 128), (700, 32), (1500, 256)):
+        check_linear(T, d_in, d_out - 3, dt, group)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_linear_in_panels(dt):
     """A weight of more rows than a panel holds: the last panel is a short one."""
     d_in = 1 << 17
-    check_linear(66, d_in, 2 * (512 if dt == BF else 256) + 37, dt, 512)
+    check_linear(258, d_in, 2 * (512 if dt == BF else 256) + 37, dt, 512)
 
 
 def test_linear_nonfinite_tokens_and_scales():
@@ -244,7 +255,7 @@ def test_linear_no_tokens_and_padding():
     assert torch.equal(D.dora_linear_fourbit(x, codes, scale, group=32), y)
 
 
-@pytest.mark.parametrize("T", [1, 20, 200])
+@pytest.mark.parametrize("T", [1, 20, 200, 300])
 def test_streams_and_graphs(T):
     x, codes, scale, y = check_linear(T, 1024, 640, BF, 128)
     x = x.to(DEV)
@@ -328,7 +339,7 @@ def test_python_refuses():
             (TypeError, lambda: D.dora_linear_fourbit(x, codes, scale, group=32,
                                                       y=torch.empty(4, 4, device=DEV))),
             (D.DoraError, lambda: D.dora_linear_fourbit(
-                torch.zeros(100, 64, device=DEV, dtype=BF), codes, scale, group=32,
+                torch.zeros(300, 64, device=DEV, dtype=BF), codes, scale, group=32,
                 ws=torch.empty(16, dtype=torch.uint8, device=DEV)))):
         with pytest.raises(bad):
             call()
