@@ -43,10 +43,11 @@ hipError_t launch_block_norm_grad(int bf16, const BlockNormGradArgs &a, const Bl
 // 4-bit rows: e2m1 codes two a byte, rows of whole groups (`groups` of them), bf16 scales.
 hipError_t launch_quantize_fourbit(int bf16, const void *x, int64_t rows, int64_t d, int group,
                                    uint8_t *codes, uint16_t *scale, hipStream_t st);
-// ldo: elements between rows of `out`.
 hipError_t launch_dequantize_fourbit(int bf16, const uint8_t *codes, const uint16_t *scale,
-                                     int64_t rows, int64_t d, int group, void *out, int64_t ldo,
-                                     hipStream_t st);
+                                     int64_t rows, int64_t d, int group, void *out, hipStream_t st);
+// out[m, n] = sum_z part[z, m, n] in order, rounded once; ldo elements between rows of `out`.
+hipError_t launch_sum_splits(int bf16, const float *part, int splits, int64_t M, int64_t N, void *out,
+                             int64_t ldo, hipStream_t st);
 struct FourbitArgs {
     const void *x;  // [T, d_in]
     const uint8_t *codes;

@@ -2412,14 +2412,17 @@ FourbitPlan plan_fourbit(int64_t T, int64_t d_in, int64_t d_out, int dtype)
     const int64_t most = std::max<int64_t>(kFourbitPanel / row / 256 * 256, 256);
     const int64_t count = (d_out + most - 1) / most;
     p.panel = count == 1 ? d_out : ((d_out + count - 1) / count + 255) / 256 * 256;
-    const int64_t part = count == 1 ? T * d_out : kNoSplit;
-    p.g = plan_gemm(bf, nt_shape(T, p.panel, d_in), part);
+    p.g = plan_gemm(bf, nt_shape(T, p.panel, d_in), T * p.panel);
     p.last = p.g;
-    if (d_out % p.panel)
-        p.last = plan_gemm(bf, nt_shape(T, d_out % p.panel, d_in), part);
+    size_t part = p.g.splits > 1 ? static_cast<size_t>(p.g.splits) * T * p.panel * 4 : 0;
+    if (const int64_t rest = d_out % p.panel) {
+        p.last = plan_gemm(bf, nt_shape(T, rest, d_in), T * rest);
+        if (p.last.splits > 1)
+            part = std::max(part, static_cast<size_t>(p.last.splits) * T * rest * 4);
+    }
     Carve cv;
     cv.take(static_cast<size_t>(p.panel) * row);
-    p.o_part = cv.take(p.g.splits > 1 ? static_cast<size_t>(p.g.splits) * T * d_out * 4 : 0);
+    p.o_part = cv.take(part);
     p.bytes = cv.off;
     return p;
 }
@@ -2459,7 +2462,7 @@ int dora_dequantize_fourbit(const void *codes, const void *scale, int64_t rows, 
                                {{scale, fourbit_scales(rows, d, group)}, "scale"}}));
     DORA_LAUNCH(launch_dequantize_fourbit(dtype == DORA_BF16, static_cast<const uint8_t *>(codes),
                                           static_cast<const uint16_t *>(scale), rows, d,
-                                          static_cast<int>(group), out, d,
+                                          static_cast<int>(group), out,
                                           static_cast<hipStream_t>(stream)),
                 "restore from 4 bits");
     return DORA_OK;
@@ -2505,12 +2508,18 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
     for (int64_t n0 = 0; n0 < d_out; n0 += p.panel) {
         const int64_t n = std::min(p.panel, d_out - n0);
         DORA_LAUNCH(launch_dequantize_fourbit(bf, c + n0 * groups * (group / 2), s + n0 * groups, n,
-                                              d_in, static_cast<int>(group), ws, d_in, st),
+                                              d_in, static_cast<int>(group), ws, st),
                     "restore from 4 bits");
-        DORA_CHECK(run_store(bf, n == p.panel ? p.g : p.last, seg1(T, n, x, d_in, ws, d_in, d_in), 0,
-                             static_cast<char *>(y) + n0 * e, d_out, 1.0f,
-                             reinterpret_cast<float *>(static_cast<char *>(ws) + p.o_part), st,
-                             "linear x W^T"));
+        const GPlan &g = n == p.panel ? p.g : p.last;
+        const GemmArgs a = seg1(T, n, x, d_in, ws, d_in, d_in);
+        char *const out = static_cast<char *>(y) + n0 * e;
+        if (g.splits <= 1) {
+            DORA_CHECK(run_store(bf, g, a, 0, out, d_out, 1.0f, nullptr, st, "linear x W^T"));
+        } else {
+            float *const part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.o_part);
+            DORA_CHECK(run_slots(bf, g, a, 0, part, 1.0f, st, "linear x W^T"));
+            DORA_LAUNCH(launch_sum_splits(bf, part, g.splits, T, n, out, d_out, st), "linear x W^T");
+        }
     }
     return DORA_OK;
 }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS)
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
     dequantize_fourbit_kernel(const uint8_t *codes, const uint16_t *scale, int64_t rows, int64_t d,
-                              int64_t groups, int group, T *out, int64_t ldo)
+                              int64_t groups, int group, T *out)
 {
     const int lanes = group / 8, shift = 31 - __clz(lanes);
     const int64_t row_vecs = groups * lanes, vecs = (d + 7) / 8;
@@ -139,9 +139,39 @@ __global__ void __launch_bounds__(THREADS)
                                     e[0] * by, e[1] * by, g[0] * by, g[1] * by};
                 Raw8<T> o;
                 o.set(f);
-                o.store(out + t * ldo + v * 8, count8(d, v * 8));
+                o.store(out + t * d + v * 8, count8(d, v * 8));
             }
         }
+    }
+}
+
+// out[m, n] = sum_z part[z, m, n], in order, rounded once; rows of `out` ldo apart.
+template <typename T>
+__global__ void __launch_bounds__(THREADS)
+    sum_splits_kernel(const float *part, int splits, int64_t M, int64_t N, T *out, int64_t ldo)
+{
+    const int64_t vecs = (N + 7) / 8, total = vecs * M;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(THREADS) + threadIdx.x; i < total;
+         i += gridDim.x * static_cast<int64_t>(THREADS)) {
+        const int64_t m = i / vecs, n = i % vecs * 8;
+        const int cnt = count8(N, n);
+        float acc[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            acc[q] = 0.f;
+#pragma unroll 4
+        for (int z = 0; z < splits; ++z) {
+            Raw8<float> r;
+            r.load(part + (z * M + m) * N + n, cnt);
+            float f[8];
+            r.get(f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                acc[q] += f[q];
+        }
+        Raw8<T> o;
+        o.set(acc);
+        o.store(out + m * ldo + n, cnt);
     }
 }
 
@@ -165,8 +195,7 @@ hipError_t launch_quantize_fourbit(int bf16, const void *x, int64_t rows, int64_
 }
 
 hipError_t launch_dequantize_fourbit(int bf16, const uint8_t *codes, const uint16_t *scale,
-                                     int64_t rows, int64_t d, int group, void *out, int64_t ldo,
-                                     hipStream_t st)
+                                     int64_t rows, int64_t d, int group, void *out, hipStream_t st)
 {
     if (rows == 0)
         return hipSuccess;
@@ -175,10 +204,24 @@ hipError_t launch_dequantize_fourbit(int bf16, const uint8_t *codes, const uint1
     const dim3 grid(static_cast<unsigned>(s.groups), s.shares), block(s.along, s.rows);
     if (bf16)
         hipLaunchKernelGGL((dequantize_fourbit_kernel<uint16_t>), grid, block, 0, st, codes, scale,
-                           rows, d, groups, group, static_cast<uint16_t *>(out), ldo);
+                           rows, d, groups, group, static_cast<uint16_t *>(out));
     else
         hipLaunchKernelGGL((dequantize_fourbit_kernel<float>), grid, block, 0, st, codes, scale, rows,
-                           d, groups, group, static_cast<float *>(out), ldo);
+                           d, groups, group, static_cast<float *>(out));
+    return hipGetLastError();
+}
+
+hipError_t launch_sum_splits(int bf16, const float *part, int splits, int64_t M, int64_t N, void *out,
+                             int64_t ldo, hipStream_t st)
+{
+    const int64_t groups = ((N + 7) / 8 * M + THREADS - 1) / THREADS;
+    const dim3 grid(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20));
+    if (bf16)
+        hipLaunchKernelGGL((sum_splits_kernel<uint16_t>), grid, dim3(THREADS), 0, st, part, splits, M,
+                           N, static_cast<uint16_t *>(out), ldo);
+    else
+        hipLaunchKernelGGL((sum_splits_kernel<float>), grid, dim3(THREADS), 0, st, part, splits, M, N,
+                           static_cast<float *>(out), ldo);
     return hipGetLastError();
 }
 
