@@ -24,7 +24,7 @@ SOURCES = [("gemm_bf16.hip", (), "gemm_bf16"), ("gemm_bf16_any.hip", (), "gemm_b
            ("noalloc.hip", (), "noalloc"),
            ("rows8.hip", (), "rows8"), ("gemm_rows8.hip", (), "gemm_rows8"),
            ("block_norm.hip", (), "block_norm"), ("fourbit.hip", (), "fourbit"),
-           ("gemm_fourbit.hip", (), "gemm_fourbit"),
+           ("gemm_fourbit.hip", (), "gemm_fourbit"), ("newton_schulz.hip", (), "newton_schulz"),
            ("gemm_i8.hip", (), "gemm_i8"),
            ("gemm_i8_dma.hip", (), "gemm_i8_dma"), ("gemm_i8_rows.hip", (), "gemm_i8_rows")] + \
           [("gemm_dma_cfg.hip", (f"-DDORA_DMA_CFG={k}",), f"gemm_dma_cfg{k}") for k in range(8)]

@@ -59,4 +59,27 @@ struct FourbitArgs {
 };
 hipError_t launch_linear_fourbit(int bf16, const FourbitArgs &a, hipStream_t st);
 
+// --------------------------------------------------------------- newton_schulz.hip
+// One matrix U [rows, cols]: the gradient g alone, or, with a momentum, g + mu M' or M' for
+// M' = mu M + g.  Its orthogonalised form O goes to `out`, or out = keep p - step O.
+struct NsMatrix {
+    const void *g, *p;  // p may be null
+    const float *m;     // may be null
+    float *m_out;
+    void *out;
+    int64_t rows, cols;
+    float step, keep;
+};
+struct NsParams {
+    float mu;
+    int nesterov, steps;
+    float a, b, c, eps;
+};
+constexpr int NS_MAX_STEPS = 16;
+constexpr int64_t NS_MAX_SHORT = 8192;  // the shorter side
+bool newton_schulz_fits(int64_t rows, int64_t cols);
+size_t newton_schulz_workspace(int bf16, const NsMatrix *mats, int count);
+hipError_t launch_newton_schulz(int bf16, const NsMatrix *mats, int count, const NsParams &p, void *ws,
+                                hipStream_t st);
+
 }  // namespace dora

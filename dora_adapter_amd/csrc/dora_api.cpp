@@ -13,6 +13,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <exception>
 #include <initializer_list>
 #include <vector>
 
@@ -2522,6 +2523,188 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
         }
     }
     return DORA_OK;
+}
+
+// ------------------------------------------------- orthogonalised updates
+namespace {
+
+constexpr float kQuintic[3] = {3.4445f, -4.7750f, 2.0315f};
+
+int check_newton_schulz(int steps, const float *coefficients, float eps, NsParams &p)
+{
+    if (steps < 1 || steps > NS_MAX_STEPS)
+        return fail(DORA_E_VALUE, "steps=%d out of range [1, %d]", steps, NS_MAX_STEPS);
+    if (!(eps >= 0.f) || eps > 3.4e38f)
+        return fail(DORA_E_VALUE, "eps must be finite and not negative");
+    const float *c = coefficients ? coefficients : kQuintic;
+    DORA_CHECK(check_scalars({{c[0], "coefficients[0]"}, {c[1], "coefficients[1]"},
+                              {c[2], "coefficients[2]"}}));
+    p.steps = steps;
+    p.a = c[0];
+    p.b = c[1];
+    p.c = c[2];
+    p.eps = eps;
+    p.mu = 0.f;
+    p.nesterov = 0;
+    return DORA_OK;
+}
+
+int check_matrix(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || rows > kMaxDim || cols < 1 || cols > kMaxDim)
+        return fail(DORA_E_SHAPE, "need 1 <= rows, cols < 2^31 (got %lld, %lld)", (long long)rows,
+                    (long long)cols);
+    if (!newton_schulz_fits(rows, cols))
+        return fail(DORA_E_SHAPE, "[%lld, %lld]: the shorter side may be up to %lld, and the matrix "
+                    "hold 2^33 elements", (long long)rows, (long long)cols, (long long)NS_MAX_SHORT);
+    return DORA_OK;
+}
+
+NsMatrix shape_only(int64_t rows, int64_t cols)
+{
+    NsMatrix m;
+    memset(&m, 0, sizeof m);
+    m.rows = rows;
+    m.cols = cols;
+    return m;
+}
+
+constexpr int kMaxUpdates = 1 << 16;
+
+// The matrices of a list of updates (their shapes alone for a query).
+int update_matrices(const dora_update *updates, int count, std::vector<NsMatrix> &mats)
+{
+    if (count < 0 || count > kMaxUpdates)
+        return fail(DORA_E_SHAPE, "count=%d out of range [0, %d]", count, kMaxUpdates);
+    if (count > 0 && !updates)
+        return fail(DORA_E_NULL, "updates is NULL");
+    mats.reserve(static_cast<size_t>(count));
+    for (int i = 0; i < count; ++i) {
+        DORA_CHECK(check_matrix(updates[i].rows, updates[i].cols));
+        mats.push_back(shape_only(updates[i].rows, updates[i].cols));
+    }
+    return DORA_OK;
+}
+
+}  // namespace
+
+size_t dora_orthogonalize_workspace(int64_t rows, int64_t cols, int dtype)
+{
+    if (check_dtype(dtype) || check_matrix(rows, cols))
+        return 0;
+    const NsMatrix m = shape_only(rows, cols);
+    return newton_schulz_workspace(dtype == DORA_BF16, &m, 1);
+}
+
+int dora_orthogonalize(const void *U, int64_t rows, int64_t cols, int dtype, int steps,
+                       const float *coefficients, float eps, void *O, void *ws, size_t ws_bytes,
+                       void *stream)
+{
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    DORA_CHECK(check_matrix(rows, cols));
+    NsParams p;
+    DORA_CHECK(check_newton_schulz(steps, coefficients, eps, p));
+    DORA_CHECK(check_ptrs({{U, "U", true}, {O, "O", true}}));
+    NsMatrix m = shape_only(rows, cols);
+    m.g = U;
+    m.out = O;
+    const bool bf = dtype == DORA_BF16;
+    const size_t need = newton_schulz_workspace(bf, &m, 1);
+    DORA_CHECK(check_ws(ws, ws_bytes, need));
+    const size_t bytes = static_cast<size_t>(rows) * cols * esize(dtype);
+    if (O != U && overlap({O, bytes}, {U, bytes}))
+        return fail(DORA_E_ALIAS, "O partially overlaps U");
+    DORA_CHECK(check_disjoint({{{ws, need}, "workspace"}}, {{{U, bytes}, "U"}, {{O, bytes}, "O"}}));
+    DORA_LAUNCH(launch_newton_schulz(bf, &m, 1, p, ws, static_cast<hipStream_t>(stream)),
+                "orthogonalize");
+    return DORA_OK;
+}
+
+size_t dora_muon_workspace(const dora_update *updates, int count, int dtype)
+try {
+    std::vector<NsMatrix> mats;
+    if (check_dtype(dtype) || update_matrices(updates, count, mats))
+        return 0;
+    return newton_schulz_workspace(dtype == DORA_BF16, mats.data(), count);
+} catch (const std::exception &) {
+    return 0;
+}
+
+int dora_muon(const dora_update *updates, int count, int dtype, float mu, int nesterov, int steps,
+              const float *coefficients, float eps, void *ws, size_t ws_bytes, void *stream)
+try {
+    g_last_error[0] = '\0';
+    DORA_CHECK(check_dtype(dtype));
+    std::vector<NsMatrix> mats;
+    DORA_CHECK(update_matrices(updates, count, mats));
+    NsParams p;
+    DORA_CHECK(check_newton_schulz(steps, coefficients, eps, p));
+    DORA_CHECK(check_scalars({{mu, "mu"}}));
+    p.mu = mu;
+    p.nesterov = nesterov != 0;
+    const bool bf = dtype == DORA_BF16;
+    const size_t need = newton_schulz_workspace(bf, mats.data(), count);
+    DORA_CHECK(check_ws(ws, ws_bytes, need));
+    // Every buffer of the list but the inputs that their own output replaces (the same element,
+    // read before it is written): no output may overlap any other of them.
+    struct Buffer {
+        const char *from, *to;
+        bool out;
+        int item;
+    };
+    std::vector<Buffer> all;
+    all.reserve(5 * static_cast<size_t>(count) + 1);
+    auto add = [&](const void *q, size_t bytes, bool out, int item) {
+        if (q && bytes > 0)
+            all.push_back({static_cast<const char *>(q), static_cast<const char *>(q) + bytes, out, item});
+    };
+    for (int i = 0; i < count; ++i) {
+        const dora_update &u = updates[i];
+        const int rc = [&]() {
+            DORA_CHECK(check_ptrs({{u.param, "param", true}, {u.grad, "grad", true},
+                                   {u.momentum, "momentum", true}, {u.param_out, "param_out", true},
+                                   {u.momentum_out, "momentum_out", true}}));
+            return check_scalars({{u.lr, "lr"}, {u.weight_decay, "weight_decay"}, {u.scale, "scale"}});
+        }();
+        if (rc != DORA_OK) {
+            char why[256];
+            snprintf(why, sizeof why, "%s", g_last_error);
+            return fail(rc, "update %d: %s", i, why);
+        }
+        const size_t size = static_cast<size_t>(u.rows) * u.cols, pb = size * esize(dtype), mb = size * 4;
+        add(u.param_out, pb, true, i);
+        add(u.momentum_out, mb, true, i);
+        add(u.param == u.param_out ? nullptr : u.param, pb, false, i);
+        add(u.momentum == u.momentum_out ? nullptr : u.momentum, mb, false, i);
+        add(u.grad, pb, false, i);
+        NsMatrix &m = mats[static_cast<size_t>(i)];
+        m.g = u.grad;
+        m.p = u.param;
+        m.m = u.momentum;
+        m.m_out = u.momentum_out;
+        m.out = u.param_out;
+        m.keep = static_cast<float>(1.0 - static_cast<double>(u.lr) * u.weight_decay);
+        m.step = static_cast<float>(static_cast<double>(u.lr) * u.scale);
+    }
+    add(ws, need, true, -1);
+    std::sort(all.begin(), all.end(), [](const Buffer &x, const Buffer &y) { return x.from < y.from; });
+    const char *end = nullptr, *out_end = nullptr;  // of all so far, of the outputs
+    for (const Buffer &b : all) {
+        if (b.from < out_end || (b.out && b.from < end))
+            return fail(DORA_E_ALIAS, "an output overlaps another buffer of the list (at one of "
+                        "update %d; -1: the workspace)", b.item);
+        end = std::max(end, b.to);
+        if (b.out)
+            out_end = std::max(out_end, b.to);
+    }
+    if (count == 0)
+        return DORA_OK;
+    DORA_LAUNCH(launch_newton_schulz(bf, mats.data(), count, p, ws, static_cast<hipStream_t>(stream)),
+                "muon step");
+    return DORA_OK;
+} catch (const std::exception &e) {
+    return fail(DORA_E_VALUE, "muon step: %s", e.what());
 }
 
 }  // extern "C"

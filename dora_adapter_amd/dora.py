@@ -31,7 +31,8 @@ EXPORTS = ("dora_strerror", "dora_last_error", "dora_norm_workspace", "dora_forw
            "dora_linear_quantized", "dora_backward_checkpoint_workspace",
            "dora_backward_checkpoint", "dora_block_norm", "dora_block_norm_backward_workspace",
            "dora_block_norm_backward", "dora_quantize_fourbit", "dora_dequantize_fourbit",
-           "dora_linear_fourbit_workspace", "dora_linear_fourbit")
+           "dora_linear_fourbit_workspace", "dora_linear_fourbit", "dora_orthogonalize_workspace",
+           "dora_orthogonalize", "dora_muon_workspace", "dora_muon")
 
 _lib = None
 
@@ -41,6 +42,15 @@ class DoraModule(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("m", ctypes.c_void_p), ("s", ctypes.c_float), ("d_out", ctypes.c_int64),
                 ("d_in", ctypes.c_int64), ("r", ctypes.c_int64)]
+
+
+class DoraUpdate(ctypes.Structure):
+    """struct dora_update of include/dora.h."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p), ("param_out", ctypes.c_void_p),
+                ("momentum_out", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
 class DoraError(RuntimeError):
@@ -138,6 +148,15 @@ def lib():
         L.dora_linear_fourbit_workspace.argtypes = [i64, i64, i64, c_int]
         L.dora_linear_fourbit.restype = c_int
         L.dora_linear_fourbit.argtypes = [p, p, p, i64, i64, i64, i64, c_int, p, p, sz, p]
+        up, fp = ctypes.POINTER(DoraUpdate), ctypes.POINTER(f)
+        L.dora_orthogonalize_workspace.restype = sz
+        L.dora_orthogonalize_workspace.argtypes = [i64, i64, c_int]
+        L.dora_orthogonalize.restype = c_int
+        L.dora_orthogonalize.argtypes = [p, i64, i64, c_int, c_int, fp, f, p, p, sz, p]
+        L.dora_muon_workspace.restype = sz
+        L.dora_muon_workspace.argtypes = [up, c_int, c_int]
+        L.dora_muon.restype = c_int
+        L.dora_muon.argtypes = [up, c_int, c_int, f, c_int, c_int, fp, f, p, sz, p]
         _lib = L
     return _lib
 
@@ -809,3 +828,78 @@ def dora_linear_fourbit(x, codes, scale, group=128, y=None, ws=None):
     _launch(dev, lib().dora_linear_fourbit, _at(x), _at(codes), _at(scale), group, T, d_in, d_out,
             dt, _at(y), _at(ws), 0 if ws is None else ws.numel())
     return y
+
+
+# ------------------------------------------------- orthogonalised updates
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def _coefficients(c):
+    a, b, d = (float(v) for v in c)
+    return (ctypes.c_float * 3)(a, b, d)
+
+
+def dora_orthogonalize_workspace(rows, cols, dtype):
+    return lib().dora_orthogonalize_workspace(rows, cols, dtype)
+
+
+def dora_orthogonalize(U, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, ws=None):
+    """Newton-Schulz steps X <- a X + b (X X^T) X + c (X X^T)^2 X from X = U / (|U| + eps), U
+    [rows, cols]: the orthogonal matrix near U, its singular values brought close to one.  out
+    may be U."""
+    dev = _dev(U)
+    rows, cols = _rows("U", U)
+    dt = _dt(U)
+    _need("U", U, dev, U.dtype, rows, cols)
+    out = torch.empty_like(U) if out is None else _need("out", out, dev, U.dtype, rows, cols)
+    if _need_ws(ws, dev) is None:
+        ws = _ws(dora_orthogonalize_workspace(rows, cols, dt), dev)
+    _launch(dev, lib().dora_orthogonalize, _at(U), rows, cols, dt, int(steps),
+            _coefficients(coefficients), float(eps), _at(out), _at(ws), ws.numel())
+    return out
+
+
+def dora_muon_workspace(params):
+    """Bytes for dora_muon on these parameters (their shapes and type)."""
+    if not params:
+        return 0
+    arr = (DoraUpdate * len(params))()
+    for k, q in enumerate(params):
+        arr[k].rows, arr[k].cols = _rows(f"params[{k}]", q)
+    return lib().dora_muon_workspace(arr, len(params), _dt(params[0]))
+
+
+def dora_muon(params, grads, momenta, lr, mu=0.95, weight_decay=0.0, scales=None, nesterov=True,
+              steps=5, coefficients=QUINTIC, eps=1e-7, params_out=None, momenta_out=None, ws=None):
+    """One step of the Muon optimiser on a list of matrices (for instance every adapter's A and
+    B with the gradients of dora_backward), in few launches: momentum M <- mu M + grad (fp32),
+    param <- param - lr (weight_decay param + scale O) with O the orthogonalised grad + mu M
+    (nesterov; else M).  scales: one number a matrix (default 1).  In place unless params_out /
+    momenta_out are given; returns (params_out, momenta_out)."""
+    params_out = params if params_out is None else params_out
+    momenta_out = momenta if momenta_out is None else momenta_out
+    n = len(params)
+    scales = [1.0] * n if scales is None else scales
+    for name, ts in (("grads", grads), ("momenta", momenta), ("scales", scales),
+                     ("params_out", params_out), ("momenta_out", momenta_out)):
+        if len(ts) != n:
+            raise ValueError(f"{name} has {len(ts)} entries for {n} params")
+    if n == 0:
+        return params_out, momenta_out
+    dev = _dev(params[0])
+    kind, dt = params[0].dtype, _dt(params[0])
+    arr = (DoraUpdate * n)()
+    for k in range(n):
+        shape = _rows(f"params[{k}]", params[k])
+        for name, ts, t in (("params", params, kind), ("grads", grads, kind),
+                            ("momenta", momenta, torch.float32), ("params_out", params_out, kind),
+                            ("momenta_out", momenta_out, torch.float32)):
+            _need(f"{name}[{k}]", ts[k], dev, t, *shape)
+        arr[k] = DoraUpdate(params[k].data_ptr(), grads[k].data_ptr(), momenta[k].data_ptr(),
+                            params_out[k].data_ptr(), momenta_out[k].data_ptr(), *shape, float(lr),
+                            float(weight_decay), float(scales[k]))
+    if _need_ws(ws, dev) is None:
+        ws = _ws(lib().dora_muon_workspace(arr, n, dt), dev)
+    _launch(dev, lib().dora_muon, arr, n, dt, float(mu), int(bool(nesterov)), int(steps),
+            _coefficients(coefficients), float(eps), _at(ws), ws.numel())
+    return params_out, momenta_out

@@ -508,6 +508,54 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
                         int64_t T, int64_t d_in, int64_t d_out, int dtype, void *y, void *ws,
                         size_t ws_bytes, void *stream);
 
+/*
+ * Orthogonalised updates - the step of an optimiser that moves a matrix along the
+ * nearest orthogonal one to its momentum (Muon), for the factors A and B of an
+ * adapter and the gradients that dora_backward gives them.
+ *
+ * dora_orthogonalize - O = Newton-Schulz steps from U [rows, cols]:
+ *     X_0 = U / (|U|_F + eps)
+ *     X_{k+1} = a X_k + b (X_k X_k^T) X_k + c (X_k X_k^T)^2 X_k     `steps` times
+ *   (for rows > cols of the transpose, which is the same matrix), (a, b, c) =
+ *   coefficients, a host array, or 3.4445, -4.7750, 2.0315 where it is NULL: after
+ *   five steps from a matrix of singular values above 0.0015 of its norm those of O
+ *   lie between 0.68 and 1.21.  U, O in `dtype`; O may be U itself.  Formed from 16
+ *   bits of bf16 matrices' U (and 24 of fp32 ones') with the polynomials of X X^T in
+ *   64 bits, rounded once.
+ *   1 <= steps <= 16; eps finite, >= 0; the shorter side up to 8192 (or
+ *   DORA_E_SHAPE), the matrix up to 2^33 elements with its sides padded to 128s.
+ *   U may have any magnitude; an infinity or a NaN in it makes all of O NaN.
+ *
+ * dora_muon - the step of a list of matrices:
+ *     momentum_out = mu momentum + grad
+ *     U            = grad + mu momentum_out   (nesterov), else momentum_out
+ *     param_out    = param - lr (weight_decay param + scale O(U))
+ *   param, grad, param_out [rows, cols] in `dtype`, momentum, momentum_out fp32.
+ *   param_out may be param, momentum_out momentum (in place); every output is
+ *   otherwise disjoint from every other buffer of the list.  Up to 16 matrices (in 256
+ *   MiB of workspace) share each launch; the array is read during the call only.
+ *   ws: dora_orthogonalize_workspace / dora_muon_workspace bytes: copies of the
+ *   matrices (4 bytes an element, sides padded), and the short sides' squares in 64
+ *   bits.
+ */
+typedef struct dora_update {
+    const void *param;
+    const void *grad;
+    const float *momentum;
+    void *param_out;
+    float *momentum_out;
+    int64_t rows, cols;
+    float lr, weight_decay, scale;
+} dora_update;
+
+size_t dora_orthogonalize_workspace(int64_t rows, int64_t cols, int dtype);
+int dora_orthogonalize(const void *U, int64_t rows, int64_t cols, int dtype, int steps,
+                       const float *coefficients, float eps, void *O, void *ws, size_t ws_bytes,
+                       void *stream);
+size_t dora_muon_workspace(const dora_update *updates, int count, int dtype);
+int dora_muon(const dora_update *updates, int count, int dtype, float mu, int nesterov, int steps,
+              const float *coefficients, float eps, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

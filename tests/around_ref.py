@@ -124,3 +124,61 @@ def unpack(codes):
 
 def restored(codes, scale, d, group):
     return (unpack(codes) * scale.double().repeat_interleave(group, dim=1))[:, :d]
+
+
+# ---------------------------------------------------------- Newton-Schulz steps
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonal(U, steps=5, coefficients=QUINTIC, eps=1e-7):
+    """The literal steps in 64 bits."""
+    a, b, c = (float(torch.tensor(v, dtype=torch.float32)) for v in coefficients)
+    X = U.double()
+    tall = X.shape[0] > X.shape[1]
+    X = X.T if tall else X
+    X = X / (torch.linalg.vector_norm(X) + float(torch.tensor(eps, dtype=torch.float32)))
+    for _ in range(steps):
+        G = X @ X.T
+        X = a * X + (b * G + c * (G @ G)) @ X
+    return X.T if tall else X
+
+
+def steepest(steps, coefficients):
+    """The largest |f'| on [0, 1] of what the steps do to a singular value."""
+    a, b, c = coefficients
+    s = torch.linspace(0, 1, 20001, dtype=torch.float64)
+    d = torch.ones_like(s)
+    for _ in range(steps):
+        d = d * (a + 3 * b * s ** 2 + 5 * c * s ** 4)
+        s = a * s + b * s ** 3 + c * s ** 5
+    return float(d.abs().max())
+
+
+def orthogonal_bound(U, O, dt, steps=5, coefficients=QUINTIC, eps=1e-7, moved=0.0):
+    """How far (Frobenius norm) an O formed from U may be from the 64-bit one.
+
+    A change of U by d moves O by at most steepest |d| / |U| (the steps act on
+    singular values, and the divided differences of an odd f are no steeper than
+    f); bf16 matrices keep U to 2^-17 of each element, and `moved` is what U
+    itself is off by.  The product at the end is Q U with O = Q U: its elements
+    are off by 2^-15 of |Q| |U| with two bf16 numbers an operand (16 bits each, the
+    product of the low parts left out, fp32 sums), by (6 n + 8) 2^-24 with three.
+    Then the output's rounding."""
+    X = U.double() if U.shape[0] <= U.shape[1] else U.double().T
+    n = X.shape[0]
+    size = float(torch.linalg.vector_norm(X)) + eps
+    a, b, c = coefficients
+    G = X @ X.T / size ** 2
+    Q = torch.eye(n, dtype=torch.float64)
+    for _ in range(steps):
+        P = a * torch.eye(n, dtype=torch.float64) + b * G + c * (G @ G)
+        Q, G = P @ Q, P @ G @ P
+    QU = float(torch.linalg.vector_norm((Q / size).abs() @ X.abs()))
+    bf = dt == torch.bfloat16
+    off = (2.0 ** -17 if bf else 0.0) + moved
+    return (steepest(steps, coefficients) * off * min(1.0, float(torch.linalg.vector_norm(X)) / size)
+            + QU * (2.0 ** -15 if bf else (6 * n + 8) * U_) + float(torch.linalg.vector_norm(O)) * half(dt)
+            + 1e-12)
+
+
+U_ = U

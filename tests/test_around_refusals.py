@@ -190,3 +190,95 @@ def test_plain_fourbit_is_the_nearest_value():
     assert torch.equal((x - v).abs(), best)
     assert torch.equal(s.to(torch.bfloat16).double(), s)
     assert torch.equal(v.to(torch.bfloat16).double(), v)
+
+
+def ortho(U=AT[0], rows=16, cols=64, dt=BF16, steps=5, c=(3.0, -4.0, 2.0), eps=1e-7, O=AT[1], ws=AT[2],
+          ws_bytes=1 << 30):
+    k = None if c is None else (ctypes.c_float * 3)(*c)
+    return D.lib().dora_orthogonalize(_p(U), rows, cols, dt, steps, k, eps, _p(O), _p(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"U": 0}, E_NULL), ({"O": 0}, E_NULL), ({"dt": 5}, E_DTYPE), ({"rows": 0}, E_SHAPE),
+    ({"cols": -1}, E_SHAPE), ({"rows": 1 << 31}, E_SHAPE), ({"rows": 8193, "cols": 9000}, E_SHAPE),
+    ({"rows": 64, "cols": 1 << 30}, E_SHAPE), ({"steps": 0}, E_VALUE), ({"steps": 17}, E_VALUE),
+    ({"c": (float("inf"), 0, 0)}, E_VALUE), ({"eps": -1.0}, E_VALUE), ({"eps": float("nan")}, E_VALUE),
+    ({"U": AT[0] + 8}, E_ALIGN), ({"ws": 0}, E_WS), ({"ws_bytes": 1000}, E_WS),
+    ({"O": AT[0] + 16}, E_ALIAS), ({"ws": AT[0]}, E_ALIAS), ({"ws": AT[1] + 512}, E_ALIAS),
+])
+def test_orthogonalize_refuses(kw, code):
+    assert ortho(**kw) == code
+    assert D.lib().dora_last_error()
+
+
+def muon(count=2, dt=BF16, mu=0.9, steps=5, eps=1e-7, ws=AT[20], ws_bytes=1 << 32, null=False, **kw):
+    arr = (D.DoraUpdate * 2)()
+    for k in range(2):
+        at = AT[5 * k:5 * k + 5]
+        v = dict(param=at[0], grad=at[1], momentum=at[2], param_out=at[3], momentum_out=at[4], rows=16,
+                 cols=64, lr=0.1, weight_decay=0.0, scale=1.0)
+        v.update({n[:-1]: x for n, x in kw.items() if n[-1] == str(k)})
+        arr[k] = D.DoraUpdate(**{n: (x or None) if n in ("param", "grad", "momentum", "param_out",
+                                                         "momentum_out") else x for n, x in v.items()})
+    return D.lib().dora_muon(None if null else arr, count, dt, mu, 1, steps, None, eps, _p(ws), ws_bytes,
+                             None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"null": True}, E_NULL), ({"count": -1}, E_SHAPE), ({"count": (1 << 16) + 1}, E_SHAPE),
+    ({"param0": 0}, E_NULL), ({"grad1": 0}, E_NULL), ({"momentum0": 0}, E_NULL),
+    ({"param_out1": 0}, E_NULL), ({"momentum_out0": 0}, E_NULL), ({"dt": 2}, E_DTYPE),
+    ({"rows1": 0}, E_SHAPE), ({"cols0": -5}, E_SHAPE), ({"mu": float("nan")}, E_VALUE),
+    ({"lr1": float("inf")}, E_VALUE), ({"weight_decay0": float("nan")}, E_VALUE),
+    ({"scale1": float("nan")}, E_VALUE), ({"steps": 0}, E_VALUE), ({"eps": -1.0}, E_VALUE),
+    ({"grad0": AT[1] + 4}, E_ALIGN), ({"ws": 0}, E_WS), ({"ws_bytes": 4096}, E_WS),
+    ({"param_out0": AT[0] + 16}, E_ALIAS),            # a shifted view of its parameter
+    ({"param_out0": AT[1]}, E_ALIAS),                 # its gradient
+    ({"param_out1": AT[3]}, E_ALIAS),                 # the other's output
+    ({"param_out1": AT[0]}, E_ALIAS),                 # the other's parameter
+    ({"momentum_out0": AT[2] + 64}, E_ALIAS), ({"momentum_out1": AT[2]}, E_ALIAS),
+    ({"momentum_out0": AT[0]}, E_ALIAS), ({"ws": AT[6]}, E_ALIAS), ({"ws": AT[4]}, E_ALIAS),
+    # in place, but another update reads or writes it too
+    ({"param_out0": AT[0], "param1": AT[0]}, E_ALIAS),
+    ({"param_out0": AT[0], "param1": AT[0], "param_out1": AT[0]}, E_ALIAS),
+    ({"momentum_out0": AT[2], "momentum1": AT[2] + 32}, E_ALIAS),
+])
+def test_muon_refuses(kw, code):
+    assert muon(**kw) == code
+    assert D.lib().dora_last_error()
+
+
+def test_newton_schulz_workspaces():
+    q = D.dora_orthogonalize_workspace
+    assert q(0, 5, BF16) == 0 and q(5, 5, 7) == 0 and q(9000, 9000, F32) == 0
+    for dt in (BF16, F32):
+        # U, the Gram partials of 32 splits at most, six squares in 64 bits and the planes of Q
+        for rows, cols in ((16, 4096), (384, 8192), (28672, 384), (37, 1027)):
+            n, long = min(rows, cols), max(rows, cols)
+            n = 64 if n <= 64 else -(-n // 128) * 128
+            long = -(-long // 128) * 128
+            assert 0 < q(rows, cols, dt) <= n * long * 4 + n * n * (32 * 8 + 48 + 6) + 4096
+
+    def list_of(shapes):
+        arr = (D.DoraUpdate * len(shapes))()
+        for k, (r, c) in enumerate(shapes):
+            arr[k].rows, arr[k].cols = r, c
+        return D.lib().dora_muon_workspace(arr, len(shapes), BF16)
+
+    one = list_of([(384, 8192)])
+    assert one == q(384, 8192, BF16) and list_of([]) == 0
+    # sets of matrices take the workspace in turn
+    assert list_of([(384, 8192)] * 400) <= max(256 << 20, one)
+    assert list_of([(384, 8192), (0, 5)]) == 0
+
+
+@pytest.mark.parametrize("shape", [(5, 12), (12, 5), (7, 7)])
+def test_plain_steps_act_on_singular_values(shape):
+    U = torch.randn(*shape, generator=torch.Generator().manual_seed(2), dtype=torch.float64)
+    u, s, v = torch.linalg.svd(U, full_matrices=False)
+    s = s / (torch.linalg.vector_norm(s) + float(torch.tensor(1e-7)))
+    a, b, c = (float(torch.tensor(k)) for k in R.QUINTIC)
+    for _ in range(5):
+        s = a * s + b * s ** 3 + c * s ** 5
+    assert torch.allclose(R.orthogonal(U), u @ torch.diag(s) @ v, atol=1e-11)
+    assert R.steepest(5, R.QUINTIC) == pytest.approx(3.4445 ** 5, rel=1e-3)
