@@ -13,7 +13,9 @@
 // literal steps in fp32 move them by about 2^-24 / sigma; with 2^-53 the fp32 product at
 // the end is all that is left (measured against 64 bits: as far off as the literal steps).
 // That product takes its operands as two bf16 numbers each (three for fp32 matrices), which
-// hold 16 (24) bits, on the bf16 matrix cores with fp32 sums.
+// hold 16 (24) bits, on the bf16 matrix cores with fp32 sums; so does G of bf16 matrices, whose
+// output's 8 bits leave room for that (about 1e-4 of its norm), while G of fp32 matrices is formed
+// in 64 bits.
 //
 // Up to 16 matrices share each launch.
 #include "around.hpp"
@@ -41,7 +43,10 @@ struct NsItem {
     int tall, np;        // rows > cols; the shorter side padded to 64 or to 128s
     int64_t rp, cp, lp;  // rows, columns and the longer side as padded (128s)
     char *u;             // U padded with zeros, [rp, cp]: bf16 hi and lo, or fp32
-    double *part;        // Gram partials [splits, np, np], tiles on and below the diagonal
+    unsigned int *tops;  // bf16: the largest |U| of each workgroup that wrote it, as bits
+    int top_count;
+    void *part;          // Gram partials [splits, np, np], tiles on and below the diagonal:
+                         // fp32 (bf16 matrices) or fp64
     double *mat;         // G, P, Q, H [np, np] (larger matrices)
     double *scal;        // 1 / (|U|_F + eps)
     uint16_t *q;         // planes of Q / (|U|_F + eps), [planes, np, np]
@@ -55,7 +60,7 @@ struct NsGroup {
     int count;
     NsParams p;
 };
-static_assert(sizeof(NsGroup) <= 4000, "a group must fit the kernel argument space");
+static_assert(sizeof(NsGroup) <= 4032, "a group must fit the kernel argument space");
 
 __device__ __forceinline__ int find_item(const NsGroup &g, int block)
 {
@@ -95,6 +100,8 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
 {
     const NsItem &it = g.it[find_item(g, blockIdx.x)];
     const unsigned int block = blockIdx.x - g.start[find_item(g, blockIdx.x)];
+    __shared__ unsigned int wave_top[THREADS / 64];
+    unsigned int top = 0u;
     const unsigned int along = static_cast<unsigned int>(it.cp / 8);
     const unsigned int total = static_cast<unsigned int>(it.rp * it.cp / 8);
 #pragma unroll
@@ -129,6 +136,11 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
         }
         const int64_t at = static_cast<int64_t>(v) * 8;
         if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const unsigned int b = abs_bits(u[q]);
+                top = top > b ? top : b;
+            }
             u32x4_t w[2];
             split_planes(u, w);
             uint16_t *const h = reinterpret_cast<uint16_t *>(it.u) + at;
@@ -142,14 +154,41 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
                     f32x4_t{u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]};
         }
     }
+    if constexpr (sizeof(T) == 2) {
+        top = lane_max(top, 64);
+        if ((threadIdx.x & 63) == 0)
+            wave_top[threadIdx.x >> 6] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < THREADS / 64; ++w)
+                top = top > wave_top[w] ? top : wave_top[w];
+            it.tops[block] = top;
+        }
+    }
+}
+
+// The power of two that brings a bf16 matrix's largest |U| near one, where its squares (or theirs
+// of what is 2^-24 as large) would leave fp32's range; else 1.  Called by whole workgroups.
+__device__ __forceinline__ float range_scale(const NsItem &it, unsigned int *red)
+{
+    unsigned int top = 0u;
+    for (int i = threadIdx.x; i < it.top_count; i += blockDim.x) {
+        const unsigned int b = it.tops[i];
+        top = top > b ? top : b;
+    }
+    top = block_max(top, red, static_cast<int>(blockDim.x) >> 6);
+    const int e = static_cast<int>(top >> 23) - 127;
+    if (top == 0u || e == 128 || (e > -30 && e < 40))
+        return 1.f;
+    // (2^-e; |e| is at most 127)
+    return __uint_as_float(static_cast<unsigned int>(e == 127 ? 1 : 127 - e) << 23);
 }
 
 // ------------------------------------------------------------------- G = U U^T
-// 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L at a time
-// straight into registers.  An MFMA takes four of them: of a wide matrix a lane's eight
-// consecutive ones give it one each time, of a tall one they are four rows.
-template <bool FP32U>
-__global__ void __launch_bounds__(THREADS) ns_gram_kernel(NsGroup g)
+// fp32 matrices: 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L
+// at a time straight into registers.  An MFMA takes four of them: of a wide matrix a lane's
+// eight consecutive ones give it one each time, of a tall one they are four rows.
+__global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup g)
 {
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
@@ -166,7 +205,6 @@ __global__ void __launch_bounds__(THREADS) ns_gram_kernel(NsGroup g)
     const int lr = lane & 15, kq = lane >> 4;
     const int i0 = ti * TILE + 32 * (wave >> 1), j0 = tj * TILE + 32 * (wave & 1);
     const int64_t k0 = z * it.per_split, k1 = k0 + it.per_split < it.lp ? k0 + it.per_split : it.lp;
-    const uint16_t *const hi = reinterpret_cast<const uint16_t *>(it.u), *const lo = hi + it.rp * it.cp;
     const float *const f = reinterpret_cast<const float *>(it.u);
 
     f64x4_t acc[2][2];
@@ -176,56 +214,49 @@ __global__ void __launch_bounds__(THREADS) ns_gram_kernel(NsGroup g)
         for (int b = 0; b < 2; ++b)
             acc[a][b] = f64x4_t{0., 0., 0., 0.};
     // the operand of 16 rows from r0: v[s] for MFMA step s of the 32 values from k
-    auto operand = [&](double (&v)[8], int r0, int64_t k) {
+    auto operand = [&](float (&v)[8], int r0, int64_t k) {
         if (!it.tall) {
             const int64_t at = (r0 + lr) * it.cp + k + 8 * kq;
-            if constexpr (FP32U) {
-                const f32x4_t x = *reinterpret_cast<const f32x4_t *>(f + at),
-                              y = *reinterpret_cast<const f32x4_t *>(f + at + 4);
+            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(f + at),
+                          y = *reinterpret_cast<const f32x4_t *>(f + at + 4);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    v[s] = x[s];
-                    v[4 + s] = y[s];
-                }
-            } else {
-                const u32x4_t x = *reinterpret_cast<const u32x4_t *>(hi + at),
-                              y = *reinterpret_cast<const u32x4_t *>(lo + at);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    v[2 * s] = static_cast<double>(__uint_as_float(x[s] << 16)) +
-                               static_cast<double>(__uint_as_float(y[s] << 16));
-                    v[2 * s + 1] = static_cast<double>(__uint_as_float(x[s] & 0xffff0000u)) +
-                                   static_cast<double>(__uint_as_float(y[s] & 0xffff0000u));
-                }
+            for (int s = 0; s < 4; ++s) {
+                v[s] = x[s];
+                v[4 + s] = y[s];
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int64_t at = (k + 4 * s + kq) * it.cp + r0 + lr;
-                if constexpr (FP32U)
-                    v[s] = f[at];
-                else
-                    v[s] = static_cast<double>(__uint_as_float(static_cast<unsigned int>(hi[at]) << 16)) +
-                           static_cast<double>(__uint_as_float(static_cast<unsigned int>(lo[at]) << 16));
-            }
+            for (int s = 0; s < 8; ++s)
+                v[s] = f[(k + 4 * s + kq) * it.cp + r0 + lr];
         }
     };
-    for (int64_t k = k0; k < k1; k += 32) {
-        double a[2][8], b[2][8];
+    // (the next 32 values on their way)
+    float a[2][2][8], b[2][2][8];
+    auto fetch = [&](int to, int64_t k) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            operand(a[q], i0 + 16 * q, k);
-            operand(b[q], j0 + 16 * q, k);
+            operand(a[to][q], i0 + 16 * q, k);
+            operand(b[to][q], j0 + 16 * q, k);
         }
+    };
+    fetch(0, k0);
+    for (int64_t k = k0; k < k1; k += 64) {  // (whole 128s)
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int half = 0; half < 2; ++half) {
+            const int64_t next = k + 32 * half + 32;
+            fetch(half ^ 1, next < k1 ? next : k0);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int s = 0; s < 8; ++s)
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[x][s], b[y][s], acc[x][y], 0, 0, 0);
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(
+                            static_cast<double>(a[half][x][s]), static_cast<double>(b[half][y][s]),
+                            acc[x][y], 0, 0, 0);
+        }
     }
-    double *const out = it.part + static_cast<int64_t>(z) * it.np * it.np;
+    double *const out = static_cast<double *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -236,74 +267,325 @@ __global__ void __launch_bounds__(THREADS) ns_gram_kernel(NsGroup g)
                     acc[x][y][q];
 }
 
+// LDS tiles of one plane: 64 K values of R rows of the shorter side, as rows of K values 144 bytes
+// apart (16 of them at one chunk on distinct banks), or, where the matrix lies the other way,
+// as 64 rows of R values (four rows of 32 bytes on distinct banks), read by transposing loads.
+template <int R>
+struct Tiles {
+    static constexpr int KP = 144, MP = R == 128 ? 288 : 160;
+    static constexpr int K_BYTES = R * KP, M_BYTES = 64 * MP;
+    // operands of 32 K values (h: the first or the second half of the stage) of 16 rows from r0
+    __device__ __forceinline__ static bf16x8_t rows16(const unsigned char *tile, int r0, int h, int lane)
+    {
+        return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(
+                                                tile + (r0 + (lane & 15)) * KP + 64 * h + 16 * (lane >> 4)));
+    }
+    __device__ __forceinline__ static bf16x8_t columns16(const unsigned char *tile, int c0, int h, int lane)
+    {
+        const int lr = lane & 15, kq = lane >> 4;
+        const unsigned char *const p =
+            tile + (32 * h + 8 * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
+        const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
+        const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * MP));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// bf16 matrices: both planes of both operands, all four products, in fp32 over a share of L (the
+// shares are added in 64 bits).  NB x NB tiles on and below the diagonal, eight waves (4 x 2),
+// 64 values of L a stage, the next one on its way.
+constexpr int WAVES8 = 512;
+template <bool TALL, int NB>
+__global__ void __launch_bounds__(WAVES8) ns_gram_kernel(NsGroup g)
+{
+    using Tl = Tiles<NB>;
+    constexpr int BYTES = TALL ? Tl::M_BYTES : Tl::K_BYTES;
+    constexpr int TM = NB / 64, TN = NB / 32;       // 16 x 16 blocks of a wave
+    constexpr int V = NB * 8 / WAVES8;              // 16-byte chunks of a plane a thread
+    __shared__ __align__(16) unsigned char sa[2][BYTES], sb[2][BYTES];
+    __shared__ unsigned int red[WAVES8 / 64];
+    const int item = find_item(g, blockIdx.x);
+    const NsItem &it = g.it[item];
+    const int nt = it.np / NB, tiles = nt * (nt + 1) / 2;
+    const int block = static_cast<int>(blockIdx.x) - g.start[item];
+    const int z = block / tiles;
+    int t = block % tiles, ti = 0;
+    while (t > ti) {
+        t -= ti + 1;
+        ++ti;
+    }
+    const int i0 = ti * NB, j0 = t * NB;
+    const bool diagonal = i0 == j0;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t k0 = z * it.per_split, k1 = k0 + it.per_split < it.lp ? k0 + it.per_split : it.lp;
+    const int64_t usize = it.rp * it.cp;
+    const float scale = range_scale(it, red);
+
+    u32x4_t ra[V][2], rb[V][2];
+    auto fetch = [&](u32x4_t (&r)[V][2], int r0, int64_t k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = tid + i * WAVES8;
+            const int64_t at = TALL ? (k + v / (NB / 8)) * it.cp + r0 + v % (NB / 8) * 8
+                                    : (r0 + v / 8) * it.cp + k + v % 8 * 8;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                r[i][p] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const uint16_t *>(it.u) +
+                                                             p * usize + at);
+        }
+    };
+    auto keep = [&](const u32x4_t (&r)[V][2], unsigned char (&to)[2][BYTES]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = tid + i * WAVES8;
+            const int at = TALL ? v / (NB / 8) * Tl::MP + v % (NB / 8) * 16 : v / 8 * Tl::KP + v % 8 * 16;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                u32x4_t w = r[i][p];
+                if (scale != 1.f) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        w[q] = pack_bf16x2(scale * __uint_as_float(w[q] << 16),
+                                           scale * __uint_as_float(w[q] & 0xffff0000u));
+                }
+                *reinterpret_cast<u32x4_t *>(&to[p][at]) = w;
+            }
+        }
+    };
+    f32x4_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto operand = [&](const unsigned char *tile, int r0, int h) {
+        if constexpr (TALL)
+            return Tl::columns16(tile, r0, h, lane);
+        else
+            return Tl::rows16(tile, r0, h, lane);
+    };
+    unsigned char(*const other)[BYTES] = diagonal ? sa : sb;
+    fetch(ra, i0, k0);
+    if (!diagonal)
+        fetch(rb, j0, k0);
+    for (int64_t k = k0; k < k1; k += 64) {
+        __syncthreads();
+        keep(ra, sa);
+        if (!diagonal)
+            keep(rb, sb);
+        __syncthreads();
+        if (k + 64 < k1) {
+            fetch(ra, i0, k + 64);
+            if (!diagonal)
+                fetch(rb, j0, k + 64);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8_t a[TM][2], b[TN][2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    a[i][p] = operand(sa[p], wm * (NB / 4) + 16 * i, h);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    b[j][p] = operand(other[p], wn * (NB / 2) + 16 * j, h);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int s = 3; s >= 0; --s)  // the small products first
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][s & 1], a[i][s >> 1],
+                                                                            acc[i][j], 0, 0, 0);
+        }
+    }
+    // a lane holds row lr and four consecutive columns of each block
+    float *const out = static_cast<float *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            *reinterpret_cast<f32x4_t *>(
+                out + static_cast<int64_t>(i0 + wm * (NB / 4) + 16 * i + (lane & 15)) * it.np + j0 +
+                wn * (NB / 2) + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+}
+
+// The sum of the Gram partials at place e, and what a range scale took from it.
+template <bool F32>
+__device__ __forceinline__ double gram_at(const NsItem &it, int64_t size, int64_t e, double back)
+{
+    double s = 0.;
+    if constexpr (F32) {
+        const double *const p = static_cast<const double *>(it.part);
+#pragma unroll 8
+        for (int z = 0; z < it.splits; ++z)
+            s += p[z * size + e];
+    } else {
+        const float *const p = static_cast<const float *>(it.part);
+#pragma unroll 8
+        for (int z = 0; z < it.splits; ++z)
+            s += static_cast<double>(p[z * size + e]);
+    }
+    return s * back;
+}
+
 // ------------------------------------------------------- the n x n part, n <= 64
-// One workgroup a matrix: everything in LDS, a wave for each 16 x 16 tile.
+// One workgroup a matrix, everything in LDS: bound by one CU's 64-bit matrix rate, so that only
+// tiles on and below the diagonal are formed (16 x 16, as many as n has), and a single product's
+// waves split K in two, which balances them over the SIMDs.
 constexpr int SP = SMALL + 4;  // pitch
 template <int PLANES>
 __global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup g)
 {
+    constexpr bool F32 = PLANES == 3;
+    constexpr int UNITS = 20;  // tiles of two products, or of one by half its K
     __shared__ double m[4][SMALL][SP];
+    __shared__ double half[10][16][17];
+    __shared__ unsigned int red[16];
     double(*G)[SP] = m[0], (*P)[SP] = m[1], (*Q)[SP] = m[2], (*H)[SP] = m[3];
     const NsItem &it = g.it[blockIdx.x];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    const int lr = lane & 15, kq = lane >> 4, i0 = 16 * (wave >> 2), j0 = 16 * (wave & 3);
-    for (int e = tid; e < SMALL * SMALL; e += 1024) {
-        double s = 0.;
-#pragma unroll 8
-        for (int z = 0; z < it.splits; ++z)
-            s += it.part[z * SMALL * SMALL + e];
-        G[e / SMALL][e % SMALL] = s;
+    const int lr = lane & 15, kq = lane >> 4;
+    const int n = static_cast<int>(it.tall ? it.m.cols : it.m.rows);
+    const int nt = (n + 15) / 16, tiles = nt * (nt + 1) / 2, K = 16 * nt;
+    double back = 1.;
+    if constexpr (!F32) {
+        const double scale = range_scale(it, red);
+        back = 1. / (scale * scale);
+    }
+    {
+        double v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = gram_at<F32>(it, SMALL * SMALL, tid + i * 1024, back);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            G[(tid + i * 1024) / SMALL][tid % SMALL] = v[i];
     }
     __syncthreads();
     double trace = 0.;
-    for (int i = 0; i < SMALL; ++i)
+    for (int i = 0; i < K; ++i)
         trace += G[i][i];
     const double inv = 1. / (sqrt(trace) + static_cast<double>(g.p.eps));
     __syncthreads();
-    for (int e = tid; e < SMALL * SMALL; e += 1024) {
-        G[e / SMALL][e % SMALL] *= inv * inv;
-        Q[e / SMALL][e % SMALL] = e / SMALL == e % SMALL ? 1. : 0.;
-    }
-    __syncthreads();
-    // rows i0.. of X against rows j0.. of Y (symmetric)
-    auto product = [&](double(*X)[SP], double(*Y)[SP]) {
-        f64x4_t acc = {0., 0., 0., 0.};
 #pragma unroll
-        for (int s = 0; s < SMALL / 4; ++s)
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64(X[i0 + lr][4 * s + kq], Y[j0 + lr][4 * s + kq], acc,
-                                                       0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+        G[(tid + i * 1024) / SMALL][tid % SMALL] *= inv * inv;
+    __syncthreads();
+    auto tile_of = [](int t, int &i0, int &j0) {
+        int ti = 0;
+        while (t > ti) {
+            t -= ti + 1;
+            ++ti;
+        }
+        i0 = 16 * ti;
+        j0 = 16 * t;
+    };
+    // rows i0.. of X against rows j0.. of Y (symmetric), K values from k0 to k1
+    auto product = [&](double(*X)[SP], double(*Y)[SP], int i0, int j0, int k0, int k1) {
+        f64x4_t acc = {0., 0., 0., 0.};
+        for (int k = k0; k < k1; k += 8) {
+#pragma unroll
+            for (int s = 0; s < 8; s += 4)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(X[i0 + lr][k + s + kq], Y[j0 + lr][k + s + kq],
+                                                           acc, 0, 0, 0);
+        }
         return acc;
     };
-    auto row = [&](int q) { return i0 + 4 * q + kq; };
-    const int col = j0 + lr;
-    for (int step = 0; step < g.p.steps; ++step) {
-        const f64x4_t g2 = product(G, G);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            P[row(q)][col] = (row(q) == col ? static_cast<double>(g.p.a) : 0.) +
-                             static_cast<double>(g.p.b) * G[row(q)][col] +
-                             static_cast<double>(g.p.c) * g2[q];
-        __syncthreads();
-        const f64x4_t h = product(P, G), nq = product(P, Q);
-        __syncthreads();
+    auto place = [&](double(*Z)[SP], int i0, int j0, const f64x4_t &v) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            H[row(q)][col] = h[q];
-            Q[row(q)][col] = nq[q];
+            const int i = i0 + 4 * q + kq, j = j0 + lr;
+            if (j <= i) {
+                Z[i][j] = v[q];
+                Z[j][i] = v[q];
+            }
+        }
+    };
+    // (a wave takes units wave and wave + 16)
+    auto one = [&](double(*X)[SP], double(*Y)[SP], double(*Z)[SP], bool poly) {
+        f64x4_t acc[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int u = wave + 16 * r;
+            int i0, j0;
+            tile_of(u < tiles ? u : u - tiles, i0, j0);
+            if (u < 2 * tiles)
+                acc[r] = product(X, Y, i0, j0, u < tiles ? 0 : K / 2, u < tiles ? K / 2 : K);
+            if (u >= tiles && u < 2 * tiles)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    half[u - tiles][4 * q + kq][lr] = acc[r][q];
         }
         __syncthreads();
-        const f64x4_t ng = product(H, P);
+        if (wave < tiles) {
+            int i0, j0;
+            tile_of(wave, i0, j0);
+            f64x4_t v;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            G[row(q)][col] = ng[q];
+            for (int q = 0; q < 4; ++q) {
+                v[q] = acc[0][q] + half[wave][4 * q + kq][lr];
+                if (poly) {
+                    const int i = i0 + 4 * q + kq, j = j0 + lr;
+                    v[q] = (i == j ? static_cast<double>(g.p.a) : 0.) +
+                           static_cast<double>(g.p.b) * X[i][j] + static_cast<double>(g.p.c) * v[q];
+                }
+            }
+            place(Z, i0, j0, v);
+        }
         __syncthreads();
+    };
+    auto copy = [&](double(*from)[SP], double(*to)[SP]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            to[(tid + i * 1024) / SMALL][tid % SMALL] = from[(tid + i * 1024) / SMALL][tid % SMALL];
+        __syncthreads();
+    };
+    for (int step = 0; step < g.p.steps; ++step) {
+        const bool first = step == 0, last = step + 1 == g.p.steps;
+        one(G, G, P, true);
+        if (first) {
+            copy(P, Q);
+            if (!last)
+                one(P, G, H, false);
+        } else if (last) {
+            one(P, Q, H, false);
+            copy(H, Q);
+        } else {
+            // H = P G and Q = P Q at once
+            f64x4_t acc[2];
+            static_assert(UNITS <= 32, "two units a wave");
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int u = wave + 16 * r;
+                int i0, j0;
+                tile_of(u < tiles ? u : u - tiles, i0, j0);
+                if (u < 2 * tiles)
+                    acc[r] = product(P, u < tiles ? G : Q, i0, j0, 0, K);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int u = wave + 16 * r;
+                int i0, j0;
+                tile_of(u < tiles ? u : u - tiles, i0, j0);
+                if (u < 2 * tiles)
+                    place(u < tiles ? H : Q, i0, j0, acc[r]);
+            }
+            __syncthreads();
+        }
+        if (!last)
+            one(H, P, G, false);
     }
     if (tid < SMALL * SMALL / 8) {
         const int i = tid / (SMALL / 8), j = tid % (SMALL / 8) * 8;
         float v[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            v[q] = static_cast<float>(Q[i][j + q] * inv);
+        for (int q = 0; q < 8; ++q)  // (zeros past n's tiles: U is zero there, too)
+            v[q] = i < K && j + q < K ? static_cast<float>(Q[i][j + q] * inv) : 0.f;
         u32x4_t w[PLANES];
         split_planes(v, w);
 #pragma unroll
@@ -313,19 +595,23 @@ __global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup g)
 }
 
 // ------------------------------------------------------- the n x n part, larger
+template <bool F32>
 __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup g)
 {
+    __shared__ unsigned int red[THREADS / 64];
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
     const int64_t size = static_cast<int64_t>(it.np) * it.np;
+    double back = 1.;
+    if constexpr (!F32) {
+        const double scale = range_scale(it, red);
+        back = 1. / (scale * scale);
+    }
     const int64_t e = (static_cast<int64_t>(blockIdx.x) - g.start[item]) * THREADS + threadIdx.x;
     const int i = static_cast<int>(e / it.np), j = static_cast<int>(e % it.np);
     if (i >= it.np || j > i)
         return;
-    double s = 0.;
-#pragma unroll 8
-    for (int z = 0; z < it.splits; ++z)
-        s += it.part[z * size + e];
+    const double s = gram_at<F32>(it, size, e, back);
     it.mat[e] = s;
     it.mat[static_cast<int64_t>(j) * it.np + i] = s;
 }
@@ -342,12 +628,12 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
     const int np = it.np, nt = np / POLY, tiles = nt * (nt + 1) / 2;
-    int t = static_cast<int>(blockIdx.x) - g.start[item];
-    const bool second = t >= tiles;  // Q's tiles behind H's
-    t -= second ? tiles : 0;
+    int tj = static_cast<int>(blockIdx.x) - g.start[item];
+    const bool second = tj >= tiles;  // Q's tiles behind H's
+    tj -= second ? tiles : 0;
     int ti = 0;
-    while (t > ti) {
-        t -= ti + 1;
+    while (tj > ti) {
+        tj -= ti + 1;
         ++ti;
     }
     const int64_t size = static_cast<int64_t>(np) * np;
@@ -373,7 +659,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
         out = Q2;
     }
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    const int lr = lane & 15, kq = lane >> 4, i0 = ti * POLY, j0 = t * POLY;
+    const int lr = lane & 15, kq = lane >> 4, i0 = ti * POLY, j0 = tj * POLY;
 
     // the first G's scale
     double inv = 1.;
@@ -403,23 +689,35 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
 #pragma unroll
         for (int y = 0; y < 2; ++y)
             acc[x][y] = f64x4_t{0., 0., 0., 0.};
-    // 16 values of K a turn, four consecutive ones a lane
-    for (int k = 16 * wave; k < np; k += 16 * POLY_WAVES) {
-        f64x4_t a[2], b[2];
+    // 16 values of K a turn (np is whole turns of the waves), four consecutive ones a lane; three
+    // turns' loads at once: another CU wrote them, and each wait is one for its cache
+    constexpr int TURN = 16 * POLY_WAVES, AHEAD = 3;
+    for (int k0 = 16 * wave; k0 < np; k0 += AHEAD * TURN) {
+        f64x4_t a[AHEAD][2], b[AHEAD][2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            a[q] = *reinterpret_cast<const f64x4_t *>(
-                X + static_cast<int64_t>(i0 + 16 * q + lr) * np + k + 4 * kq);
-            b[q] = *reinterpret_cast<const f64x4_t *>(
-                Y + static_cast<int64_t>(j0 + 16 * q + lr) * np + k + 4 * kq);
+        for (int t = 0; t < AHEAD; ++t) {
+            const int k = k0 + t * TURN < np ? k0 + t * TURN : k0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                a[t][q] = *reinterpret_cast<const f64x4_t *>(
+                    X + static_cast<int64_t>(i0 + 16 * q + lr) * np + k + 4 * kq);
+                b[t][q] = *reinterpret_cast<const f64x4_t *>(
+                    Y + static_cast<int64_t>(j0 + 16 * q + lr) * np + k + 4 * kq);
+            }
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int t = 0; t < AHEAD; ++t) {
+            if (k0 + t * TURN >= np)
+                break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[x][s], b[y][s], acc[x][y], 0, 0, 0);
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[t][x][s], b[t][y][s],
+                                                                         acc[x][y], 0, 0, 0);
+        }
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -481,18 +779,18 @@ __global__ void __launch_bounds__(THREADS) ns_q_planes_kernel(NsGroup g)
 }
 
 // ------------------------------------------------------------- O = Q U (or U Q)
-// Tiles of NB values of the shorter side by 128 of the longer one, four waves (2 x 2), 64 values
-// of K a stage.  LDS rows of 64 K values (Q, and U where it is tall) are 144 bytes apart, 16 of
-// them at one chunk on distinct banks; U of a wide matrix lies as [64 K][128 columns],
-// 288 bytes apart (four rows of 32 bytes on distinct banks), and is read by transposing loads.
+// Tiles of NB values of the shorter side by 128 of the longer one, eight waves (4 x 2), 64 values
+// of K (the shorter side) a stage, the next one on its way.
 template <typename T, bool TALL, int NB>
-__global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
+__global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
 {
     constexpr int P = sizeof(T) == 2 ? 2 : 3;
     constexpr int BM = TALL ? 128 : NB, BN = TALL ? NB : 128;
-    constexpr int KP = 144, MP = 288;
-    constexpr int Q_ROWS = NB, Q_BYTES = Q_ROWS * KP, U_BYTES = TALL ? 128 * KP : 64 * MP;
-    constexpr int TM = BM / 32, TN = BN / 32;  // 16 x 16 blocks of a wave
+    using Tq = Tiles<NB>;
+    using Tu = Tiles<128>;
+    constexpr int KP = Tu::KP, MP = Tu::MP;
+    constexpr int Q_ROWS = NB, Q_BYTES = Tq::K_BYTES, U_BYTES = TALL ? Tu::K_BYTES : Tu::M_BYTES;
+    constexpr int TM = BM / 64, TN = BN / 32;  // 16 x 16 blocks of a wave
     __shared__ __align__(16) unsigned char qs[P][Q_BYTES], us[P][U_BYTES];
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
@@ -506,7 +804,7 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
     const int np = it.np;
     const int64_t qsize = static_cast<int64_t>(np) * np, usize = it.rp * it.cp;
 
-    constexpr int QV = Q_ROWS * 8 / THREADS, UV = 128 * 8 / THREADS;  // 16-byte chunks a thread
+    constexpr int QV = Q_ROWS * 8 / WAVES8, UV = 128 * 8 / WAVES8;  // 16-byte chunks a thread
     u32x4_t qr[QV][P];
     Raw8<float> uf[UV];
     u32x4_t up[UV][2];
@@ -519,7 +817,7 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
     auto fetch = [&](int k) {
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
-            const int v = tid + i * THREADS;
+            const int v = tid + i * WAVES8;
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 qr[i][p] = *reinterpret_cast<const u32x4_t *>(
@@ -527,7 +825,7 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
         }
 #pragma unroll
         for (int i = 0; i < UV; ++i) {
-            const int64_t at = u_at(tid + i * THREADS, k);
+            const int64_t at = u_at(tid + i * WAVES8, k);
             if constexpr (P == 3) {
                 uf[i].template load<true>(reinterpret_cast<const float *>(it.u) + at, 8);
             } else {
@@ -541,14 +839,14 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
     auto keep = [&]() {
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
-            const int v = tid + i * THREADS;
+            const int v = tid + i * WAVES8;
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 *reinterpret_cast<u32x4_t *>(&qs[p][v / 8 * KP + v % 8 * 16]) = qr[i][p];
         }
 #pragma unroll
         for (int i = 0; i < UV; ++i) {
-            const int v = tid + i * THREADS;
+            const int v = tid + i * WAVES8;
             u32x4_t w[P];
             if constexpr (P == 3) {
                 float f[8];
@@ -564,19 +862,6 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
                     &us[p][TALL ? v / 8 * KP + v % 8 * 16 : v / 16 * MP + v % 16 * 16]) = w[p];
         }
     };
-    // operands of 32 K values (h: the first or the second half of the stage)
-    auto rows16 = [&](const unsigned char *tile, int r0, int h) {
-        return __builtin_bit_cast(
-            bf16x8_t, *reinterpret_cast<const u32x4_t *>(tile + (r0 + lr) * KP + 64 * h + 16 * kq));
-    };
-    auto columns16 = [&](const unsigned char *tile, int c0, int h) {
-        const unsigned char *const p0 =
-            tile + (32 * h + 8 * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
-        const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p0));
-        const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p0 + 4 * MP));
-        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-
     f32x4_t acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -597,12 +882,12 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
             for (int p = 0; p < P; ++p) {
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    a[i][p] = TALL ? rows16(us[p], wm * (BM / 2) + 16 * i, h)
-                                   : rows16(qs[p], wm * (BM / 2) + 16 * i, h);
+                    a[i][p] = TALL ? Tu::rows16(us[p], wm * (BM / 4) + 16 * i, h, lane)
+                                   : Tq::rows16(qs[p], wm * (BM / 4) + 16 * i, h, lane);
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    b[j][p] = TALL ? rows16(qs[p], wn * (BN / 2) + 16 * j, h)
-                                   : columns16(us[p], wn * (BN / 2) + 16 * j, h);
+                    b[j][p] = TALL ? Tq::rows16(qs[p], wn * (BN / 2) + 16 * j, h, lane)
+                                   : Tu::columns16(us[p], wn * (BN / 2) + 16 * j, h, lane);
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i)
@@ -617,7 +902,7 @@ __global__ void __launch_bounds__(THREADS) ns_final_kernel(NsGroup g)
         }
     }
     // a lane holds row lr and four consecutive columns of each block
-    const int64_t m0 = (TALL ? l0 : n0) + wm * (BM / 2), c0 = (TALL ? n0 : l0) + wn * (BN / 2);
+    const int64_t m0 = (TALL ? l0 : n0) + wm * (BM / 4), c0 = (TALL ? n0 : l0) + wn * (BN / 2);
     const bool aligned = it.m.cols % 4 == 0;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -713,6 +998,12 @@ struct Chunk {
 };
 constexpr size_t CHUNK_BYTES = size_t(256) << 20;
 
+int64_t gram_tile(int bf16, int64_t np) { return bf16 && np > SMALL ? 128 : 64; }
+int64_t prepare_groups(int64_t rp, int64_t cp)
+{
+    return (rp * cp / 8 + THREADS * PREP_VPT - 1) / (THREADS * PREP_VPT);
+}
+
 Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
 {
     Chunk c;
@@ -727,9 +1018,10 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         it.rp = s.rp;
         it.cp = s.cp;
         it.lp = s.lp;
-        const int64_t nt = s.np / TILE, tiles = nt * (nt + 1) / 2;
-        // about 1024 workgroups for the Gram products of the set, of 128 values of L at least
-        int64_t z = 1024 / (tiles * share);
+        // about 512 workgroups for the Gram products of the set (1024 in 64 bits, of four
+        // waves), of 128 values of L each at least
+        const int64_t nt = s.np / gram_tile(bf16, s.np), tiles = nt * (nt + 1) / 2;
+        int64_t z = (bf16 ? 512 : 1024) / (tiles * share);
         z = z < 1 ? 1 : z > 32 ? 32 : z;
         it.per_split = up_to((s.lp + z - 1) / z, 128);
         it.splits = static_cast<int>((s.lp + it.per_split - 1) / it.per_split);
@@ -740,7 +1032,9 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         };
         const size_t square = static_cast<size_t>(s.np) * s.np;
         it.u = take(static_cast<size_t>(s.rp) * s.cp * 4);
-        it.part = reinterpret_cast<double *>(take(it.splits * square * 8));
+        it.top_count = bf16 ? static_cast<int>(prepare_groups(s.rp, s.cp)) : 0;
+        it.tops = reinterpret_cast<unsigned int *>(take(it.top_count * sizeof(unsigned int)));
+        it.part = take(it.splits * square * (bf16 ? 4 : 8));
         it.mat = reinterpret_cast<double *>(take(s.np > SMALL ? 6 * square * 8 : 0));
         it.scal = reinterpret_cast<double *>(take(8));
         it.q = reinterpret_cast<uint16_t *>(take((bf16 ? 2 : 3) * square * 2));
@@ -797,14 +1091,32 @@ hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
         if (e_ != hipSuccess)                  \
             return e_;                         \
     } while (0)
-    int n = group_of(g, c, all, [](const NsItem &i) {
-        return (i.rp * i.cp / 8 + THREADS * PREP_VPT - 1) / (THREADS * PREP_VPT);
-    });
+    int n = group_of(g, c, all, [](const NsItem &i) { return prepare_groups(i.rp, i.cp); });
     NS_LAUNCH((ns_prepare_kernel<T>), dim3(n), dim3(THREADS), 0, st, g);
-    n = group_of(g, c, all, [](const NsItem &i) {
-        return static_cast<int64_t>(i.np / TILE) * (i.np / TILE + 1) / 2 * i.splits;
-    });
-    NS_LAUNCH((ns_gram_kernel<F32>), dim3(n), dim3(THREADS), 0, st, g);
+    auto gram_groups = [](const NsItem &i) {
+        const int64_t nt = i.np / gram_tile(!F32, i.np);
+        return nt * (nt + 1) / 2 * i.splits;
+    };
+    if constexpr (F32) {
+        n = group_of(g, c, all, gram_groups);
+        NS_LAUNCH(ns_gram_f64_kernel, dim3(n), dim3(THREADS), 0, st, g);
+    } else {
+        for (int kind = 0; kind < 4; ++kind) {
+            const bool tall = kind & 1, big = kind & 2;
+            n = group_of(g, c, [&](const NsItem &i) { return (i.tall != 0) == tall && (i.np > SMALL) == big; },
+                         gram_groups);
+            if (n == 0)
+                continue;
+            if (tall && big)
+                NS_LAUNCH((ns_gram_kernel<true, 128>), dim3(n), dim3(WAVES8), 0, st, g);
+            else if (tall)
+                NS_LAUNCH((ns_gram_kernel<true, 64>), dim3(n), dim3(WAVES8), 0, st, g);
+            else if (big)
+                NS_LAUNCH((ns_gram_kernel<false, 128>), dim3(n), dim3(WAVES8), 0, st, g);
+            else
+                NS_LAUNCH((ns_gram_kernel<false, 64>), dim3(n), dim3(WAVES8), 0, st, g);
+        }
+    }
     n = group_of(g, c, small, [](const NsItem &) { return 1; });
     if (n > 0)
         NS_LAUNCH((ns_small_kernel<PLANES>), dim3(n), dim3(1024), 0, st, g);
@@ -812,7 +1124,7 @@ hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
         return (static_cast<int64_t>(i.np) * i.np + THREADS - 1) / THREADS;
     });
     if (n > 0) {
-        NS_LAUNCH(ns_gram_sum_kernel, dim3(n), dim3(THREADS), 0, st, g);
+        NS_LAUNCH((ns_gram_sum_kernel<F32>), dim3(n), dim3(THREADS), 0, st, g);
         auto tiles = [](const NsItem &i) {
             return static_cast<int64_t>(i.np / POLY) * (i.np / POLY + 1) / 2;
         };
@@ -848,13 +1160,13 @@ hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
             if (n == 0)
                 continue;
             if (tall && wide_n)
-                NS_LAUNCH((ns_final_kernel<T, true, 128>), dim3(n), dim3(THREADS), 0, st, g);
+                NS_LAUNCH((ns_final_kernel<T, true, 128>), dim3(n), dim3(WAVES8), 0, st, g);
             else if (tall)
-                NS_LAUNCH((ns_final_kernel<T, true, 64>), dim3(n), dim3(THREADS), 0, st, g);
+                NS_LAUNCH((ns_final_kernel<T, true, 64>), dim3(n), dim3(WAVES8), 0, st, g);
             else if (wide_n)
-                NS_LAUNCH((ns_final_kernel<T, false, 128>), dim3(n), dim3(THREADS), 0, st, g);
+                NS_LAUNCH((ns_final_kernel<T, false, 128>), dim3(n), dim3(WAVES8), 0, st, g);
             else
-                NS_LAUNCH((ns_final_kernel<T, false, 64>), dim3(n), dim3(THREADS), 0, st, g);
+                NS_LAUNCH((ns_final_kernel<T, false, 64>), dim3(n), dim3(WAVES8), 0, st, g);
         }
 #undef NS_LAUNCH
     return hipSuccess;
