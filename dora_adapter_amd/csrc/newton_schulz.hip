@@ -8,16 +8,18 @@
 // between one product along L, G = U U^T, and another, O = Q U / (|U|_F + eps), whose epilogue is
 // the update: 4 n^2 L flops instead of 4 n^2 L a step, and U is read twice.
 //
-// The n x n part is in 64 bits: G holds squares of singular values, so that an error of 2^-24 of
-// its largest one would move the small ones' directions by 2^-24 / (2 sigma^2), where the
-// literal steps in fp32 move them by about 2^-24 / sigma; with 2^-53 the fp32 product at
-// the end is all that is left (measured against 64 bits: as far off as the literal steps).
-// That product takes its operands as two bf16 numbers each (three for fp32 matrices), which
-// hold 16 (24) bits, on the bf16 matrix cores with fp32 sums; so does G of bf16 matrices, whose
-// output's 8 bits leave room for that (about 1e-4 of its norm), while G of fp32 matrices is formed
-// in 64 bits.
+// G holds squares of singular values, so that an error of 2^-24 of its largest one would move the
+// small ones' directions by 2^-24 / (2 sigma^2), where the literal steps in fp32 move them by
+// about 2^-24 / sigma.  So the n x n part of fp32 matrices is in 64 bits, and the fp32 product at
+// the end is all that is left (measured against 64 bits: as far off as the literal steps); it
+// takes its operands as three bf16 numbers each, which hold 24 bits, on the bf16 matrix cores
+// with fp32 sums.  bf16 matrices, whose output's 8 bits leave room for 1e-4 of its norm, take two
+// numbers (16 bits) there and for G, and have their n x n part in fp32.
 //
-// Up to 16 matrices share each launch.
+// Up to 40 matrices share each launch.
+#include <climits>
+#include <type_traits>
+
 #include "around.hpp"
 #include "rows8.hpp"
 
@@ -38,37 +40,85 @@ constexpr int SMALL = 64;      // n x n matrices of one workgroup's LDS
 constexpr int POLY = 32;       // tile of the n x n products
 constexpr int POLY_WAVES = 8;  // which split their K
 
+// A matrix as its kernels see it.  The n x n part of bf16 matrices is formed in fp32, theirs of
+// fp32 matrices in fp64: `part` and `mat` are of that type.
 struct NsItem {
-    NsMatrix m;
-    int tall, np;        // rows > cols; the shorter side padded to 64 or to 128s
-    int64_t rp, cp, lp;  // rows, columns and the longer side as padded (128s)
     char *u;             // U padded with zeros, [rp, cp]: bf16 hi and lo, or fp32
     unsigned int *tops;  // bf16: the largest |U| of each workgroup that wrote it, as bits
-    int top_count;
-    void *part;          // Gram partials [splits, np, np], tiles on and below the diagonal:
-                         // fp32 (bf16 matrices) or fp64
-    double *mat;         // G, P, Q, H [np, np] (larger matrices)
-    double *scal;        // 1 / (|U|_F + eps)
+    char *part;          // Gram partials [splits, np, np], tiles on and below the diagonal
+    char *mat;           // G, P, Q, H and the other G and Q [np, np] (larger matrices)
+    double *scal;        // 1 / (|U|_F + eps), and what makes the first G of U U^T
     uint16_t *q;         // planes of Q / (|U|_F + eps), [planes, np, np]
-    int splits;
-    int64_t per_split;   // of L, a multiple of 128
+    int n, np;           // the shorter side, padded to 64 or to 128s
+    int tall;            // rows > cols
+    int rp, cp;          // rows and columns as padded (the longer side to 128s)
+    int top_count;
+    int splits, per_split;  // of the longer side, a multiple of 128
 };
-constexpr int MAX_ITEMS = 16;
+struct NsInput {  // what the prepare kernel reads and writes
+    char *u;
+    unsigned int *tops;
+    const void *g;
+    const float *m;
+    float *m_out;
+    int64_t rows, cols;
+    int rp, cp;
+};
+struct NsOutput {  // what the last kernel reads and writes
+    const char *u;
+    const uint16_t *q;
+    const void *p;
+    void *out;
+    int64_t rows, cols;
+    float step, keep;
+    int np, tall, rp, cp;
+};
+constexpr int MAX_ITEMS = 40;
+template <typename I>
 struct NsGroup {
-    NsItem it[MAX_ITEMS];
-    int start[MAX_ITEMS + 1];  // workgroups of the items before
-    int count;
+    I it[MAX_ITEMS];
+    int start[MAX_ITEMS];  // workgroups of the items before; behind the last item INT_MAX
     NsParams p;
 };
-static_assert(sizeof(NsGroup) <= 4032, "a group must fit the kernel argument space");
+static_assert(sizeof(NsGroup<NsItem>) <= 4000 && sizeof(NsGroup<NsInput>) <= 4000 &&
+                  sizeof(NsGroup<NsOutput>) <= 4000,
+              "a group must fit the kernel argument space");
 
-__device__ __forceinline__ int find_item(const NsGroup &g, int block)
+// (without a chain of dependent scalar loads)
+template <typename G>
+__device__ __forceinline__ int find_item(const G &g, int block)
 {
     int i = 0;
-    while (i + 1 < g.count && block >= g.start[i + 1])
-        ++i;
+#pragma unroll
+    for (int k = 1; k < MAX_ITEMS; ++k)
+        i += block >= g.start[k] ? 1 : 0;
     return i;
 }
+
+// A launch's workgroups go round the eight XCDs.  This gives each of them consecutive places, so
+// that the tiles that read the same stretch of U share an L2.
+__device__ __forceinline__ int place_on_xcd()
+{
+    const int n = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+    const int xcd = b & 7, each = n >> 3, more = n & 7;
+    return xcd * each + (xcd < more ? xcd : more) + (b >> 3);
+}
+
+template <bool F32>
+using Part = std::conditional_t<F32, double, float>;
+__device__ __forceinline__ f64x4_t mfma4(double a, double b, f64x4_t c)
+{
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+// the row of D's register q (its column is lane % 16)
+__device__ __forceinline__ int d_row(double, int q, int lane) { return 4 * q + (lane >> 4); }
+__device__ __forceinline__ int d_row(float, int q, int lane) { return 4 * (lane >> 4) + q; }
+template <typename R>
+using Quad = std::conditional_t<sizeof(R) == 8, f64x4_t, f32x4_t>;
 
 // v as P bf16 numbers whose sum it is (to 16 bits with two of them, 24 with three)
 template <int P>
@@ -96,14 +146,16 @@ __device__ __forceinline__ void split_planes(const float (&v)[8], u32x4_t (&w)[P
 // ------------------------------------------------------------- U and the momentum
 constexpr int PREP_VPT = 4;
 template <typename T>
-__global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
+__global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
 {
-    const NsItem &it = g.it[find_item(g, blockIdx.x)];
-    const unsigned int block = blockIdx.x - g.start[find_item(g, blockIdx.x)];
+    const int item = find_item(g, blockIdx.x);
+    const NsInput &it = g.it[item];
+    const unsigned int block = blockIdx.x - g.start[item];
     __shared__ unsigned int wave_top[THREADS / 64];
     unsigned int top = 0u;
     const unsigned int along = static_cast<unsigned int>(it.cp / 8);
-    const unsigned int total = static_cast<unsigned int>(it.rp * it.cp / 8);
+    const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
+    const unsigned int total = static_cast<unsigned int>(usize / 8);
 #pragma unroll
     for (int i = 0; i < PREP_VPT; ++i) {
         const unsigned int v = block * (THREADS * PREP_VPT) + i * THREADS + threadIdx.x;
@@ -114,15 +166,15 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
             u[q] = 0.f;
-        const int cnt = r < it.m.rows ? count8(it.m.cols, c) : 0;
+        const int cnt = r < it.rows ? count8(it.cols, c) : 0;
         if (cnt > 0) {
-            const int64_t at = r * it.m.cols + c;
+            const int64_t at = r * it.cols + c;
             Raw8<T> gr;
-            gr.load(static_cast<const T *>(it.m.g) + at, cnt);
+            gr.load(static_cast<const T *>(it.g) + at, cnt);
             gr.get(u);
-            if (it.m.m != nullptr) {
+            if (it.m != nullptr) {
                 Raw8<float> mr;
-                mr.load(it.m.m + at, cnt);
+                mr.load(it.m + at, cnt);
                 float m[8];
                 mr.get(m);
 #pragma unroll
@@ -131,7 +183,7 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
                     u[q] = g.p.nesterov ? __fmaf_rn(g.p.mu, m[q], u[q]) : m[q];
                 }
                 mr.set(m);
-                mr.store(it.m.m_out + at, cnt);
+                mr.store(it.m_out + at, cnt);
             }
         }
         const int64_t at = static_cast<int64_t>(v) * 8;
@@ -145,7 +197,7 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
             split_planes(u, w);
             uint16_t *const h = reinterpret_cast<uint16_t *>(it.u) + at;
             *reinterpret_cast<u32x4_t *>(h) = w[0];
-            *reinterpret_cast<u32x4_t *>(h + it.rp * it.cp) = w[1];
+            *reinterpret_cast<u32x4_t *>(h + usize) = w[1];
         } else {
             float *const o = reinterpret_cast<float *>(it.u) + at;
 #pragma unroll
@@ -167,18 +219,23 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup g)
     }
 }
 
-// The power of two that brings a bf16 matrix's largest |U| near one, where its squares (or theirs
-// of what is 2^-24 as large) would leave fp32's range; else 1.  Called by whole workgroups.
-__device__ __forceinline__ float range_scale(const NsItem &it, unsigned int *red)
+// The power of two that brings a bf16 matrix's largest |U| near one where fp32 might not hold its
+// Gram matrix, or the square of that, to the last bits that count; else 1.  `top`: the largest of
+// the thread's share (own_top).  Called by whole workgroups.
+__device__ __forceinline__ unsigned int own_top(const NsItem &it)
 {
     unsigned int top = 0u;
     for (int i = threadIdx.x; i < it.top_count; i += blockDim.x) {
         const unsigned int b = it.tops[i];
         top = top > b ? top : b;
     }
+    return top;
+}
+__device__ __forceinline__ float range_scale(unsigned int top, unsigned int *red)
+{
     top = block_max(top, red, static_cast<int>(blockDim.x) >> 6);
     const int e = static_cast<int>(top >> 23) - 127;
-    if (top == 0u || e == 128 || (e > -30 && e < 40))
+    if (top == 0u || e == 128 || (e > -24 && e < 9))
         return 1.f;
     // (2^-e; |e| is at most 127)
     return __uint_as_float(static_cast<unsigned int>(e == 127 ? 1 : 127 - e) << 23);
@@ -188,12 +245,12 @@ __device__ __forceinline__ float range_scale(const NsItem &it, unsigned int *red
 // fp32 matrices: 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L
 // at a time straight into registers.  An MFMA takes four of them: of a wide matrix a lane's
 // eight consecutive ones give it one each time, of a tall one they are four rows.
-__global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup g)
+__global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
 {
-    const int item = find_item(g, blockIdx.x);
+    const int place = place_on_xcd(), item = find_item(g, place);
     const NsItem &it = g.it[item];
     const int nt = it.np / TILE, tiles = nt * (nt + 1) / 2;
-    const int block = static_cast<int>(blockIdx.x) - g.start[item];
+    const int block = place - g.start[item];
     const int z = block / tiles;
     int t = block % tiles, ti = 0;
     while (t > ti) {
@@ -204,7 +261,8 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup g)
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
     const int lr = lane & 15, kq = lane >> 4;
     const int i0 = ti * TILE + 32 * (wave >> 1), j0 = tj * TILE + 32 * (wave & 1);
-    const int64_t k0 = z * it.per_split, k1 = k0 + it.per_split < it.lp ? k0 + it.per_split : it.lp;
+    const int64_t lp = it.tall ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
+                  k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
     const float *const f = reinterpret_cast<const float *>(it.u);
 
     f64x4_t acc[2][2];
@@ -216,7 +274,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup g)
     // the operand of 16 rows from r0: v[s] for MFMA step s of the 32 values from k
     auto operand = [&](float (&v)[8], int r0, int64_t k) {
         if (!it.tall) {
-            const int64_t at = (r0 + lr) * it.cp + k + 8 * kq;
+            const int64_t at = static_cast<int64_t>(r0 + lr) * it.cp + k + 8 * kq;
             const f32x4_t x = *reinterpret_cast<const f32x4_t *>(f + at),
                           y = *reinterpret_cast<const f32x4_t *>(f + at + 4);
 #pragma unroll
@@ -256,7 +314,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup g)
                             acc[x][y], 0, 0, 0);
         }
     }
-    double *const out = static_cast<double *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
+    double *const out = reinterpret_cast<double *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -294,20 +352,18 @@ struct Tiles {
 // bf16 matrices: both planes of both operands, all four products, in fp32 over a share of L (the
 // shares are added in 64 bits).  NB x NB tiles on and below the diagonal, eight waves (4 x 2),
 // 64 values of L a stage, the next one on its way.
-constexpr int WAVES8 = 512;
+constexpr int GRAM_WAVES = 8, FINAL_WAVES = 8;  // two in each row
+template <int NB>
+using GramTiles = unsigned char[2][Tiles<NB>::K_BYTES > Tiles<NB>::M_BYTES ? Tiles<NB>::K_BYTES
+                                                                            : Tiles<NB>::M_BYTES];
 template <bool TALL, int NB>
-__global__ void __launch_bounds__(WAVES8) ns_gram_kernel(NsGroup g)
+__device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, GramTiles<NB> &sa,
+                                               GramTiles<NB> &sb, unsigned int *red)
 {
     using Tl = Tiles<NB>;
-    constexpr int BYTES = TALL ? Tl::M_BYTES : Tl::K_BYTES;
-    constexpr int TM = NB / 64, TN = NB / 32;       // 16 x 16 blocks of a wave
-    constexpr int V = NB * 8 / WAVES8;              // 16-byte chunks of a plane a thread
-    __shared__ __align__(16) unsigned char sa[2][BYTES], sb[2][BYTES];
-    __shared__ unsigned int red[WAVES8 / 64];
-    const int item = find_item(g, blockIdx.x);
-    const NsItem &it = g.it[item];
+    constexpr int TM = NB / (8 * GRAM_WAVES), TN = NB / 32;       // 16 x 16 blocks of a wave
+    constexpr int V = NB * 8 / (64 * GRAM_WAVES);              // 16-byte chunks of a plane a thread
     const int nt = it.np / NB, tiles = nt * (nt + 1) / 2;
-    const int block = static_cast<int>(blockIdx.x) - g.start[item];
     const int z = block / tiles;
     int t = block % tiles, ti = 0;
     while (t > ti) {
@@ -318,27 +374,29 @@ __global__ void __launch_bounds__(WAVES8) ns_gram_kernel(NsGroup g)
     const bool diagonal = i0 == j0;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t k0 = z * it.per_split, k1 = k0 + it.per_split < it.lp ? k0 + it.per_split : it.lp;
-    const int64_t usize = it.rp * it.cp;
-    const float scale = range_scale(it, red);
+    const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
+                  k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
+    const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
+    const unsigned int top = own_top(it);
 
     u32x4_t ra[V][2], rb[V][2];
     auto fetch = [&](u32x4_t (&r)[V][2], int r0, int64_t k) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = tid + i * WAVES8;
+            const int v = tid + i * (64 * GRAM_WAVES);
             const int64_t at = TALL ? (k + v / (NB / 8)) * it.cp + r0 + v % (NB / 8) * 8
-                                    : (r0 + v / 8) * it.cp + k + v % 8 * 8;
+                                    : static_cast<int64_t>(r0 + v / 8) * it.cp + k + v % 8 * 8;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
                 r[i][p] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const uint16_t *>(it.u) +
                                                              p * usize + at);
         }
     };
-    auto keep = [&](const u32x4_t (&r)[V][2], unsigned char (&to)[2][BYTES]) {
+    float scale = 1.f;
+    auto keep = [&](const u32x4_t (&r)[V][2], GramTiles<NB> &to) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int v = tid + i * WAVES8;
+            const int v = tid + i * (64 * GRAM_WAVES);
             const int at = TALL ? v / (NB / 8) * Tl::MP + v % (NB / 8) * 16 : v / 8 * Tl::KP + v % 8 * 16;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -365,10 +423,11 @@ __global__ void __launch_bounds__(WAVES8) ns_gram_kernel(NsGroup g)
         else
             return Tl::rows16(tile, r0, h, lane);
     };
-    unsigned char(*const other)[BYTES] = diagonal ? sa : sb;
+    auto &other = diagonal ? sa : sb;
     fetch(ra, i0, k0);
     if (!diagonal)
         fetch(rb, j0, k0);
+    scale = range_scale(top, red);
     for (int64_t k = k0; k < k1; k += 64) {
         __syncthreads();
         keep(ra, sa);
@@ -382,249 +441,249 @@ __global__ void __launch_bounds__(WAVES8) ns_gram_kernel(NsGroup g)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            bf16x8_t a[TM][2], b[TN][2];
+            bf16x8_t a[TM][2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    a[i][p] = operand(sa[p], wm * (NB / 4) + 16 * i, h);
+                    a[i][p] = operand(sa[p], wm * (16 * TM) + 16 * i, h);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    b[j][p] = operand(other[p], wn * (NB / 2) + 16 * j, h);
-            }
+            for (int j = 0; j < TN; ++j) {
+                bf16x8_t b[2];
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int p = 0; p < 2; ++p)
+                    b[p] = operand(other[p], wn * (NB / 2) + 16 * j, h);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
                     for (int s = 3; s >= 0; --s)  // the small products first
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][s & 1], a[i][s >> 1],
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s & 1], a[i][s >> 1],
                                                                             acc[i][j], 0, 0, 0);
+            }
         }
     }
     // a lane holds row lr and four consecutive columns of each block
-    float *const out = static_cast<float *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
+    float *const out = reinterpret_cast<float *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j)
             *reinterpret_cast<f32x4_t *>(
-                out + static_cast<int64_t>(i0 + wm * (NB / 4) + 16 * i + (lane & 15)) * it.np + j0 +
+                out + static_cast<int64_t>(i0 + wm * (16 * TM) + 16 * i + (lane & 15)) * it.np + j0 +
                 wn * (NB / 2) + 16 * j + 4 * (lane >> 4)) = acc[i][j];
 }
 
-// The sum of the Gram partials at place e, and what a range scale took from it.
-template <bool F32>
-__device__ __forceinline__ double gram_at(const NsItem &it, int64_t size, int64_t e, double back)
+template <int NB>
+__global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kernel(NsGroup<NsItem> g)
 {
-    double s = 0.;
-    if constexpr (F32) {
-        const double *const p = static_cast<const double *>(it.part);
+    __shared__ __align__(16) GramTiles<NB> sa, sb;
+    __shared__ unsigned int red[GRAM_WAVES];
+    const int at = place_on_xcd(), item = find_item(g, at);
+    const NsItem &it = g.it[item];
+    const int block = at - g.start[item];
+    if (it.tall)
+        gram_tile_bf16<true, NB>(it, block, sa, sb, red);
+    else
+        gram_tile_bf16<false, NB>(it, block, sa, sb, red);
+}
+
+// The sums of the Gram partials at N places from e.
+template <bool F32, int N>
+__device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)[N])
+{
+    typedef Part<F32> vec_t __attribute__((ext_vector_type(N)));
+    const Part<F32> *const p = reinterpret_cast<const Part<F32> *>(it.part) + e;
+    const int64_t size = static_cast<int64_t>(it.np) * it.np;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        s[q] = 0.;
 #pragma unroll 8
-        for (int z = 0; z < it.splits; ++z)
-            s += p[z * size + e];
-    } else {
-        const float *const p = static_cast<const float *>(it.part);
-#pragma unroll 8
-        for (int z = 0; z < it.splits; ++z)
-            s += static_cast<double>(p[z * size + e]);
+    for (int z = 0; z < it.splits; ++z) {
+        const vec_t v = *reinterpret_cast<const vec_t *>(p + z * size);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            s[q] += static_cast<double>(v[q]);
     }
-    return s * back;
 }
 
 // ------------------------------------------------------- the n x n part, n <= 64
-// One workgroup a matrix, everything in LDS: bound by one CU's 64-bit matrix rate, so that only
-// tiles on and below the diagonal are formed (16 x 16, as many as n has), and a single product's
-// waves split K in two, which balances them over the SIMDs.
-constexpr int SP = SMALL + 4;  // pitch
-template <int PLANES>
-__global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup g)
+// One workgroup a matrix, everything in LDS; a wave for each 16 x 16 tile on and below the
+// diagonal, whose operands are all on their way before the first product.
+template <int NT, bool F32>
+struct SmallLds {
+    static constexpr int PITCH = 16 * NT + (F32 ? 2 : 4);  // 16 bytes of 16 rows on distinct banks
+    alignas(16) Part<F32> m[4][16 * NT][PITCH];
+};
+template <int NT, bool F32>
+__device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p, unsigned char *lds,
+                                            double *diagonal, unsigned int *red)
 {
-    constexpr bool F32 = PLANES == 3;
-    constexpr int UNITS = 20;  // tiles of two products, or of one by half its K
-    __shared__ double m[4][SMALL][SP];
-    __shared__ double half[10][16][17];
-    __shared__ unsigned int red[16];
-    double(*G)[SP] = m[0], (*P)[SP] = m[1], (*Q)[SP] = m[2], (*H)[SP] = m[3];
-    const NsItem &it = g.it[blockIdx.x];
+    using R = Part<F32>;
+    using L = SmallLds<NT, F32>;
+    constexpr int K = 16 * NT, TILES = NT * (NT + 1) / 2, PLANES = F32 ? 3 : 2;
+    auto &m = reinterpret_cast<L *>(lds)->m;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4;
-    const int n = static_cast<int>(it.tall ? it.m.cols : it.m.rows);
-    const int nt = (n + 15) / 16, tiles = nt * (nt + 1) / 2, K = 16 * nt;
-    double back = 1.;
-    if constexpr (!F32) {
-        const double scale = range_scale(it, red);
-        back = 1. / (scale * scale);
-    }
-    {
-        double v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = gram_at<F32>(it, SMALL * SMALL, tid + i * 1024, back);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            G[(tid + i * 1024) / SMALL][tid % SMALL] = v[i];
-    }
+
+    const unsigned int top = own_top(it);
+    const int gi = tid >> 4, gj = 4 * (tid & 15);
+    double v[4] = {0., 0., 0., 0.};
+    if (gi < K && gj < K)
+        gram_at<F32>(it, gi * SMALL + gj, v);
+    const double scale = F32 ? 1. : static_cast<double>(range_scale(top, red));
+    if (gi < K && gj == (gi & ~3))
+        diagonal[gi] = v[gi & 3];
     __syncthreads();
-    double trace = 0.;
-    for (int i = 0; i < K; ++i)
-        trace += G[i][i];
-    const double inv = 1. / (sqrt(trace) + static_cast<double>(g.p.eps));
+    double trace = lane < K ? diagonal[lane] : 0.;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        trace += __shfl_xor(trace, d);
+    // (1 / (|U|_F + eps), and of the scaled U)
+    const double inv = 1. / (sqrt(trace) / scale + static_cast<double>(p.eps)), in = inv / scale;
+    if (gi < K && gj < K)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            m[0][gi][gj + q] = static_cast<R>(v[q] * in * in);
     __syncthreads();
+
+    // Matrices 0 to 3: G, P, Q and H = P G.  Three stages a step,
+    //   P = a + b G + c G G    H = P G and Q = P Q    G = H P,
+    // in one piece of code, which is short enough to be fetched once.  (The first Q is P; after
+    // the last one nothing is to follow.)
+    constexpr int ROUNDS = (2 * TILES + 15) / 16;
+    const int unit = __builtin_amdgcn_readfirstlane(wave);
+    for (int step = 0, stage = 0;; stage = stage == 2 ? 0 : stage + 1) {
+        const bool first = step == 0, last = step + 1 == p.steps;
+        const int from = stage == 1 && last ? TILES : 0, to = stage == 1 && !first ? 2 * TILES : TILES;
+        Quad<R> x[ROUNDS];
+        int i0[ROUNDS], j0[ROUNDS], into[ROUNDS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        G[(tid + i * 1024) / SMALL][tid % SMALL] *= inv * inv;
-    __syncthreads();
-    auto tile_of = [](int t, int &i0, int &j0) {
-        int ti = 0;
-        while (t > ti) {
-            t -= ti + 1;
-            ++ti;
-        }
-        i0 = 16 * ti;
-        j0 = 16 * t;
-    };
-    // rows i0.. of X against rows j0.. of Y (symmetric), K values from k0 to k1
-    auto product = [&](double(*X)[SP], double(*Y)[SP], int i0, int j0, int k0, int k1) {
-        f64x4_t acc = {0., 0., 0., 0.};
-        for (int k = k0; k < k1; k += 8) {
+        for (int r = 0; r < ROUNDS; ++r) {
+            const int u = from + unit + 16 * r;
+            into[r] = -1;
+            if (u >= to)
+                continue;
+            const bool second = u >= TILES;
+            int t = second ? u - TILES : u, ti = 0;
 #pragma unroll
-            for (int s = 0; s < 8; s += 4)
-                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(X[i0 + lr][k + s + kq], Y[j0 + lr][k + s + kq],
-                                                           acc, 0, 0, 0);
-        }
-        return acc;
-    };
-    auto place = [&](double(*Z)[SP], int i0, int j0, const f64x4_t &v) {
+            for (int k = 1; k < NT; ++k)
+                ti += t >= k * (k + 1) / 2 ? 1 : 0;
+            i0[r] = 16 * ti;
+            j0[r] = 16 * (t - ti * (ti + 1) / 2);
+            into[r] = stage == 0 ? 1 : stage == 1 ? (second ? 2 : 3) : 0;
+            // rows i0.. of X against rows j0.. of Y (symmetric)
+            // (a lane's four consecutive values of 16 are four products' share)
+            const R *const X = &m[stage == 0 ? 0 : stage == 1 ? 1 : 3][i0[r] + lr][4 * kq];
+            const R *const Y = &m[stage == 0 ? 0 : stage == 1 ? (second ? 2 : 0) : 1][j0[r] + lr][4 * kq];
+            typedef R line_t __attribute__((ext_vector_type(16 / sizeof(R))));
+            constexpr int N = 16 / sizeof(R);
+            line_t v1[4 * NT / N], v2[4 * NT / N];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + 4 * q + kq, j = j0 + lr;
-            if (j <= i) {
-                Z[i][j] = v[q];
-                Z[j][i] = v[q];
+            for (int k = 0; k < 4 * NT / N; ++k) {
+                const int at = 16 * (k * N / 4) + k * N % 4;
+                v1[k] = *reinterpret_cast<const line_t *>(X + at);
+                v2[k] = *reinterpret_cast<const line_t *>(Y + at);
             }
-        }
-    };
-    // (a wave takes units wave and wave + 16)
-    auto one = [&](double(*X)[SP], double(*Y)[SP], double(*Z)[SP], bool poly) {
-        f64x4_t acc[2];
+            Quad<R> acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int u = wave + 16 * r;
-            int i0, j0;
-            tile_of(u < tiles ? u : u - tiles, i0, j0);
-            if (u < 2 * tiles)
-                acc[r] = product(X, Y, i0, j0, u < tiles ? 0 : K / 2, u < tiles ? K / 2 : K);
-            if (u >= tiles && u < 2 * tiles)
+            for (int k = 0; k < 4 * NT; ++k)
+                acc = mfma4(v1[k / N][k % N], v2[k / N][k % N], acc);
+            if (stage == 0) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    half[u - tiles][4 * q + kq][lr] = acc[r][q];
-        }
-        __syncthreads();
-        if (wave < tiles) {
-            int i0, j0;
-            tile_of(wave, i0, j0);
-            f64x4_t v;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v[q] = acc[0][q] + half[wave][4 * q + kq][lr];
-                if (poly) {
-                    const int i = i0 + 4 * q + kq, j = j0 + lr;
-                    v[q] = (i == j ? static_cast<double>(g.p.a) : 0.) +
-                           static_cast<double>(g.p.b) * X[i][j] + static_cast<double>(g.p.c) * v[q];
+                for (int q = 0; q < 4; ++q) {
+                    const int i = i0[r] + d_row(R(), q, lane), j = j0[r] + lr;
+                    acc[q] = (i == j ? static_cast<R>(p.a) : R(0)) + static_cast<R>(p.b) * m[0][i][j] +
+                             static_cast<R>(p.c) * acc[q];
                 }
             }
-            place(Z, i0, j0, v);
+            x[r] = acc;
+        }
+        if (stage == 1)
+            __syncthreads();  // (Q is read and written)
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            if (into[r] < 0)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0[r] + d_row(R(), q, lane), j = j0[r] + lr;
+                if (j <= i) {
+                    m[into[r]][i][j] = x[r][q];
+                    m[into[r]][j][i] = x[r][q];
+                    if (stage == 0 && first) {
+                        m[2][i][j] = x[r][q];
+                        m[2][j][i] = x[r][q];
+                    }
+                }
+            }
         }
         __syncthreads();
-    };
-    auto copy = [&](double(*from)[SP], double(*to)[SP]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            to[(tid + i * 1024) / SMALL][tid % SMALL] = from[(tid + i * 1024) / SMALL][tid % SMALL];
-        __syncthreads();
-    };
-    for (int step = 0; step < g.p.steps; ++step) {
-        const bool first = step == 0, last = step + 1 == g.p.steps;
-        one(G, G, P, true);
-        if (first) {
-            copy(P, Q);
-            if (!last)
-                one(P, G, H, false);
-        } else if (last) {
-            one(P, Q, H, false);
-            copy(H, Q);
-        } else {
-            // H = P G and Q = P Q at once
-            f64x4_t acc[2];
-            static_assert(UNITS <= 32, "two units a wave");
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int u = wave + 16 * r;
-                int i0, j0;
-                tile_of(u < tiles ? u : u - tiles, i0, j0);
-                if (u < 2 * tiles)
-                    acc[r] = product(P, u < tiles ? G : Q, i0, j0, 0, K);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int u = wave + 16 * r;
-                int i0, j0;
-                tile_of(u < tiles ? u : u - tiles, i0, j0);
-                if (u < 2 * tiles)
-                    place(u < tiles ? H : Q, i0, j0, acc[r]);
-            }
-            __syncthreads();
-        }
-        if (!last)
-            one(H, P, G, false);
+        if (stage == 1 && last)
+            break;
+        step += stage == 2 ? 1 : 0;
     }
+    auto &Q = m[2];
     if (tid < SMALL * SMALL / 8) {
         const int i = tid / (SMALL / 8), j = tid % (SMALL / 8) * 8;
-        float v[8];
+        float w[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)  // (zeros past n's tiles: U is zero there, too)
-            v[q] = i < K && j + q < K ? static_cast<float>(Q[i][j + q] * inv) : 0.f;
-        u32x4_t w[PLANES];
-        split_planes(v, w);
+            w[q] = i < K && j < K ? static_cast<float>(static_cast<double>(Q[i][j + q]) * inv) : 0.f;
+        u32x4_t planes[PLANES];
+        split_planes(w, planes);
 #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
-            *reinterpret_cast<u32x4_t *>(it.q + (p * SMALL + i) * SMALL + j) = w[p];
+        for (int k = 0; k < PLANES; ++k)
+            *reinterpret_cast<u32x4_t *>(it.q + (k * SMALL + i) * SMALL + j) = planes[k];
     }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup<NsItem> g)
+{
+    __shared__ __align__(16) unsigned char lds[sizeof(SmallLds<SMALL / 16, F32>)];
+    __shared__ double diagonal[SMALL];
+    __shared__ unsigned int red[16];
+    const NsItem &it = g.it[blockIdx.x];
+    if (it.n > 48)
+        small_steps<4, F32>(it, g.p, lds, diagonal, red);
+    else if (it.n > 32)
+        small_steps<3, F32>(it, g.p, lds, diagonal, red);
+    else if (it.n > 16)
+        small_steps<2, F32>(it, g.p, lds, diagonal, red);
+    else
+        small_steps<1, F32>(it, g.p, lds, diagonal, red);
 }
 
 // ------------------------------------------------------- the n x n part, larger
 template <bool F32>
-__global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup g)
+__global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
 {
-    __shared__ unsigned int red[THREADS / 64];
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
-    const int64_t size = static_cast<int64_t>(it.np) * it.np;
-    double back = 1.;
-    if constexpr (!F32) {
-        const double scale = range_scale(it, red);
-        back = 1. / (scale * scale);
-    }
     const int64_t e = (static_cast<int64_t>(blockIdx.x) - g.start[item]) * THREADS + threadIdx.x;
     const int i = static_cast<int>(e / it.np), j = static_cast<int>(e % it.np);
     if (i >= it.np || j > i)
         return;
-    const double s = gram_at<F32>(it, size, e, back);
-    it.mat[e] = s;
-    it.mat[static_cast<int64_t>(j) * it.np + i] = s;
+    double s[1];
+    gram_at<F32>(it, e, s);
+    Part<F32> *const G = reinterpret_cast<Part<F32> *>(it.mat);
+    G[e] = static_cast<Part<F32>>(s[0]);
+    G[static_cast<int64_t>(j) * it.np + i] = static_cast<Part<F32>>(s[0]);
 }
 
 // One product of symmetric matrices, 32 x 32 tiles on and below the diagonal, mirrored:
 //   0  P = a I + b G + c G G    1  H = P G, and Q = P Q    2  G = H P    3  Q = P Q
 // (Q in the first step: P).  G is not scaled in place: the first step's products take it by
-// 1 / |U|^2, which is formed from its diagonal.  Matrices 4 and 5 are the other G and Q.
-template <int OP>
-__global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int step)
+// 1 / |U|^2, which is formed from its diagonal.  Matrices 4 and 5 are the other G and Q.  The last
+// Q goes into planes.
+template <int OP, bool F32>
+__global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem> g, int step)
 {
-    __shared__ double red[POLY_WAVES][POLY][POLY + 1];
+    using R = Part<F32>;
+    constexpr int PLANES = F32 ? 3 : 2;
+    __shared__ R red[POLY_WAVES][POLY][POLY + 1];
     __shared__ double tr[POLY_WAVES];
+    __shared__ unsigned int tops[POLY_WAVES];
     const int item = find_item(g, blockIdx.x);
     const NsItem &it = g.it[item];
     const int np = it.np, nt = np / POLY, tiles = nt * (nt + 1) / 2;
@@ -637,11 +696,12 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
         ++ti;
     }
     const int64_t size = static_cast<int64_t>(np) * np;
-    double *const G = it.mat + (step & 1 ? 4 * size : 0), *const G2 = it.mat + (step & 1 ? 0 : 4 * size);
-    double *const P = it.mat + size, *const H = it.mat + 3 * size;
-    double *const Q = it.mat + (step & 1 ? 5 : 2) * size, *const Q2 = it.mat + (step & 1 ? 2 : 5) * size;
-    const double *X, *Y;
-    double *out;
+    R *const mat = reinterpret_cast<R *>(it.mat);
+    R *const G = mat + (step & 1 ? 4 * size : 0), *const G2 = mat + (step & 1 ? 0 : 4 * size);
+    R *const P = mat + size, *const H = mat + 3 * size;
+    R *const Q = mat + (step & 1 ? 5 : 2) * size, *const Q2 = mat + (step & 1 ? 2 : 5) * size;
+    const R *X, *Y;
+    R *out;
     if constexpr (OP == 0) {
         X = Y = G;
         out = P;
@@ -662,46 +722,51 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
     const int lr = lane & 15, kq = lane >> 4, i0 = ti * POLY, j0 = tj * POLY;
 
     // the first G's scale
-    double inv = 1.;
+    double scaled = 1., inv = 1.;
     if (step == 0 && OP == 0) {
+        const unsigned int top = F32 ? 0u : own_top(it);
         double s = 0.;
         for (int i = tid; i < np; i += POLY_WAVES * 64)
-            s += G[static_cast<int64_t>(i) * np + i];
+            s += static_cast<double>(G[static_cast<int64_t>(i) * np + i]);
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1)
             s += __shfl_xor(s, d);
         if (lane == 0)
             tr[wave] = s;
+        const double scale = F32 ? 1. : static_cast<double>(range_scale(top, tops));
         __syncthreads();
         s = tr[0];
         for (int w = 1; w < POLY_WAVES; ++w)
             s += tr[w];
-        inv = 1. / (sqrt(s) + static_cast<double>(g.p.eps));
-        if (ti == 0 && tid == 0)
-            *it.scal = inv;
+        inv = 1. / (sqrt(s) / scale + static_cast<double>(g.p.eps));
+        scaled = inv / scale * (inv / scale);
+        if (ti == 0 && tid == 0) {
+            it.scal[0] = inv;
+            it.scal[1] = scaled;
+        }
     } else if (step == 0) {
-        inv = *it.scal;
+        scaled = it.scal[1];
     }
 
-    f64x4_t acc[2][2];
+    Quad<R> acc[2][2];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            acc[x][y] = f64x4_t{0., 0., 0., 0.};
+            acc[x][y] = Quad<R>{0, 0, 0, 0};
     // 16 values of K a turn (np is whole turns of the waves), four consecutive ones a lane; three
     // turns' loads at once: another CU wrote them, and each wait is one for its cache
     constexpr int TURN = 16 * POLY_WAVES, AHEAD = 3;
     for (int k0 = 16 * wave; k0 < np; k0 += AHEAD * TURN) {
-        f64x4_t a[AHEAD][2], b[AHEAD][2];
+        Quad<R> a[AHEAD][2], b[AHEAD][2];
 #pragma unroll
         for (int t = 0; t < AHEAD; ++t) {
             const int k = k0 + t * TURN < np ? k0 + t * TURN : k0;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                a[t][q] = *reinterpret_cast<const f64x4_t *>(
+                a[t][q] = *reinterpret_cast<const Quad<R> *>(
                     X + static_cast<int64_t>(i0 + 16 * q + lr) * np + k + 4 * kq);
-                b[t][q] = *reinterpret_cast<const f64x4_t *>(
+                b[t][q] = *reinterpret_cast<const Quad<R> *>(
                     Y + static_cast<int64_t>(j0 + 16 * q + lr) * np + k + 4 * kq);
             }
         }
@@ -715,8 +780,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(a[t][x][s], b[t][y][s],
-                                                                         acc[x][y], 0, 0, 0);
+                        acc[x][y] = mfma4(a[t][x][s], b[t][y][s], acc[x][y]);
         }
     }
 #pragma unroll
@@ -725,76 +789,85 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup g, int
         for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                red[wave][16 * x + 4 * q + kq][16 * y + lr] = acc[x][y][q];
+                red[wave][16 * x + d_row(R(), q, lane)][16 * y + lr] = acc[x][y][q];
     __syncthreads();
+    const bool planes = (OP == 3 || OP == 0) && step + 1 == g.p.steps && (OP == 3 || step == 0);
+    // the values of the tile, and a second time transposed
+    auto put = [&](int i, int j, R x) {
+        const int64_t at = static_cast<int64_t>(i) * np + j;
+        if (planes) {
+            float r = static_cast<float>(static_cast<double>(x) * (OP == 0 ? inv : it.scal[0]));
+#pragma unroll
+            for (int k = 0; k < PLANES; ++k) {
+                const uint16_t w = f32_to_bf16(r);
+                it.q[k * size + at] = w;
+                r -= __uint_as_float(static_cast<unsigned int>(w) << 16);
+            }
+            return;
+        }
+        out[at] = x;
+        if constexpr (OP == 0) {
+            if (step == 0)  // the first Q
+                Q2[at] = x;
+        }
+    };
     for (int e = tid; e < POLY * POLY; e += POLY_WAVES * 64) {
         const int i = e / POLY, j = e % POLY;
-        double s = red[0][i][j];
+        R s = red[0][i][j];
 #pragma unroll
         for (int w = 1; w < POLY_WAVES; ++w)
             s += red[w][i][j];
-        const int64_t at = static_cast<int64_t>(i0 + i) * np + j0 + j;
         if constexpr (OP == 0) {
-            const double i2 = inv * inv;
-            s = static_cast<double>(g.p.b) * (i2 * G[at]) + static_cast<double>(g.p.c) * (i2 * i2 * s);
-            if (i0 + i == j0 + j)
-                s += static_cast<double>(g.p.a);
+            const double x = static_cast<double>(G[static_cast<int64_t>(i0 + i) * np + j0 + j]);
+            s = static_cast<R>((i0 + i == j0 + j ? static_cast<double>(g.p.a) : 0.) +
+                               static_cast<double>(g.p.b) * (scaled * x) +
+                               static_cast<double>(g.p.c) * (scaled * (scaled * static_cast<double>(s))));
         } else if constexpr (OP == 1) {
             if (!second)
-                s *= inv * inv;
+                s = static_cast<R>(static_cast<double>(s) * scaled);
         }
-        if (j0 + j <= i0 + i) {
-            out[at] = s;
-            out[static_cast<int64_t>(j0 + j) * np + i0 + i] = s;
-            if constexpr (OP == 0) {
-                if (step == 0) {  // the first Q
-                    Q2[at] = s;
-                    Q2[static_cast<int64_t>(j0 + j) * np + i0 + i] = s;
-                }
-            }
-        }
+        red[0][i][j] = s;  // (no other thread reads it before the barrier)
+        if (j0 + j <= i0 + i)
+            put(i0 + i, j0 + j, s);
     }
-}
-
-// the planes of Q / (|U|_F + eps)
-template <int PLANES>
-__global__ void __launch_bounds__(THREADS) ns_q_planes_kernel(NsGroup g)
-{
-    const int item = find_item(g, blockIdx.x);
-    const NsItem &it = g.it[item];
-    const int64_t size = static_cast<int64_t>(it.np) * it.np;
-    const double *const Q = it.mat + ((g.p.steps & 1) ? 5 : 2) * size, inv = *it.scal;
-    const int64_t e = ((static_cast<int64_t>(blockIdx.x) - g.start[item]) * THREADS + threadIdx.x) * 8;
-    if (e >= size)
-        return;
-    float v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        v[q] = static_cast<float>(Q[e + q] * inv);
-    u32x4_t w[PLANES];
-    split_planes(v, w);
-#pragma unroll
-    for (int p = 0; p < PLANES; ++p)
-        *reinterpret_cast<u32x4_t *>(it.q + p * size + e) = w[p];
+    __syncthreads();
+    for (int e = tid; e < POLY * POLY; e += POLY_WAVES * 64) {
+        const int i = e % POLY, j = e / POLY;
+        if (j0 + j < i0 + i)
+            put(j0 + j, i0 + i, red[0][i][j]);
+    }
 }
 
 // ------------------------------------------------------------- O = Q U (or U Q)
 // Tiles of NB values of the shorter side by 128 of the longer one, eight waves (4 x 2), 64 values
-// of K (the shorter side) a stage, the next one on its way.
+// of K (the shorter side) a stage, the next one on its way.  The tile goes through LDS, so that
+// the update reads and writes whole lines.
+template <typename T, int NB>
+struct FinalLds {
+    static constexpr int P = sizeof(T) == 2 ? 2 : 3;
+    static constexpr int U_BYTES = Tiles<128>::K_BYTES > Tiles<128>::M_BYTES ? Tiles<128>::K_BYTES
+                                                                             : Tiles<128>::M_BYTES;
+    static constexpr int STAGE = P * (Tiles<NB>::K_BYTES + U_BYTES);
+    static constexpr int OUT = 128 * (NB + 4) * 4 > NB * (128 + 4) * 4 ? 128 * (NB + 4) * 4
+                                                                       : NB * (128 + 4) * 4;
+    static constexpr int BYTES = STAGE > OUT ? STAGE : OUT;
+};
 template <typename T, bool TALL, int NB>
-__global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
+__device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsigned char *lds)
 {
     constexpr int P = sizeof(T) == 2 ? 2 : 3;
     constexpr int BM = TALL ? 128 : NB, BN = TALL ? NB : 128;
     using Tq = Tiles<NB>;
     using Tu = Tiles<128>;
     constexpr int KP = Tu::KP, MP = Tu::MP;
-    constexpr int Q_ROWS = NB, Q_BYTES = Tq::K_BYTES, U_BYTES = TALL ? Tu::K_BYTES : Tu::M_BYTES;
-    constexpr int TM = BM / 64, TN = BN / 32;  // 16 x 16 blocks of a wave
-    __shared__ __align__(16) unsigned char qs[P][Q_BYTES], us[P][U_BYTES];
-    const int item = find_item(g, blockIdx.x);
-    const NsItem &it = g.it[item];
-    const int block = static_cast<int>(blockIdx.x) - g.start[item];
+    constexpr int Q_ROWS = NB;
+    constexpr int TM = BM / (8 * FINAL_WAVES), TN = BN / 32;  // 16 x 16 blocks of a wave
+    unsigned char *qs[P], *us[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        qs[p] = lds + p * Tq::K_BYTES;
+        us[p] = lds + P * Tq::K_BYTES + p * FinalLds<T, NB>::U_BYTES;
+    }
     const int nb = it.np / NB;
     // (the tiles of one stretch of the longer side next to each other: they read the same U)
     const int n0 = (block % nb) * NB;
@@ -802,9 +875,9 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4, wm = wave >> 1, wn = wave & 1;
     const int np = it.np;
-    const int64_t qsize = static_cast<int64_t>(np) * np, usize = it.rp * it.cp;
+    const int64_t qsize = static_cast<int64_t>(np) * np, usize = static_cast<int64_t>(it.rp) * it.cp;
 
-    constexpr int QV = Q_ROWS * 8 / WAVES8, UV = 128 * 8 / WAVES8;  // 16-byte chunks a thread
+    constexpr int QV = Q_ROWS * 8 / (64 * FINAL_WAVES), UV = 128 * 8 / (64 * FINAL_WAVES);  // 16-byte chunks a thread
     u32x4_t qr[QV][P];
     Raw8<float> uf[UV];
     u32x4_t up[UV][2];
@@ -817,7 +890,7 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
     auto fetch = [&](int k) {
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
-            const int v = tid + i * WAVES8;
+            const int v = tid + i * (64 * FINAL_WAVES);
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 qr[i][p] = *reinterpret_cast<const u32x4_t *>(
@@ -825,7 +898,7 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
         }
 #pragma unroll
         for (int i = 0; i < UV; ++i) {
-            const int64_t at = u_at(tid + i * WAVES8, k);
+            const int64_t at = u_at(tid + i * (64 * FINAL_WAVES), k);
             if constexpr (P == 3) {
                 uf[i].template load<true>(reinterpret_cast<const float *>(it.u) + at, 8);
             } else {
@@ -839,14 +912,14 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
     auto keep = [&]() {
 #pragma unroll
         for (int i = 0; i < QV; ++i) {
-            const int v = tid + i * WAVES8;
+            const int v = tid + i * (64 * FINAL_WAVES);
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                *reinterpret_cast<u32x4_t *>(&qs[p][v / 8 * KP + v % 8 * 16]) = qr[i][p];
+                *reinterpret_cast<u32x4_t *>(qs[p] + v / 8 * KP + v % 8 * 16) = qr[i][p];
         }
 #pragma unroll
         for (int i = 0; i < UV; ++i) {
-            const int v = tid + i * WAVES8;
+            const int v = tid + i * (64 * FINAL_WAVES);
             u32x4_t w[P];
             if constexpr (P == 3) {
                 float f[8];
@@ -859,7 +932,7 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 *reinterpret_cast<u32x4_t *>(
-                    &us[p][TALL ? v / 8 * KP + v % 8 * 16 : v / 16 * MP + v % 16 * 16]) = w[p];
+                    us[p] + (TALL ? v / 8 * KP + v % 8 * 16 : v / 16 * MP + v % 16 * 16)) = w[p];
         }
     };
     f32x4_t acc[TM][TN];
@@ -877,97 +950,91 @@ __global__ void __launch_bounds__(WAVES8) ns_final_kernel(NsGroup g)
             fetch(k + 64);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            bf16x8_t a[TM][P], b[TN][P];
+            bf16x8_t a[TM][P];
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
+            for (int p = 0; p < P; ++p)
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    a[i][p] = TALL ? Tu::rows16(us[p], wm * (BM / 4) + 16 * i, h, lane)
-                                   : Tq::rows16(qs[p], wm * (BM / 4) + 16 * i, h, lane);
+                    a[i][p] = TALL ? Tu::rows16(us[p], wm * (16 * TM) + 16 * i, h, lane)
+                                   : Tq::rows16(qs[p], wm * (16 * TM) + 16 * i, h, lane);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    b[j][p] = TALL ? Tq::rows16(qs[p], wn * (BN / 2) + 16 * j, h, lane)
-                                   : Tu::columns16(us[p], wn * (BN / 2) + 16 * j, h, lane);
-            }
+            for (int j = 0; j < TN; ++j) {
+                bf16x8_t b[P];
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int p = 0; p < P; ++p)
+                    b[p] = TALL ? Tq::rows16(qs[p], wn * (BN / 2) + 16 * j, h, lane)
+                                : Tu::columns16(us[p], wn * (BN / 2) + 16 * j, h, lane);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
                     for (int s = P - 1; s >= 0; --s)  // planes x and s - x, the small ones first
 #pragma unroll
                         for (int x = 0; x <= s; ++x)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][s - x], a[i][x],
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s - x], a[i][x],
                                                                                 acc[i][j], 0, 0, 0);
+            }
         }
     }
     // a lane holds row lr and four consecutive columns of each block
-    const int64_t m0 = (TALL ? l0 : n0) + wm * (BM / 4), c0 = (TALL ? n0 : l0) + wn * (BN / 2);
-    const bool aligned = it.m.cols % 4 == 0;
+    constexpr int OP = BN + 4, ROW = BN / 8, OV = BM * ROW / (64 * FINAL_WAVES);
+    float *const tile = reinterpret_cast<float *>(lds);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t r = m0 + 16 * i + lr;
-        if (r >= it.m.rows)
-            continue;
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t c = c0 + 16 * j + 4 * kq, at = r * it.m.cols + c;
-            const T *const p = static_cast<const T *>(it.m.p) + at;
-            T *const o = static_cast<T *>(it.m.out) + at;
-            float v[4], w[4];
+        for (int j = 0; j < TN; ++j)
+            *reinterpret_cast<f32x4_t *>(tile + (wm * (16 * TM) + 16 * i + lr) * OP + wn * (BN / 2) +
+                                         16 * j + 4 * kq) = acc[i][j];
+    const int64_t m0 = TALL ? l0 : n0, c0 = TALL ? n0 : l0;
+    Raw8<T> raw[OV];
+    int cnt[OV];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v[q] = acc[i][j][q];
-                w[q] = 0.f;
-            }
-            if (aligned && c < it.m.cols) {
-                if constexpr (sizeof(T) == 2) {
-                    if (it.m.p != nullptr) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                        w[0] = __uint_as_float(u.x << 16);
-                        w[1] = __uint_as_float(u.x & 0xffff0000u);
-                        w[2] = __uint_as_float(u.y << 16);
-                        w[3] = __uint_as_float(u.y & 0xffff0000u);
-                    }
-                } else if (it.m.p != nullptr) {
-                    const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = u[q];
-                }
-            } else if (it.m.p != nullptr) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c + q < it.m.cols) {
-                        if constexpr (sizeof(T) == 2)
-                            w[q] = __uint_as_float(static_cast<unsigned int>(p[q]) << 16);
-                        else
-                            w[q] = p[q];
-                    }
-            }
-            if (it.m.p != nullptr) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = __fmaf_rn(-it.m.step, v[q], it.m.keep * w[q]);
-            }
-            if (aligned && c < it.m.cols) {
-                if constexpr (sizeof(T) == 2)
-                    *reinterpret_cast<uint2 *>(o) =
-                        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-                else
-                    *reinterpret_cast<f32x4_t *>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c + q < it.m.cols) {
-                        if constexpr (sizeof(T) == 2)
-                            o[q] = f32_to_bf16(v[q]);
-                        else
-                            o[q] = v[q];
-                    }
-            }
-        }
+    for (int i = 0; i < OV; ++i) {
+        const int v = tid + i * (64 * FINAL_WAVES);
+        const int64_t r = m0 + v / ROW, c = c0 + v % ROW * 8;
+        cnt[i] = r < it.rows ? count8(it.cols, c) : 0;
+        if (it.p != nullptr && cnt[i] > 0)
+            raw[i].load(static_cast<const T *>(it.p) + r * it.cols + c, cnt[i]);
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < OV; ++i) {
+        const int v = tid + i * (64 * FINAL_WAVES);
+        const int64_t r = m0 + v / ROW, c = c0 + v % ROW * 8;
+        if (cnt[i] <= 0)
+            continue;
+        float x[8];
+        const float *const from = tile + v / ROW * OP + v % ROW * 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const f32x4_t y = *reinterpret_cast<const f32x4_t *>(from + 4 * q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[4 * q + k] = y[k];
+        }
+        if (it.p != nullptr) {
+            float w[8];
+            raw[i].get(w);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                x[q] = __fmaf_rn(-it.step, x[q], it.keep * w[q]);
+        }
+        raw[i].set(x);
+        raw[i].store(static_cast<T *>(it.out) + r * it.cols + c, cnt[i]);
+    }
+}
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(64 * FINAL_WAVES, sizeof(T) == 2 ? FINAL_WAVES / 2 : FINAL_WAVES / 4) ns_final_kernel(NsGroup<NsOutput> g)
+{
+    __shared__ __align__(16) unsigned char lds[FinalLds<T, NB>::BYTES];
+    const int at = place_on_xcd(), item = find_item(g, at);
+    const NsOutput &it = g.it[item];
+    const int block = at - g.start[item];
+    if (it.tall)
+        final_tile<T, true, NB>(it, block, lds);
+    else
+        final_tile<T, false, NB>(it, block, lds);
 }
 
 // ------------------------------------------------------------------- planning
@@ -990,7 +1057,18 @@ Sides sides(int64_t rows, int64_t cols)
     return s;
 }
 
-// Matrices [first, first + count) of one set of launches: up to 16, in 256 MiB (or one).
+int64_t gram_tile(int bf16, int64_t np) { return bf16 && np > SMALL ? 128 : 64; }
+int64_t gram_tiles(int bf16, int64_t np)
+{
+    const int64_t nt = np / gram_tile(bf16, np);
+    return nt * (nt + 1) / 2;
+}
+int64_t prepare_groups(int64_t rp, int64_t cp)
+{
+    return (rp * cp / 8 + THREADS * PREP_VPT - 1) / (THREADS * PREP_VPT);
+}
+
+// Matrices [first, first + count) of one set of launches: up to 40, in 256 MiB (or one).
 struct Chunk {
     int first, count;
     size_t bytes;
@@ -998,92 +1076,78 @@ struct Chunk {
 };
 constexpr size_t CHUNK_BYTES = size_t(256) << 20;
 
-int64_t gram_tile(int bf16, int64_t np) { return bf16 && np > SMALL ? 128 : 64; }
-int64_t prepare_groups(int64_t rp, int64_t cp)
-{
-    return (rp * cp / 8 + THREADS * PREP_VPT - 1) / (THREADS * PREP_VPT);
-}
-
 Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
 {
     Chunk c;
     c.first = first;
-    c.count = 0;
-    c.bytes = 0;
-    auto fill = [&](NsItem &it, const NsMatrix &m, size_t off, int share) {
+    int64_t per_split = 0;
+    auto fill = [&](NsItem &it, const NsMatrix &m, size_t off) {
         const Sides s = sides(m.rows, m.cols);
-        it.m = m;
         it.tall = s.tall;
+        it.n = static_cast<int>(s.tall ? m.cols : m.rows);
         it.np = static_cast<int>(s.np);
-        it.rp = s.rp;
-        it.cp = s.cp;
-        it.lp = s.lp;
-        // about 512 workgroups for the Gram products of the set (1024 in 64 bits, of four
-        // waves), of 128 values of L each at least
-        const int64_t nt = s.np / gram_tile(bf16, s.np), tiles = nt * (nt + 1) / 2;
-        int64_t z = (bf16 ? 512 : 1024) / (tiles * share);
-        z = z < 1 ? 1 : z > 32 ? 32 : z;
-        it.per_split = up_to((s.lp + z - 1) / z, 128);
+        it.rp = static_cast<int>(s.rp);
+        it.cp = static_cast<int>(s.cp);
+        it.per_split = static_cast<int>(per_split < s.lp ? per_split : s.lp);
         it.splits = static_cast<int>((s.lp + it.per_split - 1) / it.per_split);
         auto take = [&](size_t bytes) {
             const size_t at = off;
             off += (bytes + 255) / 256 * 256;
             return ws + at;
         };
-        const size_t square = static_cast<size_t>(s.np) * s.np;
+        const size_t square = static_cast<size_t>(s.np) * s.np, real = bf16 ? 4 : 8;
         it.u = take(static_cast<size_t>(s.rp) * s.cp * 4);
         it.top_count = bf16 ? static_cast<int>(prepare_groups(s.rp, s.cp)) : 0;
         it.tops = reinterpret_cast<unsigned int *>(take(it.top_count * sizeof(unsigned int)));
-        it.part = take(it.splits * square * (bf16 ? 4 : 8));
-        it.mat = reinterpret_cast<double *>(take(s.np > SMALL ? 6 * square * 8 : 0));
-        it.scal = reinterpret_cast<double *>(take(8));
+        it.part = take(it.splits * square * real);
+        it.mat = take(s.np > SMALL ? 6 * square * real : 0);
+        it.scal = reinterpret_cast<double *>(take(2 * sizeof(double)));
         it.q = reinterpret_cast<uint16_t *>(take((bf16 ? 2 : 3) * square * 2));
         return off;
     };
-    // how many matrices share the set decides their splits: count them at the most splits first
-    size_t off = 0;
-    while (first + c.count < count && c.count < MAX_ITEMS) {
-        NsItem it;
-        const size_t next = fill(it, mats[first + c.count], off, 1);
-        if (c.count > 0 && next > CHUNK_BYTES)
-            break;
-        off = next;
-        ++c.count;
-    }
-    off = 0;
-    for (int i = 0; i < c.count; ++i)
-        off = fill(c.it[i], mats[first + i], off, c.count);
-    c.bytes = off;
+    // The Gram products of the set as about 512 workgroups of equal length (1024 in 64 bits, of
+    // half the waves), of 128 values of the longer side each at least; a matrix has at most 64.
+    auto split = [&](int n) {
+        int64_t work = 0, longest = 0;
+        for (int i = first; i < first + n; ++i) {
+            const Sides s = sides(mats[i].rows, mats[i].cols);
+            work += gram_tiles(bf16, s.np) * s.lp;
+            longest = s.lp > longest ? s.lp : longest;
+        }
+        const int64_t even = work / (bf16 ? 512 : 1024), least = (longest + 63) / 64;
+        per_split = up_to(even > least ? even : least, 128);
+        size_t off = 0;
+        for (int i = 0; i < n; ++i)
+            off = fill(c.it[i], mats[first + i], off);
+        return off;
+    };
+    c.count = count - first < MAX_ITEMS ? count - first : MAX_ITEMS;
+    while ((c.bytes = split(c.count)) > CHUNK_BYTES && c.count > 1)
+        c.count -= (c.count + 7) / 8;
     return c;
 }
 
-// The items of a chunk that `take` picks, with `blocks` workgroups each.
-template <typename Take, typename Blocks>
-int group_of(NsGroup &g, const Chunk &c, Take &&take, Blocks &&blocks)
+// The items that `take` picks as a launch's group, with `blocks` workgroups each.
+template <typename I, typename Take, typename Blocks>
+int group_of(NsGroup<I> &g, const I *items, const Chunk &c, Take &&take, Blocks &&blocks)
 {
-    g.count = 0;
-    int at = 0;
+    int n = 0, at = 0;
     for (int i = 0; i < c.count; ++i) {
         if (!take(c.it[i]))
             continue;
-        g.it[g.count] = c.it[i];
-        g.start[g.count++] = at;
+        g.it[n] = items[i];
+        g.start[n++] = at;
         at += static_cast<int>(blocks(c.it[i]));
     }
-    g.start[g.count] = at;
+    for (; n < MAX_ITEMS; ++n)
+        g.start[n] = INT_MAX;
     return at;
 }
 
 template <typename T>
-hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
+hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hipStream_t st)
 {
     constexpr bool F32 = sizeof(T) == 4;
-    constexpr int PLANES = F32 ? 3 : 2;
-    NsGroup g;
-    g.p = p;
-    auto all = [](const NsItem &) { return true; };
-    auto small = [](const NsItem &i) { return i.np == SMALL; };
-    auto large = [](const NsItem &i) { return i.np > SMALL; };
 #define NS_LAUNCH(...)                         \
     do {                                       \
         hipLaunchKernelGGL(__VA_ARGS__);       \
@@ -1091,36 +1155,40 @@ hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
         if (e_ != hipSuccess)                  \
             return e_;                         \
     } while (0)
-    int n = group_of(g, c, all, [](const NsItem &i) { return prepare_groups(i.rp, i.cp); });
-    NS_LAUNCH((ns_prepare_kernel<T>), dim3(n), dim3(THREADS), 0, st, g);
-    auto gram_groups = [](const NsItem &i) {
-        const int64_t nt = i.np / gram_tile(!F32, i.np);
-        return nt * (nt + 1) / 2 * i.splits;
-    };
+    auto all = [](const NsItem &) { return true; };
+    auto small = [](const NsItem &i) { return i.np == SMALL; };
+    auto large = [](const NsItem &i) { return i.np > SMALL; };
+    int n;
+    {
+        NsInput in[MAX_ITEMS];
+        for (int i = 0; i < c.count; ++i) {
+            const NsItem &it = c.it[i];
+            const NsMatrix &m = mats[c.first + i];
+            in[i] = NsInput{it.u, it.tops, m.g, m.m, m.m_out, m.rows, m.cols, it.rp, it.cp};
+        }
+        NsGroup<NsInput> g;
+        g.p = p;
+        n = group_of(g, in, c, all, [](const NsItem &i) { return prepare_groups(i.rp, i.cp); });
+        NS_LAUNCH((ns_prepare_kernel<T>), dim3(n), dim3(THREADS), 0, st, g);
+    }
+    NsGroup<NsItem> g;
+    g.p = p;
+    auto gram_groups = [](const NsItem &i) { return gram_tiles(!F32, i.np) * i.splits; };
     if constexpr (F32) {
-        n = group_of(g, c, all, gram_groups);
+        n = group_of(g, c.it, c, all, gram_groups);
         NS_LAUNCH(ns_gram_f64_kernel, dim3(n), dim3(THREADS), 0, st, g);
     } else {
-        for (int kind = 0; kind < 4; ++kind) {
-            const bool tall = kind & 1, big = kind & 2;
-            n = group_of(g, c, [&](const NsItem &i) { return (i.tall != 0) == tall && (i.np > SMALL) == big; },
-                         gram_groups);
-            if (n == 0)
-                continue;
-            if (tall && big)
-                NS_LAUNCH((ns_gram_kernel<true, 128>), dim3(n), dim3(WAVES8), 0, st, g);
-            else if (tall)
-                NS_LAUNCH((ns_gram_kernel<true, 64>), dim3(n), dim3(WAVES8), 0, st, g);
-            else if (big)
-                NS_LAUNCH((ns_gram_kernel<false, 128>), dim3(n), dim3(WAVES8), 0, st, g);
-            else
-                NS_LAUNCH((ns_gram_kernel<false, 64>), dim3(n), dim3(WAVES8), 0, st, g);
-        }
+        n = group_of(g, c.it, c, small, gram_groups);
+        if (n > 0)
+            NS_LAUNCH((ns_gram_kernel<64>), dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
+        n = group_of(g, c.it, c, large, gram_groups);
+        if (n > 0)
+            NS_LAUNCH((ns_gram_kernel<128>), dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
     }
-    n = group_of(g, c, small, [](const NsItem &) { return 1; });
+    n = group_of(g, c.it, c, small, [](const NsItem &) { return 1; });
     if (n > 0)
-        NS_LAUNCH((ns_small_kernel<PLANES>), dim3(n), dim3(1024), 0, st, g);
-    n = group_of(g, c, large, [](const NsItem &i) {
+        NS_LAUNCH((ns_small_kernel<F32>), dim3(n), dim3(1024), 0, st, g);
+    n = group_of(g, c.it, c, large, [](const NsItem &i) {
         return (static_cast<int64_t>(i.np) * i.np + THREADS - 1) / THREADS;
     });
     if (n > 0) {
@@ -1131,43 +1199,38 @@ hipError_t run_chunk(const Chunk &c, const NsParams &p, hipStream_t st)
         const dim3 block(POLY_WAVES * 64);
         for (int s = 0; s < p.steps; ++s) {
             const bool first = s == 0, last = s + 1 == p.steps;
-            n = group_of(g, c, large, tiles);
-            NS_LAUNCH((ns_poly_kernel<0>), dim3(n), block, 0, st, g, s);
+            n = group_of(g, c.it, c, large, tiles);
+            NS_LAUNCH((ns_poly_kernel<0, F32>), dim3(n), block, 0, st, g, s);
             if (last) {
                 if (!first)
-                    NS_LAUNCH((ns_poly_kernel<3>), dim3(n), block, 0, st, g, s);
+                    NS_LAUNCH((ns_poly_kernel<3, F32>), dim3(n), block, 0, st, g, s);
                 continue;
             }
             // (the first Q is P)
             const int each = first ? 1 : 2;
-            n = group_of(g, c, large, [&](const NsItem &i) { return each * tiles(i); });
-            NS_LAUNCH((ns_poly_kernel<1>), dim3(n), block, 0, st, g, s);
-            n = group_of(g, c, large, tiles);
-            NS_LAUNCH((ns_poly_kernel<2>), dim3(n), block, 0, st, g, s);
+            n = group_of(g, c.it, c, large, [&](const NsItem &i) { return each * tiles(i); });
+            NS_LAUNCH((ns_poly_kernel<1, F32>), dim3(n), block, 0, st, g, s);
+            n = group_of(g, c.it, c, large, tiles);
+            NS_LAUNCH((ns_poly_kernel<2, F32>), dim3(n), block, 0, st, g, s);
         }
-        n = group_of(g, c, large, [](const NsItem &i) {
-            return (static_cast<int64_t>(i.np) * i.np / 8 + THREADS - 1) / THREADS;
-        });
-        NS_LAUNCH((ns_q_planes_kernel<PLANES>), dim3(n), dim3(THREADS), 0, st, g);
     }
-    for (int tall = 0; tall < 2; ++tall)
-        for (int wide_n = 0; wide_n < 2; ++wide_n) {
-            n = group_of(g, c,
-                         [&](const NsItem &i) { return i.tall == tall && (i.np > SMALL) == wide_n; },
-                         [](const NsItem &i) {
-                             return i.lp / 128 * (i.np > SMALL ? i.np / 128 : 1);
-                         });
-            if (n == 0)
-                continue;
-            if (tall && wide_n)
-                NS_LAUNCH((ns_final_kernel<T, true, 128>), dim3(n), dim3(WAVES8), 0, st, g);
-            else if (tall)
-                NS_LAUNCH((ns_final_kernel<T, true, 64>), dim3(n), dim3(WAVES8), 0, st, g);
-            else if (wide_n)
-                NS_LAUNCH((ns_final_kernel<T, false, 128>), dim3(n), dim3(WAVES8), 0, st, g);
-            else
-                NS_LAUNCH((ns_final_kernel<T, false, 64>), dim3(n), dim3(WAVES8), 0, st, g);
-        }
+    NsOutput to[MAX_ITEMS];
+    for (int i = 0; i < c.count; ++i) {
+        const NsItem &it = c.it[i];
+        const NsMatrix &m = mats[c.first + i];
+        to[i] = NsOutput{it.u,   it.q,    m.p,   m.out,   m.rows, m.cols,
+                         m.step, m.keep, it.np, it.tall, it.rp,  it.cp};
+    }
+    NsGroup<NsOutput> o;
+    o.p = p;
+    n = group_of(o, to, c, small, [](const NsItem &i) { return (i.tall ? i.rp : i.cp) / 128; });
+    if (n > 0)
+        NS_LAUNCH((ns_final_kernel<T, 64>), dim3(n), dim3(64 * FINAL_WAVES), 0, st, o);
+    n = group_of(o, to, c, large, [](const NsItem &i) {
+        return static_cast<int64_t>(i.tall ? i.rp : i.cp) / 128 * (i.np / 128);
+    });
+    if (n > 0)
+        NS_LAUNCH((ns_final_kernel<T, 128>), dim3(n), dim3(64 * FINAL_WAVES), 0, st, o);
 #undef NS_LAUNCH
     return hipSuccess;
 }
@@ -1197,7 +1260,8 @@ hipError_t launch_newton_schulz(int bf16, const NsMatrix *mats, int count, const
 {
     for (int first = 0; first < count;) {
         const Chunk c = plan_chunk(bf16, mats, count, first, static_cast<char *>(ws));
-        const hipError_t e = bf16 ? run_chunk<uint16_t>(c, p, st) : run_chunk<float>(c, p, st);
+        const hipError_t e = bf16 ? run_chunk<uint16_t>(c, mats, p, st)
+                                  : run_chunk<float>(c, mats, p, st);
         if (e != hipSuccess)
             return e;
         first += c.count;

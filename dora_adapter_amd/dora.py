@@ -888,16 +888,21 @@ def dora_muon(params, grads, momenta, lr, mu=0.95, weight_decay=0.0, scales=None
         return params_out, momenta_out
     dev = _dev(params[0])
     kind, dt = params[0].dtype, _dt(params[0])
-    arr = (DoraUpdate * n)()
-    for k in range(n):
-        shape = _rows(f"params[{k}]", params[k])
-        for name, ts, t in (("params", params, kind), ("grads", grads, kind),
-                            ("momenta", momenta, torch.float32), ("params_out", params_out, kind),
-                            ("momenta_out", momenta_out, torch.float32)):
-            _need(f"{name}[{k}]", ts[k], dev, t, *shape)
-        arr[k] = DoraUpdate(params[k].data_ptr(), grads[k].data_ptr(), momenta[k].data_ptr(),
-                            params_out[k].data_ptr(), momenta_out[k].data_ptr(), *shape, float(lr),
-                            float(weight_decay), float(scales[k]))
+    lists = [("params", params, kind), ("grads", grads, kind), ("momenta", momenta, torch.float32)]
+    if params_out is not params:
+        lists.append(("params_out", params_out, kind))
+    if momenta_out is not momenta:
+        lists.append(("momenta_out", momenta_out, torch.float32))
+    lr, weight_decay, fields = float(lr), float(weight_decay), []
+    for k, p in enumerate(params):
+        shape = _rows("params", p)
+        for name, ts, t in lists:
+            x = ts[k]
+            if not (x.shape == shape and x.dtype is t and x.device == dev and x.is_contiguous()):
+                _need(f"{name}[{k}]", x, dev, t, *shape)
+        fields.append((p.data_ptr(), grads[k].data_ptr(), momenta[k].data_ptr(), params_out[k].data_ptr(),
+                       momenta_out[k].data_ptr(), *shape, lr, weight_decay, float(scales[k])))
+    arr = (DoraUpdate * n)(*fields)
     if _need_ws(ws, dev) is None:
         ws = _ws(lib().dora_muon_workspace(arr, n, dt), dev)
     _launch(dev, lib().dora_muon, arr, n, dt, float(mu), int(bool(nesterov)), int(steps),
