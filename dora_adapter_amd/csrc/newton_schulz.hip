@@ -53,7 +53,7 @@ struct NsItem {
     int tall;            // rows > cols
     int rp, cp;          // rows and columns as padded (the longer side to 128s)
     int top_count;
-    int splits, per_split;  // of the longer side, a multiple of 128
+    int splits, per_split;  // of the longer side, a multiple of 64
 };
 struct NsInput {  // what the prepare kernel reads and writes
     char *u;
@@ -84,15 +84,30 @@ static_assert(sizeof(NsGroup<NsItem>) <= 4000 && sizeof(NsGroup<NsInput>) <= 400
                   sizeof(NsGroup<NsOutput>) <= 4000,
               "a group must fit the kernel argument space");
 
-// (without a chain of dependent scalar loads)
-template <typename G>
-__device__ __forceinline__ int find_item(const G &g, int block)
+// The item of a workgroup and its place among that item's workgroups.  Each lane reads one item and
+// where it starts, so that there is one round trip to the arguments, which no cache holds yet
+// (a scalar search makes two, and 1.2 us of a kernel's 7).
+template <typename I>
+struct Found {
+    I it;
+    int block;
+};
+template <typename I>
+__device__ __forceinline__ Found<I> find_item(const NsGroup<I> &g, int block)
 {
-    int i = 0;
+    constexpr int WORDS = sizeof(I) / 4;
+    struct Words {
+        int w[WORDS];
+    };
+    const int lane = static_cast<int>(threadIdx.x) & 63, k = lane < MAX_ITEMS ? lane : MAX_ITEMS - 1;
+    const int start = g.start[k];
+    const Words mine = *reinterpret_cast<const Words *>(&g.it[k]);
+    const int i = __popcll(__ballot(lane < MAX_ITEMS && block >= start)) - 1;
+    Words one;
 #pragma unroll
-    for (int k = 1; k < MAX_ITEMS; ++k)
-        i += block >= g.start[k] ? 1 : 0;
-    return i;
+    for (int q = 0; q < WORDS; ++q)
+        one.w[q] = __builtin_amdgcn_readlane(mine.w[q], i);
+    return Found<I>{__builtin_bit_cast(I, one), block - __builtin_amdgcn_readlane(start, i)};
 }
 
 // A launch's workgroups go round the eight XCDs.  This gives each of them consecutive places, so
@@ -148,9 +163,9 @@ constexpr int PREP_VPT = 4;
 template <typename T>
 __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
 {
-    const int item = find_item(g, blockIdx.x);
-    const NsInput &it = g.it[item];
-    const unsigned int block = blockIdx.x - g.start[item];
+    const Found<NsInput> found = find_item(g, blockIdx.x);
+    const NsInput &it = found.it;
+    const unsigned int block = found.block;
     __shared__ unsigned int wave_top[THREADS / 64];
     unsigned int top = 0u;
     const unsigned int along = static_cast<unsigned int>(it.cp / 8);
@@ -247,10 +262,10 @@ __device__ __forceinline__ float range_scale(unsigned int top, unsigned int *red
 // eight consecutive ones give it one each time, of a tall one they are four rows.
 __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
 {
-    const int place = place_on_xcd(), item = find_item(g, place);
-    const NsItem &it = g.it[item];
+    const Found<NsItem> found = find_item(g, place_on_xcd());
+    const NsItem &it = found.it;
     const int nt = it.np / TILE, tiles = nt * (nt + 1) / 2;
-    const int block = place - g.start[item];
+    const int block = found.block;
     const int z = block / tiles;
     int t = block % tiles, ti = 0;
     while (t > ti) {
@@ -298,7 +313,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
         }
     };
     fetch(0, k0);
-    for (int64_t k = k0; k < k1; k += 64) {  // (whole 128s)
+    for (int64_t k = k0; k < k1; k += 64) {  // (whole 64s)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int64_t next = k + 32 * half + 32;
@@ -371,13 +386,11 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
         ++ti;
     }
     const int i0 = ti * NB, j0 = t * NB;
-    const bool diagonal = i0 == j0;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
                   k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
     const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
-    const unsigned int top = own_top(it);
 
     u32x4_t ra[V][2], rb[V][2];
     auto fetch = [&](u32x4_t (&r)[V][2], int r0, int64_t k) {
@@ -423,22 +436,18 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
         else
             return Tl::rows16(tile, r0, h, lane);
     };
-    auto &other = diagonal ? sa : sb;
     fetch(ra, i0, k0);
-    if (!diagonal)
-        fetch(rb, j0, k0);
-    scale = range_scale(top, red);
+    fetch(rb, j0, k0);
+    scale = range_scale(own_top(it), red);
     for (int64_t k = k0; k < k1; k += 64) {
         __syncthreads();
         keep(ra, sa);
-        if (!diagonal)
-            keep(rb, sb);
+        keep(rb, sb);
+        // (no branch round a load: the compiler would wait for it where the branch ends)
+        const int64_t next = k + 64 < k1 ? k + 64 : k0;
+        fetch(ra, i0, next);
+        fetch(rb, j0, next);
         __syncthreads();
-        if (k + 64 < k1) {
-            fetch(ra, i0, k + 64);
-            if (!diagonal)
-                fetch(rb, j0, k + 64);
-        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             bf16x8_t a[TM][2];
@@ -452,7 +461,7 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
                 bf16x8_t b[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    b[p] = operand(other[p], wn * (NB / 2) + 16 * j, h);
+                    b[p] = operand(sb[p], wn * (NB / 2) + 16 * j, h);
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -478,13 +487,11 @@ __global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kerne
 {
     __shared__ __align__(16) GramTiles<NB> sa, sb;
     __shared__ unsigned int red[GRAM_WAVES];
-    const int at = place_on_xcd(), item = find_item(g, at);
-    const NsItem &it = g.it[item];
-    const int block = at - g.start[item];
-    if (it.tall)
-        gram_tile_bf16<true, NB>(it, block, sa, sb, red);
+    const Found<NsItem> found = find_item(g, place_on_xcd());
+    if (found.it.tall)
+        gram_tile_bf16<true, NB>(found.it, found.block, sa, sb, red);
     else
-        gram_tile_bf16<false, NB>(it, block, sa, sb, red);
+        gram_tile_bf16<false, NB>(found.it, found.block, sa, sb, red);
 }
 
 // The sums of the Gram partials at N places from e.
@@ -658,9 +665,9 @@ __global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup<NsItem> g)
 template <bool F32>
 __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
 {
-    const int item = find_item(g, blockIdx.x);
-    const NsItem &it = g.it[item];
-    const int64_t e = (static_cast<int64_t>(blockIdx.x) - g.start[item]) * THREADS + threadIdx.x;
+    const Found<NsItem> found = find_item(g, blockIdx.x);
+    const NsItem &it = found.it;
+    const int64_t e = static_cast<int64_t>(found.block) * THREADS + threadIdx.x;
     const int i = static_cast<int>(e / it.np), j = static_cast<int>(e % it.np);
     if (i >= it.np || j > i)
         return;
@@ -684,10 +691,10 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
     __shared__ R red[POLY_WAVES][POLY][POLY + 1];
     __shared__ double tr[POLY_WAVES];
     __shared__ unsigned int tops[POLY_WAVES];
-    const int item = find_item(g, blockIdx.x);
-    const NsItem &it = g.it[item];
+    const Found<NsItem> found = find_item(g, place_on_xcd());
+    const NsItem &it = found.it;
     const int np = it.np, nt = np / POLY, tiles = nt * (nt + 1) / 2;
-    int tj = static_cast<int>(blockIdx.x) - g.start[item];
+    int tj = found.block;
     const bool second = tj >= tiles;  // Q's tiles behind H's
     tj -= second ? tiles : 0;
     int ti = 0;
@@ -754,14 +761,16 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 #pragma unroll
         for (int y = 0; y < 2; ++y)
             acc[x][y] = Quad<R>{0, 0, 0, 0};
-    // 16 values of K a turn (np is whole turns of the waves), four consecutive ones a lane; three
-    // turns' loads at once: another CU wrote them, and each wait is one for its cache
-    constexpr int TURN = 16 * POLY_WAVES, AHEAD = 3;
-    for (int k0 = 16 * wave; k0 < np; k0 += AHEAD * TURN) {
+    // A wave's share of K (whole 16s, next to each other: of a line's halves one load finds what the
+    // other brought), 16 values a turn, four consecutive ones a lane; three turns' loads at once:
+    // another CU wrote them, and each wait is one for its cache
+    constexpr int TURN = 16, AHEAD = 3;
+    const int k1 = (wave + 1) * (np / POLY_WAVES);
+    for (int k0 = wave * (np / POLY_WAVES); k0 < k1; k0 += AHEAD * TURN) {
         Quad<R> a[AHEAD][2], b[AHEAD][2];
 #pragma unroll
         for (int t = 0; t < AHEAD; ++t) {
-            const int k = k0 + t * TURN < np ? k0 + t * TURN : k0;
+            const int k = k0 + t * TURN < k1 ? k0 + t * TURN : k0;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 a[t][q] = *reinterpret_cast<const Quad<R> *>(
@@ -772,7 +781,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         }
 #pragma unroll
         for (int t = 0; t < AHEAD; ++t) {
-            if (k0 + t * TURN >= np)
+            if (k0 + t * TURN >= k1)
                 break;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
@@ -946,8 +955,7 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
         __syncthreads();
         keep();
         __syncthreads();
-        if (k + 64 < np)
-            fetch(k + 64);
+        fetch(k + 64 < np ? k + 64 : 0);  // (no branch round a load, as above)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             bf16x8_t a[TM][P];
@@ -977,14 +985,6 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
     }
     // a lane holds row lr and four consecutive columns of each block
     constexpr int OP = BN + 4, ROW = BN / 8, OV = BM * ROW / (64 * FINAL_WAVES);
-    float *const tile = reinterpret_cast<float *>(lds);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            *reinterpret_cast<f32x4_t *>(tile + (wm * (16 * TM) + 16 * i + lr) * OP + wn * (BN / 2) +
-                                         16 * j + 4 * kq) = acc[i][j];
     const int64_t m0 = TALL ? l0 : n0, c0 = TALL ? n0 : l0;
     Raw8<T> raw[OV];
     int cnt[OV];
@@ -996,6 +996,14 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
         if (it.p != nullptr && cnt[i] > 0)
             raw[i].load(static_cast<const T *>(it.p) + r * it.cols + c, cnt[i]);
     }
+    float *const tile = reinterpret_cast<float *>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            *reinterpret_cast<f32x4_t *>(tile + (wm * (16 * TM) + 16 * i + lr) * OP + wn * (BN / 2) +
+                                         16 * j + 4 * kq) = acc[i][j];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < OV; ++i) {
@@ -1028,13 +1036,11 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(64 * FINAL_WAVES, sizeof(T) == 2 ? FINAL_WAVES / 2 : FINAL_WAVES / 4) ns_final_kernel(NsGroup<NsOutput> g)
 {
     __shared__ __align__(16) unsigned char lds[FinalLds<T, NB>::BYTES];
-    const int at = place_on_xcd(), item = find_item(g, at);
-    const NsOutput &it = g.it[item];
-    const int block = at - g.start[item];
-    if (it.tall)
-        final_tile<T, true, NB>(it, block, lds);
+    const Found<NsOutput> found = find_item(g, place_on_xcd());
+    if (found.it.tall)
+        final_tile<T, true, NB>(found.it, found.block, lds);
     else
-        final_tile<T, false, NB>(it, block, lds);
+        final_tile<T, false, NB>(found.it, found.block, lds);
 }
 
 // ------------------------------------------------------------------- planning
@@ -1106,7 +1112,7 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         return off;
     };
     // The Gram products of the set as about 512 workgroups of equal length (1024 in 64 bits, of
-    // half the waves), of 128 values of the longer side each at least; a matrix has at most 64.
+    // half the waves), of 64 values of the longer side each at least; a matrix has at most 64 shares.
     auto split = [&](int n) {
         int64_t work = 0, longest = 0;
         for (int i = first; i < first + n; ++i) {
@@ -1115,7 +1121,7 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
             longest = s.lp > longest ? s.lp : longest;
         }
         const int64_t even = work / (bf16 ? 512 : 1024), least = (longest + 63) / 64;
-        per_split = up_to(even > least ? even : least, 128);
+        per_split = up_to(even > least ? even : least, 64);
         size_t off = 0;
         for (int i = 0; i < n; ++i)
             off = fill(c.it[i], mats[first + i], off);
