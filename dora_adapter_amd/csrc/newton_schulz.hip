@@ -35,7 +35,7 @@ typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
 constexpr int THREADS = 256;
-constexpr int TILE = 64;       // Gram tile
+constexpr int TILE = 64, GRAM = 128;  // Gram tiles of fp32 and of bf16 matrices
 constexpr int SMALL = 64;      // n x n matrices of one workgroup's LDS
 constexpr int POLY = 32;       // tile of the n x n products
 constexpr int POLY_WAVES = 8;  // which split their K
@@ -44,7 +44,8 @@ constexpr int POLY_WAVES = 8;  // which split their K
 // fp32 matrices in fp64: `part` and `mat` are of that type.
 struct NsItem {
     char *u;             // U padded with zeros, [rp, cp]: bf16 hi and lo, or fp32
-    unsigned int *tops;  // bf16: the largest |U| of each workgroup that wrote it, as bits
+    unsigned int *tops;  // bf16: the largest |U| of each workgroup that wrote it, as bits; with a
+                         // shorter side to 64 each partial's scale, as its exponent
     char *part;          // Gram partials [splits, np, np], tiles on and below the diagonal
     char *mat;           // G, P, Q, H and the other G and Q [np, np] (larger matrices)
     double *scal;        // 1 / (|U|_F + eps), and what makes the first G of U U^T
@@ -55,14 +56,14 @@ struct NsItem {
     int top_count;
     int splits, per_split;  // of the longer side, a multiple of 64
 };
-struct NsInput {  // what the prepare kernel reads and writes
-    char *u;
+struct NsInput {  // what the first kernel reads and writes
+    char *u, *part;
     unsigned int *tops;
     const void *g;
     const float *m;
     float *m_out;
     int64_t rows, cols;
-    int rp, cp;
+    int rp, cp, tall, per_split;
 };
 struct NsOutput {  // what the last kernel reads and writes
     const char *u;
@@ -235,8 +236,8 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
 }
 
 // The power of two that brings a bf16 matrix's largest |U| near one where fp32 might not hold its
-// Gram matrix, or the square of that, to the last bits that count; else 1.  `top`: the largest of
-// the thread's share (own_top).  Called by whole workgroups.
+// Gram matrix, or the square of that, to the last bits that count; else 1 (range_scale: of the
+// largest of each thread's share, own_top, by whole workgroups).
 __device__ __forceinline__ unsigned int own_top(const NsItem &it)
 {
     unsigned int top = 0u;
@@ -246,14 +247,18 @@ __device__ __forceinline__ unsigned int own_top(const NsItem &it)
     }
     return top;
 }
+__device__ __forceinline__ int range_exponent(unsigned int top)
+{
+    const int e = static_cast<int>(top >> 23) - 127;
+    return top == 0u || e == 128 || (e > -24 && e < 9) ? 0 : e == 127 ? -126 : -e;
+}
+__device__ __forceinline__ float power(int e)  // 2^e, -126 <= e <= 127
+{
+    return __uint_as_float(static_cast<unsigned int>(127 + e) << 23);
+}
 __device__ __forceinline__ float range_scale(unsigned int top, unsigned int *red)
 {
-    top = block_max(top, red, static_cast<int>(blockDim.x) >> 6);
-    const int e = static_cast<int>(top >> 23) - 127;
-    if (top == 0u || e == 128 || (e > -24 && e < 9))
-        return 1.f;
-    // (2^-e; |e| is at most 127)
-    return __uint_as_float(static_cast<unsigned int>(e == 127 ? 1 : 127 - e) << 23);
+    return power(range_exponent(block_max(top, red, static_cast<int>(blockDim.x) >> 6)));
 }
 
 // ------------------------------------------------------------------- G = U U^T
@@ -365,27 +370,26 @@ struct Tiles {
 };
 
 // bf16 matrices: both planes of both operands, all four products, in fp32 over a share of L (the
-// shares are added in 64 bits).  NB x NB tiles on and below the diagonal, eight waves (4 x 2),
+// shares are added in 64 bits).  128 x 128 tiles on and below the diagonal, eight waves (4 x 2),
 // 64 values of L a stage, the next one on its way.
 constexpr int GRAM_WAVES = 8, FINAL_WAVES = 8;  // two in each row
-template <int NB>
-using GramTiles = unsigned char[2][Tiles<NB>::K_BYTES > Tiles<NB>::M_BYTES ? Tiles<NB>::K_BYTES
-                                                                            : Tiles<NB>::M_BYTES];
-template <bool TALL, int NB>
-__device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, GramTiles<NB> &sa,
-                                               GramTiles<NB> &sb, unsigned int *red)
+using GramTiles = unsigned char[2][Tiles<GRAM>::K_BYTES > Tiles<GRAM>::M_BYTES ? Tiles<GRAM>::K_BYTES
+                                                                            : Tiles<GRAM>::M_BYTES];
+template <bool TALL>
+__device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, GramTiles &sa,
+                                               GramTiles &sb, unsigned int *red)
 {
-    using Tl = Tiles<NB>;
-    constexpr int TM = NB / (8 * GRAM_WAVES), TN = NB / 32;       // 16 x 16 blocks of a wave
-    constexpr int V = NB * 8 / (64 * GRAM_WAVES);              // 16-byte chunks of a plane a thread
-    const int nt = it.np / NB, tiles = nt * (nt + 1) / 2;
+    using Tl = Tiles<GRAM>;
+    constexpr int TM = GRAM / (8 * GRAM_WAVES), TN = GRAM / 32;       // 16 x 16 blocks of a wave
+    constexpr int V = GRAM * 8 / (64 * GRAM_WAVES);              // 16-byte chunks of a plane a thread
+    const int nt = it.np / GRAM, tiles = nt * (nt + 1) / 2;
     const int z = block / tiles;
     int t = block % tiles, ti = 0;
     while (t > ti) {
         t -= ti + 1;
         ++ti;
     }
-    const int i0 = ti * NB, j0 = t * NB;
+    const int i0 = ti * GRAM, j0 = t * GRAM;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
@@ -397,7 +401,7 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * (64 * GRAM_WAVES);
-            const int64_t at = TALL ? (k + v / (NB / 8)) * it.cp + r0 + v % (NB / 8) * 8
+            const int64_t at = TALL ? (k + v / (GRAM / 8)) * it.cp + r0 + v % (GRAM / 8) * 8
                                     : static_cast<int64_t>(r0 + v / 8) * it.cp + k + v % 8 * 8;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
@@ -406,11 +410,11 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
         }
     };
     float scale = 1.f;
-    auto keep = [&](const u32x4_t (&r)[V][2], GramTiles<NB> &to) {
+    auto keep = [&](const u32x4_t (&r)[V][2], GramTiles &to) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * (64 * GRAM_WAVES);
-            const int at = TALL ? v / (NB / 8) * Tl::MP + v % (NB / 8) * 16 : v / 8 * Tl::KP + v % 8 * 16;
+            const int at = TALL ? v / (GRAM / 8) * Tl::MP + v % (GRAM / 8) * 16 : v / 8 * Tl::KP + v % 8 * 16;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 u32x4_t w = r[i][p];
@@ -461,7 +465,7 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
                 bf16x8_t b[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
-                    b[p] = operand(sb[p], wn * (NB / 2) + 16 * j, h);
+                    b[p] = operand(sb[p], wn * (GRAM / 2) + 16 * j, h);
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -479,23 +483,296 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
         for (int j = 0; j < TN; ++j)
             *reinterpret_cast<f32x4_t *>(
                 out + static_cast<int64_t>(i0 + wm * (16 * TM) + 16 * i + (lane & 15)) * it.np + j0 +
-                wn * (NB / 2) + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+                wn * (GRAM / 2) + 16 * j + 4 * (lane >> 4)) = acc[i][j];
 }
 
-template <int NB>
 __global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kernel(NsGroup<NsItem> g)
 {
-    __shared__ __align__(16) GramTiles<NB> sa, sb;
+    __shared__ __align__(16) GramTiles sa, sb;
     __shared__ unsigned int red[GRAM_WAVES];
     const Found<NsItem> found = find_item(g, place_on_xcd());
     if (found.it.tall)
-        gram_tile_bf16<true, NB>(found.it, found.block, sa, sb, red);
+        gram_tile_bf16<true>(found.it, found.block, sa, sb, red);
     else
-        gram_tile_bf16<false, NB>(found.it, found.block, sa, sb, red);
+        gram_tile_bf16<false>(found.it, found.block, sa, sb, red);
 }
 
-// The sums of the Gram partials at N places from e.
-template <bool F32, int N>
+// ------------------------------------------------- U and its Gram partial, n <= 64
+// A workgroup has all rows of a stretch of the longer side, so that it forms U, writes it for the
+// last kernel and multiplies it from LDS at once; 128 values of the longer side a turn.
+template <bool F32>
+struct FrontLds {
+    static constexpr int K = 128;
+    // fp32: rows of K values (four places of 16 rows on distinct banks) or K rows of n values (four
+    // rows of 16); bf16: the planes' tiles of 64 values
+    static constexpr int KP = K + 4, MP = SMALL + 16;
+    static constexpr int TILE_BYTES = Tiles<SMALL>::M_BYTES;
+    static_assert(Tiles<SMALL>::M_BYTES >= Tiles<SMALL>::K_BYTES, "a tile either way");
+    static constexpr int BYTES = F32 ? (SMALL * KP > K * MP ? SMALL * KP : K * MP) * 4
+                                     : 2 * K / 64 * TILE_BYTES;
+};
+constexpr int FRONT = 512;
+template <typename T, bool TALL>
+__device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams &p, int block,
+                                              unsigned char *lds)
+{
+    constexpr bool F32 = sizeof(T) == 4;
+    using L = FrontLds<F32>;
+    constexpr int V = SMALL * L::K / 8 / FRONT, PLANE = L::K / 64 * L::TILE_BYTES;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+    const int lr = lane & 15, kq = lane >> 4;
+    const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(block) * it.per_split,
+                  k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
+    const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
+    // (in what the first tile's layout leaves: two workgroups fill a CU's LDS to the last byte)
+    unsigned int *const red =
+        reinterpret_cast<unsigned int *>(lds + (TALL ? 2 * SMALL : Tiles<SMALL>::K_BYTES));
+    static_assert(2 * SMALL + FRONT / 16 <= Tiles<SMALL>::MP &&
+                      Tiles<SMALL>::K_BYTES + FRONT / 16 <= L::TILE_BYTES,
+                  "a word for each wave");
+    const int n = static_cast<int>(TALL ? it.cols : it.rows), nt = (n + 15) / 16;
+    const int64_t l = TALL ? it.rows : it.cols;
+
+    // fp32: tiles wave and wave + 8 on and below the diagonal; bf16: 16 x 32 of the square
+    f64x4_t acc64[2];
+    f32x4_t acc32[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        acc64[r] = f64x4_t{0., 0., 0., 0.};
+        acc32[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    auto tile_of = [](int t, int &i0, int &j0) {
+        const int ti = (t >= 1 ? 1 : 0) + (t >= 3 ? 1 : 0) + (t >= 6 ? 1 : 0);
+        i0 = 16 * ti;
+        j0 = 16 * (t - ti * (ti + 1) / 2);
+    };
+    int exponent = 127;  // of the scale that acc32 is kept at
+    for (int64_t k = k0; k < k1; k += L::K) {
+        const int kc = static_cast<int>(k1 - k < L::K ? k1 - k : L::K);  // whole 64s
+        // place of chunk v of eight: row and column in the matrix
+        auto place = [&](int v, int64_t &r, int64_t &c) {
+            r = TALL ? k + v / 8 : v / (L::K / 8);
+            c = TALL ? v % 8 * 8 : k + v % (L::K / 8) * 8;
+        };
+        auto inside = [&](int v) { return TALL ? v / 8 < kc : v % (L::K / 8) * 8 < kc; };
+        auto lds_at = [&](int v) {
+            if constexpr (F32)
+                return 4 * (TALL ? v / 8 * L::MP + v % 8 * 8 : v / (L::K / 8) * L::KP + v % (L::K / 8) * 8);
+            else if constexpr (TALL)
+                return v / 512 * L::TILE_BYTES + v / 8 % 64 * Tiles<SMALL>::MP + v % 8 * 16;
+            else
+                return v % (L::K / 8) / 8 * L::TILE_BYTES + v / (L::K / 8) * Tiles<SMALL>::KP + v % 8 * 16;
+        };
+        Raw8<T> gr[V];
+        Raw8<float> mr[V];
+        int cnt[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = tid + i * FRONT;
+            int64_t r, c;
+            place(v, r, c);
+            cnt[i] = inside(v) && r < it.rows ? count8(it.cols, c) : 0;
+        }
+        // no chunk that a row's end cuts: all loads at once (no branch round one), from the
+        // matrix's start where there is nothing
+        const bool whole = TALL ? n % 8 == 0 : k + kc <= l || l % 8 == 0;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                int64_t r, c;
+                place(tid + i * FRONT, r, c);
+                const int64_t at = cnt[i] > 0 ? r * it.cols + c : 0;
+                gr[i].load(static_cast<const T *>(it.g) + at, 8);
+                if (it.m != nullptr)
+                    mr[i].load(it.m + at, 8);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                int64_t r, c;
+                place(tid + i * FRONT, r, c);
+                const int64_t at = r * it.cols + c;
+                gr[i].load(static_cast<const T *>(it.g) + at, cnt[i]);
+                if (it.m != nullptr)
+                    mr[i].load(it.m + at, cnt[i]);
+            }
+        }
+        if (k > k0)
+            __syncthreads();  // (the last turn's tiles)
+        unsigned int top = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int v = tid + i * FRONT;
+            if (!inside(v))
+                continue;
+            int64_t r, c;
+            place(v, r, c);
+            float u[8];
+            gr[i].get(u);
+            if (it.m != nullptr) {
+                float m[8];
+                mr[i].get(m);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    m[q] = __fmaf_rn(p.mu, m[q], u[q]);
+                    u[q] = p.nesterov ? __fmaf_rn(p.mu, m[q], u[q]) : m[q];
+                }
+                if (cnt[i] > 0) {
+                    mr[i].set(m);
+                    mr[i].store(it.m_out + r * it.cols + c, cnt[i]);
+                }
+            }
+            if (cnt[i] <= 0)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    u[q] = 0.f;
+            const int64_t at = r * it.cp + c;
+            if constexpr (F32) {
+                float *const o = reinterpret_cast<float *>(it.u) + at;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x4_t x = {u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]};
+                    *reinterpret_cast<f32x4_t *>(o + 4 * q) = x;
+                    *reinterpret_cast<f32x4_t *>(lds + lds_at(v) + 16 * q) = x;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const unsigned int b = abs_bits(u[q]);
+                    top = top > b ? top : b;
+                }
+                u32x4_t w[2];
+                split_planes(u, w);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    *reinterpret_cast<u32x4_t *>(reinterpret_cast<uint16_t *>(it.u) + q * usize + at) = w[q];
+                    *reinterpret_cast<u32x4_t *>(lds + q * PLANE + lds_at(v)) = w[q];
+                }
+            }
+        }
+        if constexpr (F32) {
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int t = wave + 8 * r;
+                if (t >= nt * (nt + 1) / 2)
+                    continue;
+                int i0, j0;
+                tile_of(t, i0, j0);
+                const float *const f = reinterpret_cast<const float *>(lds);
+                for (int kk = 0; kk < kc; kk += 16) {
+                    float a[4], b[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = kk + 4 * q + kq;
+                        a[q] = TALL ? f[at * L::MP + i0 + lr] : f[(i0 + lr) * L::KP + at];
+                        b[q] = TALL ? f[at * L::MP + j0 + lr] : f[(j0 + lr) * L::KP + at];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc64[r] = mfma4(static_cast<double>(a[q]), static_cast<double>(b[q]), acc64[r]);
+                }
+            }
+        } else {
+            // The scale of the sums so far and of this turn: the smaller one (what is far below the
+            // largest values does not count).
+            top = block_max(top, red, FRONT / 64);  // (a barrier: the tiles are there)
+            const int mine = top == 0u ? 127 : range_exponent(top), next = mine < exponent ? mine : exponent;
+            if (next != exponent) {
+                const double ratio = __hiloint2double((1023 + 2 * (next - exponent)) << 20, 0);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc32[r][q] = static_cast<float>(static_cast<double>(acc32[r][q]) * ratio);
+                exponent = next;
+            }
+            if (exponent != 0 && top != 0u) {
+                const float scale = power(exponent);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int v = tid + i * FRONT;
+                    if (!inside(v))
+                        continue;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        u32x4_t *const w = reinterpret_cast<u32x4_t *>(lds + q * PLANE + lds_at(v));
+                        u32x4_t x = *w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = pack_bf16x2(scale * __uint_as_float(x[e] << 16),
+                                               scale * __uint_as_float(x[e] & 0xffff0000u));
+                        *w = x;
+                    }
+                }
+                __syncthreads();
+            }
+            const int i0 = 16 * (wave >> 1), j0 = 32 * (wave & 1);
+            auto operand = [&](int plane, int stage, int r0, int h) {
+                const unsigned char *const tile = lds + plane * PLANE + stage * L::TILE_BYTES;
+                if constexpr (TALL)
+                    return Tiles<SMALL>::columns16(tile, r0, h, lane);
+                else
+                    return Tiles<SMALL>::rows16(tile, r0, h, lane);
+            };
+            for (int stage = 0; stage < kc / 64; ++stage)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bf16x8_t a[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        a[q] = operand(q, stage, i0, h);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        bf16x8_t b[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            b[q] = operand(q, stage, j0 + 16 * r, h);
+#pragma unroll
+                        for (int x = 3; x >= 0; --x)  // the small products first
+                            acc32[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[x & 1], a[x >> 1], acc32[r],
+                                                                               0, 0, 0);
+                    }
+                }
+        }
+    }
+    if constexpr (F32) {
+        double *const out = reinterpret_cast<double *>(it.part) + block * SMALL * SMALL;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = wave + 8 * r;
+            if (t >= nt * (nt + 1) / 2)
+                continue;
+            int i0, j0;
+            tile_of(t, i0, j0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                out[(i0 + d_row(0., q, lane)) * SMALL + j0 + lr] = acc64[r][q];
+        }
+    } else {
+        float *const out = reinterpret_cast<float *>(it.part) + block * SMALL * SMALL;
+        const int i0 = 16 * (wave >> 1), j0 = 32 * (wave & 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<f32x4_t *>(out + (i0 + lr) * SMALL + j0 + 16 * r + 4 * kq) = acc32[r];
+        if (tid == 0)
+            it.tops[block] = static_cast<unsigned int>(exponent);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(FRONT, sizeof(T) == 2 ? 4 : 2) ns_front_kernel(NsGroup<NsInput> g)
+{
+    __shared__ __align__(16) unsigned char lds[FrontLds<sizeof(T) == 4>::BYTES];
+    const Found<NsInput> found = find_item(g, blockIdx.x);
+    if (found.it.tall)
+        front_stretch<T, true>(found.it, g.p, found.block, lds);
+    else
+        front_stretch<T, false>(found.it, g.p, found.block, lds);
+}
+
+// The sums of the Gram partials at N places from e (SCALED: each at a scale of its own).
+template <bool F32, bool SCALED, int N>
 __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)[N])
 {
     typedef Part<F32> vec_t __attribute__((ext_vector_type(N)));
@@ -507,9 +784,11 @@ __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)
 #pragma unroll 8
     for (int z = 0; z < it.splits; ++z) {
         const vec_t v = *reinterpret_cast<const vec_t *>(p + z * size);
+        const double back =
+            SCALED ? __hiloint2double((1023 - 2 * static_cast<int>(it.tops[z])) << 20, 0) : 1.;
 #pragma unroll
         for (int q = 0; q < N; ++q)
-            s[q] += static_cast<double>(v[q]);
+            s[q] += static_cast<double>(v[q]) * back;
     }
 }
 
@@ -523,7 +802,7 @@ struct SmallLds {
 };
 template <int NT, bool F32>
 __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p, unsigned char *lds,
-                                            double *diagonal, unsigned int *red)
+                                            double *diagonal)
 {
     using R = Part<F32>;
     using L = SmallLds<NT, F32>;
@@ -532,12 +811,11 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4;
 
-    const unsigned int top = own_top(it);
     const int gi = tid >> 4, gj = 4 * (tid & 15);
+    const bool below = gi < K && gj >> 4 <= gi >> 4;  // in a tile on or below the diagonal
     double v[4] = {0., 0., 0., 0.};
-    if (gi < K && gj < K)
-        gram_at<F32>(it, gi * SMALL + gj, v);
-    const double scale = F32 ? 1. : static_cast<double>(range_scale(top, red));
+    if (below)
+        gram_at<F32, !F32>(it, gi * SMALL + gj, v);
     if (gi < K && gj == (gi & ~3))
         diagonal[gi] = v[gi & 3];
     __syncthreads();
@@ -545,12 +823,15 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         trace += __shfl_xor(trace, d);
-    // (1 / (|U|_F + eps), and of the scaled U)
-    const double inv = 1. / (sqrt(trace) / scale + static_cast<double>(p.eps)), in = inv / scale;
-    if (gi < K && gj < K)
+    const double inv = 1. / (sqrt(trace) + static_cast<double>(p.eps));
+    if (below)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            m[0][gi][gj + q] = static_cast<R>(v[q] * in * in);
+            if (gj + q <= gi) {
+                const R x = static_cast<R>(v[q] * inv * inv);
+                m[0][gi][gj + q] = x;
+                m[0][gj + q][gi] = x;
+            }
     __syncthreads();
 
     // Matrices 0 to 3: G, P, Q and H = P G.  Three stages a step,
@@ -649,16 +930,15 @@ __global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup<NsItem> g)
 {
     __shared__ __align__(16) unsigned char lds[sizeof(SmallLds<SMALL / 16, F32>)];
     __shared__ double diagonal[SMALL];
-    __shared__ unsigned int red[16];
     const NsItem &it = g.it[blockIdx.x];
     if (it.n > 48)
-        small_steps<4, F32>(it, g.p, lds, diagonal, red);
+        small_steps<4, F32>(it, g.p, lds, diagonal);
     else if (it.n > 32)
-        small_steps<3, F32>(it, g.p, lds, diagonal, red);
+        small_steps<3, F32>(it, g.p, lds, diagonal);
     else if (it.n > 16)
-        small_steps<2, F32>(it, g.p, lds, diagonal, red);
+        small_steps<2, F32>(it, g.p, lds, diagonal);
     else
-        small_steps<1, F32>(it, g.p, lds, diagonal, red);
+        small_steps<1, F32>(it, g.p, lds, diagonal);
 }
 
 // ------------------------------------------------------- the n x n part, larger
@@ -672,7 +952,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
     if (i >= it.np || j > i)
         return;
     double s[1];
-    gram_at<F32>(it, e, s);
+    gram_at<F32, false>(it, e, s);
     Part<F32> *const G = reinterpret_cast<Part<F32> *>(it.mat);
     G[e] = static_cast<Part<F32>>(s[0]);
     G[static_cast<int64_t>(j) * it.np + i] = static_cast<Part<F32>>(s[0]);
@@ -886,7 +1166,8 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
     const int np = it.np;
     const int64_t qsize = static_cast<int64_t>(np) * np, usize = static_cast<int64_t>(it.rp) * it.cp;
 
-    constexpr int QV = Q_ROWS * 8 / (64 * FINAL_WAVES), UV = 128 * 8 / (64 * FINAL_WAVES);  // 16-byte chunks a thread
+    // 16-byte chunks a thread
+    constexpr int QV = Q_ROWS * 8 / (64 * FINAL_WAVES), UV = 128 * 8 / (64 * FINAL_WAVES);
     u32x4_t qr[QV][P];
     Raw8<float> uf[UV];
     u32x4_t up[UV][2];
@@ -1033,7 +1314,8 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
 }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(64 * FINAL_WAVES, sizeof(T) == 2 ? FINAL_WAVES / 2 : FINAL_WAVES / 4) ns_final_kernel(NsGroup<NsOutput> g)
+__global__ void __launch_bounds__(64 * FINAL_WAVES, FINAL_WAVES / (sizeof(T) == 2 ? 2 : 4))
+    ns_final_kernel(NsGroup<NsOutput> g)
 {
     __shared__ __align__(16) unsigned char lds[FinalLds<T, NB>::BYTES];
     const Found<NsOutput> found = find_item(g, place_on_xcd());
@@ -1063,10 +1345,9 @@ Sides sides(int64_t rows, int64_t cols)
     return s;
 }
 
-int64_t gram_tile(int bf16, int64_t np) { return bf16 && np > SMALL ? 128 : 64; }
 int64_t gram_tiles(int bf16, int64_t np)
 {
-    const int64_t nt = np / gram_tile(bf16, np);
+    const int64_t nt = np / (bf16 ? GRAM : TILE);
     return nt * (nt + 1) / 2;
 }
 int64_t prepare_groups(int64_t rp, int64_t cp)
@@ -1086,7 +1367,7 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
 {
     Chunk c;
     c.first = first;
-    int64_t per_split = 0;
+    int64_t per_split = 0, per_front = 0;
     auto fill = [&](NsItem &it, const NsMatrix &m, size_t off) {
         const Sides s = sides(m.rows, m.cols);
         it.tall = s.tall;
@@ -1094,7 +1375,8 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         it.np = static_cast<int>(s.np);
         it.rp = static_cast<int>(s.rp);
         it.cp = static_cast<int>(s.cp);
-        it.per_split = static_cast<int>(per_split < s.lp ? per_split : s.lp);
+        const int64_t share = s.np > SMALL ? per_split : per_front;
+        it.per_split = static_cast<int>(share < s.lp ? share : s.lp);
         it.splits = static_cast<int>((s.lp + it.per_split - 1) / it.per_split);
         auto take = [&](size_t bytes) {
             const size_t at = off;
@@ -1103,7 +1385,9 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         };
         const size_t square = static_cast<size_t>(s.np) * s.np, real = bf16 ? 4 : 8;
         it.u = take(static_cast<size_t>(s.rp) * s.cp * 4);
-        it.top_count = bf16 ? static_cast<int>(prepare_groups(s.rp, s.cp)) : 0;
+        it.top_count = !bf16          ? 0
+                       : s.np > SMALL ? static_cast<int>(prepare_groups(s.rp, s.cp))
+                                      : it.splits;
         it.tops = reinterpret_cast<unsigned int *>(take(it.top_count * sizeof(unsigned int)));
         it.part = take(it.splits * square * real);
         it.mat = take(s.np > SMALL ? 6 * square * real : 0);
@@ -1112,16 +1396,23 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         return off;
     };
     // The Gram products of the set as about 512 workgroups of equal length (1024 in 64 bits, of
-    // half the waves), of 64 values of the longer side each at least; a matrix has at most 64 shares.
+    // half the waves), of 64 values of the longer side each at least; a matrix has at most 64
+    // shares, or 32 in 64 bits, or where one workgroup adds them (n <= 64: 16 KiB each).
     auto split = [&](int n) {
-        int64_t work = 0, longest = 0;
+        int64_t work = 0, longest = 0, work_front = 0, longest_front = 0;
         for (int i = first; i < first + n; ++i) {
             const Sides s = sides(mats[i].rows, mats[i].cols);
-            work += gram_tiles(bf16, s.np) * s.lp;
-            longest = s.lp > longest ? s.lp : longest;
+            if (s.np > SMALL) {
+                work += gram_tiles(bf16, s.np) * s.lp;
+                longest = s.lp > longest ? s.lp : longest;
+            } else {
+                work_front += s.lp;
+                longest_front = s.lp > longest_front ? s.lp : longest_front;
+            }
         }
-        const int64_t even = work / (bf16 ? 512 : 1024), least = (longest + 63) / 64;
-        per_split = up_to(even > least ? even : least, 64);
+        auto share = [](int64_t even, int64_t least) { return up_to(even > least ? even : least, 64); };
+        per_split = bf16 ? share(work / 512, (longest + 63) / 64) : share(work / 1024, (longest + 31) / 32);
+        per_front = share(work_front / 512, (longest_front + 31) / 32);
         size_t off = 0;
         for (int i = 0; i < n; ++i)
             off = fill(c.it[i], mats[first + i], off);
@@ -1161,7 +1452,6 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
         if (e_ != hipSuccess)                  \
             return e_;                         \
     } while (0)
-    auto all = [](const NsItem &) { return true; };
     auto small = [](const NsItem &i) { return i.np == SMALL; };
     auto large = [](const NsItem &i) { return i.np > SMALL; };
     int n;
@@ -1170,26 +1460,27 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
         for (int i = 0; i < c.count; ++i) {
             const NsItem &it = c.it[i];
             const NsMatrix &m = mats[c.first + i];
-            in[i] = NsInput{it.u, it.tops, m.g, m.m, m.m_out, m.rows, m.cols, it.rp, it.cp};
+            in[i] = NsInput{it.u,   it.part, it.tops, m.g,   m.m,     m.m_out,
+                            m.rows, m.cols,  it.rp,   it.cp, it.tall, it.per_split};
         }
         NsGroup<NsInput> g;
         g.p = p;
-        n = group_of(g, in, c, all, [](const NsItem &i) { return prepare_groups(i.rp, i.cp); });
-        NS_LAUNCH((ns_prepare_kernel<T>), dim3(n), dim3(THREADS), 0, st, g);
+        n = group_of(g, in, c, small, [](const NsItem &i) { return i.splits; });
+        if (n > 0)
+            NS_LAUNCH((ns_front_kernel<T>), dim3(n), dim3(FRONT), 0, st, g);
+        n = group_of(g, in, c, large, [](const NsItem &i) { return prepare_groups(i.rp, i.cp); });
+        if (n > 0)
+            NS_LAUNCH((ns_prepare_kernel<T>), dim3(n), dim3(THREADS), 0, st, g);
     }
     NsGroup<NsItem> g;
     g.p = p;
     auto gram_groups = [](const NsItem &i) { return gram_tiles(!F32, i.np) * i.splits; };
-    if constexpr (F32) {
-        n = group_of(g, c.it, c, all, gram_groups);
-        NS_LAUNCH(ns_gram_f64_kernel, dim3(n), dim3(THREADS), 0, st, g);
-    } else {
-        n = group_of(g, c.it, c, small, gram_groups);
-        if (n > 0)
-            NS_LAUNCH((ns_gram_kernel<64>), dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
-        n = group_of(g, c.it, c, large, gram_groups);
-        if (n > 0)
-            NS_LAUNCH((ns_gram_kernel<128>), dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
+    n = group_of(g, c.it, c, large, gram_groups);
+    if (n > 0) {
+        if constexpr (F32)
+            NS_LAUNCH(ns_gram_f64_kernel, dim3(n), dim3(THREADS), 0, st, g);
+        else
+            NS_LAUNCH(ns_gram_kernel, dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
     }
     n = group_of(g, c.it, c, small, [](const NsItem &) { return 1; });
     if (n > 0)

@@ -67,6 +67,26 @@ def test_any_magnitude(power, dt):
         check((U.double() * 2.0 ** power).to(dt), eps=0.0)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("powers", [(-100, 0, 90), (90, 0, -100), (None, -100, -100), (None, None, 0),
+                                    (0, -100, None), (-100, -90, -80)])
+def test_magnitudes_that_change_along_the_longer_side(powers, dt):
+    """Whole stretches far below the others, or of zeros."""
+    for n, length in ((30, 9000), (61, 2050), (150, 2100)):
+        U = matrix(n, n, length, dt).double()
+        for k, power in enumerate(powers):
+            U[:, length * k // 3:length * (k + 1) // 3] *= 0.0 if power is None else 2.0 ** power
+        check(U.to(dt), eps=0.0)
+        check(U.T.contiguous().to(dt), eps=0.0)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n,length", [(20, 40001), (64, 33000), (33, 40000)])
+def test_long_and_narrow(n, length, dt):
+    check(matrix(n, n, length, dt, fall=0.2))
+    check(matrix(n, length, n, dt, fall=0.2))
+
+
 def test_singular_values_come_close_to_one():
     """Each one becomes what the steps make of it (two matrices' singular values differ by no
     more than the matrices do)."""
