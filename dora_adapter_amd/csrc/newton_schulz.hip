@@ -968,7 +968,9 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 {
     using R = Part<F32>;
     constexpr int PLANES = F32 ? 3 : 2;
-    __shared__ R red[POLY_WAVES][POLY][POLY + 1];
+    constexpr int OPERANDS = POLY_WAVES * 2 * POLY * 144, SUMS = POLY_WAVES * POLY * (POLY + 1) * sizeof(R);
+    __shared__ __align__(16) unsigned char lds[OPERANDS > SUMS ? OPERANDS : SUMS];
+    auto &red = *reinterpret_cast<R(*)[POLY_WAVES][POLY][POLY + 1]>(lds);
     __shared__ double tr[POLY_WAVES];
     __shared__ unsigned int tops[POLY_WAVES];
     const Found<NsItem> found = find_item(g, place_on_xcd());
@@ -1041,37 +1043,63 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 #pragma unroll
         for (int y = 0; y < 2; ++y)
             acc[x][y] = Quad<R>{0, 0, 0, 0};
-    // A wave's share of K (whole 16s, next to each other: of a line's halves one load finds what the
-    // other brought), 16 values a turn, four consecutive ones a lane; three turns' loads at once:
-    // another CU wrote them, and each wait is one for its cache
-    constexpr int TURN = 16, AHEAD = 3;
-    const int k1 = (wave + 1) * (np / POLY_WAVES);
-    for (int k0 = wave * (np / POLY_WAVES); k0 < k1; k0 += AHEAD * TURN) {
-        Quad<R> a[AHEAD][2], b[AHEAD][2];
+    // Each wave takes every eighth 128-byte line of the 32 rows and the 32 columns' rows: whole lines
+    // (half of them an instruction took 3 us longer to come, from caches that other CUs wrote), two
+    // turns' on their way at once, turned in LDS of the wave's own into operands of 16 rows.
+    constexpr int LINE = 128 / sizeof(R), PITCH = 144;  // (16 bytes of 16 rows on distinct banks)
+    unsigned char *const mine = lds + wave * 64 * PITCH;
+    const int lines = np / LINE;
+    const int own = __builtin_amdgcn_readfirstlane(wave);
+    const unsigned int in_line = (lane >> 3) * np + (lane & 7) * (16 / sizeof(R));
+    u32x4_t v[2][8];
+    auto fetch = [&](u32x4_t (&to)[8], int line) {
 #pragma unroll
-        for (int t = 0; t < AHEAD; ++t) {
-            const int k = k0 + t * TURN < k1 ? k0 + t * TURN : k0;
+        for (int i = 0; i < 8; ++i) {  // (uniform addresses and the lane's place: fewer registers)
+            const R *const from = (i < 4 ? X + static_cast<int64_t>(i0 + 8 * i) * np
+                                         : Y + static_cast<int64_t>(j0 + 8 * (i - 4)) * np) + line * LINE;
+            to[i] = *reinterpret_cast<const u32x4_t *>(from + in_line);
+        }
+    };
+    auto use = [&](const u32x4_t (&from)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<u32x4_t *>(mine + (8 * i + (lane >> 3)) * PITCH + (lane & 7) * 16) = from[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int t = 0; t < LINE / 16; ++t) {  // 16 values of K, four consecutive ones a lane
+            Quad<R> a[2], b[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                a[t][q] = *reinterpret_cast<const Quad<R> *>(
-                    X + static_cast<int64_t>(i0 + 16 * q + lr) * np + k + 4 * kq);
-                b[t][q] = *reinterpret_cast<const Quad<R> *>(
-                    Y + static_cast<int64_t>(j0 + 16 * q + lr) * np + k + 4 * kq);
+                const int at = (16 * t + 4 * kq) * static_cast<int>(sizeof(R));
+                a[q] = *reinterpret_cast<const Quad<R> *>(mine + (16 * q + lr) * PITCH + at);
+                b[q] = *reinterpret_cast<const Quad<R> *>(mine + (32 + 16 * q + lr) * PITCH + at);
             }
-        }
-#pragma unroll
-        for (int t = 0; t < AHEAD; ++t) {
-            if (k0 + t * TURN >= k1)
-                break;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        acc[x][y] = mfma4(a[t][x][s], b[t][y][s], acc[x][y]);
+                        acc[x][y] = mfma4(a[x][s], b[y][s], acc[x][y]);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    if (own < lines) {
+        fetch(v[0], own);
+        fetch(v[1], own + POLY_WAVES < lines ? own + POLY_WAVES : own);
     }
+    for (int line = own; line < lines; line += 2 * POLY_WAVES) {
+        use(v[0]);
+        if (line + 2 * POLY_WAVES < lines)
+            fetch(v[0], line + 2 * POLY_WAVES);
+        if (line + POLY_WAVES < lines)
+            use(v[1]);
+        if (line + 3 * POLY_WAVES < lines)
+            fetch(v[1], line + 3 * POLY_WAVES);
+    }
+    __syncthreads();  // (the sums lie where the operands were)
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
