@@ -240,13 +240,14 @@ struct Sums {
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                acc[i][j] = part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     // step `step` of a line: the products of 32 columns, and the scale where a group ends
     template <int PER, int P>
     __device__ __forceinline__ void step(const bf16x8_t (&x)[TM][P], const unsigned int (&c)[NT][4],
                                          const Line<NT, PER> &l, int step)
     {
+        constexpr int EVERY = STEPS / PER;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const bf16x8_t w = weights8(c[j][step % 4]);
@@ -254,9 +255,10 @@ struct Sums {
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int p = P - 1; p >= 0; --p)  // the smallest parts first
-                    part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i][p], w, part[i][j], 0, 0, 0);
+                    part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        x[i][p], w, step % EVERY == 0 && p == P - 1 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : part[i][j],
+                        0, 0, 0);
         }
-        constexpr int EVERY = STEPS / PER;
         if ((step + 1) % EVERY == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -264,10 +266,8 @@ struct Sums {
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 4; ++q)
                         acc[i][j][q] = __fmaf_rn(by, part[i][j][q], acc[i][j][q]);
-                        part[i][j][q] = 0.f;
-                    }
             }
         }
     }
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(W * 64) linear_fourbit_kernel(FourbitArgs a)
 
 // More tokens: CW waves a K group take 16 NT channels each and share the tokens' line, which lies
 // in LDS, the next one on its way; KG such groups split K.  (d_in of a line at least.)
-template <typename T, int TM, int NT, int PER, int CW, int KG, int D>
+template <typename T, int TM, int NT, int PER, int CW, int KG, int D, int XD>
 __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(FourbitArgs a)
 {
     constexpr int P = planes<T>;
@@ -424,14 +424,22 @@ __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(Four
     struct Tokens {
         Raw8<T> v[LOADS];
     };
+    // (uniform addresses and the thread's place in bytes, of 32 bits: 64 rows below 2^23 at most)
+    const T *const xrows = static_cast<const T *>(a.x) + t0 * a.d_in;
+    unsigned int place[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int v = tid + i * CW * 64, r = v / 32;
+        place[i] = sizeof(T) * ((r < tokens ? r : tokens - 1) * static_cast<unsigned int>(a.d_in) +
+                                8 * (v % 32));
+    }
     auto fetch = [&](Tokens &x, int64_t line, auto WHOLE) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int v = tid + i * CW * 64, r = v / 32;
-            const int64_t k = line * LINE + 8 * (v % 32);
-            const T *p = static_cast<const T *>(a.x) + (t0 + (r < tokens ? r : tokens - 1)) * a.d_in;
-            x.v[i].template load<true>(p + k, WHOLE() ? 8 : count8(a.d_in, k));
-        }
+        for (int i = 0; i < LOADS; ++i)
+            x.v[i].template load<true>(reinterpret_cast<const T *>(
+                                           reinterpret_cast<const unsigned char *>(xrows + line * LINE) +
+                                           place[i]),
+                                       WHOLE() ? 8 : count8(a.d_in, line * LINE + 8 * (tid % 32)));
     };
     using Yes = std::true_type;
     // (the next whole line, or the last one again, with no branch; the row's end apart)
@@ -476,18 +484,20 @@ __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(Four
             }
         }
     };
-    // Two lines of the tokens are on their way: loads return in order, so that a wait for them is
-    // one for all codes loaded before them too.
-    Tokens x[2];
+    // XD lines of the tokens are on their way.  Loads return in order, so that a wait for them is one
+    // for all codes loaded before them too: two lines where few waves are there to fill it, one
+    // where the registers of more waves are worth more.
+    Tokens x[XD];
     fetch_next(x[0], kg);
-    fetch_next(x[1], kg + KG);
+    if constexpr (XD == 2)
+        fetch_next(x[1], kg + KG);
     keep(x[0], 0);
     __syncthreads();
     for (int64_t r0 = 0; r0 < rounds; r0 += 2) {
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
             const int64_t line = kg + (r0 + d) * KG;
-            fetch_next(x[d], line + 2 * KG);
+            fetch_next(x[d % XD], line + XD * KG);
             if (line < whole) {
                 products(ring[d % D], d);
             } else if (line < lines && mine) {
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(Four
             }
             const int64_t ahead = line + static_cast<int64_t>(D) * KG;
             codes.load(ring[d % D], mine ? tile : 0, ahead, mine && ahead < whole);
-            keep(x[d ^ 1], d ^ 1);
+            keep(x[(d ^ 1) % XD], d ^ 1);
             __syncthreads();
         }
     }
@@ -546,23 +556,25 @@ hipError_t launch_few(const FourbitArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <typename T, int TM, int NT, int PER, int CW, int KG, int D>
+template <typename T, int TM, int NT, int PER, int CW, int KG, int D, int XD = 2>
 hipError_t launch_shared(const FourbitArgs &a, hipStream_t st)
 {
     constexpr size_t LDS = 2 * KG * planes<T> * 16 * TM * LINE * 2 + KG * CW * NT * 2048;
     static_assert(LDS <= 160 * 1024, "LDS");
     const dim3 grid(static_cast<unsigned>((a.d_out + CW * 16 * NT - 1) / (CW * 16 * NT)),
                     static_cast<unsigned>((a.T + 16 * TM - 1) / (16 * TM)));
-    hipLaunchKernelGGL((linear_fourbit_shared_kernel<T, TM, NT, PER, CW, KG, D>), grid,
+    hipLaunchKernelGGL((linear_fourbit_shared_kernel<T, TM, NT, PER, CW, KG, D, XD>), grid,
                        dim3(CW * KG * 64), 0, st, a);
     return hipGetLastError();
 }
 
 // Up to four tokens whose rows fit in LDS, and rows of less than a line, take the first kernel.
 // The other one's tile is the widest that makes 192 workgroups (us at 14336 channels of 4096, 24
-// tokens: 64 channels 14, 128 19, 32 20; at 8192 of 8192: 32 channels 18, 64 23, 128 34); 33 to
-// 64 tokens over many channels share a read of the codes (28672 of 8192: 59, two blocks of 32
-// tokens 74).
+// tokens: 64 channels 14, 128 19, 32 20; at 8192 of 8192: 32 channels 18, 64 23, 128 34), with
+// the K groups that LDS holds (64 channels of 14336, 32 tokens: four 36 us, two 40; 128 channels of
+// 8192, 24 tokens, eight waves of 16 channels in two groups 39.5, four of 32 in two 42); 33 to
+// 64 tokens over many channels share a read of the codes (28672 of 8192, 48 tokens: four waves of
+// 32 channels in two groups 53, eight of 16 in one 59, two blocks of 32 tokens 74).
 template <typename T, int PER>
 hipError_t launch_per(const FourbitArgs &a, hipStream_t st)
 {
@@ -581,11 +593,11 @@ hipError_t launch_per(const FourbitArgs &a, hipStream_t st)
             return fills(64, 16) ? launch_shared<T, 1, 1, PER, 4, 2, 2>(a, st)
                                  : launch_shared<T, 1, 1, PER, 2, 4, 1>(a, st);
         if (a.T > 32 && fills(128, 64))
-            return launch_shared<T, 4, 1, PER, 8, 1, 1>(a, st);
+            return launch_shared<T, 4, 2, PER, 4, 2, 1, 1>(a, st);
         if (fills(128, 32))
-            return launch_shared<T, 2, 2, PER, 4, 2, 2>(a, st);
+            return launch_shared<T, 2, 1, PER, 8, 2, 1, 1>(a, st);
         if (fills(64, 32))
-            return launch_shared<T, 2, 1, PER, 4, 2, 1>(a, st);
+            return launch_shared<T, 2, 1, PER, 4, 4, 1, 1>(a, st);
         return launch_shared<T, 2, 1, PER, 2, 4, 1>(a, st);
     }
 }
