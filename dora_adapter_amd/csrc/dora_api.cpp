@@ -6,7 +6,8 @@
 // and the norm-detached backward.  Every step of the computation runs in
 // the HIP kernels: products in gemm_bf16.hip, gemm_bf16_any.hip, gemm_dma_cfg.hip and
 // gemm_f32.hip, of int8 operands in gemm_i8.hip, gemm_i8_dma.hip, gemm_i8_rows.hip and
-// gemm_rows8.hip, the rest in elementwise.hip and rows8.hip.
+// gemm_rows8.hip, of 4-bit weights in gemm_fourbit.hip, the rest in elementwise.hip, rows8.hip,
+// fourbit.hip, block_norm.hip and newton_schulz.hip.
 #include <stdio.h>
 #include <stdarg.h>
 #include <stdlib.h>

@@ -1,5 +1,6 @@
 // fourbit.hip - rows to 4 bits and back (gfx950).  Both are bound by memory traffic, a thread
-// takes eight consecutive columns at a time: 16 bytes of bf16, four of codes.
+// takes eight consecutive columns at a time: 16 bytes of bf16, four of codes.  28672 x 8192 in
+// bf16: 108 us to codes (5.5 TB/s), 102 back (5.8).
 #include "around.hpp"
 #include "fourbit.hpp"
 

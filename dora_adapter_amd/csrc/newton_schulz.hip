@@ -6,7 +6,8 @@
 // Every factor is a polynomial of the first G, so the steps run on n x n matrices alone,
 //     Q <- P(G) Q,   G <- P(G) G P(G),
 // between one product along L, G = U U^T, and another, O = Q U / (|U|_F + eps), whose epilogue is
-// the update: 4 n^2 L flops instead of 4 n^2 L a step, and U is read twice.
+// the update: 4 n^2 L flops instead of 4 n^2 L a step, and U is read twice.  Where n comes near L
+// that is no gain (4096 x 4096, five steps: bf16 14.1 ms, the literal steps 14.3; fp32 27.6).
 //
 // G holds squares of singular values, so that an error of 2^-24 of its largest one would move the
 // small ones' directions by 2^-24 / (2 sigma^2), where the literal steps in fp32 move them by
@@ -16,7 +17,9 @@
 // with fp32 sums.  bf16 matrices, whose output's 8 bits leave room for 1e-4 of its norm, take two
 // numbers (16 bits) there and for G, and have their n x n part in fp32.
 //
-// Up to 40 matrices share each launch.
+// Up to 40 matrices share each launch.  Measured: a step of the factors 384 x 8192 and 28672 x 384
+// in bf16 234 us (nineteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
+// (three), 37 x 1027 in fp32 36 us (three).
 #include <climits>
 #include <type_traits>
 
@@ -160,6 +163,7 @@ __device__ __forceinline__ void split_planes(const float (&v)[8], u32x4_t (&w)[P
 }
 
 // ------------------------------------------------------------- U and the momentum
+// Bound by memory traffic: 6 bytes an element in, 8 out (14.2 million in bf16: 39 us, 5.1 TB/s).
 constexpr int PREP_VPT = 4;
 template <typename T>
 __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
@@ -264,7 +268,8 @@ __device__ __forceinline__ float range_scale(unsigned int top, unsigned int *red
 // ------------------------------------------------------------------- G = U U^T
 // fp32 matrices: 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L
 // at a time straight into registers.  An MFMA takes four of them: of a wide matrix a lane's
-// eight consecutive ones give it one each time, of a tall one they are four rows.
+// eight consecutive ones give it one each time, of a tall one they are four rows.  Bound by the
+// matrix cores' 64-bit rate (72 TFLOP/s in a large product).
 __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
 {
     const Found<NsItem> found = find_item(g, place_on_xcd());
@@ -371,7 +376,9 @@ struct Tiles {
 
 // bf16 matrices: both planes of both operands, all four products, in fp32 over a share of L (the
 // shares are added in 64 bits).  128 x 128 tiles on and below the diagonal, eight waves (4 x 2),
-// 64 values of L a stage, the next one on its way.
+// 64 values of L a stage, the next one on its way.  Two workgroups a CU by registers and LDS, so
+// that one's loads pass under the other's products; bound by what is left of the loads' round
+// trips (36 us for 57 MB and 29 GFLOP of products, four waves of 64 x 64 42).
 constexpr int GRAM_WAVES = 8, FINAL_WAVES = 8;  // two in each row
 using GramTiles = unsigned char[2][Tiles<GRAM>::K_BYTES > Tiles<GRAM>::M_BYTES ? Tiles<GRAM>::K_BYTES
                                                                             : Tiles<GRAM>::M_BYTES];
@@ -499,7 +506,9 @@ __global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kerne
 
 // ------------------------------------------------- U and its Gram partial, n <= 64
 // A workgroup has all rows of a stretch of the longer side, so that it forms U, writes it for the
-// last kernel and multiplies it from LDS at once; 128 values of the longer side a turn.
+// last kernel and multiplies it from LDS at once; 128 values of the longer side a turn (256, at
+// half the workgroups a CU: 32 us against 28 for 28 matrices of 64 x 4096; a kernel for U and one for
+// its product: 37).  Bound by memory traffic, 6 bytes an element in and 8 out (3.7 TB/s).
 template <bool F32>
 struct FrontLds {
     static constexpr int K = 128;
@@ -794,7 +803,9 @@ __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)
 
 // ------------------------------------------------------- the n x n part, n <= 64
 // One workgroup a matrix, everything in LDS; a wave for each 16 x 16 tile on and below the
-// diagonal, whose operands are all on their way before the first product.
+// diagonal, whose operands are all on their way before the first product.  Bound by the latency of
+// the chain, 14 products of five steps: 1.5 us each at n = 64 in fp32, of which the CU's matrix
+// rate is 0.8, and 1.4 at n = 37 in fp64.
 template <int NT, bool F32>
 struct SmallLds {
     static constexpr int PITCH = 16 * NT + (F32 ? 2 : 4);  // 16 bytes of 16 rows on distinct banks
@@ -962,7 +973,9 @@ __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
 //   0  P = a I + b G + c G G    1  H = P G, and Q = P Q    2  G = H P    3  Q = P Q
 // (Q in the first step: P).  G is not scaled in place: the first step's products take it by
 // 1 / |U|^2, which is formed from its diagonal.  Matrices 4 and 5 are the other G and Q.  The last
-// Q goes into planes.
+// Q goes into planes.  Bound by latency where n is a few hundred (384: 6.2 us a product, 9.2 for
+// two; of a workgroup's 5 us the arguments take 0.5, the operands' way from memory 1.1 to 2.3, the
+// products 1.2, the sum over the waves 0.7).
 template <int OP, bool F32>
 __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem> g, int step)
 {
@@ -1158,7 +1171,9 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 // ------------------------------------------------------------- O = Q U (or U Q)
 // Tiles of NB values of the shorter side by 128 of the longer one, eight waves (4 x 2), 64 values
 // of K (the shorter side) a stage, the next one on its way.  The tile goes through LDS, so that
-// the update reads and writes whole lines.
+// the update reads and writes whole lines.  Bound like the Gram product (52 us for 85 MB read, 28
+// written and 33 GFLOP of products; four waves of 64 x 64 55, rows of the update straight from the
+// accumulators 67).
 template <typename T, int NB>
 struct FinalLds {
     static constexpr int P = sizeof(T) == 2 ? 2 : 3;
