@@ -51,8 +51,8 @@ struct NsItem {
                          // shorter side to 64 each partial's scale, as its exponent
     char *part;          // Gram partials [splits, np, np], tiles on and below the diagonal
     char *mat;           // G, P, Q, H and the other G and Q [np, np] (larger matrices)
-    double *scal;        // 1 / (|U|_F + eps), and what makes the first G of U U^T
-    uint16_t *q;         // planes of Q / (|U|_F + eps), [planes, np, np]
+    double *scal;        // what makes the planes of Q, the first G of U U^T, and what U meets
+    uint16_t *q;         // planes of Q / (|U|_F + eps) times a power of two, [planes, np, np]
     int n, np;           // the shorter side, padded to 64 or to 128s
     int tall;            // rows > cols
     int rp, cp;          // rows and columns as padded (the longer side to 128s)
@@ -71,6 +71,7 @@ struct NsInput {  // what the first kernel reads and writes
 struct NsOutput {  // what the last kernel reads and writes
     const char *u;
     const uint16_t *q;
+    const double *scal;
     const void *p;
     void *out;
     int64_t rows, cols;
@@ -123,6 +124,28 @@ __device__ __forceinline__ int place_on_xcd()
     return xcd * each + (xcd < more ? xcd : more) + (b >> 3);
 }
 
+// 1 / (|U|_F + eps), and the power of two that goes from it to U where the norm is so far from one
+// that planes of Q times it would leave fp32's range (O is Q times it times U).  No U, no O.
+struct NormScale {
+    double inv;  // of |U|_F + eps
+    int s;
+    __device__ __forceinline__ static double power(int e)
+    {
+        return __hiloint2double((1023 + e) << 20, 0);
+    }
+    __device__ __forceinline__ double for_q() const { return inv * power(s); }
+    __device__ __forceinline__ double for_u() const { return power(-s); }
+};
+__device__ __forceinline__ NormScale norm_scale(double norm, double eps)
+{
+    const double t = norm + eps;
+    const int e = ((__double2hiint(t) >> 20) & 0x7ff) - 1023;  // (zero -1023, infinity and NaN 1024)
+    NormScale n;
+    n.inv = norm == 0. && eps > 0. ? 0. : 1. / t;
+    n.s = e < -1000 || e > 1000 || (e > -60 && e < 60) ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
+    return n;
+}
+
 template <bool F32>
 using Part = std::conditional_t<F32, double, float>;
 __device__ __forceinline__ f64x4_t mfma4(double a, double b, f64x4_t c)
@@ -138,6 +161,15 @@ __device__ __forceinline__ int d_row(double, int q, int lane) { return 4 * q + (
 __device__ __forceinline__ int d_row(float, int q, int lane) { return 4 * (lane >> 4) + q; }
 template <typename R>
 using Quad = std::conditional_t<sizeof(R) == 8, f64x4_t, f32x4_t>;
+
+// eight bf16 numbers times a power of two
+__device__ __forceinline__ u32x4_t scaled_bf16(u32x4_t w, float scale)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        w[q] = pack_bf16x2(scale * __uint_as_float(w[q] << 16), scale * __uint_as_float(w[q] & 0xffff0000u));
+    return w;
+}
 
 // v as P bf16 numbers whose sum it is (to 16 bits with two of them, 24 with three)
 template <int P>
@@ -425,12 +457,8 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 u32x4_t w = r[i][p];
-                if (scale != 1.f) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        w[q] = pack_bf16x2(scale * __uint_as_float(w[q] << 16),
-                                           scale * __uint_as_float(w[q] & 0xffff0000u));
-                }
+                if (scale != 1.f)
+                    w = scaled_bf16(w, scale);
                 *reinterpret_cast<u32x4_t *>(&to[p][at]) = w;
             }
         }
@@ -706,12 +734,7 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         u32x4_t *const w = reinterpret_cast<u32x4_t *>(lds + q * PLANE + lds_at(v));
-                        u32x4_t x = *w;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = pack_bf16x2(scale * __uint_as_float(x[e] << 16),
-                                               scale * __uint_as_float(x[e] & 0xffff0000u));
-                        *w = x;
+                        *w = scaled_bf16(*w, scale);
                     }
                 }
                 __syncthreads();
@@ -834,7 +857,10 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         trace += __shfl_xor(trace, d);
-    const double inv = 1. / (sqrt(trace) + static_cast<double>(p.eps));
+    const NormScale norm = norm_scale(sqrt(trace), static_cast<double>(p.eps));
+    const double inv = norm.inv;
+    if (tid == 0)
+        it.scal[2] = norm.for_u();
     if (below)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -927,7 +953,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
         float w[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)  // (zeros past n's tiles: U is zero there, too)
-            w[q] = i < K && j < K ? static_cast<float>(static_cast<double>(Q[i][j + q]) * inv) : 0.f;
+            w[q] = i < K && j < K ? static_cast<float>(static_cast<double>(Q[i][j + q]) * norm.for_q()) : 0.f;
         u32x4_t planes[PLANES];
         split_planes(w, planes);
 #pragma unroll
@@ -1024,7 +1050,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
     const int lr = lane & 15, kq = lane >> 4, i0 = ti * POLY, j0 = tj * POLY;
 
     // the first G's scale
-    double scaled = 1., inv = 1.;
+    double scaled = 1., for_q = 1.;
     if (step == 0 && OP == 0) {
         const unsigned int top = F32 ? 0u : own_top(it);
         double s = 0.;
@@ -1040,11 +1066,13 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         s = tr[0];
         for (int w = 1; w < POLY_WAVES; ++w)
             s += tr[w];
-        inv = 1. / (sqrt(s) / scale + static_cast<double>(g.p.eps));
-        scaled = inv / scale * (inv / scale);
+        const NormScale norm = norm_scale(sqrt(s) / scale, static_cast<double>(g.p.eps));
+        scaled = norm.inv / scale * (norm.inv / scale);
+        for_q = norm.for_q();
         if (ti == 0 && tid == 0) {
-            it.scal[0] = inv;
+            it.scal[0] = for_q;
             it.scal[1] = scaled;
+            it.scal[2] = norm.for_u();
         }
     } else if (step == 0) {
         scaled = it.scal[1];
@@ -1126,7 +1154,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
     auto put = [&](int i, int j, R x) {
         const int64_t at = static_cast<int64_t>(i) * np + j;
         if (planes) {
-            float r = static_cast<float>(static_cast<double>(x) * (OP == 0 ? inv : it.scal[0]));
+            float r = static_cast<float>(static_cast<double>(x) * (OP == 0 ? for_q : it.scal[0]));
 #pragma unroll
             for (int k = 0; k < PLANES; ++k) {
                 const uint16_t w = f32_to_bf16(r);
@@ -1208,6 +1236,7 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
     const int lr = lane & 15, kq = lane >> 4, wm = wave >> 1, wn = wave & 1;
     const int np = it.np;
     const int64_t qsize = static_cast<int64_t>(np) * np, usize = static_cast<int64_t>(it.rp) * it.cp;
+    const float scale = static_cast<float>(it.scal[2]);
 
     // 16-byte chunks a thread
     constexpr int QV = Q_ROWS * 8 / (64 * FINAL_WAVES), UV = 128 * 8 / (64 * FINAL_WAVES);
@@ -1257,10 +1286,17 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
             if constexpr (P == 3) {
                 float f[8];
                 uf[i].get(f);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    f[q] *= scale;
                 split_planes(f, w);
             } else {
-                w[0] = up[i][0];
-                w[1] = up[i][1];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    w[p] = up[i][p];
+                    if (scale != 1.f)
+                        w[p] = scaled_bf16(w[p], scale);
+                }
             }
 #pragma unroll
             for (int p = 0; p < P; ++p)
@@ -1434,7 +1470,7 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
         it.tops = reinterpret_cast<unsigned int *>(take(it.top_count * sizeof(unsigned int)));
         it.part = take(it.splits * square * real);
         it.mat = take(s.np > SMALL ? 6 * square * real : 0);
-        it.scal = reinterpret_cast<double *>(take(2 * sizeof(double)));
+        it.scal = reinterpret_cast<double *>(take(3 * sizeof(double)));
         it.q = reinterpret_cast<uint16_t *>(take((bf16 ? 2 : 3) * square * 2));
         return off;
     };
@@ -1558,8 +1594,8 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
     for (int i = 0; i < c.count; ++i) {
         const NsItem &it = c.it[i];
         const NsMatrix &m = mats[c.first + i];
-        to[i] = NsOutput{it.u,   it.q,    m.p,   m.out,   m.rows, m.cols,
-                         m.step, m.keep, it.np, it.tall, it.rp,  it.cp};
+        to[i] = NsOutput{it.u,   it.q,   it.scal, m.p,   m.out,   m.rows, m.cols,
+                         m.step, m.keep, it.np,   it.tall, it.rp, it.cp};
     }
     NsGroup<NsOutput> o;
     o.p = p;

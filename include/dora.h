@@ -520,8 +520,8 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
  *   coefficients, a host array, or 3.4445, -4.7750, 2.0315 where it is NULL: after
  *   five steps from a matrix of singular values above 0.0015 of its norm those of O
  *   lie between 0.68 and 1.21.  U, O in `dtype`; O may be U itself.  Formed from 16
- *   bits of bf16 matrices' U (and 24 of fp32 ones') with the polynomials of X X^T in
- *   64 bits, rounded once.
+ *   bits of bf16 matrices' U (and 24 of fp32 ones') with X X^T and its polynomials in
+ *   32 bits (64 for fp32 matrices), rounded once.
  *   1 <= steps <= 16; eps finite, >= 0; the shorter side up to 8192 (or
  *   DORA_E_SHAPE), the matrix up to 2^33 elements with its sides padded to 128s.
  *   U may have any magnitude; an infinity or a NaN in it makes all of O NaN.

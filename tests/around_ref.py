@@ -163,6 +163,8 @@ def orthogonal_bound(U, O, dt, steps=5, coefficients=QUINTIC, eps=1e-7, moved=0.
     itself is off by.  The product at the end is Q U with O = Q U: its elements
     are off by 2^-15 of |Q| |U| with two bf16 numbers an operand (16 bits each, the
     product of the low parts left out, fp32 sums), by (6 n + 8) 2^-24 with three.
+    (The n x n part of bf16 matrices is in 32 bits; its roundings have no share of
+    their own here: a product's are 2^-24 of what the 2^-15 is taken of.)
     Then the output's rounding."""
     X = U.double() if U.shape[0] <= U.shape[1] else U.double().T
     n = X.shape[0]

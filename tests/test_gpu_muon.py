@@ -68,6 +68,24 @@ def test_any_magnitude(power, dt):
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("shape", [(30, 700), (700, 150)])
+def test_norms_at_the_ends_of_the_range(shape, dt):
+    """|U| of 2^-117 and 2^126 or so: 1 / |U| times Q's elements would leave fp32's range."""
+    for power in (-126, -122, -118, 110, 114, 118):
+        U = matrix(5, *shape, F32).to(dt).double() * 2.0 ** power
+        assert float(U.abs().max()) < 2.0 ** 127
+        check(U.to(dt), eps=0.0)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_zeros_stay_zeros_whatever_eps(dt):
+    for shape in ((30, 700), (700, 150)):
+        for eps in (1e-7, 1e-37, 2e-38):
+            O = D.dora_orthogonalize(torch.zeros(*shape, dtype=dt, device=DEV), eps=eps)
+            assert torch.count_nonzero(O) == 0
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("powers", [(-100, 0, 90), (90, 0, -100), (None, -100, -100), (None, None, 0),
                                     (0, -100, None), (-100, -90, -80)])
 def test_magnitudes_that_change_along_the_longer_side(powers, dt):
