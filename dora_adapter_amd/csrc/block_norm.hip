@@ -684,13 +684,14 @@ __global__ void __launch_bounds__(LOOP_THREADS) block_norm_grad_kernel(BlockNorm
     }
 }
 
-// The partial sums in order: blockIdx.y 0 dw_pre, 1 dw_post, then the gate rows, one at a time or,
-// where they have few slots (a slot at least a chunk of rows, see the plan), 16 of them, a wave
-// each; 64 columns a workgroup, whose 16 waves take every 16th part each.
+// The partial sums in a fixed order: blockIdx.y 0 dw_pre, 1 dw_post, then the gate rows, one at a
+// time or, where they have few slots (a slot at least a chunk of rows, see the plan), 16 of them,
+// a wave each; 16, 32 or 64 columns a workgroup (`cols`), whose 16 waves take every 16th part, or
+// group of 2 or 4 of them, each.
 template <typename T>
 __global__ void __launch_bounds__(1024)
     block_norm_finish_kernel(GradOut part, int parts, int64_t Tn, int64_t d, int64_t gate_rows,
-                             float *dw_pre, float *dw_post, T *dgate)
+                             int cols, float *dw_pre, float *dw_post, T *dgate)
 {
     __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -709,15 +710,19 @@ __global__ void __launch_bounds__(1024)
     } else if ((blockIdx.y == 0 ? dw_pre : dw_post) == nullptr) {
         return;
     }
-    for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * 64; j0 < d;
-         j0 += static_cast<int64_t>(gridDim.x) * 64) {
-        const int64_t j = j0 + lane;
+    const int at_once = 64 / cols, part_of = lane / cols, column = lane & (cols - 1);
+    for (int64_t j0 = static_cast<int64_t>(blockIdx.x) * cols; j0 < d;
+         j0 += static_cast<int64_t>(gridDim.x) * cols) {
+        const int64_t j = j0 + column;
         float acc = 0.f;
         if (j < d) {
 #pragma unroll 8
-            for (int64_t p = alone ? 0 : wave; p < count; p += alone ? 1 : 16)
+            for (int64_t p = (alone ? 0 : wave * at_once) + part_of; p < count;
+                 p += alone ? at_once : 16 * at_once)
                 acc += from[p * d + j];
         }
+        for (int m = cols; m < 64; m *= 2)
+            acc += __shfl_xor(acc, m);
         if (!alone) {
             __syncthreads();  // the last columns' sums have been read
             sums[wave][lane] = acc;
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(1024)
             for (int k = 1; k < 16; ++k)
                 acc += sums[k][lane];
         }
-        if ((alone || wave == 0) && j < d) {
+        if ((alone || wave == 0) && part_of == 0 && j < d) {
             if (g >= 0) {
                 if constexpr (sizeof(T) == 2)
                     dgate[g * d + j] = f32_to_bf16(acc);
@@ -821,12 +826,19 @@ hipError_t backward_any(const BlockNormGradArgs &a, const BlockNormPlan &p, char
     const bool sums = (!one || a.T == 0) && (a.dw_pre != nullptr || a.dw_post != nullptr);
     if (e != hipSuccess || (!slots && !sums))
         return e;
-    const int64_t blocks = (a.d + 63) / 64, rows = !slots ? 0 : a.T == 0 ? 1 : (a.T + a.gate_rows - 1) / a.gate_rows;
+    const int64_t rows = !slots ? 0 : a.T == 0 ? 1 : (a.T + a.gate_rows - 1) / a.gate_rows;
     const bool few = a.gate_rows <= 16 * p.chunk && a.gate_rows < a.T;
+    const int64_t arrays = 2 + (few ? (rows + 15) / 16 : rows);
+    // the widest columns that make 256 workgroups, but a line's half at least (the sums of 256
+    // parts of 4096 columns: 32 columns 2 us less than 64; with eight gates' 4 us more)
+    int cols = 64;
+    while (cols > 16 && (a.d + cols - 1) / cols * arrays < 256)
+        cols /= 2;
+    const int64_t blocks = (a.d + cols - 1) / cols;
     hipLaunchKernelGGL((block_norm_finish_kernel<T>),
                        dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536),
-                            static_cast<unsigned>(2 + (few ? (rows + 15) / 16 : rows))),
-                       dim3(1024), 0, st, out, p.parts, a.T, a.d, a.gate_rows,
+                            static_cast<unsigned>(arrays)),
+                       dim3(1024), 0, st, out, p.parts, a.T, a.d, a.gate_rows, cols,
                        sums ? a.dw_pre : nullptr, sums ? a.dw_post : nullptr,
                        slots ? static_cast<T *>(a.dgate) : nullptr);
     return hipGetLastError();
@@ -848,10 +860,14 @@ BlockNormPlan plan_block_norm_grad(int64_t T, int64_t d, int64_t gate_rows)
     const int64_t vecs = (d + 7) / 8;
     int64_t parts;
     if (p.held) {
-        // a workgroup a CU, and the shorter the rows the more of them
+        // A workgroup a CU, and the shorter the rows the more of them from eight rows each on (2048 x
+        // 4096 in bf16: 42 us, from four on 47); of wide rows fewer, down to 128, before
+        // they have less than four, since each leaves a row of sums (512 x 8192: 39 us, 256 of
+        // them 41; 256 x 8192: 32 and 37).
         const int most = vecs > 512 ? 1 : vecs > 128 ? 2 : vecs > 64 ? 4 : 8;
-        const int64_t share = T / 4;
-        parts = share > 256 ? share : 256;
+        const int64_t share = T / 8, few = T / 4 < 128 ? 128 : T / 4 < 256 ? T / 4 : 256;
+        const int64_t least = vecs > 512 ? few : 256;
+        parts = share > least ? share : least;
         parts = parts < 256 * most ? parts : 256 * most;
         parts = parts < T ? parts : T;
     } else {
