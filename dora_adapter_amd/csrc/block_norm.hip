@@ -13,7 +13,7 @@
 //
 // Both are bound by memory traffic: two matrices in and two out forward, four in and two out
 // backward, each once.  A workgroup takes whole rows, a thread eight consecutive columns at a
-// time (16 bytes of bf16).  8192 x 8192 in bf16: 94 us forward (5.7 TB/s), 152 + 9 backward (5.5).
+// time (16 bytes of bf16).  8192 x 8192 in bf16: 94 us forward (5.7 TB/s), 145 + 10 backward (5.7).
 #include "around.hpp"
 #include "rows8.hpp"
 
