@@ -532,11 +532,12 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
  *     param_out    = param - lr (weight_decay param + scale O(U))
  *   param, grad, param_out [rows, cols] in `dtype`, momentum, momentum_out fp32.
  *   param_out may be param, momentum_out momentum (in place); every output is
- *   otherwise disjoint from every other buffer of the list.  Up to 16 matrices (in 256
- *   MiB of workspace) share each launch; the array is read during the call only.
+ *   otherwise disjoint from every other buffer of the list.  Up to 40 matrices (in 256
+ *   MiB of workspace) share each launch, and a matrix's share of it decides the order
+ *   of its sums; the array is read during the call only.
  *   ws: dora_orthogonalize_workspace / dora_muon_workspace bytes: copies of the
  *   matrices (4 bytes an element, sides padded), and the short sides' squares in 64
- *   bits.
+ *   bits (32 for bf16).
  */
 typedef struct dora_update {
     const void *param;

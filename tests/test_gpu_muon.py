@@ -188,6 +188,20 @@ def test_muon(which, dt):
         assert torch.equal(p2[k], po[k]) and torch.equal(m2[k], mo[k]), k
 
 
+@pytest.mark.parametrize("shapes", [[(8, 300), (300, 8), (70, 90)] * 30, [(33, 200000), (200000, 9)] * 4])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_more_than_one_set_of_launches(shapes, dt):
+    """More matrices than share a launch, and more bytes."""
+    ps, gs, ms = problem(shapes, dt, seed=3)
+    up = [[t.to(DEV) for t in ts] for ts in (ps, gs, ms)]
+    po, mo = p2(up[0]), p2(up[2])
+    D.dora_muon(*up, 0.02, params_out=po, momenta_out=mo)
+    check_step(ps, gs, ms, po, mo, 0.02)
+    again, m2 = p2(up[0]), p2(up[2])
+    D.dora_muon(*up, 0.02, params_out=again, momenta_out=m2)
+    assert all(torch.equal(x, y) for x, y in zip(again + m2, po + mo))
+
+
 def test_a_matrix_does_not_depend_on_its_neighbours():
     """(Beyond the order of its sums, which its share of the launch decides.)"""
     ps, gs, ms = problem([(48, 900), (260, 70), (48, 900)], F32, seed=4)
