@@ -183,6 +183,14 @@ def test_linear_every_kernel(dt, T, d_out):
         check_linear(T, d_in, d_out - 3, dt, group)
 
 
+@pytest.mark.parametrize("T", [4, 16, 17, 32, 33, 64, 100])
+@pytest.mark.parametrize("d_out", [70, 4000, 12301, 24590])
+def test_linear_groups_of_64(T, d_out):
+    """Each tile rule again with four scales a line, the last line a whole one and not."""
+    for d_in in (768, 1091):
+        check_linear(T, d_in, d_out, BF, 64)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_linear_in_panels(dt):
     """A weight of more rows than a panel holds: the last panel is a short one."""
