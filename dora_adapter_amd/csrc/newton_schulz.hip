@@ -18,7 +18,7 @@
 // numbers (16 bits) there and for G, and have their n x n part in fp32.
 //
 // Up to 40 matrices share each launch.  Measured: a step of the factors 384 x 8192 and 28672 x 384
-// in bf16 234 us (nineteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
+// in bf16 234 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
 // (three), 37 x 1027 in fp32 36 us (three).
 #include <climits>
 #include <type_traits>
