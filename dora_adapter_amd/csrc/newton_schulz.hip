@@ -382,12 +382,13 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
                     acc[x][y][q];
 }
 
-// LDS tiles of one plane: 64 K values of R rows of the shorter side, as rows of K values 144 bytes
-// apart (16 of them at one chunk on distinct banks), or, where the matrix lies the other way,
-// as 64 rows of R values (four rows of 32 bytes on distinct banks), read by transposing loads.
+// LDS tiles of one plane: 64 K values of R rows of the shorter side, as rows of K values 160 bytes
+// apart (a 16-byte read takes lanes 0-3, 12-15 and 20-27 at once, and so on: sixteen chunks of two
+// neighbouring columns, which lie on distinct banks; 144 bytes: two on each), or, where the
+// matrix lies the other way, as 64 rows of R values, read by transposing loads.
 template <int R>
 struct Tiles {
-    static constexpr int KP = 144, MP = R == 128 ? 288 : 160;
+    static constexpr int KP = 160, MP = R == 128 ? 288 : 160;
     static constexpr int K_BYTES = R * KP, M_BYTES = 64 * MP;
     // operands of 32 K values (h: the first or the second half of the stage) of 16 rows from r0
     __device__ __forceinline__ static bf16x8_t rows16(const unsigned char *tile, int r0, int h, int lane)
@@ -395,13 +396,17 @@ struct Tiles {
         return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(
                                                 tile + (r0 + (lane & 15)) * KP + 64 * h + 16 * (lane >> 4)));
     }
+    // (SPREAD: the K values in another order, the same for any operand read so, in which the
+    // eight rows of half a wave lie next to each other: on distinct banks)
+    template <bool SPREAD = false>
     __device__ __forceinline__ static bf16x8_t columns16(const unsigned char *tile, int c0, int h, int lane)
     {
         const int lr = lane & 15, kq = lane >> 4;
         const unsigned char *const p =
-            tile + (32 * h + 8 * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
+            tile + (32 * h + (SPREAD ? 4 : 8) * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
         const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-        const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * MP));
+        const s16x4_t y =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (SPREAD ? 16 : 4) * MP));
         return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 };
@@ -416,7 +421,7 @@ using GramTiles = unsigned char[2][Tiles<GRAM>::K_BYTES > Tiles<GRAM>::M_BYTES ?
                                                                             : Tiles<GRAM>::M_BYTES];
 template <bool TALL>
 __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, GramTiles &sa,
-                                               GramTiles &sb, unsigned int *red)
+                                               GramTiles &sb)
 {
     using Tl = Tiles<GRAM>;
     constexpr int TM = GRAM / (8 * GRAM_WAVES), TN = GRAM / 32;       // 16 x 16 blocks of a wave
@@ -471,13 +476,15 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
             acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     auto operand = [&](const unsigned char *tile, int r0, int h) {
         if constexpr (TALL)
-            return Tl::columns16(tile, r0, h, lane);
+            return Tl::template columns16<true>(tile, r0, h, lane);
         else
             return Tl::rows16(tile, r0, h, lane);
     };
     fetch(ra, i0, k0);
     fetch(rb, j0, k0);
-    scale = range_scale(own_top(it), red);
+    // (in what the tiles' layout leaves of a row: two workgroups fill a CU's LDS to the last byte)
+    static_assert(GRAM * 2 + GRAM_WAVES * 4 <= Tl::MP && 128 + GRAM_WAVES * 4 <= Tl::KP, "a word for each wave");
+    scale = range_scale(own_top(it), reinterpret_cast<unsigned int *>(&sa[0][TALL ? GRAM * 2 : 128]));
     for (int64_t k = k0; k < k1; k += 64) {
         __syncthreads();
         keep(ra, sa);
@@ -524,12 +531,11 @@ __device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, Gram
 __global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kernel(NsGroup<NsItem> g)
 {
     __shared__ __align__(16) GramTiles sa, sb;
-    __shared__ unsigned int red[GRAM_WAVES];
     const Found<NsItem> found = find_item(g, place_on_xcd());
     if (found.it.tall)
-        gram_tile_bf16<true>(found.it, found.block, sa, sb, red);
+        gram_tile_bf16<true>(found.it, found.block, sa, sb);
     else
-        gram_tile_bf16<false>(found.it, found.block, sa, sb, red);
+        gram_tile_bf16<false>(found.it, found.block, sa, sb);
 }
 
 // ------------------------------------------------- U and its Gram partial, n <= 64
@@ -563,9 +569,8 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
     const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
     // (in what the first tile's layout leaves: two workgroups fill a CU's LDS to the last byte)
     unsigned int *const red =
-        reinterpret_cast<unsigned int *>(lds + (TALL ? 2 * SMALL : Tiles<SMALL>::K_BYTES));
-    static_assert(2 * SMALL + FRONT / 16 <= Tiles<SMALL>::MP &&
-                      Tiles<SMALL>::K_BYTES + FRONT / 16 <= L::TILE_BYTES,
+        reinterpret_cast<unsigned int *>(lds + 2 * SMALL);
+    static_assert(2 * SMALL + FRONT / 16 <= Tiles<SMALL>::MP && 2 * SMALL + FRONT / 16 <= Tiles<SMALL>::KP,
                   "a word for each wave");
     const int n = static_cast<int>(TALL ? it.cols : it.rows), nt = (n + 15) / 16;
     const int64_t l = TALL ? it.rows : it.cols;
@@ -743,7 +748,7 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
             auto operand = [&](int plane, int stage, int r0, int h) {
                 const unsigned char *const tile = lds + plane * PLANE + stage * L::TILE_BYTES;
                 if constexpr (TALL)
-                    return Tiles<SMALL>::columns16(tile, r0, h, lane);
+                    return Tiles<SMALL>::template columns16<true>(tile, r0, h, lane);
                 else
                     return Tiles<SMALL>::rows16(tile, r0, h, lane);
             };
