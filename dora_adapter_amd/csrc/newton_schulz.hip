@@ -18,7 +18,7 @@
 // numbers (16 bits) there and for G, and have their n x n part in fp32.
 //
 // Up to 40 matrices share each launch.  Measured: a step of the factors 384 x 8192 and 28672 x 384
-// in bf16 234 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
+// in bf16 229 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
 // (three), 37 x 1027 in fp32 36 us (three).
 #include <climits>
 #include <type_traits>
@@ -1204,7 +1204,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 // ------------------------------------------------------------- O = Q U (or U Q)
 // Tiles of NB values of the shorter side by 128 of the longer one, eight waves (4 x 2), 64 values
 // of K (the shorter side) a stage, the next one on its way.  The tile goes through LDS, so that
-// the update reads and writes whole lines.  Bound like the Gram product (52 us for 85 MB read, 28
+// the update reads and writes whole lines.  Bound like the Gram product (50 us for 85 MB read, 28
 // written and 33 GFLOP of products; four waves of 64 x 64 55, rows of the update straight from the
 // accumulators 67).
 template <typename T, int NB>
