@@ -140,6 +140,14 @@ constexpr int AUX_NT = 2;  // non-temporal
 // nor 16 rows read at one chunk meet on a bank.
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
 
+// The same for rows of 512 bytes, whose chunks all lie on the same banks: a 16-byte read takes
+// lanes 0-3, 12-15 and 20-27 at once (and so on), eight rows at one chunk and the other eight at
+// the next one.
+__device__ __forceinline__ int swizzle_line(int r)
+{
+    return swizzle(r) | ((((r >> 2) ^ (r >> 3)) & 1) << 3);
+}
+
 // A wave's reader of the codes of tiles of 16 NT channels.
 template <int NT, int PER>
 struct Codes {
@@ -457,7 +465,7 @@ __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(Four
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 *reinterpret_cast<u32x4_t *>(&xs[kg][buf][(p * 16 * TM + r) * ROW +
-                                                          16 * (c ^ swizzle(r))]) =
+                                                          16 * (c ^ swizzle_line(r))]) =
                     u32x4_t{w[p][0], w[p][1], w[p][2], w[p][3]};
         }
     };
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(CW *KG * 64) linear_fourbit_shared_kernel(Four
                         x[i][p] = __builtin_bit_cast(
                             bf16x8_t, *reinterpret_cast<const u32x4_t *>(
                                           &xs[kg][buf][(p * 16 * TM + 16 * i + nl) * ROW +
-                                                       16 * ((4 * s + kq) ^ swizzle(nl))]));
+                                                       16 * ((4 * s + kq) ^ swizzle_line(nl))]));
                 sum.step(x, c, l, s);
             }
         }
