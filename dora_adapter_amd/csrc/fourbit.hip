@@ -11,6 +11,8 @@ constexpr int THREADS = 256;
 constexpr int VPT = 4;  // vectors of eight columns a thread
 
 // Threads along a row and rows a workgroup: a workgroup takes `rows` rows by VPT * along vectors.
+// No more threads along a row than its vectors have work for, VPT each (28672 x 384 in bf16 to
+// codes: 8.8 us, 22 with a thread a vector).
 struct Shape {
     unsigned along, rows, shares;
     int64_t groups;  // workgroups along the rows
@@ -19,7 +21,7 @@ Shape shape_of(int64_t rows, int64_t vecs, int lanes)
 {
     Shape s;
     s.along = static_cast<unsigned>(lanes);
-    while (s.along < THREADS && s.along < vecs)
+    while (s.along < THREADS && s.along * VPT < vecs)
         s.along *= 2;
     s.rows = THREADS / s.along;
     const int64_t shares = (vecs + s.along * VPT - 1) / (s.along * VPT);
