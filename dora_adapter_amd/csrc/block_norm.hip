@@ -118,7 +118,9 @@ __device__ __forceinline__ float squares8(const Raw8<T> &v, float k, float acc)
     return acc;
 }
 
-// 1 / rms of a row held as VPT vectors a thread; red [2][16], its first row written once.
+// 1 / rms of a row held as VPT vectors a thread.  red [2][16] is of this call alone: neither row is
+// written again by another one, whose waves might be ahead of those that still read it (there
+// is no barrier behind the last read; group_sums has none in front of its writes).
 template <typename T, int VPT>
 __device__ __forceinline__ float row_rstd(const Raw8<T> (&v)[VPT], const BlockNormArgs &a,
                                           float (*red)[16], int waves)
@@ -142,7 +144,7 @@ __device__ __forceinline__ float row_rstd(const Raw8<T> (&v)[VPT], const BlockNo
 template <typename T, int VPT>
 __global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
 {
-    __shared__ float red[3][16];
+    __shared__ float red[4][16];  // two rows for each row_rstd
     const int threads = static_cast<int>(blockDim.x), waves = threads >> 6;
     const int d = static_cast<int>(a.d);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * a.d;
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(1024) block_norm_held_kernel(BlockNormArgs a)
         h[i] = block_h(a, x[i], h[i], w1[i], g[i], r1);
         h[i].store(static_cast<T *>(a.h) + row + col(i), count8(d, col(i)));
     }
-    const float r2 = row_rstd(h, a, red + 1, waves);
+    const float r2 = row_rstd(h, a, red + 2, waves);
     if (a.rstd_pre != nullptr && threadIdx.x == 0)
         a.rstd_pre[blockIdx.x] = r2;
 #pragma unroll
