@@ -148,6 +148,14 @@ __device__ __forceinline__ int swizzle_line(int r)
     return swizzle(r) | ((((r >> 2) ^ (r >> 3)) & 1) << 3);
 }
 
+// Orders the wave's LDS accesses around it: to the compiler, for which accesses of one lane to
+// different places could change places, though other lanes meet them (LDS itself takes a wave's in order).
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's reader of the codes of tiles of 16 NT channels.
 template <int NT, int PER>
 struct Codes {
@@ -217,6 +225,7 @@ struct Codes {
     // a line into the wave's LDS, and the four operand registers of its half h from there
     __device__ __forceinline__ void turn(const Line<NT, PER> &l) const
     {
+        wave_lds_order();  // (the line before it has been read)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -225,6 +234,7 @@ struct Codes {
                 *reinterpret_cast<u32x4_t *>(turned + i * 2048 + r * 128 + 16 * (lchunk ^ swizzle(r))) =
                     l.c[i][u];
             }
+        wave_lds_order();
     }
     __device__ __forceinline__ void half(unsigned int (&c)[NT][4], int h) const
     {
