@@ -78,7 +78,7 @@ struct NsParams {
 constexpr int NS_MAX_STEPS = 16;
 constexpr int64_t NS_MAX_SHORT = 8192;  // the shorter side
 bool newton_schulz_fits(int64_t rows, int64_t cols);
-size_t newton_schulz_workspace(int bf16, const NsMatrix *mats, int count);
+size_t newton_schulz_workspace(const NsMatrix *mats, int count);
 hipError_t launch_newton_schulz(int bf16, const NsMatrix *mats, int count, const NsParams &p, void *ws,
                                 hipStream_t st);
 

@@ -2594,7 +2594,7 @@ size_t dora_orthogonalize_workspace(int64_t rows, int64_t cols, int dtype)
     if (check_dtype(dtype) || check_matrix(rows, cols))
         return 0;
     const NsMatrix m = shape_only(rows, cols);
-    return newton_schulz_workspace(dtype == DORA_BF16, &m, 1);
+    return newton_schulz_workspace(&m, 1);
 }
 
 int dora_orthogonalize(const void *U, int64_t rows, int64_t cols, int dtype, int steps,
@@ -2611,7 +2611,7 @@ int dora_orthogonalize(const void *U, int64_t rows, int64_t cols, int dtype, int
     m.g = U;
     m.out = O;
     const bool bf = dtype == DORA_BF16;
-    const size_t need = newton_schulz_workspace(bf, &m, 1);
+    const size_t need = newton_schulz_workspace(&m, 1);
     DORA_CHECK(check_ws(ws, ws_bytes, need));
     const size_t bytes = static_cast<size_t>(rows) * cols * esize(dtype);
     if (O != U && overlap({O, bytes}, {U, bytes}))
@@ -2627,7 +2627,7 @@ try {
     std::vector<NsMatrix> mats;
     if (check_dtype(dtype) || update_matrices(updates, count, mats))
         return 0;
-    return newton_schulz_workspace(dtype == DORA_BF16, mats.data(), count);
+    return newton_schulz_workspace(mats.data(), count);
 } catch (const std::exception &) {
     return 0;
 }
@@ -2645,7 +2645,7 @@ try {
     p.mu = mu;
     p.nesterov = nesterov != 0;
     const bool bf = dtype == DORA_BF16;
-    const size_t need = newton_schulz_workspace(bf, mats.data(), count);
+    const size_t need = newton_schulz_workspace(mats.data(), count);
     DORA_CHECK(check_ws(ws, ws_bytes, need));
     // Every buffer of the list but the inputs that their own output replaces (the same element,
     // read before it is written): no output may overlap any other of them.

@@ -7,19 +7,22 @@
 //     Q <- P(G) Q,   G <- P(G) G P(G),
 // between one product along L, G = U U^T, and another, O = Q U / (|U|_F + eps), whose epilogue is
 // the update: 4 n^2 L flops instead of 4 n^2 L a step, and U is read twice.  Where n comes near L
-// that is no gain (4096 x 4096, five steps: bf16 14.1 ms, the literal steps 14.3; fp32 27.6).
+// that is a loss (4096 x 4096, five steps: 28.9 ms, the literal steps in fp32 14.5; 1024 x 8192 1.0
+// against 1.6).
 //
 // G holds squares of singular values, so that an error of 2^-24 of its largest one would move the
 // small ones' directions by 2^-24 / (2 sigma^2), where the literal steps in fp32 move them by
-// about 2^-24 / sigma.  So the n x n part of fp32 matrices is in 64 bits, and the fp32 product at
-// the end is all that is left (measured against 64 bits: as far off as the literal steps); it
-// takes its operands as three bf16 numbers each, which hold 24 bits, on the bf16 matrix cores
-// with fp32 sums.  bf16 matrices, whose output's 8 bits leave room for 1e-4 of its norm, take two
-// numbers (16 bits) there and for G, and have their n x n part in fp32.
+// about 2^-24 / sigma.  Worse, an eigenvalue that it takes below zero is multiplied by a^2 a
+// step, as U U^T's cannot be, and leaves the range where the polynomial is bounded: with G in
+// 32 bits that is seven steps of the quintic for a matrix of low rank.  So G and the n x n part
+// are in 64 bits, for matrices of either type, and the product at the end is all that is left (a
+// quarter of the literal fp32 steps' error against 64 bits, whatever the rank); it takes Q and U as
+// three bf16 numbers each, which hold 24 bits, on the bf16 matrix cores with fp32 sums.
 //
 // Up to 40 matrices share each launch.  Measured: a step of the factors 384 x 8192 and 28672 x 384
-// in bf16 229 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 90 us
-// (three), 37 x 1027 in fp32 36 us (three).
+// in bf16 432 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 98 us
+// (three), 37 x 1027 in fp32 37 us (three).  (G, the n x n part and the planes of bf16 matrices at
+// 16 to 24 bits took 229 and 90 us, and are not right for a low rank: see above.)
 #include <climits>
 #include <type_traits>
 
@@ -34,34 +37,29 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
 constexpr int THREADS = 256;
-constexpr int TILE = 64, GRAM = 128;  // Gram tiles of fp32 and of bf16 matrices
+constexpr int TILE = 64;       // Gram tiles
 constexpr int SMALL = 64;      // n x n matrices of one workgroup's LDS
 constexpr int POLY = 32;       // tile of the n x n products
 constexpr int POLY_WAVES = 8;  // which split their K
 
-// A matrix as its kernels see it.  The n x n part of bf16 matrices is formed in fp32, theirs of
-// fp32 matrices in fp64: `part` and `mat` are of that type.
+// A matrix as its kernels see it.
 struct NsItem {
-    char *u;             // U padded with zeros, [rp, cp]: bf16 hi and lo, or fp32
-    unsigned int *tops;  // bf16: the largest |U| of each workgroup that wrote it, as bits; with a
-                         // shorter side to 64 each partial's scale, as its exponent
-    char *part;          // Gram partials [splits, np, np], tiles on and below the diagonal
-    char *mat;           // G, P, Q, H and the other G and Q [np, np] (larger matrices)
-    double *scal;        // what makes the planes of Q, the first G of U U^T, and what U meets
-    uint16_t *q;         // planes of Q / (|U|_F + eps) times a power of two, [planes, np, np]
-    int n, np;           // the shorter side, padded to 64 or to 128s
-    int tall;            // rows > cols
-    int rp, cp;          // rows and columns as padded (the longer side to 128s)
-    int top_count;
+    float *u;      // U padded with zeros, [rp, cp]
+    double *part;  // Gram partials [splits, np, np], tiles on and below the diagonal
+    double *mat;   // G, P, Q, H and the other G and Q [np, np] (larger matrices)
+    double *scal;  // what makes the planes of Q, the first G of U U^T, and what U meets
+    uint16_t *q;   // planes of Q / (|U|_F + eps) times a power of two, [3, np, np]
+    int n, np;     // the shorter side, padded to 64 or to 128s
+    int tall;      // rows > cols
+    int rp, cp;    // rows and columns as padded (the longer side to 128s)
     int splits, per_split;  // of the longer side, a multiple of 64
 };
 struct NsInput {  // what the first kernel reads and writes
-    char *u, *part;
-    unsigned int *tops;
+    float *u;
+    double *part;
     const void *g;
     const float *m;
     float *m_out;
@@ -69,7 +67,7 @@ struct NsInput {  // what the first kernel reads and writes
     int rp, cp, tall, per_split;
 };
 struct NsOutput {  // what the last kernel reads and writes
-    const char *u;
+    const float *u;
     const uint16_t *q;
     const double *scal;
     const void *p;
@@ -146,45 +144,27 @@ __device__ __forceinline__ NormScale norm_scale(double norm, double eps)
     return n;
 }
 
-template <bool F32>
-using Part = std::conditional_t<F32, double, float>;
+// the row of an fp64 product's register q (its column is lane % 16)
+__device__ __forceinline__ int d_row(int q, int lane) { return 4 * q + (lane >> 4); }
 __device__ __forceinline__ f64x4_t mfma4(double a, double b, f64x4_t c)
 {
     return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4_t mfma4(float a, float b, f32x4_t c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-// the row of D's register q (its column is lane % 16)
-__device__ __forceinline__ int d_row(double, int q, int lane) { return 4 * q + (lane >> 4); }
-__device__ __forceinline__ int d_row(float, int q, int lane) { return 4 * (lane >> 4) + q; }
-template <typename R>
-using Quad = std::conditional_t<sizeof(R) == 8, f64x4_t, f32x4_t>;
 
-// eight bf16 numbers times a power of two
-__device__ __forceinline__ u32x4_t scaled_bf16(u32x4_t w, float scale)
-{
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        w[q] = pack_bf16x2(scale * __uint_as_float(w[q] << 16), scale * __uint_as_float(w[q] & 0xffff0000u));
-    return w;
-}
-
-// v as P bf16 numbers whose sum it is (to 16 bits with two of them, 24 with three)
-template <int P>
-__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4_t (&w)[P])
+// v as three bf16 numbers whose sum it is, to 24 bits
+constexpr int PLANES = 3;
+__device__ __forceinline__ void split_planes(const float (&v)[8], u32x4_t (&w)[PLANES])
 {
     float r[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
         r[q] = v[q];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
+    for (int p = 0; p < PLANES; ++p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             w[p][q] = pack_bf16x2(r[2 * q], r[2 * q + 1]);
-        if (p + 1 < P) {
+        if (p + 1 < PLANES) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 r[2 * q] -= __uint_as_float(w[p][q] << 16);
@@ -194,8 +174,16 @@ __device__ __forceinline__ void split_planes(const float (&v)[8], u32x4_t (&w)[P
     }
 }
 
+// the next eight of the fp32 numbers of U
+__device__ __forceinline__ void put_u(float *o, const float (&u)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<f32x4_t *>(o + 4 * k) = f32x4_t{u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]};
+}
+
 // ------------------------------------------------------------- U and the momentum
-// Bound by memory traffic: 6 bytes an element in, 8 out (14.2 million in bf16: 39 us, 5.1 TB/s).
+// Bound by memory traffic: 6 bytes an element in, 8 out (14.2 million in bf16: 42 us, 4.7 TB/s).
 constexpr int PREP_VPT = 4;
 template <typename T>
 __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
@@ -203,8 +191,6 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
     const Found<NsInput> found = find_item(g, blockIdx.x);
     const NsInput &it = found.it;
     const unsigned int block = found.block;
-    __shared__ unsigned int wave_top[THREADS / 64];
-    unsigned int top = 0u;
     const unsigned int along = static_cast<unsigned int>(it.cp / 8);
     const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
     const unsigned int total = static_cast<unsigned int>(usize / 8);
@@ -238,71 +224,17 @@ __global__ void __launch_bounds__(THREADS) ns_prepare_kernel(NsGroup<NsInput> g)
                 mr.store(it.m_out + at, cnt);
             }
         }
-        const int64_t at = static_cast<int64_t>(v) * 8;
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const unsigned int b = abs_bits(u[q]);
-                top = top > b ? top : b;
-            }
-            u32x4_t w[2];
-            split_planes(u, w);
-            uint16_t *const h = reinterpret_cast<uint16_t *>(it.u) + at;
-            *reinterpret_cast<u32x4_t *>(h) = w[0];
-            *reinterpret_cast<u32x4_t *>(h + usize) = w[1];
-        } else {
-            float *const o = reinterpret_cast<float *>(it.u) + at;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<f32x4_t *>(o + 4 * k) =
-                    f32x4_t{u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]};
-        }
+        put_u(it.u + static_cast<int64_t>(v) * 8, u);
     }
-    if constexpr (sizeof(T) == 2) {
-        top = lane_max(top, 64);
-        if ((threadIdx.x & 63) == 0)
-            wave_top[threadIdx.x >> 6] = top;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < THREADS / 64; ++w)
-                top = top > wave_top[w] ? top : wave_top[w];
-            it.tops[block] = top;
-        }
-    }
-}
-
-// The power of two that brings a bf16 matrix's largest |U| near one where fp32 might not hold its
-// Gram matrix, or the square of that, to the last bits that count; else 1 (range_scale: of the
-// largest of each thread's share, own_top, by whole workgroups).
-__device__ __forceinline__ unsigned int own_top(const NsItem &it)
-{
-    unsigned int top = 0u;
-    for (int i = threadIdx.x; i < it.top_count; i += blockDim.x) {
-        const unsigned int b = it.tops[i];
-        top = top > b ? top : b;
-    }
-    return top;
-}
-__device__ __forceinline__ int range_exponent(unsigned int top)
-{
-    const int e = static_cast<int>(top >> 23) - 127;
-    return top == 0u || e == 128 || (e > -24 && e < 9) ? 0 : e == 127 ? -126 : -e;
-}
-__device__ __forceinline__ float power(int e)  // 2^e, -126 <= e <= 127
-{
-    return __uint_as_float(static_cast<unsigned int>(127 + e) << 23);
-}
-__device__ __forceinline__ float range_scale(unsigned int top, unsigned int *red)
-{
-    return power(range_exponent(block_max(top, red, static_cast<int>(blockDim.x) >> 6)));
 }
 
 // ------------------------------------------------------------------- G = U U^T
-// fp32 matrices: 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L
+// 64 x 64 tiles on and below the diagonal, four waves of 32 x 32, 32 values of L
 // at a time straight into registers.  An MFMA takes four of them: of a wide matrix a lane's
 // eight consecutive ones give it one each time, of a tall one they are four rows.  Bound by the
-// matrix cores' 64-bit rate (72 TFLOP/s in a large product).
-__global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
+// matrix cores' 64-bit rate (72 TFLOP/s in a large product; 384 x 8192 and 28672 x 384: 6.3 GFLOP of
+// tiles in 152 us).
+__global__ void __launch_bounds__(THREADS) ns_gram_kernel(NsGroup<NsItem> g)
 {
     const Found<NsItem> found = find_item(g, place_on_xcd());
     const NsItem &it = found.it;
@@ -320,7 +252,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
     const int i0 = ti * TILE + 32 * (wave >> 1), j0 = tj * TILE + 32 * (wave & 1);
     const int64_t lp = it.tall ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
                   k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
-    const float *const f = reinterpret_cast<const float *>(it.u);
+    const float *const f = it.u;
 
     f64x4_t acc[2][2];
 #pragma unroll
@@ -366,229 +298,56 @@ __global__ void __launch_bounds__(THREADS) ns_gram_f64_kernel(NsGroup<NsItem> g)
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        acc[x][y] = __builtin_amdgcn_mfma_f64_16x16x4f64(
-                            static_cast<double>(a[half][x][s]), static_cast<double>(b[half][y][s]),
-                            acc[x][y], 0, 0, 0);
+                        acc[x][y] = mfma4(static_cast<double>(a[half][x][s]),
+                                          static_cast<double>(b[half][y][s]), acc[x][y]);
         }
     }
-    double *const out = reinterpret_cast<double *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
+    double *const out = it.part + static_cast<int64_t>(z) * it.np * it.np;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                out[static_cast<int64_t>(i0 + 16 * x + 4 * q + kq) * it.np + j0 + 16 * y + lr] =
+                out[static_cast<int64_t>(i0 + 16 * x + d_row(q, lane)) * it.np + j0 + 16 * y + lr] =
                     acc[x][y][q];
-}
-
-// LDS tiles of one plane: 64 K values of R rows of the shorter side, as rows of K values 160 bytes
-// apart (a 16-byte read takes lanes 0-3, 12-15 and 20-27 at once, and so on: sixteen chunks of two
-// neighbouring columns, which lie on distinct banks; 144 bytes: two on each), or, where the
-// matrix lies the other way, as 64 rows of R values, read by transposing loads.
-template <int R>
-struct Tiles {
-    static constexpr int KP = 160, MP = R == 128 ? 288 : 160;
-    static constexpr int K_BYTES = R * KP, M_BYTES = 64 * MP;
-    // operands of 32 K values (h: the first or the second half of the stage) of 16 rows from r0
-    __device__ __forceinline__ static bf16x8_t rows16(const unsigned char *tile, int r0, int h, int lane)
-    {
-        return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(
-                                                tile + (r0 + (lane & 15)) * KP + 64 * h + 16 * (lane >> 4)));
-    }
-    // (SPREAD: the K values in another order, the same for any operand read so, in which the
-    // eight rows of half a wave lie next to each other: on distinct banks)
-    template <bool SPREAD = false>
-    __device__ __forceinline__ static bf16x8_t columns16(const unsigned char *tile, int c0, int h, int lane)
-    {
-        const int lr = lane & 15, kq = lane >> 4;
-        const unsigned char *const p =
-            tile + (32 * h + (SPREAD ? 4 : 8) * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
-        const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-        const s16x4_t y =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (SPREAD ? 16 : 4) * MP));
-        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-};
-
-// bf16 matrices: both planes of both operands, all four products, in fp32 over a share of L (the
-// shares are added in 64 bits).  128 x 128 tiles on and below the diagonal, eight waves (4 x 2),
-// 64 values of L a stage, the next one on its way.  Two workgroups a CU by registers and LDS, so
-// that one's loads pass under the other's products; bound by what is left of the loads' round
-// trips (36 us for 57 MB and 29 GFLOP of products, four waves of 64 x 64 42).
-constexpr int GRAM_WAVES = 8, FINAL_WAVES = 8;  // two in each row
-using GramTiles = unsigned char[2][Tiles<GRAM>::K_BYTES > Tiles<GRAM>::M_BYTES ? Tiles<GRAM>::K_BYTES
-                                                                            : Tiles<GRAM>::M_BYTES];
-template <bool TALL>
-__device__ __forceinline__ void gram_tile_bf16(const NsItem &it, int block, GramTiles &sa,
-                                               GramTiles &sb)
-{
-    using Tl = Tiles<GRAM>;
-    constexpr int TM = GRAM / (8 * GRAM_WAVES), TN = GRAM / 32;       // 16 x 16 blocks of a wave
-    constexpr int V = GRAM * 8 / (64 * GRAM_WAVES);              // 16-byte chunks of a plane a thread
-    const int nt = it.np / GRAM, tiles = nt * (nt + 1) / 2;
-    const int z = block / tiles;
-    int t = block % tiles, ti = 0;
-    while (t > ti) {
-        t -= ti + 1;
-        ++ti;
-    }
-    const int i0 = ti * GRAM, j0 = t * GRAM;
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
-    const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(z) * it.per_split,
-                  k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
-    const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
-
-    u32x4_t ra[V][2], rb[V][2];
-    auto fetch = [&](u32x4_t (&r)[V][2], int r0, int64_t k) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * (64 * GRAM_WAVES);
-            const int64_t at = TALL ? (k + v / (GRAM / 8)) * it.cp + r0 + v % (GRAM / 8) * 8
-                                    : static_cast<int64_t>(r0 + v / 8) * it.cp + k + v % 8 * 8;
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-                r[i][p] = *reinterpret_cast<const u32x4_t *>(reinterpret_cast<const uint16_t *>(it.u) +
-                                                             p * usize + at);
-        }
-    };
-    float scale = 1.f;
-    auto keep = [&](const u32x4_t (&r)[V][2], GramTiles &to) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = tid + i * (64 * GRAM_WAVES);
-            const int at = TALL ? v / (GRAM / 8) * Tl::MP + v % (GRAM / 8) * 16 : v / 8 * Tl::KP + v % 8 * 16;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                u32x4_t w = r[i][p];
-                if (scale != 1.f)
-                    w = scaled_bf16(w, scale);
-                *reinterpret_cast<u32x4_t *>(&to[p][at]) = w;
-            }
-        }
-    };
-    f32x4_t acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto operand = [&](const unsigned char *tile, int r0, int h) {
-        if constexpr (TALL)
-            return Tl::template columns16<true>(tile, r0, h, lane);
-        else
-            return Tl::rows16(tile, r0, h, lane);
-    };
-    fetch(ra, i0, k0);
-    fetch(rb, j0, k0);
-    // (in what the tiles' layout leaves of a row: two workgroups fill a CU's LDS to the last byte)
-    static_assert(GRAM * 2 + GRAM_WAVES * 4 <= Tl::MP && 128 + GRAM_WAVES * 4 <= Tl::KP, "a word for each wave");
-    scale = range_scale(own_top(it), reinterpret_cast<unsigned int *>(&sa[0][TALL ? GRAM * 2 : 128]));
-    for (int64_t k = k0; k < k1; k += 64) {
-        __syncthreads();
-        keep(ra, sa);
-        keep(rb, sb);
-        // (no branch round a load: the compiler would wait for it where the branch ends)
-        const int64_t next = k + 64 < k1 ? k + 64 : k0;
-        fetch(ra, i0, next);
-        fetch(rb, j0, next);
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bf16x8_t a[TM][2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    a[i][p] = operand(sa[p], wm * (16 * TM) + 16 * i, h);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                bf16x8_t b[2];
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    b[p] = operand(sb[p], wn * (GRAM / 2) + 16 * j, h);
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int s = 3; s >= 0; --s)  // the small products first
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s & 1], a[i][s >> 1],
-                                                                            acc[i][j], 0, 0, 0);
-            }
-        }
-    }
-    // a lane holds row lr and four consecutive columns of each block
-    float *const out = reinterpret_cast<float *>(it.part) + static_cast<int64_t>(z) * it.np * it.np;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            *reinterpret_cast<f32x4_t *>(
-                out + static_cast<int64_t>(i0 + wm * (16 * TM) + 16 * i + (lane & 15)) * it.np + j0 +
-                wn * (GRAM / 2) + 16 * j + 4 * (lane >> 4)) = acc[i][j];
-}
-
-__global__ void __launch_bounds__(64 * GRAM_WAVES, GRAM_WAVES / 2) ns_gram_kernel(NsGroup<NsItem> g)
-{
-    __shared__ __align__(16) GramTiles sa, sb;
-    const Found<NsItem> found = find_item(g, place_on_xcd());
-    if (found.it.tall)
-        gram_tile_bf16<true>(found.it, found.block, sa, sb);
-    else
-        gram_tile_bf16<false>(found.it, found.block, sa, sb);
 }
 
 // ------------------------------------------------- U and its Gram partial, n <= 64
 // A workgroup has all rows of a stretch of the longer side, so that it forms U, writes it for the
-// last kernel and multiplies it from LDS at once; 128 values of the longer side a turn (256, at
-// half the workgroups a CU: 32 us against 28 for 28 matrices of 64 x 4096; a kernel for U and one for
-// its product: 37).  Bound by memory traffic, 6 bytes an element in and 8 out (3.7 TB/s).
-template <bool F32>
+// last kernel and multiplies it from LDS at once; 128 values of the longer side a turn.  28
+// matrices of 64 x 4096 in bf16: 35 us for 103 MB, the 64-bit products between the turns' loads.
 struct FrontLds {
     static constexpr int K = 128;
-    // fp32: rows of K values (four places of 16 rows on distinct banks) or K rows of n values (four
-    // rows of 16); bf16: the planes' tiles of 64 values
+    // rows of K values (four places of 16 rows on distinct banks) or K rows of n values (four
+    // rows of 16)
     static constexpr int KP = K + 4, MP = SMALL + 16;
-    static constexpr int TILE_BYTES = Tiles<SMALL>::M_BYTES;
-    static_assert(Tiles<SMALL>::M_BYTES >= Tiles<SMALL>::K_BYTES, "a tile either way");
-    static constexpr int BYTES = F32 ? (SMALL * KP > K * MP ? SMALL * KP : K * MP) * 4
-                                     : 2 * K / 64 * TILE_BYTES;
+    static constexpr int BYTES = (SMALL * KP > K * MP ? SMALL * KP : K * MP) * 4;
 };
 constexpr int FRONT = 512;
 template <typename T, bool TALL>
 __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams &p, int block,
-                                              unsigned char *lds)
+                                              float *lds)
 {
-    constexpr bool F32 = sizeof(T) == 4;
-    using L = FrontLds<F32>;
-    constexpr int V = SMALL * L::K / 8 / FRONT, PLANE = L::K / 64 * L::TILE_BYTES;
+    using L = FrontLds;
+    constexpr int V = SMALL * L::K / 8 / FRONT;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4;
     const int64_t lp = TALL ? it.rp : it.cp, k0 = static_cast<int64_t>(block) * it.per_split,
                   k1 = k0 + it.per_split < lp ? k0 + it.per_split : lp;
-    const int64_t usize = static_cast<int64_t>(it.rp) * it.cp;
-    // (in what the first tile's layout leaves: two workgroups fill a CU's LDS to the last byte)
-    unsigned int *const red =
-        reinterpret_cast<unsigned int *>(lds + 2 * SMALL);
-    static_assert(2 * SMALL + FRONT / 16 <= Tiles<SMALL>::MP && 2 * SMALL + FRONT / 16 <= Tiles<SMALL>::KP,
-                  "a word for each wave");
     const int n = static_cast<int>(TALL ? it.cols : it.rows), nt = (n + 15) / 16;
     const int64_t l = TALL ? it.rows : it.cols;
 
-    // fp32: tiles wave and wave + 8 on and below the diagonal; bf16: 16 x 32 of the square
-    f64x4_t acc64[2];
-    f32x4_t acc32[2];
+    // tiles wave and wave + 8 on and below the diagonal
+    f64x4_t acc[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        acc64[r] = f64x4_t{0., 0., 0., 0.};
-        acc32[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int r = 0; r < 2; ++r)
+        acc[r] = f64x4_t{0., 0., 0., 0.};
     auto tile_of = [](int t, int &i0, int &j0) {
         const int ti = (t >= 1 ? 1 : 0) + (t >= 3 ? 1 : 0) + (t >= 6 ? 1 : 0);
         i0 = 16 * ti;
         j0 = 16 * (t - ti * (ti + 1) / 2);
     };
-    int exponent = 127;  // of the scale that acc32 is kept at
     for (int64_t k = k0; k < k1; k += L::K) {
         const int kc = static_cast<int>(k1 - k < L::K ? k1 - k : L::K);  // whole 64s
         // place of chunk v of eight: row and column in the matrix
@@ -598,12 +357,7 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
         };
         auto inside = [&](int v) { return TALL ? v / 8 < kc : v % (L::K / 8) * 8 < kc; };
         auto lds_at = [&](int v) {
-            if constexpr (F32)
-                return 4 * (TALL ? v / 8 * L::MP + v % 8 * 8 : v / (L::K / 8) * L::KP + v % (L::K / 8) * 8);
-            else if constexpr (TALL)
-                return v / 512 * L::TILE_BYTES + v / 8 % 64 * Tiles<SMALL>::MP + v % 8 * 16;
-            else
-                return v % (L::K / 8) / 8 * L::TILE_BYTES + v / (L::K / 8) * Tiles<SMALL>::KP + v % 8 * 16;
+            return TALL ? v / 8 * L::MP + v % 8 * 8 : v / (L::K / 8) * L::KP + v % (L::K / 8) * 8;
         };
         Raw8<T> gr[V];
         Raw8<float> mr[V];
@@ -641,7 +395,6 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
         }
         if (k > k0)
             __syncthreads();  // (the last turn's tiles)
-        unsigned int top = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int v = tid + i * FRONT;
@@ -668,113 +421,10 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     u[q] = 0.f;
-            const int64_t at = r * it.cp + c;
-            if constexpr (F32) {
-                float *const o = reinterpret_cast<float *>(it.u) + at;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const f32x4_t x = {u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]};
-                    *reinterpret_cast<f32x4_t *>(o + 4 * q) = x;
-                    *reinterpret_cast<f32x4_t *>(lds + lds_at(v) + 16 * q) = x;
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const unsigned int b = abs_bits(u[q]);
-                    top = top > b ? top : b;
-                }
-                u32x4_t w[2];
-                split_planes(u, w);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    *reinterpret_cast<u32x4_t *>(reinterpret_cast<uint16_t *>(it.u) + q * usize + at) = w[q];
-                    *reinterpret_cast<u32x4_t *>(lds + q * PLANE + lds_at(v)) = w[q];
-                }
-            }
+            put_u(it.u + r * it.cp + c, u);
+            put_u(lds + lds_at(v), u);
         }
-        if constexpr (F32) {
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int t = wave + 8 * r;
-                if (t >= nt * (nt + 1) / 2)
-                    continue;
-                int i0, j0;
-                tile_of(t, i0, j0);
-                const float *const f = reinterpret_cast<const float *>(lds);
-                for (int kk = 0; kk < kc; kk += 16) {
-                    float a[4], b[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int at = kk + 4 * q + kq;
-                        a[q] = TALL ? f[at * L::MP + i0 + lr] : f[(i0 + lr) * L::KP + at];
-                        b[q] = TALL ? f[at * L::MP + j0 + lr] : f[(j0 + lr) * L::KP + at];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        acc64[r] = mfma4(static_cast<double>(a[q]), static_cast<double>(b[q]), acc64[r]);
-                }
-            }
-        } else {
-            // The scale of the sums so far and of this turn: the smaller one (what is far below the
-            // largest values does not count).
-            top = block_max(top, red, FRONT / 64);  // (a barrier: the tiles are there)
-            const int mine = top == 0u ? 127 : range_exponent(top), next = mine < exponent ? mine : exponent;
-            if (next != exponent) {
-                const double ratio = __hiloint2double((1023 + 2 * (next - exponent)) << 20, 0);
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        acc32[r][q] = static_cast<float>(static_cast<double>(acc32[r][q]) * ratio);
-                exponent = next;
-            }
-            if (exponent != 0 && top != 0u) {
-                const float scale = power(exponent);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int v = tid + i * FRONT;
-                    if (!inside(v))
-                        continue;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        u32x4_t *const w = reinterpret_cast<u32x4_t *>(lds + q * PLANE + lds_at(v));
-                        *w = scaled_bf16(*w, scale);
-                    }
-                }
-                __syncthreads();
-            }
-            const int i0 = 16 * (wave >> 1), j0 = 32 * (wave & 1);
-            auto operand = [&](int plane, int stage, int r0, int h) {
-                const unsigned char *const tile = lds + plane * PLANE + stage * L::TILE_BYTES;
-                if constexpr (TALL)
-                    return Tiles<SMALL>::template columns16<true>(tile, r0, h, lane);
-                else
-                    return Tiles<SMALL>::rows16(tile, r0, h, lane);
-            };
-            for (int stage = 0; stage < kc / 64; ++stage)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    bf16x8_t a[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        a[q] = operand(q, stage, i0, h);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        bf16x8_t b[2];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            b[q] = operand(q, stage, j0 + 16 * r, h);
-#pragma unroll
-                        for (int x = 3; x >= 0; --x)  // the small products first
-                            acc32[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[x & 1], a[x >> 1], acc32[r],
-                                                                               0, 0, 0);
-                    }
-                }
-        }
-    }
-    if constexpr (F32) {
-        double *const out = reinterpret_cast<double *>(it.part) + block * SMALL * SMALL;
+        __syncthreads();
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int t = wave + 8 * r;
@@ -782,25 +432,38 @@ __device__ __forceinline__ void front_stretch(const NsInput &it, const NsParams 
                 continue;
             int i0, j0;
             tile_of(t, i0, j0);
+            for (int kk = 0; kk < kc; kk += 16) {
+                float a[4], b[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                out[(i0 + d_row(0., q, lane)) * SMALL + j0 + lr] = acc64[r][q];
+                for (int q = 0; q < 4; ++q) {
+                    const int at = kk + 4 * q + kq;
+                    a[q] = TALL ? lds[at * L::MP + i0 + lr] : lds[(i0 + lr) * L::KP + at];
+                    b[q] = TALL ? lds[at * L::MP + j0 + lr] : lds[(j0 + lr) * L::KP + at];
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[r] = mfma4(static_cast<double>(a[q]), static_cast<double>(b[q]), acc[r]);
+            }
         }
-    } else {
-        float *const out = reinterpret_cast<float *>(it.part) + block * SMALL * SMALL;
-        const int i0 = 16 * (wave >> 1), j0 = 32 * (wave & 1);
+    }
+    double *const out = it.part + block * SMALL * SMALL;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<f32x4_t *>(out + (i0 + lr) * SMALL + j0 + 16 * r + 4 * kq) = acc32[r];
-        if (tid == 0)
-            it.tops[block] = static_cast<unsigned int>(exponent);
+    for (int r = 0; r < 2; ++r) {
+        const int t = wave + 8 * r;
+        if (t >= nt * (nt + 1) / 2)
+            continue;
+        int i0, j0;
+        tile_of(t, i0, j0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            out[(i0 + d_row(q, lane)) * SMALL + j0 + lr] = acc[r][q];
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(FRONT, sizeof(T) == 2 ? 4 : 2) ns_front_kernel(NsGroup<NsInput> g)
+__global__ void __launch_bounds__(FRONT, 2) ns_front_kernel(NsGroup<NsInput> g)
 {
-    __shared__ __align__(16) unsigned char lds[FrontLds<sizeof(T) == 4>::BYTES];
+    __shared__ __align__(16) float lds[FrontLds::BYTES / 4];
     const Found<NsInput> found = find_item(g, blockIdx.x);
     if (found.it.tall)
         front_stretch<T, true>(found.it, g.p, found.block, lds);
@@ -808,12 +471,12 @@ __global__ void __launch_bounds__(FRONT, sizeof(T) == 2 ? 4 : 2) ns_front_kernel
         front_stretch<T, false>(found.it, g.p, found.block, lds);
 }
 
-// The sums of the Gram partials at N places from e (SCALED: each at a scale of its own).
-template <bool F32, bool SCALED, int N>
+// The sums of the Gram partials at N places from e.
+template <int N>
 __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)[N])
 {
-    typedef Part<F32> vec_t __attribute__((ext_vector_type(N)));
-    const Part<F32> *const p = reinterpret_cast<const Part<F32> *>(it.part) + e;
+    typedef double vec_t __attribute__((ext_vector_type(N)));
+    const double *const p = it.part + e;
     const int64_t size = static_cast<int64_t>(it.np) * it.np;
 #pragma unroll
     for (int q = 0; q < N; ++q)
@@ -821,32 +484,27 @@ __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)
 #pragma unroll 8
     for (int z = 0; z < it.splits; ++z) {
         const vec_t v = *reinterpret_cast<const vec_t *>(p + z * size);
-        const double back =
-            SCALED ? __hiloint2double((1023 - 2 * static_cast<int>(it.tops[z])) << 20, 0) : 1.;
 #pragma unroll
         for (int q = 0; q < N; ++q)
-            s[q] += static_cast<double>(v[q]) * back;
+            s[q] += v[q];
     }
 }
 
 // ------------------------------------------------------- the n x n part, n <= 64
 // One workgroup a matrix, everything in LDS; a wave for each 16 x 16 tile on and below the
 // diagonal, whose operands are all on their way before the first product.  Bound by the latency of
-// the chain, 14 products of five steps: 1.5 us each at n = 64 in fp32, of which the CU's matrix
-// rate is 0.8, and 1.4 at n = 37 in fp64.
-template <int NT, bool F32>
+// the chain, 14 products of five steps: 1.4 us each at n = 37; 28 matrices of n = 64 in 41 us.
+template <int NT>
 struct SmallLds {
-    static constexpr int PITCH = 16 * NT + (F32 ? 2 : 4);  // 16 bytes of 16 rows on distinct banks
-    alignas(16) Part<F32> m[4][16 * NT][PITCH];
+    static constexpr int PITCH = 16 * NT + 2;  // 16 bytes of 16 rows on distinct banks
+    alignas(16) double m[4][16 * NT][PITCH];
 };
-template <int NT, bool F32>
+template <int NT>
 __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p, unsigned char *lds,
                                             double *diagonal)
 {
-    using R = Part<F32>;
-    using L = SmallLds<NT, F32>;
-    constexpr int K = 16 * NT, TILES = NT * (NT + 1) / 2, PLANES = F32 ? 3 : 2;
-    auto &m = reinterpret_cast<L *>(lds)->m;
+    constexpr int K = 16 * NT, TILES = NT * (NT + 1) / 2;
+    auto &m = reinterpret_cast<SmallLds<NT> *>(lds)->m;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4;
 
@@ -854,7 +512,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
     const bool below = gi < K && gj >> 4 <= gi >> 4;  // in a tile on or below the diagonal
     double v[4] = {0., 0., 0., 0.};
     if (below)
-        gram_at<F32, !F32>(it, gi * SMALL + gj, v);
+        gram_at(it, gi * SMALL + gj, v);
     if (gi < K && gj == (gi & ~3))
         diagonal[gi] = v[gi & 3];
     __syncthreads();
@@ -870,7 +528,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             if (gj + q <= gi) {
-                const R x = static_cast<R>(v[q] * inv * inv);
+                const double x = v[q] * inv * inv;
                 m[0][gi][gj + q] = x;
                 m[0][gj + q][gi] = x;
             }
@@ -885,7 +543,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
     for (int step = 0, stage = 0;; stage = stage == 2 ? 0 : stage + 1) {
         const bool first = step == 0, last = step + 1 == p.steps;
         const int from = stage == 1 && last ? TILES : 0, to = stage == 1 && !first ? 2 * TILES : TILES;
-        Quad<R> x[ROUNDS];
+        f64x4_t x[ROUNDS];
         int i0[ROUNDS], j0[ROUNDS], into[ROUNDS];
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
@@ -903,27 +561,26 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
             into[r] = stage == 0 ? 1 : stage == 1 ? (second ? 2 : 3) : 0;
             // rows i0.. of X against rows j0.. of Y (symmetric)
             // (a lane's four consecutive values of 16 are four products' share)
-            const R *const X = &m[stage == 0 ? 0 : stage == 1 ? 1 : 3][i0[r] + lr][4 * kq];
-            const R *const Y = &m[stage == 0 ? 0 : stage == 1 ? (second ? 2 : 0) : 1][j0[r] + lr][4 * kq];
-            typedef R line_t __attribute__((ext_vector_type(16 / sizeof(R))));
-            constexpr int N = 16 / sizeof(R);
-            line_t v1[4 * NT / N], v2[4 * NT / N];
+            const double *const X = &m[stage == 0 ? 0 : stage == 1 ? 1 : 3][i0[r] + lr][4 * kq];
+            const double *const Y = &m[stage == 0 ? 0 : stage == 1 ? (second ? 2 : 0) : 1][j0[r] + lr][4 * kq];
+            typedef double pair_t __attribute__((ext_vector_type(2)));
+            pair_t v1[2 * NT], v2[2 * NT];
 #pragma unroll
-            for (int k = 0; k < 4 * NT / N; ++k) {
-                const int at = 16 * (k * N / 4) + k * N % 4;
-                v1[k] = *reinterpret_cast<const line_t *>(X + at);
-                v2[k] = *reinterpret_cast<const line_t *>(Y + at);
+            for (int k = 0; k < 2 * NT; ++k) {
+                const int at = 16 * (k / 2) + 2 * (k % 2);
+                v1[k] = *reinterpret_cast<const pair_t *>(X + at);
+                v2[k] = *reinterpret_cast<const pair_t *>(Y + at);
             }
-            Quad<R> acc = {0, 0, 0, 0};
+            f64x4_t acc = {0., 0., 0., 0.};
 #pragma unroll
             for (int k = 0; k < 4 * NT; ++k)
-                acc = mfma4(v1[k / N][k % N], v2[k / N][k % N], acc);
+                acc = mfma4(v1[k / 2][k % 2], v2[k / 2][k % 2], acc);
             if (stage == 0) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int i = i0[r] + d_row(R(), q, lane), j = j0[r] + lr;
-                    acc[q] = (i == j ? static_cast<R>(p.a) : R(0)) + static_cast<R>(p.b) * m[0][i][j] +
-                             static_cast<R>(p.c) * acc[q];
+                    const int i = i0[r] + d_row(q, lane), j = j0[r] + lr;
+                    acc[q] = (i == j ? static_cast<double>(p.a) : 0.) +
+                             static_cast<double>(p.b) * m[0][i][j] + static_cast<double>(p.c) * acc[q];
                 }
             }
             x[r] = acc;
@@ -936,7 +593,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
                 continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int i = i0[r] + d_row(R(), q, lane), j = j0[r] + lr;
+                const int i = i0[r] + d_row(q, lane), j = j0[r] + lr;
                 if (j <= i) {
                     m[into[r]][i][j] = x[r][q];
                     m[into[r]][j][i] = x[r][q];
@@ -958,7 +615,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
         float w[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)  // (zeros past n's tiles: U is zero there, too)
-            w[q] = i < K && j < K ? static_cast<float>(static_cast<double>(Q[i][j + q]) * norm.for_q()) : 0.f;
+            w[q] = i < K && j < K ? static_cast<float>(Q[i][j + q] * norm.for_q()) : 0.f;
         u32x4_t planes[PLANES];
         split_planes(w, planes);
 #pragma unroll
@@ -967,24 +624,22 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
     }
 }
 
-template <bool F32>
 __global__ void __launch_bounds__(1024) ns_small_kernel(NsGroup<NsItem> g)
 {
-    __shared__ __align__(16) unsigned char lds[sizeof(SmallLds<SMALL / 16, F32>)];
+    __shared__ __align__(16) unsigned char lds[sizeof(SmallLds<SMALL / 16>)];
     __shared__ double diagonal[SMALL];
     const NsItem &it = g.it[blockIdx.x];
     if (it.n > 48)
-        small_steps<4, F32>(it, g.p, lds, diagonal);
+        small_steps<4>(it, g.p, lds, diagonal);
     else if (it.n > 32)
-        small_steps<3, F32>(it, g.p, lds, diagonal);
+        small_steps<3>(it, g.p, lds, diagonal);
     else if (it.n > 16)
-        small_steps<2, F32>(it, g.p, lds, diagonal);
+        small_steps<2>(it, g.p, lds, diagonal);
     else
-        small_steps<1, F32>(it, g.p, lds, diagonal);
+        small_steps<1>(it, g.p, lds, diagonal);
 }
 
 // ------------------------------------------------------- the n x n part, larger
-template <bool F32>
 __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
 {
     const Found<NsItem> found = find_item(g, blockIdx.x);
@@ -994,29 +649,25 @@ __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
     if (i >= it.np || j > i)
         return;
     double s[1];
-    gram_at<F32, false>(it, e, s);
-    Part<F32> *const G = reinterpret_cast<Part<F32> *>(it.mat);
-    G[e] = static_cast<Part<F32>>(s[0]);
-    G[static_cast<int64_t>(j) * it.np + i] = static_cast<Part<F32>>(s[0]);
+    gram_at(it, e, s);
+    it.mat[e] = s[0];
+    it.mat[static_cast<int64_t>(j) * it.np + i] = s[0];
 }
 
 // One product of symmetric matrices, 32 x 32 tiles on and below the diagonal, mirrored:
 //   0  P = a I + b G + c G G    1  H = P G, and Q = P Q    2  G = H P    3  Q = P Q
 // (Q in the first step: P).  G is not scaled in place: the first step's products take it by
 // 1 / |U|^2, which is formed from its diagonal.  Matrices 4 and 5 are the other G and Q.  The last
-// Q goes into planes.  Bound by latency where n is a few hundred (384: 6.2 us a product, 9.2 for
-// two; of a workgroup's 5 us the arguments take 0.5, the operands' way from memory 1.1 to 2.3, the
-// products 1.2, the sum over the waves 0.7).
-template <int OP, bool F32>
+// Q goes into planes.  Bound by latency and the 64-bit rate where n is a few hundred (two of 384:
+// 8.5 us a product, 13.2 for two).
+template <int OP>
 __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem> g, int step)
 {
-    using R = Part<F32>;
-    constexpr int PLANES = F32 ? 3 : 2;
+    using R = double;
     constexpr int OPERANDS = POLY_WAVES * 2 * POLY * 144, SUMS = POLY_WAVES * POLY * (POLY + 1) * sizeof(R);
     __shared__ __align__(16) unsigned char lds[OPERANDS > SUMS ? OPERANDS : SUMS];
     auto &red = *reinterpret_cast<R(*)[POLY_WAVES][POLY][POLY + 1]>(lds);
     __shared__ double tr[POLY_WAVES];
-    __shared__ unsigned int tops[POLY_WAVES];
     const Found<NsItem> found = find_item(g, place_on_xcd());
     const NsItem &it = found.it;
     const int np = it.np, nt = np / POLY, tiles = nt * (nt + 1) / 2;
@@ -1029,7 +680,7 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         ++ti;
     }
     const int64_t size = static_cast<int64_t>(np) * np;
-    R *const mat = reinterpret_cast<R *>(it.mat);
+    R *const mat = it.mat;
     R *const G = mat + (step & 1 ? 4 * size : 0), *const G2 = mat + (step & 1 ? 0 : 4 * size);
     R *const P = mat + size, *const H = mat + 3 * size;
     R *const Q = mat + (step & 1 ? 5 : 2) * size, *const Q2 = mat + (step & 1 ? 2 : 5) * size;
@@ -1057,22 +708,20 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
     // the first G's scale
     double scaled = 1., for_q = 1.;
     if (step == 0 && OP == 0) {
-        const unsigned int top = F32 ? 0u : own_top(it);
         double s = 0.;
         for (int i = tid; i < np; i += POLY_WAVES * 64)
-            s += static_cast<double>(G[static_cast<int64_t>(i) * np + i]);
+            s += G[static_cast<int64_t>(i) * np + i];
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1)
             s += __shfl_xor(s, d);
         if (lane == 0)
             tr[wave] = s;
-        const double scale = F32 ? 1. : static_cast<double>(range_scale(top, tops));
         __syncthreads();
         s = tr[0];
         for (int w = 1; w < POLY_WAVES; ++w)
             s += tr[w];
-        const NormScale norm = norm_scale(sqrt(s) / scale, static_cast<double>(g.p.eps));
-        scaled = norm.inv / scale * (norm.inv / scale);
+        const NormScale norm = norm_scale(sqrt(s), static_cast<double>(g.p.eps));
+        scaled = norm.inv * norm.inv;
         for_q = norm.for_q();
         if (ti == 0 && tid == 0) {
             it.scal[0] = for_q;
@@ -1083,12 +732,12 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         scaled = it.scal[1];
     }
 
-    Quad<R> acc[2][2];
+    f64x4_t acc[2][2];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            acc[x][y] = Quad<R>{0, 0, 0, 0};
+            acc[x][y] = f64x4_t{0., 0., 0., 0.};
     // Each wave takes every eighth 128-byte line of the 32 rows and the 32 columns' rows: whole lines
     // (half of them an instruction took 3 us longer to come, from caches that other CUs wrote), two
     // turns' on their way at once, turned in LDS of the wave's own into operands of 16 rows.
@@ -1114,12 +763,12 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int t = 0; t < LINE / 16; ++t) {  // 16 values of K, four consecutive ones a lane
-            Quad<R> a[2], b[2];
+            f64x4_t a[2], b[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int at = (16 * t + 4 * kq) * static_cast<int>(sizeof(R));
-                a[q] = *reinterpret_cast<const Quad<R> *>(mine + (16 * q + lr) * PITCH + at);
-                b[q] = *reinterpret_cast<const Quad<R> *>(mine + (32 + 16 * q + lr) * PITCH + at);
+                a[q] = *reinterpret_cast<const f64x4_t *>(mine + (16 * q + lr) * PITCH + at);
+                b[q] = *reinterpret_cast<const f64x4_t *>(mine + (32 + 16 * q + lr) * PITCH + at);
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s)
@@ -1152,14 +801,14 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                red[wave][16 * x + d_row(R(), q, lane)][16 * y + lr] = acc[x][y][q];
+                red[wave][16 * x + d_row(q, lane)][16 * y + lr] = acc[x][y][q];
     __syncthreads();
     const bool planes = (OP == 3 || OP == 0) && step + 1 == g.p.steps && (OP == 3 || step == 0);
     // the values of the tile, and a second time transposed
     auto put = [&](int i, int j, R x) {
         const int64_t at = static_cast<int64_t>(i) * np + j;
         if (planes) {
-            float r = static_cast<float>(static_cast<double>(x) * (OP == 0 ? for_q : it.scal[0]));
+            float r = static_cast<float>(x * (OP == 0 ? for_q : it.scal[0]));
 #pragma unroll
             for (int k = 0; k < PLANES; ++k) {
                 const uint16_t w = f32_to_bf16(r);
@@ -1181,13 +830,13 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
         for (int w = 1; w < POLY_WAVES; ++w)
             s += red[w][i][j];
         if constexpr (OP == 0) {
-            const double x = static_cast<double>(G[static_cast<int64_t>(i0 + i) * np + j0 + j]);
-            s = static_cast<R>((i0 + i == j0 + j ? static_cast<double>(g.p.a) : 0.) +
-                               static_cast<double>(g.p.b) * (scaled * x) +
-                               static_cast<double>(g.p.c) * (scaled * (scaled * static_cast<double>(s))));
+            const double x = G[static_cast<int64_t>(i0 + i) * np + j0 + j];
+            s = (i0 + i == j0 + j ? static_cast<double>(g.p.a) : 0.) +
+                static_cast<double>(g.p.b) * (scaled * x) +
+                static_cast<double>(g.p.c) * (scaled * (scaled * s));
         } else if constexpr (OP == 1) {
             if (!second)
-                s = static_cast<R>(static_cast<double>(s) * scaled);
+                s *= scaled;
         }
         red[0][i][j] = s;  // (no other thread reads it before the barrier)
         if (j0 + j <= i0 + i)
@@ -1204,15 +853,39 @@ __global__ void __launch_bounds__(POLY_WAVES * 64) ns_poly_kernel(NsGroup<NsItem
 // ------------------------------------------------------------- O = Q U (or U Q)
 // Tiles of NB values of the shorter side by 128 of the longer one, eight waves (4 x 2), 64 values
 // of K (the shorter side) a stage, the next one on its way.  The tile goes through LDS, so that
-// the update reads and writes whole lines.  Bound like the Gram product (50 us for 85 MB read, 28
-// written and 33 GFLOP of products; four waves of 64 x 64 55, rows of the update straight from the
-// accumulators 67).
-template <typename T, int NB>
+// the update reads and writes whole lines.  Bound by its loads' round trips, the splitting and the
+// products in turn, at one workgroup a CU (384 x 8192 and 28672 x 384 in bf16: 98 us for 85 MB read,
+// 28 written and six products of 11 GFLOP).
+constexpr int FINAL_WAVES = 8;  // two in each row
+
+// LDS tiles of one plane: 64 K values of R rows, as rows of K values 160 bytes apart (a 16-byte
+// read takes lanes 0-3, 12-15 and 20-27 at once, and so on: sixteen chunks of two neighbouring
+// columns, which lie on distinct banks; 144 bytes: two on each), or, where the matrix lies the
+// other way, as 64 rows of R values, read by transposing loads.
+template <int R>
+struct Tiles {
+    static constexpr int KP = 160, MP = 2 * R + 32;
+    static constexpr int K_BYTES = R * KP, M_BYTES = 64 * MP;
+    // operands of 32 K values (h: the first or the second half of the stage) of 16 rows from r0
+    __device__ __forceinline__ static bf16x8_t rows16(const unsigned char *tile, int r0, int h, int lane)
+    {
+        return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t *>(
+                                                tile + (r0 + (lane & 15)) * KP + 64 * h + 16 * (lane >> 4)));
+    }
+    __device__ __forceinline__ static bf16x8_t columns16(const unsigned char *tile, int c0, int h, int lane)
+    {
+        const int lr = lane & 15, kq = lane >> 4;
+        const unsigned char *const p = tile + (32 * h + 8 * kq + (lr >> 2)) * MP + (c0 + 4 * (lr & 3)) * 2;
+        const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
+        const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * MP));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+template <int NB>
 struct FinalLds {
-    static constexpr int P = sizeof(T) == 2 ? 2 : 3;
     static constexpr int U_BYTES = Tiles<128>::K_BYTES > Tiles<128>::M_BYTES ? Tiles<128>::K_BYTES
                                                                              : Tiles<128>::M_BYTES;
-    static constexpr int STAGE = P * (Tiles<NB>::K_BYTES + U_BYTES);
+    static constexpr int STAGE = PLANES * (Tiles<NB>::K_BYTES + U_BYTES);
     static constexpr int OUT = 128 * (NB + 4) * 4 > NB * (128 + 4) * 4 ? 128 * (NB + 4) * 4
                                                                        : NB * (128 + 4) * 4;
     static constexpr int BYTES = STAGE > OUT ? STAGE : OUT;
@@ -1220,7 +893,7 @@ struct FinalLds {
 template <typename T, bool TALL, int NB>
 __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsigned char *lds)
 {
-    constexpr int P = sizeof(T) == 2 ? 2 : 3;
+    constexpr int P = PLANES;
     constexpr int BM = TALL ? 128 : NB, BN = TALL ? NB : 128;
     using Tq = Tiles<NB>;
     using Tu = Tiles<128>;
@@ -1231,7 +904,7 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         qs[p] = lds + p * Tq::K_BYTES;
-        us[p] = lds + P * Tq::K_BYTES + p * FinalLds<T, NB>::U_BYTES;
+        us[p] = lds + P * Tq::K_BYTES + p * FinalLds<NB>::U_BYTES;
     }
     const int nb = it.np / NB;
     // (the tiles of one stretch of the longer side next to each other: they read the same U)
@@ -1240,14 +913,13 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, kq = lane >> 4, wm = wave >> 1, wn = wave & 1;
     const int np = it.np;
-    const int64_t qsize = static_cast<int64_t>(np) * np, usize = static_cast<int64_t>(it.rp) * it.cp;
+    const int64_t qsize = static_cast<int64_t>(np) * np;
     const float scale = static_cast<float>(it.scal[2]);
 
     // 16-byte chunks a thread
     constexpr int QV = Q_ROWS * 8 / (64 * FINAL_WAVES), UV = 128 * 8 / (64 * FINAL_WAVES);
     u32x4_t qr[QV][P];
     Raw8<float> uf[UV];
-    u32x4_t up[UV][2];
     auto u_at = [&](int v, int k) {  // row-major place of chunk v of the stage at k
         if constexpr (TALL)
             return (l0 + v / 8) * it.cp + k + v % 8 * 8;
@@ -1264,17 +936,8 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
                     it.q + p * qsize + static_cast<int64_t>(n0 + v / 8) * np + k + v % 8 * 8);
         }
 #pragma unroll
-        for (int i = 0; i < UV; ++i) {
-            const int64_t at = u_at(tid + i * (64 * FINAL_WAVES), k);
-            if constexpr (P == 3) {
-                uf[i].template load<true>(reinterpret_cast<const float *>(it.u) + at, 8);
-            } else {
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    up[i][p] = *reinterpret_cast<const u32x4_t *>(
-                        reinterpret_cast<const uint16_t *>(it.u) + p * usize + at);
-            }
-        }
+        for (int i = 0; i < UV; ++i)
+            uf[i].template load<true>(it.u + u_at(tid + i * (64 * FINAL_WAVES), k), 8);
     };
     auto keep = [&]() {
 #pragma unroll
@@ -1288,21 +951,12 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
         for (int i = 0; i < UV; ++i) {
             const int v = tid + i * (64 * FINAL_WAVES);
             u32x4_t w[P];
-            if constexpr (P == 3) {
-                float f[8];
-                uf[i].get(f);
+            float f[8];
+            uf[i].get(f);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    f[q] *= scale;
-                split_planes(f, w);
-            } else {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    w[p] = up[i][p];
-                    if (scale != 1.f)
-                        w[p] = scaled_bf16(w[p], scale);
-                }
-            }
+            for (int q = 0; q < 8; ++q)
+                f[q] *= scale;
+            split_planes(f, w);
 #pragma unroll
             for (int p = 0; p < P; ++p)
                 *reinterpret_cast<u32x4_t *>(
@@ -1398,10 +1052,9 @@ __device__ __forceinline__ void final_tile(const NsOutput &it, int block, unsign
 }
 
 template <typename T, int NB>
-__global__ void __launch_bounds__(64 * FINAL_WAVES, FINAL_WAVES / (sizeof(T) == 2 ? 2 : 4))
-    ns_final_kernel(NsGroup<NsOutput> g)
+__global__ void __launch_bounds__(64 * FINAL_WAVES, FINAL_WAVES / 4) ns_final_kernel(NsGroup<NsOutput> g)
 {
-    __shared__ __align__(16) unsigned char lds[FinalLds<T, NB>::BYTES];
+    __shared__ __align__(16) unsigned char lds[FinalLds<NB>::BYTES];
     const Found<NsOutput> found = find_item(g, place_on_xcd());
     if (found.it.tall)
         final_tile<T, true, NB>(found.it, found.block, lds);
@@ -1429,11 +1082,7 @@ Sides sides(int64_t rows, int64_t cols)
     return s;
 }
 
-int64_t gram_tiles(int bf16, int64_t np)
-{
-    const int64_t nt = np / (bf16 ? GRAM : TILE);
-    return nt * (nt + 1) / 2;
-}
+int64_t gram_tiles(int64_t np) { return np / TILE * (np / TILE + 1) / 2; }
 int64_t prepare_groups(int64_t rp, int64_t cp)
 {
     return (rp * cp / 8 + THREADS * PREP_VPT - 1) / (THREADS * PREP_VPT);
@@ -1447,7 +1096,7 @@ struct Chunk {
 };
 constexpr size_t CHUNK_BYTES = size_t(256) << 20;
 
-Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
+Chunk plan_chunk(const NsMatrix *mats, int count, int first, char *ws)
 {
     Chunk c;
     c.first = first;
@@ -1467,27 +1116,22 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
             off += (bytes + 255) / 256 * 256;
             return ws + at;
         };
-        const size_t square = static_cast<size_t>(s.np) * s.np, real = bf16 ? 4 : 8;
-        it.u = take(static_cast<size_t>(s.rp) * s.cp * 4);
-        it.top_count = !bf16          ? 0
-                       : s.np > SMALL ? static_cast<int>(prepare_groups(s.rp, s.cp))
-                                      : it.splits;
-        it.tops = reinterpret_cast<unsigned int *>(take(it.top_count * sizeof(unsigned int)));
-        it.part = take(it.splits * square * real);
-        it.mat = take(s.np > SMALL ? 6 * square * real : 0);
+        const size_t square = static_cast<size_t>(s.np) * s.np;
+        it.u = reinterpret_cast<float *>(take(static_cast<size_t>(s.rp) * s.cp * sizeof(float)));
+        it.part = reinterpret_cast<double *>(take(it.splits * square * sizeof(double)));
+        it.mat = reinterpret_cast<double *>(take(s.np > SMALL ? 6 * square * sizeof(double) : 0));
         it.scal = reinterpret_cast<double *>(take(3 * sizeof(double)));
-        it.q = reinterpret_cast<uint16_t *>(take((bf16 ? 2 : 3) * square * 2));
+        it.q = reinterpret_cast<uint16_t *>(take(PLANES * square * sizeof(uint16_t)));
         return off;
     };
-    // The Gram products of the set as about 512 workgroups of equal length (1024 in 64 bits, of
-    // half the waves), of 64 values of the longer side each at least; a matrix has at most 64
-    // shares, or 32 in 64 bits, or where one workgroup adds them (n <= 64: 16 KiB each).
+    // The Gram products of the set as about 1024 workgroups of equal length (512 where one forms U,
+    // too), of 64 values of the longer side each at least; a matrix has at most 32 shares.
     auto split = [&](int n) {
         int64_t work = 0, longest = 0, work_front = 0, longest_front = 0;
         for (int i = first; i < first + n; ++i) {
             const Sides s = sides(mats[i].rows, mats[i].cols);
             if (s.np > SMALL) {
-                work += gram_tiles(bf16, s.np) * s.lp;
+                work += gram_tiles(s.np) * s.lp;
                 longest = s.lp > longest ? s.lp : longest;
             } else {
                 work_front += s.lp;
@@ -1495,7 +1139,7 @@ Chunk plan_chunk(int bf16, const NsMatrix *mats, int count, int first, char *ws)
             }
         }
         auto share = [](int64_t even, int64_t least) { return up_to(even > least ? even : least, 64); };
-        per_split = bf16 ? share(work / 512, (longest + 63) / 64) : share(work / 1024, (longest + 31) / 32);
+        per_split = share(work / 1024, (longest + 31) / 32);
         per_front = share(work_front / 512, (longest_front + 31) / 32);
         size_t off = 0;
         for (int i = 0; i < n; ++i)
@@ -1528,7 +1172,6 @@ int group_of(NsGroup<I> &g, const I *items, const Chunk &c, Take &&take, Blocks 
 template <typename T>
 hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hipStream_t st)
 {
-    constexpr bool F32 = sizeof(T) == 4;
 #define NS_LAUNCH(...)                         \
     do {                                       \
         hipLaunchKernelGGL(__VA_ARGS__);       \
@@ -1544,8 +1187,8 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
         for (int i = 0; i < c.count; ++i) {
             const NsItem &it = c.it[i];
             const NsMatrix &m = mats[c.first + i];
-            in[i] = NsInput{it.u,   it.part, it.tops, m.g,   m.m,     m.m_out,
-                            m.rows, m.cols,  it.rp,   it.cp, it.tall, it.per_split};
+            in[i] = NsInput{it.u,   it.part, m.g,   m.m,   m.m_out, m.rows,
+                            m.cols, it.rp,   it.cp, it.tall, it.per_split};
         }
         NsGroup<NsInput> g;
         g.p = p;
@@ -1558,22 +1201,17 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
     }
     NsGroup<NsItem> g;
     g.p = p;
-    auto gram_groups = [](const NsItem &i) { return gram_tiles(!F32, i.np) * i.splits; };
-    n = group_of(g, c.it, c, large, gram_groups);
-    if (n > 0) {
-        if constexpr (F32)
-            NS_LAUNCH(ns_gram_f64_kernel, dim3(n), dim3(THREADS), 0, st, g);
-        else
-            NS_LAUNCH(ns_gram_kernel, dim3(n), dim3(64 * GRAM_WAVES), 0, st, g);
-    }
+    n = group_of(g, c.it, c, large, [](const NsItem &i) { return gram_tiles(i.np) * i.splits; });
+    if (n > 0)
+        NS_LAUNCH(ns_gram_kernel, dim3(n), dim3(THREADS), 0, st, g);
     n = group_of(g, c.it, c, small, [](const NsItem &) { return 1; });
     if (n > 0)
-        NS_LAUNCH((ns_small_kernel<F32>), dim3(n), dim3(1024), 0, st, g);
+        NS_LAUNCH(ns_small_kernel, dim3(n), dim3(1024), 0, st, g);
     n = group_of(g, c.it, c, large, [](const NsItem &i) {
         return (static_cast<int64_t>(i.np) * i.np + THREADS - 1) / THREADS;
     });
     if (n > 0) {
-        NS_LAUNCH((ns_gram_sum_kernel<F32>), dim3(n), dim3(THREADS), 0, st, g);
+        NS_LAUNCH(ns_gram_sum_kernel, dim3(n), dim3(THREADS), 0, st, g);
         auto tiles = [](const NsItem &i) {
             return static_cast<int64_t>(i.np / POLY) * (i.np / POLY + 1) / 2;
         };
@@ -1581,18 +1219,18 @@ hipError_t run_chunk(const Chunk &c, const NsMatrix *mats, const NsParams &p, hi
         for (int s = 0; s < p.steps; ++s) {
             const bool first = s == 0, last = s + 1 == p.steps;
             n = group_of(g, c.it, c, large, tiles);
-            NS_LAUNCH((ns_poly_kernel<0, F32>), dim3(n), block, 0, st, g, s);
+            NS_LAUNCH((ns_poly_kernel<0>), dim3(n), block, 0, st, g, s);
             if (last) {
                 if (!first)
-                    NS_LAUNCH((ns_poly_kernel<3, F32>), dim3(n), block, 0, st, g, s);
+                    NS_LAUNCH((ns_poly_kernel<3>), dim3(n), block, 0, st, g, s);
                 continue;
             }
             // (the first Q is P)
             const int each = first ? 1 : 2;
             n = group_of(g, c.it, c, large, [&](const NsItem &i) { return each * tiles(i); });
-            NS_LAUNCH((ns_poly_kernel<1, F32>), dim3(n), block, 0, st, g, s);
+            NS_LAUNCH((ns_poly_kernel<1>), dim3(n), block, 0, st, g, s);
             n = group_of(g, c.it, c, large, tiles);
-            NS_LAUNCH((ns_poly_kernel<2, F32>), dim3(n), block, 0, st, g, s);
+            NS_LAUNCH((ns_poly_kernel<2>), dim3(n), block, 0, st, g, s);
         }
     }
     NsOutput to[MAX_ITEMS];
@@ -1625,11 +1263,11 @@ bool newton_schulz_fits(int64_t rows, int64_t cols)
     return s.np <= NS_MAX_SHORT && s.rp <= (int64_t(1) << 33) / s.cp;
 }
 
-size_t newton_schulz_workspace(int bf16, const NsMatrix *mats, int count)
+size_t newton_schulz_workspace(const NsMatrix *mats, int count)
 {
     size_t most = 0;
     for (int first = 0; first < count;) {
-        const Chunk c = plan_chunk(bf16, mats, count, first, nullptr);
+        const Chunk c = plan_chunk(mats, count, first, nullptr);
         most = c.bytes > most ? c.bytes : most;
         first += c.count;
     }
@@ -1640,7 +1278,7 @@ hipError_t launch_newton_schulz(int bf16, const NsMatrix *mats, int count, const
                                 hipStream_t st)
 {
     for (int first = 0; first < count;) {
-        const Chunk c = plan_chunk(bf16, mats, count, first, static_cast<char *>(ws));
+        const Chunk c = plan_chunk(mats, count, first, static_cast<char *>(ws));
         const hipError_t e = bf16 ? run_chunk<uint16_t>(c, mats, p, st)
                                   : run_chunk<float>(c, mats, p, st);
         if (e != hipSuccess)

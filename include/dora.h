@@ -519,9 +519,12 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
  *   (for rows > cols of the transpose, which is the same matrix), (a, b, c) =
  *   coefficients, a host array, or 3.4445, -4.7750, 2.0315 where it is NULL: after
  *   five steps from a matrix of singular values above 0.0015 of its norm those of O
- *   lie between 0.68 and 1.21.  U, O in `dtype`; O may be U itself.  Formed from 16
- *   bits of bf16 matrices' U (and 24 of fp32 ones') with X X^T and its polynomials in
- *   32 bits (64 for fp32 matrices), rounded once.
+ *   lie between 0.68 and 1.21.  U, O in `dtype`; O may be U itself.  X X^T and its
+ *   polynomials are formed in 64 bits, the product of the last one with U from 24 bits
+ *   of both, rounded once, for either `dtype`: as near the steps in exact arithmetic as
+ *   the steps in fp32 are.  Like those it loses |a|^steps 2^-24 of |U|_F or so in the
+ *   directions that U (of low rank) does not have: 3e-5 after five of these steps, a
+ *   hundredth after ten.
  *   1 <= steps <= 16; eps finite, >= 0; the shorter side up to 8192 (or
  *   DORA_E_SHAPE), the matrix up to 2^33 elements with its sides padded to 128s.
  *   U may have any magnitude; an infinity or a NaN in it makes all of O NaN.
@@ -537,7 +540,7 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
  *   of its sums; the array is read during the call only.
  *   ws: dora_orthogonalize_workspace / dora_muon_workspace bytes: copies of the
  *   matrices (4 bytes an element, sides padded), and the short sides' squares in 64
- *   bits (32 for bf16).
+ *   bits.
  */
 typedef struct dora_update {
     const void *param;
