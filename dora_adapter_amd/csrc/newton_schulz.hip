@@ -23,7 +23,9 @@
 // in bf16 432 us (eighteen launches), of fourteen 64 x 4096 and fourteen 4096 x 64 98 us
 // (three), 37 x 1027 in fp32 37 us (three).  (G, the n x n part and the planes of bf16 matrices at
 // 16 to 24 bits took 229 and 90 us, and are not right for a low rank: see above.)
+#include <algorithm>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "around.hpp"
@@ -56,6 +58,7 @@ struct NsItem {
     int tall;      // rows > cols
     int rp, cp;    // rows and columns as padded (the longer side to 128s)
     int splits, per_split;  // of the longer side, a multiple of 64
+    float lift;             // of G's diagonal
 };
 struct NsInput {  // what the first kernel reads and writes
     float *u;
@@ -471,9 +474,15 @@ __global__ void __launch_bounds__(FRONT, 2) ns_front_kernel(NsGroup<NsInput> g)
         front_stretch<T, false>(found.it, g.p, found.block, lds);
 }
 
-// The sums of the Gram partials at N places from e.
+// The sums of the Gram partials at N places from e, in row i from column j on.  The diagonal is
+// lifted by more than G's own rounding may take from its eigenvalues: 64 bits leave some of a
+// matrix of low rank at -2^-56 or so of its norm, and sixteen steps take those out of the
+// polynomial's range (16 x 333 of rank 1: O 180 times its size).  The rounding of a row and a column
+// goes by the root of their diagonal elements' product, so that a share of each of those makes up
+// for it, however far apart they are.  (An O that depends on singular values so small is
+// lost to 24 bits of U in any case.)
 template <int N>
-__device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)[N])
+__device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, int i, int j, double (&s)[N])
 {
     typedef double vec_t __attribute__((ext_vector_type(N)));
     const double *const p = it.part + e;
@@ -488,6 +497,9 @@ __device__ __forceinline__ void gram_at(const NsItem &it, int64_t e, double (&s)
         for (int q = 0; q < N; ++q)
             s[q] += v[q];
     }
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        s[q] += i == j + q ? s[q] * static_cast<double>(it.lift) : 0.;
 }
 
 // ------------------------------------------------------- the n x n part, n <= 64
@@ -512,7 +524,7 @@ __device__ __forceinline__ void small_steps(const NsItem &it, const NsParams &p,
     const bool below = gi < K && gj >> 4 <= gi >> 4;  // in a tile on or below the diagonal
     double v[4] = {0., 0., 0., 0.};
     if (below)
-        gram_at(it, gi * SMALL + gj, v);
+        gram_at(it, gi * SMALL + gj, gi, gj, v);
     if (gi < K && gj == (gi & ~3))
         diagonal[gi] = v[gi & 3];
     __syncthreads();
@@ -649,7 +661,7 @@ __global__ void __launch_bounds__(THREADS) ns_gram_sum_kernel(NsGroup<NsItem> g)
     if (i >= it.np || j > i)
         return;
     double s[1];
-    gram_at(it, e, s);
+    gram_at(it, e, i, j, s);
     it.mat[e] = s[0];
     it.mat[static_cast<int64_t>(j) * it.np + i] = s[0];
 }
@@ -1108,6 +1120,8 @@ Chunk plan_chunk(const NsMatrix *mats, int count, int first, char *ws)
         it.np = static_cast<int>(s.np);
         it.rp = static_cast<int>(s.rp);
         it.cp = static_cast<int>(s.cp);
+        // (a product's n terms a row, and the sums over a share of the longer side before that)
+        it.lift = static_cast<float>((16. + 4. * it.n) * std::max(1., std::sqrt(double(s.lp)) / 64.) * 0x1p-53);
         const int64_t share = s.np > SMALL ? per_split : per_front;
         it.per_split = static_cast<int>(share < s.lp ? share : s.lp);
         it.splits = static_cast<int>((s.lp + it.per_split - 1) / it.per_split);

@@ -18,7 +18,7 @@ from low_rank_ref import COEFFICIENTS, QUINTIC, U, Steps, low_rank
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF, F32 = torch.bfloat16, torch.float32
-STEPS = (1, 2, 4, 5, 6, 7, 8, 9, 10, 12, 14)
+STEPS = (1, 2, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16)
 
 
 def ranks(n):
@@ -48,7 +48,7 @@ def test_whole_numbers(n, length, dt):
     for rank in ranks(n):
         say("low rank", n, length, rank, dt)
         check(low_rank(n + rank, n, length, rank, dt), dt)
-        check(low_rank(n + rank, length, n, rank, dt), dt, steps=(5, 8, 14))
+        check(low_rank(n + rank, length, n, rank, dt), dt, steps=(5, 8, 16))
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -73,8 +73,22 @@ def test_singular_values_far_apart(shape, dt):
         * torch.exp2(-20 * torch.rand(n, 1, generator=g).double())
     for m in (M, graded):
         say("singular values far apart", shape, dt)
-        check((m if shape[0] == n else m.T).to(dt).contiguous(), dt, steps=(3, 5, 8, 12, 14),
+        check((m if shape[0] == n else m.T).to(dt).contiguous(), dt, steps=(3, 5, 8, 12, 16),
               coefficients=(QUINTIC,))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n,length", [(5, 70000), (48, 9000), (64, 64), (256, 256), (700, 1500)])
+def test_sixteen_steps_stay_bounded(n, length, dt):
+    """No rounding of G leaves an eigenvalue that the last steps take out of their range."""
+    for rank in {1, max(n // 3, 1)}:
+        for whole in (True, False):
+            say("sixteen steps", n, length, rank, dt, whole)
+            M = low_rank(rank, n, length, rank, dt, whole)
+            for co in COEFFICIENTS:
+                for m in (M, M.T.contiguous()):
+                    O = D.dora_orthogonalize(m.to(DEV), steps=16, coefficients=co).cpu().double()
+                    assert torch.isfinite(O).all() and float(torch.linalg.matrix_norm(O, 2)) <= 1.21 + 4
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
