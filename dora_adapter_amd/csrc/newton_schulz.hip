@@ -126,7 +126,8 @@ __device__ __forceinline__ int place_on_xcd()
 }
 
 // 1 / (|U|_F + eps), and the power of two that goes from it to U where the norm is so far from one
-// that planes of Q times it would leave fp32's range (O is Q times it times U).  No U, no O.
+// that planes of Q times it would leave fp32's range (O is Q times it times U).  Of zeros O is
+// zeros whatever eps, 0 too.
 struct NormScale {
     double inv;  // of |U|_F + eps
     int s;
@@ -142,7 +143,7 @@ __device__ __forceinline__ NormScale norm_scale(double norm, double eps)
     const double t = norm + eps;
     const int e = ((__double2hiint(t) >> 20) & 0x7ff) - 1023;  // (zero -1023, infinity and NaN 1024)
     NormScale n;
-    n.inv = norm == 0. && eps > 0. ? 0. : 1. / t;
+    n.inv = norm == 0. ? 0. : 1. / t;
     n.s = e < -1000 || e > 1000 || (e > -60 && e < 60) ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
     return n;
 }

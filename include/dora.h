@@ -527,7 +527,8 @@ int dora_linear_fourbit(const void *x, const void *codes, const void *scale, int
  *   hundredth after ten.
  *   1 <= steps <= 16; eps finite, >= 0; the shorter side up to 8192 (or
  *   DORA_E_SHAPE), the matrix up to 2^33 elements with its sides padded to 128s.
- *   U may have any magnitude; an infinity or a NaN in it makes all of O NaN.
+ *   U may have any magnitude; an infinity or a NaN in it makes all of O NaN, and a U
+ *   of zeros gives an O of zeros, with eps = 0 too.
  *
  * dora_muon - the step of a list of matrices:
  *     momentum_out = mu momentum + grad
