@@ -125,8 +125,9 @@ __device__ __forceinline__ int place_on_xcd()
     return xcd * each + (xcd < more ? xcd : more) + (b >> 3);
 }
 
-// 1 / (|U|_F + eps), and the power of two that goes from it to U where the norm is so far from one
-// that planes of Q times it would leave fp32's range (O is Q times it times U).  Of zeros O is
+// 1 / (|U|_F + eps), and the power of two that goes from it to U where one of them is so far from
+// one that its planes would leave fp32's range (O is Q times it times U): half of the way from
+// one to the other, so that both keep their bits where U lies far below eps, too.  Of zeros O is
 // zeros whatever eps, 0 too.
 struct NormScale {
     double inv;  // of |U|_F + eps
@@ -140,11 +141,13 @@ struct NormScale {
 };
 __device__ __forceinline__ NormScale norm_scale(double norm, double eps)
 {
+    // (zero -1023, infinity and NaN 1024)
+    auto exponent = [](double v) { return ((__double2hiint(v) >> 20) & 0x7ff) - 1023; };
     const double t = norm + eps;
-    const int e = ((__double2hiint(t) >> 20) & 0x7ff) - 1023;  // (zero -1023, infinity and NaN 1024)
+    const int en = exponent(norm), et = exponent(t), e = (en + et) / 2;
     NormScale n;
     n.inv = norm == 0. ? 0. : 1. / t;
-    n.s = e < -1000 || e > 1000 || (e > -60 && e < 60) ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
+    n.s = en < -1000 || et > 1000 || (en > -60 && et < 60) ? 0 : e < -126 ? -126 : e > 126 ? 126 : e;
     return n;
 }
 

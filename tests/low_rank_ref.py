@@ -37,7 +37,7 @@ class Steps:
         self.share = norm / self.size
         self.W, self.s, self.V = torch.linalg.svd(self.X / self.size, full_matrices=False)
 
-    def run(self, steps, coefficients):
+    def run(self, steps, coefficients, least=1e-12):
         """(O, bound of |O' - O|_F in fp32 outputs, without what U itself is off by)."""
         a, b, c = (float(torch.tensor(v, dtype=torch.float32)) for v in coefficients)
         first = self.s ** 2
@@ -63,7 +63,7 @@ class Steps:
         divided = torch.where(away, (q[:, None] - q[None, :]) / gap, (dq[:, None] + dq[None, :]) / 2)
         D = (16 + 4 * n) * 2.0 ** -53 * max(1.0, length ** 0.5 / 64) * float((first ** 2).sum().sqrt())
         inner = steps * D * float((divided.abs() * self.s[None, :]).max())
-        return O.T if self.tall else O, end + inner + 1e-12
+        return O.T if self.tall else O, end + inner + least
 
     def steepest(self, steps, coefficients):
         """The largest |f'| on [0, 1] of what the steps make of a singular value."""
