@@ -669,10 +669,10 @@ def _gate_rows(gate, T, d):
         return 0
     if gate.dim() == 1:
         return max(T, 1)
-    G = gate.shape[0]
+    G = gate.shape[0] if gate.dim() == 2 else 0
     if T == 0 and G == 1:
         return 1
-    if gate.dim() != 2 or G < 1 or T < G or T % G:
+    if G < 1 or T < G or T % G:
         raise ValueError(f"gate of shape {tuple(gate.shape)} for {T} tokens: [d], or [G, d] with "
                          "G dividing them")
     return T // G
