@@ -2399,6 +2399,10 @@ struct FourbitPlan {
     GPlan g, last;
     size_t o_part = 0, bytes = 0;
 };
+// Straight from the codes every 64 tokens (16 of fp32) read and turn them again, a panel is restored
+// once whatever the tokens.  At 256 tokens the first is still twice as fast: 8192 -> 28672 in
+// bf16 199 us against 389 in panels (257 tokens), 4096 -> 4096 18 against 43, in fp32 895 against 2347.
+// Up to here no workspace is needed.
 constexpr int64_t kFourbitTokens = 256;
 constexpr int64_t kFourbitPanel = int64_t(128) << 20;
 

@@ -435,8 +435,9 @@ int dora_backward_checkpoint(const void *dy, const void *xq, const float *xs, co
  *   a gate a channel, 1 a gate a token and channel, and the length of sequences of
  *   one length a gate vector for each.  rstd_post, rstd_pre [T] fp32 (each NULL to
  *   skip): the two factors 1 / sqrt(...), for the backward.  eps finite, >= 0; rows
- *   of any magnitude.  h may be residual itself, y may be x itself; no other
- *   overlap.
+ *   of any magnitude whose factor is an fp32 number (with eps = 0 not those of zeros,
+ *   NaN as the formula is, nor of fp32 values below 2^-127 alone).  h may be residual
+ *   itself, y may be x itself; no other overlap.
  *
  * dora_block_norm_backward - its gradients, from the x, h and factors of the
  * forward; dy is the gradient of y, dh (nullable) the one that reaches h along the
